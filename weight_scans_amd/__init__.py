@@ -486,3 +486,10 @@ def scan(x, g, eta, alpha, W0, chunk=0, flags=0):
     if _fn is None:
         _fn = _make_function()
     return _fn.apply(x, g, eta, alpha, W0, chunk, flags)
+
+
+# The gated delta rule and the query / key norms (include/gl_delta.h).
+from .delta import (DELTA_EXPORTS, GL_FLAG_INTERLEAVED, DeltaDesc, QkDesc, delta_lib,  # noqa: E402,F401
+                    delta_path_name, delta_rule, delta_saved_size, delta_workspace_size, gl_delta_bwd,
+                    gl_delta_fwd, gl_delta_step, gl_qknorm_rope_bwd, gl_qknorm_rope_fwd, make_delta_desc,
+                    qknorm_rope)

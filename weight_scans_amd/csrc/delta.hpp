@@ -1,0 +1,112 @@
+// delta.hpp -- argument blocks and launchers of the gated delta rule and of the
+// query / key norms, shared by gl_delta.cpp and the kernels.  Not part of the
+// public ABI.
+#pragma once
+
+#include <hip/hip_runtime.h>
+
+#include <cstddef>
+#include <cstdint>
+
+#include "internal.hpp"
+
+namespace gls {
+
+struct Str3 {
+  int64_t b, h, t;
+};
+
+// One call of the gated delta rule.  N sequences: b = 0..B-1 of T tokens each,
+// or (cu != NULL) n = 0..N-1 of the packed axis of T tokens.
+struct DeltaArgs {
+  const void* q = nullptr;
+  const void* k = nullptr;
+  const void* v = nullptr;
+  const void* la = nullptr;
+  const void* be = nullptr;
+  const void* state_in = nullptr;
+  const int32_t* cu = nullptr;
+  void* y = nullptr;
+  void* state_out = nullptr;
+  const void* dy = nullptr;
+  const void* dstate_out = nullptr;
+  void* dq = nullptr;
+  void* dk_ = nullptr;
+  void* dv_ = nullptr;
+  void* dla = nullptr;
+  void* dbe = nullptr;
+  void* dstate_in = nullptr;
+  int64_t N = 0, B = 0, T = 0;
+  int H = 0, Hk = 0, dk = 0, dv = 0;
+  bool gate_io = false;  // gates in the io dtype, not the compute type
+  double scale = 1.0;
+  Str3 sq, sk, sv, sy, sg, sdq, sdk, sdv, sdy, sdg;
+  // token-serial kernels: states before every kSerialCk-th token
+  // [slot][H][dv][dk], slot = serial_slot() + chunk
+  void* ckpt = nullptr;
+  // token-serial backward: sums over 16 rows of S, [tiles][H][B*T][dk] and [tiles][H][B*T]
+  void* part_dq = nullptr;
+  void* part_dk = nullptr;
+  void* part_la = nullptr;
+  void* part_be = nullptr;
+  // step
+  const int32_t* slots = nullptr;
+  int64_t n_slots = 0;
+};
+
+// Slot of the first chunk of sequence n: sequences get consecutive, disjoint
+// runs of slots for any lengths (a sequence of `len` tokens from t0 needs
+// ceil(len / chunk) <= (t0 + len) / chunk - t0 / chunk + 1 of them).
+__host__ __device__ inline int64_t chunk_slot0(bool packed, int64_t n, int64_t t0, int64_t T, int chunk) {
+  return packed ? t0 / chunk + n : n * ((T + chunk - 1) / chunk);
+}
+inline int64_t chunk_slots(bool packed, int64_t N, int64_t T, int chunk) {
+  return packed ? T / chunk + N : N * ((T + chunk - 1) / chunk);
+}
+
+// Batch row, first token and length of sequence n; cu's values are clamped to
+// 0..T, so that a wrong table cannot lead outside the tensors.
+struct SeqRange {
+  int64_t b, t0, len;
+};
+__device__ __forceinline__ SeqRange seq_range(const int32_t* cu, int64_t n, int64_t T) {
+  if (!cu) return {n, 0, T};
+  int64_t lo = cu[n], hi = cu[n + 1];
+  lo = lo < 0 ? 0 : lo > T ? T : lo;
+  hi = hi < lo ? lo : hi > T ? T : hi;
+  return {0, lo, hi - lo};
+}
+
+constexpr int kSerialRows = 16;  // rows of S per work-group of the token-serial kernels
+inline int serial_ck(int io) { return io == IO_F64 ? 8 : 16; }
+hipError_t launch_delta_serial_fwd(int io, const DeltaArgs& a, hipStream_t s);
+hipError_t launch_delta_serial_bwd(int io, const DeltaArgs& a, hipStream_t s);
+hipError_t launch_delta_step(int io, const DeltaArgs& a, hipStream_t s);
+
+// Norms of queries and keys with the rotation.
+struct QkArgs {
+  const void* x[2];    // q, k
+  const void* w[2];
+  void* out[2];        // forward: normed rows; backward: dq, dk
+  const void* dout[2]; // backward: gradients of the normed rows
+  Str3 sx[2], so[2], sdo[2];
+  int Hn[2];
+  double scale[2];
+  const void* cos;
+  const void* sin;
+  const int32_t* pos;
+  int64_t B, T, n_pos, pos0;
+  int d, rot;
+  bool interleaved;
+  double eps;
+  void* part;          // backward: [2][groups][d] sums for dw
+  void* dw[2];
+  int64_t n_part;      // work-groups (parts)
+  int hpg;             // heads per group of lanes (vector kernels)
+};
+// Work-groups of the backward (parts of the dw sums) for B*T tokens.
+int64_t qknorm_bwd_parts(int io, const QkArgs& a);
+hipError_t launch_qknorm_fwd(int io, const QkArgs& a, hipStream_t s);
+hipError_t launch_qknorm_bwd(int io, const QkArgs& a, hipStream_t s);
+
+}  // namespace gls

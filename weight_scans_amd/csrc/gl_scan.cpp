@@ -290,6 +290,11 @@ gls::DecArgs dec_args(const gl_scan_desc_t* d) {
 
 }  // namespace
 
+namespace gls {
+// Text of gl_last_error() for the library's other host files.
+void set_last_error(const char* text) { set_err("%s", text); }
+}  // namespace gls
+
 extern "C" {
 
 gl_status_t gl_scan_saved_size(const gl_scan_desc_t* desc, size_t* saved_bytes) {

@@ -9,6 +9,9 @@
 
 namespace gls {
 
+// Text of gl_last_error() on the calling thread (gl_scan.cpp).
+void set_last_error(const char* text);
+
 enum IoType { IO_F64 = 0, IO_F32 = 1, IO_BF16 = 2 };
 
 // Forward scan.  One work-group owns one (b, h) and a tile of rows of the
