@@ -83,6 +83,54 @@ hipError_t launch_delta_serial_fwd(int io, const DeltaArgs& a, hipStream_t s);
 hipError_t launch_delta_serial_bwd(int io, const DeltaArgs& a, hipStream_t s);
 hipError_t launch_delta_step(int io, const DeltaArgs& a, hipStream_t s);
 
+// Chunked matrix-core path (bf16, dk and dv multiples of 8, at most 128).  Per
+// chunk of 64 tokens and value head (record = slot * H + h) the preparation
+// leaves, as fragments of 64 lanes x 8 bf16 in the order in which the
+// recurrences use them:
+//   yf   Y  = (I + L beta)^-1 L, rows i     [6 blocks][hi, lo]
+//   pf   P  = scale (decayed q_i.k_j), rows i   [6][hi, lo]
+//   ytf, ptf   the same with rows j         [6][hi, lo] each (training)
+// and gates [5][64] fp32: e^l, beta, e^(l_C - l), and the cumulative log2
+// decay l in two parts (whole and fraction).  The recurrences leave (training),
+// as pieces of 64 lanes x 4 bf16 that the gradients take as operands:
+//   sf, lf   the state before, the adjoint after the chunk: piece (rt, kb) has
+//            element (lane (g, l), q) = S[16 rt + 4 g + q][16 kb + l]
+//   yb       y before its rounding: (rt, tb) has [lane (g, l)][4] fp32 = y[token 16 tb + l][16 rt + 4 g + q]
+//   st       the last state [N][H][dv][dk] fp32
+// and, as two fragments a row tile (row l in lanes, tokens in order; rows and
+// halves exchanged as raw_at says),
+//   ef, gf   e and dL/d(beta e)
+//   zf, bf   dL/dlog_alpha and dL/dbeta over the tile's rows [64] fp32
+constexpr int kDeltaChunk = 64;
+constexpr int kFrag = 512;                       // bf16 per fragment
+constexpr int kYf = 12 * kFrag;                  // per record
+constexpr int kGates = 5 * 64;
+constexpr int kPiece = 256;                      // bf16 per piece
+struct ChunkArgs {
+  DeltaArgs a;
+  uint16_t* yf = nullptr;
+  uint16_t* pf = nullptr;
+  uint16_t* ytf = nullptr;
+  uint16_t* ptf = nullptr;
+  float* gates = nullptr;
+  uint16_t* sf = nullptr;
+  uint16_t* ef = nullptr;
+  float* yb = nullptr;
+  float* st = nullptr;
+  float* zf = nullptr;
+  float* bf = nullptr;
+  uint16_t* lf = nullptr;
+  uint16_t* gf = nullptr;
+  int64_t slots = 0;    // chunk slots of the call
+};
+inline int delta_wide(int d) { return d <= 64 ? 64 : 128; }
+__host__ __device__ inline int delta_row_tiles(int dv) { return (dv + 31) / 32 * 2; }
+bool delta_chunk_ok(int io, const DeltaArgs& a);  // sizes and strides of q, k, v
+bool delta_rows_ok(const Str3& s, int d);         // strides of the other row tensors
+hipError_t launch_delta_prep(const ChunkArgs& c, hipStream_t s);
+hipError_t launch_delta_chunk_fwd(const ChunkArgs& c, hipStream_t s);
+hipError_t launch_delta_chunk_bwd(const ChunkArgs& c, hipStream_t s);
+
 // Norms of queries and keys with the rotation.
 struct QkArgs {
   const void* x[2];    // q, k

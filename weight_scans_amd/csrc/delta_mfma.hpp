@@ -1,0 +1,183 @@
+// delta_mfma.hpp -- fragments and LDS tiles of the chunked gated delta rule.
+//
+// Register chaining: the result layout of v_mfma_f32_16x16x32_bf16 (lane
+// (g, l) = (lane / 16, lane % 16) holds rows 4g..4g+3 of column l) becomes an
+// operand of the next product without leaving the registers, because the order
+// of the contraction index is free as long as both operands share it.  Two
+// results over rows 0..15 and 16..31 packed side by side give lane (g, l) the
+// rows {4g..4g+3, 16 + 4g..16 + 4g + 3} of column l; the other operand takes
+// the same eight positions of its row: two 8-byte LDS reads instead of one of
+// 16.  "Order O" below is this order within every 32.
+//
+// Two-term operands: x = hi + lo, both bf16 (round to nearest), keeps 16
+// significand bits; products with an exact bf16 operand take two matrix
+// instructions, products of two such operands three (lo lo is dropped).
+#pragma once
+
+#include "delta.hpp"
+#include "mfma.hpp"
+
+namespace gls {
+
+struct Pair8 {  // hi and lo fragments
+  bf16x8 hi, lo;
+};
+
+typedef uint32_t u32x4_t __attribute__((ext_vector_type(4)));
+__device__ __forceinline__ bf16x8 as_frag(uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
+  const u32x4_t v = {a, b, c, d};
+  return __builtin_bit_cast(bf16x8, v);
+}
+// Rounded fragment of two stacked results (order O).
+__device__ __forceinline__ bf16x8 round8(const f32x4& x, const f32x4& y) {
+  return as_frag(pack2(x[0], x[1]), pack2(x[2], x[3]), pack2(y[0], y[1]), pack2(y[2], y[3]));
+}
+__device__ __forceinline__ float lo16f(uint32_t u) { return __uint_as_float(u << 16); }
+__device__ __forceinline__ float hi16f(uint32_t u) { return __uint_as_float(u & 0xffff0000u); }
+__device__ __forceinline__ Pair8 split8(const f32x4& x, const f32x4& y) {
+  const uint32_t a = pack2(x[0], x[1]), b = pack2(x[2], x[3]);
+  const uint32_t c = pack2(y[0], y[1]), d = pack2(y[2], y[3]);
+  Pair8 p;
+  p.hi = as_frag(a, b, c, d);
+  p.lo = as_frag(pack2(x[0] - lo16f(a), x[1] - hi16f(a)), pack2(x[2] - lo16f(b), x[3] - hi16f(b)),
+                 pack2(y[0] - lo16f(c), y[1] - hi16f(c)), pack2(y[2] - lo16f(d), y[3] - hi16f(d)));
+  return p;
+}
+
+// ---- LDS tiles [64][W] bf16, W in {16, 32, 64, 128}, in units of 8 bytes
+// (four elements) whose index within the row is XORed with flip(row).  Chosen
+// so that 32 lanes reading either 16 rows x 2 units (order-O fragments) or 8
+// rows x 4 units (transposing reads) touch each pair of the 64 banks once; bit
+// 0 stays, so that 16-byte loads keep their place.
+template <int W>
+__device__ __forceinline__ constexpr int flip(int r) {
+  if (W == 128) return ((r & 7) << 2) | (((r >> 3) & 1) << 1);
+  if (W == 64) return (((r >> 1) & 3) << 2) | (((r >> 3) & 1) << 1);
+  if (W == 32) return ((r >> 2) & 1) << 2;
+  return 0;
+}
+
+typedef __attribute__((address_space(3))) s16x4 lds_s16x4_t;
+__device__ __forceinline__ s16x4 tr4(const char* p) {
+  return __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4_t*)(p));
+}
+__device__ __forceinline__ bf16x8 join(const s16x4& a, const s16x4& b) {
+  return __builtin_bit_cast(bf16x8, __builtin_shufflevector(a, b, 0, 1, 2, 3, 4, 5, 6, 7));
+}
+__device__ __forceinline__ f32x4 widen(const s16x4& v) {
+  f32x4 f;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) f[i] = bf16_val(static_cast<uint16_t>(v[i]));
+  return f;
+}
+
+// Per-lane byte offsets into a tile: of an order-O fragment read (row l, unit
+// g) and of a transposing read (row 4g + l/4, unit l%4).
+template <int W>
+struct TileLane {
+  uint32_t o, t;
+};
+template <int W>
+__device__ __forceinline__ TileLane<W> tile_lane(int lane) {
+  const int l = lane & 15, g = lane >> 4, r = 4 * g + (l >> 2);
+  TileLane<W> x;
+  x.o = static_cast<uint32_t>(l * W * 2 + 8 * (g ^ flip<W>(l)));
+  x.t = static_cast<uint32_t>(r * W * 2 + 8 * ((l & 3) ^ flip<W>(r)));
+  return x;
+}
+// Rows 16 tb + l, columns 32 s.. in order O: an operand over the columns.
+template <int W>
+__device__ __forceinline__ bf16x8 frag_o(const char* tile, const TileLane<W>& x, int tb, int s) {
+  const char* p = tile + tb * 16 * W * 2;
+  const s16x4 a = *reinterpret_cast<const s16x4*>(p + (x.o ^ (8 * s * 8)));
+  const s16x4 b = *reinterpret_cast<const s16x4*>(p + (x.o ^ ((8 * s + 4) * 8)));
+  return join(a, b);
+}
+// Column 16 cb + l of rows 16 tb + 4g .. + 3 (a result-layout block).
+template <int W>
+__device__ __forceinline__ s16x4 col4(const char* tile, const TileLane<W>& x, int tb, int cb) {
+  return tr4(tile + tb * 16 * W * 2 + (x.t ^ (4 * cb * 8)));
+}
+// Column 16 cb + l of rows 32 s.. in order O: an operand over the rows.
+template <int W>
+__device__ __forceinline__ bf16x8 frag_c(const char* tile, const TileLane<W>& x, int s, int cb) {
+  return join(col4<W>(tile, x, 2 * s, cb), col4<W>(tile, x, 2 * s + 1, cb));
+}
+
+// ---- turning a block: fragments as a wave wrote them (row l of the wave's 16
+// in lanes, order O of the other index) read back with that index in lanes.
+// Block b of 16 of the other index: lane (g, l) gets rows 4g..4g+3 of its
+// index 16 b + l.
+__device__ __forceinline__ s16x4 turned(const uint16_t* frags, int b, int lane) {
+  const int l = lane & 15, g = lane >> 4;
+  return tr4(reinterpret_cast<const char*>(frags + (b >> 1) * kFrag) + ((l & 3) * 16 + 4 * g + (l >> 2)) * 16 +
+             (b & 1) * 8);
+}
+
+// Fragments kept for a turned read later lie so that 32 lanes of that read meet
+// every pair of banks once: lane (g, l)'s 16 bytes at raw_at, its two halves
+// exchanged for g >= 2.
+__device__ __forceinline__ int raw_at(int lane) { return (lane ^ (8 * ((lane >> 4) & 1))) * 8; }
+__device__ __forceinline__ bf16x8 raw_order(const bf16x8& f, int lane) {
+  const u32x4_t v = __builtin_bit_cast(u32x4_t, f);
+  const bool x = lane >= 32;
+  return as_frag(x ? v[2] : v[0], x ? v[3] : v[1], x ? v[0] : v[2], x ? v[1] : v[3]);
+}
+// Byte offset of a turned read within a row tile's fragments, block b of 16.
+__device__ __forceinline__ uint32_t raw_turned(int lane) {
+  const int l = lane & 15, g = lane >> 4, u = l & 3, r = 4 * g + (l >> 2);
+  return static_cast<uint32_t>((u * 16 + (r ^ (8 * (u & 1)))) * 16 + 8 * (u >> 1));
+}
+__device__ __forceinline__ s16x4 turned_raw(const uint16_t* frags, uint32_t at, int b) {
+  return tr4(reinterpret_cast<const char*>(frags) + (b >> 1) * 1024 + (at ^ (8 * (b & 1))));
+}
+
+// Lane l of each row of 16 lanes gets the row's sum of x[l].  Each step pairs
+// lanes that differ in one bit of what they still have to choose between and
+// agree in what they have chosen (lane ^ 8, ^ 7, ^ 3, ^ 1).
+template <int CTRL, int N>
+__device__ __forceinline__ void row_sums_step(float (&x)[16], bool up) {
+#pragma unroll
+  for (int i = 0; i < N; ++i) {
+    const float give = up ? x[i] : x[i + N], keep = up ? x[i + N] : x[i];
+    x[i] = keep + dpp<CTRL>(0.f, give);
+  }
+}
+__device__ __forceinline__ float row_sums(float (&x)[16], int l) {
+  row_sums_step<0x128, 8>(x, l & 8);
+  row_sums_step<0x141, 4>(x, l & 4);
+  row_sums_step<0x1b, 2>(x, l & 2);
+  row_sums_step<0xb1, 1>(x, l & 1);
+  return x[0];
+}
+
+// ---- direct loads of a [64][W] tile: instruction n of a wave fills 64
+// consecutive 16-byte units.  Byte offset, from the chunk's first row, of what
+// lane `lane` loads; past the buffer's end (zeros) for columns past d.
+constexpr uint32_t kPastEnd = 0x7ffffff0u;
+template <int W>
+__device__ __forceinline__ uint32_t tile_off(int n, int lane, int64_t st, int c0, int d) {
+  constexpr int U = W / 8;
+  const int i = n * 64 + lane, r = i / U, u = (i % U) ^ (flip<W>(r) >> 1);
+  const int c = c0 + 8 * u;
+  return c < d ? static_cast<uint32_t>((r * st + c) * 2) : kPastEnd;
+}
+// Buffer over rows t0 .. t0 + 63 (those below len) of d columns, row stride st.
+__device__ __forceinline__ __amdgpu_buffer_rsrc_t rows_rsrc(const uint16_t* base, int64_t t0, int64_t len, int64_t st,
+                                                            int d) {
+  const int64_t n = len - t0 < 64 ? len - t0 : 64;
+  return buffer_rsrc(base + (n > 0 ? t0 * st : 0), n > 0 ? static_cast<int>(((n - 1) * st + d) * 2) : 0);
+}
+
+// Work-groups are dealt to the 8 XCDs in turn: all `tiles` of a sequence-head
+// get the same XCD (they share its chunks through the XCD's L2).  Returns
+// false past the end.
+__device__ __forceinline__ bool head_of_block(int64_t id, int tiles, int64_t heads, int64_t& head, int& tile) {
+  const int64_t j = id >> 3;
+  head = j / tiles * 8 + (id & 7);
+  tile = static_cast<int>(j % tiles);
+  return head < heads;
+}
+inline int64_t head_blocks(int64_t heads, int tiles) { return (heads + 7) / 8 * 8 * tiles; }
+
+}  // namespace gls

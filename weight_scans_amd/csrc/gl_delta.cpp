@@ -56,9 +56,32 @@ struct Plan {
   size_t align = 2;                     // of q, k, v, y and their gradients
   int64_t N = 0, tok = 0;
   bool packed = false;
+  bool chunk = false;                   // the chunked matrix-core path
+  int64_t slots = 0;                    // its chunk slots
   size_t saved = 0, fwd_ws = 0, bwd_ws = 0;  // bwd_ws: with `saved` given
+  size_t state_bytes = 0, err_bytes = 0, gate_bytes = 0, y_bytes = 0, last_bytes = 0, z_bytes = 0;
   const char* name = "";
 };
+
+gls::DeltaArgs base_args(const gl_delta_desc_t* d, const Plan& p) {
+  gls::DeltaArgs a;
+  a.N = p.N; a.B = d->B; a.T = d->T;
+  a.H = static_cast<int>(d->H); a.Hk = static_cast<int>(d->Hk);
+  a.dk = static_cast<int>(d->dk); a.dv = static_cast<int>(d->dv);
+  a.gate_io = d->gate_dtype == d->io_dtype;
+  a.scale = d->scale;
+  a.sq = dense(d->sq, d->Hk, d->T, d->dk);
+  a.sk = dense(d->sk, d->Hk, d->T, d->dk);
+  a.sv = dense(d->sv, d->H, d->T, d->dv);
+  a.sy = dense(d->sy, d->H, d->T, d->dv);
+  a.sg = dense(d->sg, d->H, d->T, 1);
+  a.sdq = dense(d->sdq, d->Hk, d->T, d->dk);
+  a.sdk = dense(d->sdk, d->Hk, d->T, d->dk);
+  a.sdv = dense(d->sdv, d->H, d->T, d->dv);
+  a.sdy = dense(d->sdy, d->H, d->T, d->dv);
+  a.sdg = dense(d->sdg, d->H, d->T, 1);
+  return a;
+}
 
 gl_status_t make_plan(const gl_delta_desc_t* d, Plan* p) {
   if (!d) return fail(GL_ERROR_INVALID_VALUE, "desc is NULL");
@@ -93,6 +116,28 @@ gl_status_t make_plan(const gl_delta_desc_t* d, Plan* p) {
   p->elem = p->io == GL_DTYPE_F64 ? 8 : p->io == GL_DTYPE_F32 ? 4 : 2;
   p->align = p->elem;
   const size_t dd = static_cast<size_t>(d->dk) * d->dv;
+  const gls::DeltaArgs a = base_args(d, *p);
+  if (!(d->flags & GL_FLAG_GENERIC) && gls::delta_chunk_ok(p->io, a)) {
+    p->chunk = true;
+    p->align = 16;
+    p->name = d->dk <= 64 ? (d->dv <= 64 ? "delta-mfma-bf16-64x64" : "delta-mfma-bf16-64x128")
+                          : (d->dv <= 64 ? "delta-mfma-bf16-128x64" : "delta-mfma-bf16-128x128");
+    p->slots = gls::chunk_slots(p->packed, p->N, d->T, gls::kDeltaChunk);
+    if (double(p->slots) * double(d->H) > 2147483647.0)
+      return fail(GL_ERROR_NOT_SUPPORTED, "chunks above the launch limits");
+    const size_t rec = static_cast<size_t>(p->slots) * d->H;
+    p->fwd_ws = 2 * round_up(rec * gls::kYf * 2);
+    p->state_bytes = round_up(rec * gls::delta_row_tiles(a.dv) * (gls::delta_wide(a.dk) / 16) * gls::kPiece * 2);
+    p->err_bytes = round_up(rec * 4 * gls::delta_row_tiles(a.dv) * gls::kPiece * 2);
+    p->gate_bytes = round_up(rec * gls::kGates * 4);
+    p->y_bytes = round_up(rec * gls::delta_row_tiles(a.dv) * 4096);
+    p->last_bytes = round_up(static_cast<size_t>(p->N) * d->H * dd * 4);
+    p->z_bytes = round_up(rec * gls::delta_row_tiles(a.dv) * 64 * 4);
+    p->saved = p->gate_bytes + 2 * round_up(rec * gls::kYf * 2) + p->state_bytes + p->err_bytes + p->y_bytes +
+               p->last_bytes;
+    p->bwd_ws = p->state_bytes + p->err_bytes + 2 * p->z_bytes;
+    return GL_SUCCESS;
+  }
   const int ck = gls::serial_ck(p->io);
   p->name = p->io == GL_DTYPE_F64 ? "delta-serial-f64" : p->io == GL_DTYPE_F32 ? "delta-serial-f32" : "delta-serial-bf16";
   if (d->segments > 1) return fail(GL_ERROR_NOT_SUPPORTED, "segments apply to the matrix-core kernels only");
@@ -102,31 +147,51 @@ gl_status_t make_plan(const gl_delta_desc_t* d, Plan* p) {
   return GL_SUCCESS;
 }
 
-gls::DeltaArgs base_args(const gl_delta_desc_t* d, const Plan& p) {
-  gls::DeltaArgs a;
-  a.N = p.N; a.B = d->B; a.T = d->T;
-  a.H = static_cast<int>(d->H); a.Hk = static_cast<int>(d->Hk);
-  a.dk = static_cast<int>(d->dk); a.dv = static_cast<int>(d->dv);
-  a.gate_io = d->gate_dtype == d->io_dtype;
-  a.scale = d->scale;
-  a.sq = dense(d->sq, d->Hk, d->T, d->dk);
-  a.sk = dense(d->sk, d->Hk, d->T, d->dk);
-  a.sv = dense(d->sv, d->H, d->T, d->dv);
-  a.sy = dense(d->sy, d->H, d->T, d->dv);
-  a.sg = dense(d->sg, d->H, d->T, 1);
-  a.sdq = dense(d->sdq, d->Hk, d->T, d->dk);
-  a.sdk = dense(d->sdk, d->Hk, d->T, d->dk);
-  a.sdv = dense(d->sdv, d->H, d->T, d->dv);
-  a.sdy = dense(d->sdy, d->H, d->T, d->dv);
-  a.sdg = dense(d->sdg, d->H, d->T, 1);
-  return a;
-}
-
 gl_status_t check_cu(const Plan& p, const int32_t* cu) {
   if (p.packed && !cu) return fail(GL_ERROR_INVALID_VALUE, "n_seq > 0 needs cu_seqlens");
   if (!p.packed && cu) return fail(GL_ERROR_INVALID_VALUE, "cu_seqlens needs n_seq > 0");
   if (reinterpret_cast<uintptr_t>(cu) & 3) return fail(GL_ERROR_MISALIGNED, "cu_seqlens not 4-byte aligned");
   return GL_SUCCESS;
+}
+
+struct Cut {  // runs of a workspace
+  char* at;
+  template <typename T>
+  void take(T*& p, size_t bytes) {
+    p = reinterpret_cast<T*>(at);
+    at += round_up(bytes);
+  }
+};
+
+// Chunked path: arguments with `saved` and the forward's workspace laid out.
+gls::ChunkArgs chunk_args(const gls::DeltaArgs& a, const Plan& p, void* saved, void* ws) {
+  gls::ChunkArgs c;
+  c.a = a;
+  c.slots = p.slots;
+  const size_t rec = static_cast<size_t>(p.slots) * a.H;
+  Cut w{static_cast<char*>(ws)};
+  if (ws) {
+    w.take(c.yf, rec * gls::kYf * 2);
+    w.take(c.pf, rec * gls::kYf * 2);
+  }
+  if (saved) {
+    Cut s{static_cast<char*>(saved)};
+    s.take(c.gates, p.gate_bytes);
+    s.take(c.ytf, rec * gls::kYf * 2);
+    s.take(c.ptf, rec * gls::kYf * 2);
+    s.take(c.sf, p.state_bytes);
+    s.take(c.ef, p.err_bytes);
+    s.take(c.yb, p.y_bytes);
+    s.take(c.st, p.last_bytes);
+  } else {
+    w.take(c.gates, p.gate_bytes);
+  }
+  return c;
+}
+
+gl_status_t chunk_fwd(const gls::ChunkArgs& c, hipStream_t s) {
+  const gl_status_t st = hip_status(gls::launch_delta_prep(c, s), "delta chunk preparation launch");
+  return st != GL_SUCCESS ? st : hip_status(gls::launch_delta_chunk_fwd(c, s), "delta forward launch");
 }
 
 gl_status_t check_ws(const void* ws, size_t have, size_t need) {
@@ -156,7 +221,8 @@ gl_status_t gl_delta_workspace_size(const gl_delta_desc_t* desc, int have_saved,
   const gl_status_t st = make_plan(desc, &p);
   if (st != GL_SUCCESS) return st;
   if (!fwd_ws_bytes || !bwd_ws_bytes) return fail(GL_ERROR_INVALID_VALUE, "size pointer is NULL");
-  *fwd_ws_bytes = p.fwd_ws;
+  // without `saved` the forward's gate factors are workspace too
+  *fwd_ws_bytes = p.fwd_ws + (have_saved ? 0 : p.gate_bytes);
   *bwd_ws_bytes = p.bwd_ws + (have_saved ? 0 : p.saved + p.fwd_ws);
   return GL_SUCCESS;
 }
@@ -173,11 +239,16 @@ gl_status_t gl_delta_fwd(const gl_delta_desc_t* desc, const void* q, const void*
   if (p.tok > 0 && (st = check_ptrs(true, {q, k, v, y}, p.align)) != GL_SUCCESS) return st;
   if (p.tok > 0 && (st = check_ptrs(true, {log_alpha, beta}, p.gate)) != GL_SUCCESS) return st;
   if ((st = check_ptrs(false, {state_in, state_out, saved})) != GL_SUCCESS) return st;
-  if ((st = check_ws(ws, ws_bytes, p.fwd_ws)) != GL_SUCCESS) return st;
+  if ((st = check_ws(ws, ws_bytes, p.fwd_ws + (saved ? 0 : p.gate_bytes))) != GL_SUCCESS) return st;
   if (p.tok == 0 && !state_out) return GL_SUCCESS;
   gls::DeltaArgs a = base_args(desc, p);
   a.q = q; a.k = k; a.v = v; a.la = log_alpha; a.be = beta;
   a.state_in = state_in; a.cu = cu_seqlens; a.y = y; a.state_out = state_out; a.ckpt = saved;
+  if (p.chunk) {
+    if (p.tok > 0 && !gls::delta_rows_ok(a.sy, a.dv))
+      return fail(GL_ERROR_NOT_SUPPORTED, "strides of y: multiples of 8, rows apart");
+    return chunk_fwd(chunk_args(a, p, saved, ws), static_cast<hipStream_t>(stream));
+  }
   return hip_status(gls::launch_delta_serial_fwd(p.io, a, static_cast<hipStream_t>(stream)), "delta forward launch");
 }
 
@@ -201,21 +272,37 @@ gl_status_t gl_delta_bwd(const gl_delta_desc_t* desc, const void* q, const void*
   a.q = q; a.k = k; a.v = v; a.la = log_alpha; a.be = beta;
   a.state_in = state_in; a.cu = cu_seqlens; a.dy = dy; a.dstate_out = dstate_out;
   a.dq = dq; a.dk_ = dk; a.dv_ = dv; a.dla = dlog_alpha; a.dbe = dbeta; a.dstate_in = dstate_in;
-  char* w = static_cast<char*>(ws);
-  const auto take = [&w](size_t bytes) {
-    char* at = w;
-    w += round_up(bytes);
-    return static_cast<void*>(at);
-  };
   const hipStream_t s = static_cast<hipStream_t>(stream);
+  Cut w{static_cast<char*>(ws)};
+  if (p.chunk) {
+    if (p.tok > 0 && !(gls::delta_rows_ok(a.sdy, a.dv) && gls::delta_rows_ok(a.sdv, a.dv) &&
+                       gls::delta_rows_ok(a.sdq, a.dk) && gls::delta_rows_ok(a.sdk, a.dk)))
+      return fail(GL_ERROR_NOT_SUPPORTED, "strides of dy, dq, dk, dv: multiples of 8, rows apart");
+    uint16_t *lf, *gf;
+    float *zf, *bf;
+    char *again, *fws;
+    w.take(lf, p.state_bytes);
+    w.take(gf, p.err_bytes);
+    w.take(zf, p.z_bytes);
+    w.take(bf, p.z_bytes);
+    w.take(again, saved ? 0 : p.saved);
+    w.take(fws, saved ? 0 : p.fwd_ws);
+    gls::ChunkArgs c = chunk_args(a, p, saved ? const_cast<void*>(saved) : again, saved ? nullptr : fws);
+    if (!saved && (st = chunk_fwd(c, s)) != GL_SUCCESS) return st;  // a.y and a.state_out NULL: what is saved only
+    c.lf = lf;
+    c.gf = gf;
+    c.zf = zf;
+    c.bf = bf;
+    return hip_status(gls::launch_delta_chunk_bwd(c, s), "delta backward launch");
+  }
   const size_t tiles = (desc->dv + gls::kSerialRows - 1) / gls::kSerialRows;
-  a.part_dq = take(tiles * desc->H * p.tok * desc->dk * p.comp);
-  a.part_dk = take(tiles * desc->H * p.tok * desc->dk * p.comp);
-  a.part_la = take(tiles * desc->H * p.tok * p.comp);
-  a.part_be = take(tiles * desc->H * p.tok * p.comp);
+  w.take(a.part_dq, tiles * desc->H * p.tok * desc->dk * p.comp);
+  w.take(a.part_dk, tiles * desc->H * p.tok * desc->dk * p.comp);
+  w.take(a.part_la, tiles * desc->H * p.tok * p.comp);
+  w.take(a.part_be, tiles * desc->H * p.tok * p.comp);
   a.ckpt = const_cast<void*>(saved);
   if (!saved && p.saved) {
-    a.ckpt = take(p.saved);
+    w.take(a.ckpt, p.saved);
     st = hip_status(gls::launch_delta_serial_fwd(p.io, a, s), "delta states launch");  // a.y NULL: states only
     if (st != GL_SUCCESS) return st;
   }

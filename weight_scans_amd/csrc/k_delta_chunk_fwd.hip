@@ -1,0 +1,320 @@
+// k_delta_chunk_fwd.hip -- the gated delta rule over the chunks of a sequence,
+// forward (bf16 on the matrix cores).  Per chunk, with S the state before it:
+//
+//   R = V - e^l (K S^T),  E = R - Y (beta R),  U = beta E
+//   y = scale e^l (Q S^T) + P U,   S <- e^(l_C) S + U^T (e^(l_C - l) K)
+//
+// The rows of S are independent, so one wave carries 16 of them through the
+// whole sequence without meeting another: S^T stays in its accumulators, and
+// every product's result is the next product's operand in registers (see
+// delta_mfma.hpp); only the chunk's K, V and Y come from outside.  Operands that
+// are not exact bf16 inputs are split into two bf16 terms.
+//
+// A work-group is NW state waves, NW output waves (they get S and U of the
+// chunk before through LDS and form y one chunk behind, so that y is off the
+// chain) and two waves that keep the direct loads of the next two chunks in
+// flight: one barrier per chunk.
+#include "delta_mfma.hpp"
+#include "dev_common.hpp"
+
+namespace gls {
+namespace {
+
+template <int DK, int NW>
+struct FwdLds {
+  static constexpr int NS = DK / 32, VW = 16 * NW;
+  alignas(16) char k[3][64 * DK * 2];
+  alignas(16) char q[3][64 * DK * 2];
+  alignas(16) char v[3][64 * VW * 2];
+  alignas(16) float gt[3][192];
+  alignas(16) uint16_t sx[2][NW][2 * NS * kFrag];  // hi, then lo
+  alignas(16) uint16_t ux[2][NW][4 * kFrag];
+};
+
+template <int DK, int NW, bool SAVE>
+__global__ __launch_bounds__(64 * (2 * NW + 2)) void delta_chunk_fwd(ChunkArgs ca) {
+  const DeltaArgs& a = ca.a;
+  constexpr int NS = DK / 32, NB = DK / 16, VW = 16 * NW;
+  __shared__ FwdLds<DK, NW> lds;
+  const int lane = threadIdx.x & 63, l = lane & 15, g = lane >> 4;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int tiles = (a.dv + VW - 1) / VW;
+  int64_t head;
+  int tile;
+  if (!head_of_block(blockIdx.x, tiles, a.N * a.H, head, tile)) return;
+  const int h = static_cast<int>(head % a.H);
+  const int64_t n = head / a.H;
+  const int hk = h / (a.H / a.Hk), r0 = tile * VW;
+  const SeqRange sr = seq_range(a.cu, n, a.T);
+  const int nc = static_cast<int>((sr.len + kDeltaChunk - 1) / kDeltaChunk);
+  const int64_t slot0 = chunk_slot0(a.cu != nullptr, n, sr.t0, a.T, kDeltaChunk);
+  const int64_t rec0 = slot0 * a.H + h;
+
+  if (wave == 2 * NW) {  // ---- loads: K, V and gates, two chunks ahead
+    constexpr int NK = DK / 8, NV = VW / 8, PER = NK + NV + 3;
+    const uint16_t* kp = static_cast<const uint16_t*>(a.k) + sr.b * a.sk.b + hk * a.sk.h + sr.t0 * a.sk.t;
+    const uint16_t* vp = static_cast<const uint16_t*>(a.v) + sr.b * a.sv.b + h * a.sv.h + sr.t0 * a.sv.t + r0;
+    uint32_t ko[NK], vo[NV];
+#pragma unroll
+    for (int i = 0; i < NK; ++i) ko[i] = tile_off<DK>(i, lane, a.sk.t, 0, a.dk);
+#pragma unroll
+    for (int i = 0; i < NV; ++i) vo[i] = tile_off<VW>(i, lane, a.sv.t, 0, a.dv - r0);
+    const auto issue = [&](int c) {
+      const bool in = c < nc;
+      const int s = c % 3;
+      const __amdgpu_buffer_rsrc_t rk = rows_rsrc(kp, c * 64LL, in ? sr.len : 0, a.sk.t, a.dk);
+      const __amdgpu_buffer_rsrc_t rv = rows_rsrc(vp, c * 64LL, in ? sr.len : 0, a.sv.t, min(VW, a.dv - r0));
+      const __amdgpu_buffer_rsrc_t rg =
+          buffer_rsrc(ca.gates + (in ? (rec0 + static_cast<int64_t>(c) * a.H) * kGates : 0), in ? 768 : 0);
+#pragma unroll
+      for (int i = 0; i < NK; ++i) dma16(rk, ko[i], lds.k[s] + i * 1024);
+#pragma unroll
+      for (int i = 0; i < NV; ++i) dma16(rv, vo[i], lds.v[s] + i * 1024);
+#pragma unroll
+      for (int i = 0; i < 3; ++i) dma4(rg, (i * 64 + lane) * 4, lds.gt[s] + i * 64);
+    };
+    issue(0);
+    issue(1);
+    for (int c = 0; c <= nc; ++c) {
+      wait_vm<PER>();  // chunk c is there, c + 1 in flight
+      lds_barrier();
+      issue(c + 2);    // into the slot of chunk c - 1
+    }
+    wait_vm<0>();
+    return;
+  }
+  if (wave == 2 * NW + 1) {  // ---- loads: Q, used one step later
+    constexpr int NK = DK / 8;
+    const uint16_t* qp = static_cast<const uint16_t*>(a.q) + sr.b * a.sq.b + hk * a.sq.h + sr.t0 * a.sq.t;
+    uint32_t qo[NK];
+#pragma unroll
+    for (int i = 0; i < NK; ++i) qo[i] = tile_off<DK>(i, lane, a.sq.t, 0, a.dk);
+    const auto issue = [&](int c) {
+      const __amdgpu_buffer_rsrc_t rq = rows_rsrc(qp, c * 64LL, c < nc ? sr.len : 0, a.sq.t, a.dk);
+#pragma unroll
+      for (int i = 0; i < NK; ++i) dma16(rq, qo[i], lds.q[c % 3] + i * 1024);
+    };
+    issue(0);
+    lds_barrier();
+    issue(1);
+    for (int c = 0; c < nc; ++c) {
+      wait_vm<NK>();   // chunk c is there, c + 1 in flight
+      lds_barrier();   // step c + 1: the output waves take chunk c
+      issue(c + 2);    // into the slot of chunk c - 1
+    }
+    wait_vm<0>();
+    return;
+  }
+
+  const TileLane<DK> tk = tile_lane<DK>(lane);
+  if (wave >= NW) {  // ---- outputs, one chunk behind
+    const int w = wave - NW;
+    const int rr = r0 + 16 * w + 4 * g;
+    uint16_t* yp = static_cast<uint16_t*>(a.y) + sr.b * a.sy.b + h * a.sy.h + sr.t0 * a.sy.t + rr;
+    const float sc = static_cast<float>(a.scale);
+    const int rt = tile * NW + w, n_rt = delta_row_tiles(a.dv);
+    bf16x8 pf[12];
+    float gs[4];
+    const auto fetch = [&](int c) {
+      const int64_t rec = rec0 + static_cast<int64_t>(c) * a.H;
+#pragma unroll
+      for (int f = 0; f < 12; ++f)
+        pf[f] = *reinterpret_cast<const bf16x8*>(ca.pf + rec * kYf + f * kFrag + lane * 8);
+#pragma unroll
+      for (int tb = 0; tb < 4; ++tb) gs[tb] = sc * ca.gates[rec * kGates + 16 * tb + l];
+    };
+    if (nc > 0) fetch(0);
+    lds_barrier();
+    for (int c = 0; c < nc; ++c) {
+      lds_barrier();
+      const char* qt = lds.q[c % 3];
+      const uint16_t* sx = lds.sx[c & 1][w];
+      const uint16_t* ux = lds.ux[c & 1][w];
+      f32x4 o[4];
+#pragma unroll
+      for (int tb = 0; tb < 4; ++tb) o[tb] = zero4();
+#pragma unroll
+      for (int s = 0; s < NS; ++s) {
+        const bf16x8 sh = *reinterpret_cast<const bf16x8*>(sx + s * kFrag + lane * 8);
+        const bf16x8 sl = *reinterpret_cast<const bf16x8*>(sx + (NS + s) * kFrag + lane * 8);
+#pragma unroll
+        for (int tb = 0; tb < 4; ++tb) {
+          const bf16x8 qf = frag_o<DK>(qt, tk, tb, s);
+          o[tb] = mfma16x16x32(sl, qf, o[tb]);
+          o[tb] = mfma16x16x32(sh, qf, o[tb]);
+        }
+      }
+#pragma unroll
+      for (int tb = 0; tb < 4; ++tb)
+#pragma unroll
+        for (int q = 0; q < 4; ++q) o[tb][q] *= gs[tb];
+#pragma unroll
+      for (int s = 0; s < 2; ++s) {
+        const bf16x8 uh = *reinterpret_cast<const bf16x8*>(ux + s * kFrag + lane * 8);
+        const bf16x8 ul = *reinterpret_cast<const bf16x8*>(ux + (2 + s) * kFrag + lane * 8);
+#pragma unroll
+        for (int tb = 2 * s; tb < 4; ++tb) {
+          const int f = tb < 2 ? tb : 2 * tb - 2 + s;
+          o[tb] = mfma16x16x32(uh, pf[2 * f + 1], o[tb]);
+          o[tb] = mfma16x16x32(ul, pf[2 * f], o[tb]);
+          o[tb] = mfma16x16x32(uh, pf[2 * f], o[tb]);
+        }
+      }
+      if (c + 1 < nc) fetch(c + 1);
+      if constexpr (SAVE) {
+        const int64_t rec = rec0 + static_cast<int64_t>(c) * a.H;
+#pragma unroll
+        for (int b = 0; b < NB; ++b)
+          *reinterpret_cast<s16x4*>(ca.sf + ((rec * n_rt + rt) * NB + b) * kPiece + lane * 4) = turned(sx, b, lane);
+#pragma unroll
+        for (int tb = 0; tb < 4; ++tb)
+          *reinterpret_cast<f32x4*>(ca.yb + ((rec * n_rt + rt) * 4 + tb) * 256 + lane * 4) = o[tb];
+      }
+#pragma unroll
+      for (int tb = 0; tb < 4; ++tb) {
+        const int64_t t = 64LL * c + 16 * tb + l;
+        if (a.y && t < sr.len && rr < a.dv)
+          *reinterpret_cast<uint2*>(yp + t * a.sy.t) = make_uint2(pack2(o[tb][0], o[tb][1]), pack2(o[tb][2], o[tb][3]));
+      }
+    }
+    return;
+  }
+
+  // ---- states
+  const TileLane<VW> tv = tile_lane<VW>(lane);
+  const int r = r0 + 16 * wave + l;
+  const int64_t so = (head * a.dv + r) * a.dk + 4 * g;
+  f32x4 S[NB];
+#pragma unroll
+  for (int b = 0; b < NB; ++b)
+    S[b] = a.state_in && r < a.dv && 16 * b + 4 * g < a.dk
+               ? *reinterpret_cast<const f32x4*>(static_cast<const float*>(a.state_in) + so + 16 * b)
+               : zero4();
+  bf16x8 yf[12];
+  const auto fetch = [&](int c) {
+    const uint16_t* p = ca.yf + (rec0 + static_cast<int64_t>(c) * a.H) * kYf + lane * 8;
+#pragma unroll
+    for (int f = 0; f < 12; ++f) yf[f] = *reinterpret_cast<const bf16x8*>(p + f * kFrag);
+  };
+  if (nc > 0) fetch(0);
+  const int rt = tile * NW + wave, n_rt = delta_row_tiles(a.dv);
+  for (int c = 0; c < nc; ++c) {
+    Pair8 sp[NS];
+#pragma unroll
+    for (int s = 0; s < NS; ++s) sp[s] = split8(S[2 * s], S[2 * s + 1]);
+    lds_barrier();
+    const int sl = c % 3;
+    const char* kt = lds.k[sl];
+#pragma unroll
+    for (int s = 0; s < NS; ++s) {
+      *reinterpret_cast<bf16x8*>(&lds.sx[c & 1][wave][s * kFrag + lane * 8]) = sp[s].hi;
+      *reinterpret_cast<bf16x8*>(&lds.sx[c & 1][wave][(NS + s) * kFrag + lane * 8]) = sp[s].lo;
+    }
+    f32x4 E[4];
+#pragma unroll
+    for (int tb = 0; tb < 4; ++tb) E[tb] = zero4();
+#pragma unroll
+    for (int s = 0; s < NS; ++s)
+#pragma unroll
+      for (int tb = 0; tb < 4; ++tb) {
+        const bf16x8 kf = frag_o<DK>(kt, tk, tb, s);
+        E[tb] = mfma16x16x32(kf, sp[s].hi, E[tb]);
+        E[tb] = mfma16x16x32(kf, sp[s].lo, E[tb]);
+      }
+    f32x4 be[4], Z[4];
+#pragma unroll
+    for (int tb = 0; tb < 4; ++tb) {
+      const f32x4 gm = *reinterpret_cast<const f32x4*>(&lds.gt[sl][16 * tb + 4 * g]);
+      be[tb] = *reinterpret_cast<const f32x4*>(&lds.gt[sl][64 + 16 * tb + 4 * g]);
+      const f32x4 v = widen(col4<VW>(lds.v[sl], tv, tb, wave));
+#pragma unroll
+      for (int q = 0; q < 4; ++q) {
+        E[tb][q] = v[q] - gm[q] * E[tb][q];
+        Z[tb][q] = be[tb][q] * E[tb][q];
+      }
+    }
+    const float whole = lds.gt[sl][63];
+#pragma unroll
+    for (int b = 0; b < NB; ++b)
+#pragma unroll
+      for (int q = 0; q < 4; ++q) S[b][q] *= whole;
+    {
+      const Pair8 z0 = split8(Z[0], Z[1]), z1 = split8(Z[2], Z[3]);
+#pragma unroll
+      for (int ib = 0; ib < 4; ++ib) {
+        f32x4 x = zero4();
+#pragma unroll
+        for (int s = 0; s <= ib / 2; ++s) {
+          const int f = ib < 2 ? ib : 2 * ib - 2 + s;
+          const Pair8& z = s ? z1 : z0;
+          x = mfma16x16x32(yf[2 * f + 1], z.hi, x);
+          x = mfma16x16x32(yf[2 * f], z.lo, x);
+          x = mfma16x16x32(yf[2 * f], z.hi, x);
+        }
+#pragma unroll
+        for (int q = 0; q < 4; ++q) E[ib][q] -= x[q];
+      }
+    }
+    if (c + 1 < nc) fetch(c + 1);
+    uint16_t* ux = lds.ux[c & 1][wave];
+    if constexpr (SAVE) {
+      const int64_t rec = rec0 + static_cast<int64_t>(c) * a.H;
+#pragma unroll
+      for (int s = 0; s < 2; ++s)
+        *reinterpret_cast<bf16x8*>(ca.ef + ((rec * n_rt + rt) * 2 + s) * kFrag + raw_at(lane)) =
+            raw_order(round8(E[2 * s], E[2 * s + 1]), lane);
+    }
+#pragma unroll
+    for (int tb = 0; tb < 4; ++tb)
+#pragma unroll
+      for (int q = 0; q < 4; ++q) E[tb][q] *= be[tb][q];
+#pragma unroll
+    for (int s = 0; s < 2; ++s) {
+      const Pair8 u = split8(E[2 * s], E[2 * s + 1]);
+      *reinterpret_cast<bf16x8*>(ux + s * kFrag + lane * 8) = u.hi;
+      *reinterpret_cast<bf16x8*>(ux + (2 + s) * kFrag + lane * 8) = u.lo;
+    }
+#pragma unroll
+    for (int tb = 0; tb < 4; ++tb) {
+      const f32x4 rs = *reinterpret_cast<const f32x4*>(&lds.gt[sl][128 + 16 * tb + 4 * g]);
+#pragma unroll
+      for (int q = 0; q < 4; ++q) E[tb][q] *= rs[q];
+    }
+    const Pair8 u0 = split8(E[0], E[1]), u1 = split8(E[2], E[3]);
+#pragma unroll
+    for (int b = 0; b < NB; ++b) {
+      const bf16x8 k0 = frag_c<DK>(kt, tk, 0, b), k1 = frag_c<DK>(kt, tk, 1, b);
+      S[b] = mfma16x16x32(k0, u0.hi, S[b]);
+      S[b] = mfma16x16x32(k0, u0.lo, S[b]);
+      S[b] = mfma16x16x32(k1, u1.hi, S[b]);
+      S[b] = mfma16x16x32(k1, u1.lo, S[b]);
+    }
+  }
+  lds_barrier();
+  if (r < a.dv) {
+#pragma unroll
+    for (int b = 0; b < NB; ++b)
+      if (16 * b + 4 * g < a.dk) {
+        if (a.state_out) *reinterpret_cast<f32x4*>(static_cast<float*>(a.state_out) + so + 16 * b) = S[b];
+        if constexpr (SAVE) *reinterpret_cast<f32x4*>(ca.st + so + 16 * b) = S[b];
+      }
+  }
+}
+
+template <int DK, int NW>
+hipError_t launch(const ChunkArgs& c, hipStream_t s) {
+  const int tiles = (c.a.dv + 16 * NW - 1) / (16 * NW);
+  const dim3 grid(static_cast<unsigned>(head_blocks(c.a.N * c.a.H, tiles)));
+  if (c.sf) delta_chunk_fwd<DK, NW, true><<<grid, 64 * (2 * NW + 2), 0, s>>>(c);
+  else delta_chunk_fwd<DK, NW, false><<<grid, 64 * (2 * NW + 2), 0, s>>>(c);
+  return hipGetLastError();
+}
+
+}  // namespace
+
+hipError_t launch_delta_chunk_fwd(const ChunkArgs& c, hipStream_t s) {
+  if (c.a.N * c.a.H == 0) return hipSuccess;
+  return c.a.dk <= 64 ? launch<64, 2>(c, s) : launch<128, 2>(c, s);
+}
+
+}  // namespace gls
