@@ -94,8 +94,8 @@ hipError_t launch_delta_step(int io, const DeltaArgs& a, hipStream_t s);
 // decay l in two parts (whole and fraction).  The recurrences leave (training),
 // as pieces of 64 lanes x 4 bf16 that the gradients take as operands:
 //   sf, lf   the state before, the adjoint after the chunk: piece (rt, kb) has
-//            element (lane (g, l), q) = S[16 rt + 4 g + q][16 kb + l]
-//   yb       y before its rounding: (rt, tb) has [lane (g, l)][4] fp32 = y[token 16 tb + l][16 rt + 4 g + q]
+//            element (lane (g, l), q) = S[index(rt, 4 g + q)][index(kb, l)]  (delta_mfma.hpp)
+//   yb       y before its rounding: (rt, tb) has [lane (g, l)][4] fp32 = y[token 16 tb + l][index(rt, 4 g + q)]
 //   st       the last state [N][H][dv][dk] fp32
 // and, as two fragments a row tile (row l in lanes, tokens in order; rows and
 // halves exchanged as raw_at says),

@@ -4,10 +4,12 @@
 // (g, l) = (lane / 16, lane % 16) holds rows 4g..4g+3 of column l) becomes an
 // operand of the next product without leaving the registers, because the order
 // of the contraction index is free as long as both operands share it.  Two
-// results over rows 0..15 and 16..31 packed side by side give lane (g, l) the
-// rows {4g..4g+3, 16 + 4g..16 + 4g + 3} of column l; the other operand takes
-// the same eight positions of its row: two 8-byte LDS reads instead of one of
-// 16.  "Order O" below is this order within every 32.
+// stacked results (h = 0, 1) give lane (g, l) the rows 4g + q of both as eight
+// values (h, q): "order O".  So that the other operand is one 16-byte read of
+// eight neighbouring columns, the indices k and r of a state are not taken in
+// blocks of 16 as they come: row 4g + q of block 2s + h is
+//     index(2s + h, 4g + q) = 32 s + 8 g + 4 h + q.
+// Tokens keep their order (their operands are prepared in order O).
 //
 // Two-term operands: x = hi + lo, both bf16 (round to nearest), keeps 16
 // significand bits; products with an exact bf16 operand take two matrix
@@ -44,19 +46,9 @@ __device__ __forceinline__ Pair8 split8(const f32x4& x, const f32x4& y) {
   return p;
 }
 
-// ---- LDS tiles [64][W] bf16, W in {16, 32, 64, 128}, in units of 8 bytes
-// (four elements) whose index within the row is XORed with flip(row).  Chosen
-// so that 32 lanes reading either 16 rows x 2 units (order-O fragments) or 8
-// rows x 4 units (transposing reads) touch each pair of the 64 banks once; bit
-// 0 stays, so that 16-byte loads keep their place.
-template <int W>
-__device__ __forceinline__ constexpr int flip(int r) {
-  if (W == 128) return ((r & 7) << 2) | (((r >> 3) & 1) << 1);
-  if (W == 64) return (((r >> 1) & 3) << 2) | (((r >> 3) & 1) << 1);
-  if (W == 32) return ((r >> 2) & 1) << 2;
-  return 0;
-}
-
+// ---- LDS tiles [64][W] bf16, W in {32, 64, 128}: 16-byte groups XORed with
+// swz<W>(row), which makes the 16-byte operand reads conflict-free; the
+// transposing reads (four 8-byte halves of neighbouring groups) are two-way.
 typedef __attribute__((address_space(3))) s16x4 lds_s16x4_t;
 __device__ __forceinline__ s16x4 tr4(const char* p) {
   return __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4_t*)(p));
@@ -65,14 +57,17 @@ __device__ __forceinline__ bf16x8 join(const s16x4& a, const s16x4& b) {
   return __builtin_bit_cast(bf16x8, __builtin_shufflevector(a, b, 0, 1, 2, 3, 4, 5, 6, 7));
 }
 __device__ __forceinline__ f32x4 widen(const s16x4& v) {
+  const u32x2_t u = __builtin_bit_cast(u32x2_t, v);
   f32x4 f;
-#pragma unroll
-  for (int i = 0; i < 4; ++i) f[i] = bf16_val(static_cast<uint16_t>(v[i]));
+  f[0] = __uint_as_float(u[0] << 16);
+  f[1] = __uint_as_float(u[0] & 0xffff0000u);
+  f[2] = __uint_as_float(u[1] << 16);
+  f[3] = __uint_as_float(u[1] & 0xffff0000u);
   return f;
 }
 
-// Per-lane byte offsets into a tile: of an order-O fragment read (row l, unit
-// g) and of a transposing read (row 4g + l/4, unit l%4).
+// Per-lane byte offsets into a tile: of an operand read (row l, group g) and of
+// a transposing read (row 4g + l/4, group l%4).
 template <int W>
 struct TileLane {
   uint32_t o, t;
@@ -81,33 +76,37 @@ template <int W>
 __device__ __forceinline__ TileLane<W> tile_lane(int lane) {
   const int l = lane & 15, g = lane >> 4, r = 4 * g + (l >> 2);
   TileLane<W> x;
-  x.o = static_cast<uint32_t>(l * W * 2 + 8 * (g ^ flip<W>(l)));
-  x.t = static_cast<uint32_t>(r * W * 2 + 8 * ((l & 3) ^ flip<W>(r)));
+  x.o = static_cast<uint32_t>(l * W * 2 + 16 * (g ^ swz<W>(l)));
+  x.t = static_cast<uint32_t>(r * W * 2 + 16 * ((l & 3) ^ swz<W>(r)));
   return x;
 }
-// Rows 16 tb + l, columns 32 s.. in order O: an operand over the columns.
+// Rows 16 tb + l, blocks 2s and 2s + 1 of the columns: an operand over them.
 template <int W>
-__device__ __forceinline__ bf16x8 frag_o(const char* tile, const TileLane<W>& x, int tb, int s) {
-  const char* p = tile + tb * 16 * W * 2;
-  const s16x4 a = *reinterpret_cast<const s16x4*>(p + (x.o ^ (8 * s * 8)));
-  const s16x4 b = *reinterpret_cast<const s16x4*>(p + (x.o ^ ((8 * s + 4) * 8)));
-  return join(a, b);
+__device__ __forceinline__ bf16x8 frag_n(const char* tile, const TileLane<W>& x, int tb, int s) {
+  return *reinterpret_cast<const bf16x8*>(tile + tb * 16 * W * 2 + (x.o ^ (64 * s)));
 }
-// Column 16 cb + l of rows 16 tb + 4g .. + 3 (a result-layout block).
+// Index l of block cb of the columns, rows 16 tb + 4g .. + 3 (result layout).
 template <int W>
 __device__ __forceinline__ s16x4 col4(const char* tile, const TileLane<W>& x, int tb, int cb) {
-  return tr4(tile + tb * 16 * W * 2 + (x.t ^ (4 * cb * 8)));
+  return tr4(tile + tb * 16 * W * 2 + (x.t ^ (64 * (cb >> 1))) + 8 * (cb & 1));
 }
-// Column 16 cb + l of rows 32 s.. in order O: an operand over the rows.
+// The same over rows 32 s.. in order O: an operand over the rows.
 template <int W>
 __device__ __forceinline__ bf16x8 frag_c(const char* tile, const TileLane<W>& x, int s, int cb) {
   return join(col4<W>(tile, x, 2 * s, cb), col4<W>(tile, x, 2 * s + 1, cb));
 }
+// Row 16 tb + l, indices 4g..4g+3 of block cb of the columns.
+template <int W>
+__device__ __forceinline__ s16x4 row4(const char* tile, const TileLane<W>& x, int tb, int cb) {
+  return *reinterpret_cast<const s16x4*>(tile + tb * 16 * W * 2 + (x.o ^ (64 * (cb >> 1))) + 8 * (cb & 1));
+}
+// First of the four indices that rows 4g..4g+3 of block b stand for.
+__device__ __forceinline__ int index4(int b, int g) { return 32 * (b >> 1) + 8 * g + 4 * (b & 1); }
+__device__ __forceinline__ int index1(int b, int l) { return index4(b, l >> 2) + (l & 3); }
 
 // ---- turning a block: fragments as a wave wrote them (row l of the wave's 16
 // in lanes, order O of the other index) read back with that index in lanes.
-// Block b of 16 of the other index: lane (g, l) gets rows 4g..4g+3 of its
-// index 16 b + l.
+// Block b of the other index: lane (g, l) gets rows 4g..4g+3 of its index l.
 __device__ __forceinline__ s16x4 turned(const uint16_t* frags, int b, int lane) {
   const int l = lane & 15, g = lane >> 4;
   return tr4(reinterpret_cast<const char*>(frags + (b >> 1) * kFrag) + ((l & 3) * 16 + 4 * g + (l >> 2)) * 16 +
@@ -158,7 +157,7 @@ constexpr uint32_t kPastEnd = 0x7ffffff0u;
 template <int W>
 __device__ __forceinline__ uint32_t tile_off(int n, int lane, int64_t st, int c0, int d) {
   constexpr int U = W / 8;
-  const int i = n * 64 + lane, r = i / U, u = (i % U) ^ (flip<W>(r) >> 1);
+  const int i = n * 64 + lane, r = i / U, u = (i % U) ^ swz<W>(r);
   const int c = c0 + 8 * u;
   return c < d ? static_cast<uint32_t>((r * st + c) * 2) : kPastEnd;
 }

@@ -159,13 +159,13 @@ __global__ __launch_bounds__(64 * (2 * NW + 2)) void delta_chunk_rev(ChunkArgs c
     };
     if (nc > 0) fetch(nc - 1);
     float z = 0.f;  // <dL/dS, S> after the chunk, over this wave's rows
-    if (a.dstate_out && r0 + 16 * w + l < a.dv) {
-      const int64_t so = (head * a.dv + r0 + 16 * w + l) * a.dk + 4 * g;
+    if (a.dstate_out && r0 + index1(w, l) < a.dv) {
+      const int64_t so = (head * a.dv + r0 + index1(w, l)) * a.dk;
 #pragma unroll
       for (int b = 0; b < NB; ++b)
-        if (16 * b + 4 * g < a.dk) {
-          const f32x4 u = *reinterpret_cast<const f32x4*>(static_cast<const float*>(a.dstate_out) + so + 16 * b);
-          const f32x4 s = *reinterpret_cast<const f32x4*>(ca.st + so + 16 * b);
+        if (index4(b, g) < a.dk) {
+          const f32x4 u = *reinterpret_cast<const f32x4*>(static_cast<const float*>(a.dstate_out) + so + index4(b, g));
+          const f32x4 s = *reinterpret_cast<const f32x4*>(ca.st + so + index4(b, g));
 #pragma unroll
           for (int q = 0; q < 4; ++q) z = fmaf(u[q], s[q], z);
         }
@@ -185,7 +185,7 @@ __global__ __launch_bounds__(64 * (2 * NW + 2)) void delta_chunk_rev(ChunkArgs c
         const int sl = i % 3;
 #pragma unroll
         for (int tb = 0; tb < 4; ++tb) {  // dy.y: token 16 tb + l
-          const f32x4 d = widen(*reinterpret_cast<const s16x4*>(lds.o[sl] + tb * 16 * VW * 2 + (to.o ^ (4 * w * 8))));
+          const f32x4 d = widen(row4<VW>(lds.o[sl], to, tb, w));
           const float x = sum_rows((d[0] * yb[tb][0] + d[1] * yb[tb][1]) + (d[2] * yb[tb][2] + d[3] * yb[tb][3]));
           if (g == 0) lds.dyy[w][i % 3][16 * tb + l] = x;
         }
@@ -233,13 +233,13 @@ __global__ __launch_bounds__(64 * (2 * NW + 2)) void delta_chunk_rev(ChunkArgs c
 
   // ---- adjoint states
   const TileLane<VW> tv = tile_lane<VW>(lane);
-  const int r = r0 + 16 * wave + l;
-  const int64_t so = (head * a.dv + r) * a.dk + 4 * g;
+  const int r = r0 + index1(wave, l);
+  const int64_t so = (head * a.dv + r) * a.dk;
   f32x4 S[NB];
 #pragma unroll
   for (int b = 0; b < NB; ++b)
-    S[b] = a.dstate_out && r < a.dv && 16 * b + 4 * g < a.dk
-               ? *reinterpret_cast<const f32x4*>(static_cast<const float*>(a.dstate_out) + so + 16 * b)
+    S[b] = a.dstate_out && r < a.dv && index4(b, g) < a.dk
+               ? *reinterpret_cast<const f32x4*>(static_cast<const float*>(a.dstate_out) + so + index4(b, g))
                : zero4();
   bf16x8 yf[12], ef[2];
   const int rt = tile * NW + wave, n_rt = delta_row_tiles(a.dv);
@@ -300,7 +300,7 @@ __global__ __launch_bounds__(64 * (2 * NW + 2)) void delta_chunk_rev(ChunkArgs c
     for (int s = 0; s < NS; ++s)
 #pragma unroll
       for (int tb = 0; tb < 4; ++tb) {
-        const bf16x8 kf = frag_o<DK>(kt, tk, tb, s);
+        const bf16x8 kf = frag_n<DK>(kt, tk, tb, s);
         G[tb] = mfma16x16x32(kf, sp[s].hi, G[tb]);
         G[tb] = mfma16x16x32(kf, sp[s].lo, G[tb]);
       }
@@ -383,8 +383,8 @@ __global__ __launch_bounds__(64 * (2 * NW + 2)) void delta_chunk_rev(ChunkArgs c
   if (a.dstate_in && r < a.dv) {
 #pragma unroll
     for (int b = 0; b < NB; ++b)
-      if (16 * b + 4 * g < a.dk)
-        *reinterpret_cast<f32x4*>(static_cast<float*>(a.dstate_in) + so + 16 * b) = S[b];
+      if (index4(b, g) < a.dk)
+        *reinterpret_cast<f32x4*>(static_cast<float*>(a.dstate_in) + so + index4(b, g)) = S[b];
   }
 }
 
@@ -508,7 +508,7 @@ __global__ __launch_bounds__(kGradThreads) void delta_chunk_grad(ChunkArgs ca) {
       f32x4 v = zero4(), v2 = zero4();
       for (int R = 0; R < nr; ++R) {
         if (!sym) {
-          const bf16x8 of = frag_o<DV>(lds.o, to, b < 10 ? y : x, R);
+          const bf16x8 of = frag_n<DV>(lds.o, to, b < 10 ? y : x, R);
           const bf16x8 ef = piece(lds.e, b < 10 ? x : y, R);
           v = b < 10 ? mfma16x16x32(ef, of, v) : mfma16x16x32(of, ef, v);
         } else {
@@ -533,7 +533,7 @@ __global__ __launch_bounds__(kGradThreads) void delta_chunk_grad(ChunkArgs ca) {
     }
     // ---- dv: row tiles w, w + 8, .. of 16 columns of v
     for (int rt = w; rt < n_rt; rt += 8) {
-      const int r = 16 * rt + 4 * g;
+      const int r = index4(rt, g);
 #pragma unroll
       for (int tb = 0; tb < 4; ++tb) {
         const int t = 16 * tb + l;
@@ -555,7 +555,7 @@ __global__ __launch_bounds__(kGradThreads) void delta_chunk_grad(ChunkArgs ca) {
       const bf16x8 sf = join(sp[2 * R], sp[2 * R + 1]), lf = join(lp[2 * R], lp[2 * R + 1]);
 #pragma unroll
       for (int t = 0; t < NT; ++t) {
-        a1[t] = mfma16x16x32(sf, frag_o<DV>(lds.o, to, tb0 + t, R), a1[t]);
+        a1[t] = mfma16x16x32(sf, frag_n<DV>(lds.o, to, tb0 + t, R), a1[t]);
         a2[t] = mfma16x16x32(lf, piece(lds.e, tb0 + t, R), a2[t]);
         a3[t] = mfma16x16x32(sf, piece(lds.g, tb0 + t, R), a3[t]);
       }
@@ -620,7 +620,7 @@ __global__ __launch_bounds__(kGradThreads) void delta_chunk_grad(ChunkArgs ca) {
   }
 #pragma unroll
   for (int t = 0; t < NT; ++t) {
-    const int tok = 16 * (tb0 + t) + l, col = 16 * kb + 4 * g;
+    const int tok = 16 * (tb0 + t) + l, col = index4(kb, g);
     if (tok < nt && col < a.dk) {
       const int64_t tt = sr.t0 + t0 + tok;
       *reinterpret_cast<uint2*>(static_cast<uint16_t*>(a.dq) + sr.b * a.sdq.b + hk * a.sdq.h + tt * a.sdq.t + col) =

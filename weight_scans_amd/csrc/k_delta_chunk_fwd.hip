@@ -109,7 +109,7 @@ __global__ __launch_bounds__(64 * (2 * NW + 2)) void delta_chunk_fwd(ChunkArgs c
   const TileLane<DK> tk = tile_lane<DK>(lane);
   if (wave >= NW) {  // ---- outputs, one chunk behind
     const int w = wave - NW;
-    const int rr = r0 + 16 * w + 4 * g;
+    const int rr = r0 + index4(w, g);
     uint16_t* yp = static_cast<uint16_t*>(a.y) + sr.b * a.sy.b + h * a.sy.h + sr.t0 * a.sy.t + rr;
     const float sc = static_cast<float>(a.scale);
     const int rt = tile * NW + w, n_rt = delta_row_tiles(a.dv);
@@ -121,7 +121,7 @@ __global__ __launch_bounds__(64 * (2 * NW + 2)) void delta_chunk_fwd(ChunkArgs c
       for (int f = 0; f < 12; ++f)
         pf[f] = *reinterpret_cast<const bf16x8*>(ca.pf + rec * kYf + f * kFrag + lane * 8);
 #pragma unroll
-      for (int tb = 0; tb < 4; ++tb) gs[tb] = sc * ca.gates[rec * kGates + 16 * tb + l];
+      for (int tb = 0; tb < 4; ++tb) gs[tb] = ca.gates[rec * kGates + 16 * tb + l];
     };
     if (nc > 0) fetch(0);
     lds_barrier();
@@ -139,15 +139,17 @@ __global__ __launch_bounds__(64 * (2 * NW + 2)) void delta_chunk_fwd(ChunkArgs c
         const bf16x8 sl = *reinterpret_cast<const bf16x8*>(sx + (NS + s) * kFrag + lane * 8);
 #pragma unroll
         for (int tb = 0; tb < 4; ++tb) {
-          const bf16x8 qf = frag_o<DK>(qt, tk, tb, s);
+          const bf16x8 qf = frag_n<DK>(qt, tk, tb, s);
           o[tb] = mfma16x16x32(sl, qf, o[tb]);
           o[tb] = mfma16x16x32(sh, qf, o[tb]);
         }
       }
 #pragma unroll
-      for (int tb = 0; tb < 4; ++tb)
+      for (int tb = 0; tb < 4; ++tb) {
+        const float f = sc * gs[tb];
 #pragma unroll
-        for (int q = 0; q < 4; ++q) o[tb][q] *= gs[tb];
+        for (int q = 0; q < 4; ++q) o[tb][q] *= f;
+      }
 #pragma unroll
       for (int s = 0; s < 2; ++s) {
         const bf16x8 uh = *reinterpret_cast<const bf16x8*>(ux + s * kFrag + lane * 8);
@@ -160,7 +162,7 @@ __global__ __launch_bounds__(64 * (2 * NW + 2)) void delta_chunk_fwd(ChunkArgs c
           o[tb] = mfma16x16x32(uh, pf[2 * f], o[tb]);
         }
       }
-      if (c + 1 < nc) fetch(c + 1);
+      fetch(min(c + 1, nc - 1));
       if constexpr (SAVE) {
         const int64_t rec = rec0 + static_cast<int64_t>(c) * a.H;
 #pragma unroll
@@ -182,121 +184,135 @@ __global__ __launch_bounds__(64 * (2 * NW + 2)) void delta_chunk_fwd(ChunkArgs c
 
   // ---- states
   const TileLane<VW> tv = tile_lane<VW>(lane);
-  const int r = r0 + 16 * wave + l;
-  const int64_t so = (head * a.dv + r) * a.dk + 4 * g;
+  const int r = r0 + index1(wave, l);
+  const int64_t so = (head * a.dv + r) * a.dk;
   f32x4 S[NB];
 #pragma unroll
   for (int b = 0; b < NB; ++b)
-    S[b] = a.state_in && r < a.dv && 16 * b + 4 * g < a.dk
-               ? *reinterpret_cast<const f32x4*>(static_cast<const float*>(a.state_in) + so + 16 * b)
+    S[b] = a.state_in && r < a.dv && index4(b, g) < a.dk
+               ? *reinterpret_cast<const f32x4*>(static_cast<const float*>(a.state_in) + so + index4(b, g))
                : zero4();
   bf16x8 yf[12];
-  const auto fetch = [&](int c) {
-    const uint16_t* p = ca.yf + (rec0 + static_cast<int64_t>(c) * a.H) * kYf + lane * 8;
+  const uint16_t* yp = ca.yf + rec0 * kYf + lane * 8;
 #pragma unroll
-    for (int f = 0; f < 12; ++f) yf[f] = *reinterpret_cast<const bf16x8*>(p + f * kFrag);
-  };
-  if (nc > 0) fetch(0);
+  for (int f = 0; f < 12; ++f)
+    if (nc > 0) yf[f] = *reinterpret_cast<const bf16x8*>(yp + f * kFrag);
   const int rt = tile * NW + wave, n_rt = delta_row_tiles(a.dv);
-  for (int c = 0; c < nc; ++c) {
-    Pair8 sp[NS];
+  Pair8 sp[NS];
 #pragma unroll
-    for (int s = 0; s < NS; ++s) sp[s] = split8(S[2 * s], S[2 * s + 1]);
+  for (int s = 0; s < NS; ++s) sp[s] = split8(S[2 * s], S[2 * s + 1]);
+  for (int c = 0; c < nc; ++c) {
     lds_barrier();
     const int sl = c % 3;
     const char* kt = lds.k[sl];
-#pragma unroll
-    for (int s = 0; s < NS; ++s) {
-      *reinterpret_cast<bf16x8*>(&lds.sx[c & 1][wave][s * kFrag + lane * 8]) = sp[s].hi;
-      *reinterpret_cast<bf16x8*>(&lds.sx[c & 1][wave][(NS + s) * kFrag + lane * 8]) = sp[s].lo;
-    }
-    f32x4 E[4];
-#pragma unroll
-    for (int tb = 0; tb < 4; ++tb) E[tb] = zero4();
-#pragma unroll
-    for (int s = 0; s < NS; ++s)
-#pragma unroll
-      for (int tb = 0; tb < 4; ++tb) {
-        const bf16x8 kf = frag_o<DK>(kt, tk, tb, s);
-        E[tb] = mfma16x16x32(kf, sp[s].hi, E[tb]);
-        E[tb] = mfma16x16x32(kf, sp[s].lo, E[tb]);
-      }
-    f32x4 be[4], Z[4];
+    const float* gt = lds.gt[sl] + 4 * g;
+    const auto gate = [&](int m, int tb) { return *reinterpret_cast<const f32x4*>(gt + 64 * m + 16 * tb); };
+    // the next chunk's Y, fetched as this one's is used up
+    yp += (c + 1 < nc ? static_cast<int64_t>(a.H) : 0) * kYf;
+    f32x4 E[4], be[4];
+    s16x4 vv[4];
 #pragma unroll
     for (int tb = 0; tb < 4; ++tb) {
-      const f32x4 gm = *reinterpret_cast<const f32x4*>(&lds.gt[sl][16 * tb + 4 * g]);
-      be[tb] = *reinterpret_cast<const f32x4*>(&lds.gt[sl][64 + 16 * tb + 4 * g]);
-      const f32x4 v = widen(col4<VW>(lds.v[sl], tv, tb, wave));
+      E[tb] = zero4();
+      vv[tb] = col4<VW>(lds.v[sl], tv, tb, wave);
+      be[tb] = gate(1, tb);
+    }
 #pragma unroll
-      for (int q = 0; q < 4; ++q) {
-        E[tb][q] = v[q] - gm[q] * E[tb][q];
-        Z[tb][q] = be[tb][q] * E[tb][q];
-      }
+    for (int half = 0; half < 2; ++half)
+#pragma unroll
+      for (int s = 0; s < NS; ++s)
+#pragma unroll
+        for (int tb = 2 * half; tb < 2 * half + 2; ++tb) {
+          const bf16x8 kf = frag_n<DK>(kt, tk, tb, s);
+          E[tb] = mfma16x16x32(kf, sp[s].hi, E[tb]);
+          E[tb] = mfma16x16x32(kf, sp[s].lo, E[tb]);
+        }
+    // S and U of this chunk for the output wave
+    uint16_t* sx = lds.sx[c & 1][wave] + lane * 8;
+    uint16_t* ux = lds.ux[c & 1][wave] + lane * 8;
+#pragma unroll
+    for (int s = 0; s < NS; ++s) {
+      *reinterpret_cast<bf16x8*>(sx + s * kFrag) = sp[s].hi;
+      *reinterpret_cast<bf16x8*>(sx + (NS + s) * kFrag) = sp[s].lo;
     }
     const float whole = lds.gt[sl][63];
 #pragma unroll
     for (int b = 0; b < NB; ++b)
 #pragma unroll
       for (int q = 0; q < 4; ++q) S[b][q] *= whole;
-    {
-      const Pair8 z0 = split8(Z[0], Z[1]), z1 = split8(Z[2], Z[3]);
+    Pair8 z[2];
 #pragma unroll
-      for (int ib = 0; ib < 4; ++ib) {
-        f32x4 x = zero4();
+    for (int half = 0; half < 2; ++half) {
+      f32x4 Z[2];
 #pragma unroll
-        for (int s = 0; s <= ib / 2; ++s) {
-          const int f = ib < 2 ? ib : 2 * ib - 2 + s;
-          const Pair8& z = s ? z1 : z0;
-          x = mfma16x16x32(yf[2 * f + 1], z.hi, x);
-          x = mfma16x16x32(yf[2 * f], z.lo, x);
-          x = mfma16x16x32(yf[2 * f], z.hi, x);
+      for (int i = 0; i < 2; ++i) {
+        const int tb = 2 * half + i;
+        const f32x4 gm = gate(0, tb), v = widen(vv[tb]);
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+          E[tb][q] = fmaf(-gm[q], E[tb][q], v[q]);
+          Z[i][q] = be[tb][q] * E[tb][q];
         }
+      }
+      z[half] = split8(Z[0], Z[1]);
+    }
 #pragma unroll
-        for (int q = 0; q < 4; ++q) E[ib][q] -= x[q];
+    for (int half = 0; half < 2; ++half) {
+      f32x4 x[2];
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        const int ib = 2 * half + i;
+        x[i] = zero4();
+#pragma unroll
+        for (int s = 0; s <= half; ++s) {
+          const int f = half ? 2 * ib - 2 + s : ib;
+          x[i] = mfma16x16x32(yf[2 * f + 1], z[s].hi, x[i]);
+          x[i] = mfma16x16x32(yf[2 * f], z[s].lo, x[i]);
+          x[i] = mfma16x16x32(yf[2 * f], z[s].hi, x[i]);
+        }
+      }
+#pragma unroll
+      for (int f = half ? 4 : 0; f < (half ? 12 : 4); ++f) yf[f] = *reinterpret_cast<const bf16x8*>(yp + f * kFrag);
+#pragma unroll
+      for (int i = 0; i < 2; ++i)
+#pragma unroll
+        for (int q = 0; q < 4; ++q) E[2 * half + i][q] -= x[i][q];
+      if constexpr (SAVE)
+        *reinterpret_cast<bf16x8*>(ca.ef + (((rec0 + static_cast<int64_t>(c) * a.H) * n_rt + rt) * 2 + half) * kFrag +
+                                   raw_at(lane)) = raw_order(round8(E[2 * half], E[2 * half + 1]), lane);
+#pragma unroll
+      for (int i = 0; i < 2; ++i)
+#pragma unroll
+        for (int q = 0; q < 4; ++q) E[2 * half + i][q] *= be[2 * half + i][q];
+      {
+        const Pair8 u = split8(E[2 * half], E[2 * half + 1]);
+        *reinterpret_cast<bf16x8*>(ux + half * kFrag) = u.hi;
+        *reinterpret_cast<bf16x8*>(ux + (2 + half) * kFrag) = u.lo;
+      }
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        const f32x4 rs = gate(2, 2 * half + i);
+#pragma unroll
+        for (int q = 0; q < 4; ++q) E[2 * half + i][q] *= rs[q];
+      }
+      const Pair8 u = split8(E[2 * half], E[2 * half + 1]);
+#pragma unroll
+      for (int b = 0; b < NB; ++b) {
+        const bf16x8 kc = frag_c<DK>(kt, tk, half, b);
+        S[b] = mfma16x16x32(kc, u.hi, S[b]);
+        S[b] = mfma16x16x32(kc, u.lo, S[b]);
       }
     }
-    if (c + 1 < nc) fetch(c + 1);
-    uint16_t* ux = lds.ux[c & 1][wave];
-    if constexpr (SAVE) {
-      const int64_t rec = rec0 + static_cast<int64_t>(c) * a.H;
 #pragma unroll
-      for (int s = 0; s < 2; ++s)
-        *reinterpret_cast<bf16x8*>(ca.ef + ((rec * n_rt + rt) * 2 + s) * kFrag + raw_at(lane)) =
-            raw_order(round8(E[2 * s], E[2 * s + 1]), lane);
-    }
-#pragma unroll
-    for (int tb = 0; tb < 4; ++tb)
-#pragma unroll
-      for (int q = 0; q < 4; ++q) E[tb][q] *= be[tb][q];
-#pragma unroll
-    for (int s = 0; s < 2; ++s) {
-      const Pair8 u = split8(E[2 * s], E[2 * s + 1]);
-      *reinterpret_cast<bf16x8*>(ux + s * kFrag + lane * 8) = u.hi;
-      *reinterpret_cast<bf16x8*>(ux + (2 + s) * kFrag + lane * 8) = u.lo;
-    }
-#pragma unroll
-    for (int tb = 0; tb < 4; ++tb) {
-      const f32x4 rs = *reinterpret_cast<const f32x4*>(&lds.gt[sl][128 + 16 * tb + 4 * g]);
-#pragma unroll
-      for (int q = 0; q < 4; ++q) E[tb][q] *= rs[q];
-    }
-    const Pair8 u0 = split8(E[0], E[1]), u1 = split8(E[2], E[3]);
-#pragma unroll
-    for (int b = 0; b < NB; ++b) {
-      const bf16x8 k0 = frag_c<DK>(kt, tk, 0, b), k1 = frag_c<DK>(kt, tk, 1, b);
-      S[b] = mfma16x16x32(k0, u0.hi, S[b]);
-      S[b] = mfma16x16x32(k0, u0.lo, S[b]);
-      S[b] = mfma16x16x32(k1, u1.hi, S[b]);
-      S[b] = mfma16x16x32(k1, u1.lo, S[b]);
-    }
+    for (int s = 0; s < NS; ++s) sp[s] = split8(S[2 * s], S[2 * s + 1]);
   }
   lds_barrier();
   if (r < a.dv) {
 #pragma unroll
     for (int b = 0; b < NB; ++b)
-      if (16 * b + 4 * g < a.dk) {
-        if (a.state_out) *reinterpret_cast<f32x4*>(static_cast<float*>(a.state_out) + so + 16 * b) = S[b];
-        if constexpr (SAVE) *reinterpret_cast<f32x4*>(ca.st + so + 16 * b) = S[b];
+      if (index4(b, g) < a.dk) {
+        if (a.state_out) *reinterpret_cast<f32x4*>(static_cast<float*>(a.state_out) + so + index4(b, g)) = S[b];
+        if constexpr (SAVE) *reinterpret_cast<f32x4*>(ca.st + so + index4(b, g)) = S[b];
       }
   }
 }

@@ -20,7 +20,7 @@ from __future__ import annotations
 
 import ctypes
 
-from . import GLScanError, _io_code, _ptr, _stream, _torch, gate_dtype  # noqa: F401
+from . import GLScanError, _io_code, _torch, gate_dtype
 from . import lib as _load
 
 DELTA_EXPORTS = (
@@ -141,31 +141,66 @@ def _three(st, shape, name):
     return Strides(*st)
 
 
-def _empty_like_order(t, shape, dtype):
-    """Empty [B,H,T,...] in t's order of heads and tokens."""
+def _key(t):
+    """What a call's checks and descriptor depend on in a tensor (not its address)."""
+    return None if t is None else (t.shape, t.stride(), t.dtype, t.get_device())
+
+
+def _ptr(t):
+    return None if t is None else t.data_ptr()
+
+
+class _Plan:
+    """A checked descriptor with its sizes, and the shapes and strides of the outputs."""
+
+    def __init__(self, desc, device):
+        self.desc, self.ref, self.device = desc, ctypes.byref(desc), device
+
+
+_plans: dict = {}
+
+
+def _plan(key, make):
+    """The plan of `key`, made and checked by `make` the first time: a decoding
+    loop makes thousands of calls of one kind, and the checks cost more than
+    the launch."""
+    p = _plans.get(key)
+    if p is None:
+        p = make()
+        if len(_plans) >= 512:
+            _plans.clear()
+        _plans[key] = p
+    return p
+
+
+def _launch(fn, plan, *args):
+    """fn(desc, *args, current stream) with the tensors' device current."""
     torch = _torch()
+    index = plan.device.index
+    stream = torch._C._cuda_getCurrentRawStream(index)
+    if index == torch.cuda.current_device():
+        status = fn(plan.ref, *args, stream)
+    else:
+        with torch.cuda.device(index):
+            status = fn(plan.ref, *args, stream)
+    if status:
+        _check(status)
+
+
+def _strides_like(t, shape):
+    """Strides of an output of `shape` [B,H,T,...] in t's order of heads and tokens."""
+    st = [1]
+    for n in reversed(shape[1:]):
+        st.append(st[-1] * max(n, 1))
+    st.reverse()
     if len(shape) > 2 and t.dim() > 2 and t.shape[1] > 1 and t.shape[2] > 1 and t.stride(1) < t.stride(2):
-        B, H, T = shape[:3]
-        return torch.empty((B, T, H, *shape[3:]), dtype=dtype, device=t.device).transpose(1, 2)
-    return torch.empty(shape, dtype=dtype, device=t.device)
+        row = st[2]
+        st[1], st[2] = row, row * shape[1]
+    return tuple(st)
 
 
-class _On:
-    """Makes the tensors' device current for the call."""
-
-    def __init__(self, device):
-        self.guard = None
-        torch = _torch()
-        if device.index is not None and device.index != torch.cuda.current_device():
-            self.guard = torch.cuda.device(device)
-
-    def __enter__(self):
-        if self.guard:
-            self.guard.__enter__()
-
-    def __exit__(self, *e):
-        if self.guard:
-            self.guard.__exit__(*e)
+def _with(desc, name, shape, strides):
+    setattr(desc, name, _three(strides[:3], shape[:3], name))
 
 
 def _delta_desc(q, k, v, log_alpha, beta, scale, state, cu, flags, segments):
@@ -217,19 +252,26 @@ def gl_delta_fwd(q, k, v, log_alpha, beta, *, scale=None, state=None, want_state
     """Gated delta rule over whole sequences.  Returns (y, final state or None,
     saved or None).  scale: of y, 1/sqrt(dk) by default."""
     torch = _torch()
-    desc, n = _delta_desc(q, k, v, log_alpha, beta, scale, state, cu_seqlens, flags, segments)
-    L = delta_lib()
-    B, H, T, dv = v.shape
-    y = _empty_like_order(v, (B, H, T, dv), v.dtype)
-    desc.sy = _rows(y, "y")
-    out = torch.empty((n, H, dv, q.shape[3]), dtype=gate_dtype(q.dtype), device=q.device) if want_state else None
-    saved = torch.empty(max(delta_saved_size(desc), 16), dtype=torch.uint8, device=q.device) if save else None
-    need, _ = delta_workspace_size(desc, save)
-    ws = torch.empty(need, dtype=torch.uint8, device=q.device) if need else None
-    with _On(q.device):
-        _check(L.gl_delta_fwd(ctypes.byref(desc), _ptr(q), _ptr(k), _ptr(v), _ptr(log_alpha), _ptr(beta),
-                              _ptr(state), _ptr(cu_seqlens), _ptr(y), _ptr(out), _ptr(saved), _ptr(ws), need,
-                              _stream(q.device)))
+
+    def make():
+        desc, n = _delta_desc(q, k, v, log_alpha, beta, scale, state, cu_seqlens, flags, segments)
+        p = _Plan(desc, q.device)
+        p.y_shape, p.y_strides = tuple(v.shape), _strides_like(v, v.shape)
+        _with(desc, "sy", p.y_shape, p.y_strides)
+        p.state_shape, p.state_dtype = (n, v.shape[1], v.shape[3], q.shape[3]), gate_dtype(q.dtype)
+        p.saved = max(delta_saved_size(desc), 16) if save else 0
+        p.ws = delta_workspace_size(desc, save)[0]
+        p.fn = delta_lib().gl_delta_fwd
+        return p
+    p = _plan(("fwd", _key(q), _key(k), _key(v), _key(log_alpha), _key(beta), scale, _key(state), save,
+               _key(cu_seqlens), flags, segments), make)
+    device = p.device
+    y = torch.empty_strided(p.y_shape, p.y_strides, dtype=v.dtype, device=device)
+    out = torch.empty(p.state_shape, dtype=p.state_dtype, device=device) if want_state else None
+    saved = torch.empty(p.saved, dtype=torch.uint8, device=device) if save else None
+    ws = torch.empty(p.ws, dtype=torch.uint8, device=device) if p.ws else None
+    _launch(p.fn, p, q.data_ptr(), k.data_ptr(), v.data_ptr(), log_alpha.data_ptr(), beta.data_ptr(), _ptr(state),
+            _ptr(cu_seqlens), y.data_ptr(), _ptr(out), _ptr(saved), _ptr(ws), p.ws)
     return y, out, saved
 
 
@@ -239,29 +281,40 @@ def gl_delta_bwd(q, k, v, log_alpha, beta, dy, saved=None, *, scale=None, state=
     None).  Returns (dq, dk, dv, dlog_alpha, dbeta, dstate of the first state);
     the last is None unless `state` was given or want_dstate is true."""
     torch = _torch()
-    desc, n = _delta_desc(q, k, v, log_alpha, beta, scale, state, cu_seqlens, flags, segments)
-    L = delta_lib()
-    B, H, T, dvv = v.shape
-    if dy.shape != v.shape or dy.dtype != v.dtype:
-        raise ValueError("dy must have the shape and dtype of v")
-    _on_gpu((q, dy, dstate, saved))
-    _check_state(dstate, (n, H, dvv, q.shape[3]), q.dtype, "dstate")
-    dq, dk = _empty_like_order(q, q.shape, q.dtype), _empty_like_order(k, k.shape, k.dtype)
-    dv = _empty_like_order(v, v.shape, v.dtype)
-    dla, db = (torch.empty_strided(beta.shape, beta.stride(), dtype=beta.dtype, device=q.device)
-               if _dense(beta) else torch.empty(beta.shape, dtype=beta.dtype, device=q.device) for _ in range(2))
-    desc.sdq, desc.sdk, desc.sdv = _rows(dq, "dq"), _rows(dk, "dk"), _rows(dv, "dv")
-    desc.sdy, desc.sdg = _rows(dy, "dy"), _three(db.stride(), db.shape, "dbeta")
+
+    def make():
+        desc, n = _delta_desc(q, k, v, log_alpha, beta, scale, state, cu_seqlens, flags, segments)
+        if dy.shape != v.shape or dy.dtype != v.dtype:
+            raise ValueError("dy must have the shape and dtype of v")
+        _on_gpu((q, dy, dstate, saved))
+        p = _Plan(desc, q.device)
+        p.state_shape, p.state_dtype = (n, v.shape[1], v.shape[3], q.shape[3]), gate_dtype(q.dtype)
+        _check_state(dstate, p.state_shape, q.dtype, "dstate")
+        if saved is not None and (saved.dtype != torch.uint8 or not saved.is_contiguous()
+                                  or saved.numel() < delta_saved_size(desc)):
+            raise ValueError("saved must be what gl_delta_fwd returned for these inputs")
+        p.outs = []
+        for name, t in (("sdq", q), ("sdk", k), ("sdv", v), ("sdg", beta)):
+            st = tuple(t.stride()) if t.dim() == 3 and _dense(t) else _strides_like(t, t.shape)
+            p.outs.append((tuple(t.shape), st, t.dtype))
+            _with(desc, name, t.shape, st)
+        desc.sdy = _rows(dy, "dy")
+        p.ws = delta_workspace_size(desc, saved is not None)[1]
+        p.fn = delta_lib().gl_delta_bwd
+        return p
+    p = _plan(("bwd", _key(q), _key(k), _key(v), _key(log_alpha), _key(beta), _key(dy), _key(saved), scale,
+               _key(state), _key(dstate), _key(cu_seqlens), flags, segments), make)
+    device = p.device
+    dq, dk, dv, dla = (torch.empty_strided(s, st, dtype=d, device=device) for s, st, d in p.outs)
+    s, st, d = p.outs[3]
+    db = torch.empty_strided(s, st, dtype=d, device=device)
     if want_dstate is None:
         want_dstate = state is not None
-    ds = torch.empty((n, H, dvv, q.shape[3]), dtype=gate_dtype(q.dtype), device=q.device) if want_dstate else None
-    _, need = delta_workspace_size(desc, saved is not None)
-    ws = torch.empty(need, dtype=torch.uint8, device=q.device) if need else None
-    with _On(q.device):
-        _check(L.gl_delta_bwd(ctypes.byref(desc), _ptr(q), _ptr(k), _ptr(v), _ptr(log_alpha), _ptr(beta),
-                              _ptr(state), _ptr(cu_seqlens), _ptr(dy), _ptr(dstate), _ptr(saved), _ptr(dq),
-                              _ptr(dk), _ptr(dv), _ptr(dla), _ptr(db), _ptr(ds), _ptr(ws), need,
-                              _stream(q.device)))
+    ds = torch.empty(p.state_shape, dtype=p.state_dtype, device=device) if want_dstate else None
+    ws = torch.empty(p.ws, dtype=torch.uint8, device=device) if p.ws else None
+    _launch(p.fn, p, q.data_ptr(), k.data_ptr(), v.data_ptr(), log_alpha.data_ptr(), beta.data_ptr(), _ptr(state),
+            _ptr(cu_seqlens), dy.data_ptr(), _ptr(dstate), _ptr(saved), dq.data_ptr(), dk.data_ptr(), dv.data_ptr(),
+            dla.data_ptr(), db.data_ptr(), _ptr(ds), _ptr(ws), p.ws)
     return dq, dk, dv, dla, db, ds
 
 
@@ -272,7 +325,7 @@ def _dense(t):
         if s != expect:
             return False
         expect *= n
-    return True
+    return t.numel() > 0
 
 
 def gl_delta_step(q, k, v, log_alpha, beta, state, *, scale=None, slots=None, y=None):
@@ -280,36 +333,46 @@ def gl_delta_step(q, k, v, log_alpha, beta, state, *, scale=None, slots=None, y=
     [n,H,dv,dk] is updated in place, row b's at slots[b] (int32; outside
     0..n-1: nothing to do, y = 0), or at b.  Returns y [B,H,dv]."""
     torch = _torch()
-    if q.dim() != 3 or k.shape != q.shape or v.dim() != 3 or v.shape[0] != q.shape[0] or state.dim() != 4:
-        raise ValueError("q, k must be [B,Hk,dk], v [B,H,dv] and state [n,H,dv,dk]")
-    B, Hk, dk = q.shape
-    H, dv = v.shape[1:]
-    if tuple(log_alpha.shape) != (B, H) or tuple(beta.shape) != (B, H):
-        raise ValueError("log_alpha and beta must be [B,H]")
-    if k.dtype != q.dtype or v.dtype != q.dtype:
-        raise TypeError("q, k and v must share the io dtype")
-    if log_alpha.dtype != beta.dtype or beta.dtype not in (q.dtype, gate_dtype(q.dtype)):
-        raise TypeError(f"log_alpha and beta must both be {q.dtype} or {gate_dtype(q.dtype)}")
-    _check_state(state, (state.shape[0], H, dv, dk), q.dtype, "state")
-    if slots is None:
-        if state.shape[0] < B:
-            raise ValueError(f"{state.shape[0]} states for {B} rows")
-    elif slots.dtype != torch.int32 or tuple(slots.shape) != (B,) or not slots.is_contiguous():
-        raise ValueError("slots must be a contiguous int32 tensor [B]")
+
+    def make():
+        if q.dim() != 3 or k.shape != q.shape or v.dim() != 3 or v.shape[0] != q.shape[0] or state.dim() != 4:
+            raise ValueError("q, k must be [B,Hk,dk], v [B,H,dv] and state [n,H,dv,dk]")
+        B, Hk, dk = q.shape
+        H, dv = v.shape[1:]
+        if tuple(log_alpha.shape) != (B, H) or tuple(beta.shape) != (B, H):
+            raise ValueError("log_alpha and beta must be [B,H]")
+        if q.dtype not in (torch.float64, torch.float32, torch.bfloat16):
+            raise TypeError("q must be float64, float32 or bfloat16")
+        if k.dtype != q.dtype or v.dtype != q.dtype:
+            raise TypeError("q, k and v must share the io dtype")
+        if log_alpha.dtype != beta.dtype or beta.dtype not in (q.dtype, gate_dtype(q.dtype)):
+            raise TypeError(f"log_alpha and beta must both be {q.dtype} or {gate_dtype(q.dtype)}")
+        _check_state(state, (state.shape[0], H, dv, dk), q.dtype, "state")
+        if slots is None:
+            if state.shape[0] < B:
+                raise ValueError(f"{state.shape[0]} states for {B} rows")
+        elif slots.dtype != torch.int32 or tuple(slots.shape) != (B,) or not slots.is_contiguous():
+            raise ValueError("slots must be a contiguous int32 tensor [B]")
+        if y is not None and (tuple(y.shape) != (B, H, dv) or y.dtype != v.dtype):
+            raise ValueError("y must be [B,H,dv] of v's dtype")
+        if log_alpha.stride() != beta.stride():
+            raise ValueError("log_alpha and beta must have the same strides")
+        _on_gpu((q, k, v, log_alpha, beta, state, slots, y))
+        desc = make_delta_desc(B, 1, H, Hk, dk, dv, _io_code(q.dtype), _io_code(beta.dtype),
+                               scale=dk ** -0.5 if scale is None else scale)
+        p = _Plan(desc, q.device)
+        p.y_shape, p.n = (B, H, dv), state.shape[0]
+        desc.sq, desc.sk, desc.sv = _rows(q, "q"), _rows(k, "k"), _rows(v, "v")
+        desc.sy = _three((H * dv, dv), (B, H), "y") if y is None else _rows(y, "y")
+        desc.sg = _three(beta.stride(), beta.shape, "beta")
+        p.fn = delta_lib().gl_delta_step
+        return p
+    p = _plan(("step", _key(q), _key(k), _key(v), _key(log_alpha), _key(beta), _key(state), scale, _key(slots),
+               _key(y)), make)
     if y is None:
-        y = torch.empty((B, H, dv), dtype=v.dtype, device=v.device)
-    elif tuple(y.shape) != (B, H, dv) or y.dtype != v.dtype:
-        raise ValueError("y must be [B,H,dv] of v's dtype")
-    _on_gpu((q, k, v, log_alpha, beta, state, slots, y))
-    if log_alpha.stride() != beta.stride():
-        raise ValueError("log_alpha and beta must have the same strides")
-    desc = make_delta_desc(B, 1, H, Hk, dk, dv, _io_code(q.dtype), _io_code(beta.dtype),
-                           scale=dk ** -0.5 if scale is None else scale)
-    desc.sq, desc.sk, desc.sv, desc.sy = _rows(q, "q"), _rows(k, "k"), _rows(v, "v"), _rows(y, "y")
-    desc.sg = _three(beta.stride(), beta.shape, "beta")
-    with _On(q.device):
-        _check(delta_lib().gl_delta_step(ctypes.byref(desc), _ptr(q), _ptr(k), _ptr(v), _ptr(log_alpha), _ptr(beta),
-                                         _ptr(slots), state.shape[0], _ptr(state), _ptr(y), _stream(q.device)))
+        y = torch.empty(p.y_shape, dtype=v.dtype, device=p.device)
+    _launch(p.fn, p, q.data_ptr(), k.data_ptr(), v.data_ptr(), log_alpha.data_ptr(), beta.data_ptr(), _ptr(slots),
+            p.n, state.data_ptr(), y.data_ptr())
     return y
 
 
@@ -349,12 +412,17 @@ def gl_qknorm_rope_fwd(q, k, wq=None, wk=None, cos=None, sin=None, *, pos=None, 
     [n_pos, rot/2] at pos [B,T] (or pos0 + t).  Returns the two results, dense
     [B,H,T,d] (what gl_delta_fwd reads row after row)."""
     torch = _torch()
-    desc = _qk_desc(q, k, wq, wk, cos, sin, pos, pos0, eps, q_scale, k_scale, interleaved)
-    oq = torch.empty(q.shape, dtype=q.dtype, device=q.device)
-    ok = torch.empty(k.shape, dtype=k.dtype, device=k.device)
-    with _On(q.device):
-        _check(delta_lib().gl_qknorm_rope_fwd(ctypes.byref(desc), _ptr(q), _ptr(k), _ptr(wq), _ptr(wk), _ptr(cos),
-                                              _ptr(sin), _ptr(pos), _ptr(oq), _ptr(ok), _stream(q.device)))
+
+    def make():
+        p = _Plan(_qk_desc(q, k, wq, wk, cos, sin, pos, pos0, eps, q_scale, k_scale, interleaved), q.device)
+        p.fn = delta_lib().gl_qknorm_rope_fwd
+        return p
+    p = _plan(("qk", _key(q), _key(k), _key(wq), _key(wk), _key(cos), _key(sin), _key(pos), pos0, eps, q_scale,
+               k_scale, interleaved), make)
+    oq = torch.empty(q.shape, dtype=q.dtype, device=p.device)
+    ok = torch.empty(k.shape, dtype=q.dtype, device=p.device)
+    _launch(p.fn, p, q.data_ptr(), k.data_ptr(), _ptr(wq), _ptr(wk), _ptr(cos), _ptr(sin), _ptr(pos), oq.data_ptr(),
+            ok.data_ptr())
     return oq, ok
 
 
@@ -364,22 +432,31 @@ def gl_qknorm_rope_bwd(q, k, wq, wk, cos, sin, dqn, dkn, *, pos=None, pos0=0, ep
     dwk), dq and dk in their inputs' order of dimensions, dwq and dwk [d] in
     fp32 (fp64), None where there is no weight."""
     torch = _torch()
-    desc = _qk_desc(q, k, wq, wk, cos, sin, pos, pos0, eps, q_scale, k_scale, interleaved)
-    if dqn.shape != q.shape or dkn.shape != k.shape or dqn.dtype != q.dtype or dkn.dtype != k.dtype:
-        raise ValueError("dqn and dkn must have the shapes and dtype of q and k")
-    _on_gpu((q, dqn, dkn))
-    dq, dk = _empty_like_order(q, q.shape, q.dtype), _empty_like_order(k, k.shape, k.dtype)
-    desc.sdoq, desc.sdok, desc.sdq, desc.sdk = (_rows(dqn, "dqn"), _rows(dkn, "dkn"), _rows(dq, "dq"),
-                                                _rows(dk, "dk"))
-    gd = gate_dtype(q.dtype)
-    dwq, dwk = (None if w is None else torch.empty(w.shape, dtype=gd, device=q.device) for w in (wq, wk))
-    n = ctypes.c_size_t()
-    _check(delta_lib().gl_qknorm_rope_workspace_size(ctypes.byref(desc), ctypes.byref(n)))
-    ws = torch.empty(max(n.value, 16), dtype=torch.uint8, device=q.device)
-    with _On(q.device):
-        _check(delta_lib().gl_qknorm_rope_bwd(
-            ctypes.byref(desc), _ptr(q), _ptr(k), _ptr(wq), _ptr(wk), _ptr(cos), _ptr(sin), _ptr(pos), _ptr(dqn),
-            _ptr(dkn), _ptr(dq), _ptr(dk), _ptr(dwq), _ptr(dwk), _ptr(ws), n.value, _stream(q.device)))
+
+    def make():
+        desc = _qk_desc(q, k, wq, wk, cos, sin, pos, pos0, eps, q_scale, k_scale, interleaved)
+        if dqn.shape != q.shape or dkn.shape != k.shape or dqn.dtype != q.dtype or dkn.dtype != k.dtype:
+            raise ValueError("dqn and dkn must have the shapes and dtype of q and k")
+        _on_gpu((q, dqn, dkn))
+        p = _Plan(desc, q.device)
+        p.sq, p.sk = _strides_like(q, q.shape), _strides_like(k, k.shape)
+        desc.sdoq, desc.sdok = _rows(dqn, "dqn"), _rows(dkn, "dkn")
+        _with(desc, "sdq", q.shape, p.sq)
+        _with(desc, "sdk", k.shape, p.sk)
+        n = ctypes.c_size_t()
+        _check(delta_lib().gl_qknorm_rope_workspace_size(ctypes.byref(desc), ctypes.byref(n)))
+        p.ws, p.dw_dtype = n.value, gate_dtype(q.dtype)
+        p.fn = delta_lib().gl_qknorm_rope_bwd
+        return p
+    p = _plan(("qkb", _key(q), _key(k), _key(wq), _key(wk), _key(cos), _key(sin), _key(pos), _key(dqn), _key(dkn),
+               pos0, eps, q_scale, k_scale, interleaved), make)
+    device = p.device
+    dq = torch.empty_strided(q.shape, p.sq, dtype=q.dtype, device=device)
+    dk = torch.empty_strided(k.shape, p.sk, dtype=q.dtype, device=device)
+    dwq, dwk = (None if w is None else torch.empty(w.shape, dtype=p.dw_dtype, device=device) for w in (wq, wk))
+    ws = torch.empty(max(p.ws, 16), dtype=torch.uint8, device=device)
+    _launch(p.fn, p, q.data_ptr(), k.data_ptr(), _ptr(wq), _ptr(wk), _ptr(cos), _ptr(sin), _ptr(pos),
+            dqn.data_ptr(), dkn.data_ptr(), dq.data_ptr(), dk.data_ptr(), _ptr(dwq), _ptr(dwk), ws.data_ptr(), p.ws)
     return dq, dk, dwq, dwk
 
 
