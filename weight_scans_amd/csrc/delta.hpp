@@ -90,11 +90,13 @@ hipError_t launch_delta_step(int io, const DeltaArgs& a, hipStream_t s);
 //   yf   Y  = (I + L beta)^-1 L, rows i     [6 blocks][hi, lo]
 //   pf   P  = scale (decayed q_i.k_j), rows i   [6][hi, lo]
 //   ytf, ptf   the same with rows j         [6][hi, lo] each (training)
-// and gates [5][64] fp32: e^l, beta, e^(l_C - l), and the cumulative log2
-// decay l in two parts (whole and fraction).  The recurrences leave (training),
-// as pieces of 64 lanes x 4 bf16 that the gradients take as operands:
-//   sf, lf   the state before, the adjoint after the chunk: piece (rt, kb) has
-//            element (lane (g, l), q) = S[index(rt, 4 g + q)][index(kb, l)]  (delta_mfma.hpp)
+// and gates [9][64] fp32: e^l, beta, e^(l_C - l), the cumulative log2 decay l in
+// two parts (whole and fraction), and the decay between blocks of 16 tokens as
+// a product of two factors <= 1, with m_x the l before block x: e^(l_i - m_x)
+// of i in block x, and e^(m_x - l_j) of j before it (x = 1, 2, 3).  The recurrences leave (training),
+// in the form in which the gradients take them as operands:
+//   sf, lf   the state before, the adjoint after the chunk: (rt, kb / 2) has
+//            [lane (g, l)][kb % 2][q] = S[index(rt, 4 g + q)][index(kb, l)]  (delta_mfma.hpp)
 //   yb       y before its rounding: (rt, tb) has [lane (g, l)][4] fp32 = y[token 16 tb + l][index(rt, 4 g + q)]
 //   st       the last state [N][H][dv][dk] fp32
 // and, as two fragments a row tile (row l in lanes, tokens in order; rows and
@@ -104,7 +106,7 @@ hipError_t launch_delta_step(int io, const DeltaArgs& a, hipStream_t s);
 constexpr int kDeltaChunk = 64;
 constexpr int kFrag = 512;                       // bf16 per fragment
 constexpr int kYf = 12 * kFrag;                  // per record
-constexpr int kGates = 5 * 64;
+constexpr int kGates = 9 * 64;
 constexpr int kPiece = 256;                      // bf16 per piece
 struct ChunkArgs {
   DeltaArgs a;

@@ -168,6 +168,15 @@ __device__ __forceinline__ __amdgpu_buffer_rsrc_t rows_rsrc(const uint16_t* base
   return buffer_rsrc(base + (n > 0 ? t0 * st : 0), n > 0 ? static_cast<int>(((n - 1) * st + d) * 2) : 0);
 }
 
+// 16- and 4-byte buffer loads, zeros past the end: unlike loads under a
+// condition they draw no branch and no wait of their own.
+__device__ __forceinline__ bf16x8 load16(__amdgpu_buffer_rsrc_t r, uint32_t off) {
+  return __builtin_bit_cast(bf16x8, __builtin_amdgcn_raw_buffer_load_b128(r, off, 0, 0));
+}
+__device__ __forceinline__ float load4(__amdgpu_buffer_rsrc_t r, uint32_t off) {
+  return __builtin_bit_cast(float, __builtin_amdgcn_raw_buffer_load_b32(r, off, 0, 0));
+}
+
 // Work-groups are dealt to the 8 XCDs in turn: all `tiles` of a sequence-head
 // get the same XCD (they share its chunks through the XCD's L2).  Returns
 // false past the end.

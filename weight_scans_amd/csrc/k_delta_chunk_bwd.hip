@@ -271,8 +271,9 @@ __global__ __launch_bounds__(64 * (2 * NW + 2)) void delta_chunk_rev(ChunkArgs c
 #pragma unroll
     for (int s = 0; s < NS; ++s) *reinterpret_cast<bf16x8*>(&turn[s * kFrag + lane * 8]) = sp[s].hi;
 #pragma unroll
-    for (int b = 0; b < NB; ++b)
-      *reinterpret_cast<s16x4*>(ca.lf + ((rec * n_rt + rt) * NB + b) * kPiece + lane * 4) = turned(turn, b, lane);
+    for (int b = 0; b < NB; b += 2)
+      *reinterpret_cast<bf16x8*>(ca.lf + ((rec * n_rt + rt) * NB + b) * kPiece + lane * 8) =
+          join(turned(turn, b, lane), turned(turn, b + 1, lane));
     lds_barrier();  // A
     const int sl = (i - 1) % 3;
     const char* kt = lds.k[sl];
@@ -389,27 +390,47 @@ __global__ __launch_bounds__(64 * (2 * NW + 2)) void delta_chunk_rev(ChunkArgs c
 }
 
 // ---- the gradients of one chunk, for the value heads of one key head in turn
-// (their sums stay in registers).  Eight waves: first the score blocks dP, dP^T
-// and H + H^T, dealt over the waves and handed on through LDS as operands;
-// then wave w takes 16 columns of dq and dk (S and Lam enter as operands
-// straight from global memory, each column block once).
+// (their sums stay in registers), on four waves.
+//
+// Scores: dO e^T and G e^T below the diagonal, each in both orientations (every
+// later product wants its operand with another index in lanes), one kind a
+// wave, handed on through LDS.  Off the diagonal the decay is a product of two
+// factors; on it, exact per element.
+//
+// Then a wave takes two column blocks of dq and dk (for a share of the tokens
+// where there are fewer than eight blocks): operands of tokens (dO, e, G,
+// scores) come from LDS and serve both blocks, S and Lam straight from global
+// memory.  Loading a chunk's 160 KB (128 x 128) and multiplying take about as
+// long: dO, e and G are done with before K and Q are needed, which take their
+// place, so that two work-groups fit a CU and one loads while the other
+// multiplies.
 template <int DK, int DV>
 struct GradLds {
-  alignas(16) char k[64 * DK * 2];
-  alignas(16) char q[64 * DK * 2];
-  alignas(16) char o[64 * DV * 2];
-  alignas(16) uint16_t e[DV / 16 * 4 * kPiece];
-  alignas(16) uint16_t g[DV / 16 * 4 * kPiece];
-  alignas(16) uint16_t sc[3][16 * kPiece];   // dP [i][j], dP^T [j][i], H + H^T [a][b]
+  static constexpr int kCols = 64 * DK * 2;
+  union {
+    struct {
+      alignas(16) char o[64 * DV * 2];
+      alignas(16) uint16_t e[64 * DV];
+      alignas(16) uint16_t g[64 * DV];
+    };
+    struct {
+      alignas(16) char k[kCols];
+      alignas(16) char q[kCols];
+    };
+  };
+  // operand pieces (lane block, contraction block): dP [i][j], dP^T [j][i], and
+  // H + H^T with the two halves of its diagonal blocks apart (48.. 51: the other)
+  alignas(16) uint16_t sc[52 * kPiece];
   alignas(16) float gt[kGates];
 };
 
-constexpr int kGradThreads = 512;
+constexpr int kGradThreads = 256;
 
 template <int DK, int DV>
-__global__ __launch_bounds__(kGradThreads) void delta_chunk_grad(ChunkArgs ca) {
+__global__ __launch_bounds__(kGradThreads) void
+delta_chunk_grad(ChunkArgs ca) {
   const DeltaArgs& a = ca.a;
-  constexpr int NB = DK / 16, NT = DK == 128 ? 4 : 2, NR = DV / 32;
+  constexpr int NB = DK / 16, NP = NB / 2, NT = NP, NR = DV / 32;  // NT blocks of 16 tokens a wave
   __shared__ GradLds<DK, DV> lds;
   const int lane = threadIdx.x & 63, l = lane & 15, g = lane >> 4;
   const int w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
@@ -426,35 +447,27 @@ __global__ __launch_bounds__(kGradThreads) void delta_chunk_grad(ChunkArgs ca) {
     n = lo;
     c = slot - chunk_slot0(true, n, seq_range(a.cu, n, a.T).t0, a.T, kDeltaChunk);
   } else {
-    const int64_t nc = (a.T + kDeltaChunk - 1) / kDeltaChunk;
-    n = slot / nc;
-    c = slot % nc;
+    const uint32_t nc = static_cast<uint32_t>((a.T + kDeltaChunk - 1) / kDeltaChunk);
+    n = static_cast<uint32_t>(slot) / nc;
+    c = static_cast<uint32_t>(slot) % nc;
   }
   const SeqRange sr = seq_range(a.cu, n, a.T);
   const int64_t t0 = c * kDeltaChunk;
   if (c < 0 || t0 >= sr.len) return;
   const int nt = static_cast<int>(sr.len - t0 < 64 ? sr.len - t0 : 64);
-  const int n_rt = delta_row_tiles(a.dv);
-  const int kb = w % NB, tb0 = DK == 128 ? 0 : 2 * (w / NB);
+  const int n_rt = delta_row_tiles(a.dv), nr = n_rt / 2;
+  const int kb0 = 2 * (w % NP), tb0 = NT * (w / NP);
   const TileLane<DK> tk = tile_lane<DK>(lane);
   const TileLane<DV> to = tile_lane<DV>(lane);
   const uint32_t ra = raw_turned(lane);
   const float sc = static_cast<float>(a.scale);
+  const s16x4 none = {0, 0, 0, 0};
 
   const uint16_t* kp = static_cast<const uint16_t*>(a.k) + sr.b * a.sk.b + hk * a.sk.h + sr.t0 * a.sk.t;
   const uint16_t* qp = static_cast<const uint16_t*>(a.q) + sr.b * a.sq.b + hk * a.sq.h + sr.t0 * a.sq.t;
-  {
-    const __amdgpu_buffer_rsrc_t rk = rows_rsrc(kp, t0, sr.len, a.sk.t, a.dk);
-    const __amdgpu_buffer_rsrc_t rq = rows_rsrc(qp, t0, sr.len, a.sq.t, a.dk);
+  f32x4 dq[2][NT], dk[2][NT];
 #pragma unroll
-    for (int i = w; i < DK / 8; i += 8) {
-      dma16(rk, tile_off<DK>(i, lane, a.sk.t, 0, a.dk), lds.k + i * 1024);
-      dma16(rq, tile_off<DK>(i, lane, a.sq.t, 0, a.dk), lds.q + i * 1024);
-    }
-  }
-  f32x4 dq[NT], dk[NT];
-#pragma unroll
-  for (int t = 0; t < NT; ++t) dq[t] = dk[t] = zero4();
+  for (int t = 0; t < NT; ++t) dq[0][t] = dq[1][t] = dk[0][t] = dk[1][t] = zero4();
 
   for (int gi = 0; gi < grp; ++gi) {
     const int h = hk * grp + gi;
@@ -467,142 +480,206 @@ __global__ __launch_bounds__(kGradThreads) void delta_chunk_grad(ChunkArgs ca) {
       const int eb = n_rt * 2 * kFrag * 2;  // bytes of e's fragments
       const __amdgpu_buffer_rsrc_t re = buffer_rsrc(ca.ef + rec * 2 * n_rt * kFrag, eb);
       const __amdgpu_buffer_rsrc_t rr = buffer_rsrc(ca.gf + rec * 2 * n_rt * kFrag, eb);
+      if (w < 3) {
 #pragma unroll
-      for (int i = w; i < DV / 8; i += 8) {
-        dma16(ro, tile_off<DV>(i, lane, a.sdy.t, 0, a.dv), lds.o + i * 1024);
+        for (int i = 0; i < 3; ++i) dma4(rg, ((3 * w + i) * 64 + lane) * 4, lds.gt + (3 * w + i) * 64);
+      }
+#pragma unroll
+      for (int j = 0; j < DV / 32; ++j) {
+        const int i = w * (DV / 32) + j;
         dma16(re, i * 1024 + lane * 16, reinterpret_cast<char*>(lds.e) + i * 1024);
+        dma16(ro, tile_off<DV>(i, lane, a.sdy.t, 0, a.dv), lds.o + i * 1024);
         dma16(rr, i * 1024 + lane * 16, reinterpret_cast<char*>(lds.g) + i * 1024);
       }
-      if (w < 5) dma4(rg, (w * 64 + lane) * 4, lds.gt + w * 64);
     }
-    // S and Lam, columns of this wave
-    s16x4 sp[2 * NR], lp[2 * NR];
+    // columns of this wave, of Lam and of S
+    s16x8 lc[2 * NR], sc_[2 * NR];
+    const auto columns = [&](const uint16_t* p, s16x8 (&st)[2 * NR]) {
+      const __amdgpu_buffer_rsrc_t r = buffer_rsrc(p + rec * n_rt * (NB * kPiece), n_rt * NB * kPiece * 2);
 #pragma unroll
-    for (int rt = 0; rt < 2 * NR; ++rt) {
-      const s16x4 none = {0, 0, 0, 0};
-      sp[rt] = rt < n_rt ? *reinterpret_cast<const s16x4*>(ca.sf + ((rec * n_rt + rt) * NB + kb) * kPiece + lane * 4) : none;
-      lp[rt] = rt < n_rt ? *reinterpret_cast<const s16x4*>(ca.lf + ((rec * n_rt + rt) * NB + kb) * kPiece + lane * 4) : none;
+      for (int rt = 0; rt < 2 * NR; ++rt)
+        st[rt] = __builtin_bit_cast(s16x8, load16(r, (rt * NB + kb0) * (kPiece * 2) + lane * 16));
+    };
+    columns(ca.lf, lc);
+    columns(ca.sf, sc_);
+    // gates: dlog_alpha and dbeta of token `lane`, over the row tiles
+    float dl = 0.f, ge = 0.f;
+    if (w == 3) {
+      const __amdgpu_buffer_rsrc_t rz = buffer_rsrc(ca.zf + rec * n_rt * 64, n_rt * 256);
+      const __amdgpu_buffer_rsrc_t rb = buffer_rsrc(ca.bf + rec * n_rt * 64, n_rt * 256);
+      float z[2 * NR], b[2 * NR];
+#pragma unroll
+      for (int i = 0; i < 2 * NR; ++i) {
+        z[i] = load4(rz, (i * 64 + lane) * 4);
+        b[i] = load4(rb, (i * 64 + lane) * 4);
+      }
+#pragma unroll
+      for (int i = 0; i < 2 * NR; ++i) {
+        dl += z[i];
+        ge += b[i];
+      }
     }
     wait_vm<0>();
     __syncthreads();
     const float* gam = lds.gt;
     const float* bet = lds.gt + 64;
     const float* rst = lds.gt + 128;
-    const auto decay = [&](int i, int j) {
-      return fexp2((lds.gt[192 + i] - lds.gt[192 + j]) + (lds.gt[256 + i] - lds.gt[256 + j]));
-    };
+    const auto four = [&](const float* p, int b) { return *reinterpret_cast<const f32x4*>(p + 16 * b + 4 * g); };
     // e and G turned: tokens 16 tb + l in lanes, rows 32 R.. in order O
     const auto piece = [&](const uint16_t* p, int tb, int R) {
       return join(turned_raw(p + (4 * R) * kFrag, ra, tb), turned_raw(p + (4 * R + 2) * kFrag, ra, tb));
     };
-    // ---- scores.  Result layout [row block index 4g + q][column l]; the piece
-    // of (column block, row block) is then an operand with the column in lanes.
-    const int nr = n_rt / 2;
-    for (int b = w; b < 36; b += 8) {
-      const bool sym = b >= 20;
-      int x, y;  // row and column block of the result
-      const int tb = b < 10 ? b : b - 10;
-      if (sym) { x = (b - 20) >> 2; y = (b - 20) & 3; }
-      else if (b < 10) { x = tri_j(tb); y = tri_i(tb); }   // [j][i]
-      else { x = tri_i(tb); y = tri_j(tb); }               // [i][j]
-      f32x4 v = zero4(), v2 = zero4();
-      for (int R = 0; R < nr; ++R) {
-        if (!sym) {
-          const bf16x8 of = frag_n<DV>(lds.o, to, b < 10 ? y : x, R);
-          const bf16x8 ef = piece(lds.e, b < 10 ? x : y, R);
-          v = b < 10 ? mfma16x16x32(ef, of, v) : mfma16x16x32(of, ef, v);
-        } else {
-          if (x <= y) v = mfma16x16x32(piece(lds.e, x, R), piece(lds.g, y, R), v);   // H[y][x]
-          if (x >= y) v2 = mfma16x16x32(piece(lds.g, x, R), piece(lds.e, y, R), v2);  // H[x][y]
-        }
-      }
-      f32x4 o;
+
+    // ---- scores: wave w has kind w: dO e^T as [j][i] and [i][j], G e^T as
+    // [j][i] and [i][j] (result rows first; the piece has the result's columns
+    // in lanes).
+    {
+      const int kind = w;
+      const bool isG = kind >= 2, ij = kind & 1;
+      f32x4 v[10];
 #pragma unroll
-      for (int q = 0; q < 4; ++q) {
-        const int p = 16 * x + 4 * g + q, m = 16 * y + l;  // tokens of row and column
-        if (!sym) {
-          const int i = b < 10 ? m : p, j = b < 10 ? p : m;
-          o[q] = j <= i ? sc * bet[j] * decay(i, j) * v[q] : 0.f;
-        } else {
-          const float bb = bet[p] * bet[m];
-          o[q] = p < m ? bb * decay(m, p) * v[q] : p > m ? bb * decay(p, m) * v2[q] : 0.f;
+      for (int b = 0; b < 10; ++b) v[b] = zero4();
+#pragma unroll 1
+      for (int R = 0; R < nr; ++R) {
+        bf16x8 i[4], j[4];
+#pragma unroll
+        for (int b = 0; b < 4; ++b) {
+          i[b] = isG ? piece(lds.g, b, R) : frag_n<DV>(lds.o, to, b, R);
+          j[b] = piece(lds.e, b, R);
         }
+#pragma unroll
+        for (int x = 0; x < 4; ++x)
+#pragma unroll
+          for (int y = 0; y <= x; ++y) {
+            f32x4& acc = v[x * (x + 1) / 2 + y];
+            acc = ij ? mfma16x16x32(i[x], j[y], acc) : mfma16x16x32(j[y], i[x], acc);
+          }
       }
-      uint16_t* dst = lds.sc[sym ? 2 : b < 10 ? 0 : 1] + (y * 4 + x) * kPiece + lane * 4;
-      *reinterpret_cast<uint2*>(dst) = make_uint2(pack2(o[0], o[1]), pack2(o[2], o[3]));
+      const auto finish = [&](int x, int y, f32x4 o) {  // block row x, column y <= x
+        const int rb = ij ? x : y, cb = ij ? y : x;     // of the result
+        if (x > y) {
+          const float* ai = lds.gt + 320;
+          const float* bj = lds.gt + 320 + 64 * x;
+          const float fl = (ij ? bj : ai)[16 * cb + l] * (ij || isG ? bet[16 * cb + l] : 1.f) * (isG ? 1.f : sc);
+          f32x4 fr = four(ij ? ai : bj, rb);
+          if (!ij || isG) fr *= four(bet, rb);
+#pragma unroll
+          for (int q = 0; q < 4; ++q) o[q] *= fr[q] * fl;
+        } else {
+          const float lw = lds.gt[192 + 16 * x + l], lf = lds.gt[256 + 16 * x + l], bl = bet[16 * x + l];
+          const f32x4 rw = four(lds.gt + 192, x), rf = four(lds.gt + 256, x), rbt = four(bet, x);
+#pragma unroll
+          for (int q = 0; q < 4; ++q) {
+            const int r = 4 * g + q, i = ij ? r : l, j = ij ? l : r;
+            const float d = fexp2(ij ? (rw[q] - lw) + (rf[q] - lf) : (lw - rw[q]) + (lf - rf[q]));
+            const float f = isG ? rbt[q] * bl : sc * (ij ? bl : rbt[q]);
+            o[q] = j < i || (j == i && !isG) ? o[q] * d * f : 0.f;
+          }
+        }
+        const int at = (isG ? 32 : 16 * kind) + (isG && ij && x == y ? 16 + x : 4 * cb + rb);
+        *reinterpret_cast<uint2*>(&lds.sc[at * kPiece + lane * 4]) = make_uint2(pack2(o[0], o[1]), pack2(o[2], o[3]));
+      };
+#pragma unroll
+      for (int x = 0; x < 4; ++x)
+#pragma unroll
+        for (int y = 0; y <= x; ++y) finish(x, y, v[x * (x + 1) / 2 + y]);
     }
-    // ---- dv: row tiles w, w + 8, .. of 16 columns of v
-    for (int rt = w; rt < n_rt; rt += 8) {
-      const int r = index4(rt, g);
+    // ---- dv: a pair of row tiles, eight neighbouring columns of v
+    for (int R = w; R < nr; R += 4) {
+      const int col = 32 * R + 8 * g;
+      uint16_t* dvp = static_cast<uint16_t*>(a.dv_) + sr.b * a.sdv.b + h * a.sdv.h + (sr.t0 + t0 + l) * a.sdv.t + col;
 #pragma unroll
       for (int tb = 0; tb < 4; ++tb) {
-        const int t = 16 * tb + l;
-        const f32x4 gv = widen(turned_raw(lds.g + 2 * rt * kFrag, ra, tb));
-        const float b = bet[t];
-        if (t < nt && r < a.dv)
-          *reinterpret_cast<uint2*>(static_cast<uint16_t*>(a.dv_) + sr.b * a.sdv.b + h * a.sdv.h +
-                                    (sr.t0 + t0 + t) * a.sdv.t + r) =
-              make_uint2(pack2(b * gv[0], b * gv[1]), pack2(b * gv[2], b * gv[3]));
+        const f32x4 g0 = widen(turned_raw(lds.g + 4 * R * kFrag, ra, tb));
+        const f32x4 g1 = widen(turned_raw(lds.g + (4 * R + 2) * kFrag, ra, tb));
+        const float b = bet[16 * tb + l];
+        if (16 * tb + l < nt && col < a.dv)
+          *reinterpret_cast<uint4*>(dvp + 16 * tb * a.sdv.t) =
+              make_uint4(pack2(b * g0[0], b * g0[1]), pack2(b * g0[2], b * g0[3]), pack2(b * g1[0], b * g1[1]),
+                         pack2(b * g1[2], b * g1[3]));
       }
     }
     // ---- products with the states: result layout [column k: 4g + q][token l]
-    f32x4 a1[NT], a2[NT], a3[NT];
+    f32x4 x[2][NT];
+    const auto states = [&](const s16x8 (&st)[2 * NR], auto&& operand) {
 #pragma unroll
-    for (int t = 0; t < NT; ++t) a1[t] = a2[t] = a3[t] = zero4();
+      for (int t = 0; t < NT; ++t) x[0][t] = x[1][t] = zero4();
 #pragma unroll
-    for (int R = 0; R < NR; ++R) {
-      if (R >= nr) break;
-      const bf16x8 sf = join(sp[2 * R], sp[2 * R + 1]), lf = join(lp[2 * R], lp[2 * R + 1]);
+      for (int R = 0; R < NR; ++R) {
+        if (R >= nr) break;
+        const bf16x8 s0 = __builtin_bit_cast(bf16x8, __builtin_shufflevector(st[2 * R], st[2 * R + 1], 0, 1, 2, 3, 8, 9, 10, 11));
+        const bf16x8 s1 = __builtin_bit_cast(bf16x8, __builtin_shufflevector(st[2 * R], st[2 * R + 1], 4, 5, 6, 7, 12, 13, 14, 15));
+#pragma unroll
+        for (int t = 0; t < NT; ++t) {
+          const bf16x8 f = operand(tb0 + t, R);
+          x[0][t] = mfma16x16x32(s0, f, x[0][t]);
+          x[1][t] = mfma16x16x32(s1, f, x[1][t]);
+        }
+      }
+    };
+    const auto add = [&](f32x4 (&d)[2][NT], auto&& factor) {
 #pragma unroll
       for (int t = 0; t < NT; ++t) {
-        a1[t] = mfma16x16x32(sf, frag_n<DV>(lds.o, to, tb0 + t, R), a1[t]);
-        a2[t] = mfma16x16x32(lf, piece(lds.e, tb0 + t, R), a2[t]);
-        a3[t] = mfma16x16x32(sf, piece(lds.g, tb0 + t, R), a3[t]);
+        const float f = factor(16 * (tb0 + t) + l);
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+          d[0][t][q] = fmaf(f, x[0][t][q], d[0][t][q]);
+          d[1][t][q] = fmaf(f, x[1][t][q], d[1][t][q]);
+        }
       }
-    }
+    };
+    states(lc, [&](int tb, int R) { return piece(lds.e, tb, R); });
+    add(dk, [&](int tok) { return rst[tok] * bet[tok]; });
+    states(sc_, [&](int tb, int R) { return frag_n<DV>(lds.o, to, tb, R); });
+    add(dq, [&](int tok) { return sc * gam[tok]; });
+    states(sc_, [&](int tb, int R) { return piece(lds.g, tb, R); });
+    add(dk, [&](int tok) { return -gam[tok] * bet[tok]; });
+    __syncthreads();  // dO, e and G are done with, the scores are there
+    {
+      const __amdgpu_buffer_rsrc_t rk = rows_rsrc(kp, t0, sr.len, a.sk.t, a.dk);
+      const __amdgpu_buffer_rsrc_t rq = rows_rsrc(qp, t0, sr.len, a.sq.t, a.dk);
 #pragma unroll
-    for (int t = 0; t < NT; ++t) {
-      const int tok = 16 * (tb0 + t) + l;
-      const float ga = gam[tok], rb = rst[tok] * bet[tok], gb = ga * bet[tok];
-#pragma unroll
-      for (int q = 0; q < 4; ++q) {
-        a1[t][q] *= sc * ga;
-        dk[t][q] += rb * a2[t][q] - gb * a3[t][q];
+      for (int j = 0; j < DK / 32; ++j) {
+        const int i = w * (DK / 32) + j;
+        dma16(rk, tile_off<DK>(i, lane, a.sk.t, 0, a.dk), lds.k + i * 1024);
+        dma16(rq, tile_off<DK>(i, lane, a.sq.t, 0, a.dk), lds.q + i * 1024);
       }
+      wait_vm<0>();
     }
-    __syncthreads();  // the scores are there
+    __syncthreads();
 #pragma unroll
-    for (int s = 0; s < 2; ++s) {
-      // tokens 32 s.. as the contraction index
-      const bf16x8 kf = frag_c<DK>(lds.k, tk, s, kb), qf = frag_c<DK>(lds.q, tk, s, kb);
-      const bf16x8 kn = __builtin_bit_cast(bf16x8, __builtin_bit_cast(s16x8, kf) ^ static_cast<short>(0x8000));
+    for (int s = 0; s < 2; ++s) {  // tokens 32 s.. as the contraction index
+      bf16x8 kf[2], kn[2], qf[2];
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        kf[i] = frag_c<DK>(lds.k, tk, s, kb0 + i);
+        qf[i] = frag_c<DK>(lds.q, tk, s, kb0 + i);
+        kn[i] = __builtin_bit_cast(bf16x8, __builtin_bit_cast(s16x8, kf[i]) ^ static_cast<short>(0x8000));
+      }
 #pragma unroll
       for (int t = 0; t < NT; ++t) {
         const int tb = tb0 + t;
-        const s16x4 none = {0, 0, 0, 0};
-        const auto pc = [&](int m, int b) { return *reinterpret_cast<const s16x4*>(lds.sc[m] + (tb * 4 + b) * kPiece + lane * 4); };
+        const auto pc = [&](int m, int at) { return *reinterpret_cast<const s16x4*>(lds.sc + (16 * m + at) * kPiece + lane * 4); };
         if (s <= tb / 2) {  // j <= i
-          const s16x4 p0 = pc(0, 2 * s), p1 = 2 * s + 1 <= tb ? pc(0, 2 * s + 1) : none;
-          a1[t] = mfma16x16x32(kf, join(p0, p1), a1[t]);
+          const bf16x8 f = join(pc(0, tb * 4 + 2 * s), 2 * s + 1 <= tb ? pc(0, tb * 4 + 2 * s + 1) : none);
+          dq[0][t] = mfma16x16x32(kf[0], f, dq[0][t]);
+          dq[1][t] = mfma16x16x32(kf[1], f, dq[1][t]);
         }
         if (s >= tb / 2) {  // i >= j
-          const s16x4 p0 = 2 * s >= tb ? pc(1, 2 * s) : none, p1 = pc(1, 2 * s + 1);
-          dk[t] = mfma16x16x32(qf, join(p0, p1), dk[t]);
+          const bf16x8 f = join(2 * s >= tb ? pc(1, tb * 4 + 2 * s) : none, pc(1, tb * 4 + 2 * s + 1));
+          dk[0][t] = mfma16x16x32(qf[0], f, dk[0][t]);
+          dk[1][t] = mfma16x16x32(qf[1], f, dk[1][t]);
         }
-        dk[t] = mfma16x16x32(kn, join(pc(2, 2 * s), pc(2, 2 * s + 1)), dk[t]);
+        // a diagonal block's halves have their zeros where the other has not
+        s16x4 m0 = pc(2, tb * 4 + 2 * s), m1 = pc(2, tb * 4 + 2 * s + 1);
+        if (2 * s == tb) m0 |= pc(2, 16 + tb);
+        if (2 * s + 1 == tb) m1 |= pc(2, 16 + tb);
+        const bf16x8 f = join(m0, m1);
+        dk[0][t] = mfma16x16x32(kn[0], f, dk[0][t]);
+        dk[1][t] = mfma16x16x32(kn[1], f, dk[1][t]);
       }
     }
-#pragma unroll
-    for (int t = 0; t < NT; ++t) {
-#pragma unroll
-      for (int q = 0; q < 4; ++q) dq[t][q] += a1[t][q];
-    }
-    if (w == 0) {  // gates, lane = token
-      float ge = 0.f, dl = 0.f;
-      for (int i = 0; i < n_rt; ++i) {
-        ge += ca.bf[(rec * n_rt + i) * 64 + lane];
-        dl += ca.zf[(rec * n_rt + i) * 64 + lane];
-      }
+    if (w == 3) {
       // a token that forgets everything has no gradient to its decay
       const float lw = lds.gt[192 + lane];
       if (lw - wave_shift_up(lw, 0.f) < -149.f) dl = 0.f;
@@ -618,15 +695,20 @@ __global__ __launch_bounds__(kGradThreads) void delta_chunk_grad(ChunkArgs ca) {
       }
     }
   }
+  // blocks kb0 and kb0 + 1 are eight neighbouring columns
+  const int col = index4(kb0, g);
+  if (col < a.dk) {
 #pragma unroll
-  for (int t = 0; t < NT; ++t) {
-    const int tok = 16 * (tb0 + t) + l, col = index4(kb, g);
-    if (tok < nt && col < a.dk) {
+    for (int t = 0; t < NT; ++t) {
+      const int tok = 16 * (tb0 + t) + l;
+      if (tok >= nt) continue;
       const int64_t tt = sr.t0 + t0 + tok;
-      *reinterpret_cast<uint2*>(static_cast<uint16_t*>(a.dq) + sr.b * a.sdq.b + hk * a.sdq.h + tt * a.sdq.t + col) =
-          make_uint2(pack2(dq[t][0], dq[t][1]), pack2(dq[t][2], dq[t][3]));
-      *reinterpret_cast<uint2*>(static_cast<uint16_t*>(a.dk_) + sr.b * a.sdk.b + hk * a.sdk.h + tt * a.sdk.t + col) =
-          make_uint2(pack2(dk[t][0], dk[t][1]), pack2(dk[t][2], dk[t][3]));
+      const auto put = [&](void* p, const Str3& s, const f32x4& u, const f32x4& v) {
+        *reinterpret_cast<uint4*>(static_cast<uint16_t*>(p) + sr.b * s.b + hk * s.h + tt * s.t + col) =
+            make_uint4(pack2(u[0], u[1]), pack2(u[2], u[3]), pack2(v[0], v[1]), pack2(v[2], v[3]));
+      };
+      put(a.dq, a.sdq, dq[0][t], dq[1][t]);
+      put(a.dk_, a.sdk, dk[0][t], dk[1][t]);
     }
   }
 }

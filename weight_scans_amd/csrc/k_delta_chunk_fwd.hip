@@ -166,8 +166,9 @@ __global__ __launch_bounds__(64 * (2 * NW + 2)) void delta_chunk_fwd(ChunkArgs c
       if constexpr (SAVE) {
         const int64_t rec = rec0 + static_cast<int64_t>(c) * a.H;
 #pragma unroll
-        for (int b = 0; b < NB; ++b)
-          *reinterpret_cast<s16x4*>(ca.sf + ((rec * n_rt + rt) * NB + b) * kPiece + lane * 4) = turned(sx, b, lane);
+        for (int b = 0; b < NB; b += 2)
+          *reinterpret_cast<bf16x8*>(ca.sf + ((rec * n_rt + rt) * NB + b) * kPiece + lane * 8) =
+              join(turned(sx, b, lane), turned(sx, b + 1, lane));
 #pragma unroll
         for (int tb = 0; tb < 4; ++tb)
           *reinterpret_cast<f32x4*>(ca.yb + ((rec * n_rt + rt) * 4 + tb) * 256 + lane * 4) = o[tb];

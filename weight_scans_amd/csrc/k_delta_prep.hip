@@ -58,9 +58,9 @@ __global__ __launch_bounds__(kThreads) void delta_prep(ChunkArgs ca) {
     n = lo;
     c = slot - chunk_slot0(true, n, seq_range(a.cu, n, a.T).t0, a.T, kDeltaChunk);
   } else {
-    const int64_t nc = (a.T + kDeltaChunk - 1) / kDeltaChunk;
-    n = slot / nc;
-    c = slot % nc;
+    const uint32_t nc = static_cast<uint32_t>((a.T + kDeltaChunk - 1) / kDeltaChunk);
+    n = static_cast<uint32_t>(slot) / nc;
+    c = static_cast<uint32_t>(slot) % nc;
   }
   const SeqRange sr = seq_range(a.cu, n, a.T);
   const int64_t t0 = c * kDeltaChunk;
@@ -87,21 +87,31 @@ __global__ __launch_bounds__(kThreads) void delta_prep(ChunkArgs ca) {
     gt[128 + lane] = fexp2((readlane_f(lw, 63) - lw) + (readlane_f(lf, 63) - lf));
     gt[192 + lane] = lw;
     gt[256 + lane] = lf;
+    if (ca.ytf) {  // training only
+#pragma unroll
+      for (int x = 1; x < 4; ++x) {
+        const float mw = readlane_f(lw, 16 * x - 1), mf = readlane_f(lf, 16 * x - 1);
+        if (lane >> 4 == x) gt[320 + lane] = fexp2((lw - mw) + (lf - mf));
+        if (lane < 16 * x) gt[320 + 64 * x + lane] = fexp2((mw - lw) + (mf - lf));
+      }
+    }
   }
   __syncthreads();
 
   const uint16_t* kp = static_cast<const uint16_t*>(a.k) + sr.b * a.sk.b + hk * a.sk.h + (sr.t0 + t0) * a.sk.t;
   const uint16_t* qp = static_cast<const uint16_t*>(a.q) + sr.b * a.sq.b + hk * a.sq.h + (sr.t0 + t0) * a.sq.t;
-  const bf16x8 none = as_frag(0, 0, 0, 0);
-  const auto row = [&](const uint16_t* p, int64_t st, int tb, int s) {
-    const int t = 16 * tb + l, col = 32 * s + 8 * g;
-    return t < nt && col < a.dk ? *reinterpret_cast<const bf16x8*>(p + t * st + col) : none;
+  // rows past the chunk's end and columns past dk read as zeros
+  const __amdgpu_buffer_rsrc_t rk = buffer_rsrc(kp, static_cast<int>(((nt - 1) * a.sk.t + a.dk) * 2));
+  const __amdgpu_buffer_rsrc_t rq = buffer_rsrc(qp, static_cast<int>(((nt - 1) * a.sq.t + a.dk) * 2));
+  const auto row = [&](const __amdgpu_buffer_rsrc_t& r, int64_t st, int tb, int s) {
+    const int col = 32 * s + 8 * g;
+    return load16(r, col < a.dk ? static_cast<uint32_t>(((16 * tb + l) * static_cast<int>(st) + col) * 2) : kPastEnd);
   };
   bf16x8 kf[4][NS];
 #pragma unroll
   for (int tb = 0; tb < 4; ++tb)
 #pragma unroll
-    for (int s = 0; s < NS; ++s) kf[tb][s] = row(kp, a.sk.t, tb, s);
+    for (int s = 0; s < NS; ++s) kf[tb][s] = row(rk, a.sk.t, tb, s);
 
   // decay e^(l_i - l_j), zero above the diagonal (and on it for `strict`)
   const auto decay = [&](int i, int j, bool strict) {
@@ -209,7 +219,7 @@ __global__ __launch_bounds__(kThreads) void delta_prep(ChunkArgs ca) {
   for (int tb = 0; tb < 4; ++tb)
 #pragma unroll
     for (int s = 0; s < NS; ++s)
-      qf[tb][s] = (tb == w || (ca.ptf && tb > w)) ? row(qp, a.sq.t, tb, s) : none;
+      qf[tb][s] = row(rq, a.sq.t, tb, s);
 #pragma unroll
   for (int wc = 0; wc < 4; ++wc) {
     if (wc != w) continue;
