@@ -426,15 +426,15 @@ struct GradLds {
 
 constexpr int kGradThreads = 256;
 
-template <int DK, int DV>
-__global__ __launch_bounds__(kGradThreads) void
+template <int DK, int DV, bool SHARED>
+__global__ __launch_bounds__(kGradThreads) __attribute__((amdgpu_waves_per_eu(2))) void
 delta_chunk_grad(ChunkArgs ca) {
   const DeltaArgs& a = ca.a;
   constexpr int NB = DK / 16, NP = NB / 2, NT = NP, NR = DV / 32;  // NT blocks of 16 tokens a wave
   __shared__ GradLds<DK, DV> lds;
   const int lane = threadIdx.x & 63, l = lane & 15, g = lane >> 4;
   const int w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const int hk = static_cast<int>(blockIdx.x % a.Hk), grp = a.H / a.Hk;
+  const int hk = static_cast<int>(blockIdx.x % a.Hk), grp = SHARED ? a.H / a.Hk : 1;
   const int64_t slot = blockIdx.x / a.Hk;
   int64_t n, c;
   if (a.cu) {
@@ -501,7 +501,6 @@ delta_chunk_grad(ChunkArgs ca) {
         st[rt] = __builtin_bit_cast(s16x8, load16(r, (rt * NB + kb0) * (kPiece * 2) + lane * 16));
     };
     columns(ca.lf, lc);
-    columns(ca.sf, sc_);
     // gates: dlog_alpha and dbeta of token `lane`, over the row tiles
     float dl = 0.f, ge = 0.f;
     if (w == 3) {
@@ -584,6 +583,7 @@ delta_chunk_grad(ChunkArgs ca) {
 #pragma unroll
         for (int y = 0; y <= x; ++y) finish(x, y, v[x * (x + 1) / 2 + y]);
     }
+    columns(ca.sf, sc_);
     // ---- dv: a pair of row tiles, eight neighbouring columns of v
     for (int R = w; R < nr; R += 4) {
       const int col = 32 * R + 8 * g;
@@ -721,8 +721,14 @@ hipError_t launch(const ChunkArgs& c, hipStream_t s) {
   hipError_t e = hipGetLastError();
   if (e != hipSuccess || c.slots == 0) return e;
   const dim3 grid(static_cast<unsigned>(c.slots * c.a.Hk));
-  if (c.a.dv <= 64) delta_chunk_grad<DK, 64><<<grid, kGradThreads, 0, s>>>(c);
-  else delta_chunk_grad<DK, 128><<<grid, kGradThreads, 0, s>>>(c);
+  const bool shared = c.a.H != c.a.Hk;
+  if (c.a.dv <= 64) {
+    if (shared) delta_chunk_grad<DK, 64, true><<<grid, kGradThreads, 0, s>>>(c);
+    else delta_chunk_grad<DK, 64, false><<<grid, kGradThreads, 0, s>>>(c);
+  } else {
+    if (shared) delta_chunk_grad<DK, 128, true><<<grid, kGradThreads, 0, s>>>(c);
+    else delta_chunk_grad<DK, 128, false><<<grid, kGradThreads, 0, s>>>(c);
+  }
   return hipGetLastError();
 }
 
