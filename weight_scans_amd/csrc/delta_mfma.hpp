@@ -168,6 +168,20 @@ __device__ __forceinline__ __amdgpu_buffer_rsrc_t rows_rsrc(const uint16_t* base
   return buffer_rsrc(base + (n > 0 ? t0 * st : 0), n > 0 ? static_cast<int>(((n - 1) * st + d) * 2) : 0);
 }
 
+// Order of the instructions between two of these fences: N times MF matrix
+// instructions and then VA vector ones.  A wave issues in order and runs alone
+// on its SIMD here, so a matrix product hides only the vector work that stands
+// between its instructions.
+template <int N, int MF, int VA>
+__device__ __forceinline__ void interleave() {
+#pragma unroll
+  for (int i = 0; i < N; ++i) {
+    __builtin_amdgcn_sched_group_barrier(0x8, MF, 0);
+    __builtin_amdgcn_sched_group_barrier(0x2, VA, 0);
+  }
+  __builtin_amdgcn_sched_barrier(0);
+}
+
 // 16- and 4-byte buffer loads, zeros past the end: unlike loads under a
 // condition they draw no branch and no wait of their own.
 __device__ __forceinline__ bf16x8 load16(__amdgpu_buffer_rsrc_t r, uint32_t off) {

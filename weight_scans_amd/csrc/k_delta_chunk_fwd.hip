@@ -210,74 +210,61 @@ __global__ __launch_bounds__(64 * (2 * NW + 2)) void delta_chunk_fwd(ChunkArgs c
     const auto gate = [&](int m, int tb) { return *reinterpret_cast<const f32x4*>(gt + 64 * m + 16 * tb); };
     // the next chunk's Y, fetched as this one's is used up
     yp += (c + 1 < nc ? static_cast<int64_t>(a.H) : 0) * kYf;
-    f32x4 E[4], be[4];
+    uint16_t* sx = lds.sx[c & 1][wave] + lane * 8;
+    uint16_t* ux = lds.ux[c & 1][wave] + lane * 8;
+    f32x4 E[4], be[4], gm[4], rs[4];
     s16x4 vv[4];
+    bf16x8 kf[2][NS], kc[NB];
+    Pair8 z[2], u;
+    f32x4 x[4];
+    // R = V - e^l (K S^T) and the operand beta R, a half of the tokens at a time
+    const auto read_k = [&](int half) {
 #pragma unroll
-    for (int tb = 0; tb < 4; ++tb) {
-      E[tb] = zero4();
-      vv[tb] = col4<VW>(lds.v[sl], tv, tb, wave);
-      be[tb] = gate(1, tb);
-    }
+      for (int i = 0; i < 2; ++i)
 #pragma unroll
-    for (int half = 0; half < 2; ++half)
+        for (int s = 0; s < NS; ++s) kf[i][s] = frag_n<DK>(kt, tk, 2 * half + i, s);
+    };
+    const auto ks = [&](int half) {
 #pragma unroll
       for (int s = 0; s < NS; ++s)
 #pragma unroll
-        for (int tb = 2 * half; tb < 2 * half + 2; ++tb) {
-          const bf16x8 kf = frag_n<DK>(kt, tk, tb, s);
-          E[tb] = mfma16x16x32(kf, sp[s].hi, E[tb]);
-          E[tb] = mfma16x16x32(kf, sp[s].lo, E[tb]);
+        for (int i = 0; i < 2; ++i) {
+          E[2 * half + i] = mfma16x16x32(kf[i][s], sp[s].hi, s ? E[2 * half + i] : zero4());
+          E[2 * half + i] = mfma16x16x32(kf[i][s], sp[s].lo, E[2 * half + i]);
         }
-    // S and U of this chunk for the output wave
-    uint16_t* sx = lds.sx[c & 1][wave] + lane * 8;
-    uint16_t* ux = lds.ux[c & 1][wave] + lane * 8;
-#pragma unroll
-    for (int s = 0; s < NS; ++s) {
-      *reinterpret_cast<bf16x8*>(sx + s * kFrag) = sp[s].hi;
-      *reinterpret_cast<bf16x8*>(sx + (NS + s) * kFrag) = sp[s].lo;
-    }
-    const float whole = lds.gt[sl][63];
-#pragma unroll
-    for (int b = 0; b < NB; ++b)
-#pragma unroll
-      for (int q = 0; q < 4; ++q) S[b][q] *= whole;
-    Pair8 z[2];
-#pragma unroll
-    for (int half = 0; half < 2; ++half) {
+    };
+    const auto residual = [&](int half) {
       f32x4 Z[2];
 #pragma unroll
       for (int i = 0; i < 2; ++i) {
         const int tb = 2 * half + i;
-        const f32x4 gm = gate(0, tb), v = widen(vv[tb]);
+        const f32x4 v = widen(vv[tb]);
 #pragma unroll
         for (int q = 0; q < 4; ++q) {
-          E[tb][q] = fmaf(-gm[q], E[tb][q], v[q]);
+          E[tb][q] = fmaf(-gm[tb][q], E[tb][q], v[q]);
           Z[i][q] = be[tb][q] * E[tb][q];
         }
       }
       z[half] = split8(Z[0], Z[1]);
-    }
+    };
+    // Y (beta R)
+    const auto solve = [&](int half) {
 #pragma unroll
-    for (int half = 0; half < 2; ++half) {
-      f32x4 x[2];
+      for (int s = 0; s <= half; ++s)
 #pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        const int ib = 2 * half + i;
-        x[i] = zero4();
+        for (int m = 0; m < 3; ++m)
 #pragma unroll
-        for (int s = 0; s <= half; ++s) {
-          const int f = half ? 2 * ib - 2 + s : ib;
-          x[i] = mfma16x16x32(yf[2 * f + 1], z[s].hi, x[i]);
-          x[i] = mfma16x16x32(yf[2 * f], z[s].lo, x[i]);
-          x[i] = mfma16x16x32(yf[2 * f], z[s].hi, x[i]);
-        }
-      }
-#pragma unroll
-      for (int f = half ? 4 : 0; f < (half ? 12 : 4); ++f) yf[f] = *reinterpret_cast<const bf16x8*>(yp + f * kFrag);
+          for (int i = 0; i < 2; ++i) {
+            const int ib = 2 * half + i, f = half ? 2 * ib - 2 + s : ib;
+            x[ib] = mfma16x16x32(yf[2 * f + (m == 0)], m == 1 ? z[s].lo : z[s].hi, m + s ? x[ib] : zero4());
+          }
+    };
+    // e, U for the output wave, and the operand e^(l_C - l) U
+    const auto errors = [&](int half) {
 #pragma unroll
       for (int i = 0; i < 2; ++i)
 #pragma unroll
-        for (int q = 0; q < 4; ++q) E[2 * half + i][q] -= x[i][q];
+        for (int q = 0; q < 4; ++q) E[2 * half + i][q] -= x[2 * half + i][q];
       if constexpr (SAVE)
         *reinterpret_cast<bf16x8*>(ca.ef + (((rec0 + static_cast<int64_t>(c) * a.H) * n_rt + rt) * 2 + half) * kFrag +
                                    raw_at(lane)) = raw_order(round8(E[2 * half], E[2 * half + 1]), lane);
@@ -285,27 +272,75 @@ __global__ __launch_bounds__(64 * (2 * NW + 2)) void delta_chunk_fwd(ChunkArgs c
       for (int i = 0; i < 2; ++i)
 #pragma unroll
         for (int q = 0; q < 4; ++q) E[2 * half + i][q] *= be[2 * half + i][q];
-      {
-        const Pair8 u = split8(E[2 * half], E[2 * half + 1]);
-        *reinterpret_cast<bf16x8*>(ux + half * kFrag) = u.hi;
-        *reinterpret_cast<bf16x8*>(ux + (2 + half) * kFrag) = u.lo;
-      }
+      const Pair8 p = split8(E[2 * half], E[2 * half + 1]);
+      *reinterpret_cast<bf16x8*>(ux + half * kFrag) = p.hi;
+      *reinterpret_cast<bf16x8*>(ux + (2 + half) * kFrag) = p.lo;
 #pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        const f32x4 rs = gate(2, 2 * half + i);
+      for (int i = 0; i < 2; ++i)
 #pragma unroll
-        for (int q = 0; q < 4; ++q) E[2 * half + i][q] *= rs[q];
-      }
-      const Pair8 u = split8(E[2 * half], E[2 * half + 1]);
+        for (int q = 0; q < 4; ++q) E[2 * half + i][q] *= rs[2 * half + i][q];
+      u = split8(E[2 * half], E[2 * half + 1]);
+    };
+    const auto read_kc = [&](int half) {
 #pragma unroll
-      for (int b = 0; b < NB; ++b) {
-        const bf16x8 kc = frag_c<DK>(kt, tk, half, b);
-        S[b] = mfma16x16x32(kc, u.hi, S[b]);
-        S[b] = mfma16x16x32(kc, u.lo, S[b]);
-      }
+      for (int b = 0; b < NB; ++b) kc[b] = frag_c<DK>(kt, tk, half, b);
+    };
+    const auto update = [&](const Pair8& p) {
+#pragma unroll
+      for (int b = 0; b < NB; ++b) S[b] = mfma16x16x32(kc[b], p.hi, S[b]);
+#pragma unroll
+      for (int b = 0; b < NB; ++b) S[b] = mfma16x16x32(kc[b], p.lo, S[b]);
+    };
+
+    read_k(0);
+#pragma unroll
+    for (int tb = 0; tb < 4; ++tb) {
+      gm[tb] = gate(0, tb);
+      be[tb] = gate(1, tb);
+      rs[tb] = gate(2, tb);
+      vv[tb] = col4<VW>(lds.v[sl], tv, tb, wave);
+    }
+    const float whole = lds.gt[sl][63];
+    ks(0);
+#pragma unroll
+    for (int s = 0; s < NS; ++s) {  // S of this chunk for the output wave
+      *reinterpret_cast<bf16x8*>(sx + s * kFrag) = sp[s].hi;
+      *reinterpret_cast<bf16x8*>(sx + (NS + s) * kFrag) = sp[s].lo;
+    }
+#pragma unroll
+    for (int b = 0; b < NB; ++b)
+#pragma unroll
+      for (int q = 0; q < 4; ++q) S[b][q] *= whole;
+    read_k(1);
+    interleave<4 * NS, 1, 2>();
+    ks(1);
+    residual(0);
+    interleave<4 * NS, 1, 48 / (4 * NS)>();
+    solve(0);
+    residual(1);
+    interleave<6, 1, 8>();
+    read_kc(0);
+    solve(1);
+    errors(0);
+#pragma unroll
+    for (int f = 0; f < 4; ++f) yf[f] = *reinterpret_cast<const bf16x8*>(yp + f * kFrag);
+    interleave<12, 1, 6>();
+    const Pair8 u0 = u;
+    update(u0);
+    errors(1);
+#pragma unroll
+    for (int f = 4; f < 12; ++f) yf[f] = *reinterpret_cast<const bf16x8*>(yp + f * kFrag);
+    interleave<2 * NB, 1, 72 / (2 * NB)>();
+    read_kc(1);
+#pragma unroll
+    for (int b = 0; b < NB; ++b) {
+      S[b] = mfma16x16x32(kc[b], u.hi, S[b]);
+      S[b] = mfma16x16x32(kc[b], u.lo, S[b]);
     }
 #pragma unroll
     for (int s = 0; s < NS; ++s) sp[s] = split8(S[2 * s], S[2 * s + 1]);
+    __builtin_amdgcn_sched_group_barrier(0x8, 6, 0);
+    interleave<(2 * NB - 6) / 2, 2, 12>();
   }
   lds_barrier();
   if (r < a.dv) {
