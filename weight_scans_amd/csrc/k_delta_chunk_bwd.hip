@@ -259,125 +259,155 @@ __global__ __launch_bounds__(64 * (2 * NW + 2)) void delta_chunk_rev(ChunkArgs c
     fetch(nc - 1);
     fetch_e(nc - 1);
   }
+  Pair8 sp[NS];
+#pragma unroll
+  for (int s = 0; s < NS; ++s) sp[s] = split8(S[2 * s], S[2 * s + 1]);
+  uint16_t* turn = lds.turn[wave];
   lds_barrier();
   lds_barrier();
   for (int i = 1; i <= nc; ++i) {
     const int c = nc - i;
     const int64_t rec = rec0 + static_cast<int64_t>(c) * a.H;
-    Pair8 sp[NS];
-#pragma unroll
-    for (int s = 0; s < NS; ++s) sp[s] = split8(S[2 * s], S[2 * s + 1]);
-    uint16_t* turn = lds.turn[wave];
 #pragma unroll
     for (int s = 0; s < NS; ++s) *reinterpret_cast<bf16x8*>(&turn[s * kFrag + lane * 8]) = sp[s].hi;
-#pragma unroll
-    for (int b = 0; b < NB; b += 2)
-      *reinterpret_cast<bf16x8*>(ca.lf + ((rec * n_rt + rt) * NB + b) * kPiece + lane * 8) =
-          join(turned(turn, b, lane), turned(turn, b + 1, lane));
     lds_barrier();  // A
     const int sl = (i - 1) % 3;
     const char* kt = lds.k[sl];
     const float* gt = lds.gt[(i - 1) & 3];
     const auto gate = [&](int m, int tb) { return *reinterpret_cast<const f32x4*>(gt + 64 * m + 16 * tb + 4 * g); };
-    f32x4 x1[4];
+    f32x4 x1[4], x2[NB], G[4], x[4];
     s16x4 vv[4];
+    bf16x8 kf[2][NS], kc[NB], gf[2], lf[NB / 2];
+    Pair8 z[2], u;
+    float xe[16], yv[16];
+    const auto read_k = [&](int half) {
+#pragma unroll
+      for (int i = 0; i < 2; ++i)
+#pragma unroll
+        for (int s = 0; s < NS; ++s) kf[i][s] = frag_n<DK>(kt, tk, 2 * half + i, s);
+    };
+    const auto ks = [&](int half) {
+#pragma unroll
+      for (int s = 0; s < NS; ++s)
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          G[2 * half + i] = mfma16x16x32(kf[i][s], sp[s].hi, s ? G[2 * half + i] : zero4());
+          G[2 * half + i] = mfma16x16x32(kf[i][s], sp[s].lo, G[2 * half + i]);
+        }
+    };
+    // dU, and the operand beta dU
+    const auto residual = [&](int half) {
+      f32x4 Z[2];
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        const int tb = 2 * half + i;
+        const f32x4 rs = gate(2, tb), be = gate(1, tb);
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+          G[tb][q] = fmaf(rs[q], G[tb][q], x1[tb][q]);
+          Z[i][q] = be[q] * G[tb][q];
+        }
+      }
+      z[half] = split8(Z[0], Z[1]);
+    };
+    // Y^T (beta dU): tokens of the first half also take the second's
+    const auto solve = [&](int half) {
+#pragma unroll
+      for (int s = 1; s >= half; --s)
+#pragma unroll
+        for (int m = 0; m < 3; ++m)
+#pragma unroll
+          for (int i = 0; i < 2; ++i) {
+            const int jb = 2 * half + i, f = half ? jb + 2 : 2 * jb + s;
+            x[jb] = mfma16x16x32(yf[2 * f + (m == 0)], m == 1 ? z[s].lo : z[s].hi, m || s == 0 ? x[jb] : zero4());
+          }
+    };
+    // G, its products with e and v, and the operand -e^l F
+    const auto errors = [&](int half) {
+#pragma unroll
+      for (int i = 0; i < 2; ++i)
+#pragma unroll
+        for (int q = 0; q < 4; ++q) G[2 * half + i][q] -= x[2 * half + i][q];
+      gf[half] = raw_order(round8(G[2 * half], G[2 * half + 1]), lane);
+      const s16x8 e = __builtin_bit_cast(s16x8, raw_order(ef[half], lane));
+      const f32x4 ee[2] = {widen(__builtin_shufflevector(e, e, 0, 1, 2, 3)), widen(__builtin_shufflevector(e, e, 4, 5, 6, 7))};
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        const int tb = 2 * half + i;
+        const f32x4 v = widen(vv[tb]), be = gate(1, tb), gm = gate(0, tb);
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+          xe[4 * tb + q] = G[tb][q] * ee[i][q];
+          G[tb][q] *= be[q];
+          yv[4 * tb + q] = v[q] * G[tb][q];
+          G[tb][q] *= -gm[q];
+        }
+      }
+      u = split8(G[2 * half], G[2 * half + 1]);
+    };
+    const auto read_kc = [&](int half) {
+#pragma unroll
+      for (int b = 0; b < NB; ++b) kc[b] = frag_c<DK>(kt, tk, half, b);
+    };
+
+#pragma unroll
+    for (int b = 0; b < NB; ++b) x2[b] = *reinterpret_cast<const f32x4*>(&lds.x2[wave][b * 256 + lane * 4]);
 #pragma unroll
     for (int tb = 0; tb < 4; ++tb) {
       vv[tb] = col4<VW>(lds.v[sl], tv, tb, wave);
       x1[tb] = *reinterpret_cast<const f32x4*>(&lds.x1[wave][tb * 256 + lane * 4]);
     }
     const float whole = gt[63];
+    read_k(1);
+    lds_barrier();  // B
+#pragma unroll
+    for (int b = 0; b < NB; b += 2) lf[b / 2] = join(turned(turn, b, lane), turned(turn, b + 1, lane));
+    ks(1);
+#pragma unroll
+    for (int b = 0; b < NB; ++b)
+#pragma unroll
+      for (int q = 0; q < 4; ++q) S[b][q] = fmaf(whole, S[b][q], x2[b][q]);
+    read_k(0);
+    interleave<4 * NS, 1, 2>();
+    ks(0);
+    residual(1);
+    interleave<4 * NS, 1, 40 / (4 * NS)>();
+    solve(1);
+    residual(0);
+    interleave<6, 1, 7>();
+    read_kc(1);
+    solve(0);
+    errors(1);
+    interleave<12, 1, 7>();
 #pragma unroll
     for (int b = 0; b < NB; ++b) {
-      const f32x4 x2 = *reinterpret_cast<const f32x4*>(&lds.x2[wave][b * 256 + lane * 4]);
-#pragma unroll
-      for (int q = 0; q < 4; ++q) S[b][q] = fmaf(whole, S[b][q], x2[q]);
+      S[b] = mfma16x16x32(kc[b], u.hi, S[b]);
+      S[b] = mfma16x16x32(kc[b], u.lo, S[b]);
     }
-    lds_barrier();  // B
-    f32x4 G[4], Z[4];
+    errors(0);
+    interleave<2 * NB, 1, 80 / (2 * NB)>();
+    // the next chunk's, before this one's stores (waited for in order of issue)
+    fetch(max(c - 1, 0));
+    fetch_e(max(c - 1, 0));
+    read_kc(0);
 #pragma unroll
-    for (int tb = 0; tb < 4; ++tb) G[tb] = zero4();
-#pragma unroll
-    for (int s = 0; s < NS; ++s)
-#pragma unroll
-      for (int tb = 0; tb < 4; ++tb) {
-        const bf16x8 kf = frag_n<DK>(kt, tk, tb, s);
-        G[tb] = mfma16x16x32(kf, sp[s].hi, G[tb]);
-        G[tb] = mfma16x16x32(kf, sp[s].lo, G[tb]);
-      }
-#pragma unroll
-    for (int tb = 0; tb < 4; ++tb) {
-      const f32x4 rs = gate(2, tb), be = gate(1, tb);
-#pragma unroll
-      for (int q = 0; q < 4; ++q) {
-        G[tb][q] = fmaf(rs[q], G[tb][q], x1[tb][q]);
-        Z[tb][q] = be[q] * G[tb][q];
-      }
+    for (int b = 0; b < NB; ++b) {
+      S[b] = mfma16x16x32(kc[b], u.hi, S[b]);
+      S[b] = mfma16x16x32(kc[b], u.lo, S[b]);
     }
-    {
-      const Pair8 z0 = split8(Z[0], Z[1]), z1 = split8(Z[2], Z[3]);
+    const int tok = 16 * (l >> 2) + 4 * g + (l & 3);
+    const float be_ = row_sums(xe, l);
+    lds.vdv[wave][(i - 1) & 1][tok] = row_sums(yv, l);
+    interleave<2 * NB, 1, 96 / (2 * NB)>();
 #pragma unroll
-      for (int jb = 0; jb < 4; ++jb) {
-        f32x4 x = zero4();
+    for (int s = 0; s < NS; ++s) sp[s] = split8(S[2 * s], S[2 * s + 1]);
 #pragma unroll
-        for (int s = jb / 2; s < 2; ++s) {
-          const int f = jb < 2 ? 2 * jb + s : jb + 2;
-          const Pair8& z = s ? z1 : z0;
-          x = mfma16x16x32(yf[2 * f + 1], z.hi, x);
-          x = mfma16x16x32(yf[2 * f], z.lo, x);
-          x = mfma16x16x32(yf[2 * f], z.hi, x);
-        }
-#pragma unroll
-        for (int q = 0; q < 4; ++q) G[jb][q] -= x[q];
-      }
-    }
-    if (i < nc) fetch(c - 1);
+    for (int b = 0; b < NB; b += 2)
+      *reinterpret_cast<bf16x8*>(ca.lf + ((rec * n_rt + rt) * NB + b) * kPiece + lane * 8) = lf[b / 2];
 #pragma unroll
     for (int s = 0; s < 2; ++s)
-      *reinterpret_cast<bf16x8*>(ca.gf + ((rec * n_rt + rt) * 2 + s) * kFrag + raw_at(lane)) =
-          raw_order(round8(G[2 * s], G[2 * s + 1]), lane);
-    {  // G.e and v.dv: token 16 (l / 4) + 4 g + l % 4
-      float x[16], y[16];
-#pragma unroll
-      for (int s = 0; s < 2; ++s) {
-        const s16x8 e = __builtin_bit_cast(s16x8, raw_order(ef[s], lane));
-        const f32x4 e0 = widen(__builtin_shufflevector(e, e, 0, 1, 2, 3));
-        const f32x4 e1 = widen(__builtin_shufflevector(e, e, 4, 5, 6, 7));
-#pragma unroll
-        for (int q = 0; q < 4; ++q) {
-          x[8 * s + q] = G[2 * s][q] * e0[q];
-          x[8 * s + 4 + q] = G[2 * s + 1][q] * e1[q];
-        }
-      }
-      if (i < nc) fetch_e(c - 1);
-#pragma unroll
-      for (int tb = 0; tb < 4; ++tb) {
-        const f32x4 v = widen(vv[tb]), be = gate(1, tb);
-#pragma unroll
-        for (int q = 0; q < 4; ++q) {
-          G[tb][q] *= be[q];
-          y[4 * tb + q] = v[q] * G[tb][q];
-        }
-      }
-      const int tok = 16 * (l >> 2) + 4 * g + (l & 3);
-      ca.bf[(rec * n_rt + rt) * 64 + tok] = row_sums(x, l);
-      lds.vdv[wave][(i - 1) & 1][tok] = row_sums(y, l);
-    }
-#pragma unroll
-    for (int tb = 0; tb < 4; ++tb) {
-      const f32x4 gm = gate(0, tb);
-#pragma unroll
-      for (int q = 0; q < 4; ++q) G[tb][q] *= -gm[q];
-    }
-    const Pair8 u0 = split8(G[0], G[1]), u1 = split8(G[2], G[3]);
-#pragma unroll
-    for (int b = 0; b < NB; ++b) {
-      const bf16x8 k0 = frag_c<DK>(kt, tk, 0, b), k1 = frag_c<DK>(kt, tk, 1, b);
-      S[b] = mfma16x16x32(k0, u0.hi, S[b]);
-      S[b] = mfma16x16x32(k0, u0.lo, S[b]);
-      S[b] = mfma16x16x32(k1, u1.hi, S[b]);
-      S[b] = mfma16x16x32(k1, u1.lo, S[b]);
-    }
+      *reinterpret_cast<bf16x8*>(ca.gf + ((rec * n_rt + rt) * 2 + s) * kFrag + raw_at(lane)) = gf[s];
+    ca.bf[(rec * n_rt + rt) * 64 + tok] = be_;
   }
   lds_barrier();
   lds_barrier();

@@ -216,6 +216,7 @@ __global__ __launch_bounds__(64 * (2 * NW + 2)) void delta_chunk_fwd(ChunkArgs c
     s16x4 vv[4];
     bf16x8 kf[2][NS], kc[NB];
     Pair8 z[2], u;
+    bf16x8 ef[2];
     f32x4 x[4];
     // R = V - e^l (K S^T) and the operand beta R, a half of the tokens at a time
     const auto read_k = [&](int half) {
@@ -265,9 +266,7 @@ __global__ __launch_bounds__(64 * (2 * NW + 2)) void delta_chunk_fwd(ChunkArgs c
       for (int i = 0; i < 2; ++i)
 #pragma unroll
         for (int q = 0; q < 4; ++q) E[2 * half + i][q] -= x[2 * half + i][q];
-      if constexpr (SAVE)
-        *reinterpret_cast<bf16x8*>(ca.ef + (((rec0 + static_cast<int64_t>(c) * a.H) * n_rt + rt) * 2 + half) * kFrag +
-                                   raw_at(lane)) = raw_order(round8(E[2 * half], E[2 * half + 1]), lane);
+      if constexpr (SAVE) ef[half] = raw_order(round8(E[2 * half], E[2 * half + 1]), lane);
 #pragma unroll
       for (int i = 0; i < 2; ++i)
 #pragma unroll
@@ -341,6 +340,13 @@ __global__ __launch_bounds__(64 * (2 * NW + 2)) void delta_chunk_fwd(ChunkArgs c
     for (int s = 0; s < NS; ++s) sp[s] = split8(S[2 * s], S[2 * s + 1]);
     __builtin_amdgcn_sched_group_barrier(0x8, 6, 0);
     interleave<(2 * NB - 6) / 2, 2, 12>();
+    if constexpr (SAVE) {
+      // after the loads of the next chunk's Y: these are waited for in the order
+      // of issue, and a store before them would be waited for as well
+      uint16_t* p = ca.ef + ((rec0 + static_cast<int64_t>(c) * a.H) * n_rt + rt) * 2 * kFrag + raw_at(lane);
+      *reinterpret_cast<bf16x8*>(p) = ef[0];
+      *reinterpret_cast<bf16x8*>(p + kFrag) = ef[1];
+    }
   }
   lds_barrier();
   if (r < a.dv) {
