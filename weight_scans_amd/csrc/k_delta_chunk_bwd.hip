@@ -172,7 +172,8 @@ __global__ __launch_bounds__(64 * (2 * NW + 2)) void delta_chunk_rev(ChunkArgs c
     }
     z = wave_sum(z);
     for (int i = 0; i <= nc + 1; ++i) {
-      lds_barrier();
+      lds_barrier();  // A
+      lds_barrier();  // B: the results of the step before have been taken
       if (i >= 2) {
         const int64_t rec = rec0 + static_cast<int64_t>(nc + 1 - i) * a.H;
         const float x = lds.dyy[w][(i - 2) % 3][lane] - lds.vdv[w][i & 1][lane];
@@ -220,7 +221,6 @@ __global__ __launch_bounds__(64 * (2 * NW + 2)) void delta_chunk_rev(ChunkArgs c
           x2[b] = mfma16x16x32(q1, d1.lo, x2[b]);
         }
       }
-      lds_barrier();
       if (i < nc) {
 #pragma unroll
         for (int tb = 0; tb < 4; ++tb) *reinterpret_cast<f32x4*>(&lds.x1[w][tb * 256 + lane * 4]) = x1[tb];
