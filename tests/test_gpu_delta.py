@@ -279,3 +279,35 @@ def test_empty():
     assert torch.equal(grads[5], g["dstate"])
     _, end, _ = ws.gl_delta_fwd(*none, want_state=True)
     assert (end == 0).all()
+
+
+@pytest.mark.parametrize("dk,dv,T,lens", [
+    (64, 64, 64, None), (64, 64, 65, None), (64, 64, 1, None), (20, 36, 200, None), (128, 128, 257, None),
+    (96, 80, 130, None), (4, 4, 70, None), (64, 64, 264, [1, 63, 0, 65, 130, 5]), (128, 44, 200, [0, 200])])
+@pytest.mark.parametrize("order", ["bhtd", "bthd"])
+def test_fp32_chunks(dk, dv, T, lens, order):
+    """A forward in fp32 that saves nothing runs on the matrix cores."""
+    d = ws.make_delta_desc(1, T, 4, 2, dk, dv, ws.GL_DTYPE_F32, ws.GL_DTYPE_F32)
+    assert ws.delta_path_name(d).startswith("delta-mfma-f32")
+    run_case(dk + T, 1 if lens else 2, 4, 2, T, dk, dv, F32, lens=lens, order=order, saved=False)
+
+
+def test_fp32_chunks_forgetting():
+    def edit(x):
+        x["log_alpha"][0, 0, 3] = x["log_alpha"][0, 0, 70] = x["log_alpha"][0, 1, 0] = -torch.inf
+        x["log_alpha"][0, 1, 40:100] = 0.0
+        x["beta"][0, 0, 10:90] = 0.0
+        x["beta"][0, 1, ::2] = 1.0
+        x["log_alpha"][1, 0, 20:40] = -torch.inf
+        x["log_alpha"][1, 1, :] = -60.0
+    run_case(5, 2, 2, 2, 140, 64, 64, F32, edit=edit, saved=False)
+
+
+def test_fp32_unaligned_views_take_the_serial_kernel():
+    """Slices of a wider row that start at 4 bytes: same results, token by token."""
+    x = inputs(4, 1, 2, 2, 70, 64, 64, F32, F32)
+    y, _ = delta(x["q"], x["k"], x["v"], x["log_alpha"], x["beta"], 0.125, x["state"])
+    g = to_gpu(x, F32, F32)
+    wide = lambda t: torch.nn.functional.pad(t, (1, 3))[..., 1:-3]
+    got, _, _ = ws.gl_delta_fwd(wide(g["q"]), wide(g["k"]), g["v"], g["log_alpha"], g["beta"], state=g["state"])
+    assert rel(got, y) <= TOL[F32]

@@ -108,6 +108,7 @@ constexpr int kFrag = 512;                       // bf16 per fragment
 constexpr int kYf = 12 * kFrag;                  // per record
 constexpr int kGates = 9 * 64;
 constexpr int kPiece = 256;                      // bf16 per piece
+constexpr int kY32 = 10 * 256;                   // fp32 per record
 struct ChunkArgs {
   DeltaArgs a;
   uint16_t* yf = nullptr;
@@ -121,6 +122,8 @@ struct ChunkArgs {
   float* st = nullptr;
   float* zf = nullptr;
   float* bf = nullptr;
+  float* y32 = nullptr;  // fp32 chunks: Y and P by blocks of 16, [10][256] each
+  float* p32 = nullptr;
   uint16_t* lf = nullptr;
   uint16_t* gf = nullptr;
   int64_t slots = 0;    // chunk slots of the call
@@ -132,6 +135,9 @@ bool delta_rows_ok(const Str3& s, int d);         // strides of the other row te
 hipError_t launch_delta_prep(const ChunkArgs& c, hipStream_t s);
 hipError_t launch_delta_chunk_fwd(const ChunkArgs& c, hipStream_t s);
 hipError_t launch_delta_chunk_bwd(const ChunkArgs& c, hipStream_t s);
+// The forward in fp32 without anything saved (dk and dv multiples of 4).
+bool delta_chunk_f32_ok(int io, const DeltaArgs& a);  // sizes and strides
+hipError_t launch_delta_chunk_f32(const ChunkArgs& c, hipStream_t s);
 
 // Norms of queries and keys with the rotation.
 struct QkArgs {

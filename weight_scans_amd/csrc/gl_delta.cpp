@@ -57,6 +57,7 @@ struct Plan {
   int64_t N = 0, tok = 0;
   bool packed = false;
   bool chunk = false;                   // the chunked matrix-core path
+  bool chunk32 = false;                 // its fp32 form, for a forward that saves nothing
   int64_t slots = 0;                    // its chunk slots
   size_t saved = 0, fwd_ws = 0, bwd_ws = 0;  // bwd_ws: with `saved` given
   size_t state_bytes = 0, err_bytes = 0, gate_bytes = 0, y_bytes = 0, last_bytes = 0, z_bytes = 0;
@@ -82,6 +83,12 @@ gls::DeltaArgs base_args(const gl_delta_desc_t* d, const Plan& p) {
   a.sdg = dense(d->sdg, d->H, d->T, 1);
   return a;
 }
+
+// Sequences shorter than this (packed: their mean) go token by token, one
+// launch for two.  Forward at 1 x 16 heads of 128, bf16, token by token against
+// chunks: 8 tokens 11 / 16 us, 16 tokens 14 / 16, 32 tokens 20 / 16; backward 28
+// / 22, 41 / 21, 70 / 21.
+constexpr int64_t kChunkFrom = 16;
 
 gl_status_t make_plan(const gl_delta_desc_t* d, Plan* p) {
   if (!d) return fail(GL_ERROR_INVALID_VALUE, "desc is NULL");
@@ -117,7 +124,8 @@ gl_status_t make_plan(const gl_delta_desc_t* d, Plan* p) {
   p->align = p->elem;
   const size_t dd = static_cast<size_t>(d->dk) * d->dv;
   const gls::DeltaArgs a = base_args(d, *p);
-  if (!(d->flags & GL_FLAG_GENERIC) && gls::delta_chunk_ok(p->io, a)) {
+  const bool chunks = !(d->flags & GL_FLAG_GENERIC) && d->T >= kChunkFrom * (p->packed ? p->N : 1);
+  if (chunks && gls::delta_chunk_ok(p->io, a)) {
     p->chunk = true;
     p->align = 16;
     p->name = d->dk <= 64 ? (d->dv <= 64 ? "delta-mfma-bf16-64x64" : "delta-mfma-bf16-64x128")
@@ -142,6 +150,15 @@ gl_status_t make_plan(const gl_delta_desc_t* d, Plan* p) {
   p->name = p->io == GL_DTYPE_F64 ? "delta-serial-f64" : p->io == GL_DTYPE_F32 ? "delta-serial-f32" : "delta-serial-bf16";
   if (d->segments > 1) return fail(GL_ERROR_NOT_SUPPORTED, "segments apply to the matrix-core kernels only");
   p->saved = round_up(static_cast<size_t>(gls::chunk_slots(p->packed, p->N, d->T, ck)) * d->H * dd * p->comp);
+  if (chunks && gls::delta_chunk_f32_ok(p->io, a)) {
+    p->slots = gls::chunk_slots(p->packed, p->N, d->T, gls::kDeltaChunk);
+    const size_t rec = static_cast<size_t>(p->slots) * d->H;
+    if (double(p->slots) * double(d->H) <= 2147483647.0) {
+      p->chunk32 = true;
+      p->name = d->dk <= 64 ? "delta-mfma-f32-64" : "delta-mfma-f32-128";
+      p->gate_bytes = 2 * round_up(rec * gls::kY32 * 4) + round_up(rec * gls::kGates * 4);
+    }
+  }
   const size_t tiles = (d->dv + gls::kSerialRows - 1) / gls::kSerialRows;
   p->bwd_ws = 2 * round_up(tiles * d->H * p->tok * d->dk * p->comp) + 2 * round_up(tiles * d->H * p->tok * p->comp);
   return GL_SUCCESS;
@@ -248,6 +265,16 @@ gl_status_t gl_delta_fwd(const gl_delta_desc_t* desc, const void* q, const void*
     if (p.tok > 0 && !gls::delta_rows_ok(a.sy, a.dv))
       return fail(GL_ERROR_NOT_SUPPORTED, "strides of y: multiples of 8, rows apart");
     return chunk_fwd(chunk_args(a, p, saved, ws), static_cast<hipStream_t>(stream));
+  }
+  if (p.chunk32 && !saved && !(misaligned(q) || misaligned(k) || misaligned(y))) {
+    gls::ChunkArgs c;
+    c.a = a;
+    c.slots = p.slots;
+    Cut w{static_cast<char*>(ws)};
+    w.take(c.y32, static_cast<size_t>(p.slots) * a.H * gls::kY32 * 4);
+    w.take(c.p32, static_cast<size_t>(p.slots) * a.H * gls::kY32 * 4);
+    c.gates = reinterpret_cast<float*>(w.at);
+    return hip_status(gls::launch_delta_chunk_f32(c, static_cast<hipStream_t>(stream)), "delta forward launch");
   }
   return hip_status(gls::launch_delta_serial_fwd(p.io, a, static_cast<hipStream_t>(stream)), "delta forward launch");
 }

@@ -26,7 +26,7 @@
 // rounded states and e, as the sum of the flows past token t, has no long sum,
 // but the rounding of each flow left errors of up to 7e-3.)  dbeta = G.e is
 // formed there too, from the fp32 G.
-#include "delta_mfma.hpp"
+#include "delta_solve.hpp"
 #include "dev_common.hpp"
 
 namespace gls {
@@ -466,24 +466,9 @@ delta_chunk_grad(ChunkArgs ca) {
   const int w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int hk = static_cast<int>(blockIdx.x % a.Hk), grp = SHARED ? a.H / a.Hk : 1;
   const int64_t slot = blockIdx.x / a.Hk;
-  int64_t n, c;
-  if (a.cu) {
-    int64_t lo = 0, hi = a.N - 1;
-    while (lo < hi) {
-      const int64_t m = (lo + hi + 1) / 2;
-      if (chunk_slot0(true, m, seq_range(a.cu, m, a.T).t0, a.T, kDeltaChunk) <= slot) lo = m;
-      else hi = m - 1;
-    }
-    n = lo;
-    c = slot - chunk_slot0(true, n, seq_range(a.cu, n, a.T).t0, a.T, kDeltaChunk);
-  } else {
-    const uint32_t nc = static_cast<uint32_t>((a.T + kDeltaChunk - 1) / kDeltaChunk);
-    n = static_cast<uint32_t>(slot) / nc;
-    c = static_cast<uint32_t>(slot) % nc;
-  }
-  const SeqRange sr = seq_range(a.cu, n, a.T);
-  const int64_t t0 = c * kDeltaChunk;
-  if (c < 0 || t0 >= sr.len) return;
+  SeqRange sr;
+  int64_t t0;
+  if (!chunk_of_slot(a, slot, sr, t0)) return;
   const int nt = static_cast<int>(sr.len - t0 < 64 ? sr.len - t0 : 64);
   const int n_rt = delta_row_tiles(a.dv), nr = n_rt / 2;
   const int kb0 = 2 * (w % NP), tb0 = NT * (w / NP);
