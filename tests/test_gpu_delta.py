@@ -286,9 +286,9 @@ def test_empty():
     (96, 80, 130, None), (4, 4, 70, None), (64, 64, 264, [1, 63, 0, 65, 130, 5]), (128, 44, 200, [0, 200])])
 @pytest.mark.parametrize("order", ["bhtd", "bthd"])
 def test_fp32_chunks(dk, dv, T, lens, order):
-    """A forward in fp32 that saves nothing runs on the matrix cores."""
+    """A forward in fp32 that saves nothing runs on the matrix cores from 16 tokens on."""
     d = ws.make_delta_desc(1, T, 4, 2, dk, dv, ws.GL_DTYPE_F32, ws.GL_DTYPE_F32)
-    assert ws.delta_path_name(d).startswith("delta-mfma-f32")
+    assert ws.delta_path_name(d).startswith("delta-mfma-f32" if T >= 16 else "delta-serial-f32")
     run_case(dk + T, 1 if lens else 2, 4, 2, T, dk, dv, F32, lens=lens, order=order, saved=False)
 
 
@@ -311,3 +311,21 @@ def test_fp32_unaligned_views_take_the_serial_kernel():
     wide = lambda t: torch.nn.functional.pad(t, (1, 3))[..., 1:-3]
     got, _, _ = ws.gl_delta_fwd(wide(g["q"]), wide(g["k"]), g["v"], g["log_alpha"], g["beta"], state=g["state"])
     assert rel(got, y) <= TOL[F32]
+
+
+@pytest.mark.parametrize("dk,dv", [(64, 64), (128, 128), (24, 72), (128, 40), (72, 128)])
+@pytest.mark.parametrize("segments,T,lens", [(2, 129, None), (3, 400, None), (5, 64 * 5, None), (7, 64 * 11 + 1, None),
+                                             (4, 700, [1, 0, 500, 64, 135]), (100, 300, None)])
+def test_segments(dk, dv, segments, T, lens):
+    """The chunks of a sequence cut into segments that run at once."""
+    run_case(dk + T, 1, 2, 1, T, dk, dv, BF16, lens=lens, order="bthd", segments=segments, decay="near1")
+
+
+def test_segments_chosen_for_few_heads_and_long_sequences():
+    """One head of 2,600 tokens is cut by itself; results as for one segment."""
+    g, y, end, _ = run_case(11, 1, 1, 1, 2600, 64, 64, BF16, saved=False)
+    one, end1, _ = ws.gl_delta_fwd(g["q"], g["k"], g["v"], g["log_alpha"], g["beta"], state=g["state"],
+                                   want_state=True, segments=1)
+    assert rel(y, one.double().cpu()) <= TOL[BF16] and rel(end, end1.double().cpu()) <= STATE_TOL[BF16]
+    again = ws.gl_delta_fwd(g["q"], g["k"], g["v"], g["log_alpha"], g["beta"], state=g["state"], want_state=True)
+    assert torch.equal(again[0], y) and torch.equal(again[1], end)

@@ -59,6 +59,8 @@ struct Plan {
   bool chunk = false;                   // the chunked matrix-core path
   bool chunk32 = false;                 // its fp32 form, for a forward that saves nothing
   int64_t slots = 0;                    // its chunk slots
+  int n_seg = 1;                        // segments per sequence of the bf16 forward
+  size_t seg_bytes = 0;                 // their first states, then their M
   size_t saved = 0, fwd_ws = 0, bwd_ws = 0;  // bwd_ws: with `saved` given
   size_t state_bytes = 0, err_bytes = 0, gate_bytes = 0, y_bytes = 0, last_bytes = 0, z_bytes = 0;
   const char* name = "";
@@ -89,6 +91,20 @@ gls::DeltaArgs base_args(const gl_delta_desc_t* d, const Plan& p) {
 // chunks: 8 tokens 11 / 16 us, 16 tokens 14 / 16, 32 tokens 20 / 16; backward 28
 // / 22, 41 / 21, 70 / 21.
 constexpr int64_t kChunkFrom = 16;
+
+// Segments of the chunked bf16 forward.  n of them take two passes of 1 / n of the
+// chunks each plus some 2 us a segment to join them, and need n times the
+// work-groups, of which one fits a CU.
+int segments_of(const gl_delta_desc_t* d, const Plan& p) {
+  const int64_t chunks = std::max<int64_t>(1, d->T / (std::max<int64_t>(p.N, 1) * gls::kDeltaChunk));
+  const int64_t heads = std::max<int64_t>(1, p.N * d->H), groups = heads * ((d->dv + 31) / 32);
+  if (d->segments > 0)
+    return static_cast<int>(std::max<int64_t>(
+        1, std::min<int64_t>({static_cast<int64_t>(d->segments), chunks, 1024, (1 << 28) / heads})));
+  const int64_t n = std::min<int64_t>(
+      {256 / groups, static_cast<int64_t>(std::sqrt(1.5 * static_cast<double>(chunks))), chunks / 8});
+  return n >= 3 ? static_cast<int>(n) : 1;
+}
 
 gl_status_t make_plan(const gl_delta_desc_t* d, Plan* p) {
   if (!d) return fail(GL_ERROR_INVALID_VALUE, "desc is NULL");
@@ -134,7 +150,10 @@ gl_status_t make_plan(const gl_delta_desc_t* d, Plan* p) {
     if (double(p->slots) * double(d->H) > 2147483647.0)
       return fail(GL_ERROR_NOT_SUPPORTED, "chunks above the launch limits");
     const size_t rec = static_cast<size_t>(p->slots) * d->H;
-    p->fwd_ws = 2 * round_up(rec * gls::kYf * 2);
+    p->n_seg = segments_of(d, *p);
+    const size_t segs = p->n_seg > 1 ? static_cast<size_t>(p->N) * d->H * p->n_seg : 0;
+    p->seg_bytes = round_up(segs * dd * 4);
+    p->fwd_ws = 2 * round_up(rec * gls::kYf * 2) + p->seg_bytes + round_up(segs * d->dk * d->dk * 4);
     p->state_bytes = round_up(rec * gls::delta_row_tiles(a.dv) * (gls::delta_wide(a.dk) / 16) * gls::kPiece * 2);
     p->err_bytes = round_up(rec * 4 * gls::delta_row_tiles(a.dv) * gls::kPiece * 2);
     p->gate_bytes = round_up(rec * gls::kGates * 4);
@@ -148,7 +167,6 @@ gl_status_t make_plan(const gl_delta_desc_t* d, Plan* p) {
   }
   const int ck = gls::serial_ck(p->io);
   p->name = p->io == GL_DTYPE_F64 ? "delta-serial-f64" : p->io == GL_DTYPE_F32 ? "delta-serial-f32" : "delta-serial-bf16";
-  if (d->segments > 1) return fail(GL_ERROR_NOT_SUPPORTED, "segments apply to the matrix-core kernels only");
   p->saved = round_up(static_cast<size_t>(gls::chunk_slots(p->packed, p->N, d->T, ck)) * d->H * dd * p->comp);
   if (chunks && gls::delta_chunk_f32_ok(p->io, a)) {
     p->slots = gls::chunk_slots(p->packed, p->N, d->T, gls::kDeltaChunk);
@@ -190,6 +208,9 @@ gls::ChunkArgs chunk_args(const gls::DeltaArgs& a, const Plan& p, void* saved, v
   if (ws) {
     w.take(c.yf, rec * gls::kYf * 2);
     w.take(c.pf, rec * gls::kYf * 2);
+    c.n_seg = p.n_seg;
+    w.take(c.seg_s, p.seg_bytes);
+    w.take(c.seg_m, p.n_seg > 1 ? static_cast<size_t>(p.N) * a.H * p.n_seg * a.dk * a.dk * 4 : 0);
   }
   if (saved) {
     Cut s{static_cast<char*>(saved)};

@@ -14,43 +14,71 @@
 // chunk before through LDS and form y one chunk behind, so that y is off the
 // chain) and two waves that keep the direct loads of the next two chunks in
 // flight: one barrier per chunk.
+//
+// Few heads and many chunks: the chunks of a sequence are cut into n_seg
+// segments that run at once.  What a segment does to the state is
+//   S_end = S_begin M + Z
+// row by row; a first pass (STATES: no outputs) gets Z as the end of the
+// segment from S = 0 and M as its end from S = I without values, delta_join
+// forms the segments' first states one after another, and the pass over the
+// tokens then starts every segment from its own.
 #include "delta_mfma.hpp"
 #include "dev_common.hpp"
 
 namespace gls {
 namespace {
 
-template <int DK, int NW>
+enum { OUTPUTS, TRAINING, STATES };  // y; y and what the backward needs; M and Z of segments
+
+template <int DK, int NW, int MODE>
 struct FwdLds {
-  static constexpr int NS = DK / 32, VW = 16 * NW;
+  static constexpr int NS = DK / 32, VW = 16 * NW, OUT = MODE != STATES;
   alignas(16) char k[3][64 * DK * 2];
-  alignas(16) char q[3][64 * DK * 2];
+  alignas(16) char q[OUT ? 3 : 1][OUT ? 64 * DK * 2 : 16];
   alignas(16) char v[3][64 * VW * 2];
   alignas(16) float gt[3][192];
-  alignas(16) uint16_t sx[2][NW][2 * NS * kFrag];  // hi, then lo
-  alignas(16) uint16_t ux[2][NW][4 * kFrag];
+  alignas(16) uint16_t sx[2][NW][OUT ? 2 * NS * kFrag : 8];  // hi, then lo
+  alignas(16) uint16_t ux[2][NW][OUT ? 4 * kFrag : 8];
 };
+template <int NW, int MODE>
+constexpr int kFwdThreads = 64 * (MODE == STATES ? NW + 1 : 2 * NW + 2);
 
-template <int DK, int NW, bool SAVE>
-__global__ __launch_bounds__(64 * (2 * NW + 2)) void delta_chunk_fwd(ChunkArgs ca) {
+template <int DK, int NW, int MODE>
+__global__ __launch_bounds__((kFwdThreads<NW, MODE>)) void delta_chunk_fwd(ChunkArgs ca) {
   const DeltaArgs& a = ca.a;
-  constexpr int NS = DK / 32, NB = DK / 16, VW = 16 * NW;
-  __shared__ FwdLds<DK, NW> lds;
+  constexpr bool SAVE = MODE == TRAINING, OUT = MODE != STATES;
+  constexpr int NS = DK / 32, NB = DK / 16, VW = 16 * NW, LOADER = OUT ? 2 * NW : NW;
+  __shared__ FwdLds<DK, NW, MODE> lds;
   const int lane = threadIdx.x & 63, l = lane & 15, g = lane >> 4;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const int tiles = (a.dv + VW - 1) / VW;
+  const int ztiles = (a.dv + VW - 1) / VW, tiles = ztiles + (OUT ? 0 : (a.dk + VW - 1) / VW);
+  const int runs = OUT ? ca.n_seg : ca.n_seg - 1;  // segments of this pass
   int64_t head;
   int tile;
-  if (!head_of_block(blockIdx.x, tiles, a.N * a.H, head, tile)) return;
+  if (!head_of_block(blockIdx.x, tiles, a.N * a.H * runs, head, tile)) return;
+  const int seg = static_cast<int>(static_cast<uint32_t>(head) % static_cast<uint32_t>(runs));
+  head = static_cast<uint32_t>(head) / static_cast<uint32_t>(runs);
+  const bool ident = !OUT && tile >= ztiles;  // rows of M, not of Z
+  if (ident) {
+    if (seg == 0) return;  // its first state is known: Z is its end from there
+    tile -= ztiles;
+  }
   const int h = static_cast<int>(head % a.H);
   const int64_t n = head / a.H;
   const int hk = h / (a.H / a.Hk), r0 = tile * VW;
-  const SeqRange sr = seq_range(a.cu, n, a.T);
-  const int nc = static_cast<int>((sr.len + kDeltaChunk - 1) / kDeltaChunk);
-  const int64_t slot0 = chunk_slot0(a.cu != nullptr, n, sr.t0, a.T, kDeltaChunk);
+  SeqRange sr = seq_range(a.cu, n, a.T);
+  int nc = static_cast<int>((sr.len + kDeltaChunk - 1) / kDeltaChunk);
+  int64_t slot0 = chunk_slot0(a.cu != nullptr, n, sr.t0, a.T, kDeltaChunk);
+  if (ca.n_seg > 1) {
+    const int per = (nc + ca.n_seg - 1) / ca.n_seg, c0 = static_cast<int>(min(static_cast<int64_t>(seg) * per, static_cast<int64_t>(nc)));
+    nc = min(per, nc - c0);
+    slot0 += c0;
+    sr.t0 += c0 * static_cast<int64_t>(kDeltaChunk);
+    sr.len = min(sr.len - c0 * static_cast<int64_t>(kDeltaChunk), nc * static_cast<int64_t>(kDeltaChunk));
+  }
   const int64_t rec0 = slot0 * a.H + h;
 
-  if (wave == 2 * NW) {  // ---- loads: K, V and gates, two chunks ahead
+  if (wave == LOADER) {  // ---- loads: K, V and gates, two chunks ahead
     constexpr int NK = DK / 8, NV = VW / 8, PER = NK + NV + 3;
     const uint16_t* kp = static_cast<const uint16_t*>(a.k) + sr.b * a.sk.b + hk * a.sk.h + sr.t0 * a.sk.t;
     const uint16_t* vp = static_cast<const uint16_t*>(a.v) + sr.b * a.sv.b + h * a.sv.h + sr.t0 * a.sv.t + r0;
@@ -63,7 +91,7 @@ __global__ __launch_bounds__(64 * (2 * NW + 2)) void delta_chunk_fwd(ChunkArgs c
       const bool in = c < nc;
       const int s = c % 3;
       const __amdgpu_buffer_rsrc_t rk = rows_rsrc(kp, c * 64LL, in ? sr.len : 0, a.sk.t, a.dk);
-      const __amdgpu_buffer_rsrc_t rv = rows_rsrc(vp, c * 64LL, in ? sr.len : 0, a.sv.t, min(VW, a.dv - r0));
+      const __amdgpu_buffer_rsrc_t rv = rows_rsrc(vp, c * 64LL, in && !ident ? sr.len : 0, a.sv.t, min(VW, a.dv - r0));
       const __amdgpu_buffer_rsrc_t rg =
           buffer_rsrc(ca.gates + (in ? (rec0 + static_cast<int64_t>(c) * a.H) * kGates : 0), in ? 768 : 0);
 #pragma unroll
@@ -83,7 +111,7 @@ __global__ __launch_bounds__(64 * (2 * NW + 2)) void delta_chunk_fwd(ChunkArgs c
     wait_vm<0>();
     return;
   }
-  if (wave == 2 * NW + 1) {  // ---- loads: Q, used one step later
+  if (OUT && wave == LOADER + 1) {  // ---- loads: Q, used one step later
     constexpr int NK = DK / 8;
     const uint16_t* qp = static_cast<const uint16_t*>(a.q) + sr.b * a.sq.b + hk * a.sq.h + sr.t0 * a.sq.t;
     uint32_t qo[NK];
@@ -107,7 +135,7 @@ __global__ __launch_bounds__(64 * (2 * NW + 2)) void delta_chunk_fwd(ChunkArgs c
   }
 
   const TileLane<DK> tk = tile_lane<DK>(lane);
-  if (wave >= NW) {  // ---- outputs, one chunk behind
+  if (OUT && wave >= NW) {  // ---- outputs, one chunk behind
     const int w = wave - NW;
     const int rr = r0 + index4(w, g);
     uint16_t* yp = static_cast<uint16_t*>(a.y) + sr.b * a.sy.b + h * a.sy.h + sr.t0 * a.sy.t + rr;
@@ -187,12 +215,20 @@ __global__ __launch_bounds__(64 * (2 * NW + 2)) void delta_chunk_fwd(ChunkArgs c
   const TileLane<VW> tv = tile_lane<VW>(lane);
   const int r = r0 + index1(wave, l);
   const int64_t so = (head * a.dv + r) * a.dk;
+  // segment states [head][n_seg][dv][dk], M [head][n_seg][dk][dk]
+  const auto seg_at = [&](int s) { return ((head * ca.n_seg + s) * a.dv + r) * a.dk; };
+  const float* from = seg == 0 ? (a.state_in ? static_cast<const float*>(a.state_in) + so : nullptr)
+                      : OUT    ? ca.seg_s + seg_at(seg)
+                               : nullptr;
   f32x4 S[NB];
 #pragma unroll
-  for (int b = 0; b < NB; ++b)
-    S[b] = a.state_in && r < a.dv && index4(b, g) < a.dk
-               ? *reinterpret_cast<const f32x4*>(static_cast<const float*>(a.state_in) + so + index4(b, g))
-               : zero4();
+  for (int b = 0; b < NB; ++b) {
+    const int c = index4(b, g);
+    S[b] = from && r < a.dv && c < a.dk ? *reinterpret_cast<const f32x4*>(from + c) : zero4();
+    if (ident)
+#pragma unroll
+      for (int q = 0; q < 4; ++q) S[b][q] = c + q == r ? 1.f : 0.f;
+  }
   bf16x8 yf[12];
   const uint16_t* yp = ca.yf + rec0 * kYf + lane * 8;
 #pragma unroll
@@ -210,8 +246,8 @@ __global__ __launch_bounds__(64 * (2 * NW + 2)) void delta_chunk_fwd(ChunkArgs c
     const auto gate = [&](int m, int tb) { return *reinterpret_cast<const f32x4*>(gt + 64 * m + 16 * tb); };
     // the next chunk's Y, fetched as this one's is used up
     yp += (c + 1 < nc ? static_cast<int64_t>(a.H) : 0) * kYf;
-    uint16_t* sx = lds.sx[c & 1][wave] + lane * 8;
-    uint16_t* ux = lds.ux[c & 1][wave] + lane * 8;
+    uint16_t* sx = OUT ? lds.sx[c & 1][wave] + lane * 8 : nullptr;
+    uint16_t* ux = OUT ? lds.ux[c & 1][wave] + lane * 8 : nullptr;
     f32x4 E[4], be[4], gm[4], rs[4];
     s16x4 vv[4];
     bf16x8 kf[2][NS], kc[NB];
@@ -271,9 +307,11 @@ __global__ __launch_bounds__(64 * (2 * NW + 2)) void delta_chunk_fwd(ChunkArgs c
       for (int i = 0; i < 2; ++i)
 #pragma unroll
         for (int q = 0; q < 4; ++q) E[2 * half + i][q] *= be[2 * half + i][q];
-      const Pair8 p = split8(E[2 * half], E[2 * half + 1]);
-      *reinterpret_cast<bf16x8*>(ux + half * kFrag) = p.hi;
-      *reinterpret_cast<bf16x8*>(ux + (2 + half) * kFrag) = p.lo;
+      if constexpr (OUT) {
+        const Pair8 p = split8(E[2 * half], E[2 * half + 1]);
+        *reinterpret_cast<bf16x8*>(ux + half * kFrag) = p.hi;
+        *reinterpret_cast<bf16x8*>(ux + (2 + half) * kFrag) = p.lo;
+      }
 #pragma unroll
       for (int i = 0; i < 2; ++i)
 #pragma unroll
@@ -301,10 +339,12 @@ __global__ __launch_bounds__(64 * (2 * NW + 2)) void delta_chunk_fwd(ChunkArgs c
     }
     const float whole = lds.gt[sl][63];
     ks(0);
+    if constexpr (OUT) {
 #pragma unroll
-    for (int s = 0; s < NS; ++s) {  // S of this chunk for the output wave
-      *reinterpret_cast<bf16x8*>(sx + s * kFrag) = sp[s].hi;
-      *reinterpret_cast<bf16x8*>(sx + (NS + s) * kFrag) = sp[s].lo;
+      for (int s = 0; s < NS; ++s) {  // S of this chunk for the output wave
+        *reinterpret_cast<bf16x8*>(sx + s * kFrag) = sp[s].hi;
+        *reinterpret_cast<bf16x8*>(sx + (NS + s) * kFrag) = sp[s].lo;
+      }
     }
 #pragma unroll
     for (int b = 0; b < NB; ++b)
@@ -349,30 +389,112 @@ __global__ __launch_bounds__(64 * (2 * NW + 2)) void delta_chunk_fwd(ChunkArgs c
     }
   }
   lds_barrier();
-  if (r < a.dv) {
+  float* to = OUT ? (seg == ca.n_seg - 1 && a.state_out ? static_cast<float*>(a.state_out) + so : nullptr)
+              : ident ? ca.seg_m + ((head * ca.n_seg + seg) * a.dk + r) * a.dk
+                      : ca.seg_s + seg_at(seg + 1);
+  if (r < (ident ? a.dk : a.dv)) {
 #pragma unroll
     for (int b = 0; b < NB; ++b)
       if (index4(b, g) < a.dk) {
-        if (a.state_out) *reinterpret_cast<f32x4*>(static_cast<float*>(a.state_out) + so + index4(b, g)) = S[b];
-        if constexpr (SAVE) *reinterpret_cast<f32x4*>(ca.st + so + index4(b, g)) = S[b];
+        if (to) *reinterpret_cast<f32x4*>(to + index4(b, g)) = S[b];
+        if (SAVE && seg == ca.n_seg - 1) *reinterpret_cast<f32x4*>(ca.st + so + index4(b, g)) = S[b];
       }
   }
 }
 
-template <int DK, int NW>
+// First states of the segments: S_(s+1) = S_s M_s + Z_s, s = 1 .. n_seg - 2, in
+// fp32; Z_s stands where S_(s+1) goes.  A work-group has 16 rows of a head,
+// which stay in LDS between the segments; wave w forms the column blocks w and
+// w + 4 of 16.
+template <int DK>
+__global__ __launch_bounds__(256) void delta_join(ChunkArgs ca) {
+  const DeltaArgs& a = ca.a;
+  constexpr int NB = DK / 16, P = DK + 4;
+  __shared__ __align__(16) float rows[2][16 * P];
+  const int lane = threadIdx.x & 63, l = lane & 15, g = lane >> 4;
+  const int w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int tiles = (a.dv + 15) / 16;
+  const int64_t head = blockIdx.x / tiles;
+  const int r0 = static_cast<int>(blockIdx.x % tiles) * 16;
+  const int nr = min(16, a.dv - r0);
+  // rows r0.. of S_s, zeros past dv and dk
+  const auto states = [&](int s) {
+    return buffer_rsrc(ca.seg_s + ((head * ca.n_seg + s) * a.dv + r0) * a.dk, nr * a.dk * 4);
+  };
+  const __amdgpu_buffer_rsrc_t r1 = states(1);
+  for (int i = threadIdx.x; i < 16 * DK; i += 256) {
+    const int r = i / DK, c = i % DK;
+    rows[0][r * P + c] = load4(r1, c < a.dk ? static_cast<uint32_t>((r * a.dk + c) * 4) : kPastEnd);
+  }
+  for (int s = 1; s + 1 < ca.n_seg; ++s) {
+    const __amdgpu_buffer_rsrc_t rm = buffer_rsrc(ca.seg_m + (head * ca.n_seg + s) * a.dk * a.dk, a.dk * a.dk * 4);
+    const __amdgpu_buffer_rsrc_t rz = states(s + 1);
+    const float* from = rows[(s + 1) & 1];
+    float* to = rows[s & 1];
+    float m[(NB + 3) / 4][NB][4];
+    f32x4 x[(NB + 3) / 4];
+#pragma unroll
+    for (int i = 0; i < (NB + 3) / 4; ++i) {
+      const int c = 16 * (w + 4 * i) + l;
+      const uint32_t o = c < a.dk ? static_cast<uint32_t>(c * 4) : kPastEnd;
+#pragma unroll
+      for (int kb = 0; kb < NB; ++kb)
+#pragma unroll
+        for (int q = 0; q < 4; ++q) m[i][kb][q] = load4(rm, o + (16 * kb + 4 * g + q) * a.dk * 4);
+#pragma unroll
+      for (int q = 0; q < 4; ++q) x[i][q] = load4(rz, o + (4 * g + q) * a.dk * 4);
+    }
+    lds_barrier();
+#pragma unroll
+    for (int kb = 0; kb < NB; ++kb) {
+      const f32x4 sf = *reinterpret_cast<const f32x4*>(from + l * P + 16 * kb + 4 * g);
+#pragma unroll
+      for (int q = 0; q < 4; ++q)
+#pragma unroll
+        for (int i = 0; i < (NB + 3) / 4; ++i)
+          x[i] = __builtin_amdgcn_mfma_f32_16x16x4f32(sf[q], m[i][kb][q], x[i], 0, 0, 0);
+    }
+#pragma unroll
+    for (int i = 0; i < (NB + 3) / 4; ++i) {
+      const int c = 16 * (w + 4 * i) + l;
+#pragma unroll
+      for (int q = 0; q < 4; ++q) {
+        const int r = 4 * g + q;
+        to[r * P + c] = x[i][q];
+        if (r < nr && c < a.dk) ca.seg_s[((head * ca.n_seg + s + 1) * a.dv + r0 + r) * a.dk + c] = x[i][q];
+      }
+    }
+  }
+}
+
+template <int DK, int NW, int MODE>
 hipError_t launch(const ChunkArgs& c, hipStream_t s) {
-  const int tiles = (c.a.dv + 16 * NW - 1) / (16 * NW);
-  const dim3 grid(static_cast<unsigned>(head_blocks(c.a.N * c.a.H, tiles)));
-  if (c.sf) delta_chunk_fwd<DK, NW, true><<<grid, 64 * (2 * NW + 2), 0, s>>>(c);
-  else delta_chunk_fwd<DK, NW, false><<<grid, 64 * (2 * NW + 2), 0, s>>>(c);
+  constexpr int VW = 16 * NW;
+  const int tiles = (c.a.dv + VW - 1) / VW + (MODE == STATES ? (c.a.dk + VW - 1) / VW : 0);
+  const int64_t runs = c.a.N * c.a.H * (MODE == STATES ? c.n_seg - 1 : c.n_seg);
+  const dim3 grid(static_cast<unsigned>(head_blocks(runs, tiles)));
+  delta_chunk_fwd<DK, NW, MODE><<<grid, kFwdThreads<NW, MODE>, 0, s>>>(c);
   return hipGetLastError();
+}
+
+template <int DK>
+hipError_t launch_all(const ChunkArgs& c, hipStream_t s) {
+  if (c.n_seg > 1) {
+    hipError_t e = launch<DK, 4, STATES>(c, s);
+    if (e != hipSuccess) return e;
+    if (c.n_seg > 2) {
+      delta_join<DK><<<dim3(static_cast<unsigned>(c.a.N * c.a.H * ((c.a.dv + 15) / 16))), 256, 0, s>>>(c);
+      if ((e = hipGetLastError()) != hipSuccess) return e;
+    }
+  }
+  return c.sf ? launch<DK, 2, TRAINING>(c, s) : launch<DK, 2, OUTPUTS>(c, s);
 }
 
 }  // namespace
 
 hipError_t launch_delta_chunk_fwd(const ChunkArgs& c, hipStream_t s) {
   if (c.a.N * c.a.H == 0) return hipSuccess;
-  return c.a.dk <= 64 ? launch<64, 2>(c, s) : launch<128, 2>(c, s);
+  return c.a.dk <= 64 ? launch_all<64>(c, s) : launch_all<128>(c, s);
 }
 
 }  // namespace gls
