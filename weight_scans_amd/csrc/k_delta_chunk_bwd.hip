@@ -462,7 +462,6 @@ delta_chunk_grad(ChunkArgs ca) {
   const DeltaArgs& a = ca.a;
   constexpr int NB = DK / 16, NP = NB / 2, NT = NP, NR = DV / 32;  // NT blocks of 16 tokens a wave
   __shared__ GradLds<DK, DV> lds;
-  const int lane = threadIdx.x & 63, l = lane & 15, g = lane >> 4;
   const int w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int hk = static_cast<int>(blockIdx.x % a.Hk), grp = SHARED ? a.H / a.Hk : 1;
   const int64_t slot = blockIdx.x / a.Hk;
@@ -472,9 +471,6 @@ delta_chunk_grad(ChunkArgs ca) {
   const int nt = static_cast<int>(sr.len - t0 < 64 ? sr.len - t0 : 64);
   const int n_rt = delta_row_tiles(a.dv), nr = n_rt / 2;
   const int kb0 = 2 * (w % NP), tb0 = NT * (w / NP);
-  const TileLane<DK> tk = tile_lane<DK>(lane);
-  const TileLane<DV> to = tile_lane<DV>(lane);
-  const uint32_t ra = raw_turned(lane);
   const float sc = static_cast<float>(a.scale);
   const s16x4 none = {0, 0, 0, 0};
 
@@ -487,6 +483,13 @@ delta_chunk_grad(ChunkArgs ca) {
   for (int gi = 0; gi < grp; ++gi) {
     const int h = hk * grp + gi;
     const int64_t rec = slot * a.H + h;
+    int lane = threadIdx.x & 63;
+    // Anew for each head: addresses kept over the loop cost more registers than there are.
+    if constexpr (SHARED) asm volatile("" : "+v"(lane));
+    const int l = lane & 15, g = lane >> 4;
+    const TileLane<DK> tk = tile_lane<DK>(lane);
+    const TileLane<DV> to = tile_lane<DV>(lane);
+    const uint32_t ra = raw_turned(lane);
     if (gi) __syncthreads();  // the head before is done with the tiles
     {
       const uint16_t* op = static_cast<const uint16_t*>(a.dy) + sr.b * a.sdy.b + h * a.sdy.h + sr.t0 * a.sdy.t;
@@ -711,6 +714,7 @@ delta_chunk_grad(ChunkArgs ca) {
     }
   }
   // blocks kb0 and kb0 + 1 are eight neighbouring columns
+  const int l = threadIdx.x & 15, g = (threadIdx.x & 63) >> 4;
   const int col = index4(kb0, g);
   if (col < a.dk) {
 #pragma unroll
