@@ -19,7 +19,7 @@
  *   log_alpha, beta and gradients   [B][H][T]        gate dtype
  *   states                          [n][H][dv][dk]   dense, fp64 if io is F64, else fp32
  * Pointers are 16-byte aligned; those of gates, and of q, k, v, y and their
- * gradients on the token-serial path and in a step, only to their elements.
+ * gradients except on BF16 io's matrix-core path, only to their elements.
  * Value head h reads query and key head h / (H / Hk); dq and dk sum over the
  * value heads that share them.
  *
@@ -35,15 +35,22 @@
  * dy and states; log_alpha <= 0, minus infinity included (the state is
  * forgotten before that token is written).  With |k_t| <= 1 and 0 <= beta <= 1
  * every factor of the recurrence is a contraction; other keys are taken as
- * they are.
+ * they are.  A value that is not finite reaches every token of its chunk of 64
+ * and all later ones on the matrix-core paths (only later ones token by token).
  *
  * Arithmetic: F32 and F64 io compute in their own type.  BF16 io keeps the
  * states and every accumulator in fp32.  Its matrix-core path carries the
- * recurrence (states in both directions, e_t) through operands split into two
- * bf16 terms (16 significand bits), so that states and their gradients hold
- * about 1e-5, and rounds once to bf16 the operands of products that end in an
- * io-typed output; gradients of the gates hold about 3e-3 there in any gate
- * dtype.
+ * recurrences (states in both directions, e_t) through operands split into two
+ * bf16 terms (16 significand bits): final states and the gradient of the first
+ * hold about 3e-6 (relative 2-norm), as do dlog_alpha's sums before they are
+ * rounded to the gate dtype.  y is rounded once, at the end (1.7e-3).  dq and dk
+ * come from products of two bf16 operands of which one (states, e_t, dv / beta)
+ * was rounded once: 3e-3; dv and dbeta 2.5e-3.
+ *
+ * Kernels: BF16 io with dk and dv multiples of 8 runs in chunks of 64 tokens on
+ * the matrix cores; so does F32 io with dk and dv multiples of 4 in a forward
+ * that saves nothing.  Everything else, and sequences of fewer than 16 tokens
+ * on average, goes token by token on the vector ALU.
  */
 #ifndef GL_DELTA_H
 #define GL_DELTA_H
@@ -66,8 +73,9 @@ typedef struct {
   int32_t io_dtype;    /* gl_dtype_t                                            */
   int32_t gate_dtype;  /* the io dtype, or F32 with BF16 io                     */
   uint32_t flags;      /* GL_FLAG_GENERIC: the token-serial vector kernels      */
-  uint32_t segments;   /* matrix-core forward: 0 = automatic, 1 = one per
-                          sequence, n > 1 = n (at most one per chunk)           */
+  uint32_t segments;   /* BF16 matrix-core forward: parts of a sequence that run
+                          at once; 0 = chosen by the number of heads and chunks,
+                          n = n (at most one per chunk); elsewhere not used     */
   double scale;        /* of y                                                  */
   gl_strides_t sq, sk, sv, sy, sg;      /* q, k, v, y, log_alpha and beta       */
   gl_strides_t sdq, sdk, sdv, sdy, sdg; /* their gradients (gl_delta_bwd)       */

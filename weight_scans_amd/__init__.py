@@ -18,6 +18,14 @@ raises if the library is missing.
     dq, dk, dv, deta, dalpha, dW0 = gl_scan_qkv_bwd(q, k, v, eta, alpha, W0, dy)
     z = transpose_read(u, g, x, eta, alpha, W0)       # (W0 + D_t)^T u_t
 
+The gated delta rule (the fast weight that forms its own costate) and the norms
+of its queries and keys, behind ``include/gl_delta.h`` (see ``delta.py``; a layer
+and a command that run them together: ``gated_delta.py``):
+
+    y, state = delta_rule(q, k, v, log_alpha, beta, want_state=True)   # autograd-aware
+    y1 = gl_delta_step(q1, k1, v1, log_alpha1, beta1, state)           # one token
+    qn, kn = qknorm_rope(q, k, wq, wk, cos, sin)                       # autograd-aware
+
 Shapes: x [B,H,T,d_in], g [B,H,T,d_out], eta/alpha [B,H,T], W0 [H,d_out,d_in];
 one decode token: x1 [B,H,d_in], g1 [B,H,d_out], eta1/alpha1 [B,H];
 state [B,H,d_out,d_in] in the gate dtype.

@@ -364,9 +364,10 @@ gl_status_t gl_delta_step(const gl_delta_desc_t* desc, const void* q, const void
   gl_status_t st = make_plan(desc, &p);
   if (st != GL_SUCCESS) return st;
   if (p.packed) return fail(GL_ERROR_INVALID_VALUE, "a step takes no packed sequences");
-  if (n_slots < 0 || (!slots && n_slots < desc->B))
-    return fail(GL_ERROR_INVALID_VALUE, "%lld states for %lld rows", (long long)n_slots, (long long)desc->B);
+  if (n_slots < 0) return fail(GL_ERROR_INVALID_VALUE, "n_slots is negative");
   if (desc->B * desc->H == 0) return GL_SUCCESS;
+  if (!slots && n_slots < desc->B)
+    return fail(GL_ERROR_INVALID_VALUE, "%lld states for %lld rows", (long long)n_slots, (long long)desc->B);
   if ((st = check_ptrs(true, {q, k, v, y}, p.elem)) != GL_SUCCESS) return st;
   if ((st = check_ptrs(true, {log_alpha, beta}, p.gate)) != GL_SUCCESS) return st;
   if ((st = check_ptrs(n_slots > 0, {state})) != GL_SUCCESS) return st;

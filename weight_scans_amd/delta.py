@@ -461,6 +461,11 @@ def gl_qknorm_rope_bwd(q, k, wq, wk, cos, sin, dqn, dkn, *, pos=None, pos0=0, ep
 
 
 # ---------------------------------------------------------------- autograd
+def _whole(t):
+    """t as it is if it is dense in some order of its heads and tokens, else a copy."""
+    return t if _dense(t) and t.stride(-1) == 1 and t.data_ptr() % 16 == 0 else t.contiguous()
+
+
 def _make_functions():
     torch = _torch()
 
@@ -476,7 +481,7 @@ def _make_functions():
         @staticmethod
         def backward(ctx, dy, dstate):
             q, k, v, log_alpha, beta, state, cu_seqlens, saved = ctx.saved_tensors
-            grads = gl_delta_bwd(q, k, v, log_alpha, beta, dy.contiguous(), saved, scale=ctx.scale, state=state,
+            grads = gl_delta_bwd(q, k, v, log_alpha, beta, _whole(dy), saved, scale=ctx.scale, state=state,
                                  dstate=None if dstate is None else dstate.contiguous(), cu_seqlens=cu_seqlens)
             return (*grads, None, None, None)
 
@@ -490,8 +495,8 @@ def _make_functions():
         @staticmethod
         def backward(ctx, dqn, dkn):
             q, k, wq, wk, cos, sin, pos = ctx.saved_tensors
-            dq, dk, dwq, dwk = gl_qknorm_rope_bwd(q, k, wq, wk, cos, sin, dqn.contiguous(), dkn.contiguous(),
-                                                  pos=pos, **ctx.opts)
+            dq, dk, dwq, dwk = gl_qknorm_rope_bwd(q, k, wq, wk, cos, sin, _whole(dqn), _whole(dkn), pos=pos,
+                                                  **ctx.opts)
             dwq, dwk = (None if g is None else g.to(w.dtype) for g, w in ((dwq, wq), (dwk, wk)))
             return dq, dk, dwq, dwk, None, None, None, None
 
@@ -509,7 +514,12 @@ def _functions():
 
 
 def delta_rule(q, k, v, log_alpha, beta, *, scale=None, state=None, cu_seqlens=None, want_state=False):
-    """Autograd-aware gl_delta_fwd: (y, final state or None)."""
+    """Autograd-aware gl_delta_fwd: (y, final state or None).  Nothing is kept
+    for a backward where no gradient is wanted."""
+    inputs = (q, k, v, log_alpha, beta, state)
+    if not (_torch().is_grad_enabled() and any(t is not None and t.requires_grad for t in inputs)):
+        return gl_delta_fwd(q, k, v, log_alpha, beta, scale=scale, state=state, want_state=want_state,
+                            cu_seqlens=cu_seqlens)[:2]
     return _functions()[0].apply(q, k, v, log_alpha, beta, state, scale, cu_seqlens, want_state)
 
 
