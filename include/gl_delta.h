@@ -19,7 +19,8 @@
  *   log_alpha, beta and gradients   [B][H][T]        gate dtype
  *   states                          [n][H][dv][dk]   dense, fp64 if io is F64, else fp32
  * Pointers are 16-byte aligned; those of gates, and of q, k, v, y and their
- * gradients except on BF16 io's matrix-core path, only to their elements.
+ * gradients off the matrix-core paths, only to their elements (an F32 forward
+ * that saves nothing takes the other path by itself where they are not).
  * Value head h reads query and key head h / (H / Hk); dq and dk sum over the
  * value heads that share them.
  *
@@ -42,15 +43,15 @@
  * states and every accumulator in fp32.  Its matrix-core path carries the
  * recurrences (states in both directions, e_t) through operands split into two
  * bf16 terms (16 significand bits): final states and the gradient of the first
- * hold about 3e-6 (relative 2-norm), as do dlog_alpha's sums before they are
- * rounded to the gate dtype.  y is rounded once, at the end (1.7e-3).  dq and dk
+ * hold about 3e-6 (relative 2-norm), dlog_alpha 1e-5 before it is rounded to the
+ * gate dtype.  y is rounded once, at the end (1.7e-3).  dq and dk
  * come from products of two bf16 operands of which one (states, e_t, dv / beta)
  * was rounded once: 3e-3; dv and dbeta 2.5e-3.
  *
- * Kernels: BF16 io with dk and dv multiples of 8 runs in chunks of 64 tokens on
- * the matrix cores; so does F32 io with dk and dv multiples of 4 in a forward
- * that saves nothing.  Everything else, and sequences of fewer than 16 tokens
- * on average, goes token by token on the vector ALU.
+ * Kernels: BF16 io with dk and dv multiples of 8, and F32 io with multiples of
+ * 4, run in chunks of 64 tokens on the matrix cores.  Everything else, and
+ * sequences of fewer than 16 tokens on average, goes token by token on the
+ * vector ALU.
  */
 #ifndef GL_DELTA_H
 #define GL_DELTA_H

@@ -286,7 +286,7 @@ def test_empty():
     (96, 80, 130, None), (4, 4, 70, None), (64, 64, 264, [1, 63, 0, 65, 130, 5]), (128, 44, 200, [0, 200])])
 @pytest.mark.parametrize("order", ["bhtd", "bthd"])
 def test_fp32_chunks(dk, dv, T, lens, order):
-    """A forward in fp32 that saves nothing runs on the matrix cores from 16 tokens on."""
+    """fp32 runs on the matrix cores from 16 tokens on; here a forward that saves nothing."""
     d = ws.make_delta_desc(1, T, 4, 2, dk, dv, ws.GL_DTYPE_F32, ws.GL_DTYPE_F32)
     assert ws.delta_path_name(d).startswith("delta-mfma-f32" if T >= 16 else "delta-serial-f32")
     run_case(dk + T, 1 if lens else 2, 4, 2, T, dk, dv, F32, lens=lens, order=order, saved=False)
@@ -329,3 +329,23 @@ def test_segments_chosen_for_few_heads_and_long_sequences():
     assert rel(y, one.double().cpu()) <= TOL[BF16] and rel(end, end1.double().cpu()) <= STATE_TOL[BF16]
     again = ws.gl_delta_fwd(g["q"], g["k"], g["v"], g["log_alpha"], g["beta"], state=g["state"], want_state=True)
     assert torch.equal(again[0], y) and torch.equal(again[1], end)
+
+
+@pytest.mark.parametrize("dk,dv,T,lens", [
+    (64, 64, 64, None), (64, 64, 65, None), (20, 36, 200, None), (128, 128, 257, None), (96, 80, 130, None),
+    (4, 4, 70, None), (64, 64, 264, [1, 63, 0, 65, 130, 5]), (128, 44, 200, [0, 200]), (128, 128, 700, None)])
+@pytest.mark.parametrize("H,Hk,decay", [(4, 2, "mix"), (3, 3, "near1"), (3, 1, "base")])
+def test_fp32_training_chunks(dk, dv, T, lens, H, Hk, decay):
+    run_case(dk + T + H, 1 if lens else 2, H, Hk, T, dk, dv, F32, lens=lens, order="bthd", decay=decay)
+
+
+@pytest.mark.parametrize("dtype", [F32, F64])
+def test_serial_training(dtype):
+    run_case(9, 1, 4, 2, 100, 64, 72, dtype, flags=ws.GL_FLAG_GENERIC)
+    run_case(10, 1, 2, 2, 100, 128, 30, dtype, lens=[0, 17, 70, 13])
+
+
+def test_fp32_long_sequence_gradients():
+    """The decay's gradient is a sum over what follows: no error may grow along it."""
+    run_case(12, 1, 1, 1, 3000, 16, 16, F32, decay="near1")
+    run_case(13, 1, 1, 1, 3000, 16, 16, BF16, gate=F32, decay="near1")

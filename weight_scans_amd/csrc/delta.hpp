@@ -122,8 +122,18 @@ struct ChunkArgs {
   float* st = nullptr;
   float* zf = nullptr;
   float* bf = nullptr;
-  float* y32 = nullptr;  // fp32 chunks: Y and P by blocks of 16, [10][256] each
+  // fp32 chunks: Y and P by blocks of 16, [10][256] each, rows i in lanes, and
+  // (training) rows j; the states before and the adjoints after the chunks by
+  // blocks [row tile][dk / 16][256], row index 4g + q, column l in lanes; e, y
+  // (yb) and dL/d(beta e), [64][16 row tiles] each
+  float* y32 = nullptr;
   float* p32 = nullptr;
+  float* yt32 = nullptr;
+  float* pt32 = nullptr;
+  float* s32 = nullptr;
+  float* l32 = nullptr;
+  float* e32 = nullptr;
+  float* g32 = nullptr;
   uint16_t* lf = nullptr;
   uint16_t* gf = nullptr;
   int64_t slots = 0;    // chunk slots of the call
@@ -138,9 +148,11 @@ bool delta_rows_ok(const Str3& s, int d);         // strides of the other row te
 hipError_t launch_delta_prep(const ChunkArgs& c, hipStream_t s);
 hipError_t launch_delta_chunk_fwd(const ChunkArgs& c, hipStream_t s);
 hipError_t launch_delta_chunk_bwd(const ChunkArgs& c, hipStream_t s);
-// The forward in fp32 without anything saved (dk and dv multiples of 4).
-bool delta_chunk_f32_ok(int io, const DeltaArgs& a);  // sizes and strides
+// The same in fp32 (dk and dv multiples of 4).
+bool delta_chunk_f32_ok(int io, const DeltaArgs& a);  // sizes and strides of q, k, v
+bool delta_rows_f32_ok(const Str3& s, int d);         // strides of the other row tensors
 hipError_t launch_delta_chunk_f32(const ChunkArgs& c, hipStream_t s);
+hipError_t launch_delta_chunk_f32_bwd(const ChunkArgs& c, hipStream_t s);
 
 // Norms of queries and keys with the rotation.
 struct QkArgs {

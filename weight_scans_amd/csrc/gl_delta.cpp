@@ -57,7 +57,7 @@ struct Plan {
   int64_t N = 0, tok = 0;
   bool packed = false;
   bool chunk = false;                   // the chunked matrix-core path
-  bool chunk32 = false;                 // its fp32 form, for a forward that saves nothing
+  bool chunk32 = false;                 // its fp32 form
   int64_t slots = 0;                    // its chunk slots
   int n_seg = 1;                        // segments per sequence of the bf16 forward
   size_t seg_bytes = 0;                 // their first states, then their M
@@ -165,18 +165,26 @@ gl_status_t make_plan(const gl_delta_desc_t* d, Plan* p) {
     p->bwd_ws = p->state_bytes + p->err_bytes + 2 * p->z_bytes;
     return GL_SUCCESS;
   }
+  if (chunks && gls::delta_chunk_f32_ok(p->io, a)) {
+    p->chunk32 = true;
+    p->name = d->dk <= 64 ? "delta-mfma-f32-64" : "delta-mfma-f32-128";
+    p->slots = gls::chunk_slots(p->packed, p->N, d->T, gls::kDeltaChunk);
+    if (double(p->slots) * double(d->H) > 2147483647.0)
+      return fail(GL_ERROR_NOT_SUPPORTED, "chunks above the launch limits");
+    const size_t rec = static_cast<size_t>(p->slots) * d->H, tiles = gls::delta_row_tiles(a.dv);
+    p->gate_bytes = round_up(rec * gls::kGates * 4);
+    p->fwd_ws = 2 * round_up(rec * gls::kY32 * 4);
+    p->state_bytes = round_up(rec * tiles * gls::delta_wide(a.dk) * 16 * 4);
+    p->y_bytes = p->err_bytes = round_up(rec * tiles * 64 * 16 * 4);
+    p->z_bytes = round_up(rec * tiles * 64 * 4);
+    p->last_bytes = round_up(static_cast<size_t>(p->N) * d->H * dd * 4);
+    p->saved = p->gate_bytes + p->fwd_ws + p->state_bytes + p->err_bytes + p->y_bytes + p->last_bytes;
+    p->bwd_ws = p->state_bytes + p->err_bytes + 2 * p->z_bytes;
+    return GL_SUCCESS;
+  }
   const int ck = gls::serial_ck(p->io);
   p->name = p->io == GL_DTYPE_F64 ? "delta-serial-f64" : p->io == GL_DTYPE_F32 ? "delta-serial-f32" : "delta-serial-bf16";
   p->saved = round_up(static_cast<size_t>(gls::chunk_slots(p->packed, p->N, d->T, ck)) * d->H * dd * p->comp);
-  if (chunks && gls::delta_chunk_f32_ok(p->io, a)) {
-    p->slots = gls::chunk_slots(p->packed, p->N, d->T, gls::kDeltaChunk);
-    const size_t rec = static_cast<size_t>(p->slots) * d->H;
-    if (double(p->slots) * double(d->H) <= 2147483647.0) {
-      p->chunk32 = true;
-      p->name = d->dk <= 64 ? "delta-mfma-f32-64" : "delta-mfma-f32-128";
-      p->gate_bytes = 2 * round_up(rec * gls::kY32 * 4) + round_up(rec * gls::kGates * 4);
-    }
-  }
   const size_t tiles = (d->dv + gls::kSerialRows - 1) / gls::kSerialRows;
   p->bwd_ws = 2 * round_up(tiles * d->H * p->tok * d->dk * p->comp) + 2 * round_up(tiles * d->H * p->tok * p->comp);
   return GL_SUCCESS;
@@ -219,6 +227,32 @@ gls::ChunkArgs chunk_args(const gls::DeltaArgs& a, const Plan& p, void* saved, v
     s.take(c.ptf, rec * gls::kYf * 2);
     s.take(c.sf, p.state_bytes);
     s.take(c.ef, p.err_bytes);
+    s.take(c.yb, p.y_bytes);
+    s.take(c.st, p.last_bytes);
+  } else {
+    w.take(c.gates, p.gate_bytes);
+  }
+  return c;
+}
+
+// The same in fp32.
+gls::ChunkArgs chunk32_args(const gls::DeltaArgs& a, const Plan& p, void* saved, void* ws) {
+  gls::ChunkArgs c;
+  c.a = a;
+  c.slots = p.slots;
+  const size_t y = static_cast<size_t>(p.slots) * a.H * gls::kY32 * 4;
+  Cut w{static_cast<char*>(ws)};
+  if (ws) {
+    w.take(c.y32, y);
+    w.take(c.p32, y);
+  }
+  if (saved) {
+    Cut s{static_cast<char*>(saved)};
+    s.take(c.gates, p.gate_bytes);
+    s.take(c.yt32, y);
+    s.take(c.pt32, y);
+    s.take(c.s32, p.state_bytes);
+    s.take(c.e32, p.err_bytes);
     s.take(c.yb, p.y_bytes);
     s.take(c.st, p.last_bytes);
   } else {
@@ -287,15 +321,15 @@ gl_status_t gl_delta_fwd(const gl_delta_desc_t* desc, const void* q, const void*
       return fail(GL_ERROR_NOT_SUPPORTED, "strides of y: multiples of 8, rows apart");
     return chunk_fwd(chunk_args(a, p, saved, ws), static_cast<hipStream_t>(stream));
   }
-  if (p.chunk32 && !saved && !(misaligned(q) || misaligned(k) || misaligned(y))) {
-    gls::ChunkArgs c;
-    c.a = a;
-    c.slots = p.slots;
-    Cut w{static_cast<char*>(ws)};
-    w.take(c.y32, static_cast<size_t>(p.slots) * a.H * gls::kY32 * 4);
-    w.take(c.p32, static_cast<size_t>(p.slots) * a.H * gls::kY32 * 4);
-    c.gates = reinterpret_cast<float*>(w.at);
-    return hip_status(gls::launch_delta_chunk_f32(c, static_cast<hipStream_t>(stream)), "delta forward launch");
+  if (p.chunk32) {
+    const bool fits = !(misaligned(q) || misaligned(k) || misaligned(y)) && gls::delta_rows_f32_ok(a.sy, a.dv);
+    if (saved && !fits)
+      return fail(misaligned(q) || misaligned(k) || misaligned(y) ? GL_ERROR_MISALIGNED : GL_ERROR_NOT_SUPPORTED,
+                  "q, k and y of a training call: 16-byte aligned, strides multiples of 4, rows apart");
+    if (fits)
+      return hip_status(gls::launch_delta_chunk_f32(chunk32_args(a, p, saved, ws), static_cast<hipStream_t>(stream)),
+                        "delta forward launch");
+    // else token by token, without the workspace
   }
   return hip_status(gls::launch_delta_serial_fwd(p.io, a, static_cast<hipStream_t>(stream)), "delta forward launch");
 }
@@ -342,6 +376,27 @@ gl_status_t gl_delta_bwd(const gl_delta_desc_t* desc, const void* q, const void*
     c.zf = zf;
     c.bf = bf;
     return hip_status(gls::launch_delta_chunk_bwd(c, s), "delta backward launch");
+  }
+  if (p.chunk32) {
+    for (const void* x : {q, k, dy, static_cast<const void*>(dv)})
+      if (misaligned(x)) return fail(GL_ERROR_MISALIGNED, "q, k, dy and dv: 16-byte aligned");
+    if (p.tok > 0 && !(gls::delta_rows_f32_ok(a.sdy, a.dv) && gls::delta_rows_f32_ok(a.sdv, a.dv)))
+      return fail(GL_ERROR_NOT_SUPPORTED, "strides of dy, dv: multiples of 4, rows apart");
+    float *lf, *gf, *zf, *bf;
+    char *again, *fws;
+    w.take(lf, p.state_bytes);
+    w.take(gf, p.err_bytes);
+    w.take(zf, p.z_bytes);
+    w.take(bf, p.z_bytes);
+    w.take(again, saved ? 0 : p.saved);
+    w.take(fws, saved ? 0 : p.fwd_ws);
+    gls::ChunkArgs c = chunk32_args(a, p, saved ? const_cast<void*>(saved) : again, saved ? nullptr : fws);
+    if (!saved && (st = hip_status(gls::launch_delta_chunk_f32(c, s), "delta forward launch")) != GL_SUCCESS) return st;
+    c.l32 = lf;
+    c.g32 = gf;
+    c.zf = zf;
+    c.bf = bf;
+    return hip_status(gls::launch_delta_chunk_f32_bwd(c, s), "delta backward launch");
   }
   const size_t tiles = (desc->dv + gls::kSerialRows - 1) / gls::kSerialRows;
   w.take(a.part_dq, tiles * desc->H * p.tok * desc->dk * p.comp);

@@ -1,57 +1,22 @@
 // k_delta_chunk_f32.hip -- the gated delta rule over the chunks of a sequence in
-// fp32 (forward without anything saved).  Per chunk of 64 tokens, with S the
-// state before it and Y, P as the bf16 chunks have them:
+// fp32, forward.  Per chunk of 64 tokens, with S the state before it and Y, P as
+// the bf16 chunks have them:
 //
 //   R = V - e^l (K S^T),  E = R - Y (beta R),  U = beta E
 //   y = scale e^l (Q S^T) + P U,   S <- e^(l_C) S + U^T (e^(l_C - l) K)
 //
-// All products are v_mfma_f32_16x16x4_f32, whose result (lane (g, l): rows
-// 4g + q of column l) is an operand over its rows as it stands: step q of a
-// block of 16 takes value q, and lane group g then holds index 4g + q of both
-// operands.  So a wave carries 16 rows of S through the sequence in registers,
-// as in bf16, without any split into terms.
-#include "delta_solve.hpp"
+// All products are v_mfma_f32_16x16x4_f32, whose results chain as operands in
+// registers (delta_f32.hpp): a wave carries 16 rows of S through the sequence,
+// as in bf16.
+#include "delta_f32.hpp"
 #include "dev_common.hpp"
 
 namespace gls {
 namespace {
 
-// ---- LDS tile [64][DK] fp32: 16-byte groups XORed with the row's low four
-// bits; conflict-free along a row (operands over k) and down a column.
-template <int DK>
-__device__ __forceinline__ uint32_t row_at(int lane) {
-  const int l = lane & 15, g = lane >> 4;
-  return static_cast<uint32_t>(l * DK * 4 + 16 * (g ^ l));
-}
-template <int DK>
-__device__ __forceinline__ f32x4 row_frag(const char* tile, uint32_t at, int tb, int b) {
-  return *reinterpret_cast<const f32x4*>(tile + tb * 16 * DK * 4 + (at ^ (64 * b)));
-}
-template <int DK>
-__device__ __forceinline__ uint32_t col_at(int lane, int q) {
-  const int l = lane & 15, r = 4 * (lane >> 4) + q;
-  return static_cast<uint32_t>(r * DK * 4 + 16 * ((l >> 2) ^ r) + 4 * (l & 3));
-}
-template <int DK>
-__device__ __forceinline__ f32x4 col_frag(const char* tile, const uint32_t (&at)[4], int tb, int b) {
-  f32x4 x;
-#pragma unroll
-  for (int q = 0; q < 4; ++q) x[q] = *reinterpret_cast<const float*>(tile + tb * 16 * DK * 4 + (at[q] ^ (64 * b)));
-  return x;
-}
-
-// Buffer over rows t0 .. t0 + 63 (those below len) of d columns, row stride st.
-__device__ __forceinline__ __amdgpu_buffer_rsrc_t rows_f32(const float* base, int64_t t0, int64_t len, int64_t st,
-                                                           int d) {
-  const int64_t n = len - t0 < 64 ? len - t0 : 64;
-  return buffer_rsrc(base + (n > 0 ? t0 * st : 0), n > 0 ? static_cast<int>(((n - 1) * st + d) * 4) : 0);
-}
-__device__ __forceinline__ f32x4 load_f32x4(__amdgpu_buffer_rsrc_t r, uint32_t off) {
-  return __builtin_bit_cast(f32x4, __builtin_amdgcn_raw_buffer_load_b128(r, off, 0, 0));
-}
-
 // Y and P of a chunk: blocks (i, j <= i) of 16 x 16, row 16 i + l in lanes,
-// columns 16 j + 4g .. + 3; and the gates' factors.
+// columns 16 j + 4g .. + 3; for training also with column 16 j + l in lanes, rows
+// 16 i + 4g .. + 3; and the gates' factors.
 template <int DK>
 __global__ __launch_bounds__(256) void delta_prep_f32(ChunkArgs ca) {
   const DeltaArgs& a = ca.a;
@@ -112,12 +77,28 @@ __global__ __launch_bounds__(256) void delta_prep_f32(ChunkArgs ca) {
     for (int q = 0; q < 4; ++q) p[q] *= sc * s.decay(16 * w + l, 16 * j + 4 * g + q, false);
     *reinterpret_cast<f32x4*>(ca.p32 + rec * kY32 + SolveLds::tri(w, j) * 256 + lane * 4) = p;
   }
+  if (ca.pt32) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      if (i < w) continue;
+      f32x4 x = zero4();
+#pragma unroll
+      for (int b = 0; b < NB; ++b) x = mul16(row(rq, a.sq.t, i, b), kw[b], x);
+#pragma unroll
+      for (int q = 0; q < 4; ++q) x[q] *= sc * s.decay(16 * i + 4 * g + q, 16 * w + l, false);
+      *reinterpret_cast<f32x4*>(ca.pt32 + rec * kY32 + SolveLds::tri(i, w) * 256 + lane * 4) = x;
+    }
+  }
   invert_diagonal(s, w, lane);
   lds_barrier();
   f32x4 y[4];
   solve_column(s, w, lane, y);
   lds_barrier();  // Lr is free
   turn_column(s, w, lane, y);
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+    if (i >= w && ca.yt32)
+      *reinterpret_cast<f32x4*>(ca.yt32 + rec * kY32 + SolveLds::tri(i, w) * 256 + lane * 4) = y[i];
 #pragma unroll
   for (int i = 0; i < 4; ++i)
     if (i >= w)
@@ -135,7 +116,7 @@ struct F32Lds {
 
 // A work-group is NW state waves, NW output waves one chunk behind, and a wave
 // that loads the next chunk's K; V, Y, Q and P go straight to registers.
-template <int DK, int NW>
+template <int DK, int NW, bool SAVE>
 __global__ __launch_bounds__(64 * (2 * NW + 1)) void delta_chunk_f32(ChunkArgs ca) {
   const DeltaArgs& a = ca.a;
   constexpr int NB = DK / 16, VW = 16 * NW;
@@ -155,14 +136,11 @@ __global__ __launch_bounds__(64 * (2 * NW + 1)) void delta_chunk_f32(ChunkArgs c
   const int64_t rec0 = slot0 * a.H + h;
 
   if (wave == 2 * NW) {  // ---- loads: K and gates, one chunk ahead
-    constexpr int NK = DK / 4, U = DK / 4;
+    constexpr int NK = DK / 4;
     const float* kp = static_cast<const float*>(a.k) + sr.b * a.sk.b + hk * a.sk.h + sr.t0 * a.sk.t;
     uint32_t ko[NK];
 #pragma unroll
-    for (int i = 0; i < NK; ++i) {
-      const int u0 = i * 64 + lane, r = u0 / U, c = 4 * ((u0 % U) ^ (r & 15));
-      ko[i] = c < a.dk ? static_cast<uint32_t>((r * static_cast<int>(a.sk.t) + c) * 4) : kPastEnd;
-    }
+    for (int i = 0; i < NK; ++i) ko[i] = tile_off_f32<DK>(i, lane, a.sk.t, a.dk);
     const auto issue = [&](int c) {
       const bool in = c < nc;
       const __amdgpu_buffer_rsrc_t rk = rows_f32(kp, c * 64LL, in ? sr.len : 0, a.sk.t, a.dk);
@@ -185,7 +163,7 @@ __global__ __launch_bounds__(64 * (2 * NW + 1)) void delta_chunk_f32(ChunkArgs c
 
   if (wave >= NW) {  // ---- outputs, one chunk behind
     const int w = wave - NW;
-    const int rr = r0 + 16 * w + 4 * g;
+    const int rr = r0 + 16 * w + 4 * g, rt = tile * NW + w, n_rt = delta_row_tiles(a.dv);
     float* yp = static_cast<float*>(a.y) + sr.b * a.sy.b + h * a.sy.h + sr.t0 * a.sy.t + rr;
     const float* qp = static_cast<const float*>(a.q) + sr.b * a.sq.b + hk * a.sq.h + sr.t0 * a.sq.t;
     const float sc = static_cast<float>(a.scale);
@@ -241,10 +219,20 @@ __global__ __launch_bounds__(64 * (2 * NW + 1)) void delta_chunk_f32(ChunkArgs c
           for (int tb = jb; tb < 4; ++tb) o[tb] = mfma_f32(uf[q], pf[SolveLds::tri(tb, jb)][q], o[tb]);
       }
       fetch(min(c + 1, nc - 1));
+      if constexpr (SAVE) {
+        const int64_t rec = rec0 + static_cast<int64_t>(c) * a.H;
+#pragma unroll
+        for (int b = 0; b < NB; ++b)
+          *reinterpret_cast<f32x4*>(ca.s32 + ((rec * n_rt + rt) * NB + b) * 256 + lane * 4) =
+              turned_f32(lds.sx[c & 1][w] + b * 256, lane);
+#pragma unroll
+        for (int tb = 0; tb < 4; ++tb)
+          *reinterpret_cast<f32x4*>(ca.yb + (rec * 64 + 16 * tb + l) * (16 * n_rt) + rr) = o[tb];
+      }
 #pragma unroll
       for (int tb = 0; tb < 4; ++tb) {
         const int64_t t = 64LL * c + 16 * tb + l;
-        if (t < sr.len && rr < a.dv) *reinterpret_cast<f32x4*>(yp + t * a.sy.t) = o[tb];
+        if (a.y && t < sr.len && rr < a.dv) *reinterpret_cast<f32x4*>(yp + t * a.sy.t) = o[tb];
       }
     }
     return;
@@ -322,6 +310,13 @@ __global__ __launch_bounds__(64 * (2 * NW + 1)) void delta_chunk_f32(ChunkArgs c
 #pragma unroll
         for (int i = j; i < 4; ++i) E[i] = mfma_f32(yf[SolveLds::tri(i, j)][q], Z[j][q], E[i]);
     fetch(min(c + 1, nc - 1));
+    if constexpr (SAVE) {
+      const int VP = 16 * delta_row_tiles(a.dv);
+      const __amdgpu_buffer_rsrc_t re =
+          buffer_rsrc(ca.e32 + (rec0 + static_cast<int64_t>(c) * a.H) * 64 * VP, 256 * VP);
+#pragma unroll
+      for (int tb = 0; tb < 4; ++tb) store_rows(re, static_cast<uint32_t>((4 * g * VP + r) * 4), VP, tb, E[tb]);
+    }
 #pragma unroll
     for (int tb = 0; tb < 4; ++tb) {
       const f32x4 rs = gate(2, tb);
@@ -343,11 +338,14 @@ __global__ __launch_bounds__(64 * (2 * NW + 1)) void delta_chunk_f32(ChunkArgs c
     }
   }
   lds_barrier();
-  if (r < a.dv && a.state_out) {
+  if (r < a.dv) {
 #pragma unroll
-    for (int b = 0; b < NB; ++b)
-      if (16 * b + 4 * g < a.dk)
-        *reinterpret_cast<f32x4*>(static_cast<float*>(a.state_out) + so + 16 * b + 4 * g) = S[b];
+    for (int b = 0; b < NB; ++b) {
+      const int c = 16 * b + 4 * g;
+      if (c >= a.dk) continue;
+      if (a.state_out) *reinterpret_cast<f32x4*>(static_cast<float*>(a.state_out) + so + c) = S[b];
+      if constexpr (SAVE) *reinterpret_cast<f32x4*>(ca.st + so + c) = S[b];
+    }
   }
 }
 
@@ -361,7 +359,8 @@ hipError_t launch(const ChunkArgs& c, hipStream_t s) {
   }
   const int tiles = (c.a.dv + 16 * NW - 1) / (16 * NW);
   const dim3 grid(static_cast<unsigned>(head_blocks(c.a.N * c.a.H, tiles)));
-  delta_chunk_f32<DK, NW><<<grid, 64 * (2 * NW + 1), 0, s>>>(c);
+  if (c.s32) delta_chunk_f32<DK, NW, true><<<grid, 64 * (2 * NW + 1), 0, s>>>(c);
+  else delta_chunk_f32<DK, NW, false><<<grid, 64 * (2 * NW + 1), 0, s>>>(c);
   return hipGetLastError();
 }
 
@@ -374,7 +373,7 @@ bool delta_rows_f32_ok(const Str3& s, int d) {
 
 bool delta_chunk_f32_ok(int io, const DeltaArgs& a) {
   return io == IO_F32 && a.dk % 4 == 0 && a.dv % 4 == 0 && delta_rows_f32_ok(a.sq, a.dk) &&
-         delta_rows_f32_ok(a.sk, a.dk) && delta_rows_f32_ok(a.sv, a.dv) && delta_rows_f32_ok(a.sy, a.dv);
+         delta_rows_f32_ok(a.sk, a.dk) && delta_rows_f32_ok(a.sv, a.dv);
 }
 
 hipError_t launch_delta_chunk_f32(const ChunkArgs& c, hipStream_t s) {

@@ -1,0 +1,450 @@
+// k_delta_chunk_f32_bwd.hip -- the gated delta rule's gradients over chunks in
+// fp32, from what the forward left: the formulas of the bf16 chunks
+// (k_delta_chunk_bwd.hip), every product on v_mfma_f32_16x16x4_f32.
+//
+// The decay's gradient is again dlog_alpha_t = <dL/dS_T, S_T> + sum_{s >= t}
+// (dy_s.y_s - dv_s.v_s); here both states are kept in fp32, so the product
+// <Lam, S> is taken anew at every chunk's end and the sum runs over the chunk's
+// tokens only.
+#include "delta_f32.hpp"
+#include "dev_common.hpp"
+
+namespace gls {
+namespace {
+
+template <int DK, int NW>
+struct RevLds {
+  alignas(16) char k[2][64 * DK * 4];
+  alignas(16) char q[2][64 * DK * 4];
+  alignas(16) float gt[2][192];
+  alignas(16) float turn[NW][DK * 16];
+  float xs[NW][64];
+};
+
+// The recurrence of Lam, 16 rows a wave from the last chunk to the first; one
+// more wave loads the next chunk's K, Q and gates.  What belongs to a wave's own
+// rows (dO, V, y, e) goes straight to registers.
+template <int DK, int NW>
+__global__ __launch_bounds__(64 * (NW + 1), 1) void delta_rev_f32(ChunkArgs ca) {
+  const DeltaArgs& a = ca.a;
+  constexpr int NB = DK / 16, VW = 16 * NW;
+  __shared__ RevLds<DK, NW> lds;
+  const int lane = threadIdx.x & 63, l = lane & 15, g = lane >> 4;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int tiles = (a.dv + VW - 1) / VW;
+  int64_t head;
+  int tile;
+  if (!head_of_block(blockIdx.x, tiles, a.N * a.H, head, tile)) return;
+  const int h = static_cast<int>(head % a.H);
+  const int64_t n = head / a.H;
+  const int hk = h / (a.H / a.Hk), r0 = tile * VW;
+  const SeqRange sr = seq_range(a.cu, n, a.T);
+  const int nc = static_cast<int>((sr.len + kDeltaChunk - 1) / kDeltaChunk);
+  const int64_t slot0 = chunk_slot0(a.cu != nullptr, n, sr.t0, a.T, kDeltaChunk);
+  const int64_t rec0 = slot0 * a.H + h;
+
+  if (wave == NW) {  // ---- loads
+    constexpr int NK = DK / 4;
+    const float* kp = static_cast<const float*>(a.k) + sr.b * a.sk.b + hk * a.sk.h + sr.t0 * a.sk.t;
+    const float* qp = static_cast<const float*>(a.q) + sr.b * a.sq.b + hk * a.sq.h + sr.t0 * a.sq.t;
+    uint32_t ko[NK], qo[NK];
+#pragma unroll
+    for (int i = 0; i < NK; ++i) {
+      ko[i] = tile_off_f32<DK>(i, lane, a.sk.t, a.dk);
+      qo[i] = tile_off_f32<DK>(i, lane, a.sq.t, a.dk);
+    }
+    const auto issue = [&](int c) {
+      const int s = c & 1;
+      const __amdgpu_buffer_rsrc_t rk = rows_f32(kp, c * 64LL, sr.len, a.sk.t, a.dk);
+      const __amdgpu_buffer_rsrc_t rq = rows_f32(qp, c * 64LL, sr.len, a.sq.t, a.dk);
+      const __amdgpu_buffer_rsrc_t rg = buffer_rsrc(ca.gates + (rec0 + static_cast<int64_t>(c) * a.H) * kGates, 768);
+#pragma unroll
+      for (int i = 0; i < NK; ++i) dma16(rk, ko[i], lds.k[s] + i * 1024);
+#pragma unroll
+      for (int i = 0; i < NK; ++i) dma16(rq, qo[i], lds.q[s] + i * 1024);
+#pragma unroll
+      for (int i = 0; i < 3; ++i) dma4(rg, (i * 64 + lane) * 4, lds.gt[s] + i * 64);
+    };
+    if (nc > 0) issue(nc - 1);
+    for (int c = nc - 1; c >= 0; --c) {
+      wait_vm<0>();
+      lds_barrier();
+      if (c > 0) issue(c - 1);  // into the slot of chunk c + 1
+    }
+    return;
+  }
+
+  const int r = r0 + 16 * wave + l, rt = tile * NW + wave, n_rt = delta_row_tiles(a.dv), VP = 16 * n_rt;
+  const int64_t so = (head * a.dv + r) * a.dk;
+  const float sc = static_cast<float>(a.scale);
+  f32x4 S[NB];  // Lam^T
+  float z = 0.f;  // <Lam, state> after the chunk, over this wave's rows
+#pragma unroll
+  for (int b = 0; b < NB; ++b) {
+    S[b] = zero4();
+    const int c = 16 * b + 4 * g;
+    if (a.dstate_out && r < a.dv && c < a.dk) {
+      S[b] = *reinterpret_cast<const f32x4*>(static_cast<const float*>(a.dstate_out) + so + c);
+      const f32x4 s = *reinterpret_cast<const f32x4*>(ca.st + so + c);
+#pragma unroll
+      for (int q = 0; q < 4; ++q) z = fmaf(S[b][q], s[q], z);
+    }
+  }
+  z = wave_sum(z);
+  const float* vp = static_cast<const float*>(a.v) + sr.b * a.sv.b + h * a.sv.h + sr.t0 * a.sv.t;
+  const float* op = static_cast<const float*>(a.dy) + sr.b * a.sdy.b + h * a.sdy.h + sr.t0 * a.sdy.t;
+  uint32_t vo[4], oo[4];
+#pragma unroll
+  for (int q = 0; q < 4; ++q) {
+    vo[q] = r < a.dv ? static_cast<uint32_t>(((4 * g + q) * static_cast<int>(a.sv.t) + r) * 4) : kPastEnd;
+    oo[q] = r < a.dv ? static_cast<uint32_t>(((4 * g + q) * static_cast<int>(a.sdy.t) + r) * 4) : kPastEnd;
+  }
+  f32x4 sn[NB];  // the state after the chunk, turned
+  const uint32_t ra = static_cast<uint32_t>((4 * g * VP + r) * 4);
+  const uint32_t ka = row_at<DK>(lane);
+  const uint32_t kc[4] = {col_at<DK>(lane, 0), col_at<DK>(lane, 1), col_at<DK>(lane, 2), col_at<DK>(lane, 3)};
+  float* turn = lds.turn[wave];
+  for (int c = nc - 1; c >= 0; --c) {
+    const int64_t rec = rec0 + static_cast<int64_t>(c) * a.H;
+    lds_barrier();
+    const char* kt = lds.k[c & 1];
+    const char* qt = lds.q[c & 1];
+    const float* gt = lds.gt[c & 1] + 4 * g;
+    const auto gate = [&](int m, int tb) { return *reinterpret_cast<const f32x4*>(gt + 64 * m + 16 * tb); };
+    // loads that K Lam^T hides; the others follow when P is done with
+    f32x4 dO[4], V[4], Y[4], E[4], yt[10], pt[10];
+    const __amdgpu_buffer_rsrc_t ro = rows_f32(op, c * 64LL, sr.len, a.sdy.t, a.dv);
+#pragma unroll
+    for (int tb = 0; tb < 4; ++tb)
+#pragma unroll
+      for (int q = 0; q < 4; ++q)
+        dO[tb][q] = load4(ro, oo[q] + static_cast<uint32_t>(tb * 64 * static_cast<int>(a.sdy.t)));
+#pragma unroll
+    for (int f = 0; f < 10; ++f) pt[f] = *reinterpret_cast<const f32x4*>(ca.pt32 + rec * kY32 + f * 256 + lane * 4);
+#pragma unroll
+    for (int f = 0; f < 10; ++f) yt[f] = *reinterpret_cast<const f32x4*>(ca.yt32 + rec * kY32 + f * 256 + lane * 4);
+    // K Lam^T; Lam turned, for the gradients and for <Lam, state>
+    f32x4 D[4], Z[4];
+#pragma unroll
+    for (int tb = 0; tb < 4; ++tb) D[tb] = zero4();
+#pragma unroll
+    for (int b = 0; b < NB; ++b) {
+      f32x4 kf[4];
+#pragma unroll
+      for (int tb = 0; tb < 4; ++tb) kf[tb] = row_frag<DK>(kt, ka, tb, b);
+#pragma unroll
+      for (int q = 0; q < 4; ++q)
+#pragma unroll
+        for (int tb = 0; tb < 4; ++tb) D[tb] = mfma_f32(kf[tb][q], S[b][q], D[tb]);
+      *reinterpret_cast<f32x4*>(turn + b * 256 + lane * 4) = S[b];
+    }
+    float zz = 0.f;
+#pragma unroll
+    for (int b = 0; b < NB; ++b) {
+      const f32x4 x = turned_f32(turn + b * 256, lane);
+      *reinterpret_cast<f32x4*>(ca.l32 + ((rec * n_rt + rt) * NB + b) * 256 + lane * 4) = x;
+      if (c + 1 < nc)
+#pragma unroll
+        for (int q = 0; q < 4; ++q) zz = fmaf(x[q], sn[b][q], zz);
+    }
+    if (c + 1 < nc) z = wave_sum(zz);
+    // dU = e^(l_C - l) K Lam^T + P^T dO
+#pragma unroll
+    for (int tb = 0; tb < 4; ++tb) D[tb] *= gate(2, tb);
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+#pragma unroll
+      for (int q = 0; q < 4; ++q)
+#pragma unroll
+        for (int j = 0; j <= i; ++j) D[j] = mfma_f32(pt[SolveLds::tri(i, j)][q], dO[i][q], D[j]);
+    {
+      const __amdgpu_buffer_rsrc_t rv = rows_f32(vp, c * 64LL, sr.len, a.sv.t, a.dv);
+      const __amdgpu_buffer_rsrc_t re = buffer_rsrc(ca.e32 + rec * 64 * VP, 256 * VP);
+      const __amdgpu_buffer_rsrc_t ry = buffer_rsrc(ca.yb + rec * 64 * VP, 256 * VP);
+#pragma unroll
+      for (int tb = 0; tb < 4; ++tb) {
+#pragma unroll
+        for (int q = 0; q < 4; ++q)
+          V[tb][q] = load4(rv, vo[q] + static_cast<uint32_t>(tb * 64 * static_cast<int>(a.sv.t)));
+        E[tb] = load_rows(re, ra, VP, tb);
+        Y[tb] = load_rows(ry, ra, VP, tb);
+      }
+#pragma unroll
+      for (int b = 0; b < NB; ++b)
+        sn[b] = *reinterpret_cast<const f32x4*>(ca.s32 + ((rec * n_rt + rt) * NB + b) * 256 + lane * 4);
+    }
+    __builtin_amdgcn_sched_barrier(0);
+    // G = dU - Y^T (beta dU)
+#pragma unroll
+    for (int tb = 0; tb < 4; ++tb) {
+      const f32x4 be = gate(1, tb);
+#pragma unroll
+      for (int q = 0; q < 4; ++q) Z[tb][q] = -be[q] * D[tb][q];
+    }
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+#pragma unroll
+      for (int q = 0; q < 4; ++q)
+#pragma unroll
+        for (int j = 0; j <= i; ++j) D[j] = mfma_f32(yt[SolveLds::tri(i, j)][q], Z[i][q], D[j]);
+    // dbeta and the decay's terms over the wave's rows; operands of the update
+    float xe[16], xv[16];
+    f32x4 o[4], f[4], G[4];
+    const float whole = lds.gt[c & 1][63];
+#pragma unroll
+    for (int tb = 0; tb < 4; ++tb) {
+      const f32x4 gm = gate(0, tb), be = gate(1, tb);
+#pragma unroll
+      for (int q = 0; q < 4; ++q) {
+        G[tb][q] = D[tb][q];
+        xe[4 * tb + q] = G[tb][q] * E[tb][q];
+        const float F = be[q] * G[tb][q];
+        xv[4 * tb + q] = dO[tb][q] * Y[tb][q] - V[tb][q] * F;
+        o[tb][q] = sc * gm[q] * dO[tb][q];
+        f[tb][q] = -gm[q] * F;
+      }
+    }
+    const int tok = 16 * (l >> 2) + 4 * g + (l & 3);
+    const float db = row_sums(xe, l);
+    lds.xs[wave][tok] = row_sums(xv, l);
+    const float suffix = wave_scan_add(lds.xs[wave][63 - lane]);
+    ca.bf[(rec * n_rt + rt) * 64 + tok] = db;
+    ca.zf[(rec * n_rt + rt) * 64 + 63 - lane] = z + suffix;
+    const __amdgpu_buffer_rsrc_t rg = buffer_rsrc(ca.g32 + rec * 64 * VP, 256 * VP);
+#pragma unroll
+    for (int tb = 0; tb < 4; ++tb) store_rows(rg, ra, VP, tb, G[tb]);
+    __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+    for (int b = 0; b < NB; ++b) S[b] *= whole;
+#pragma unroll
+    for (int tb = 0; tb < 4; ++tb) {
+      f32x4 kf[NB], qf[NB];
+#pragma unroll
+      for (int b = 0; b < NB; ++b) {
+        kf[b] = col_frag<DK>(kt, kc, tb, b);
+        qf[b] = col_frag<DK>(qt, kc, tb, b);
+      }
+#pragma unroll
+      for (int q = 0; q < 4; ++q)
+#pragma unroll
+        for (int b = 0; b < NB; ++b) {
+          S[b] = mfma_f32(kf[b][q], f[tb][q], S[b]);
+          S[b] = mfma_f32(qf[b][q], o[tb][q], S[b]);
+        }
+      __builtin_amdgcn_sched_barrier(0);
+    }
+  }
+  if (a.dstate_in && r < a.dv) {
+#pragma unroll
+    for (int b = 0; b < NB; ++b)
+      if (16 * b + 4 * g < a.dk)
+        *reinterpret_cast<f32x4*>(static_cast<float*>(a.dstate_in) + so + 16 * b + 4 * g) = S[b];
+  }
+}
+
+// The gradients of one chunk, for the value heads of one key head in turn.  Wave
+// w has the 16 tokens of block w, of dq and of dk: every block of scores that it
+// needs comes out of the matrix cores with the index in lanes that the next
+// product wants, so the waves share K and Q in LDS and nothing else.
+template <int DK>
+struct GradLds {
+  alignas(16) char k[64 * DK * 4];
+  alignas(16) char q[64 * DK * 4];
+};
+
+template <int DK, int W>
+__device__ __forceinline__ void grad_block(const ChunkArgs& ca, const GradLds<DK>& lds, int64_t slot, const SeqRange& sr,
+                                           int64_t t0, int hk, int lane) {
+  const DeltaArgs& a = ca.a;
+  constexpr int NB = DK / 16;
+  const int grp = a.H / a.Hk;
+  const int nt = static_cast<int>(sr.len - t0 < 64 ? sr.len - t0 : 64);
+  const int n_rt = delta_row_tiles(a.dv), VP = 16 * n_rt;
+  const float sc = static_cast<float>(a.scale);
+  f32x4 dq[NB], dk[NB];
+#pragma unroll
+  for (int b = 0; b < NB; ++b) dq[b] = dk[b] = zero4();
+  for (int gi = 0; gi < grp; ++gi) {
+    const int h = hk * grp + gi;
+    const int64_t rec = slot * a.H + h;
+    // anew for each head: addresses kept over the loop cost more registers than there are
+    asm volatile("" : "+v"(lane));
+    const int l = lane & 15, g = lane >> 4;
+    const float* gt = ca.gates + rec * kGates;
+    const __amdgpu_buffer_rsrc_t ro =
+        rows_f32(static_cast<const float*>(a.dy) + sr.b * a.sdy.b + h * a.sdy.h + sr.t0 * a.sdy.t, t0, sr.len, a.sdy.t,
+                 a.dv);
+    float* dvp = static_cast<float*>(a.dv_) + sr.b * a.sdv.b + h * a.sdv.h + (sr.t0 + t0 + 16 * W + l) * a.sdv.t;
+    const float* ep = ca.e32 + (rec * 64 + l) * VP + 4 * g;
+    const float* gp = ca.g32 + (rec * 64 + l) * VP + 4 * g;
+    const float* sp = ca.s32 + rec * n_rt * (NB * 256) + lane * 4;
+    const float* lp = ca.l32 + rec * n_rt * (NB * 256) + lane * 4;
+    const float bet = gt[64 + 16 * W + l], gam = gt[16 * W + l], rst = gt[128 + 16 * W + l];
+    // e_j dO_i and e_j G_i below and on the diagonal: rows j of column i = W's
+    // tokens (pq, h2), rows i of column j = W's (pk, h1)
+    f32x4 pq[4], pk[4], h1[4], h2[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) pq[i] = pk[i] = h1[i] = h2[i] = zero4();
+#pragma unroll 1
+    for (int rt = 0; rt < n_rt; ++rt) {
+      f32x4 d[4], e[4], G[4];
+      const int c = 16 * rt + 4 * g;
+      const uint32_t co = c < a.dv ? static_cast<uint32_t>(c * 4) : kPastEnd;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        if (i >= W) {
+          d[i] = load_f32x4(ro, co + static_cast<uint32_t>((16 * i + l) * static_cast<int>(a.sdy.t) * 4));
+          G[i] = *reinterpret_cast<const f32x4*>(gp + 16 * i * VP + 16 * rt);
+        }
+        if (i <= W) e[i] = *reinterpret_cast<const f32x4*>(ep + 16 * i * VP + 16 * rt);
+      }
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        if (i <= W) {
+          pq[i] = mul16(e[i], d[W], pq[i]);
+          h2[i] = mul16(e[i], G[W], h2[i]);
+        }
+        if (i >= W) {
+          pk[i] = mul16(d[i], e[W], pk[i]);
+          h1[i] = mul16(G[i], e[W], h1[i]);
+        }
+      }
+      const f32x4 dw = d[W] * (sc * gam), ew = e[W] * (rst * bet), gw = G[W] * (-gam * bet);
+      if (16 * W + l < nt && c < a.dv) *reinterpret_cast<f32x4*>(dvp + c) = G[W] * bet;
+      // four column blocks at a time
+#pragma unroll
+      for (int b0 = 0; b0 < NB; b0 += 4) {
+        f32x4 s[4], lam[4];
+#pragma unroll
+        for (int b = 0; b < 4; ++b) {
+          s[b] = *reinterpret_cast<const f32x4*>(sp + (rt * NB + b0 + b) * 256);
+          lam[b] = *reinterpret_cast<const f32x4*>(lp + (rt * NB + b0 + b) * 256);
+        }
+#pragma unroll
+        for (int q = 0; q < 4; ++q)
+#pragma unroll
+          for (int b = 0; b < 4; ++b) {
+            dq[b0 + b] = mfma_f32(dw[q], s[b][q], dq[b0 + b]);
+            dk[b0 + b] = mfma_f32(ew[q], lam[b][q], dk[b0 + b]);
+            dk[b0 + b] = mfma_f32(gw[q], s[b][q], dk[b0 + b]);
+          }
+        __builtin_amdgcn_sched_barrier(0);
+      }
+    }
+    // decay, beta and the triangle
+    const float lw = gt[192 + 16 * W + l], lf = gt[256 + 16 * W + l];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const f32x4 rw = *reinterpret_cast<const f32x4*>(gt + 192 + 16 * i + 4 * g);
+      const f32x4 rf = *reinterpret_cast<const f32x4*>(gt + 256 + 16 * i + 4 * g);
+      const f32x4 rb = *reinterpret_cast<const f32x4*>(gt + 64 + 16 * i + 4 * g);
+#pragma unroll
+      for (int q = 0; q < 4; ++q) {
+        const int x = 16 * i + 4 * g + q, y = 16 * W + l;  // the row's token, the column's
+        const float up = fexp2((lw - rw[q]) + (lf - rf[q])), down = fexp2((rw[q] - lw) + (rf[q] - lf));
+        if (i <= W) {
+          pq[i][q] = x <= y ? pq[i][q] * (sc * rb[q] * up) : 0.f;
+          h2[i][q] = x < y ? h2[i][q] * (rb[q] * bet * up) : 0.f;
+        }
+        if (i >= W) {
+          pk[i][q] = x >= y ? pk[i][q] * (sc * bet * down) : 0.f;
+          h1[i][q] = x > y ? h1[i][q] * (rb[q] * bet * down) : 0.f;
+        }
+        h1[i][q] = -(h1[i][q] + h2[i][q]);
+      }
+    }
+    const uint32_t kc[4] = {col_at<DK>(lane, 0), col_at<DK>(lane, 1), col_at<DK>(lane, 2), col_at<DK>(lane, 3)};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+#pragma unroll
+      for (int b = 0; b < NB; ++b) {
+        const f32x4 kf = col_frag<DK>(lds.k, kc, i, b);
+        if (i <= W) dq[b] = mul16(pq[i], kf, dq[b]);
+        dk[b] = mul16(h1[i], kf, dk[b]);
+        if (i >= W) dk[b] = mul16(pk[i], col_frag<DK>(lds.q, kc, i, b), dk[b]);
+        if (b % 4 == 3) __builtin_amdgcn_sched_barrier(0);
+      }
+    }
+    if (W == 3) {  // gates: token `lane`, over the row tiles
+      float dl = 0.f, db = 0.f;
+      for (int i = 0; i < n_rt; ++i) {
+        dl += ca.zf[(rec * n_rt + i) * 64 + lane];
+        db += ca.bf[(rec * n_rt + i) * 64 + lane];
+      }
+      // a token that forgets everything has no gradient to its decay
+      const float w = gt[192 + lane];
+      if (w - wave_shift_up(w, 0.f) < -149.f) dl = 0.f;
+      if (lane < nt) {
+        const int64_t o = sr.b * a.sdg.b + h * a.sdg.h + (sr.t0 + t0 + lane) * a.sdg.t;
+        static_cast<float*>(a.dla)[o] = dl;
+        static_cast<float*>(a.dbe)[o] = db;
+      }
+    }
+  }
+  const int l = lane & 15, g = lane >> 4;
+#pragma unroll
+  for (int q = 0; q < 4; ++q) {
+    const int tok = 16 * W + 4 * g + q;
+    if (tok >= nt) continue;
+    float* pq = static_cast<float*>(a.dq) + sr.b * a.sdq.b + hk * a.sdq.h + (sr.t0 + t0 + tok) * a.sdq.t;
+    float* pk = static_cast<float*>(a.dk_) + sr.b * a.sdk.b + hk * a.sdk.h + (sr.t0 + t0 + tok) * a.sdk.t;
+#pragma unroll
+    for (int b = 0; b < NB; ++b)
+      if (16 * b + l < a.dk) {
+        pq[16 * b + l] = dq[b][q];
+        pk[16 * b + l] = dk[b][q];
+      }
+  }
+}
+
+template <int DK>
+__global__ __launch_bounds__(256, 2) void delta_grad_f32(ChunkArgs ca) {
+  const DeltaArgs& a = ca.a;
+  __shared__ GradLds<DK> lds;
+  const int lane = threadIdx.x & 63;
+  const int w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int hk = static_cast<int>(blockIdx.x % a.Hk);
+  const int64_t slot = blockIdx.x / a.Hk;
+  SeqRange sr;
+  int64_t t0;
+  if (!chunk_of_slot(a, slot, sr, t0)) return;
+  {
+    const float* kp = static_cast<const float*>(a.k) + sr.b * a.sk.b + hk * a.sk.h + sr.t0 * a.sk.t;
+    const float* qp = static_cast<const float*>(a.q) + sr.b * a.sq.b + hk * a.sq.h + sr.t0 * a.sq.t;
+    const __amdgpu_buffer_rsrc_t rk = rows_f32(kp, t0, sr.len, a.sk.t, a.dk);
+    const __amdgpu_buffer_rsrc_t rq = rows_f32(qp, t0, sr.len, a.sq.t, a.dk);
+#pragma unroll
+    for (int j = 0; j < DK / 16; ++j) {
+      const int i = w * (DK / 16) + j;
+      dma16(rk, tile_off_f32<DK>(i, lane, a.sk.t, a.dk), lds.k + i * 1024);
+      dma16(rq, tile_off_f32<DK>(i, lane, a.sq.t, a.dk), lds.q + i * 1024);
+    }
+    wait_vm<0>();
+  }
+  __syncthreads();
+  if (w == 0) grad_block<DK, 0>(ca, lds, slot, sr, t0, hk, lane);
+  else if (w == 1) grad_block<DK, 1>(ca, lds, slot, sr, t0, hk, lane);
+  else if (w == 2) grad_block<DK, 2>(ca, lds, slot, sr, t0, hk, lane);
+  else grad_block<DK, 3>(ca, lds, slot, sr, t0, hk, lane);
+}
+
+template <int DK>
+hipError_t launch(const ChunkArgs& c, hipStream_t s) {
+  constexpr int NW = 2;
+  const int tiles = (c.a.dv + 16 * NW - 1) / (16 * NW);
+  delta_rev_f32<DK, NW>
+      <<<dim3(static_cast<unsigned>(head_blocks(c.a.N * c.a.H, tiles))), 64 * (NW + 1), 0, s>>>(c);
+  const hipError_t e = hipGetLastError();
+  if (e != hipSuccess || c.slots == 0) return e;
+  delta_grad_f32<DK><<<dim3(static_cast<unsigned>(c.slots * c.a.Hk)), 256, 0, s>>>(c);
+  return hipGetLastError();
+}
+
+}  // namespace
+
+hipError_t launch_delta_chunk_f32_bwd(const ChunkArgs& c, hipStream_t s) {
+  if (c.a.N * c.a.H == 0) return hipSuccess;
+  return c.a.dk <= 64 ? launch<64>(c, s) : launch<128>(c, s);
+}
+
+}  // namespace gls
