@@ -83,6 +83,30 @@ def test_odd_sizes(d, rot, dtype, interleaved):
     case(d * 3 + rot, 2, 9, 3, 1, d, rot, dtype, interleaved, order="bhtd")
 
 
+@pytest.mark.parametrize("dtype", [F64, F32, BF16])
+@pytest.mark.parametrize("d,rot", [(32, 30), (34, 16), (66, 0), (126, 62), (194, 194), (250, 8)])
+@pytest.mark.parametrize("interleaved", [False, True])
+def test_even_sizes(d, rot, dtype, interleaved):
+    case(d + 7 * rot, 3, 21, 4, 3, d, rot, dtype, interleaved, order="bthd")
+
+
+def test_rows_that_are_not_aligned():
+    """Slices of a wider row: strides that 16 bytes do not divide."""
+    for dtype in (F32, BF16):
+        wide = torch.randn(2, 20, 3, 64 + 1, device="cuda").to(dtype)[..., :64].transpose(1, 2)
+        oq, ok = ws.gl_qknorm_rope_fwd(wide, wide, q_scale=0.5)
+        want = qknorm(wide.double().cpu(), None, None, None, None, 1e-6, 0.5)
+        assert rel(oq, want) <= TOL[dtype] and rel(ok, 2 * want) <= TOL[dtype]
+        dq, dk, _, _ = ws.gl_qknorm_rope_bwd(wide, wide, None, None, None, None, oq, ok, q_scale=0.5)
+        x = wide.double().cpu().requires_grad_(True)
+        z = qknorm(x, None, None, None, None, 1e-6, 0.5)
+        ref = torch.autograd.grad((z * oq.double().cpu()).sum(), x)[0]
+        # the gradient of half the squared norm nearly cancels (|out| hardly depends on |x|): against |dz| / |x|
+        scale = 0.5 * oq.double().cpu().norm() / x.detach().norm() * 64 ** 0.5
+        assert float((dq.double().cpu() - ref).norm()) <= 4 * TOL[dtype] * float(scale)
+        assert torch.isfinite(dk.double()).all()
+
+
 @pytest.mark.parametrize("B,T", [(1, 1), (64, 1), (1, 777), (3, 300)])
 @pytest.mark.parametrize("Hq,Hk", [(16, 8), (1, 1), (5, 0), (0, 2)])
 def test_tokens_and_heads(B, T, Hq, Hk):

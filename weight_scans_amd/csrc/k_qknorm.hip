@@ -13,8 +13,9 @@
 // takes one token and walks its heads: cosines and sines (as many bytes as a
 // bf16 row has) are loaded once per token and stay in registers, and so do the
 // weights.  Sums for dw stay in registers over the walk, meet in LDS, and
-// leave as one part per work-group, added in a fixed order.  Other sizes take
-// one wave per row with the row in LDS.
+// leave as one part per work-group, added in a fixed order.  Other even sizes
+// take half a wave per row and go pair by pair of elements; odd and short rows
+// one wave with the row in LDS.
 #include <algorithm>
 
 #include "delta.hpp"
@@ -328,8 +329,161 @@ __global__ __launch_bounds__(16 * kDwRows) void qknorm_dw(QkArgs a) {
   }
 }
 
-// ---- any size: one wave per row, the row in LDS, four columns a lane.  These
-// sizes are rare and short rows among them, whose gradient w dz - n mean(w dz n)
+// ---- even d of at least 32 that the vector kernels do not take (their sizes,
+// strides or alignment): half a wave per row, a lane with the pairs of columns
+// l, l + 32, ... that a rotation turns (those past rot: neighbours), element by
+// element, so that again only the sums cross lanes.  Bound by the number of its
+// loads and stores: forward and backward of 4 x 4096 tokens of 24 heads of 120,
+// bf16, take 183 us (one wave a row in fp64: 621; the vector kernels at 128: 122).
+constexpr int kPairLanes = 32;
+
+template <typename S, int U>
+struct Pairs {
+  int c0[U], c1[U];
+  bool in[U], turned[U];
+  S c[U], s[U], w0[U], w1[U];
+  __device__ __forceinline__ Pairs(const QkArgs& a, int l) {
+#pragma unroll
+    for (int i = 0; i < U; ++i) {
+      const int u = l + kPairLanes * i;
+      in[i] = 2 * u < a.d;
+      turned[i] = 2 * u < a.rot;
+      c0[i] = turned[i] && !a.interleaved ? u : 2 * u;
+      c1[i] = turned[i] && !a.interleaved ? u + a.rot / 2 : 2 * u + 1;
+      c[i] = S(1);
+      s[i] = S(0);
+    }
+  }
+  __device__ __forceinline__ void angles(const QkArgs& a, int64_t bt, int l) {
+    if (!a.rot) return;
+    const int64_t o = position(a, bt) * (a.rot / 2) + l;
+#pragma unroll
+    for (int i = 0; i < U; ++i)
+      if (turned[i]) {
+        c[i] = static_cast<const S*>(a.cos)[o + kPairLanes * i];
+        s[i] = static_cast<const S*>(a.sin)[o + kPairLanes * i];
+      }
+  }
+  template <typename IO>
+  __device__ __forceinline__ void weights(const void* w) {
+#pragma unroll
+    for (int i = 0; i < U; ++i) {
+      w0[i] = w && in[i] ? load_as<S>(static_cast<const IO*>(w), c0[i]) : S(1);
+      w1[i] = w && in[i] ? load_as<S>(static_cast<const IO*>(w), c1[i]) : S(1);
+    }
+  }
+  template <typename IO>
+  __device__ __forceinline__ void load(const IO* p, S (&u)[U], S (&v)[U]) const {
+#pragma unroll
+    for (int i = 0; i < U; ++i) {
+      u[i] = in[i] ? load_as<S>(p, c0[i]) : S(0);
+      v[i] = in[i] ? load_as<S>(p, c1[i]) : S(0);
+    }
+  }
+  template <typename IO>
+  __device__ __forceinline__ void store(IO* p, const S (&u)[U], const S (&v)[U]) const {
+#pragma unroll
+    for (int i = 0; i < U; ++i)
+      if (in[i]) {
+        store_from(p, c0[i], u[i]);
+        store_from(p, c1[i], v[i]);
+      }
+  }
+};
+
+template <typename IO, typename S, int U>
+__global__ __launch_bounds__(kThreads) void qknorm_fwd_p(QkArgs a) {
+  const int64_t g = blockIdx.x * static_cast<int64_t>(kThreads / kPairLanes) + threadIdx.x / kPairLanes;
+  const int l = threadIdx.x % kPairLanes, heads = a.Hn[0] + a.Hn[1];
+  const int parts = (heads + a.hpg - 1) / a.hpg;
+  const int64_t bt = g / parts;
+  if (bt >= a.B * a.T) return;
+  const int h0 = static_cast<int>(g % parts) * a.hpg, h1 = min(heads, h0 + a.hpg);
+  const int64_t b = bt / a.T, t = bt % a.T;
+  Pairs<S, U> p(a, l);
+  p.angles(a, bt, l);
+  int had = -1;
+  for (int hh = h0; hh < h1; ++hh) {
+    const int which = hh >= a.Hn[0], h = hh - which * a.Hn[0];
+    if (which != had) p.template weights<IO>(a.w[which]);
+    had = which;
+    S x0[U], x1[U], ss = S(0);
+    p.load(static_cast<const IO*>(a.x[which]) + b * a.sx[which].b + h * a.sx[which].h + t * a.sx[which].t, x0, x1);
+#pragma unroll
+    for (int i = 0; i < U; ++i) ss += x0[i] * x0[i] + x1[i] * x1[i];
+    const S r = static_cast<S>(a.scale[which]) / root(sum_group<S, kPairLanes>(ss) / a.d + static_cast<S>(a.eps));
+#pragma unroll
+    for (int i = 0; i < U; ++i) {
+      const S u = x0[i] * (r * p.w0[i]), v = x1[i] * (r * p.w1[i]);
+      x0[i] = u * p.c[i] - v * p.s[i];
+      x1[i] = v * p.c[i] + u * p.s[i];
+    }
+    p.store(static_cast<IO*>(a.out[which]) + b * a.so[which].b + h * a.so[which].h + t * a.so[which].t, x0, x1);
+  }
+}
+
+template <typename IO, typename S, int U>
+__global__ __launch_bounds__(kThreads) void qknorm_bwd_p(QkArgs a) {
+  constexpr int G = kThreads / kPairLanes;
+  __shared__ S red[G][2 * kPairLanes * U];
+  const int which = blockIdx.y, l = threadIdx.x % kPairLanes, gi = threadIdx.x / kPairLanes;
+  const S scale = static_cast<S>(a.scale[which]);
+  const int heads = a.Hn[which], parts = (heads + a.hpg - 1) / a.hpg;
+  const int64_t units = a.B * a.T * parts;
+  Pairs<S, U> p(a, l);
+  p.template weights<IO>(a.w[which]);
+  S d0[U], d1[U];
+#pragma unroll
+  for (int i = 0; i < U; ++i) d0[i] = d1[i] = S(0);
+  for (int64_t un = blockIdx.x * static_cast<int64_t>(G) + gi; un < units; un += static_cast<int64_t>(gridDim.x) * G) {
+    const int64_t bt = un / parts, b = bt / a.T, t = bt % a.T;
+    const int h0 = static_cast<int>(un % parts) * a.hpg, h1 = min(heads, h0 + a.hpg);
+    p.angles(a, bt, l);
+    for (int h = h0; h < h1; ++h) {
+      S x0[U], x1[U], g0[U], g1[U], ss = S(0), dot = S(0);
+      p.load(static_cast<const IO*>(a.x[which]) + b * a.sx[which].b + h * a.sx[which].h + t * a.sx[which].t, x0, x1);
+      p.load(static_cast<const IO*>(a.dout[which]) + b * a.sdo[which].b + h * a.sdo[which].h + t * a.sdo[which].t, g0,
+             g1);
+#pragma unroll
+      for (int i = 0; i < U; ++i) {
+        const S u = scale * g0[i], v = scale * g1[i];
+        g0[i] = u * p.c[i] + v * p.s[i];
+        g1[i] = v * p.c[i] - u * p.s[i];
+        ss += x0[i] * x0[i] + x1[i] * x1[i];
+        dot += g0[i] * p.w0[i] * x0[i] + g1[i] * p.w1[i] * x1[i];
+      }
+      ss = sum_group<S, kPairLanes>(ss);
+      dot = sum_group<S, kPairLanes>(dot);
+      const S r = S(1) / root(ss / a.d + static_cast<S>(a.eps));
+      const S m = dot * r * r / a.d;
+#pragma unroll
+      for (int i = 0; i < U; ++i) {
+        d0[i] += g0[i] * (x0[i] * r);
+        d1[i] += g1[i] * (x1[i] * r);
+        x0[i] = r * (p.w0[i] * g0[i] - x0[i] * m);
+        x1[i] = r * (p.w1[i] * g1[i] - x1[i] * m);
+      }
+      p.store(static_cast<IO*>(a.out[which]) + b * a.so[which].b + h * a.so[which].h + t * a.so[which].t, x0, x1);
+    }
+  }
+  if (!a.dw[which]) return;
+#pragma unroll
+  for (int i = 0; i < U; ++i)
+    if (p.in[i]) {
+      red[gi][p.c0[i]] = d0[i];
+      red[gi][p.c1[i]] = d1[i];
+    }
+  __syncthreads();
+  S* part = static_cast<S*>(a.part) + (static_cast<int64_t>(which) * a.n_part + blockIdx.x) * a.d;
+  for (int c = threadIdx.x; c < a.d; c += kThreads) {
+    S x = S(0);
+    for (int g = 0; g < G; ++g) x += red[g][c];
+    part[c] = x;
+  }
+}
+
+// ---- any size: one wave per row, the row in LDS, four columns a lane.  Odd and
+// short rows are left, among them some whose gradient w dz - n mean(w dz n)
 // nearly cancels (for d = 1 it is eps / (x^2 + eps) of its first term), so the
 // row is computed in fp64; tables and sums keep the type S.
 constexpr int kWaves = kThreads / 64, kMaxD = 256;
@@ -441,6 +595,8 @@ bool vector_ok(int io, const QkArgs& a, bool bwd) {
   return ok;
 }
 
+bool pairs_ok(const QkArgs& a) { return a.d % 2 == 0 && a.d >= 32; }
+
 // Heads per group of lanes: all of a token's, so that its angles are loaded
 // once, unless that leaves the chip short of groups (256 CUs of 2048 lanes).
 int heads_per_group(int64_t tokens, int heads, int L) {
@@ -456,6 +612,18 @@ hipError_t fwd_io(int io, QkArgs a, hipStream_t s) {
   const int64_t tok = a.B * a.T;
   const int heads = a.Hn[0] + a.Hn[1];
   if (tok == 0 || heads == 0) return hipSuccess;
+  if (!vector_ok(io, a, false) && pairs_ok(a)) {
+    a.hpg = heads_per_group(tok, heads, kPairLanes);
+    const int64_t groups = tok * ((heads + a.hpg - 1) / a.hpg);
+    const unsigned g = static_cast<unsigned>((groups * kPairLanes + kThreads - 1) / kThreads);
+    switch ((a.d + 2 * kPairLanes - 1) / (2 * kPairLanes)) {
+      case 1: qknorm_fwd_p<IO, S, 1><<<g, kThreads, 0, s>>>(a); break;
+      case 2: qknorm_fwd_p<IO, S, 2><<<g, kThreads, 0, s>>>(a); break;
+      case 3: qknorm_fwd_p<IO, S, 3><<<g, kThreads, 0, s>>>(a); break;
+      default: qknorm_fwd_p<IO, S, 4><<<g, kThreads, 0, s>>>(a); break;
+    }
+    return hipGetLastError();
+  }
   if (!vector_ok(io, a, false)) {
     const int64_t rows = tok * std::max(a.Hn[0], a.Hn[1]);
     const int64_t g = std::min<int64_t>((rows + kWaves - 1) / kWaves, 16384);
@@ -479,11 +647,17 @@ hipError_t fwd_io(int io, QkArgs a, hipStream_t s) {
 template <typename IO, typename S>
 hipError_t bwd_io(int io, QkArgs a, hipStream_t s) {
   const int64_t tok = a.B * a.T;
-  const bool vec = vector_ok(io, a, true);
-  const int L = lanes(a.d);
+  const bool vec = vector_ok(io, a, true), pairs = !vec && pairs_ok(a);
+  const int L = pairs ? kPairLanes : lanes(a.d);
   a.hpg = heads_per_group(tok, std::max(1, std::max(a.Hn[0], a.Hn[1])), L);
   const dim3 grid(static_cast<unsigned>(a.n_part), 2);
-  if (!vec) qknorm_any<IO, S, true><<<grid, kThreads, 0, s>>>(a);
+  if (pairs) switch ((a.d + 2 * kPairLanes - 1) / (2 * kPairLanes)) {
+    case 1: qknorm_bwd_p<IO, S, 1><<<grid, kThreads, 0, s>>>(a); break;
+    case 2: qknorm_bwd_p<IO, S, 2><<<grid, kThreads, 0, s>>>(a); break;
+    case 3: qknorm_bwd_p<IO, S, 3><<<grid, kThreads, 0, s>>>(a); break;
+    default: qknorm_bwd_p<IO, S, 4><<<grid, kThreads, 0, s>>>(a); break;
+  }
+  else if (!vec) qknorm_any<IO, S, true><<<grid, kThreads, 0, s>>>(a);
   else switch (L) {
     case 1: qknorm_bwd_v<IO, S, 1><<<grid, kThreads, 0, s>>>(a); break;
     case 2: qknorm_bwd_v<IO, S, 2><<<grid, kThreads, 0, s>>>(a); break;
