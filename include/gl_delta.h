@@ -49,9 +49,9 @@
  * was rounded once: 3e-3; dv and dbeta 2.5e-3.
  *
  * Kernels: BF16 io with dk and dv multiples of 8, and F32 io with multiples of
- * 4, run in chunks of 64 tokens on the matrix cores.  Everything else, and
- * sequences of fewer than 16 tokens on average, goes token by token on the
- * vector ALU.
+ * 4, run in chunks of 64 tokens on the matrix cores.  Everything else goes token
+ * by token on the vector ALU, and so do sequences of fewer than 4 tokens on
+ * average (fewer than 16 in a forward that saves nothing).
  */
 #ifndef GL_DELTA_H
 #define GL_DELTA_H

@@ -99,8 +99,8 @@ def test_null_arguments():
     (dict(), "delta-mfma-bf16-64x64"), (dict(gate_dtype=F32), "delta-mfma-bf16-64x64"),
     (dict(dk=8, dv=128), "delta-mfma-bf16-64x128"), (dict(dk=72, dv=8), "delta-mfma-bf16-128x64"),
     (dict(dk=128, dv=128, B=1, n_seq=3), "delta-mfma-bf16-128x128"),
-    (dict(T=15), "delta-serial-bf16"), (dict(T=16), "delta-mfma-bf16-64x64"),
-    (dict(B=1, n_seq=7), "delta-serial-bf16"),  # 100 tokens of 7 sequences
+    (dict(T=3), "delta-serial-bf16"), (dict(T=4), "delta-mfma-bf16-64x64"),
+    (dict(B=1, n_seq=26), "delta-serial-bf16"),  # 100 tokens of 26 sequences
     (dict(dk=60), "delta-serial-bf16"), (dict(dv=4), "delta-serial-bf16"),
     (dict(flags=ws.GL_FLAG_GENERIC), "delta-serial-bf16"),
     (dict(sq=(0, 64, 64)), "delta-mfma-bf16-64x64"), (dict(sk=(0, 64, 0)), "delta-serial-bf16"),
@@ -108,7 +108,7 @@ def test_null_arguments():
     (dict(io_dtype=F32, gate_dtype=F32), "delta-mfma-f32-64"),
     (dict(io_dtype=F32, gate_dtype=F32, dk=68, dv=20), "delta-mfma-f32-128"),
     (dict(io_dtype=F32, gate_dtype=F32, dk=66), "delta-serial-f32"),
-    (dict(io_dtype=F32, gate_dtype=F32, T=8), "delta-serial-f32"),
+    (dict(io_dtype=F32, gate_dtype=F32, T=2), "delta-serial-f32"),
     (dict(io_dtype=F64, gate_dtype=F64), "delta-serial-f64"),
 ])
 def test_paths(kw, path):
@@ -157,7 +157,7 @@ def step(d, edit=(), n_slots=8):
     return status("gl_delta_step", ctypes.byref(d), *p[:6], n_slots, *p[6:], None)
 
 
-@pytest.mark.parametrize("kw", [dict(), dict(io_dtype=F64, gate_dtype=F64), dict(T=5),
+@pytest.mark.parametrize("kw", [dict(), dict(io_dtype=F64, gate_dtype=F64), dict(T=5), dict(T=3),
                                 dict(io_dtype=F32, gate_dtype=F32)])
 def test_pointers_refused(kw):
     d = desc(**kw)

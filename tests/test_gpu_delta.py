@@ -286,9 +286,9 @@ def test_empty():
     (96, 80, 130, None), (4, 4, 70, None), (64, 64, 264, [1, 63, 0, 65, 130, 5]), (128, 44, 200, [0, 200])])
 @pytest.mark.parametrize("order", ["bhtd", "bthd"])
 def test_fp32_chunks(dk, dv, T, lens, order):
-    """fp32 runs on the matrix cores from 16 tokens on; here a forward that saves nothing."""
+    """fp32 on the matrix cores; here a forward that saves nothing."""
     d = ws.make_delta_desc(1, T, 4, 2, dk, dv, ws.GL_DTYPE_F32, ws.GL_DTYPE_F32)
-    assert ws.delta_path_name(d).startswith("delta-mfma-f32" if T >= 16 else "delta-serial-f32")
+    assert ws.delta_path_name(d).startswith("delta-mfma-f32" if T >= 4 else "delta-serial-f32")
     run_case(dk + T, 1 if lens else 2, 4, 2, T, dk, dv, F32, lens=lens, order=order, saved=False)
 
 
@@ -349,3 +349,11 @@ def test_fp32_long_sequence_gradients():
     """The decay's gradient is a sum over what follows: no error may grow along it."""
     run_case(12, 1, 1, 1, 3000, 16, 16, F32, decay="near1")
     run_case(13, 1, 1, 1, 3000, 16, 16, BF16, gate=F32, decay="near1")
+
+
+@pytest.mark.parametrize("T,lens", [(3, None), (4, None), (15, None), (16, None), (40, [3, 1, 0, 2, 34]),
+                                    (12, [3, 3, 3, 3]), (11, [3, 3, 3, 2])])
+@pytest.mark.parametrize("dtype", [F32, BF16])
+def test_around_the_shortest_chunked_sequences(T, lens, dtype):
+    for saved in (True, False):
+        run_case(T, 1 if lens else 3, 4, 2, T, 64, 64, dtype, lens=lens, saved=saved)

@@ -58,6 +58,7 @@ struct Plan {
   bool packed = false;
   bool chunk = false;                   // the chunked matrix-core path
   bool chunk32 = false;                 // its fp32 form
+  bool brief = false;                   // so short that a forward which saves nothing goes token by token
   int64_t slots = 0;                    // its chunk slots
   int n_seg = 1;                        // segments per sequence of the bf16 forward
   size_t seg_bytes = 0;                 // their first states, then their M
@@ -86,11 +87,13 @@ gls::DeltaArgs base_args(const gl_delta_desc_t* d, const Plan& p) {
   return a;
 }
 
-// Sequences shorter than this (packed: their mean) go token by token, one
-// launch for two.  Forward at 1 x 16 heads of 128, bf16, token by token against
-// chunks: 8 tokens 11 / 16 us, 16 tokens 14 / 16, 32 tokens 20 / 16; backward 28
-// / 22, 41 / 21, 70 / 21.
-constexpr int64_t kChunkFrom = 16;
+// Sequences shorter than this (packed: their mean) go token by token: with one
+// launch instead of two where nothing is saved, and in training where so few
+// tokens leave the chunks' tiles all but empty.  Token by token against chunks,
+// bf16, 8 x 16 heads of 128: forward 8 tokens 13 / 20 us, 16 tokens 17 / 20, 32
+// tokens 27 / 21; backward 4 tokens 52 / 28, 8 tokens 81 / 28 (1 x 16 heads:
+// forward 8 tokens 11 / 16, 16 tokens 14 / 16; backward 4 tokens 21 / 22).
+constexpr int64_t kChunkFrom = 4, kChunkFwdFrom = 16;
 
 // Segments of the chunked bf16 forward.  n of them take two passes of 1 / n of the
 // chunks each plus some 2 us a segment to join them, and need n times the
@@ -140,7 +143,9 @@ gl_status_t make_plan(const gl_delta_desc_t* d, Plan* p) {
   p->align = p->elem;
   const size_t dd = static_cast<size_t>(d->dk) * d->dv;
   const gls::DeltaArgs a = base_args(d, *p);
-  const bool chunks = !(d->flags & GL_FLAG_GENERIC) && d->T >= kChunkFrom * (p->packed ? p->N : 1);
+  const int64_t shared = p->packed ? p->N : 1;  // sequences that share T tokens
+  const bool chunks = !(d->flags & GL_FLAG_GENERIC) && d->T >= kChunkFrom * shared;
+  p->brief = d->T < kChunkFwdFrom * shared;
   if (chunks && gls::delta_chunk_ok(p->io, a)) {
     p->chunk = true;
     p->align = 16;
@@ -316,12 +321,13 @@ gl_status_t gl_delta_fwd(const gl_delta_desc_t* desc, const void* q, const void*
   gls::DeltaArgs a = base_args(desc, p);
   a.q = q; a.k = k; a.v = v; a.la = log_alpha; a.be = beta;
   a.state_in = state_in; a.cu = cu_seqlens; a.y = y; a.state_out = state_out; a.ckpt = saved;
-  if (p.chunk) {
+  const bool serial = p.brief && !saved;
+  if (p.chunk && !serial) {
     if (p.tok > 0 && !gls::delta_rows_ok(a.sy, a.dv))
       return fail(GL_ERROR_NOT_SUPPORTED, "strides of y: multiples of 8, rows apart");
     return chunk_fwd(chunk_args(a, p, saved, ws), static_cast<hipStream_t>(stream));
   }
-  if (p.chunk32) {
+  if (p.chunk32 && !serial) {
     const bool fits = !(misaligned(q) || misaligned(k) || misaligned(y)) && gls::delta_rows_f32_ok(a.sy, a.dv);
     if (saved && !fits)
       return fail(misaligned(q) || misaligned(k) || misaligned(y) ? GL_ERROR_MISALIGNED : GL_ERROR_NOT_SUPPORTED,
