@@ -30,6 +30,11 @@ as for the main line.
 With --qkv it prints the line of the transpose read z_t = (W0 + D_t)^T u_t
 (gl_scan_qkv_fwd with q = u, k = g, v = x, W0 transposed) on the named
 workload, caches flushed between steps; its roofline is the vector ALU.
+
+With --delta it prints the line of a training step of the gated delta rule at
+the named workload's sizes ([B,H,T,dk = d_in,dv = d_out], as many key heads):
+norms and rotation of queries and keys, the rule's forward and backward, the
+norms' backward, each timed by itself, caches flushed between steps.
 """
 from __future__ import annotations
 
@@ -724,6 +729,87 @@ def qkv_main(args, w):
     print(json.dumps(rec), flush=True)
 
 
+def delta_main(args, w):
+    """Training step of the gated delta rule with the norms and the rotation of
+    its queries and keys (seeded N(0, 1) rows, log_alpha = logsigmoid(4 + n),
+    beta = sigmoid(n))."""
+    import torch
+
+    import weight_scans_amd as ws
+
+    dev = torch.device("cuda:0")
+    torch.cuda.set_device(dev)
+    tio = {"f64": torch.float64, "f32": torch.float32, "bf16": torch.bfloat16}[w.dtype]
+    gen = torch.Generator(device=dev).manual_seed(w.seed)
+    draw = lambda *s: torch.randn(s, generator=gen, device=dev, dtype=torch.float32)  # noqa: E731
+    q, k = (draw(w.B, w.H, w.T, w.d_in).to(tio) for _ in range(2))
+    v, dy = (draw(w.B, w.H, w.T, w.d_out).to(tio) for _ in range(2))
+    la = torch.nn.functional.logsigmoid(4 + draw(w.B, w.H, w.T)).to(tio)
+    be = torch.sigmoid(draw(w.B, w.H, w.T)).to(tio)
+    wq, wk = ((1 + 0.1 * draw(w.d_in)).to(tio) for _ in range(2))
+    angle = torch.arange(w.T, device=dev)[:, None] / 1e4 ** (torch.arange(0, w.d_in, 2, device=dev) / w.d_in)
+    table = ws.gate_dtype(tio)
+    cos, sin = angle.cos().to(table), angle.sin().to(table)
+    flags = ws.GL_FLAG_GENERIC if args.generic else 0
+    opts = dict(q_scale=w.d_in ** -0.5, k_scale=w.d_in ** -0.5)
+    flush = torch.ones(1 << 28, dtype=torch.float32, device=dev)
+    # the plain copy of known size that calibrates FETCH_SIZE / WRITE_SIZE
+    calib_src = torch.ones(64 << 20, dtype=torch.float32, device=dev)
+    calib_dst = torch.empty_like(calib_src)
+    torch.neg(calib_src, out=calib_dst)  # 256 MiB in, 256 MiB out
+    torch.cuda.synchronize()
+    del calib_src, calib_dst
+    stream = torch.cuda.current_stream(dev)
+    names = ("qk_norm_fwd", "delta_fwd", "delta_bwd", "qk_norm_bwd")
+
+    def step(mark):
+        mark(0)
+        qn, kn = ws.gl_qknorm_rope_fwd(q, k, wq, wk, cos, sin, **opts)
+        mark(1)
+        _, _, saved = ws.gl_delta_fwd(qn, kn, v, la, be, scale=1.0, save=True, flags=flags, segments=args.segments)
+        mark(2)
+        dq, dk, _, _, _, _ = ws.gl_delta_bwd(qn, kn, v, la, be, dy, saved, scale=1.0, flags=flags,
+                                             segments=args.segments)
+        mark(3)
+        ws.gl_qknorm_rope_bwd(q, k, wq, wk, cos, sin, dq, dk, **opts)
+        mark(4)
+
+    for _ in range(args.warmup):
+        if not args.no_flush:
+            flush_sink = torch.sum(flush)  # noqa: F841
+        step(lambda i: None)
+    ev = timing_events(args.steps, 5, stream)
+    for row in ev:
+        if not args.no_flush:
+            flush_sink = torch.sum(flush)  # noqa: F841
+        step(lambda i: row[i].record(stream))
+    torch.cuda.synchronize()
+    each = {n: [row[i].elapsed_time(row[i + 1]) for row in ev] for i, n in enumerate(names)}
+    ms = sum(row[0].elapsed_time(row[4]) for row in ev) / len(ev)
+    # algorithmic bytes of a token-head: the norms read and write q and k, then
+    # read dq, dk and q, k and write dq, dk; the rule reads q, k, v and writes y,
+    # then reads q, k, v, dy and writes dq, dk, dv; gates and their gradients
+    e = {"bf16": 2, "f32": 4, "f64": 8}[w.dtype]
+    nbytes = w.B * w.H * w.T * (e * (4 * w.d_in + 6 * w.d_in + 2 * w.d_in + 2 * w.d_out + 4 * w.d_in + 3 * w.d_out)
+                                + 6 * e)
+    desc = ws.make_delta_desc(w.B, w.T, w.H, w.H, w.d_in, w.d_out, {"f64": 0, "f32": 1, "bf16": 2}[w.dtype],
+                              {"f64": 0, "f32": 1, "bf16": 2}[w.dtype], flags=flags)
+    achieved = nbytes / 1e9 / (ms / 1e3)
+    print(json.dumps({
+        "metric": "tokens/s (gated delta rule, training step)", "value": w.B * w.T / (ms / 1e3), "unit": "tokens/s",
+        "n_gpus": 1, "steps": args.steps, "warmup": args.warmup, "ms_per_step": ms, "higher_is_better": True,
+        "scaling": "weak", "vs_baseline": None,
+        "dtype": {"bf16": "bf16 io / fp32 state", "f32": "f32", "f64": "f64"}[w.dtype], "data": "synthetic (seeded)",
+        "config": {"workload": f"{w.name}: [B,H,T,dk,dv]=[{w.B},{w.H},{w.T},{w.d_in},{w.d_out}] {w.dtype}, "
+                               "gated delta rule", "kernels": ws.delta_path_name(desc), "parallelism": "single GPU"},
+        "passes_ms": {n: {"mean": sum(x) / len(x), "median": statistics.median(x), "min": min(x), "max": max(x)}
+                      for n, x in each.items()},
+        "roofline": {"bound": "hbm", "achieved": achieved, "peak": PEAK_HBM / 1e9, "unit": "GB/s",
+                     "frac": achieved / (PEAK_HBM / 1e9), "traffic": None, "algorithmic_bytes": nbytes,
+                     "kernel": "whole step"},
+    }), flush=True)
+
+
 def main():
     ap = argparse.ArgumentParser()
     ap.add_argument("--gpus", type=int, default=1)
@@ -741,6 +827,8 @@ def main():
                     help="time Picard sweeps (forward scan + costate reconstruction)")
     ap.add_argument("--decode", action="store_true",
                     help="time one-token decode steps (readout + update) instead of the scan")
+    ap.add_argument("--delta", action="store_true",
+                    help="time a training step of the gated delta rule with its query / key norms")
     ap.add_argument("--segments", type=int, default=0,
                     help="segments per sequence (0 = the library's automatic choice)")
     args = ap.parse_args()
@@ -764,6 +852,8 @@ def main():
         return qkv_main(args, w)
     if args.qkv_bwd:
         return qkv_bwd_main(args, w)
+    if args.delta:
+        return delta_main(args, w)
     dev = torch.device("cuda:0")
     torch.cuda.set_device(dev)
     tio = {"f64": torch.float64, "f32": torch.float32, "bf16": torch.bfloat16}[w.dtype]
