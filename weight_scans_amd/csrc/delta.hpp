@@ -88,8 +88,7 @@ hipError_t launch_delta_step(int io, const DeltaArgs& a, hipStream_t s);
 // leaves, as fragments of 64 lanes x 8 bf16 in the order in which the
 // recurrences use them:
 //   yf   Y  = (I + L beta)^-1 L, rows i     [6 blocks][hi, lo]
-//   pf   P  = scale (decayed q_i.k_j), rows i   [6][hi, lo]
-//   ytf, ptf   the same with rows j         [6][hi, lo] each (training)
+//   ytf, ptf   Y and P = scale (decayed q_i.k_j) with rows j   [6][hi, lo] each (training)
 // and gates [9][64] fp32: e^l, beta, e^(l_C - l), the cumulative log2 decay l in
 // two parts (whole and fraction), and the decay between blocks of 16 tokens as
 // a product of two factors <= 1, with m_x the l before block x: e^(l_i - m_x)
@@ -112,7 +111,6 @@ constexpr int kY32 = 10 * 256;                   // fp32 per record
 struct ChunkArgs {
   DeltaArgs a;
   uint16_t* yf = nullptr;
-  uint16_t* pf = nullptr;
   uint16_t* ytf = nullptr;
   uint16_t* ptf = nullptr;
   float* gates = nullptr;

@@ -158,7 +158,7 @@ gl_status_t make_plan(const gl_delta_desc_t* d, Plan* p) {
     p->n_seg = segments_of(d, *p);
     const size_t segs = p->n_seg > 1 ? static_cast<size_t>(p->N) * d->H * p->n_seg : 0;
     p->seg_bytes = round_up(segs * dd * 4);
-    p->fwd_ws = 2 * round_up(rec * gls::kYf * 2) + p->seg_bytes + round_up(segs * d->dk * d->dk * 4);
+    p->fwd_ws = round_up(rec * gls::kYf * 2) + p->seg_bytes + round_up(segs * d->dk * d->dk * 4);
     p->state_bytes = round_up(rec * gls::delta_row_tiles(a.dv) * (gls::delta_wide(a.dk) / 16) * gls::kPiece * 2);
     p->err_bytes = round_up(rec * 4 * gls::delta_row_tiles(a.dv) * gls::kPiece * 2);
     p->gate_bytes = round_up(rec * gls::kGates * 4);
@@ -220,7 +220,6 @@ gls::ChunkArgs chunk_args(const gls::DeltaArgs& a, const Plan& p, void* saved, v
   Cut w{static_cast<char*>(ws)};
   if (ws) {
     w.take(c.yf, rec * gls::kYf * 2);
-    w.take(c.pf, rec * gls::kYf * 2);
     c.n_seg = p.n_seg;
     w.take(c.seg_s, p.seg_bytes);
     w.take(c.seg_m, p.n_seg > 1 ? static_cast<size_t>(p.N) * a.H * p.n_seg * a.dk * a.dk * 4 : 0);

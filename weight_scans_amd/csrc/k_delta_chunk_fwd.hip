@@ -35,8 +35,9 @@ struct FwdLds {
   static constexpr int NS = DK / 32, VW = 16 * NW, OUT = MODE != STATES;
   alignas(16) char k[3][64 * DK * 2];
   alignas(16) char q[OUT ? 3 : 1][OUT ? 64 * DK * 2 : 16];
-  alignas(16) char v[3][64 * VW * 2];
-  alignas(16) float gt[3][192];
+  alignas(16) char v[2][64 * VW * 2];
+  alignas(16) float gt[2][192];
+  alignas(16) float fo[2][OUT ? 384 : 4];  // the decay's factors for P, [6][64]
   alignas(16) uint16_t sx[2][NW][OUT ? 2 * NS * kFrag : 8];  // hi, then lo
   alignas(16) uint16_t ux[2][NW][OUT ? 4 * kFrag : 8];
 };
@@ -78,8 +79,8 @@ __global__ __launch_bounds__((kFwdThreads<NW, MODE>)) void delta_chunk_fwd(Chunk
   }
   const int64_t rec0 = slot0 * a.H + h;
 
-  if (wave == LOADER) {  // ---- loads: K, V and gates, two chunks ahead
-    constexpr int NK = DK / 8, NV = VW / 8, PER = NK + NV + 3;
+  if (wave == LOADER) {  // ---- loads: K two chunks ahead, V and gates one
+    constexpr int NK = DK / 8, NV = VW / 8;
     const uint16_t* kp = static_cast<const uint16_t*>(a.k) + sr.b * a.sk.b + hk * a.sk.h + sr.t0 * a.sk.t;
     const uint16_t* vp = static_cast<const uint16_t*>(a.v) + sr.b * a.sv.b + h * a.sv.h + sr.t0 * a.sv.t + r0;
     uint32_t ko[NK], vo[NV];
@@ -87,31 +88,34 @@ __global__ __launch_bounds__((kFwdThreads<NW, MODE>)) void delta_chunk_fwd(Chunk
     for (int i = 0; i < NK; ++i) ko[i] = tile_off<DK>(i, lane, a.sk.t, 0, a.dk);
 #pragma unroll
     for (int i = 0; i < NV; ++i) vo[i] = tile_off<VW>(i, lane, a.sv.t, 0, a.dv - r0);
-    const auto issue = [&](int c) {
+    const auto issue_k = [&](int c) {
+      const __amdgpu_buffer_rsrc_t rk = rows_rsrc(kp, c * 64LL, c < nc ? sr.len : 0, a.sk.t, a.dk);
+#pragma unroll
+      for (int i = 0; i < NK; ++i) dma16(rk, ko[i], lds.k[c % 3] + i * 1024);
+    };
+    const auto issue_v = [&](int c) {
       const bool in = c < nc;
-      const int s = c % 3;
-      const __amdgpu_buffer_rsrc_t rk = rows_rsrc(kp, c * 64LL, in ? sr.len : 0, a.sk.t, a.dk);
       const __amdgpu_buffer_rsrc_t rv = rows_rsrc(vp, c * 64LL, in && !ident ? sr.len : 0, a.sv.t, min(VW, a.dv - r0));
       const __amdgpu_buffer_rsrc_t rg =
           buffer_rsrc(ca.gates + (in ? (rec0 + static_cast<int64_t>(c) * a.H) * kGates : 0), in ? 768 : 0);
 #pragma unroll
-      for (int i = 0; i < NK; ++i) dma16(rk, ko[i], lds.k[s] + i * 1024);
+      for (int i = 0; i < NV; ++i) dma16(rv, vo[i], lds.v[c & 1] + i * 1024);
 #pragma unroll
-      for (int i = 0; i < NV; ++i) dma16(rv, vo[i], lds.v[s] + i * 1024);
-#pragma unroll
-      for (int i = 0; i < 3; ++i) dma4(rg, (i * 64 + lane) * 4, lds.gt[s] + i * 64);
+      for (int i = 0; i < 3; ++i) dma4(rg, (i * 64 + lane) * 4, lds.gt[c & 1] + i * 64);
     };
-    issue(0);
-    issue(1);
+    issue_v(0);
+    issue_k(0);
+    issue_k(1);
     for (int c = 0; c <= nc; ++c) {
-      wait_vm<PER>();  // chunk c is there, c + 1 in flight
+      wait_vm<NK>();  // chunk c is there, K of c + 1 in flight
       lds_barrier();
-      issue(c + 2);    // into the slot of chunk c - 1
+      issue_v(c + 1);  // into the slots of chunk c - 1
+      issue_k(c + 2);
     }
     wait_vm<0>();
     return;
   }
-  if (OUT && wave == LOADER + 1) {  // ---- loads: Q, used one step later
+  if (OUT && wave == LOADER + 1) {  // ---- loads: Q, two chunks ahead
     constexpr int NK = DK / 8;
     const uint16_t* qp = static_cast<const uint16_t*>(a.q) + sr.b * a.sq.b + hk * a.sq.h + sr.t0 * a.sq.t;
     uint32_t qo[NK];
@@ -122,13 +126,57 @@ __global__ __launch_bounds__((kFwdThreads<NW, MODE>)) void delta_chunk_fwd(Chunk
 #pragma unroll
       for (int i = 0; i < NK; ++i) dma16(rq, qo[i], lds.q[c % 3] + i * 1024);
     };
+    // Factors of the decay (lane = token, m_x the l before its block x of 16):
+    // scale e^(l_i - m_x) of block x's own tokens, e^(m_x - l_j) of those before
+    // it for x = 1, 2, 3, and l in its two parts for the diagonal blocks
+    const float sc = static_cast<float>(a.scale);
+    float lw = 0.f, lf = 0.f;
+    const auto fetch = [&](int c) {
+      const float* gt = ca.gates + (rec0 + static_cast<int64_t>(c) * a.H) * kGates;
+      lw = gt[192 + lane];
+      lf = gt[256 + lane];
+    };
+    const auto factors = [&](int c) {
+      float* fo = lds.fo[c & 1] + lane;
+      fo[256] = lw;
+      fo[320] = lf;
+      float own = 0.f;
+#pragma unroll
+      for (int x = 1; x < 4; ++x) {
+        const float dw = lw - readlane_f(lw, 16 * x - 1), df = lf - readlane_f(lf, 16 * x - 1);
+        const float e = fexp2(g == x ? dw + df : lane < 16 * x ? -dw - df : -200.f);
+        fo[64 * x] = e;
+        own = g == x ? sc * e : own;
+      }
+      fo[0] = own;
+    };
+    if (nc > 0) fetch(0);
     issue(0);
-    lds_barrier();
     issue(1);
-    for (int c = 0; c < nc; ++c) {
-      wait_vm<NK>();   // chunk c is there, c + 1 in flight
-      lds_barrier();   // step c + 1: the output waves take chunk c
-      issue(c + 2);    // into the slot of chunk c - 1
+    if (nc > 0) factors(0);
+    // Training: this wave also keeps the states (it has the time), two row tiles
+    // of the chunk before
+    constexpr int ST = SAVE ? NW * NB / 2 : 0;
+    const int n_rt = delta_row_tiles(a.dv);
+    const auto keep = [&](int c) {
+      uint16_t* to = ca.sf + ((rec0 + static_cast<int64_t>(c) * a.H) * n_rt + tile * NW) * NB * kPiece + lane * 8;
+#pragma unroll
+      for (int w = 0; w < NW; ++w)
+#pragma unroll
+        for (int b = 0; b < NB; b += 2)
+          *reinterpret_cast<bf16x8*>(to + (w * NB + b) * kPiece) =
+              join(turned(lds.sx[c & 1][w], b, lane), turned(lds.sx[c & 1][w], b + 1, lane));
+    };
+    for (int c = 0; c <= nc; ++c) {
+      // chunk c is there; newer are the loads of c + 1 and the stores of c - 2
+      if (SAVE && c >= 2) wait_vm<NK + ST>();
+      else wait_vm<NK>();
+      lds_barrier();
+      if (c + 1 < nc) fetch(c + 1);  // before the loads that need not be waited for
+      issue(c + 2);                  // into the slot of chunk c - 1
+      if (c + 1 < nc) factors(c + 1);
+      if constexpr (SAVE)
+        if (c > 0) keep(c - 1);
     }
     wait_vm<0>();
     return;
@@ -141,21 +189,60 @@ __global__ __launch_bounds__((kFwdThreads<NW, MODE>)) void delta_chunk_fwd(Chunk
     uint16_t* yp = static_cast<uint16_t*>(a.y) + sr.b * a.sy.b + h * a.sy.h + sr.t0 * a.sy.t + rr;
     const float sc = static_cast<float>(a.scale);
     const int rt = tile * NW + w, n_rt = delta_row_tiles(a.dv);
-    bf16x8 pf[12];
+    // P and Q of the chunk, formed and read in its own step, used in the next
+    Pair8 pf[6];
+    bf16x8 qf[4][NS];
     float gs[4];
-    const auto fetch = [&](int c) {
-      const int64_t rec = rec0 + static_cast<int64_t>(c) * a.H;
+    const auto scores = [&](int c) {
+      const char* qt = lds.q[c % 3];
+      const char* kt = lds.k[c % 3];
+      const float* fo = lds.fo[c & 1];
+      const auto row = [&](int at) { return *reinterpret_cast<const f32x4*>(fo + at + 4 * g); };
 #pragma unroll
-      for (int f = 0; f < 12; ++f)
-        pf[f] = *reinterpret_cast<const bf16x8*>(ca.pf + rec * kYf + f * kFrag + lane * 8);
+      for (int x = 0; x < 4; ++x) gs[x] = sc * lds.gt[c & 1][16 * x + l];
 #pragma unroll
-      for (int tb = 0; tb < 4; ++tb) gs[tb] = ca.gates[rec * kGates + 16 * tb + l];
+      for (int tb = 0; tb < 4; ++tb)
+#pragma unroll
+        for (int s = 0; s < NS; ++s) qf[tb][s] = frag_n<DK>(qt, tk, tb, s);
+#pragma unroll
+      for (int jp = 0; jp < 2; ++jp) {
+        bf16x8 kf[2][NS];
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
+#pragma unroll
+          for (int s = 0; s < NS; ++s) kf[h][s] = frag_n<DK>(kt, tk, 2 * jp + h, s);
+#pragma unroll
+        for (int tb = 2 * jp; tb < 4; ++tb) {
+          f32x4 p[2];
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            const int j = 2 * jp + h;
+            p[h] = zero4();
+            if (j > tb) continue;
+#pragma unroll
+            for (int s = 0; s < NS; ++s) p[h] = mfma16x16x32(kf[h][s], qf[tb][s], p[h]);
+            if (j < tb) {
+              const f32x4 f = row(64 * tb + 16 * j) * fo[16 * tb + l];
+#pragma unroll
+              for (int q = 0; q < 4; ++q) p[h][q] *= f[q];
+            } else {
+              const f32x4 rw = row(256 + 16 * tb), rf = row(320 + 16 * tb);
+              const float lw = fo[256 + 16 * tb + l], lf = fo[320 + 16 * tb + l];
+#pragma unroll
+              for (int q = 0; q < 4; ++q) {
+                const float d = sc * fexp2((lw - rw[q]) + (lf - rf[q]));
+                p[h][q] = 4 * g + q <= l ? p[h][q] * d : 0.f;
+              }
+            }
+          }
+          pf[tb < 2 ? tb : 2 * tb - 2 + jp] = split8(p[0], p[1]);
+        }
+      }
     };
-    if (nc > 0) fetch(0);
     lds_barrier();
+    if (nc > 0) scores(0);
     for (int c = 0; c < nc; ++c) {
       lds_barrier();
-      const char* qt = lds.q[c % 3];
       const uint16_t* sx = lds.sx[c & 1][w];
       const uint16_t* ux = lds.ux[c & 1][w];
       f32x4 o[4];
@@ -167,16 +254,14 @@ __global__ __launch_bounds__((kFwdThreads<NW, MODE>)) void delta_chunk_fwd(Chunk
         const bf16x8 sl = *reinterpret_cast<const bf16x8*>(sx + (NS + s) * kFrag + lane * 8);
 #pragma unroll
         for (int tb = 0; tb < 4; ++tb) {
-          const bf16x8 qf = frag_n<DK>(qt, tk, tb, s);
-          o[tb] = mfma16x16x32(sl, qf, o[tb]);
-          o[tb] = mfma16x16x32(sh, qf, o[tb]);
+          o[tb] = mfma16x16x32(sl, qf[tb][s], o[tb]);
+          o[tb] = mfma16x16x32(sh, qf[tb][s], o[tb]);
         }
       }
 #pragma unroll
       for (int tb = 0; tb < 4; ++tb) {
-        const float f = sc * gs[tb];
 #pragma unroll
-        for (int q = 0; q < 4; ++q) o[tb][q] *= f;
+        for (int q = 0; q < 4; ++q) o[tb][q] *= gs[tb];
       }
 #pragma unroll
       for (int s = 0; s < 2; ++s) {
@@ -185,18 +270,13 @@ __global__ __launch_bounds__((kFwdThreads<NW, MODE>)) void delta_chunk_fwd(Chunk
 #pragma unroll
         for (int tb = 2 * s; tb < 4; ++tb) {
           const int f = tb < 2 ? tb : 2 * tb - 2 + s;
-          o[tb] = mfma16x16x32(uh, pf[2 * f + 1], o[tb]);
-          o[tb] = mfma16x16x32(ul, pf[2 * f], o[tb]);
-          o[tb] = mfma16x16x32(uh, pf[2 * f], o[tb]);
+          o[tb] = mfma16x16x32(uh, pf[f].lo, o[tb]);
+          o[tb] = mfma16x16x32(ul, pf[f].hi, o[tb]);
+          o[tb] = mfma16x16x32(uh, pf[f].hi, o[tb]);
         }
       }
-      fetch(min(c + 1, nc - 1));
       if constexpr (SAVE) {
         const int64_t rec = rec0 + static_cast<int64_t>(c) * a.H;
-#pragma unroll
-        for (int b = 0; b < NB; b += 2)
-          *reinterpret_cast<bf16x8*>(ca.sf + ((rec * n_rt + rt) * NB + b) * kPiece + lane * 8) =
-              join(turned(sx, b, lane), turned(sx, b + 1, lane));
 #pragma unroll
         for (int tb = 0; tb < 4; ++tb)
           *reinterpret_cast<f32x4*>(ca.yb + ((rec * n_rt + rt) * 4 + tb) * 256 + lane * 4) = o[tb];
@@ -207,6 +287,7 @@ __global__ __launch_bounds__((kFwdThreads<NW, MODE>)) void delta_chunk_fwd(Chunk
         if (a.y && t < sr.len && rr < a.dv)
           *reinterpret_cast<uint2*>(yp + t * a.sy.t) = make_uint2(pack2(o[tb][0], o[tb][1]), pack2(o[tb][2], o[tb][3]));
       }
+      if (c + 1 < nc) scores(c + 1);
     }
     return;
   }
@@ -242,7 +323,7 @@ __global__ __launch_bounds__((kFwdThreads<NW, MODE>)) void delta_chunk_fwd(Chunk
     lds_barrier();
     const int sl = c % 3;
     const char* kt = lds.k[sl];
-    const float* gt = lds.gt[sl] + 4 * g;
+    const float* gt = lds.gt[c & 1] + 4 * g;
     const auto gate = [&](int m, int tb) { return *reinterpret_cast<const f32x4*>(gt + 64 * m + 16 * tb); };
     // the next chunk's Y, fetched as this one's is used up
     yp += (c + 1 < nc ? static_cast<int64_t>(a.H) : 0) * kYf;
@@ -335,9 +416,9 @@ __global__ __launch_bounds__((kFwdThreads<NW, MODE>)) void delta_chunk_fwd(Chunk
       gm[tb] = gate(0, tb);
       be[tb] = gate(1, tb);
       rs[tb] = gate(2, tb);
-      vv[tb] = col4<VW>(lds.v[sl], tv, tb, wave);
+      vv[tb] = col4<VW>(lds.v[c & 1], tv, tb, wave);
     }
-    const float whole = lds.gt[sl][63];
+    const float whole = lds.gt[c & 1][63];
     ks(0);
     if constexpr (OUT) {
 #pragma unroll

@@ -41,8 +41,8 @@ __global__ __launch_bounds__(kThreads, 3) void delta_prep(ChunkArgs ca) {
   const uint16_t* kp = static_cast<const uint16_t*>(a.k) + sr.b * a.sk.b + hk * a.sk.h + (sr.t0 + t0) * a.sk.t;
   const uint16_t* qp = static_cast<const uint16_t*>(a.q) + sr.b * a.sq.b + hk * a.sq.h + (sr.t0 + t0) * a.sq.t;
   // rows past the chunk's end and columns past dk read as zeros
-  // Row blocks 0 .. w of K, then w .. 3 of Q (those past w for training only):
-  // all that the wave multiplies
+  // Row blocks 0 .. w of K, then w .. 3 of Q (training only): all that the wave
+  // multiplies
   bf16x8 m[5][NS];
   uint32_t at[NS];
 #pragma unroll
@@ -52,7 +52,7 @@ __global__ __launch_bounds__(kThreads, 3) void delta_prep(ChunkArgs ca) {
   }
 #pragma unroll
   for (int i = 0; i < 5; ++i) {
-    const bool k = i <= w, in = i <= w + 1 || ca.ptf;
+    const bool k = i <= w, in = k || ca.ptf;
     const __amdgpu_buffer_rsrc_t r = buffer_rsrc(
         k ? kp : qp, in ? static_cast<int>(((nt - 1) * (k ? a.sk.t : a.sq.t) + a.dk) * 2) : 0);
     const uint32_t o = (16 * (k ? i : i - 1) + l) * static_cast<uint32_t>(k ? a.sk.t : a.sq.t) * 2;
@@ -76,33 +76,25 @@ __global__ __launch_bounds__(kThreads, 3) void delta_prep(ChunkArgs ca) {
     put(dst + (2 * f) * kFrag, p.hi);
     put(dst + (2 * f + 1) * kFrag, p.lo);
   };
-  // L: row block w, in both orientations.  P: row block w (rows i in lanes), and
-  // for training column block w (rows j in lanes).
+  // L: row block w, in both orientations; for training P's column block w (rows j
+  // in lanes)
   const float sc = static_cast<float>(a.scale);
 #pragma unroll
   for (int wc = 0; wc < 4; ++wc) {
     if (wc != w) continue;
     const auto& kw = m[wc];
-    const auto& qw = m[wc + 1];
-    f32x4 p[4];
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      p[j] = zero4();
-      if (j > wc) continue;
+    for (int j = 0; j <= wc; ++j) {
       f32x4 x = zero4(), xt = zero4();
 #pragma unroll
       for (int c = 0; c < NS; ++c) {
         x = mfma16x16x32(kw[c], m[j][c], x);
         xt = mfma16x16x32(m[j][c], kw[c], xt);
-        p[j] = mfma16x16x32(m[j][c], qw[c], p[j]);
       }
       put_scores(s, wc, j, x, xt, lane);
-#pragma unroll
-      for (int q = 0; q < 4; ++q) p[j][q] *= sc * s.decay(16 * wc + l, 16 * j + 4 * g + q, false);
     }
-#pragma unroll
-    for (int c = 0; c <= wc / 2; ++c) put2(ca.pf + rec * kYf, wc < 2 ? wc : 2 * wc - 2 + c, p[2 * c], p[2 * c + 1]);
     if (ca.ptf) {
+      f32x4 p[4];
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
         p[i] = zero4();
