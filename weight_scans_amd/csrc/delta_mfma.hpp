@@ -191,6 +191,34 @@ __device__ __forceinline__ float load4(__amdgpu_buffer_rsrc_t r, uint32_t off) {
   return __builtin_bit_cast(float, __builtin_amdgcn_raw_buffer_load_b32(r, off, 0, 0));
 }
 
+// Factors of the decay inside a chunk for the waves that form P (lane = token,
+// m_x the l before its block x of 16), by a loading wave into [6][64] of LDS:
+// scale e^(l_i - m_x) of block x's own tokens; e^(m_x - l_j) of those before it
+// for x = 1, 2, 3; and l in its two parts for the diagonal blocks.
+struct DecayFactors {
+  float scale, lw, lf;
+  int lane;
+  __device__ __forceinline__ DecayFactors(float s, int ln) : scale(s), lw(0.f), lf(0.f), lane(ln) {}
+  __device__ __forceinline__ void fetch(const float* gates) {
+    lw = gates[192 + lane];
+    lf = gates[256 + lane];
+  }
+  __device__ __forceinline__ void put(float* lds) const {
+    const int g = lane >> 4;
+    lds[256 + lane] = lw;
+    lds[320 + lane] = lf;
+    float own = 0.f;
+#pragma unroll
+    for (int x = 1; x < 4; ++x) {
+      const float dw = lw - readlane_f(lw, 16 * x - 1), df = lf - readlane_f(lf, 16 * x - 1);
+      const float e = fexp2(g == x ? dw + df : lane < 16 * x ? -dw - df : -200.f);
+      lds[64 * x + lane] = e;
+      own = g == x ? scale * e : own;
+    }
+    lds[lane] = own;
+  }
+};
+
 // Work-groups are dealt to the 8 XCDs in turn: all `tiles` of a sequence-head
 // get the same XCD (they share its chunks through the XCD's L2).  Returns
 // false past the end.

@@ -126,34 +126,12 @@ __global__ __launch_bounds__((kFwdThreads<NW, MODE>)) void delta_chunk_fwd(Chunk
 #pragma unroll
       for (int i = 0; i < NK; ++i) dma16(rq, qo[i], lds.q[c % 3] + i * 1024);
     };
-    // Factors of the decay (lane = token, m_x the l before its block x of 16):
-    // scale e^(l_i - m_x) of block x's own tokens, e^(m_x - l_j) of those before
-    // it for x = 1, 2, 3, and l in its two parts for the diagonal blocks
-    const float sc = static_cast<float>(a.scale);
-    float lw = 0.f, lf = 0.f;
-    const auto fetch = [&](int c) {
-      const float* gt = ca.gates + (rec0 + static_cast<int64_t>(c) * a.H) * kGates;
-      lw = gt[192 + lane];
-      lf = gt[256 + lane];
-    };
-    const auto factors = [&](int c) {
-      float* fo = lds.fo[c & 1] + lane;
-      fo[256] = lw;
-      fo[320] = lf;
-      float own = 0.f;
-#pragma unroll
-      for (int x = 1; x < 4; ++x) {
-        const float dw = lw - readlane_f(lw, 16 * x - 1), df = lf - readlane_f(lf, 16 * x - 1);
-        const float e = fexp2(g == x ? dw + df : lane < 16 * x ? -dw - df : -200.f);
-        fo[64 * x] = e;
-        own = g == x ? sc * e : own;
-      }
-      fo[0] = own;
-    };
-    if (nc > 0) fetch(0);
+    const auto gates = [&](int c) { return ca.gates + (rec0 + static_cast<int64_t>(c) * a.H) * kGates; };
+    DecayFactors df(static_cast<float>(a.scale), lane);
+    if (nc > 0) df.fetch(gates(0));
     issue(0);
     issue(1);
-    if (nc > 0) factors(0);
+    if (nc > 0) df.put(lds.fo[0]);
     // Training: this wave also keeps the states (it has the time), two row tiles
     // of the chunk before
     constexpr int ST = SAVE ? NW * NB / 2 : 0;
@@ -172,9 +150,9 @@ __global__ __launch_bounds__((kFwdThreads<NW, MODE>)) void delta_chunk_fwd(Chunk
       if (SAVE && c >= 2) wait_vm<NK + ST>();
       else wait_vm<NK>();
       lds_barrier();
-      if (c + 1 < nc) fetch(c + 1);  // before the loads that need not be waited for
-      issue(c + 2);                  // into the slot of chunk c - 1
-      if (c + 1 < nc) factors(c + 1);
+      if (c + 1 < nc) df.fetch(gates(c + 1));  // before the loads that need not be waited for
+      issue(c + 2);                            // into the slot of chunk c - 1
+      if (c + 1 < nc) df.put(lds.fo[(c + 1) & 1]);
       if constexpr (SAVE)
         if (c > 0) keep(c - 1);
     }
