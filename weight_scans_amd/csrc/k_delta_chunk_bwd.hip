@@ -7,7 +7,11 @@
 //
 // is again a recurrence of independent rows (delta_chunk_rev, the mirror of the
 // forward kernel: state waves with Lam^T in their accumulators; helper waves
-// form the two products with dO one chunk ahead and hand them over in fp32).
+// form the two products with dO one chunk ahead and hand them over in fp32).  As
+// there the chain of a chunk in one wave bounds it, 3.2 us a step at 128 x 128:
+// 4 x 16 x 4096 x 128 takes 205 us (794 MB, 3.9 TB/s), 8 x 16 x 4096 x 64 175 us (829
+// MB, 4.7 TB/s: near what a copy reaches).  P^T is read, not formed here: the
+// helpers would outlast the state waves (252 and 207 us).
 // The rest is one work-group per chunk and key head (delta_chunk_grad):
 //
 //   dq = scale e^l dO S + dP K,              dP_ij = scale D_ij beta_j dO_i.e_j  (j <= i)
@@ -433,7 +437,10 @@ __global__ __launch_bounds__(64 * (2 * NW + 2)) void delta_chunk_rev(ChunkArgs c
 // memory.  Loading a chunk's 160 KB (128 x 128) and multiplying take about as
 // long: dO, e and G are done with before K and Q are needed, which take their
 // place, so that two work-groups fit a CU and one loads while the other
-// multiplies.
+// multiplies.  Bound by HBM: 4 x 16 x 4096 x 128 moves 833 MB in 164 us, 8 x 16 x
+// 4096 x 64 709 MB in 141 us, 5.1 TB/s both, what a large copy reaches.  S, Lam, e
+// and G were rounded once to bf16 by the recurrences (dq, dk: 3e-3 against 1.7e-3 of
+// their own rounding); as two terms each they would add half to that traffic.
 template <int DK, int DV>
 struct GradLds {
   static constexpr int kCols = 64 * DK * 2;

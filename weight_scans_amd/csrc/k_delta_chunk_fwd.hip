@@ -13,7 +13,17 @@
 // A work-group is NW state waves, NW output waves (they get S and U of the
 // chunk before through LDS and form y one chunk behind, so that y is off the
 // chain) and two waves that keep the direct loads of the next two chunks in
-// flight: one barrier per chunk.
+// flight: one barrier per chunk.  The output waves also form the chunk's P, in
+// the step before they use it (with P left in memory by the preparation both took
+// 293 instead of 246 us together, training 8 x 16 x 4096 x 64).
+//
+// Bound by the chain of a chunk's products in one wave (128 x 128: 2.3 us a step,
+// of which its matrix instructions take 0.6; vector work that splits operands
+// stands between them, so nothing else fills the gaps of a SIMD that one wave
+// has), and in training by what is kept for the backward.  Work-groups of 32 rows,
+// two state waves: LDS holds one of them a CU, and 64 rows would leave half the
+// CUs idle at 64 sequence-heads.  4 x 16 x 4096 x 128: 145 us, training 197 us
+// (664 MB, 3.4 TB/s); 8 x 16 x 4096 x 64: 111 us, training 150 us (650 MB, 4.3 TB/s).
 //
 // Few heads and many chunks: the chunks of a sequence are cut into n_seg
 // segments that run at once.  What a segment does to the state is
@@ -21,7 +31,8 @@
 // row by row; a first pass (STATES: no outputs) gets Z as the end of the
 // segment from S = 0 and M as its end from S = I without values, delta_join
 // forms the segments' first states one after another, and the pass over the
-// tokens then starts every segment from its own.
+// tokens then starts every segment from its own.  1 x 16 x 32768 x 128, four
+// segments: 204 us + 8 us + 263 us for the passes, 940 us in one.
 #include "delta_mfma.hpp"
 #include "dev_common.hpp"
 
@@ -464,7 +475,7 @@ __global__ __launch_bounds__((kFwdThreads<NW, MODE>)) void delta_chunk_fwd(Chunk
 // First states of the segments: S_(s+1) = S_s M_s + Z_s, s = 1 .. n_seg - 2, in
 // fp32; Z_s stands where S_(s+1) goes.  A work-group has 16 rows of a head,
 // which stay in LDS between the segments; wave w forms the column blocks w and
-// w + 4 of 16.
+// w + 4 of 16.  Bound by latency: about 2 us a segment.
 template <int DK>
 __global__ __launch_bounds__(256) void delta_join(ChunkArgs ca) {
   const DeltaArgs& a = ca.a;

@@ -5,7 +5,9 @@
 //   dz = scale Rot_p^T(dout);  dw = sum_rows dz * n;
 //   dx = r (w dz - n mean(w dz * n))
 //
-// Bound by reading and writing each row once.  Vector kernels (d and rot
+// Bound by reading and writing each row once: 4 x 4096 tokens of 16 + 8 heads of
+// 128, bf16, forward 201 MB in 43 us (4.7 TB/s), backward 302 MB in 75 us (4.0 TB/s)
+// and 4 us for the sums of dw; a large copy reaches 5.2.  Vector kernels (d and rot
 // multiples of 16): a lane owns 16 columns of a row as two runs of eight that
 // hold whole pairs (run j and the run rot/2 further on, or two neighbouring
 // runs), so that the rotation needs no other lane; d/16 lanes (rounded up to a
