@@ -74,9 +74,10 @@ typedef struct {
   int32_t io_dtype;    /* gl_dtype_t                                            */
   int32_t gate_dtype;  /* the io dtype, or F32 with BF16 io                     */
   uint32_t flags;      /* GL_FLAG_GENERIC: the token-serial vector kernels      */
-  uint32_t segments;   /* BF16 matrix-core forward: parts of a sequence that run
+  uint32_t segments;   /* BF16 matrix-core kernels: parts of a sequence that run
                           at once; 0 = chosen by the number of heads and chunks,
-                          n = n (at most one per chunk); elsewhere not used     */
+                          n = n (at most one per chunk), the same in a forward
+                          and the backward of what it saved; elsewhere not used */
   double scale;        /* of y                                                  */
   gl_strides_t sq, sk, sv, sy, sg;      /* q, k, v, y, log_alpha and beta       */
   gl_strides_t sdq, sdk, sdv, sdy, sdg; /* their gradients (gl_delta_bwd)       */

@@ -125,7 +125,7 @@ def test_sizes():
         assert saved > 0 and f0 >= f1 and b0 >= b1 + saved
     assert ws.delta_saved_size(desc(T=0)) == 0 and ws.delta_saved_size(desc(B=0)) == 0
     # segments: a first state and a transition each
-    one, four = (ws.delta_workspace_size(desc(B=1, T=4096, segments=n), True)[0] for n in (1, 4))
+    one, four = (ws.delta_workspace_size(desc(B=1, T=4096, segments=n), False)[0] for n in (1, 4))
     assert four >= one + 4 * 4 * 2 * 64 * 64 * 4
     # never more than one a chunk, and chosen for few heads and many chunks only
     assert (ws.delta_workspace_size(desc(segments=50, T=128), True)

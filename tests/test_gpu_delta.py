@@ -357,3 +357,9 @@ def test_fp32_long_sequence_gradients():
 def test_around_the_shortest_chunked_sequences(T, lens, dtype):
     for saved in (True, False):
         run_case(T, 1 if lens else 3, 4, 2, T, 64, 64, dtype, lens=lens, saved=saved)
+
+
+@pytest.mark.parametrize("segments", [2, 3, 6])
+def test_segments_without_saved(segments):
+    run_case(70 + segments, 2, 2, 2, 64 * 9 + 7, 64, 64, BF16, gate=F32, saved=False, segments=segments)
+    run_case(80 + segments, 1, 3, 1, 64 * 9 + 7, 128, 96, BF16, with_state=False, segments=segments, decay="base")

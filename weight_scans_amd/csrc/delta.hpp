@@ -135,9 +135,10 @@ struct ChunkArgs {
   uint16_t* lf = nullptr;
   uint16_t* gf = nullptr;
   int64_t slots = 0;    // chunk slots of the call
-  int n_seg = 1;        // forward: segments per sequence
+  int n_seg = 1;        // segments per sequence
   float* seg_s = nullptr;  // [head][n_seg][dv][dk] their first states (from the second on)
   float* seg_m = nullptr;  // [head][n_seg][dk][dk] what they do to a state
+  float* seg_l = nullptr;  // backward: [head][n_seg][dv][dk] their last adjoints (but the last's)
 };
 inline int delta_wide(int d) { return d <= 64 ? 64 : 128; }
 __host__ __device__ inline int delta_row_tiles(int dv) { return (dv + 31) / 32 * 2; }
@@ -146,6 +147,7 @@ bool delta_rows_ok(const Str3& s, int d);         // strides of the other row te
 hipError_t launch_delta_prep(const ChunkArgs& c, hipStream_t s);
 hipError_t launch_delta_chunk_fwd(const ChunkArgs& c, hipStream_t s);
 hipError_t launch_delta_chunk_bwd(const ChunkArgs& c, hipStream_t s);
+hipError_t launch_delta_join(const ChunkArgs& c, bool back, hipStream_t s);
 // The same in fp32 (dk and dv multiples of 4).
 bool delta_chunk_f32_ok(int io, const DeltaArgs& a);  // sizes and strides of q, k, v
 bool delta_rows_f32_ok(const Str3& s, int d);         // strides of the other row tensors

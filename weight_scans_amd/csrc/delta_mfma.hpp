@@ -182,6 +182,18 @@ __device__ __forceinline__ void interleave() {
   __builtin_amdgcn_sched_barrier(0);
 }
 
+// Narrows a sequence to segment seg of n: its tokens, first slot, and number of chunks.
+__device__ __forceinline__ int segment_of(SeqRange& sr, int64_t& slot0, int seg, int n) {
+  const int nc = static_cast<int>((sr.len + kDeltaChunk - 1) / kDeltaChunk);
+  if (n == 1) return nc;
+  const int per = (nc + n - 1) / n, c0 = static_cast<int>(min(static_cast<int64_t>(seg) * per, static_cast<int64_t>(nc)));
+  const int mine = min(per, nc - c0);
+  slot0 += c0;
+  sr.t0 += c0 * static_cast<int64_t>(kDeltaChunk);
+  sr.len = min(sr.len - c0 * static_cast<int64_t>(kDeltaChunk), mine * static_cast<int64_t>(kDeltaChunk));
+  return mine;
+}
+
 // 16- and 4-byte buffer loads, zeros past the end: unlike loads under a
 // condition they draw no branch and no wait of their own.
 __device__ __forceinline__ bf16x8 load16(__amdgpu_buffer_rsrc_t r, uint32_t off) {

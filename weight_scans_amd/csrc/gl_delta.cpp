@@ -61,7 +61,7 @@ struct Plan {
   bool brief = false;                   // so short that a forward which saves nothing goes token by token
   int64_t slots = 0;                    // its chunk slots
   int n_seg = 1;                        // segments per sequence of the bf16 forward
-  size_t seg_bytes = 0;                 // their first states, then their M
+  size_t seg_bytes = 0, m_bytes = 0;    // their first states (last adjoints), their M
   size_t saved = 0, fwd_ws = 0, bwd_ws = 0;  // bwd_ws: with `saved` given
   size_t state_bytes = 0, err_bytes = 0, gate_bytes = 0, y_bytes = 0, last_bytes = 0, z_bytes = 0;
   const char* name = "";
@@ -95,7 +95,7 @@ gls::DeltaArgs base_args(const gl_delta_desc_t* d, const Plan& p) {
 // forward 8 tokens 11 / 16, 16 tokens 14 / 16; backward 4 tokens 21 / 22).
 constexpr int64_t kChunkFrom = 4, kChunkFwdFrom = 16;
 
-// Segments of the chunked bf16 forward.  n of them take two passes of 1 / n of the
+// Segments of the chunked bf16 kernels.  Forward: n of them take two passes of 1 / n of the
 // chunks each plus some 2 us a segment to join them, and need n times the
 // work-groups, of which one fits a CU.  With / without at 16 heads of 128: 32768
 // tokens 543 / 1031 us, 2048 tokens 61 / 74; 4 heads of 64: 32768 tokens 103 / 739,
@@ -161,16 +161,18 @@ gl_status_t make_plan(const gl_delta_desc_t* d, Plan* p) {
     p->n_seg = segments_of(d, *p);
     const size_t segs = p->n_seg > 1 ? static_cast<size_t>(p->N) * d->H * p->n_seg : 0;
     p->seg_bytes = round_up(segs * dd * 4);
-    p->fwd_ws = round_up(rec * gls::kYf * 2) + p->seg_bytes + round_up(segs * d->dk * d->dk * 4);
+    p->m_bytes = round_up(segs * d->dk * d->dk * 4);
+    p->fwd_ws = round_up(rec * gls::kYf * 2);
     p->state_bytes = round_up(rec * gls::delta_row_tiles(a.dv) * (gls::delta_wide(a.dk) / 16) * gls::kPiece * 2);
     p->err_bytes = round_up(rec * 4 * gls::delta_row_tiles(a.dv) * gls::kPiece * 2);
-    p->gate_bytes = round_up(rec * gls::kGates * 4);
+    // what is workspace in a forward that saves nothing
+    p->gate_bytes = round_up(rec * gls::kGates * 4) + p->seg_bytes + p->m_bytes;
     p->y_bytes = round_up(rec * gls::delta_row_tiles(a.dv) * 4096);
     p->last_bytes = round_up(static_cast<size_t>(p->N) * d->H * dd * 4);
     p->z_bytes = round_up(rec * gls::delta_row_tiles(a.dv) * 64 * 4);
     p->saved = p->gate_bytes + 2 * round_up(rec * gls::kYf * 2) + p->state_bytes + p->err_bytes + p->y_bytes +
                p->last_bytes;
-    p->bwd_ws = p->state_bytes + p->err_bytes + 2 * p->z_bytes;
+    p->bwd_ws = p->state_bytes + p->err_bytes + 2 * p->z_bytes + p->seg_bytes;
     return GL_SUCCESS;
   }
   if (chunks && gls::delta_chunk_f32_ok(p->io, a)) {
@@ -223,21 +225,20 @@ gls::ChunkArgs chunk_args(const gls::DeltaArgs& a, const Plan& p, void* saved, v
   Cut w{static_cast<char*>(ws)};
   if (ws) {
     w.take(c.yf, rec * gls::kYf * 2);
-    c.n_seg = p.n_seg;
-    w.take(c.seg_s, p.seg_bytes);
-    w.take(c.seg_m, p.n_seg > 1 ? static_cast<size_t>(p.N) * a.H * p.n_seg * a.dk * a.dk * 4 : 0);
   }
+  c.n_seg = p.n_seg;
+  Cut g{static_cast<char*>(saved)};
+  Cut& s = saved ? g : w;
+  s.take(c.gates, rec * gls::kGates * 4);
+  s.take(c.seg_s, p.seg_bytes);
+  s.take(c.seg_m, p.m_bytes);
   if (saved) {
-    Cut s{static_cast<char*>(saved)};
-    s.take(c.gates, p.gate_bytes);
     s.take(c.ytf, rec * gls::kYf * 2);
     s.take(c.ptf, rec * gls::kYf * 2);
     s.take(c.sf, p.state_bytes);
     s.take(c.ef, p.err_bytes);
     s.take(c.yb, p.y_bytes);
     s.take(c.st, p.last_bytes);
-  } else {
-    w.take(c.gates, p.gate_bytes);
   }
   return c;
 }
@@ -369,12 +370,13 @@ gl_status_t gl_delta_bwd(const gl_delta_desc_t* desc, const void* q, const void*
                        gls::delta_rows_ok(a.sdq, a.dk) && gls::delta_rows_ok(a.sdk, a.dk)))
       return fail(GL_ERROR_NOT_SUPPORTED, "strides of dy, dq, dk, dv: multiples of 8, rows apart");
     uint16_t *lf, *gf;
-    float *zf, *bf;
+    float *zf, *bf, *seg_l;
     char *again, *fws;
     w.take(lf, p.state_bytes);
     w.take(gf, p.err_bytes);
     w.take(zf, p.z_bytes);
     w.take(bf, p.z_bytes);
+    w.take(seg_l, p.seg_bytes);
     w.take(again, saved ? 0 : p.saved);
     w.take(fws, saved ? 0 : p.fwd_ws);
     gls::ChunkArgs c = chunk_args(a, p, saved ? const_cast<void*>(saved) : again, saved ? nullptr : fws);
@@ -383,6 +385,7 @@ gl_status_t gl_delta_bwd(const gl_delta_desc_t* desc, const void* q, const void*
     c.gf = gf;
     c.zf = zf;
     c.bf = bf;
+    c.seg_l = seg_l;
     return hip_status(gls::launch_delta_chunk_bwd(c, s), "delta backward launch");
   }
   if (p.chunk32) {

@@ -11,7 +11,9 @@
 // there the chain of a chunk in one wave bounds it, 3.2 us a step at 128 x 128:
 // 4 x 16 x 4096 x 128 takes 205 us (794 MB, 3.9 TB/s), 8 x 16 x 4096 x 64 175 us (829
 // MB, 4.7 TB/s: near what a copy reaches).  P^T is read, not formed here: the
-// helpers would outlast the state waves (252 and 207 us).
+// helpers would outlast the state waves (252 and 207 us).  Segments as in the
+// forward, from the right: Lam_begin = Lam_end M^T + Z, with M the forward's (1 x 16
+// x 32768 x 128: the whole backward 942 us in four, 1588 in one).
 // The rest is one work-group per chunk and key head (delta_chunk_grad):
 //
 //   dq = scale e^l dO S + dP K,              dP_ij = scale D_ij beta_j dO_i.e_j  (j <= i)
@@ -50,7 +52,8 @@ struct RevLds {
   alignas(16) uint16_t turn[NW][NS * kFrag];
 };
 
-template <int DK, int NW>
+// STATES: only what segments 1 .. n_seg - 1 do to an adjoint of zero.
+template <int DK, int NW, bool STATES>
 __global__ __launch_bounds__(64 * (2 * NW + 2)) void delta_chunk_rev(ChunkArgs ca) {
   const DeltaArgs& a = ca.a;
   constexpr int NS = DK / 32, NB = DK / 16, VW = 16 * NW;
@@ -60,14 +63,24 @@ __global__ __launch_bounds__(64 * (2 * NW + 2)) void delta_chunk_rev(ChunkArgs c
   const int tiles = (a.dv + VW - 1) / VW;
   int64_t head;
   int tile;
-  if (!head_of_block(blockIdx.x, tiles, a.N * a.H, head, tile)) return;
+  const int runs = STATES ? ca.n_seg - 1 : ca.n_seg;
+  if (!head_of_block(blockIdx.x, tiles, a.N * a.H * runs, head, tile)) return;
+  const int seg = static_cast<int>(static_cast<uint32_t>(head) % static_cast<uint32_t>(runs)) + (STATES ? 1 : 0);
+  head = static_cast<uint32_t>(head) / static_cast<uint32_t>(runs);
+  const bool last = seg == ca.n_seg - 1;
   const int h = static_cast<int>(head % a.H);
   const int64_t n = head / a.H;
   const int hk = h / (a.H / a.Hk), r0 = tile * VW;
-  const SeqRange sr = seq_range(a.cu, n, a.T);
-  const int nc = static_cast<int>((sr.len + kDeltaChunk - 1) / kDeltaChunk);
-  const int64_t slot0 = chunk_slot0(a.cu != nullptr, n, sr.t0, a.T, kDeltaChunk);
+  SeqRange sr = seq_range(a.cu, n, a.T);
+  int64_t slot0 = chunk_slot0(a.cu != nullptr, n, sr.t0, a.T, kDeltaChunk);
+  const int nc = segment_of(sr, slot0, seg, ca.n_seg);
   const int64_t rec0 = slot0 * a.H + h;
+  // the adjoint after the last chunk and the state there
+  const float* lam_end = last ? static_cast<const float*>(a.dstate_out)
+                         : STATES ? nullptr
+                                  : ca.seg_l + (head * ca.n_seg + seg) * a.dv * a.dk;
+  const float* state_end = last ? ca.st : ca.seg_s + (head * ca.n_seg + seg + 1) * a.dv * a.dk;
+  const int64_t end0 = last ? head * a.dv * a.dk : 0;
 
   // Step i: the helpers take chunk nc - 1 - i, the state waves the one before
   // (nc - i), and the helpers finish the decay's gradient of the one before
@@ -157,19 +170,20 @@ __global__ __launch_bounds__(64 * (2 * NW + 2)) void delta_chunk_rev(ChunkArgs c
       const uint16_t* p = ca.ptf + rec * kYf + lane * 8;
 #pragma unroll
       for (int f = 0; f < 12; ++f) pf[f] = *reinterpret_cast<const bf16x8*>(p + f * kFrag);
+      if constexpr (!STATES)
 #pragma unroll
-      for (int tb = 0; tb < 4; ++tb)
-        yb[tb] = *reinterpret_cast<const f32x4*>(ca.yb + ((rec * n_rt + rt) * 4 + tb) * 256 + lane * 4);
+        for (int tb = 0; tb < 4; ++tb)
+          yb[tb] = *reinterpret_cast<const f32x4*>(ca.yb + ((rec * n_rt + rt) * 4 + tb) * 256 + lane * 4);
     };
     if (nc > 0) fetch(nc - 1);
     float z = 0.f;  // <dL/dS, S> after the chunk, over this wave's rows
-    if (a.dstate_out && r0 + index1(w, l) < a.dv) {
-      const int64_t so = (head * a.dv + r0 + index1(w, l)) * a.dk;
+    if (!STATES && lam_end && r0 + index1(w, l) < a.dv) {
+      const int64_t so = end0 + static_cast<int64_t>(r0 + index1(w, l)) * a.dk;
 #pragma unroll
       for (int b = 0; b < NB; ++b)
         if (index4(b, g) < a.dk) {
-          const f32x4 u = *reinterpret_cast<const f32x4*>(static_cast<const float*>(a.dstate_out) + so + index4(b, g));
-          const f32x4 s = *reinterpret_cast<const f32x4*>(ca.st + so + index4(b, g));
+          const f32x4 u = *reinterpret_cast<const f32x4*>(lam_end + so + index4(b, g));
+          const f32x4 s = *reinterpret_cast<const f32x4*>(state_end + so + index4(b, g));
 #pragma unroll
           for (int q = 0; q < 4; ++q) z = fmaf(u[q], s[q], z);
         }
@@ -178,7 +192,7 @@ __global__ __launch_bounds__(64 * (2 * NW + 2)) void delta_chunk_rev(ChunkArgs c
     for (int i = 0; i <= nc + 1; ++i) {
       lds_barrier();  // A
       lds_barrier();  // B: the results of the step before have been taken
-      if (i >= 2) {
+      if (!STATES && i >= 2) {
         const int64_t rec = rec0 + static_cast<int64_t>(nc + 1 - i) * a.H;
         const float x = lds.dyy[w][(i - 2) % 3][lane] - lds.vdv[w][i & 1][lane];
         const float y = wave_scan_add(wave_reverse(x, lane));
@@ -188,6 +202,7 @@ __global__ __launch_bounds__(64 * (2 * NW + 2)) void delta_chunk_rev(ChunkArgs c
       f32x4 x1[4], x2[NB];
       if (i < nc) {
         const int sl = i % 3;
+        if constexpr (!STATES)
 #pragma unroll
         for (int tb = 0; tb < 4; ++tb) {  // dy.y: token 16 tb + l
           const f32x4 d = widen(row4<VW>(lds.o[sl], to, tb, w));
@@ -238,12 +253,11 @@ __global__ __launch_bounds__(64 * (2 * NW + 2)) void delta_chunk_rev(ChunkArgs c
   // ---- adjoint states
   const TileLane<VW> tv = tile_lane<VW>(lane);
   const int r = r0 + index1(wave, l);
-  const int64_t so = (head * a.dv + r) * a.dk;
   f32x4 S[NB];
 #pragma unroll
   for (int b = 0; b < NB; ++b)
-    S[b] = a.dstate_out && r < a.dv && index4(b, g) < a.dk
-               ? *reinterpret_cast<const f32x4*>(static_cast<const float*>(a.dstate_out) + so + index4(b, g))
+    S[b] = lam_end && r < a.dv && index4(b, g) < a.dk
+               ? *reinterpret_cast<const f32x4*>(lam_end + end0 + static_cast<int64_t>(r) * a.dk + index4(b, g))
                : zero4();
   bf16x8 yf[12], ef[2];
   const int rt = tile * NW + wave, n_rt = delta_row_tiles(a.dv);
@@ -254,6 +268,7 @@ __global__ __launch_bounds__(64 * (2 * NW + 2)) void delta_chunk_rev(ChunkArgs c
     for (int f = 0; f < 12; ++f) yf[f] = *reinterpret_cast<const bf16x8*>(p + f * kFrag);
   };
   const auto fetch_e = [&](int c) {
+    if constexpr (STATES) return;
     const int64_t rec = rec0 + static_cast<int64_t>(c) * a.H;
 #pragma unroll
     for (int s = 0; s < 2; ++s)
@@ -272,8 +287,9 @@ __global__ __launch_bounds__(64 * (2 * NW + 2)) void delta_chunk_rev(ChunkArgs c
   for (int i = 1; i <= nc; ++i) {
     const int c = nc - i;
     const int64_t rec = rec0 + static_cast<int64_t>(c) * a.H;
+    if constexpr (!STATES)
 #pragma unroll
-    for (int s = 0; s < NS; ++s) *reinterpret_cast<bf16x8*>(&turn[s * kFrag + lane * 8]) = sp[s].hi;
+      for (int s = 0; s < NS; ++s) *reinterpret_cast<bf16x8*>(&turn[s * kFrag + lane * 8]) = sp[s].hi;
     lds_barrier();  // A
     const int sl = (i - 1) % 3;
     const char* kt = lds.k[sl];
@@ -332,8 +348,8 @@ __global__ __launch_bounds__(64 * (2 * NW + 2)) void delta_chunk_rev(ChunkArgs c
       for (int i = 0; i < 2; ++i)
 #pragma unroll
         for (int q = 0; q < 4; ++q) G[2 * half + i][q] -= x[2 * half + i][q];
-      gf[half] = raw_order(round8(G[2 * half], G[2 * half + 1]), lane);
-      const s16x8 e = __builtin_bit_cast(s16x8, raw_order(ef[half], lane));
+      if constexpr (!STATES) gf[half] = raw_order(round8(G[2 * half], G[2 * half + 1]), lane);
+      const s16x8 e = STATES ? s16x8{} : __builtin_bit_cast(s16x8, raw_order(ef[half], lane));
       const f32x4 ee[2] = {widen(__builtin_shufflevector(e, e, 0, 1, 2, 3)), widen(__builtin_shufflevector(e, e, 4, 5, 6, 7))};
 #pragma unroll
       for (int i = 0; i < 2; ++i) {
@@ -341,9 +357,9 @@ __global__ __launch_bounds__(64 * (2 * NW + 2)) void delta_chunk_rev(ChunkArgs c
         const f32x4 v = widen(vv[tb]), be = gate(1, tb), gm = gate(0, tb);
 #pragma unroll
         for (int q = 0; q < 4; ++q) {
-          xe[4 * tb + q] = G[tb][q] * ee[i][q];
+          if constexpr (!STATES) xe[4 * tb + q] = G[tb][q] * ee[i][q];
           G[tb][q] *= be[q];
-          yv[4 * tb + q] = v[q] * G[tb][q];
+          if constexpr (!STATES) yv[4 * tb + q] = v[q] * G[tb][q];
           G[tb][q] *= -gm[q];
         }
       }
@@ -364,8 +380,9 @@ __global__ __launch_bounds__(64 * (2 * NW + 2)) void delta_chunk_rev(ChunkArgs c
     const float whole = gt[63];
     read_k(1);
     lds_barrier();  // B
+    if constexpr (!STATES)
 #pragma unroll
-    for (int b = 0; b < NB; b += 2) lf[b / 2] = join(turned(turn, b, lane), turned(turn, b + 1, lane));
+      for (int b = 0; b < NB; b += 2) lf[b / 2] = join(turned(turn, b, lane), turned(turn, b + 1, lane));
     ks(1);
 #pragma unroll
     for (int b = 0; b < NB; ++b)
@@ -400,26 +417,34 @@ __global__ __launch_bounds__(64 * (2 * NW + 2)) void delta_chunk_rev(ChunkArgs c
       S[b] = mfma16x16x32(kc[b], u.lo, S[b]);
     }
     const int tok = 16 * (l >> 2) + 4 * g + (l & 3);
-    const float be_ = row_sums(xe, l);
-    lds.vdv[wave][(i - 1) & 1][tok] = row_sums(yv, l);
+    float be_ = 0.f;
+    if constexpr (!STATES) {
+      be_ = row_sums(xe, l);
+      lds.vdv[wave][(i - 1) & 1][tok] = row_sums(yv, l);
+    }
     interleave<2 * NB, 1, 96 / (2 * NB)>();
 #pragma unroll
     for (int s = 0; s < NS; ++s) sp[s] = split8(S[2 * s], S[2 * s + 1]);
+    if constexpr (!STATES) {
 #pragma unroll
-    for (int b = 0; b < NB; b += 2)
-      *reinterpret_cast<bf16x8*>(ca.lf + ((rec * n_rt + rt) * NB + b) * kPiece + lane * 8) = lf[b / 2];
+      for (int b = 0; b < NB; b += 2)
+        *reinterpret_cast<bf16x8*>(ca.lf + ((rec * n_rt + rt) * NB + b) * kPiece + lane * 8) = lf[b / 2];
 #pragma unroll
-    for (int s = 0; s < 2; ++s)
-      *reinterpret_cast<bf16x8*>(ca.gf + ((rec * n_rt + rt) * 2 + s) * kFrag + raw_at(lane)) = gf[s];
-    ca.bf[(rec * n_rt + rt) * 64 + tok] = be_;
+      for (int s = 0; s < 2; ++s)
+        *reinterpret_cast<bf16x8*>(ca.gf + ((rec * n_rt + rt) * 2 + s) * kFrag + raw_at(lane)) = gf[s];
+      ca.bf[(rec * n_rt + rt) * 64 + tok] = be_;
+    }
   }
   lds_barrier();
   lds_barrier();
-  if (a.dstate_in && r < a.dv) {
+  float* to = STATES     ? ca.seg_l + (head * ca.n_seg + seg - 1) * a.dv * a.dk
+              : seg == 0 ? static_cast<float*>(a.dstate_in)
+                         : nullptr;
+  if (to && r < a.dv) {
+    to += (STATES ? 0 : head * a.dv * a.dk) + static_cast<int64_t>(r) * a.dk;
 #pragma unroll
     for (int b = 0; b < NB; ++b)
-      if (index4(b, g) < a.dk)
-        *reinterpret_cast<f32x4*>(static_cast<float*>(a.dstate_in) + so + index4(b, g)) = S[b];
+      if (index4(b, g) < a.dk) *reinterpret_cast<f32x4*>(to + index4(b, g)) = S[b];
   }
 }
 
@@ -743,8 +768,14 @@ template <int DK>
 hipError_t launch(const ChunkArgs& c, hipStream_t s) {
   constexpr int NW = 2;
   const int tiles = (c.a.dv + 16 * NW - 1) / (16 * NW);
-  delta_chunk_rev<DK, NW><<<dim3(static_cast<unsigned>(head_blocks(c.a.N * c.a.H, tiles))), 64 * (2 * NW + 2), 0, s>>>(c);
-  hipError_t e = hipGetLastError();
+  const auto blocks = [&](int runs) { return dim3(static_cast<unsigned>(head_blocks(c.a.N * c.a.H * runs, tiles))); };
+  hipError_t e = hipSuccess;
+  if (c.n_seg > 1) {
+    delta_chunk_rev<DK, NW, true><<<blocks(c.n_seg - 1), 64 * (2 * NW + 2), 0, s>>>(c);
+    if ((e = hipGetLastError()) != hipSuccess || (e = launch_delta_join(c, true, s)) != hipSuccess) return e;
+  }
+  delta_chunk_rev<DK, NW, false><<<blocks(c.n_seg), 64 * (2 * NW + 2), 0, s>>>(c);
+  e = hipGetLastError();
   if (e != hipSuccess || c.slots == 0) return e;
   const dim3 grid(static_cast<unsigned>(c.slots * c.a.Hk));
   const bool shared = c.a.H != c.a.Hk;

@@ -79,15 +79,8 @@ __global__ __launch_bounds__((kFwdThreads<NW, MODE>)) void delta_chunk_fwd(Chunk
   const int64_t n = head / a.H;
   const int hk = h / (a.H / a.Hk), r0 = tile * VW;
   SeqRange sr = seq_range(a.cu, n, a.T);
-  int nc = static_cast<int>((sr.len + kDeltaChunk - 1) / kDeltaChunk);
   int64_t slot0 = chunk_slot0(a.cu != nullptr, n, sr.t0, a.T, kDeltaChunk);
-  if (ca.n_seg > 1) {
-    const int per = (nc + ca.n_seg - 1) / ca.n_seg, c0 = static_cast<int>(min(static_cast<int64_t>(seg) * per, static_cast<int64_t>(nc)));
-    nc = min(per, nc - c0);
-    slot0 += c0;
-    sr.t0 += c0 * static_cast<int64_t>(kDeltaChunk);
-    sr.len = min(sr.len - c0 * static_cast<int64_t>(kDeltaChunk), nc * static_cast<int64_t>(kDeltaChunk));
-  }
+  const int nc = segment_of(sr, slot0, seg, ca.n_seg);
   const int64_t rec0 = slot0 * a.H + h;
 
   if (wave == LOADER) {  // ---- loads: K two chunks ahead, V and gates one
@@ -473,10 +466,11 @@ __global__ __launch_bounds__((kFwdThreads<NW, MODE>)) void delta_chunk_fwd(Chunk
 }
 
 // First states of the segments: S_(s+1) = S_s M_s + Z_s, s = 1 .. n_seg - 2, in
-// fp32; Z_s stands where S_(s+1) goes.  A work-group has 16 rows of a head,
+// fp32; Z_s stands where S_(s+1) goes.  BACK: their last adjoints, Lam_(s-1) =
+// Lam_s M_s^T + Z_s, s = n_seg - 2 .. 1.  A work-group has 16 rows of a head,
 // which stay in LDS between the segments; wave w forms the column blocks w and
 // w + 4 of 16.  Bound by latency: about 2 us a segment.
-template <int DK>
+template <int DK, bool BACK>
 __global__ __launch_bounds__(256) void delta_join(ChunkArgs ca) {
   const DeltaArgs& a = ca.a;
   constexpr int NB = DK / 16, P = DK + 4;
@@ -487,20 +481,20 @@ __global__ __launch_bounds__(256) void delta_join(ChunkArgs ca) {
   const int64_t head = blockIdx.x / tiles;
   const int r0 = static_cast<int>(blockIdx.x % tiles) * 16;
   const int nr = min(16, a.dv - r0);
-  // rows r0.. of S_s, zeros past dv and dk
-  const auto states = [&](int s) {
-    return buffer_rsrc(ca.seg_s + ((head * ca.n_seg + s) * a.dv + r0) * a.dk, nr * a.dk * 4);
-  };
-  const __amdgpu_buffer_rsrc_t r1 = states(1);
+  // rows r0.. of a segment's state or adjoint, zeros past dv and dk
+  const auto at = [&](int s) { return (BACK ? ca.seg_l : ca.seg_s) + ((head * ca.n_seg + s) * a.dv + r0) * a.dk; };
+  const auto states = [&](int s) { return buffer_rsrc(at(s), nr * a.dk * 4); };
+  const __amdgpu_buffer_rsrc_t r1 = states(BACK ? ca.n_seg - 2 : 1);
   for (int i = threadIdx.x; i < 16 * DK; i += 256) {
     const int r = i / DK, c = i % DK;
     rows[0][r * P + c] = load4(r1, c < a.dk ? static_cast<uint32_t>((r * a.dk + c) * 4) : kPastEnd);
   }
-  for (int s = 1; s + 1 < ca.n_seg; ++s) {
+  for (int n = 0; n + 2 < ca.n_seg; ++n) {
+    const int s = BACK ? ca.n_seg - 2 - n : n + 1, next = BACK ? s - 1 : s + 1;
     const __amdgpu_buffer_rsrc_t rm = buffer_rsrc(ca.seg_m + (head * ca.n_seg + s) * a.dk * a.dk, a.dk * a.dk * 4);
-    const __amdgpu_buffer_rsrc_t rz = states(s + 1);
-    const float* from = rows[(s + 1) & 1];
-    float* to = rows[s & 1];
+    const __amdgpu_buffer_rsrc_t rz = states(next);
+    const float* from = rows[n & 1];
+    float* to = rows[(n + 1) & 1];
     float m[(NB + 3) / 4][NB][4];
     f32x4 x[(NB + 3) / 4];
 #pragma unroll
@@ -510,7 +504,11 @@ __global__ __launch_bounds__(256) void delta_join(ChunkArgs ca) {
 #pragma unroll
       for (int kb = 0; kb < NB; ++kb)
 #pragma unroll
-        for (int q = 0; q < 4; ++q) m[i][kb][q] = load4(rm, o + (16 * kb + 4 * g + q) * a.dk * 4);
+        for (int q = 0; q < 4; ++q) {
+          const int k = 16 * kb + 4 * g + q;
+          m[i][kb][q] = BACK ? load4(rm, c < a.dk && k < a.dk ? static_cast<uint32_t>((c * a.dk + k) * 4) : kPastEnd)
+                             : load4(rm, o + k * a.dk * 4);
+        }
 #pragma unroll
       for (int q = 0; q < 4; ++q) x[i][q] = load4(rz, o + (4 * g + q) * a.dk * 4);
     }
@@ -531,7 +529,7 @@ __global__ __launch_bounds__(256) void delta_join(ChunkArgs ca) {
       for (int q = 0; q < 4; ++q) {
         const int r = 4 * g + q;
         to[r * P + c] = x[i][q];
-        if (r < nr && c < a.dk) ca.seg_s[((head * ca.n_seg + s + 1) * a.dv + r0 + r) * a.dk + c] = x[i][q];
+        if (r < nr && c < a.dk) at(next)[r * a.dk + c] = x[i][q];
       }
     }
   }
@@ -552,15 +550,25 @@ hipError_t launch_all(const ChunkArgs& c, hipStream_t s) {
   if (c.n_seg > 1) {
     hipError_t e = launch<DK, 4, STATES>(c, s);
     if (e != hipSuccess) return e;
-    if (c.n_seg > 2) {
-      delta_join<DK><<<dim3(static_cast<unsigned>(c.a.N * c.a.H * ((c.a.dv + 15) / 16))), 256, 0, s>>>(c);
-      if ((e = hipGetLastError()) != hipSuccess) return e;
-    }
+    if ((e = launch_delta_join(c, false, s)) != hipSuccess) return e;
   }
   return c.sf ? launch<DK, 2, TRAINING>(c, s) : launch<DK, 2, OUTPUTS>(c, s);
 }
 
 }  // namespace
+
+hipError_t launch_delta_join(const ChunkArgs& c, bool back, hipStream_t s) {
+  if (c.n_seg <= 2) return hipSuccess;
+  const dim3 grid(static_cast<unsigned>(c.a.N * c.a.H * ((c.a.dv + 15) / 16)));
+  if (c.a.dk <= 64) {
+    if (back) delta_join<64, true><<<grid, 256, 0, s>>>(c);
+    else delta_join<64, false><<<grid, 256, 0, s>>>(c);
+  } else {
+    if (back) delta_join<128, true><<<grid, 256, 0, s>>>(c);
+    else delta_join<128, false><<<grid, 256, 0, s>>>(c);
+  }
+  return hipGetLastError();
+}
 
 hipError_t launch_delta_chunk_fwd(const ChunkArgs& c, hipStream_t s) {
   if (c.a.N * c.a.H == 0) return hipSuccess;
