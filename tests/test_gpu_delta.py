@@ -363,3 +363,36 @@ def test_around_the_shortest_chunked_sequences(T, lens, dtype):
 def test_segments_without_saved(segments):
     run_case(70 + segments, 2, 2, 2, 64 * 9 + 7, 64, 64, BF16, gate=F32, saved=False, segments=segments)
     run_case(80 + segments, 1, 3, 1, 64 * 9 + 7, 128, 96, BF16, with_state=False, segments=segments, decay="base")
+
+
+def test_calls_of_one_kind_then_others():
+    """Checked calls are remembered by shapes, strides, types and devices: a call
+    that differs in any of them is checked anew, and refused or right."""
+    x = inputs(50, 3, 4, 2, 1, 64, 64, BF16)
+    g = to_gpu(x, BF16, BF16)
+    one = {n: g[n][:, :, 0].contiguous() for n in ("q", "k", "v", "log_alpha", "beta")}
+    names = list(one)
+    step = lambda state, **kw: ws.gl_delta_step(*[kw.get(n, one[n]) for n in names], state)  # noqa: E731
+    first = g["state"].clone()
+    y = step(first)
+    for _ in range(2):
+        again = g["state"].clone()
+        assert torch.equal(step(again), y) and torch.equal(again, first)
+    strided = torch.nn.functional.pad(one["v"], (0, 64))[..., :64]
+    again = g["state"].clone()
+    assert torch.equal(step(again, v=strided), y) and torch.equal(again, first)
+    for bad, err in ((dict(v=one["v"].cpu()), ValueError), (dict(v=one["v"].float()), TypeError),
+                     (dict(k=one["k"][..., :32]), ValueError), (dict(log_alpha=one["log_alpha"][:2]), ValueError),
+                     (dict(q=one["q"].cpu()), ValueError), (dict(beta=one["beta"].double()), TypeError)):
+        with pytest.raises(err):
+            step(g["state"].clone(), **bad)
+    with pytest.raises(ValueError):
+        step(g["state"][:2].clone())
+    assert torch.equal(step(g["state"].clone()), y)
+    # running positions are no new kind of call
+    q = g["q"]
+    cos, sin = torch.rand(2, 40, 32, device="cuda")
+    for p in range(3):
+        a = ws.gl_qknorm_rope_fwd(q, q, cos=cos, sin=sin, pos0=p)[0]
+        pos = torch.full((3, 1), p, dtype=torch.int32, device="cuda")
+        assert torch.equal(a, ws.gl_qknorm_rope_fwd(q, q, cos=cos, sin=sin, pos=pos)[0])

@@ -141,50 +141,37 @@ def _three(st, shape, name):
     return Strides(*st)
 
 
-def _key(t):
-    """What a call's checks and descriptor depend on in a tensor (not its address)."""
-    return None if t is None else (t.shape, t.stride(), t.dtype, t.get_device())
+_KINDS = {"gl_delta_fwd": 0, "gl_delta_bwd": 1, "gl_delta_step": 2, "gl_qknorm_rope_fwd": 3, "gl_qknorm_rope_bwd": 4}
+_calls: dict = {}
 
 
-def _ptr(t):
-    return None if t is None else t.data_ptr()
-
-
-class _Plan:
-    """A checked descriptor with its sizes, and the shapes and strides of the outputs."""
-
-    def __init__(self, desc, device):
-        self.desc, self.ref, self.device = desc, ctypes.byref(desc), device
-
-
-_plans: dict = {}
-
-
-def _plan(key, make):
-    """The plan of `key`, made and checked by `make` the first time: a decoding
-    loop makes thousands of calls of one kind, and the checks cost more than
-    the launch."""
-    p = _plans.get(key)
-    if p is None:
-        p = make()
-        if len(_plans) >= 512:
-            _plans.clear()
-        _plans[key] = p
-    return p
-
-
-def _launch(fn, plan, *args):
-    """fn(desc, *args, current stream) with the tensors' device current."""
-    torch = _torch()
-    index = plan.device.index
-    stream = torch._C._cuda_getCurrentRawStream(index)
-    if index == torch.cuda.current_device():
-        status = fn(plan.ref, *args, stream)
-    else:
-        with torch.cuda.device(index):
-            status = fn(plan.ref, *args, stream)
-    if status:
-        _check(status)
+def _run(name, numbers, tensors, plan, pos0=0):
+    """Calls `name` of the library on `tensors` on the current stream and returns
+    its outputs.  `plan` checks the tensors and returns (descriptor, workspace
+    bytes, count, outputs); it runs where no call of the same numbers, shapes,
+    strides, types and devices came before: a decoding loop makes thousands of
+    one kind, and the checks cost more than the launch."""
+    calls = _calls.get((name, numbers))
+    if calls is None:
+        from . import _fastcall  # needs torch to be imported
+        fn = ctypes.cast(getattr(delta_lib(), name), ctypes.c_void_p).value
+        calls = _fastcall.Calls(_KINDS[name], fn)
+        if len(_calls) >= 256:
+            _calls.clear()
+        _calls[name, numbers] = calls
+    index = tensors[0].get_device()
+    if index < 0:
+        plan()
+        raise ValueError("all tensors must be on a GPU device")
+    stream = _torch()._C._cuda_getCurrentRawStream(index)
+    out = calls.call(stream, pos0, *tensors)
+    if out is None:
+        desc, ws, count, outputs = plan()
+        calls.record(desc, ctypes.addressof(desc), ws, count, outputs, *tensors)
+        out = calls.call(stream, pos0, *tensors)
+    if type(out) is not tuple:
+        _check(out)
+    return out
 
 
 def _strides_like(t, shape):
@@ -247,32 +234,28 @@ def _check_state(t, shape, io, name):
         raise ValueError(f"{name} must be contiguous")
 
 
+def _contiguous(shape, dtype):
+    """Output of _run: dense, of shape."""
+    st = [1]
+    for n in reversed(shape[1:]):
+        st.append(st[-1] * max(n, 1))
+    return tuple(shape), tuple(reversed(st)), dtype
+
+
 def gl_delta_fwd(q, k, v, log_alpha, beta, *, scale=None, state=None, want_state=False, save=False,
                  cu_seqlens=None, flags=0, segments=0):
     """Gated delta rule over whole sequences.  Returns (y, final state or None,
     saved or None).  scale: of y, 1/sqrt(dk) by default."""
-    torch = _torch()
-
-    def make():
+    def plan():
         desc, n = _delta_desc(q, k, v, log_alpha, beta, scale, state, cu_seqlens, flags, segments)
-        p = _Plan(desc, q.device)
-        p.y_shape, p.y_strides = tuple(v.shape), _strides_like(v, v.shape)
-        _with(desc, "sy", p.y_shape, p.y_strides)
-        p.state_shape, p.state_dtype = (n, v.shape[1], v.shape[3], q.shape[3]), gate_dtype(q.dtype)
-        p.saved = max(delta_saved_size(desc), 16) if save else 0
-        p.ws = delta_workspace_size(desc, save)[0]
-        p.fn = delta_lib().gl_delta_fwd
-        return p
-    p = _plan(("fwd", _key(q), _key(k), _key(v), _key(log_alpha), _key(beta), scale, _key(state), save,
-               _key(cu_seqlens), flags, segments), make)
-    device = p.device
-    y = torch.empty_strided(p.y_shape, p.y_strides, dtype=v.dtype, device=device)
-    out = torch.empty(p.state_shape, dtype=p.state_dtype, device=device) if want_state else None
-    saved = torch.empty(p.saved, dtype=torch.uint8, device=device) if save else None
-    ws = torch.empty(p.ws, dtype=torch.uint8, device=device) if p.ws else None
-    _launch(p.fn, p, q.data_ptr(), k.data_ptr(), v.data_ptr(), log_alpha.data_ptr(), beta.data_ptr(), _ptr(state),
-            _ptr(cu_seqlens), y.data_ptr(), _ptr(out), _ptr(saved), _ptr(ws), p.ws)
-    return y, out, saved
+        shape, strides = tuple(v.shape), _strides_like(v, v.shape)
+        _with(desc, "sy", shape, strides)
+        return desc, delta_workspace_size(desc, save)[0], 0, (
+            (shape, strides, v.dtype),
+            _contiguous((n, v.shape[1], v.shape[3], q.shape[3]), gate_dtype(q.dtype)) if want_state else None,
+            _contiguous((max(delta_saved_size(desc), 16),), _torch().uint8) if save else None)
+    return _run("gl_delta_fwd", (scale, bool(want_state), bool(save), flags, segments),
+                (q, k, v, log_alpha, beta, state, cu_seqlens), plan)
 
 
 def gl_delta_bwd(q, k, v, log_alpha, beta, dy, saved=None, *, scale=None, state=None, dstate=None,
@@ -280,42 +263,29 @@ def gl_delta_bwd(q, k, v, log_alpha, beta, dy, saved=None, *, scale=None, state=
     """Gradients for upstream dy [B,H,T,dv] and dstate (of the final state, or
     None).  Returns (dq, dk, dv, dlog_alpha, dbeta, dstate of the first state);
     the last is None unless `state` was given or want_dstate is true."""
-    torch = _torch()
+    if want_dstate is None:
+        want_dstate = state is not None
 
-    def make():
+    def plan():
         desc, n = _delta_desc(q, k, v, log_alpha, beta, scale, state, cu_seqlens, flags, segments)
         if dy.shape != v.shape or dy.dtype != v.dtype:
             raise ValueError("dy must have the shape and dtype of v")
         _on_gpu((q, dy, dstate, saved))
-        p = _Plan(desc, q.device)
-        p.state_shape, p.state_dtype = (n, v.shape[1], v.shape[3], q.shape[3]), gate_dtype(q.dtype)
-        _check_state(dstate, p.state_shape, q.dtype, "dstate")
-        if saved is not None and (saved.dtype != torch.uint8 or not saved.is_contiguous()
+        states = _contiguous((n, v.shape[1], v.shape[3], q.shape[3]), gate_dtype(q.dtype))
+        _check_state(dstate, states[0], q.dtype, "dstate")
+        if saved is not None and (saved.dtype != _torch().uint8 or not saved.is_contiguous()
                                   or saved.numel() < delta_saved_size(desc)):
             raise ValueError("saved must be what gl_delta_fwd returned for these inputs")
-        p.outs = []
-        for name, t in (("sdq", q), ("sdk", k), ("sdv", v), ("sdg", beta)):
+        outs = []
+        for name, t in (("sdq", q), ("sdk", k), ("sdv", v), ("sdg", log_alpha), ("sdg", beta)):
             st = tuple(t.stride()) if t.dim() == 3 and _dense(t) else _strides_like(t, t.shape)
-            p.outs.append((tuple(t.shape), st, t.dtype))
+            outs.append((tuple(t.shape), st, t.dtype))
             _with(desc, name, t.shape, st)
         desc.sdy = _rows(dy, "dy")
-        p.ws = delta_workspace_size(desc, saved is not None)[1]
-        p.fn = delta_lib().gl_delta_bwd
-        return p
-    p = _plan(("bwd", _key(q), _key(k), _key(v), _key(log_alpha), _key(beta), _key(dy), _key(saved), scale,
-               _key(state), _key(dstate), _key(cu_seqlens), flags, segments), make)
-    device = p.device
-    dq, dk, dv, dla = (torch.empty_strided(s, st, dtype=d, device=device) for s, st, d in p.outs)
-    s, st, d = p.outs[3]
-    db = torch.empty_strided(s, st, dtype=d, device=device)
-    if want_dstate is None:
-        want_dstate = state is not None
-    ds = torch.empty(p.state_shape, dtype=p.state_dtype, device=device) if want_dstate else None
-    ws = torch.empty(p.ws, dtype=torch.uint8, device=device) if p.ws else None
-    _launch(p.fn, p, q.data_ptr(), k.data_ptr(), v.data_ptr(), log_alpha.data_ptr(), beta.data_ptr(), _ptr(state),
-            _ptr(cu_seqlens), dy.data_ptr(), _ptr(dstate), _ptr(saved), dq.data_ptr(), dk.data_ptr(), dv.data_ptr(),
-            dla.data_ptr(), db.data_ptr(), _ptr(ds), _ptr(ws), p.ws)
-    return dq, dk, dv, dla, db, ds
+        return (desc, delta_workspace_size(desc, saved is not None)[1], 0,
+                (*outs, states if want_dstate else None))
+    return _run("gl_delta_bwd", (scale, bool(want_dstate), flags, segments),
+                (q, k, v, log_alpha, beta, state, cu_seqlens, dy, dstate, saved), plan)
 
 
 def _dense(t):
@@ -332,9 +302,8 @@ def gl_delta_step(q, k, v, log_alpha, beta, state, *, scale=None, slots=None, y=
     """One token of each row: q, k [B,Hk,dk], v [B,H,dv], gates [B,H]; `state`
     [n,H,dv,dk] is updated in place, row b's at slots[b] (int32; outside
     0..n-1: nothing to do, y = 0), or at b.  Returns y [B,H,dv]."""
-    torch = _torch()
-
-    def make():
+    def plan():
+        torch = _torch()
         if q.dim() != 3 or k.shape != q.shape or v.dim() != 3 or v.shape[0] != q.shape[0] or state.dim() != 4:
             raise ValueError("q, k must be [B,Hk,dk], v [B,H,dv] and state [n,H,dv,dk]")
         B, Hk, dk = q.shape
@@ -360,20 +329,12 @@ def gl_delta_step(q, k, v, log_alpha, beta, state, *, scale=None, slots=None, y=
         _on_gpu((q, k, v, log_alpha, beta, state, slots, y))
         desc = make_delta_desc(B, 1, H, Hk, dk, dv, _io_code(q.dtype), _io_code(beta.dtype),
                                scale=dk ** -0.5 if scale is None else scale)
-        p = _Plan(desc, q.device)
-        p.y_shape, p.n = (B, H, dv), state.shape[0]
         desc.sq, desc.sk, desc.sv = _rows(q, "q"), _rows(k, "k"), _rows(v, "v")
         desc.sy = _three((H * dv, dv), (B, H), "y") if y is None else _rows(y, "y")
         desc.sg = _three(beta.stride(), beta.shape, "beta")
-        p.fn = delta_lib().gl_delta_step
-        return p
-    p = _plan(("step", _key(q), _key(k), _key(v), _key(log_alpha), _key(beta), _key(state), scale, _key(slots),
-               _key(y)), make)
-    if y is None:
-        y = torch.empty(p.y_shape, dtype=v.dtype, device=p.device)
-    _launch(p.fn, p, q.data_ptr(), k.data_ptr(), v.data_ptr(), log_alpha.data_ptr(), beta.data_ptr(), _ptr(slots),
-            p.n, state.data_ptr(), y.data_ptr())
-    return y
+        return desc, 0, state.shape[0], (_contiguous((B, H, dv), v.dtype) if y is None else None,)
+    out = _run("gl_delta_step", scale, (q, k, v, log_alpha, beta, slots, state, y), plan)[0]
+    return out if y is None else y
 
 
 # ---------------------------------------------------------------- norms and rotation
@@ -411,19 +372,11 @@ def gl_qknorm_rope_fwd(q, k, wq=None, wk=None, cos=None, sin=None, *, pos=None, 
     [B,Hk,T,d], weights wq, wk [d], and the rotation by the tables cos, sin
     [n_pos, rot/2] at pos [B,T] (or pos0 + t).  Returns the two results, dense
     [B,H,T,d] (what gl_delta_fwd reads row after row)."""
-    torch = _torch()
-
-    def make():
-        p = _Plan(_qk_desc(q, k, wq, wk, cos, sin, pos, pos0, eps, q_scale, k_scale, interleaved), q.device)
-        p.fn = delta_lib().gl_qknorm_rope_fwd
-        return p
-    p = _plan(("qk", _key(q), _key(k), _key(wq), _key(wk), _key(cos), _key(sin), _key(pos), pos0, eps, q_scale,
-               k_scale, interleaved), make)
-    oq = torch.empty(q.shape, dtype=q.dtype, device=p.device)
-    ok = torch.empty(k.shape, dtype=q.dtype, device=p.device)
-    _launch(p.fn, p, q.data_ptr(), k.data_ptr(), _ptr(wq), _ptr(wk), _ptr(cos), _ptr(sin), _ptr(pos), oq.data_ptr(),
-            ok.data_ptr())
-    return oq, ok
+    def plan():
+        desc = _qk_desc(q, k, wq, wk, cos, sin, pos, pos0, eps, q_scale, k_scale, interleaved)
+        return desc, 0, 0, (_contiguous(q.shape, q.dtype), _contiguous(k.shape, q.dtype))
+    return _run("gl_qknorm_rope_fwd", (eps, q_scale, k_scale, bool(interleaved)), (q, k, wq, wk, cos, sin, pos), plan,
+                pos0)
 
 
 def gl_qknorm_rope_bwd(q, k, wq, wk, cos, sin, dqn, dkn, *, pos=None, pos0=0, eps=1e-6, q_scale=1.0,
@@ -431,33 +384,23 @@ def gl_qknorm_rope_bwd(q, k, wq, wk, cos, sin, dqn, dkn, *, pos=None, pos0=0, ep
     """Gradients of gl_qknorm_rope_fwd for upstream dqn, dkn: (dq, dk, dwq,
     dwk), dq and dk in their inputs' order of dimensions, dwq and dwk [d] in
     fp32 (fp64), None where there is no weight."""
-    torch = _torch()
-
-    def make():
+    def plan():
         desc = _qk_desc(q, k, wq, wk, cos, sin, pos, pos0, eps, q_scale, k_scale, interleaved)
         if dqn.shape != q.shape or dkn.shape != k.shape or dqn.dtype != q.dtype or dkn.dtype != k.dtype:
             raise ValueError("dqn and dkn must have the shapes and dtype of q and k")
         _on_gpu((q, dqn, dkn))
-        p = _Plan(desc, q.device)
-        p.sq, p.sk = _strides_like(q, q.shape), _strides_like(k, k.shape)
+        sq, sk = _strides_like(q, q.shape), _strides_like(k, k.shape)
         desc.sdoq, desc.sdok = _rows(dqn, "dqn"), _rows(dkn, "dkn")
-        _with(desc, "sdq", q.shape, p.sq)
-        _with(desc, "sdk", k.shape, p.sk)
+        _with(desc, "sdq", q.shape, sq)
+        _with(desc, "sdk", k.shape, sk)
         n = ctypes.c_size_t()
         _check(delta_lib().gl_qknorm_rope_workspace_size(ctypes.byref(desc), ctypes.byref(n)))
-        p.ws, p.dw_dtype = n.value, gate_dtype(q.dtype)
-        p.fn = delta_lib().gl_qknorm_rope_bwd
-        return p
-    p = _plan(("qkb", _key(q), _key(k), _key(wq), _key(wk), _key(cos), _key(sin), _key(pos), _key(dqn), _key(dkn),
-               pos0, eps, q_scale, k_scale, interleaved), make)
-    device = p.device
-    dq = torch.empty_strided(q.shape, p.sq, dtype=q.dtype, device=device)
-    dk = torch.empty_strided(k.shape, p.sk, dtype=q.dtype, device=device)
-    dwq, dwk = (None if w is None else torch.empty(w.shape, dtype=p.dw_dtype, device=device) for w in (wq, wk))
-    ws = torch.empty(max(p.ws, 16), dtype=torch.uint8, device=device)
-    _launch(p.fn, p, q.data_ptr(), k.data_ptr(), _ptr(wq), _ptr(wk), _ptr(cos), _ptr(sin), _ptr(pos),
-            dqn.data_ptr(), dkn.data_ptr(), dq.data_ptr(), dk.data_ptr(), _ptr(dwq), _ptr(dwk), ws.data_ptr(), p.ws)
-    return dq, dk, dwq, dwk
+        dw = gate_dtype(q.dtype)
+        return desc, max(n.value, 16), 0, (
+            (tuple(q.shape), sq, q.dtype), (tuple(k.shape), sk, q.dtype),
+            None if wq is None else _contiguous(wq.shape, dw), None if wk is None else _contiguous(wk.shape, dw))
+    return _run("gl_qknorm_rope_bwd", (eps, q_scale, k_scale, bool(interleaved)),
+                (q, k, wq, wk, cos, sin, pos, dqn, dkn), plan, pos0)
 
 
 # ---------------------------------------------------------------- autograd
