@@ -51,7 +51,7 @@
  * Kernels: BF16 io with dk and dv multiples of 8, and F32 io with multiples of
  * 4, run in chunks of 64 tokens on the matrix cores.  Everything else goes token
  * by token on the vector ALU, and so do sequences of fewer than 4 tokens on
- * average (fewer than 16 in a forward that saves nothing).
+ * average (fewer than 24 in a forward that saves nothing).
  */
 #ifndef GL_DELTA_H
 #define GL_DELTA_H

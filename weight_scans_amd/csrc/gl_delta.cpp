@@ -90,10 +90,10 @@ gls::DeltaArgs base_args(const gl_delta_desc_t* d, const Plan& p) {
 // Sequences shorter than this (packed: their mean) go token by token: with one
 // launch instead of two where nothing is saved, and in training where so few
 // tokens leave the chunks' tiles all but empty.  Token by token against chunks,
-// bf16, 8 x 16 heads of 128: forward 8 tokens 13 / 20 us, 16 tokens 17 / 20, 32
-// tokens 27 / 21; backward 4 tokens 52 / 28, 8 tokens 81 / 28 (1 x 16 heads:
-// forward 8 tokens 11 / 16, 16 tokens 14 / 16; backward 4 tokens 21 / 22).
-constexpr int64_t kChunkFrom = 4, kChunkFwdFrom = 16;
+// bf16, 8 x 16 heads of 128: forward 16 tokens 15 / 19 us, 32 tokens 24 / 20;
+// backward 4 tokens 48 / 27, 8 tokens 74 / 27 (1 x 16 heads: forward 16 tokens 11
+// / 14, 32 tokens 16 / 14; backward 4 tokens 20 / 20, 8 tokens 26 / 21).
+constexpr int64_t kChunkFrom = 4, kChunkFwdFrom = 24;
 
 // Segments of the chunked bf16 kernels.  Forward: n of them take two passes of 1 / n of the
 // chunks each plus some 2 us a segment to join them, and need n times the

@@ -9,7 +9,7 @@
 // registers (delta_f32.hpp): a wave carries 16 rows of S through the sequence,
 // as in bf16.  Bound by the fp32 matrix rate of the one wave that has a row tile's
 // chain (64 x 64: 3.7 us a chunk, 2.2 of them matrix instructions): 4 x 8 x 1024 x
-// 64 takes 15 us to prepare and 59 us (token by token: 429).
+// 64 takes 15 us to prepare and 59 us (token by token: 340).
 #include "delta_f32.hpp"
 #include "dev_common.hpp"
 

@@ -9,8 +9,8 @@
 //
 // The recurrence is bound by the matrix rate of the wave that has a row tile's
 // chain, the gradients by the matrix cores and HBM: 4 x 8 x 1024 x 64 takes 106 us
-// and 32 us, 128 x 128 heads 148 us and 75 us (token by token both together: 1211
-// and 2105 us).
+// and 32 us, 128 x 128 heads 148 us and 75 us (token by token both together: 1059
+// and 1720 us).
 #include "delta_f32.hpp"
 #include "dev_common.hpp"
 

@@ -11,7 +11,7 @@
 // with p = S k, r = S q taken from the old state,
 //   e = v - a p,   y = scale (a r + beta e (k.q)).
 // Bound by the chain of one token (a product, a sum over 16 lanes, an update:
-// 0.4 us a token forward, 1.2 us backward at 64 x 64 in fp32); it serves what the
+// 0.3 us a token forward, 1.0 us backward at 64 x 64 in fp32); it serves what the
 // chunks do not take: fp64, odd sizes and strides, the shortest sequences.
 //
 // Backward, with A_t = dL/dS_t (y_t's share included), g = scale dy:
@@ -74,14 +74,35 @@ __device__ __forceinline__ S load_gate(const void* p, int64_t i, bool io) {
 // Columns of lane `l`: 4 l .. 4 l + 3 of every 64.
 __device__ __forceinline__ int col(int l, int i) { return (i >> 2) * 64 + l * 4 + (i & 3); }
 
-// Stages tokens t0 .. t0 + nt - 1 of a head of [.., T, d] rows into LDS as
-// [TC][W], zeros past d and past nt.
+// Tokens t0 .. t0 + TC - 1 of a head of [.., T, d] rows, fetched into registers
+// while the tokens before them are walked, then put into LDS as [TC][W] with
+// zeros past d and past nt.  The loads are at indices clamped into the tensor: a
+// load under a condition would be waited for before the next one is issued.
 template <typename IO, typename S, int TC, int W>
-__device__ __forceinline__ void stage(S* lds, const IO* base, int64_t st, int64_t t0, int nt, int d) {
-  for (int i = threadIdx.x; i < TC * W; i += kThreads) {
-    const int t = i / W, c = i % W;
-    lds[i] = (t < nt && c < d) ? load_as<S>(base, (t0 + t) * st + c) : S(0);
+struct Rows {
+  static constexpr int N = TC * W / kThreads;
+  S v[N];
+  __device__ __forceinline__ void fetch(const IO* base, int64_t st, int64_t t0, int64_t len, int d) {
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+      const int x = threadIdx.x + i * kThreads, t = x / W, c = min(x % W, d - 1);
+      v[i] = load_as<S>(base, min(t0 + t, len - 1) * st + c);
+    }
   }
+  __device__ __forceinline__ void put(S* lds, int nt, int d) const {
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+      const int x = threadIdx.x + i * kThreads;
+      lds[x] = x / W < nt && x % W < d ? v[i] : S(0);
+    }
+  }
+};
+// The same of one row tile of values ([TC][kRows], a thread an element) and of
+// the gates (the first TC threads).
+template <typename IO, typename S>
+__device__ __forceinline__ S fetch_rows(const IO* base, int64_t st, int64_t t0, int64_t len, int r0, int d) {
+  const int t = threadIdx.x / kRows, c = min(r0 + static_cast<int>(threadIdx.x) % kRows, d - 1);
+  return load_as<S>(base, min(t0 + t, len - 1) * st + c);
 }
 
 template <typename IO, typename S, int NI>
@@ -114,22 +135,30 @@ __global__ __launch_bounds__(kThreads) void delta_serial_fwd(DeltaArgs a) {
   const int64_t go = sr.b * a.sg.b + h * a.sg.h + sr.t0 * a.sg.t;
   const int64_t slot0 = chunk_slot0(a.cu != nullptr, n, sr.t0, a.T, CK);
 
+  Rows<IO, S, TC, W> qn, kn;
+  S vn = S(0), an = S(0), bn = S(0);
+  const auto fetch = [&](int64_t t0) {
+    if (y) qn.fetch(q, a.sq.t, t0, sr.len, a.dk);
+    kn.fetch(k, a.sk.t, t0, sr.len, a.dk);
+    vn = fetch_rows<IO, S>(v, a.sv.t, t0, sr.len, r0, a.dv);
+    const int64_t o = go + min(t0 + static_cast<int64_t>(threadIdx.x % TC), sr.len - 1) * a.sg.t;
+    an = load_gate<IO, S>(a.la, o, a.gate_io);
+    bn = load_gate<IO, S>(a.be, o, a.gate_io);
+  };
+  if (sr.len > 0) fetch(0);
   for (int64_t t0 = 0; t0 < sr.len; t0 += TC) {
     const int nt = static_cast<int>(sr.len - t0 < TC ? sr.len - t0 : TC);
     __syncthreads();
-    if (y) stage<IO, S, TC, W>(qs, q, a.sq.t, t0, nt, a.dk);
-    stage<IO, S, TC, W>(ks, k, a.sk.t, t0, nt, a.dk);
-    {
-      const int t = threadIdx.x / kRows, c = threadIdx.x % kRows;
-      vs[threadIdx.x] = (t < nt && r0 + c < a.dv) ? load_as<S>(v, (t0 + t) * a.sv.t + r0 + c) : S(0);
-    }
+    if (y) qn.put(qs, nt, a.dk);
+    kn.put(ks, nt, a.dk);
+    vs[threadIdx.x] = vn;  // rows past dv and tokens past nt go nowhere
     if (threadIdx.x < TC) {
       const bool in = static_cast<int>(threadIdx.x) < nt;
-      const int64_t o = go + (t0 + threadIdx.x) * a.sg.t;
-      ga[threadIdx.x] = in ? gexp(load_gate<IO, S>(a.la, o, a.gate_io)) : S(1);
-      gb[threadIdx.x] = in ? load_gate<IO, S>(a.be, o, a.gate_io) : S(0);
+      ga[threadIdx.x] = in ? gexp(an) : S(1);
+      gb[threadIdx.x] = in ? bn : S(0);
     }
     __syncthreads();
+    if (t0 + TC < sr.len) fetch(t0 + TC);
     if (y) {
       S p = S(0);  // k.q of token `row`
 #pragma unroll
@@ -216,28 +245,44 @@ __global__ __launch_bounds__(kThreads) void delta_serial_bwd(DeltaArgs a) {
   S* pl = static_cast<S*>(a.part_la) + part0;
   S* pb = static_cast<S*>(a.part_be) + part0;
 
-  for (int64_t t0 = (sr.len - 1) / TC * TC; t0 >= 0 && sr.len > 0; t0 -= TC) {
+  Rows<IO, S, TC, W> qn, kn;
+  S vn = S(0), on = S(0), an = S(0), bn = S(0), sn[NI];
+  const int64_t t_last = sr.len > 0 ? (sr.len - 1) / TC * TC : -1;
+  const auto fetch = [&](int64_t t0) {
+    qn.fetch(q, a.sq.t, t0, sr.len, a.dk);
+    kn.fetch(k, a.sk.t, t0, sr.len, a.dk);
+    vn = fetch_rows<IO, S>(v, a.sv.t, t0, sr.len, r0, a.dv);
+    on = fetch_rows<IO, S>(dy, a.sdy.t, t0, sr.len, r0, a.dv);
+    const int64_t o = go + min(t0 + static_cast<int64_t>(threadIdx.x % TC), sr.len - 1) * a.sg.t;
+    an = load_gate<IO, S>(a.la, o, a.gate_io);
+    bn = load_gate<IO, S>(a.be, o, a.gate_io);
+    const S* c0 =
+        static_cast<const S*>(a.ckpt) + (((slot0 + t0 / TC) * a.H + h) * a.dv + min(r, a.dv - 1)) * a.dk;
+#pragma unroll
+    for (int i = 0; i < NI; ++i) sn[i] = c0[min(col(l, i), a.dk - 1)];
+  };
+  if (t_last >= 0) fetch(t_last);
+  for (int64_t t0 = t_last; t0 >= 0; t0 -= TC) {
     const int nt = static_cast<int>(sr.len - t0 < TC ? sr.len - t0 : TC);
     __syncthreads();
-    stage<IO, S, TC, W>(qs, q, a.sq.t, t0, nt, a.dk);
-    stage<IO, S, TC, W>(ks, k, a.sk.t, t0, nt, a.dk);
+    qn.put(qs, nt, a.dk);
+    kn.put(ks, nt, a.dk);
     if (threadIdx.x < TC * kRows) {
       const int t = threadIdx.x / kRows, c = threadIdx.x % kRows;
       const bool in = t < nt && r0 + c < a.dv;
-      vs[threadIdx.x] = in ? load_as<S>(v, (t0 + t) * a.sv.t + r0 + c) : S(0);
-      gs[threadIdx.x] = in ? scale * load_as<S>(dy, (t0 + t) * a.sdy.t + r0 + c) : S(0);
+      vs[threadIdx.x] = in ? vn : S(0);
+      gs[threadIdx.x] = in ? scale * on : S(0);
     }
     if (threadIdx.x < TC) {
       const bool in = static_cast<int>(threadIdx.x) < nt;
-      const int64_t o = go + (t0 + threadIdx.x) * a.sg.t;
-      ga[threadIdx.x] = in ? gexp(load_gate<IO, S>(a.la, o, a.gate_io)) : S(1);
-      gb[threadIdx.x] = in ? load_gate<IO, S>(a.be, o, a.gate_io) : S(0);
+      ga[threadIdx.x] = in ? gexp(an) : S(1);
+      gb[threadIdx.x] = in ? bn : S(0);
     }
     S st[NI];
-    const S* c0 = static_cast<const S*>(a.ckpt) + (((slot0 + t0 / TC) * a.H + h) * a.dv + r) * a.dk;
 #pragma unroll
-    for (int i = 0; i < NI; ++i) st[i] = (r < a.dv && col(l, i) < a.dk) ? c0[col(l, i)] : S(0);
+    for (int i = 0; i < NI; ++i) st[i] = r < a.dv && col(l, i) < a.dk ? sn[i] : S(0);
     __syncthreads();
+    if (t0 > 0) fetch(t0 - TC);
     for (int t = 0; t < nt; ++t) {
       S kv[NI], p = S(0);
 #pragma unroll
@@ -346,7 +391,7 @@ __global__ __launch_bounds__(kThreads) void delta_serial_sum(DeltaArgs a) {
 // ---- one token: the state read and written once.  Bound by that traffic
 // (64 KB each way per head of 128 x 128); L lanes to a row (four columns
 // each), RU row sets in flight per wave.  256 rows of 16 heads of 128 x 128: 540 MB
-// in 103 us, 5.2 TB/s, what a large copy reaches; one row: 4.3 us, a launch.
+// in 97 us, 5.6 TB/s (a large copy: 5.2); one row: 4.5 us, a launch.
 template <int L>
 __device__ __forceinline__ float sum_l(float x) {
   x = sum16(x);
@@ -387,35 +432,42 @@ __global__ __launch_bounds__(kThreads) void delta_step(DeltaArgs a) {
     return;
   }
   S* st = static_cast<S*>(a.state_out) + (slot * a.H + h) * a.dv * a.dk;
-  S x[RU][4];
+  // All loads at indices clamped into their rows: under conditions each would be
+  // waited for before the next
+  S x[RU][4], qv[4], kv[4], vv[RU], kq = S(0);
+  const IO* q = static_cast<const IO*>(a.q) + b * a.sq.b + hk * a.sq.h;
+  const IO* k = static_cast<const IO*>(a.k) + b * a.sk.b + hk * a.sk.h;
+  const IO* v = static_cast<const IO*>(a.v) + b * a.sv.b + h * a.sv.h;
 #pragma unroll
   for (int u = 0; u < RU; ++u) {
-    const int64_t o = static_cast<int64_t>(r0 + u * RW) * a.dk + c;
-    const bool in = r0 + u * RW < a.dv;
+    const S* row = st + static_cast<int64_t>(min(r0 + u * RW, a.dv - 1)) * a.dk;
     if constexpr (VEC) {
-      Vec4<S> t = {};
-      if (in && c < a.dk) t = *reinterpret_cast<const Vec4<S>*>(st + o);
+      const Vec4<S> t = *reinterpret_cast<const Vec4<S>*>(row + min(c, a.dk - 4));
 #pragma unroll
       for (int i = 0; i < 4; ++i) x[u][i] = t.v[i];
     } else {
 #pragma unroll
-      for (int i = 0; i < 4; ++i) x[u][i] = in && c + i < a.dk ? st[o + i] : S(0);
+      for (int i = 0; i < 4; ++i) x[u][i] = row[min(c + i, a.dk - 1)];
     }
+    vv[u] = load_as<S>(v, min(r0 + u * RW, a.dv - 1));
   }
-  S qv[4], kv[4], vv[RU], kq = S(0);
-  const IO* q = static_cast<const IO*>(a.q) + b * a.sq.b + hk * a.sq.h;
-  const IO* k = static_cast<const IO*>(a.k) + b * a.sk.b + hk * a.sk.h;
-  const IO* v = static_cast<const IO*>(a.v) + b * a.sv.b + h * a.sv.h;
-  const S al = gexp(load_gate<IO, S>(a.la, b * a.sg.b + h * a.sg.h, a.gate_io));
-  const S be = load_gate<IO, S>(a.be, b * a.sg.b + h * a.sg.h, a.gate_io);
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
-    qv[i] = c + i < a.dk ? load_as<S>(q, c + i) : S(0);
-    kv[i] = c + i < a.dk ? load_as<S>(k, c + i) : S(0);
+    qv[i] = load_as<S>(q, min(c + i, a.dk - 1));
+    kv[i] = load_as<S>(k, min(c + i, a.dk - 1));
+  }
+  const int64_t go = b * a.sg.b + h * a.sg.h;
+  const S la = load_gate<IO, S>(a.la, go, a.gate_io), be = load_gate<IO, S>(a.be, go, a.gate_io), al = gexp(la);
+  // columns past dk are zero
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const bool in = c + i < a.dk;
+    qv[i] = in ? qv[i] : S(0);
+    kv[i] = in ? kv[i] : S(0);
+#pragma unroll
+    for (int u = 0; u < RU; ++u) x[u][i] = in ? x[u][i] : S(0);
     kq += qv[i] * kv[i];
   }
-#pragma unroll
-  for (int u = 0; u < RU; ++u) vv[u] = r0 + u * RW < a.dv ? load_as<S>(v, r0 + u * RW) : S(0);
   kq = sum_l<L>(kq);
 #pragma unroll
   for (int u = 0; u < RU; ++u) {
@@ -449,18 +501,12 @@ __global__ __launch_bounds__(kThreads) void delta_step(DeltaArgs a) {
 
 template <typename IO, typename S, int L, bool VEC>
 hipError_t step_ru(const DeltaArgs& a, hipStream_t s) {
-  const auto grid = [&](int ru) {
-    const int rb = 64 / L * ru * (kThreads / 64);
-    return a.B * a.H * ((a.dv + rb - 1) / rb);
-  };
-  // Eight row sets a wave keep more loads in flight, two make more work-groups:
-  // 2 / 8 sets at 16 heads of 128 x 128: 1 row 4.3 / 5.8 us, 16 rows 10.5 / 10.5
-  // (512 work-groups of eight), 32 rows 19.2 / 15.3, 256 rows 155 / 121; of 64 x
-  // 64: 64 rows (1024) 10.3 / 10.8, 256 rows 34.9 / 32.6
-  if (grid(8) >= 1024)
-    delta_step<IO, S, L, 8, VEC><<<dim3(static_cast<unsigned>(grid(8))), kThreads, 0, s>>>(a);
-  else
-    delta_step<IO, S, L, 2, VEC><<<dim3(static_cast<unsigned>(grid(2))), kThreads, 0, s>>>(a);
+  // Two / four / eight row sets a wave at 16 heads of 128 x 128: 1 row 4.3 / 4.6 /
+  // 5.2 us, 32 rows 14.5 / 12.5 / 12.6, 256 rows 97 / 97 / 100; of 64 x 64, 256
+  // rows 26 / 24 / 27
+  constexpr int RU = 4, RB = 64 / L * RU * (kThreads / 64);
+  const int64_t grid = a.B * a.H * ((a.dv + RB - 1) / RB);
+  delta_step<IO, S, L, RU, VEC><<<dim3(static_cast<unsigned>(grid)), kThreads, 0, s>>>(a);
   return hipGetLastError();
 }
 

@@ -336,7 +336,7 @@ __global__ __launch_bounds__(16 * kDwRows) void qknorm_dw(QkArgs a) {
 // l, l + 32, ... that a rotation turns (those past rot: neighbours), element by
 // element, so that again only the sums cross lanes.  Bound by the number of its
 // loads and stores: forward and backward of 4 x 4096 tokens of 24 heads of 120,
-// bf16, take 183 us (one wave a row in fp64: 621; the vector kernels at 128: 122).
+// bf16, take 151 us (one wave a row in fp64: 621; the vector kernels at 128: 120).
 constexpr int kPairLanes = 32;
 
 template <typename S, int U>
@@ -350,36 +350,53 @@ struct Pairs {
       const int u = l + kPairLanes * i;
       in[i] = 2 * u < a.d;
       turned[i] = 2 * u < a.rot;
-      c0[i] = turned[i] && !a.interleaved ? u : 2 * u;
-      c1[i] = turned[i] && !a.interleaved ? u + a.rot / 2 : 2 * u + 1;
+      // past the row: column 0, loaded and not used (a load under a condition
+      // would be waited for before the next one is issued)
+      c0[i] = !in[i] ? 0 : turned[i] && !a.interleaved ? u : 2 * u;
+      c1[i] = !in[i] ? 0 : turned[i] && !a.interleaved ? u + a.rot / 2 : 2 * u + 1;
       c[i] = S(1);
       s[i] = S(0);
     }
   }
   __device__ __forceinline__ void angles(const QkArgs& a, int64_t bt, int l) {
     if (!a.rot) return;
-    const int64_t o = position(a, bt) * (a.rot / 2) + l;
+    const int half = a.rot / 2;
+    const int64_t o = position(a, bt) * half;
+    S cc[U], ss[U];
 #pragma unroll
-    for (int i = 0; i < U; ++i)
-      if (turned[i]) {
-        c[i] = static_cast<const S*>(a.cos)[o + kPairLanes * i];
-        s[i] = static_cast<const S*>(a.sin)[o + kPairLanes * i];
-      }
+    for (int i = 0; i < U; ++i) {
+      const int u = min(l + kPairLanes * i, half - 1);
+      cc[i] = static_cast<const S*>(a.cos)[o + u];
+      ss[i] = static_cast<const S*>(a.sin)[o + u];
+    }
+#pragma unroll
+    for (int i = 0; i < U; ++i) {
+      c[i] = turned[i] ? cc[i] : S(1);
+      s[i] = turned[i] ? ss[i] : S(0);
+    }
   }
   template <typename IO>
   __device__ __forceinline__ void weights(const void* w) {
 #pragma unroll
+    for (int i = 0; i < U; ++i) w0[i] = w1[i] = S(1);
+    if (!w) return;
+#pragma unroll
     for (int i = 0; i < U; ++i) {
-      w0[i] = w && in[i] ? load_as<S>(static_cast<const IO*>(w), c0[i]) : S(1);
-      w1[i] = w && in[i] ? load_as<S>(static_cast<const IO*>(w), c1[i]) : S(1);
+      w0[i] = load_as<S>(static_cast<const IO*>(w), c0[i]);
+      w1[i] = load_as<S>(static_cast<const IO*>(w), c1[i]);
     }
   }
   template <typename IO>
   __device__ __forceinline__ void load(const IO* p, S (&u)[U], S (&v)[U]) const {
 #pragma unroll
     for (int i = 0; i < U; ++i) {
-      u[i] = in[i] ? load_as<S>(p, c0[i]) : S(0);
-      v[i] = in[i] ? load_as<S>(p, c1[i]) : S(0);
+      u[i] = load_as<S>(p, c0[i]);
+      v[i] = load_as<S>(p, c1[i]);
+    }
+#pragma unroll
+    for (int i = 0; i < U; ++i) {
+      u[i] = in[i] ? u[i] : S(0);
+      v[i] = in[i] ? v[i] : S(0);
     }
   }
   template <typename IO>
