@@ -40,9 +40,6 @@ __device__ __forceinline__ __amdgpu_buffer_rsrc_t rows_f32(const float* base, in
   const int64_t n = len - t0 < 64 ? len - t0 : 64;
   return buffer_rsrc(base + (n > 0 ? t0 * st : 0), n > 0 ? static_cast<int>(((n - 1) * st + d) * 4) : 0);
 }
-__device__ __forceinline__ f32x4 load_f32x4(__amdgpu_buffer_rsrc_t r, uint32_t off) {
-  return __builtin_bit_cast(f32x4, __builtin_amdgcn_raw_buffer_load_b128(r, off, 0, 0));
-}
 
 // Rows 16 tb + 4g + q, column r of a [64][VP] tile of a record, as results lie:
 // `at` = (4g VP + r) bytes.

@@ -203,6 +203,18 @@ __device__ __forceinline__ float load4(__amdgpu_buffer_rsrc_t r, uint32_t off) {
   return __builtin_bit_cast(float, __builtin_amdgcn_raw_buffer_load_b32(r, off, 0, 0));
 }
 
+__device__ __forceinline__ f32x4 load_f32x4(__amdgpu_buffer_rsrc_t r, uint32_t off) {
+  return __builtin_bit_cast(f32x4, __builtin_amdgcn_raw_buffer_load_b128(r, off, 0, 0));
+}
+// A state [dv][dk] of a head as a buffer, and the byte offset of columns c .. c +
+// 3 of row r in it: zeros past dv and past dk, and everywhere if p is NULL.
+__device__ __forceinline__ __amdgpu_buffer_rsrc_t state_rsrc(const float* p, int dv, int dk) {
+  return buffer_rsrc(p, p ? dv * dk * 4 : 0);
+}
+__device__ __forceinline__ uint32_t state_off(int r, int c, int dk) {
+  return c < dk ? static_cast<uint32_t>((r * dk + c) * 4) : kPastEnd;
+}
+
 // Factors of the decay inside a chunk for the waves that form P (lane = token,
 // m_x the l before its block x of 16), by a loading wave into [6][64] of LDS:
 // scale e^(l_i - m_x) of block x's own tokens; e^(m_x - l_j) of those before it

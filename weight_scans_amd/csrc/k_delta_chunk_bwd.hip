@@ -76,11 +76,11 @@ __global__ __launch_bounds__(64 * (2 * NW + 2)) void delta_chunk_rev(ChunkArgs c
   const int nc = segment_of(sr, slot0, seg, ca.n_seg);
   const int64_t rec0 = slot0 * a.H + h;
   // the adjoint after the last chunk and the state there
-  const float* lam_end = last ? static_cast<const float*>(a.dstate_out)
+  const int64_t dd = static_cast<int64_t>(a.dv) * a.dk;
+  const float* lam_end = last     ? (a.dstate_out ? static_cast<const float*>(a.dstate_out) + head * dd : nullptr)
                          : STATES ? nullptr
-                                  : ca.seg_l + (head * ca.n_seg + seg) * a.dv * a.dk;
-  const float* state_end = last ? ca.st : ca.seg_s + (head * ca.n_seg + seg + 1) * a.dv * a.dk;
-  const int64_t end0 = last ? head * a.dv * a.dk : 0;
+                                  : ca.seg_l + (head * ca.n_seg + seg) * dd;
+  const float* state_end = last ? ca.st + head * dd : ca.seg_s + (head * ca.n_seg + seg + 1) * dd;
 
   // Step i: the helpers take chunk nc - 1 - i, the state waves the one before
   // (nc - i), and the helpers finish the decay's gradient of the one before
@@ -177,16 +177,19 @@ __global__ __launch_bounds__(64 * (2 * NW + 2)) void delta_chunk_rev(ChunkArgs c
     };
     if (nc > 0) fetch(nc - 1);
     float z = 0.f;  // <dL/dS, S> after the chunk, over this wave's rows
-    if (!STATES && lam_end && r0 + index1(w, l) < a.dv) {
-      const int64_t so = end0 + static_cast<int64_t>(r0 + index1(w, l)) * a.dk;
+    if (!STATES && lam_end) {
+      const __amdgpu_buffer_rsrc_t ru = state_rsrc(lam_end, a.dv, a.dk), rs = state_rsrc(state_end, a.dv, a.dk);
+      f32x4 u[NB], s[NB];
+#pragma unroll
+      for (int b = 0; b < NB; ++b) {
+        const uint32_t o = state_off(r0 + index1(w, l), index4(b, g), a.dk);
+        u[b] = load_f32x4(ru, o);
+        s[b] = load_f32x4(rs, o);
+      }
 #pragma unroll
       for (int b = 0; b < NB; ++b)
-        if (index4(b, g) < a.dk) {
-          const f32x4 u = *reinterpret_cast<const f32x4*>(lam_end + so + index4(b, g));
-          const f32x4 s = *reinterpret_cast<const f32x4*>(state_end + so + index4(b, g));
 #pragma unroll
-          for (int q = 0; q < 4; ++q) z = fmaf(u[q], s[q], z);
-        }
+        for (int q = 0; q < 4; ++q) z = fmaf(u[b][q], s[b][q], z);
     }
     z = wave_sum(z);
     for (int i = 0; i <= nc + 1; ++i) {
@@ -253,12 +256,10 @@ __global__ __launch_bounds__(64 * (2 * NW + 2)) void delta_chunk_rev(ChunkArgs c
   // ---- adjoint states
   const TileLane<VW> tv = tile_lane<VW>(lane);
   const int r = r0 + index1(wave, l);
+  const __amdgpu_buffer_rsrc_t first = state_rsrc(lam_end, a.dv, a.dk);
   f32x4 S[NB];
 #pragma unroll
-  for (int b = 0; b < NB; ++b)
-    S[b] = lam_end && r < a.dv && index4(b, g) < a.dk
-               ? *reinterpret_cast<const f32x4*>(lam_end + end0 + static_cast<int64_t>(r) * a.dk + index4(b, g))
-               : zero4();
+  for (int b = 0; b < NB; ++b) S[b] = load_f32x4(first, state_off(r, index4(b, g), a.dk));
   bf16x8 yf[12], ef[2];
   const int rt = tile * NW + wave, n_rt = delta_row_tiles(a.dv);
   const auto fetch = [&](int c) {

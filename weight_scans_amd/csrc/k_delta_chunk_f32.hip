@@ -243,12 +243,11 @@ __global__ __launch_bounds__(64 * (2 * NW + 1)) void delta_chunk_f32(ChunkArgs c
   // ---- states
   const int r = r0 + 16 * wave + l;
   const int64_t so = (head * a.dv + r) * a.dk;
+  const __amdgpu_buffer_rsrc_t first = state_rsrc(
+      a.state_in ? static_cast<const float*>(a.state_in) + head * a.dv * a.dk : nullptr, a.dv, a.dk);
   f32x4 S[NB];
 #pragma unroll
-  for (int b = 0; b < NB; ++b)
-    S[b] = a.state_in && r < a.dv && 16 * b + 4 * g < a.dk
-               ? *reinterpret_cast<const f32x4*>(static_cast<const float*>(a.state_in) + so + 16 * b + 4 * g)
-               : zero4();
+  for (int b = 0; b < NB; ++b) S[b] = load_f32x4(first, state_off(r, 16 * b + 4 * g, a.dk));
   const float* vp = static_cast<const float*>(a.v) + sr.b * a.sv.b + h * a.sv.h + sr.t0 * a.sv.t;
   uint32_t vo[4];
 #pragma unroll

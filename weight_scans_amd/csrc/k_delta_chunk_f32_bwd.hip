@@ -84,16 +84,21 @@ __global__ __launch_bounds__(64 * (NW + 1), 1) void delta_rev_f32(ChunkArgs ca) 
   const float sc = static_cast<float>(a.scale);
   f32x4 S[NB];  // Lam^T
   float z = 0.f;  // <Lam, state> after the chunk, over this wave's rows
+  {
+    const int64_t at = head * a.dv * a.dk;
+    const __amdgpu_buffer_rsrc_t ru =
+        state_rsrc(a.dstate_out ? static_cast<const float*>(a.dstate_out) + at : nullptr, a.dv, a.dk);
+    const __amdgpu_buffer_rsrc_t rs = state_rsrc(a.dstate_out ? ca.st + at : nullptr, a.dv, a.dk);
+    f32x4 s[NB];
 #pragma unroll
-  for (int b = 0; b < NB; ++b) {
-    S[b] = zero4();
-    const int c = 16 * b + 4 * g;
-    if (a.dstate_out && r < a.dv && c < a.dk) {
-      S[b] = *reinterpret_cast<const f32x4*>(static_cast<const float*>(a.dstate_out) + so + c);
-      const f32x4 s = *reinterpret_cast<const f32x4*>(ca.st + so + c);
-#pragma unroll
-      for (int q = 0; q < 4; ++q) z = fmaf(S[b][q], s[q], z);
+    for (int b = 0; b < NB; ++b) {
+      S[b] = load_f32x4(ru, state_off(r, 16 * b + 4 * g, a.dk));
+      s[b] = load_f32x4(rs, state_off(r, 16 * b + 4 * g, a.dk));
     }
+#pragma unroll
+    for (int b = 0; b < NB; ++b)
+#pragma unroll
+      for (int q = 0; q < 4; ++q) z = fmaf(S[b][q], s[b][q], z);
   }
   z = wave_sum(z);
   const float* vp = static_cast<const float*>(a.v) + sr.b * a.sv.b + h * a.sv.h + sr.t0 * a.sv.t;
@@ -371,10 +376,18 @@ __device__ __forceinline__ void grad_block(const ChunkArgs& ca, const GradLds<DK
       }
     }
     if (W == 3) {  // gates: token `lane`, over the row tiles
-      float dl = 0.f, db = 0.f;
-      for (int i = 0; i < n_rt; ++i) {
-        dl += ca.zf[(rec * n_rt + i) * 64 + lane];
-        db += ca.bf[(rec * n_rt + i) * 64 + lane];
+      const __amdgpu_buffer_rsrc_t rz = buffer_rsrc(ca.zf + rec * n_rt * 64, n_rt * 256);
+      const __amdgpu_buffer_rsrc_t rb = buffer_rsrc(ca.bf + rec * n_rt * 64, n_rt * 256);
+      float z[8], b[8], dl = 0.f, db = 0.f;
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        z[i] = load4(rz, (i * 64 + lane) * 4);
+        b[i] = load4(rb, (i * 64 + lane) * 4);
+      }
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        dl += z[i];
+        db += b[i];
       }
       // a token that forgets everything has no gradient to its decay
       const float w = gt[192 + lane];

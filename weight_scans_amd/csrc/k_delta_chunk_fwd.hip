@@ -279,18 +279,20 @@ __global__ __launch_bounds__((kFwdThreads<NW, MODE>)) void delta_chunk_fwd(Chunk
   const int r = r0 + index1(wave, l);
   const int64_t so = (head * a.dv + r) * a.dk;
   // segment states [head][n_seg][dv][dk], M [head][n_seg][dk][dk]
-  const auto seg_at = [&](int s) { return ((head * ca.n_seg + s) * a.dv + r) * a.dk; };
-  const float* from = seg == 0 ? (a.state_in ? static_cast<const float*>(a.state_in) + so : nullptr)
-                      : OUT    ? ca.seg_s + seg_at(seg)
-                               : nullptr;
+  const auto seg_at = [&](int s) { return (head * ca.n_seg + s) * a.dv * a.dk; };
+  const float* from = ident      ? nullptr
+                      : seg == 0 ? (a.state_in ? static_cast<const float*>(a.state_in) + head * a.dv * a.dk : nullptr)
+                      : OUT      ? ca.seg_s + seg_at(seg)
+                                 : nullptr;
+  const __amdgpu_buffer_rsrc_t first = state_rsrc(from, a.dv, a.dk);
   f32x4 S[NB];
 #pragma unroll
-  for (int b = 0; b < NB; ++b) {
-    const int c = index4(b, g);
-    S[b] = from && r < a.dv && c < a.dk ? *reinterpret_cast<const f32x4*>(from + c) : zero4();
-    if (ident)
+  for (int b = 0; b < NB; ++b) S[b] = load_f32x4(first, state_off(r, index4(b, g), a.dk));
+  if (ident) {
 #pragma unroll
-      for (int q = 0; q < 4; ++q) S[b][q] = c + q == r ? 1.f : 0.f;
+    for (int b = 0; b < NB; ++b)
+#pragma unroll
+      for (int q = 0; q < 4; ++q) S[b][q] = index4(b, g) + q == r ? 1.f : 0.f;
   }
   bf16x8 yf[12];
   const uint16_t* yp = ca.yf + rec0 * kYf + lane * 8;
@@ -454,7 +456,7 @@ __global__ __launch_bounds__((kFwdThreads<NW, MODE>)) void delta_chunk_fwd(Chunk
   lds_barrier();
   float* to = OUT ? (seg == ca.n_seg - 1 && a.state_out ? static_cast<float*>(a.state_out) + so : nullptr)
               : ident ? ca.seg_m + ((head * ca.n_seg + seg) * a.dk + r) * a.dk
-                      : ca.seg_s + seg_at(seg + 1);
+                      : ca.seg_s + seg_at(seg + 1) + static_cast<int64_t>(r) * a.dk;
   if (r < (ident ? a.dk : a.dv)) {
 #pragma unroll
     for (int b = 0; b < NB; ++b)
