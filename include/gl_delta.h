@@ -19,8 +19,8 @@
  *   log_alpha, beta and gradients   [B][H][T]        gate dtype
  *   states                          [n][H][dv][dk]   dense, fp64 if io is F64, else fp32
  * Pointers are 16-byte aligned; those of gates, and of q, k, v, y and their
- * gradients off the matrix-core paths, only to their elements (an F32 forward
- * that saves nothing takes the other path by itself where they are not).
+ * gradients off the matrix-core paths, only to their elements (a forward that
+ * saves nothing takes the other path by itself where they are not).
  * Value head h reads query and key head h / (H / Hk); dq and dk sum over the
  * value heads that share them.
  *
@@ -126,7 +126,8 @@ const char* gl_delta_path_name(const gl_delta_desc_t* desc);
  *   n = x / sqrt(mean(x^2) + eps),  z = w * n,  out = scale Rot_p(z)
  *
  * for each row of d elements of q [B][Hq][T][d] and k [B][Hk][T][d] (strided as
- * above), w = wq or wk [d] io dtype (NULL = ones), scale = q_scale or k_scale
+ * above; all pointers here aligned to their elements, the workspace to 16
+ * bytes), w = wq or wk [d] io dtype (NULL = ones), scale = q_scale or k_scale
  * (1 / sqrt(d) gives rows of unit length).  Rot_p turns the pairs (i, i + rot/2)
  * of the first rot columns ((2i, 2i + 1) with GL_FLAG_INTERLEAVED) by the angle
  * whose cosine and sine are cos[p][i], sin[p][i] (tables [n_pos][rot/2], fp32,

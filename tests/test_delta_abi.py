@@ -263,12 +263,12 @@ def test_norm_pointers_refused():
     for i in (0, 1, 4, 5, 7, 8):
         assert qk_fwd(d, [(i, None)]) == INVALID, i
     for i in (0, 1, 2, 3, 4, 5, 7, 8):
-        assert qk_fwd(d, [(i, FAKE + 8)]) == MISALIGNED, i
+        assert qk_fwd(d, [(i, FAKE + 1)]) == MISALIGNED, i
     assert qk_fwd(d, [(6, FAKE + 2)]) == MISALIGNED
     for i in (0, 1, 4, 5, 7, 8, 9, 10):
         assert qk_bwd(d, [(i, None)]) == INVALID, i
     for i in (0, 1, 2, 3, 4, 5, 7, 8, 9, 10, 11, 12):
-        assert qk_bwd(d, [(i, FAKE + 8)]) == MISALIGNED, i
+        assert qk_bwd(d, [(i, FAKE + 1)]) == MISALIGNED, i
     n = ctypes.c_size_t()
     assert status("gl_qknorm_rope_workspace_size", ctypes.byref(d), ctypes.byref(n)) == 0 and n.value > 0
     assert qk_bwd(d, nb=n.value - 1) == SMALL and qk_bwd(d, wsp=None) == INVALID

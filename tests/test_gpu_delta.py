@@ -303,6 +303,19 @@ def test_fp32_chunks_forgetting():
     run_case(5, 2, 2, 2, 140, 64, 64, F32, edit=edit, saved=False)
 
 
+@pytest.mark.parametrize("T", [70, 5])
+def test_bf16_unaligned_views_take_the_serial_kernel(T):
+    x = inputs(4, 1, 2, 2, T, 64, 64, BF16, BF16)
+    y, end = delta(x["q"], x["k"], x["v"], x["log_alpha"], x["beta"], 0.125, x["state"])
+    g = to_gpu(x, BF16, BF16)
+    wide = lambda t: torch.nn.functional.pad(t, (4, 4))[..., 4:-4]  # noqa: E731
+    args = wide(g["q"]), wide(g["k"]), wide(g["v"]), g["log_alpha"], g["beta"]
+    got, gend, _ = ws.gl_delta_fwd(*args, state=g["state"], want_state=True)
+    assert rel(got, y) <= TOL[BF16] and rel(gend, end) <= STATE_TOL[BF16]
+    with pytest.raises(ws.GLScanError):
+        ws.gl_delta_fwd(*args, state=g["state"], save=True)
+
+
 def test_fp32_unaligned_views_take_the_serial_kernel():
     """Slices of a wider row that start at 4 bytes: same results, token by token."""
     x = inputs(4, 1, 2, 2, 70, 64, 64, F32, F32)
@@ -396,3 +409,21 @@ def test_calls_of_one_kind_then_others():
         a = ws.gl_qknorm_rope_fwd(q, q, cos=cos, sin=sin, pos0=p)[0]
         pos = torch.full((3, 1), p, dtype=torch.int32, device="cuda")
         assert torch.equal(a, ws.gl_qknorm_rope_fwd(q, q, cos=cos, sin=sin, pos=pos)[0])
+
+
+def test_autograd_of_unaligned_slices():
+    x = inputs(61, 1, 2, 2, 80, 64, 64, BF16, BF16)
+    names = ["q", "k", "v", "log_alpha", "beta"]
+    for n in names:
+        x[n].requires_grad_(True)
+    y, _ = delta(x["q"], x["k"], x["v"], x["log_alpha"], x["beta"], 0.125)
+    want = torch.autograd.grad((y * x["dy"]).sum(), [x[n] for n in names])
+    g = to_gpu(x, BF16, BF16)
+    leaves = [torch.nn.functional.pad(g[n], (4, 4)) if n in "qkv" else g[n].clone() for n in names]
+    for p in leaves:
+        p.requires_grad_(True)
+    got, _ = ws.delta_rule(*[p[..., 4:-4] if p.dim() == 4 else p for p in leaves])
+    (got.float() * g["dy"].float()).sum().backward()
+    assert rel(got, y) <= TOL[BF16]
+    for n, p, w in zip(names, leaves, want):
+        assert rel(p.grad[..., 4:-4] if p.dim() == 4 else p.grad, w) <= TOL[BF16], n

@@ -167,3 +167,28 @@ def test_autograd_repeats_bitwise():
         runs.append([a, b, *torch.autograd.grad(a.float().sum() + b.float().square().sum(), x)])
     for a, b in zip(*runs):
         assert torch.equal(a, b)
+
+
+@pytest.mark.parametrize("d,rot", [(92, 46), (84, 84), (64, 64), (128, 64), (20, 8), (7, 2)])
+@pytest.mark.parametrize("dtype", [F32, BF16])
+def test_slices_of_a_fused_row_at_any_element(d, rot, dtype):
+    """q and k inside one wider row, k's part at an offset that no 16 bytes divide."""
+    torch.manual_seed(d)
+    rows = torch.randn(2, 13, 1 + 3 * d + 2 * d, device="cuda").to(dtype)
+    q = rows[..., 1 : 1 + 3 * d].unflatten(-1, (3, d)).transpose(1, 2)
+    k = rows[..., 1 + 3 * d :].unflatten(-1, (2, d)).transpose(1, 2)
+    wide = torch.randn(2, d + 1, device="cuda").to(dtype)
+    wq, wk = wide[0, 1:], wide[1, 1:]
+    cos, sin = torch.randn(2, 16 * (rot // 2) + 1, device="cuda")[:, 1:].unflatten(-1, (16, rot // 2))
+    oq, ok = ws.gl_qknorm_rope_fwd(q, k, wq, wk, cos, sin)
+    dq = torch.randn(2, 3, 13, d + 1, device="cuda").to(dtype)[..., 1:]
+    dk = torch.randn(2, 2, 13, d + 1, device="cuda").to(dtype)[..., 1:]
+    got = ws.gl_qknorm_rope_bwd(q, k, wq, wk, cos, sin, dq, dk)
+    pos = torch.arange(13)[None].expand(2, 13)
+    c = lambda t: t.detach().double().cpu()  # noqa: E731
+    for x, w, o, up, gx, gw in ((q, wq, oq, dq, got[0], got[2]), (k, wk, ok, dk, got[1], got[3])):
+        xx, ww = c(x).requires_grad_(True), c(w).requires_grad_(True)
+        y = qknorm(xx, ww, c(cos), c(sin), pos, 1e-6, 1.0)
+        rx, rw = torch.autograd.grad((y * c(up)).sum(), [xx, ww])
+        assert rel(o, y) <= TOL[dtype]
+        assert rel(gx, rx) <= TOL[dtype] and rel(gw, rw) <= DW_TOL[dtype]

@@ -177,6 +177,7 @@ gl_status_t make_plan(const gl_delta_desc_t* d, Plan* p) {
   }
   if (chunks && gls::delta_chunk_f32_ok(p->io, a)) {
     p->chunk32 = true;
+    p->align = 16;
     p->name = d->dk <= 64 ? "delta-mfma-f32-64" : "delta-mfma-f32-128";
     p->slots = gls::chunk_slots(p->packed, p->N, d->T, gls::kDeltaChunk);
     if (double(p->slots) * double(d->H) > 2147483647.0)
@@ -316,7 +317,7 @@ gl_status_t gl_delta_fwd(const gl_delta_desc_t* desc, const void* q, const void*
   if (st != GL_SUCCESS) return st;
   if (p.N * desc->H == 0) return GL_SUCCESS;
   if ((st = check_cu(p, cu_seqlens)) != GL_SUCCESS) return st;
-  if (p.tok > 0 && (st = check_ptrs(true, {q, k, v, y}, p.align)) != GL_SUCCESS) return st;
+  if (p.tok > 0 && (st = check_ptrs(true, {q, k, v, y}, saved ? p.align : p.elem)) != GL_SUCCESS) return st;
   if (p.tok > 0 && (st = check_ptrs(true, {log_alpha, beta}, p.gate)) != GL_SUCCESS) return st;
   if ((st = check_ptrs(false, {state_in, state_out, saved})) != GL_SUCCESS) return st;
   if ((st = check_ws(ws, ws_bytes, p.fwd_ws + (saved ? 0 : p.gate_bytes))) != GL_SUCCESS) return st;
@@ -324,21 +325,19 @@ gl_status_t gl_delta_fwd(const gl_delta_desc_t* desc, const void* q, const void*
   gls::DeltaArgs a = base_args(desc, p);
   a.q = q; a.k = k; a.v = v; a.la = log_alpha; a.be = beta;
   a.state_in = state_in; a.cu = cu_seqlens; a.y = y; a.state_out = state_out; a.ckpt = saved;
-  const bool serial = p.brief && !saved;
-  if (p.chunk && !serial) {
-    if (p.tok > 0 && !gls::delta_rows_ok(a.sy, a.dv))
-      return fail(GL_ERROR_NOT_SUPPORTED, "strides of y: multiples of 8, rows apart");
-    return chunk_fwd(chunk_args(a, p, saved, ws), static_cast<hipStream_t>(stream));
-  }
-  if (p.chunk32 && !serial) {
-    const bool fits = !(misaligned(q) || misaligned(k) || misaligned(y)) && gls::delta_rows_f32_ok(a.sy, a.dv);
-    if (saved && !fits)
-      return fail(misaligned(q) || misaligned(k) || misaligned(y) ? GL_ERROR_MISALIGNED : GL_ERROR_NOT_SUPPORTED,
-                  "q, k and y of a training call: 16-byte aligned, strides multiples of 4, rows apart");
-    if (fits)
-      return hip_status(gls::launch_delta_chunk_f32(chunk32_args(a, p, saved, ws), static_cast<hipStream_t>(stream)),
-                        "delta forward launch");
-    // else token by token, without the workspace
+  // Chunks, or token by token (without the workspace) where that is allowed and
+  // faster, or the only way: alignment and the strides of y are known here only
+  if (p.chunk || p.chunk32) {
+    const bool rows = p.chunk ? gls::delta_rows_ok(a.sy, a.dv) : gls::delta_rows_f32_ok(a.sy, a.dv);
+    const bool fits = rows && !(misaligned(q) || misaligned(k) || misaligned(v) || misaligned(y));
+    if (saved && p.tok > 0 && !fits)
+      return fail(rows ? GL_ERROR_MISALIGNED : GL_ERROR_NOT_SUPPORTED,
+                  "q, k, v, y of a training call: 16-byte aligned, rows apart, strides multiples of 16 bytes");
+    if (saved || (fits && !p.brief)) {
+      const hipStream_t s = static_cast<hipStream_t>(stream);
+      return p.chunk ? chunk_fwd(chunk_args(a, p, saved, ws), s)
+                     : hip_status(gls::launch_delta_chunk_f32(chunk32_args(a, p, saved, ws), s), "delta forward launch");
+    }
   }
   return hip_status(gls::launch_delta_serial_fwd(p.io, a, static_cast<hipStream_t>(stream)), "delta forward launch");
 }
@@ -389,8 +388,6 @@ gl_status_t gl_delta_bwd(const gl_delta_desc_t* desc, const void* q, const void*
     return hip_status(gls::launch_delta_chunk_bwd(c, s), "delta backward launch");
   }
   if (p.chunk32) {
-    for (const void* x : {q, k, dy, static_cast<const void*>(dv)})
-      if (misaligned(x)) return fail(GL_ERROR_MISALIGNED, "q, k, dy and dv: 16-byte aligned");
     if (p.tok > 0 && !(gls::delta_rows_f32_ok(a.sdy, a.dv) && gls::delta_rows_f32_ok(a.sdv, a.dv)))
       return fail(GL_ERROR_NOT_SUPPORTED, "strides of dy, dv: multiples of 4, rows apart");
     float *lf, *gf, *zf, *bf;
@@ -494,13 +491,16 @@ static gls::QkArgs qk_args(const gl_qknorm_desc_t* d, const void* q, const void*
   return a;
 }
 
+static size_t qk_elem(const gl_qknorm_desc_t* d) { return d->io_dtype == GL_DTYPE_F64 ? 8 : d->io_dtype == GL_DTYPE_F32 ? 4 : 2; }
+static size_t qk_comp(const gl_qknorm_desc_t* d) { return d->io_dtype == GL_DTYPE_F64 ? 8 : 4; }
+
 static gl_status_t check_qk_ptrs(const gl_qknorm_desc_t* d, const void* q, const void* k, const void* wq,
                                  const void* wk, const void* cos, const void* sin, const int32_t* pos) {
   gl_status_t st;
-  if (d->Hq && (st = check_ptrs(true, {q})) != GL_SUCCESS) return st;
-  if (d->Hk && (st = check_ptrs(true, {k})) != GL_SUCCESS) return st;
-  if ((st = check_ptrs(false, {wq, wk})) != GL_SUCCESS) return st;
-  if (d->rot && (st = check_ptrs(true, {cos, sin})) != GL_SUCCESS) return st;
+  if (d->Hq && (st = check_ptrs(true, {q}, qk_elem(d))) != GL_SUCCESS) return st;
+  if (d->Hk && (st = check_ptrs(true, {k}, qk_elem(d))) != GL_SUCCESS) return st;
+  if ((st = check_ptrs(false, {wq, wk}, qk_elem(d))) != GL_SUCCESS) return st;
+  if (d->rot && (st = check_ptrs(true, {cos, sin}, qk_comp(d))) != GL_SUCCESS) return st;
   if (reinterpret_cast<uintptr_t>(pos) & 3) return fail(GL_ERROR_MISALIGNED, "pos not 4-byte aligned");
   return GL_SUCCESS;
 }
@@ -512,8 +512,8 @@ gl_status_t gl_qknorm_rope_fwd(const gl_qknorm_desc_t* desc, const void* q, cons
   if (st != GL_SUCCESS) return st;
   if (desc->B * desc->T * (desc->Hq + desc->Hk) == 0) return GL_SUCCESS;
   if ((st = check_qk_ptrs(desc, q, k, wq, wk, cos, sin, pos)) != GL_SUCCESS) return st;
-  if (desc->Hq && (st = check_ptrs(true, {out_q})) != GL_SUCCESS) return st;
-  if (desc->Hk && (st = check_ptrs(true, {out_k})) != GL_SUCCESS) return st;
+  if (desc->Hq && (st = check_ptrs(true, {out_q}, qk_elem(desc))) != GL_SUCCESS) return st;
+  if (desc->Hk && (st = check_ptrs(true, {out_k}, qk_elem(desc))) != GL_SUCCESS) return st;
   gls::QkArgs a = qk_args(desc, q, k, wq, wk, cos, sin, pos);
   a.out[0] = out_q; a.out[1] = out_k;
   return hip_status(gls::launch_qknorm_fwd(desc->io_dtype, a, static_cast<hipStream_t>(stream)),
@@ -538,9 +538,9 @@ gl_status_t gl_qknorm_rope_bwd(const gl_qknorm_desc_t* desc, const void* q, cons
   if (st != GL_SUCCESS) return st;
   const bool any = desc->B * desc->T > 0;
   if (any && (st = check_qk_ptrs(desc, q, k, wq, wk, cos, sin, pos)) != GL_SUCCESS) return st;
-  if (any && desc->Hq && (st = check_ptrs(true, {dout_q, dq})) != GL_SUCCESS) return st;
-  if (any && desc->Hk && (st = check_ptrs(true, {dout_k, dk})) != GL_SUCCESS) return st;
-  if ((st = check_ptrs(false, {dwq, dwk})) != GL_SUCCESS) return st;
+  if (any && desc->Hq && (st = check_ptrs(true, {dout_q, dq}, qk_elem(desc))) != GL_SUCCESS) return st;
+  if (any && desc->Hk && (st = check_ptrs(true, {dout_k, dk}, qk_elem(desc))) != GL_SUCCESS) return st;
+  if ((st = check_ptrs(false, {dwq, dwk}, qk_comp(desc))) != GL_SUCCESS) return st;
   if ((!any || desc->Hq + desc->Hk == 0) && !dwq && !dwk) return GL_SUCCESS;
   size_t need = 0;
   if ((st = gl_qknorm_rope_workspace_size(desc, &need)) != GL_SUCCESS) return st;

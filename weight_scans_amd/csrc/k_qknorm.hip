@@ -601,16 +601,19 @@ int lanes(int d) {
   return l;
 }
 
-// The vector kernels load runs of eight elements: rows, strides and tables
-// have to keep 16-byte alignment (pointers are checked by the caller).
+// The vector kernels load runs of eight elements: pointers, strides and tables
+// have to keep 16-byte alignment.
+bool aligned(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15) == 0; }
 bool aligned(int io, const Str3& s) {
   const int m = io == IO_BF16 ? 8 : io == IO_F32 ? 4 : 2;
   return s.b % m == 0 && s.h % m == 0 && s.t % m == 0;
 }
 bool vector_ok(int io, const QkArgs& a, bool bwd) {
   bool ok = a.d % 16 == 0 && a.rot % 16 == 0;
+  ok = ok && aligned(a.cos) && aligned(a.sin);
   for (int i = 0; i < 2; ++i)
-    ok = ok && aligned(io, a.sx[i]) && aligned(io, a.so[i]) && (!bwd || aligned(io, a.sdo[i]));
+    ok = ok && aligned(a.x[i]) && aligned(a.w[i]) && aligned(a.out[i]) && (!bwd || aligned(a.dout[i])) &&
+         aligned(io, a.sx[i]) && aligned(io, a.so[i]) && (!bwd || aligned(io, a.sdo[i]));
   return ok;
 }
 

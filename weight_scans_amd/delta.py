@@ -463,6 +463,8 @@ def delta_rule(q, k, v, log_alpha, beta, *, scale=None, state=None, cu_seqlens=N
     if not (_torch().is_grad_enabled() and any(t is not None and t.requires_grad for t in inputs)):
         return gl_delta_fwd(q, k, v, log_alpha, beta, scale=scale, state=state, want_state=want_state,
                             cu_seqlens=cu_seqlens)[:2]
+    # slices that begin between two 16-byte units: training wants them aligned
+    q, k, v = (t if t.data_ptr() % 16 == 0 else t.clone(memory_format=_torch().contiguous_format) for t in (q, k, v))
     return _functions()[0].apply(q, k, v, log_alpha, beta, state, scale, cu_seqlens, want_state)
 
 
