@@ -6,7 +6,7 @@
 //   dx = r (w dz - n mean(w dz * n))
 //
 // Bound by reading and writing each row once: 4 x 4096 tokens of 16 + 8 heads of
-// 128, bf16, forward 201 MB in 43 us (4.7 TB/s), backward 302 MB in 75 us (4.0 TB/s)
+// 128, bf16, forward 201 MB in 43 us (4.7 TB/s), backward 302 MB in 72 us (4.2 TB/s)
 // and 4 us for the sums of dw; a large copy reaches 5.2.  Vector kernels (d and rot
 // multiples of 16): a lane owns 16 columns of a row as two runs of eight that
 // hold whole pairs (run j and the run rot/2 further on, or two neighbouring
@@ -89,6 +89,14 @@ __device__ __forceinline__ S sum_group(S x) {
 #pragma unroll
   for (int m = L / 2; m >= 1; m >>= 1) x += __shfl_xor(x, m, 64);
   return x;
+}
+
+// Work-groups (and parts of the dw sums) that the backward gives to q and to k: in
+// the ratio of their heads, so that both end together (16 and 8 heads: 75 -> 71 us).
+// 1024 for the larger: 1365 78 us, 2048 78, 4096 85.
+__host__ __device__ __forceinline__ int64_t parts_of(const QkArgs& a, int which) {
+  const int most = a.Hn[0] > a.Hn[1] ? a.Hn[0] : a.Hn[1];
+  return most ? (a.n_part * a.Hn[which] + most - 1) / most : 1;
 }
 
 // Where a lane's two runs of eight begin, and its angles.
@@ -237,9 +245,9 @@ __global__ __launch_bounds__(kThreads) void qknorm_bwd_v(QkArgs a) {
   if (in) load_w<IO, S>(a.w[which], c0, c1, w0, w1);
   const S scale = static_cast<S>(a.scale[which]);
   const int heads = a.Hn[which], parts = (heads + a.hpg - 1) / a.hpg;
-  const int64_t units = a.B * a.T * parts;
-  for (int64_t un = blockIdx.x * static_cast<int64_t>(G) + gi; un < units;
-       un += static_cast<int64_t>(gridDim.x) * G) {
+  const int64_t units = a.B * a.T * parts, groups = parts_of(a, which);
+  if (blockIdx.x >= groups) return;
+  for (int64_t un = blockIdx.x * static_cast<int64_t>(G) + gi; un < units; un += groups * G) {
     const int64_t bt = un / parts;
     const int h0 = static_cast<int>(un % parts) * a.hpg, h1 = min(heads, h0 + a.hpg);
     const int64_t b = bt / a.T, t = bt % a.T;
@@ -312,7 +320,7 @@ __global__ __launch_bounds__(16 * kDwRows) void qknorm_dw(QkArgs a) {
   if (!a.dw[which]) return;
   const int c = blockIdx.x * 16 + l, cc = min(c, a.d - 1);
   const S* part = static_cast<const S*>(a.part) + static_cast<int64_t>(which) * a.n_part * a.d + cc;
-  const int n = static_cast<int>(a.n_part);
+  const int n = static_cast<int>(parts_of(a, which));
   S x = S(0);
   for (int p = w; p < n; p += 8 * kDwRows) {
     S v[8];
@@ -448,13 +456,14 @@ __global__ __launch_bounds__(kThreads) void qknorm_bwd_p(QkArgs a) {
   const int which = blockIdx.y, l = threadIdx.x % kPairLanes, gi = threadIdx.x / kPairLanes;
   const S scale = static_cast<S>(a.scale[which]);
   const int heads = a.Hn[which], parts = (heads + a.hpg - 1) / a.hpg;
-  const int64_t units = a.B * a.T * parts;
+  const int64_t units = a.B * a.T * parts, groups = parts_of(a, which);
+  if (blockIdx.x >= groups) return;
   Pairs<S, U> p(a, l);
   p.template weights<IO>(a.w[which]);
   S d0[U], d1[U];
 #pragma unroll
   for (int i = 0; i < U; ++i) d0[i] = d1[i] = S(0);
-  for (int64_t un = blockIdx.x * static_cast<int64_t>(G) + gi; un < units; un += static_cast<int64_t>(gridDim.x) * G) {
+  for (int64_t un = blockIdx.x * static_cast<int64_t>(G) + gi; un < units; un += groups * G) {
     const int64_t bt = un / parts, b = bt / a.T, t = bt % a.T;
     const int h0 = static_cast<int>(un % parts) * a.hpg, h1 = min(heads, h0 + a.hpg);
     p.angles(a, bt, l);
@@ -518,8 +527,9 @@ __global__ __launch_bounds__(kThreads) void qknorm_any(QkArgs a) {
   const double scale = (a.scale[which]);
   double* row = lds[wave];
   double dw[4] = {0, 0, 0, 0};
-  for (int64_t base = blockIdx.x * static_cast<int64_t>(kWaves); base < rows;
-       base += static_cast<int64_t>(gridDim.x) * kWaves) {
+  const int64_t groups = BWD ? parts_of(a, which) : gridDim.x;
+  if (blockIdx.x >= groups) return;
+  for (int64_t base = blockIdx.x * static_cast<int64_t>(kWaves); base < rows; base += groups * kWaves) {
     const int64_t i = base + wave;
     const bool in = i < rows;
     const int64_t bt = in ? i / heads : 0, b = bt / a.T, t = bt % a.T;
