@@ -6,10 +6,13 @@
 //   y = scale e^l (Q S^T) + P U,   S <- e^(l_C) S + U^T (e^(l_C - l) K)
 //
 // All products are v_mfma_f32_16x16x4_f32, whose results chain as operands in
-// registers (delta_f32.hpp): a wave carries 16 rows of S through the sequence,
-// as in bf16.  Bound by the fp32 matrix rate of the one wave that has a row tile's
-// chain (64 x 64: 3.7 us a chunk, 2.2 of them matrix instructions): 4 x 8 x 1024 x
-// 64 takes 15 us to prepare and 59 us (token by token: 340).
+// registers (delta_f32.hpp): 16 rows of S go through the sequence in one
+// work-group, as in bf16, here in two waves: at the fp32 matrix rate a chunk's
+// chain in one wave took 3.6 us (64 x 64), in two with their exchanges 2.3.  4 x 8 x
+// 1024 x 64 takes 15 us to prepare and 37 us (in one wave 58; token by token both
+// 340); at 8 x 16 x 4096 x 64, where all CUs are busy, 447 us against 414 in all.
+#include <type_traits>
+
 #include "delta_f32.hpp"
 #include "dev_common.hpp"
 
@@ -108,36 +111,51 @@ __global__ __launch_bounds__(256) void delta_prep_f32(ChunkArgs ca) {
           *reinterpret_cast<const f32x4*>(&s.Lr[SolveLds::tri(i, w)][lane * 4]);
 }
 
-template <int DK, int NW>
+// A work-group has 16 rows of S.  The products of a chunk are shared by two state
+// waves (the fp32 matrix rate of one SIMD bounds their chain), two output waves
+// follow one chunk behind, and one wave loads the next chunk's K; V, Y, Q and P
+// go straight to registers.  Part p of either pair has the token blocks 0 and 3,
+// or 1 and 2 (five of the ten blocks of Y or P each), and the columns of S in
+// halves.  Three barriers a chunk: S, R and U are exchanged through LDS.
+template <int DK>
 struct F32Lds {
   alignas(16) char k[2][64 * DK * 4];
   alignas(16) float gt[2][192];
-  alignas(16) float sx[2][NW][DK * 16];
-  alignas(16) float ux[2][NW][64 * 16];
+  alignas(16) float sx[3][DK * 16];  // S^T before the chunk, blocks of 16
+  alignas(16) float zx[64 * 16];     // -beta R
+  alignas(16) float ux[2][64 * 16];  // U
+};
+constexpr int kF32Threads = 5 * 64;
+
+template <int P>
+struct Part {
+  static constexpr int tb(int x) { return P ? 1 + x : 3 * x; }  // token block x of the part
+  // its blocks (tb(x), j) of a lower triangle in order
+  static constexpr int count(int x) { return tb(x) + 1; }
+  static constexpr int block(int x, int j) { return x ? count(0) + j : j; }
 };
 
-// A work-group is NW state waves, NW output waves one chunk behind, and a wave
-// that loads the next chunk's K; V, Y, Q and P go straight to registers.
-template <int DK, int NW, bool SAVE>
-__global__ __launch_bounds__(64 * (2 * NW + 1)) void delta_chunk_f32(ChunkArgs ca) {
+template <int DK, bool SAVE>
+__global__ __launch_bounds__(kF32Threads) void delta_chunk_f32(ChunkArgs ca) {
   const DeltaArgs& a = ca.a;
-  constexpr int NB = DK / 16, VW = 16 * NW;
-  __shared__ F32Lds<DK, NW> lds;
+  constexpr int NB = DK / 16, HB = NB / 2;
+  __shared__ F32Lds<DK> lds;
   const int lane = threadIdx.x & 63, l = lane & 15, g = lane >> 4;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const int tiles = (a.dv + VW - 1) / VW;
+  const int tiles = SAVE ? delta_row_tiles(a.dv) : (a.dv + 15) / 16;
   int64_t head;
-  int tile;
-  if (!head_of_block(blockIdx.x, tiles, a.N * a.H, head, tile)) return;
+  int rt;
+  if (!head_of_block(blockIdx.x, tiles, a.N * a.H, head, rt)) return;
   const int h = static_cast<int>(head % a.H);
   const int64_t n = head / a.H;
-  const int hk = h / (a.H / a.Hk), r0 = tile * VW;
+  const int hk = h / (a.H / a.Hk), r0 = 16 * rt, n_rt = delta_row_tiles(a.dv);
   const SeqRange sr = seq_range(a.cu, n, a.T);
   const int nc = static_cast<int>((sr.len + kDeltaChunk - 1) / kDeltaChunk);
   const int64_t slot0 = chunk_slot0(a.cu != nullptr, n, sr.t0, a.T, kDeltaChunk);
   const int64_t rec0 = slot0 * a.H + h;
+  const auto rec_of = [&](int c) { return rec0 + static_cast<int64_t>(c) * a.H; };
 
-  if (wave == 2 * NW) {  // ---- loads: K and gates, one chunk ahead
+  if (wave == 4) {  // ---- loads: K and gates, one chunk ahead
     constexpr int NK = DK / 4;
     const float* kp = static_cast<const float*>(a.k) + sr.b * a.sk.b + hk * a.sk.h + sr.t0 * a.sk.t;
     uint32_t ko[NK];
@@ -146,8 +164,7 @@ __global__ __launch_bounds__(64 * (2 * NW + 1)) void delta_chunk_f32(ChunkArgs c
     const auto issue = [&](int c) {
       const bool in = c < nc;
       const __amdgpu_buffer_rsrc_t rk = rows_f32(kp, c * 64LL, in ? sr.len : 0, a.sk.t, a.dk);
-      const __amdgpu_buffer_rsrc_t rg =
-          buffer_rsrc(ca.gates + (in ? (rec0 + static_cast<int64_t>(c) * a.H) * kGates : 0), in ? 768 : 0);
+      const __amdgpu_buffer_rsrc_t rg = buffer_rsrc(ca.gates + (in ? rec_of(c) * kGates : 0), in ? 768 : 0);
 #pragma unroll
       for (int i = 0; i < NK; ++i) dma16(rk, ko[i], lds.k[c & 1] + i * 1024);
 #pragma unroll
@@ -157,15 +174,18 @@ __global__ __launch_bounds__(64 * (2 * NW + 1)) void delta_chunk_f32(ChunkArgs c
     for (int c = 0; c <= nc; ++c) {
       wait_vm<0>();
       lds_barrier();
-      if (c < nc) issue(c + 1);  // into the slot of chunk c - 1
+      if (c == nc) break;
+      issue(c + 1);  // into the slot of chunk c - 1
+      lds_barrier();
+      lds_barrier();
     }
     wait_vm<0>();
     return;
   }
 
-  if (wave >= NW) {  // ---- outputs, one chunk behind
-    const int w = wave - NW;
-    const int rr = r0 + 16 * w + 4 * g, rt = tile * NW + w, n_rt = delta_row_tiles(a.dv);
+  const auto outputs = [&](auto part) {  // ---- one chunk behind
+    using Pt = Part<decltype(part)::value>;
+    const int rr = r0 + 4 * g;
     float* yp = static_cast<float*>(a.y) + sr.b * a.sy.b + h * a.sy.h + sr.t0 * a.sy.t + rr;
     const float* qp = static_cast<const float*>(a.q) + sr.b * a.sq.b + hk * a.sq.h + sr.t0 * a.sq.t;
     const float sc = static_cast<float>(a.scale);
@@ -174,183 +194,209 @@ __global__ __launch_bounds__(64 * (2 * NW + 1)) void delta_chunk_f32(ChunkArgs c
     for (int b = 0; b < NB; ++b)
       qo[b] = 16 * b + 4 * g < a.dk ? static_cast<uint32_t>((l * static_cast<int>(a.sq.t) + 16 * b + 4 * g) * 4)
                                     : kPastEnd;
-    f32x4 qf[4][NB], pf[10];
-    float gs[4];
+    f32x4 qf[2][NB], pf[5];
+    float gs[2];
     const auto fetch = [&](int c) {
-      const int64_t rec = rec0 + static_cast<int64_t>(c) * a.H;
+      const int64_t rec = rec_of(c);
       const __amdgpu_buffer_rsrc_t rq = rows_f32(qp, c * 64LL, sr.len, a.sq.t, a.dk);
 #pragma unroll
-      for (int tb = 0; tb < 4; ++tb)
+      for (int x = 0; x < 2; ++x) {
 #pragma unroll
         for (int b = 0; b < NB; ++b)
-          qf[tb][b] = load_f32x4(rq, qo[b] + static_cast<uint32_t>(tb * 64 * static_cast<int>(a.sq.t)));
+          qf[x][b] = load_f32x4(rq, qo[b] + static_cast<uint32_t>(Pt::tb(x) * 64 * static_cast<int>(a.sq.t)));
 #pragma unroll
-      for (int f = 0; f < 10; ++f) pf[f] = *reinterpret_cast<const f32x4*>(ca.p32 + rec * kY32 + f * 256 + lane * 4);
-#pragma unroll
-      for (int tb = 0; tb < 4; ++tb) gs[tb] = ca.gates[rec * kGates + 16 * tb + l];
+        for (int j = 0; j < Pt::count(x); ++j)
+          pf[Pt::block(x, j)] = *reinterpret_cast<const f32x4*>(ca.p32 + rec * kY32 +
+                                                                SolveLds::tri(Pt::tb(x), j) * 256 + lane * 4);
+        gs[x] = sc * ca.gates[rec * kGates + 16 * Pt::tb(x) + l];
+      }
     };
     if (nc > 0) fetch(0);
     lds_barrier();
     for (int c = 0; c < nc; ++c) {
+      // the two inner barriers of step c, then the one that begins step c + 1;
+      // the work on chunk c stands between those of step c + 1
+      if (c == 0) {
+        lds_barrier();
+        lds_barrier();
+      }
       lds_barrier();
-      const float* sx = lds.sx[c & 1][w] + lane * 4;
-      const float* ux = lds.ux[c & 1][w] + lane * 4;
-      f32x4 o[4];
-#pragma unroll
-      for (int tb = 0; tb < 4; ++tb) o[tb] = zero4();
-#pragma unroll
-      for (int b = 0; b < NB; ++b) {
+      const float* sx = lds.sx[c % 3] + lane * 4;
+      const float* ux = lds.ux[c & 1] + lane * 4;
+      f32x4 o[2] = {zero4(), zero4()};
+      const auto states = [&](int b) {
         const f32x4 sf = *reinterpret_cast<const f32x4*>(sx + b * 256);
 #pragma unroll
         for (int q = 0; q < 4; ++q)
 #pragma unroll
-          for (int tb = 0; tb < 4; ++tb) o[tb] = mfma_f32(sf[q], qf[tb][b][q], o[tb]);
-      }
+          for (int x = 0; x < 2; ++x) o[x] = mfma_f32(sf[q], qf[x][b][q], o[x]);
+      };
+      const bool more = c + 1 < nc;  // step c + 1 has inner barriers
 #pragma unroll
-      for (int tb = 0; tb < 4; ++tb) {
-        const float f = sc * gs[tb];
+      for (int b = 0; b < HB; ++b) states(b);
+      if (more) lds_barrier();
 #pragma unroll
-        for (int q = 0; q < 4; ++q) o[tb][q] *= f;
-      }
+      for (int b = HB; b < NB; ++b) states(b);
+      if (more) lds_barrier();
 #pragma unroll
-      for (int jb = 0; jb < 4; ++jb) {
-        const f32x4 uf = *reinterpret_cast<const f32x4*>(ux + jb * 256);
+      for (int x = 0; x < 2; ++x)
 #pragma unroll
-        for (int q = 0; q < 4; ++q)
+        for (int q = 0; q < 4; ++q) o[x][q] *= gs[x];
 #pragma unroll
-          for (int tb = jb; tb < 4; ++tb) o[tb] = mfma_f32(uf[q], pf[SolveLds::tri(tb, jb)][q], o[tb]);
+      for (int j = 0; j < 4; ++j) {
+        const f32x4 uf = *reinterpret_cast<const f32x4*>(ux + j * 256);
+#pragma unroll
+        for (int x = 0; x < 2; ++x) {
+          if (j >= Pt::count(x)) continue;
+#pragma unroll
+          for (int q = 0; q < 4; ++q) o[x] = mfma_f32(uf[q], pf[Pt::block(x, j)][q], o[x]);
+        }
       }
       fetch(min(c + 1, nc - 1));
       if constexpr (SAVE) {
-        const int64_t rec = rec0 + static_cast<int64_t>(c) * a.H;
 #pragma unroll
-        for (int b = 0; b < NB; ++b)
-          *reinterpret_cast<f32x4*>(ca.s32 + ((rec * n_rt + rt) * NB + b) * 256 + lane * 4) =
-              turned_f32(lds.sx[c & 1][w] + b * 256, lane);
-#pragma unroll
-        for (int tb = 0; tb < 4; ++tb)
-          *reinterpret_cast<f32x4*>(ca.yb + (rec * 64 + 16 * tb + l) * (16 * n_rt) + rr) = o[tb];
+        for (int b = HB * decltype(part)::value; b < HB * decltype(part)::value + HB; ++b)
+          *reinterpret_cast<f32x4*>(ca.s32 + ((rec_of(c) * n_rt + rt) * NB + b) * 256 + lane * 4) =
+              turned_f32(lds.sx[c % 3] + b * 256, lane);
       }
+#pragma unroll
+      for (int x = 0; x < 2; ++x) {
+        const int64_t t = 64LL * c + 16 * Pt::tb(x) + l;
+        if constexpr (SAVE)
+          *reinterpret_cast<f32x4*>(ca.yb + (rec_of(c) * 64 + 16 * Pt::tb(x) + l) * (16 * n_rt) + rr) = o[x];
+        if (a.y && t < sr.len && rr < a.dv) *reinterpret_cast<f32x4*>(yp + t * a.sy.t) = o[x];
+      }
+    }
+  };
+  if (wave == 2) return outputs(std::integral_constant<int, 0>{});
+  if (wave == 3) return outputs(std::integral_constant<int, 1>{});
+
+  const auto states = [&](auto part) {
+    constexpr int P = decltype(part)::value, B0 = HB * P, OB = HB - B0;  // own columns, the other's
+    using Pt = Part<P>;
+    const int r = r0 + l;
+    const __amdgpu_buffer_rsrc_t first = state_rsrc(
+        a.state_in ? static_cast<const float*>(a.state_in) + head * a.dv * a.dk : nullptr, a.dv, a.dk);
+    f32x4 S[HB];
+#pragma unroll
+    for (int b = 0; b < HB; ++b) S[b] = load_f32x4(first, state_off(r, 16 * (B0 + b) + 4 * g, a.dk));
+#pragma unroll
+    for (int b = 0; b < HB; ++b) *reinterpret_cast<f32x4*>(lds.sx[0] + (B0 + b) * 256 + lane * 4) = S[b];
+    const float* vp = static_cast<const float*>(a.v) + sr.b * a.sv.b + h * a.sv.h + sr.t0 * a.sv.t;
+    uint32_t vo[4];
+#pragma unroll
+    for (int q = 0; q < 4; ++q)
+      vo[q] = r < a.dv ? static_cast<uint32_t>(((4 * g + q) * static_cast<int>(a.sv.t) + r) * 4) : kPastEnd;
+    f32x4 V[2], yf[5];
+    const auto fetch = [&](int c) {
+      const __amdgpu_buffer_rsrc_t rv = rows_f32(vp, c * 64LL, sr.len, a.sv.t, a.dv);
+#pragma unroll
+      for (int x = 0; x < 2; ++x) {
+#pragma unroll
+        for (int q = 0; q < 4; ++q)
+          V[x][q] = load4(rv, vo[q] + static_cast<uint32_t>(Pt::tb(x) * 64 * static_cast<int>(a.sv.t)));
+#pragma unroll
+        for (int j = 0; j < Pt::count(x); ++j)
+          yf[Pt::block(x, j)] = *reinterpret_cast<const f32x4*>(ca.y32 + rec_of(c) * kY32 +
+                                                                SolveLds::tri(Pt::tb(x), j) * 256 + lane * 4);
+      }
+    };
+    if (nc > 0) fetch(0);
+    const uint32_t ka = row_at<DK>(lane);
+    const uint32_t kc[4] = {col_at<DK>(lane, 0), col_at<DK>(lane, 1), col_at<DK>(lane, 2), col_at<DK>(lane, 3)};
+    for (int c = 0; c < nc; ++c) {
+      lds_barrier();
+      const char* kt = lds.k[c & 1];
+      const float* gt = lds.gt[c & 1] + 4 * g;
+      const auto gate = [&](int m, int tb) { return *reinterpret_cast<const f32x4*>(gt + 64 * m + 16 * tb); };
+      const auto block = [&](const float* x, int b) { return *reinterpret_cast<const f32x4*>(x + b * 256 + lane * 4); };
+      const auto put = [&](float* x, int b, const f32x4& v) { *reinterpret_cast<f32x4*>(x + b * 256 + lane * 4) = v; };
+      const float* sx = lds.sx[c % 3];
+      // R and -beta R of the own tokens
+      f32x4 E[2] = {zero4(), zero4()}, be[2];
+      const auto scores = [&](int b, const f32x4& s) {
+        f32x4 kf[2];
+#pragma unroll
+        for (int x = 0; x < 2; ++x) kf[x] = row_frag<DK>(kt, ka, Pt::tb(x), b);
+#pragma unroll
+        for (int q = 0; q < 4; ++q)
+#pragma unroll
+          for (int x = 0; x < 2; ++x) E[x] = mfma_f32(kf[x][q], s[q], E[x]);
+      };
+#pragma unroll
+      for (int b = 0; b < HB; ++b) scores(B0 + b, S[b]);
+#pragma unroll
+      for (int b = 0; b < HB; ++b) scores(OB + b, block(sx, OB + b));
+      const float whole = lds.gt[c & 1][63];
+#pragma unroll
+      for (int b = 0; b < HB; ++b) S[b] *= whole;
+#pragma unroll
+      for (int x = 0; x < 2; ++x) {
+        const f32x4 gm = gate(0, Pt::tb(x));
+        be[x] = gate(1, Pt::tb(x));
+        f32x4 z;
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+          E[x][q] = fmaf(-gm[q], E[x][q], V[x][q]);
+          z[q] = -be[x][q] * E[x][q];
+        }
+        put(lds.zx, Pt::tb(x), z);
+      }
+      lds_barrier();
+      // E = R - Y (beta R)
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        if (j >= Pt::count(0) && j >= Pt::count(1)) continue;
+        const f32x4 z = block(lds.zx, j);
+#pragma unroll
+        for (int q = 0; q < 4; ++q)
+#pragma unroll
+          for (int x = 0; x < 2; ++x)
+            if (j < Pt::count(x)) E[x] = mfma_f32(yf[Pt::block(x, j)][q], z[q], E[x]);
+      }
+      fetch(min(c + 1, nc - 1));
+#pragma unroll
+      for (int x = 0; x < 2; ++x) put(lds.ux[c & 1], Pt::tb(x), E[x] * be[x]);
+      if constexpr (SAVE) {
+        const int VP = 16 * n_rt;
+        const __amdgpu_buffer_rsrc_t re = buffer_rsrc(ca.e32 + rec_of(c) * 64 * VP, 256 * VP);
+#pragma unroll
+        for (int x = 0; x < 2; ++x)
+          store_rows(re, static_cast<uint32_t>((4 * g * VP + r) * 4), VP, Pt::tb(x), E[x]);
+      }
+      lds_barrier();
+      // the own columns of S
 #pragma unroll
       for (int tb = 0; tb < 4; ++tb) {
-        const int64_t t = 64LL * c + 16 * tb + l;
-        if (a.y && t < sr.len && rr < a.dv) *reinterpret_cast<f32x4*>(yp + t * a.sy.t) = o[tb];
+        const f32x4 u = block(lds.ux[c & 1], tb) * gate(2, tb);
+        f32x4 kf[HB];
+#pragma unroll
+        for (int b = 0; b < HB; ++b) kf[b] = col_frag<DK>(kt, kc, tb, B0 + b);
+#pragma unroll
+        for (int q = 0; q < 4; ++q)
+#pragma unroll
+          for (int b = 0; b < HB; ++b) S[b] = mfma_f32(kf[b][q], u[q], S[b]);
       }
+#pragma unroll
+      for (int b = 0; b < HB; ++b) put(lds.sx[(c + 1) % 3], B0 + b, S[b]);
     }
-    return;
-  }
-
-  // ---- states
-  const int r = r0 + 16 * wave + l;
-  const int64_t so = (head * a.dv + r) * a.dk;
-  const __amdgpu_buffer_rsrc_t first = state_rsrc(
-      a.state_in ? static_cast<const float*>(a.state_in) + head * a.dv * a.dk : nullptr, a.dv, a.dk);
-  f32x4 S[NB];
-#pragma unroll
-  for (int b = 0; b < NB; ++b) S[b] = load_f32x4(first, state_off(r, 16 * b + 4 * g, a.dk));
-  const float* vp = static_cast<const float*>(a.v) + sr.b * a.sv.b + h * a.sv.h + sr.t0 * a.sv.t;
-  uint32_t vo[4];
-#pragma unroll
-  for (int q = 0; q < 4; ++q)
-    vo[q] = r < a.dv ? static_cast<uint32_t>(((4 * g + q) * static_cast<int>(a.sv.t) + r) * 4) : kPastEnd;
-  f32x4 V[4], yf[10];
-  const auto fetch = [&](int c) {
-    const int64_t rec = rec0 + static_cast<int64_t>(c) * a.H;
-    const __amdgpu_buffer_rsrc_t rv = rows_f32(vp, c * 64LL, sr.len, a.sv.t, a.dv);
-#pragma unroll
-    for (int tb = 0; tb < 4; ++tb)
-#pragma unroll
-      for (int q = 0; q < 4; ++q)
-        V[tb][q] = load4(rv, vo[q] + static_cast<uint32_t>(tb * 64 * static_cast<int>(a.sv.t)));
-#pragma unroll
-    for (int f = 0; f < 10; ++f) yf[f] = *reinterpret_cast<const f32x4*>(ca.y32 + rec * kY32 + f * 256 + lane * 4);
-  };
-  if (nc > 0) fetch(0);
-  const uint32_t ka = row_at<DK>(lane);
-  const uint32_t kc[4] = {col_at<DK>(lane, 0), col_at<DK>(lane, 1), col_at<DK>(lane, 2), col_at<DK>(lane, 3)};
-  for (int c = 0; c < nc; ++c) {
     lds_barrier();
-    const char* kt = lds.k[c & 1];
-    const float* gt = lds.gt[c & 1] + 4 * g;
-    const auto gate = [&](int m, int tb) { return *reinterpret_cast<const f32x4*>(gt + 64 * m + 16 * tb); };
-    float* sx = lds.sx[c & 1][wave] + lane * 4;
-    float* ux = lds.ux[c & 1][wave] + lane * 4;
-    f32x4 E[4], Z[4], be[4];
+    if (r < a.dv) {
+      const int64_t so = (head * a.dv + r) * a.dk;
 #pragma unroll
-    for (int tb = 0; tb < 4; ++tb) E[tb] = zero4();
-#pragma unroll
-    for (int b = 0; b < NB; ++b) {
-      f32x4 kf[4];
-#pragma unroll
-      for (int tb = 0; tb < 4; ++tb) kf[tb] = row_frag<DK>(kt, ka, tb, b);
-#pragma unroll
-      for (int q = 0; q < 4; ++q)
-#pragma unroll
-        for (int tb = 0; tb < 4; ++tb) E[tb] = mfma_f32(kf[tb][q], S[b][q], E[tb]);
-      *reinterpret_cast<f32x4*>(sx + b * 256) = S[b];  // for the output wave
-    }
-    const float whole = lds.gt[c & 1][63];
-#pragma unroll
-    for (int b = 0; b < NB; ++b)
-#pragma unroll
-      for (int q = 0; q < 4; ++q) S[b][q] *= whole;
-#pragma unroll
-    for (int tb = 0; tb < 4; ++tb) {
-      const f32x4 gm = gate(0, tb);
-      be[tb] = gate(1, tb);
-#pragma unroll
-      for (int q = 0; q < 4; ++q) {
-        E[tb][q] = fmaf(-gm[q], E[tb][q], V[tb][q]);
-        Z[tb][q] = -be[tb][q] * E[tb][q];
+      for (int b = 0; b < HB; ++b) {
+        const int c = 16 * (B0 + b) + 4 * g;
+        if (c >= a.dk) continue;
+        if (a.state_out) *reinterpret_cast<f32x4*>(static_cast<float*>(a.state_out) + so + c) = S[b];
+        if constexpr (SAVE) *reinterpret_cast<f32x4*>(ca.st + so + c) = S[b];
       }
     }
-#pragma unroll
-    for (int j = 0; j < 4; ++j)
-#pragma unroll
-      for (int q = 0; q < 4; ++q)
-#pragma unroll
-        for (int i = j; i < 4; ++i) E[i] = mfma_f32(yf[SolveLds::tri(i, j)][q], Z[j][q], E[i]);
-    fetch(min(c + 1, nc - 1));
-    if constexpr (SAVE) {
-      const int VP = 16 * delta_row_tiles(a.dv);
-      const __amdgpu_buffer_rsrc_t re =
-          buffer_rsrc(ca.e32 + (rec0 + static_cast<int64_t>(c) * a.H) * 64 * VP, 256 * VP);
-#pragma unroll
-      for (int tb = 0; tb < 4; ++tb) store_rows(re, static_cast<uint32_t>((4 * g * VP + r) * 4), VP, tb, E[tb]);
-    }
-#pragma unroll
-    for (int tb = 0; tb < 4; ++tb) {
-      const f32x4 rs = gate(2, tb);
-#pragma unroll
-      for (int q = 0; q < 4; ++q) E[tb][q] *= be[tb][q];
-      *reinterpret_cast<f32x4*>(ux + tb * 256) = E[tb];
-#pragma unroll
-      for (int q = 0; q < 4; ++q) E[tb][q] *= rs[q];
-    }
-#pragma unroll
-    for (int tb = 0; tb < 4; ++tb) {
-      f32x4 kf[NB];
-#pragma unroll
-      for (int b = 0; b < NB; ++b) kf[b] = col_frag<DK>(kt, kc, tb, b);
-#pragma unroll
-      for (int q = 0; q < 4; ++q)
-#pragma unroll
-        for (int b = 0; b < NB; ++b) S[b] = mfma_f32(kf[b][q], E[tb][q], S[b]);
-    }
-  }
-  lds_barrier();
-  if (r < a.dv) {
-#pragma unroll
-    for (int b = 0; b < NB; ++b) {
-      const int c = 16 * b + 4 * g;
-      if (c >= a.dk) continue;
-      if (a.state_out) *reinterpret_cast<f32x4*>(static_cast<float*>(a.state_out) + so + c) = S[b];
-      if constexpr (SAVE) *reinterpret_cast<f32x4*>(ca.st + so + c) = S[b];
-    }
-  }
+  };
+  if (wave == 0) states(std::integral_constant<int, 0>{});
+  else states(std::integral_constant<int, 1>{});
 }
 
-template <int DK, int NW>
+template <int DK>
 hipError_t launch(const ChunkArgs& c, hipStream_t s) {
   const int64_t n = c.slots * c.a.H;
   if (n > 0) {
@@ -358,10 +404,10 @@ hipError_t launch(const ChunkArgs& c, hipStream_t s) {
     const hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
   }
-  const int tiles = (c.a.dv + 16 * NW - 1) / (16 * NW);
+  const int tiles = c.s32 ? delta_row_tiles(c.a.dv) : (c.a.dv + 15) / 16;
   const dim3 grid(static_cast<unsigned>(head_blocks(c.a.N * c.a.H, tiles)));
-  if (c.s32) delta_chunk_f32<DK, NW, true><<<grid, 64 * (2 * NW + 1), 0, s>>>(c);
-  else delta_chunk_f32<DK, NW, false><<<grid, 64 * (2 * NW + 1), 0, s>>>(c);
+  if (c.s32) delta_chunk_f32<DK, true><<<grid, kF32Threads, 0, s>>>(c);
+  else delta_chunk_f32<DK, false><<<grid, kF32Threads, 0, s>>>(c);
   return hipGetLastError();
 }
 
@@ -379,7 +425,7 @@ bool delta_chunk_f32_ok(int io, const DeltaArgs& a) {
 
 hipError_t launch_delta_chunk_f32(const ChunkArgs& c, hipStream_t s) {
   if (c.a.N * c.a.H == 0) return hipSuccess;
-  return c.a.dk <= 64 ? launch<64, 2>(c, s) : launch<128, 2>(c, s);
+  return c.a.dk <= 64 ? launch<64>(c, s) : launch<128>(c, s);
 }
 
 }  // namespace gls
