@@ -73,4 +73,16 @@ __device__ __forceinline__ uint32_t tile_off_f32(int n, int lane, int64_t st, in
   return c < d ? static_cast<uint32_t>((r * static_cast<int>(st) + c) * 4) : kPastEnd;
 }
 
+// A chunk's token blocks shared by two waves: 0 and 3, or 1 and 2, five of a
+// triangle's ten blocks each.
+template <int P>
+struct Part {
+  static constexpr int tb(int x) { return P ? 1 + x : 3 * x; }  // token block x of the part
+  // blocks (tb(x), j) of a lower triangle in order
+  static constexpr int count(int x) { return tb(x) + 1; }
+  static constexpr int block(int x, int j) { return x ? count(0) + j : j; }
+  // blocks (i, tb(x)) in order
+  static constexpr int below(int x, int i) { return (x ? 4 - tb(0) : 0) + i - tb(x); }
+};
+
 }  // namespace gls

@@ -127,14 +127,6 @@ struct F32Lds {
 };
 constexpr int kF32Threads = 5 * 64;
 
-template <int P>
-struct Part {
-  static constexpr int tb(int x) { return P ? 1 + x : 3 * x; }  // token block x of the part
-  // its blocks (tb(x), j) of a lower triangle in order
-  static constexpr int count(int x) { return tb(x) + 1; }
-  static constexpr int block(int x, int j) { return x ? count(0) + j : j; }
-};
-
 template <int DK, bool SAVE>
 __global__ __launch_bounds__(kF32Threads) void delta_chunk_f32(ChunkArgs ca) {
   const DeltaArgs& a = ca.a;

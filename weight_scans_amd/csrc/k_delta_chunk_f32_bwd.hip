@@ -7,48 +7,62 @@
 // <Lam, S> is taken anew at every chunk's end and the sum runs over the chunk's
 // tokens only.
 //
-// The recurrence is bound by the matrix rate of the wave that has a row tile's
-// chain, the gradients by the matrix cores and HBM: 4 x 8 x 1024 x 64 takes 106 us
-// and 32 us, 128 x 128 heads 148 us and 75 us (token by token both together: 1059
-// and 1720 us).
+// The recurrence is bound by the matrix rate of the waves that have a row tile's
+// chain, the gradients by the matrix cores and HBM: 4 x 8 x 1024 x 64 takes 56 us
+// and 32 us, 128 x 128 heads 81 us and 76 us (token by token both together: 1058
+// and 1728 us).  With one wave to a row tile's chain the recurrence took 106 and
+// 150 us; where heads fill the card by themselves the two are level (256 heads of
+// 64: 439 us with the gradients, before 435).
+#include <type_traits>
+
 #include "delta_f32.hpp"
 #include "dev_common.hpp"
 
 namespace gls {
 namespace {
 
-template <int DK, int NW>
+// The recurrence of Lam from the last chunk to the first.  A work-group has 16
+// rows; two waves share the products of a chunk (token blocks as Part, columns of
+// Lam in halves; the fp32 matrix rate of one SIMD bounds their chain) and exchange
+// Lam, beta dU and G through LDS, three barriers a chunk: every buffer's reads end
+// one barrier before its next write.  A third wave has what is no part of the
+// chain: Lam turned for the gradients, dbeta and the decay's terms.  The last one
+// loads the next chunk's K, Q and gates; dO, V, y, e go straight to registers.
+template <int DK>
 struct RevLds {
   alignas(16) char k[2][64 * DK * 4];
   alignas(16) char q[2][64 * DK * 4];
   alignas(16) float gt[2][192];
-  alignas(16) float turn[NW][DK * 16];
-  float xs[NW][64];
+  alignas(16) float lx[DK * 16];  // Lam^T after the chunk, blocks of 16
+  alignas(16) float zx[64 * 16];  // -beta dU
+  alignas(16) float gx[64 * 16];  // G
+  float xs[64];
 };
+constexpr int kRevThreads = 4 * 64;
 
-// The recurrence of Lam, 16 rows a wave from the last chunk to the first; one
-// more wave loads the next chunk's K, Q and gates.  What belongs to a wave's own
-// rows (dO, V, y, e) goes straight to registers.
-template <int DK, int NW>
-__global__ __launch_bounds__(64 * (NW + 1), 1) void delta_rev_f32(ChunkArgs ca) {
+template <int DK>
+__global__ __launch_bounds__(kRevThreads) void delta_rev_f32(ChunkArgs ca) {
   const DeltaArgs& a = ca.a;
-  constexpr int NB = DK / 16, VW = 16 * NW;
-  __shared__ RevLds<DK, NW> lds;
+  constexpr int NB = DK / 16, HB = NB / 2;
+  __shared__ RevLds<DK> lds;
   const int lane = threadIdx.x & 63, l = lane & 15, g = lane >> 4;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const int tiles = (a.dv + VW - 1) / VW;
+  const int n_rt = delta_row_tiles(a.dv), VP = 16 * n_rt;
   int64_t head;
-  int tile;
-  if (!head_of_block(blockIdx.x, tiles, a.N * a.H, head, tile)) return;
+  int rt;
+  if (!head_of_block(blockIdx.x, n_rt, a.N * a.H, head, rt)) return;
   const int h = static_cast<int>(head % a.H);
   const int64_t n = head / a.H;
-  const int hk = h / (a.H / a.Hk), r0 = tile * VW;
+  const int hk = h / (a.H / a.Hk), r = 16 * rt + l;
   const SeqRange sr = seq_range(a.cu, n, a.T);
   const int nc = static_cast<int>((sr.len + kDeltaChunk - 1) / kDeltaChunk);
   const int64_t slot0 = chunk_slot0(a.cu != nullptr, n, sr.t0, a.T, kDeltaChunk);
   const int64_t rec0 = slot0 * a.H + h;
+  const auto rec_of = [&](int c) { return rec0 + static_cast<int64_t>(c) * a.H; };
+  const auto block = [&](const float* x, int b) { return *reinterpret_cast<const f32x4*>(x + b * 256 + lane * 4); };
+  const auto put = [&](float* x, int b, const f32x4& v) { *reinterpret_cast<f32x4*>(x + b * 256 + lane * 4) = v; };
 
-  if (wave == NW) {  // ---- loads
+  if (wave == 3) {  // ---- loads
     constexpr int NK = DK / 4;
     const float* kp = static_cast<const float*>(a.k) + sr.b * a.sk.b + hk * a.sk.h + sr.t0 * a.sk.t;
     const float* qp = static_cast<const float*>(a.q) + sr.b * a.sq.b + hk * a.sq.h + sr.t0 * a.sq.t;
@@ -62,7 +76,7 @@ __global__ __launch_bounds__(64 * (NW + 1), 1) void delta_rev_f32(ChunkArgs ca) 
       const int s = c & 1;
       const __amdgpu_buffer_rsrc_t rk = rows_f32(kp, c * 64LL, sr.len, a.sk.t, a.dk);
       const __amdgpu_buffer_rsrc_t rq = rows_f32(qp, c * 64LL, sr.len, a.sq.t, a.dk);
-      const __amdgpu_buffer_rsrc_t rg = buffer_rsrc(ca.gates + (rec0 + static_cast<int64_t>(c) * a.H) * kGates, 768);
+      const __amdgpu_buffer_rsrc_t rg = buffer_rsrc(ca.gates + rec_of(c) * kGates, 768);
 #pragma unroll
       for (int i = 0; i < NK; ++i) dma16(rk, ko[i], lds.k[s] + i * 1024);
 #pragma unroll
@@ -75,32 +89,12 @@ __global__ __launch_bounds__(64 * (NW + 1), 1) void delta_rev_f32(ChunkArgs ca) 
       wait_vm<0>();
       lds_barrier();
       if (c > 0) issue(c - 1);  // into the slot of chunk c + 1
+      lds_barrier();
+      lds_barrier();
     }
     return;
   }
 
-  const int r = r0 + 16 * wave + l, rt = tile * NW + wave, n_rt = delta_row_tiles(a.dv), VP = 16 * n_rt;
-  const int64_t so = (head * a.dv + r) * a.dk;
-  const float sc = static_cast<float>(a.scale);
-  f32x4 S[NB];  // Lam^T
-  float z = 0.f;  // <Lam, state> after the chunk, over this wave's rows
-  {
-    const int64_t at = head * a.dv * a.dk;
-    const __amdgpu_buffer_rsrc_t ru =
-        state_rsrc(a.dstate_out ? static_cast<const float*>(a.dstate_out) + at : nullptr, a.dv, a.dk);
-    const __amdgpu_buffer_rsrc_t rs = state_rsrc(a.dstate_out ? ca.st + at : nullptr, a.dv, a.dk);
-    f32x4 s[NB];
-#pragma unroll
-    for (int b = 0; b < NB; ++b) {
-      S[b] = load_f32x4(ru, state_off(r, 16 * b + 4 * g, a.dk));
-      s[b] = load_f32x4(rs, state_off(r, 16 * b + 4 * g, a.dk));
-    }
-#pragma unroll
-    for (int b = 0; b < NB; ++b)
-#pragma unroll
-      for (int q = 0; q < 4; ++q) z = fmaf(S[b][q], s[b][q], z);
-  }
-  z = wave_sum(z);
   const float* vp = static_cast<const float*>(a.v) + sr.b * a.sv.b + h * a.sv.h + sr.t0 * a.sv.t;
   const float* op = static_cast<const float*>(a.dy) + sr.b * a.sdy.b + h * a.sdy.h + sr.t0 * a.sdy.t;
   uint32_t vo[4], oo[4];
@@ -109,147 +103,222 @@ __global__ __launch_bounds__(64 * (NW + 1), 1) void delta_rev_f32(ChunkArgs ca) 
     vo[q] = r < a.dv ? static_cast<uint32_t>(((4 * g + q) * static_cast<int>(a.sv.t) + r) * 4) : kPastEnd;
     oo[q] = r < a.dv ? static_cast<uint32_t>(((4 * g + q) * static_cast<int>(a.sdy.t) + r) * 4) : kPastEnd;
   }
-  f32x4 sn[NB];  // the state after the chunk, turned
-  const uint32_t ra = static_cast<uint32_t>((4 * g * VP + r) * 4);
-  const uint32_t ka = row_at<DK>(lane);
-  const uint32_t kc[4] = {col_at<DK>(lane, 0), col_at<DK>(lane, 1), col_at<DK>(lane, 2), col_at<DK>(lane, 3)};
-  float* turn = lds.turn[wave];
-  for (int c = nc - 1; c >= 0; --c) {
-    const int64_t rec = rec0 + static_cast<int64_t>(c) * a.H;
-    lds_barrier();
-    const char* kt = lds.k[c & 1];
-    const char* qt = lds.q[c & 1];
-    const float* gt = lds.gt[c & 1] + 4 * g;
-    const auto gate = [&](int m, int tb) { return *reinterpret_cast<const f32x4*>(gt + 64 * m + 16 * tb); };
-    // loads that K Lam^T hides; the others follow when P is done with
-    f32x4 dO[4], V[4], Y[4], E[4], yt[10], pt[10];
-    const __amdgpu_buffer_rsrc_t ro = rows_f32(op, c * 64LL, sr.len, a.sdy.t, a.dv);
-#pragma unroll
-    for (int tb = 0; tb < 4; ++tb)
-#pragma unroll
-      for (int q = 0; q < 4; ++q)
-        dO[tb][q] = load4(ro, oo[q] + static_cast<uint32_t>(tb * 64 * static_cast<int>(a.sdy.t)));
-#pragma unroll
-    for (int f = 0; f < 10; ++f) pt[f] = *reinterpret_cast<const f32x4*>(ca.pt32 + rec * kY32 + f * 256 + lane * 4);
-#pragma unroll
-    for (int f = 0; f < 10; ++f) yt[f] = *reinterpret_cast<const f32x4*>(ca.yt32 + rec * kY32 + f * 256 + lane * 4);
-    // K Lam^T; Lam turned, for the gradients and for <Lam, state>
-    f32x4 D[4], Z[4];
-#pragma unroll
-    for (int tb = 0; tb < 4; ++tb) D[tb] = zero4();
-#pragma unroll
-    for (int b = 0; b < NB; ++b) {
-      f32x4 kf[4];
-#pragma unroll
-      for (int tb = 0; tb < 4; ++tb) kf[tb] = row_frag<DK>(kt, ka, tb, b);
-#pragma unroll
-      for (int q = 0; q < 4; ++q)
-#pragma unroll
-        for (int tb = 0; tb < 4; ++tb) D[tb] = mfma_f32(kf[tb][q], S[b][q], D[tb]);
-      *reinterpret_cast<f32x4*>(turn + b * 256 + lane * 4) = S[b];
-    }
-    float zz = 0.f;
-#pragma unroll
-    for (int b = 0; b < NB; ++b) {
-      const f32x4 x = turned_f32(turn + b * 256, lane);
-      *reinterpret_cast<f32x4*>(ca.l32 + ((rec * n_rt + rt) * NB + b) * 256 + lane * 4) = x;
-      if (c + 1 < nc)
-#pragma unroll
-        for (int q = 0; q < 4; ++q) zz = fmaf(x[q], sn[b][q], zz);
-    }
-    if (c + 1 < nc) z = wave_sum(zz);
-    // dU = e^(l_C - l) K Lam^T + P^T dO
-#pragma unroll
-    for (int tb = 0; tb < 4; ++tb) D[tb] *= gate(2, tb);
-#pragma unroll
-    for (int i = 0; i < 4; ++i)
-#pragma unroll
-      for (int q = 0; q < 4; ++q)
-#pragma unroll
-        for (int j = 0; j <= i; ++j) D[j] = mfma_f32(pt[SolveLds::tri(i, j)][q], dO[i][q], D[j]);
+  const int64_t all = head * a.dv * a.dk;
+  const __amdgpu_buffer_rsrc_t ru =
+      state_rsrc(a.dstate_out ? static_cast<const float*>(a.dstate_out) + all : nullptr, a.dv, a.dk);
+
+  if (wave == 2) {  // ---- Lam for the gradients, dbeta, the decay's terms
+    float z = 0.f;  // <Lam, state> after the chunk, over these rows
     {
-      const __amdgpu_buffer_rsrc_t rv = rows_f32(vp, c * 64LL, sr.len, a.sv.t, a.dv);
-      const __amdgpu_buffer_rsrc_t re = buffer_rsrc(ca.e32 + rec * 64 * VP, 256 * VP);
-      const __amdgpu_buffer_rsrc_t ry = buffer_rsrc(ca.yb + rec * 64 * VP, 256 * VP);
+      const __amdgpu_buffer_rsrc_t rs = state_rsrc(a.dstate_out ? ca.st + all : nullptr, a.dv, a.dk);
+      f32x4 u[NB], s[NB];
 #pragma unroll
-      for (int tb = 0; tb < 4; ++tb) {
-#pragma unroll
-        for (int q = 0; q < 4; ++q)
-          V[tb][q] = load4(rv, vo[q] + static_cast<uint32_t>(tb * 64 * static_cast<int>(a.sv.t)));
-        E[tb] = load_rows(re, ra, VP, tb);
-        Y[tb] = load_rows(ry, ra, VP, tb);
+      for (int b = 0; b < NB; ++b) {
+        u[b] = load_f32x4(ru, state_off(r, 16 * b + 4 * g, a.dk));
+        s[b] = load_f32x4(rs, state_off(r, 16 * b + 4 * g, a.dk));
       }
 #pragma unroll
       for (int b = 0; b < NB; ++b)
-        sn[b] = *reinterpret_cast<const f32x4*>(ca.s32 + ((rec * n_rt + rt) * NB + b) * 256 + lane * 4);
+#pragma unroll
+        for (int q = 0; q < 4; ++q) z = fmaf(u[b][q], s[b][q], z);
     }
-    __builtin_amdgcn_sched_barrier(0);
-    // G = dU - Y^T (beta dU)
+    z = wave_sum(z);
+    wait_vm<0>();  // dstate_in may be dstate_out
+    const uint32_t ra = static_cast<uint32_t>((4 * g * VP + r) * 4);
+    f32x4 sn[NB];  // the state after the chunk, turned
+    for (int c = nc - 1; c >= 0; --c) {
+      const int64_t rec = rec_of(c);
+      f32x4 dO[4], V[4], Y[4], E[4];
+      {
+        const __amdgpu_buffer_rsrc_t ro = rows_f32(op, c * 64LL, sr.len, a.sdy.t, a.dv);
+        const __amdgpu_buffer_rsrc_t rv = rows_f32(vp, c * 64LL, sr.len, a.sv.t, a.dv);
+        const __amdgpu_buffer_rsrc_t re = buffer_rsrc(ca.e32 + rec * 64 * VP, 256 * VP);
+        const __amdgpu_buffer_rsrc_t ry = buffer_rsrc(ca.yb + rec * 64 * VP, 256 * VP);
 #pragma unroll
-    for (int tb = 0; tb < 4; ++tb) {
-      const f32x4 be = gate(1, tb);
+        for (int tb = 0; tb < 4; ++tb) {
 #pragma unroll
-      for (int q = 0; q < 4; ++q) Z[tb][q] = -be[q] * D[tb][q];
-    }
-#pragma unroll
-    for (int i = 0; i < 4; ++i)
-#pragma unroll
-      for (int q = 0; q < 4; ++q)
-#pragma unroll
-        for (int j = 0; j <= i; ++j) D[j] = mfma_f32(yt[SolveLds::tri(i, j)][q], Z[i][q], D[j]);
-    // dbeta and the decay's terms over the wave's rows; operands of the update
-    float xe[16], xv[16];
-    f32x4 o[4], f[4], G[4];
-    const float whole = lds.gt[c & 1][63];
-#pragma unroll
-    for (int tb = 0; tb < 4; ++tb) {
-      const f32x4 gm = gate(0, tb), be = gate(1, tb);
-#pragma unroll
-      for (int q = 0; q < 4; ++q) {
-        G[tb][q] = D[tb][q];
-        xe[4 * tb + q] = G[tb][q] * E[tb][q];
-        const float F = be[q] * G[tb][q];
-        xv[4 * tb + q] = dO[tb][q] * Y[tb][q] - V[tb][q] * F;
-        o[tb][q] = sc * gm[q] * dO[tb][q];
-        f[tb][q] = -gm[q] * F;
+          for (int q = 0; q < 4; ++q) {
+            dO[tb][q] = load4(ro, oo[q] + static_cast<uint32_t>(tb * 64 * static_cast<int>(a.sdy.t)));
+            V[tb][q] = load4(rv, vo[q] + static_cast<uint32_t>(tb * 64 * static_cast<int>(a.sv.t)));
+          }
+          E[tb] = load_rows(re, ra, VP, tb);
+          Y[tb] = load_rows(ry, ra, VP, tb);
+        }
       }
-    }
-    const int tok = 16 * (l >> 2) + 4 * g + (l & 3);
-    const float db = row_sums(xe, l);
-    lds.xs[wave][tok] = row_sums(xv, l);
-    const float suffix = wave_scan_add(lds.xs[wave][63 - lane]);
-    ca.bf[(rec * n_rt + rt) * 64 + tok] = db;
-    ca.zf[(rec * n_rt + rt) * 64 + 63 - lane] = z + suffix;
-    const __amdgpu_buffer_rsrc_t rg = buffer_rsrc(ca.g32 + rec * 64 * VP, 256 * VP);
-#pragma unroll
-    for (int tb = 0; tb < 4; ++tb) store_rows(rg, ra, VP, tb, G[tb]);
-    __builtin_amdgcn_sched_barrier(0);
-#pragma unroll
-    for (int b = 0; b < NB; ++b) S[b] *= whole;
-#pragma unroll
-    for (int tb = 0; tb < 4; ++tb) {
-      f32x4 kf[NB], qf[NB];
+      lds_barrier();
+      float zz = 0.f;
 #pragma unroll
       for (int b = 0; b < NB; ++b) {
-        kf[b] = col_frag<DK>(kt, kc, tb, b);
-        qf[b] = col_frag<DK>(qt, kc, tb, b);
+        const f32x4 x = turned_f32(lds.lx + b * 256, lane);
+        *reinterpret_cast<f32x4*>(ca.l32 + ((rec * n_rt + rt) * NB + b) * 256 + lane * 4) = x;
+        if (c + 1 < nc)
+#pragma unroll
+          for (int q = 0; q < 4; ++q) zz = fmaf(x[q], sn[b][q], zz);
+      }
+      if (c + 1 < nc) z = wave_sum(zz);
+#pragma unroll
+      for (int b = 0; b < NB; ++b)
+        sn[b] = *reinterpret_cast<const f32x4*>(ca.s32 + ((rec * n_rt + rt) * NB + b) * 256 + lane * 4);
+      lds_barrier();
+      lds_barrier();
+      float xe[16], xv[16];
+      const __amdgpu_buffer_rsrc_t rg = buffer_rsrc(ca.g32 + rec * 64 * VP, 256 * VP);
+#pragma unroll
+      for (int tb = 0; tb < 4; ++tb) {
+        const f32x4 be = *reinterpret_cast<const f32x4*>(lds.gt[c & 1] + 64 + 16 * tb + 4 * g);
+        const f32x4 G = block(lds.gx, tb);
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+          xe[4 * tb + q] = G[q] * E[tb][q];
+          xv[4 * tb + q] = dO[tb][q] * Y[tb][q] - V[tb][q] * (be[q] * G[q]);
+        }
+        store_rows(rg, ra, VP, tb, G);
+      }
+      const int tok = 16 * (l >> 2) + 4 * g + (l & 3);
+      const float db = row_sums(xe, l);
+      lds.xs[tok] = row_sums(xv, l);
+      const float suffix = wave_scan_add(lds.xs[63 - lane]);
+      ca.bf[(rec * n_rt + rt) * 64 + tok] = db;
+      ca.zf[(rec * n_rt + rt) * 64 + 63 - lane] = z + suffix;
+    }
+    return;
+  }
+
+  const auto chain = [&](auto part) {
+    constexpr int B0 = HB * decltype(part)::value, OB = HB - B0;  // own columns, the other's
+    using Pt = Part<decltype(part)::value>;
+    const float sc = static_cast<float>(a.scale);
+    f32x4 S[HB];  // Lam^T
+#pragma unroll
+    for (int b = 0; b < HB; ++b) S[b] = load_f32x4(ru, state_off(r, 16 * (B0 + b) + 4 * g, a.dk));
+#pragma unroll
+    for (int b = 0; b < HB; ++b) put(lds.lx, B0 + b, S[b]);
+    f32x4 dO[4], pt[5], yt[5];
+    const auto fetch_o = [&](int c) {  // dO and P^T
+      const __amdgpu_buffer_rsrc_t ro = rows_f32(op, c * 64LL, sr.len, a.sdy.t, a.dv);
+#pragma unroll
+      for (int tb = 0; tb < 4; ++tb)
+#pragma unroll
+        for (int q = 0; q < 4; ++q)
+          dO[tb][q] = load4(ro, oo[q] + static_cast<uint32_t>(tb * 64 * static_cast<int>(a.sdy.t)));
+#pragma unroll
+      for (int x = 0; x < 2; ++x)
+#pragma unroll
+        for (int i = Pt::tb(x); i < 4; ++i)
+          pt[Pt::below(x, i)] = *reinterpret_cast<const f32x4*>(ca.pt32 + rec_of(c) * kY32 +
+                                                                SolveLds::tri(i, Pt::tb(x)) * 256 + lane * 4);
+    };
+    const auto fetch_y = [&](int c) {
+#pragma unroll
+      for (int x = 0; x < 2; ++x)
+#pragma unroll
+        for (int i = Pt::tb(x); i < 4; ++i)
+          yt[Pt::below(x, i)] = *reinterpret_cast<const f32x4*>(ca.yt32 + rec_of(c) * kY32 +
+                                                                SolveLds::tri(i, Pt::tb(x)) * 256 + lane * 4);
+    };
+    if (nc > 0) {
+      fetch_o(nc - 1);
+      fetch_y(nc - 1);
+    }
+    const uint32_t ka = row_at<DK>(lane);
+    const uint32_t kc[4] = {col_at<DK>(lane, 0), col_at<DK>(lane, 1), col_at<DK>(lane, 2), col_at<DK>(lane, 3)};
+    for (int c = nc - 1; c >= 0; --c) {
+      lds_barrier();
+      const char* kt = lds.k[c & 1];
+      const char* qt = lds.q[c & 1];
+      const float* gt = lds.gt[c & 1] + 4 * g;
+      const auto gate = [&](int m, int tb) { return *reinterpret_cast<const f32x4*>(gt + 64 * m + 16 * tb); };
+      // K Lam^T of the own tokens
+      f32x4 D[2] = {zero4(), zero4()};
+      const auto scores = [&](int b, const f32x4& s) {
+        f32x4 kf[2];
+#pragma unroll
+        for (int x = 0; x < 2; ++x) kf[x] = row_frag<DK>(kt, ka, Pt::tb(x), b);
+#pragma unroll
+        for (int q = 0; q < 4; ++q)
+#pragma unroll
+          for (int x = 0; x < 2; ++x) D[x] = mfma_f32(kf[x][q], s[q], D[x]);
+      };
+#pragma unroll
+      for (int b = 0; b < HB; ++b) scores(B0 + b, S[b]);
+#pragma unroll
+      for (int b = 0; b < HB; ++b) scores(OB + b, block(lds.lx, OB + b));
+      // dU = e^(l_C - l) K Lam^T + P^T dO
+#pragma unroll
+      for (int x = 0; x < 2; ++x) D[x] *= gate(2, Pt::tb(x));
+#pragma unroll
+      for (int i = 3; i >= 0; --i)
+#pragma unroll
+        for (int q = 0; q < 4; ++q)
+#pragma unroll
+          for (int x = 0; x < 2; ++x)
+            if (i >= Pt::tb(x)) D[x] = mfma_f32(pt[Pt::below(x, i)][q], dO[i][q], D[x]);
+#pragma unroll
+      for (int x = 0; x < 2; ++x) {
+        const f32x4 be = gate(1, Pt::tb(x));
+        f32x4 z;
+#pragma unroll
+        for (int q = 0; q < 4; ++q) z[q] = -be[q] * D[x][q];
+        put(lds.zx, Pt::tb(x), z);
+      }
+      // Q's part of the own columns before the others' beta dU is waited for
+      const float whole = lds.gt[c & 1][63];
+#pragma unroll
+      for (int b = 0; b < HB; ++b) S[b] *= whole;
+#pragma unroll
+      for (int tb = 0; tb < 4; ++tb) {
+        const f32x4 o = dO[tb] * (gate(0, tb) * sc);
+        f32x4 qf[HB];
+#pragma unroll
+        for (int b = 0; b < HB; ++b) qf[b] = col_frag<DK>(qt, kc, tb, B0 + b);
+#pragma unroll
+        for (int q = 0; q < 4; ++q)
+#pragma unroll
+          for (int b = 0; b < HB; ++b) S[b] = mfma_f32(qf[b][q], o[q], S[b]);
+      }
+      fetch_o(max(c - 1, 0));
+      lds_barrier();
+      // G = dU - Y^T (beta dU)
+#pragma unroll
+      for (int i = 3; i >= 0; --i) {
+        if (i < Pt::tb(0)) continue;
+        const f32x4 z = block(lds.zx, i);
+#pragma unroll
+        for (int q = 0; q < 4; ++q)
+#pragma unroll
+          for (int x = 0; x < 2; ++x)
+            if (i >= Pt::tb(x)) D[x] = mfma_f32(yt[Pt::below(x, i)][q], z[q], D[x]);
+      }
+      fetch_y(max(c - 1, 0));
+#pragma unroll
+      for (int x = 0; x < 2; ++x) put(lds.gx, Pt::tb(x), D[x]);
+      lds_barrier();
+      // K's part
+#pragma unroll
+      for (int tb = 0; tb < 4; ++tb) {
+        const f32x4 f = block(lds.gx, tb) * (gate(0, tb) * gate(1, tb));
+        f32x4 kf[HB];
+#pragma unroll
+        for (int b = 0; b < HB; ++b) kf[b] = col_frag<DK>(kt, kc, tb, B0 + b);
+#pragma unroll
+        for (int q = 0; q < 4; ++q)
+#pragma unroll
+          for (int b = 0; b < HB; ++b) S[b] = mfma_f32(kf[b][q], -f[q], S[b]);
       }
 #pragma unroll
-      for (int q = 0; q < 4; ++q)
-#pragma unroll
-        for (int b = 0; b < NB; ++b) {
-          S[b] = mfma_f32(kf[b][q], f[tb][q], S[b]);
-          S[b] = mfma_f32(qf[b][q], o[tb][q], S[b]);
-        }
-      __builtin_amdgcn_sched_barrier(0);
+      for (int b = 0; b < HB; ++b) put(lds.lx, B0 + b, S[b]);
     }
-  }
-  if (a.dstate_in && r < a.dv) {
+    if (a.dstate_in && r < a.dv) {
 #pragma unroll
-    for (int b = 0; b < NB; ++b)
-      if (16 * b + 4 * g < a.dk)
-        *reinterpret_cast<f32x4*>(static_cast<float*>(a.dstate_in) + so + 16 * b + 4 * g) = S[b];
-  }
+      for (int b = 0; b < HB; ++b) {
+        const int col = 16 * (B0 + b) + 4 * g;
+        if (col < a.dk)
+          *reinterpret_cast<f32x4*>(static_cast<float*>(a.dstate_in) + (head * a.dv + r) * a.dk + col) = S[b];
+      }
+    }
+  };
+  if (wave == 0) chain(std::integral_constant<int, 0>{});
+  else chain(std::integral_constant<int, 1>{});
 }
 
 // The gradients of one chunk, for the value heads of one key head in turn.  Wave
@@ -448,10 +517,8 @@ __global__ __launch_bounds__(256, 2) void delta_grad_f32(ChunkArgs ca) {
 
 template <int DK>
 hipError_t launch(const ChunkArgs& c, hipStream_t s) {
-  constexpr int NW = 2;
-  const int tiles = (c.a.dv + 16 * NW - 1) / (16 * NW);
-  delta_rev_f32<DK, NW>
-      <<<dim3(static_cast<unsigned>(head_blocks(c.a.N * c.a.H, tiles))), 64 * (NW + 1), 0, s>>>(c);
+  delta_rev_f32<DK><<<dim3(static_cast<unsigned>(head_blocks(c.a.N * c.a.H, delta_row_tiles(c.a.dv)))), kRevThreads, 0,
+                      s>>>(c);
   const hipError_t e = hipGetLastError();
   if (e != hipSuccess || c.slots == 0) return e;
   delta_grad_f32<DK><<<dim3(static_cast<unsigned>(c.slots * c.a.Hk)), 256, 0, s>>>(c);
