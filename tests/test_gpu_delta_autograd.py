@@ -1,0 +1,24 @@
+"""The autograd forms of the gated delta rule and of the norms on the GPU: what
+they cannot differentiate they refuse, and gradients arrive from any place."""
+import ctypes
+
+import pytest
+import torch
+from torch.autograd import forward_ad
+
+import weight_scans_amd as ws
+from delta_ref import delta, inputs, rel
+from test_gpu_delta import BF16, F32, F64, STATE_TOL, TOL, to_gpu
+
+pytestmark = pytest.mark.gpu
+
+NAMES = ["q", "k", "v", "log_alpha", "beta", "state"]
+
+
+def leaves(seed, dtype, T=80, B=1, H=2, Hk=2, d=64):
+    x = inputs(seed, B, H, Hk, T, d, d, dtype)
+    return x, {n: t.requires_grad_(True) for n, t in to_gpu(x, dtype, dtype).items()}
+
+
+def rule(p, **kw):
+    return ws.delta_rule(*[p[n] for n in NAMES[:5]], state=p["state"], **kw)

@@ -57,7 +57,8 @@ struct SolveLds {
 // the record.  la and be are log_alpha and beta (0 past the chunk's end).
 __device__ __forceinline__ void chunk_gate_factors(SolveLds& s, float* gt, float la, float be, bool between, int w,
                                                    int lane) {
-  const float x2 = fmaxf(la * 1.44269504088896f, -200.f);
+  // not fmaxf: a log_alpha that is no number stays one
+  const float la2 = la * 1.44269504088896f, x2 = la2 < -200.f ? -200.f : la2;
   const float xw = rintf(x2);
   const float lw = wave_scan_add(xw), lf = wave_scan_add(x2 - xw);
   if (w != 0) return;
