@@ -43,8 +43,11 @@
  * states and every accumulator in fp32.  Its matrix-core path carries the
  * recurrences (states in both directions, e_t) through operands split into two
  * bf16 terms (16 significand bits): final states and the gradient of the first
- * hold about 3e-6 (relative 2-norm), dlog_alpha 1e-5 before it is rounded to the
- * gate dtype.  y is rounded once, at the end (1.7e-3).  dq and dk
+ * hold about 3e-6 (relative 2-norm).  dlog_alpha, before it is rounded to the gate
+ * dtype, is a running sum where tokens keep more than 0.022 of the state: 1e-5 where
+ * they keep nearly all, growing as 1 / alpha (uniform log_alpha -3, 4096 tokens:
+ * 2e-3); a token that keeps less has the sum of what crosses it (1e-3, up to 5e-3 for
+ * single heads).  y is rounded once, at the end (1.7e-3).  dq and dk
  * come from products of two bf16 operands of which one (states, e_t, dv / beta)
  * was rounded once: 3e-3; dv and dbeta 2.5e-3.
  *

@@ -131,6 +131,15 @@ __device__ __forceinline__ s16x4 turned_raw(const uint16_t* frags, uint32_t at, 
   return tr4(reinterpret_cast<const char*>(frags) + (b >> 1) * 1024 + (at ^ (8 * (b & 1))));
 }
 
+// Sum over the 16 lanes of a row of lanes, in every lane.
+__device__ __forceinline__ float row_sum(float x) {
+  x += dpp<0x128>(0.f, x);  // row_ror:8, 4, 2, 1
+  x += dpp<0x124>(0.f, x);
+  x += dpp<0x122>(0.f, x);
+  x += dpp<0x121>(0.f, x);
+  return x;
+}
+
 // Lane l of each row of 16 lanes gets the row's sum of x[l].  Each step pairs
 // lanes that differ in one bit of what they still have to choose between and
 // agree in what they have chosen (lane ^ 8, ^ 7, ^ 3, ^ 1).

@@ -30,7 +30,9 @@
 // recurrence forms dv.v from its fp32 accumulators and dy.y from the forward's
 // fp32 y, and carries the sum for its 16 rows.  (The same gradient from the
 // rounded states and e, as the sum of the flows past token t, has no long sum,
-// but the rounding of each flow left errors of up to 7e-3.)  dbeta = G.e is
+// but the rounding of each flow left errors of up to 7e-3.  It is what tokens that keep
+// little of the state get, where the difference of the terms is lost in their own
+// rounding: delta_chunk_decay.)  dbeta = G.e is
 // formed there too, from the fp32 G.
 #include "delta_solve.hpp"
 #include "dev_common.hpp"
@@ -192,15 +194,16 @@ __global__ __launch_bounds__(64 * (2 * NW + 2)) void delta_chunk_rev(ChunkArgs c
         for (int q = 0; q < 4; ++q) z = fmaf(u[b][q], s[b][q], z);
     }
     z = wave_sum(z);
+    float lw = 0.f;
     for (int i = 0; i <= nc + 1; ++i) {
       lds_barrier();  // A
       lds_barrier();  // B: the results of the step before have been taken
       if (!STATES && i >= 2) {
         const int64_t rec = rec0 + static_cast<int64_t>(nc + 1 - i) * a.H;
         const float x = lds.dyy[w][(i - 2) % 3][lane] - lds.vdv[w][i & 1][lane];
-        const float y = wave_scan_add(wave_reverse(x, lane));
-        ca.zf[(rec * n_rt + rt) * 64 + 63 - lane] = z + y;
-        z += readlane_f(y, 63);
+        const float y = decay_sum(wave_reverse(x, lane), z, tokens_below(lw, kForget), lane);
+        ca.zf[(rec * n_rt + rt) * 64 + 63 - lane] = y;
+        z = readlane_f(y, 63);
       }
       f32x4 x1[4], x2[NB];
       if (i < nc) {
@@ -249,6 +252,8 @@ __global__ __launch_bounds__(64 * (2 * NW + 2)) void delta_chunk_rev(ChunkArgs c
 #pragma unroll
         for (int b = 0; b < NB; ++b) *reinterpret_cast<f32x4*>(&lds.x2[w][b * 256 + lane * 4]) = x2[b];
       }
+      if (!STATES && i >= 1 && i <= nc)  // the decay of the chunk whose sum the next step takes
+        lw = ca.gates[(rec0 + static_cast<int64_t>(nc - i) * a.H) * kGates + 192 + lane];
     }
     return;
   }
@@ -731,9 +736,6 @@ delta_chunk_grad(ChunkArgs ca) {
       }
     }
     if (w == 3) {
-      // a token that forgets everything has no gradient to its decay
-      const float lw = lds.gt[192 + lane];
-      if (lw - wave_shift_up(lw, 0.f) < -149.f) dl = 0.f;
       if (lane < nt) {
         const int64_t o = sr.b * a.sdg.b + h * a.sdg.h + (sr.t0 + t0 + lane) * a.sdg.t;
         if (a.gate_io) {
@@ -765,6 +767,181 @@ delta_chunk_grad(ChunkArgs ca) {
   }
 }
 
+// ---- dlog_alpha of the tokens that keep little (delta_solve.hpp), for chunks
+// that have one, after the gradients above: one work-group per chunk and value head,
+// four waves.
+//   m_ij = D_ij beta_j (scale q_i.k_j dO_i.e_j - beta_i k_i.k_j G_i.e_j)
+//   a_i = e^l_i (scale q_i.(dO S)_i - beta_i k_i.(G S)_i)
+//   b_j = e^(l_C - l_j) beta_j k_j.(e Lam)_j,  c = e^l_C <S, Lam>
+// from the same rounded S, Lam, e and G: relative errors of some 3e-3 of a gradient
+// that the running sum would lose.  Products as in delta_chunk_grad.  Where no chunk
+// has such a token a launch that reads 256 bytes a head and chunk.
+template <int DV>
+struct DecayLds {
+  alignas(16) char o[64 * DV * 2];
+  alignas(16) uint16_t e[64 * DV];
+  alignas(16) uint16_t g[64 * DV];
+  alignas(16) float gt[kGates];
+  float a[4][64], b[4][64], c[4];  // parts of the waves
+  Crossing x;
+  uint64_t found[16];
+};
+
+template <int DK, int DV>
+__global__ __launch_bounds__(kGradThreads) __attribute__((amdgpu_waves_per_eu(2))) void
+delta_chunk_decay(ChunkArgs ca) {
+  const DeltaArgs& a = ca.a;
+  constexpr int NB = DK / 16, NP = NB / 2, NT = NP, NR = DV / 32, NS = DK / 32;
+  __shared__ DecayLds<DV> lds;
+  const int lane = threadIdx.x & 63, l = lane & 15, g = lane >> 4;
+  const int w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  for_strong(ca, lds.found, w, lane, [&](int64_t rec, uint64_t strong) {
+    const int h = static_cast<int>(static_cast<uint32_t>(rec) % static_cast<uint32_t>(a.H));
+    const int64_t slot = static_cast<uint32_t>(rec) / static_cast<uint32_t>(a.H);
+    const int hk = h / (a.H / a.Hk);
+    SeqRange sr;
+    int64_t t0;
+    if (!chunk_of_slot(a, slot, sr, t0)) return;
+    __syncthreads();  // the one before is done with the tiles
+    const int nt = static_cast<int>(sr.len - t0 < 64 ? sr.len - t0 : 64);
+    const int n_rt = delta_row_tiles(a.dv), nr = n_rt / 2;
+    const int kb0 = 2 * (w % NP), tb0 = NT * (w / NP);
+    const float sc = static_cast<float>(a.scale);
+    const uint16_t* op = static_cast<const uint16_t*>(a.dy) + sr.b * a.sdy.b + h * a.sdy.h + sr.t0 * a.sdy.t;
+    const uint16_t* kp = static_cast<const uint16_t*>(a.k) + sr.b * a.sk.b + hk * a.sk.h + sr.t0 * a.sk.t;
+    const uint16_t* qp = static_cast<const uint16_t*>(a.q) + sr.b * a.sq.b + hk * a.sq.h + sr.t0 * a.sq.t;
+    const __amdgpu_buffer_rsrc_t rk = rows_rsrc(kp, t0, sr.len, a.sk.t, a.dk);
+    const __amdgpu_buffer_rsrc_t rq = rows_rsrc(qp, t0, sr.len, a.sq.t, a.dk);
+    {
+      const __amdgpu_buffer_rsrc_t ro = rows_rsrc(op, t0, sr.len, a.sdy.t, a.dv);
+      const __amdgpu_buffer_rsrc_t rg = buffer_rsrc(ca.gates + rec * kGates, kGates * 4);
+      const int eb = n_rt * 2 * kFrag * 2;
+      const __amdgpu_buffer_rsrc_t re = buffer_rsrc(ca.ef + rec * 2 * n_rt * kFrag, eb);
+      const __amdgpu_buffer_rsrc_t rr = buffer_rsrc(ca.gf + rec * 2 * n_rt * kFrag, eb);
+      if (w < 3) {
+#pragma unroll
+        for (int i = 0; i < 3; ++i) dma4(rg, ((3 * w + i) * 64 + lane) * 4, lds.gt + (3 * w + i) * 64);
+      }
+#pragma unroll
+      for (int j = 0; j < DV / 32; ++j) {
+        const int i = w * (DV / 32) + j;
+        dma16(re, i * 1024 + lane * 16, reinterpret_cast<char*>(lds.e) + i * 1024);
+        dma16(ro, tile_off<DV>(i, lane, a.sdy.t, 0, a.dv), lds.o + i * 1024);
+        dma16(rr, i * 1024 + lane * 16, reinterpret_cast<char*>(lds.g) + i * 1024);
+      }
+    }
+    s16x8 lc[2 * NR], st[2 * NR];  // this wave's columns of Lam and of S
+    const auto columns = [&](const uint16_t* p, s16x8 (&to)[2 * NR]) {
+      const __amdgpu_buffer_rsrc_t r = buffer_rsrc(p + rec * n_rt * (NB * kPiece), n_rt * NB * kPiece * 2);
+#pragma unroll
+      for (int rt = 0; rt < 2 * NR; ++rt)
+        to[rt] = __builtin_bit_cast(s16x8, load16(r, (rt * NB + kb0) * (kPiece * 2) + lane * 16));
+    };
+    columns(ca.lf, lc);
+    columns(ca.sf, st);
+    wait_vm<0>();
+    __syncthreads();
+    const TileLane<DV> to = tile_lane<DV>(lane);
+    const uint32_t ra = raw_turned(lane);
+    const auto piece = [&](const uint16_t* p, int tb, int R) {
+      return join(turned_raw(p + (4 * R) * kFrag, ra, tb), turned_raw(p + (4 * R + 2) * kFrag, ra, tb));
+    };
+    const auto half = [](const s16x8& v, int i) {
+      return widen(i ? __builtin_shufflevector(v, v, 4, 5, 6, 7) : __builtin_shufflevector(v, v, 0, 1, 2, 3));
+    };
+    const auto dot = [](const f32x4& u, const f32x4& v) { return (u[0] * v[0] + u[1] * v[1]) + (u[2] * v[2] + u[3] * v[3]); };
+
+    // ---- from the first state and to the end: products with the states, [column
+    // 4g + q of this wave's two blocks][token l], times the rows of q or k
+    const int col = index4(kb0, g);  // eight neighbouring columns
+    const auto product = [&](const s16x8 (&s)[2 * NR], auto&& operand, __amdgpu_buffer_rsrc_t rows, int64_t stride,
+                             int t) {
+      f32x4 x[2] = {zero4(), zero4()};
+#pragma unroll
+      for (int R = 0; R < NR; ++R) {
+        if (R >= nr) break;
+        const bf16x8 s0 = __builtin_bit_cast(bf16x8, __builtin_shufflevector(s[2 * R], s[2 * R + 1], 0, 1, 2, 3, 8, 9, 10, 11));
+        const bf16x8 s1 = __builtin_bit_cast(bf16x8, __builtin_shufflevector(s[2 * R], s[2 * R + 1], 4, 5, 6, 7, 12, 13, 14, 15));
+        const bf16x8 f = operand(tb0 + t, R);
+        x[0] = mfma16x16x32(s0, f, x[0]);
+        x[1] = mfma16x16x32(s1, f, x[1]);
+      }
+      const uint32_t at = static_cast<uint32_t>((16 * (tb0 + t) + l) * stride * 2);
+      const s16x8 v = __builtin_bit_cast(s16x8, load16(rows, col < a.dk ? at + col * 2 : kPastEnd));
+      return sum_rows(dot(x[0], half(v, 0)) + dot(x[1], half(v, 1)));
+    };
+#pragma unroll
+    for (int t = 0; t < NT; ++t) {
+      const int tok = 16 * (tb0 + t) + l;
+      const float gam = lds.gt[tok], bet = lds.gt[64 + tok], rst = lds.gt[128 + tok];
+      const float oq = product(st, [&](int tb, int R) { return frag_n<DV>(lds.o, to, tb, R); }, rq, a.sq.t, t);
+      const float gk = product(st, [&](int tb, int R) { return piece(lds.g, tb, R); }, rk, a.sk.t, t);
+      const float ek = product(lc, [&](int tb, int R) { return piece(lds.e, tb, R); }, rk, a.sk.t, t);
+      if (g == 0) {
+        lds.a[w][tok] = gam * (sc * oq - bet * gk);
+        lds.b[w][tok] = rst * bet * ek;
+      }
+    }
+    {
+      float c = 0.f;
+      if (tb0 == 0) {
+#pragma unroll
+        for (int rt = 0; rt < 2 * NR; ++rt)
+#pragma unroll
+          for (int i = 0; i < 2; ++i) c += dot(half(st[rt], i), half(lc[rt], i));
+      }
+      c = wave_sum(c);
+      if (lane == 0) lds.c[w] = c;
+    }
+    // ---- from token to token: blocks of 16 x 16 of the lower triangle in turn
+    for (int b = w; b < 10; b += 4) {
+      const int x = tri_i(b), y = tri_j(b);
+      f32x4 oe = zero4(), ge = zero4(), qk = zero4(), kk = zero4();
+      for (int R = 0; R < nr; ++R) {
+        const bf16x8 e = piece(lds.e, y, R);
+        oe = mfma16x16x32(frag_n<DV>(lds.o, to, x, R), e, oe);
+        ge = mfma16x16x32(piece(lds.g, x, R), e, ge);
+      }
+#pragma unroll
+      for (int c = 0; c < NS; ++c) {
+        const uint32_t cc = 32 * c + 8 * g < a.dk ? static_cast<uint32_t>((32 * c + 8 * g) * 2) : kPastEnd;
+        const auto row = [&](__amdgpu_buffer_rsrc_t r, int64_t stride, int tb) {
+          return load16(r, cc + static_cast<uint32_t>((16 * tb + l) * stride * 2));
+        };
+        const bf16x8 kj = row(rk, a.sk.t, y);
+        qk = mfma16x16x32(row(rq, a.sq.t, x), kj, qk);
+        kk = mfma16x16x32(row(rk, a.sk.t, x), kj, kk);
+      }
+      const int j = 16 * y + l;
+      const float lw = lds.gt[192 + j], lf = lds.gt[256 + j], bj = lds.gt[64 + j];
+#pragma unroll
+      for (int q = 0; q < 4; ++q) {
+        const int i = 16 * x + 4 * g + q;
+        const float d = bj * fexp2((lds.gt[192 + i] - lw) + (lds.gt[256 + i] - lf));
+        lds.x.m[i * 65 + j] = d * (sc * qk[q] * oe[q] - lds.gt[64 + i] * kk[q] * ge[q]);
+      }
+    }
+    __syncthreads();
+    if (w == 0) lds.x.gather(lane);
+    __syncthreads();
+    if (w != 0) return;
+    float from = 0.f, into = 0.f, all = 0.f;
+    const int w0 = (lane >> 4) / NT * NP;
+#pragma unroll
+    for (int i = 0; i < NP; ++i) {
+      from += lds.a[w0 + i][lane];
+      into += lds.b[w0 + i][lane];
+      all += lds.c[i];
+    }
+    const float z = lds.x.at(from, into, lds.gt[63] * all, lane);
+    if (lane < nt && ((strong >> lane) & 1)) {
+      const int64_t o = sr.b * a.sdg.b + h * a.sdg.h + (sr.t0 + t0 + lane) * a.sdg.t;
+      if (a.gate_io) static_cast<uint16_t*>(a.dla)[o] = f32_to_bf16(z);
+      else static_cast<float*>(a.dla)[o] = z;
+    }
+  });
+}
+
 template <int DK>
 hipError_t launch(const ChunkArgs& c, hipStream_t s) {
   constexpr int NW = 2;
@@ -787,6 +964,9 @@ hipError_t launch(const ChunkArgs& c, hipStream_t s) {
     if (shared) delta_chunk_grad<DK, 128, true><<<grid, kGradThreads, 0, s>>>(c);
     else delta_chunk_grad<DK, 128, false><<<grid, kGradThreads, 0, s>>>(c);
   }
+  if ((e = hipGetLastError()) != hipSuccess) return e;
+  if (c.a.dv <= 64) delta_chunk_decay<DK, 64><<<seek_groups(c, 2), kGradThreads, 0, s>>>(c);
+  else delta_chunk_decay<DK, 128><<<seek_groups(c, 2), kGradThreads, 0, s>>>(c);
   return hipGetLastError();
 }
 

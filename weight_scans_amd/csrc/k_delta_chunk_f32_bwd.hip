@@ -5,7 +5,8 @@
 // The decay's gradient is again dlog_alpha_t = <dL/dS_T, S_T> + sum_{s >= t}
 // (dy_s.y_s - dv_s.v_s); here both states are kept in fp32, so the product
 // <Lam, S> is taken anew at every chunk's end and the sum runs over the chunk's
-// tokens only.
+// tokens only.  Tokens that keep little of the state get it as in bf16 from what
+// crosses them (delta_decay_f32).
 //
 // The recurrence is bound by the matrix rate of the waves that have a row tile's
 // chain, the gradients by the matrix cores and HBM: 4 x 8 x 1024 x 64 takes 56 us
@@ -128,6 +129,7 @@ __global__ __launch_bounds__(kRevThreads) void delta_rev_f32(ChunkArgs ca) {
     f32x4 sn[NB];  // the state after the chunk, turned
     for (int c = nc - 1; c >= 0; --c) {
       const int64_t rec = rec_of(c);
+      const float lw = ca.gates[rec * kGates + 192 + lane];
       f32x4 dO[4], V[4], Y[4], E[4];
       {
         const __amdgpu_buffer_rsrc_t ro = rows_f32(op, c * 64LL, sr.len, a.sdy.t, a.dv);
@@ -177,9 +179,9 @@ __global__ __launch_bounds__(kRevThreads) void delta_rev_f32(ChunkArgs ca) {
       const int tok = 16 * (l >> 2) + 4 * g + (l & 3);
       const float db = row_sums(xe, l);
       lds.xs[tok] = row_sums(xv, l);
-      const float suffix = wave_scan_add(lds.xs[63 - lane]);
+      const float sum = decay_sum(lds.xs[63 - lane], z, tokens_below(lw, kForget), lane);
       ca.bf[(rec * n_rt + rt) * 64 + tok] = db;
-      ca.zf[(rec * n_rt + rt) * 64 + 63 - lane] = z + suffix;
+      ca.zf[(rec * n_rt + rt) * 64 + 63 - lane] = sum;
     }
     return;
   }
@@ -458,9 +460,6 @@ __device__ __forceinline__ void grad_block(const ChunkArgs& ca, const GradLds<DK
         dl += z[i];
         db += b[i];
       }
-      // a token that forgets everything has no gradient to its decay
-      const float w = gt[192 + lane];
-      if (w - wave_shift_up(w, 0.f) < -149.f) dl = 0.f;
       if (lane < nt) {
         const int64_t o = sr.b * a.sdg.b + h * a.sdg.h + (sr.t0 + t0 + lane) * a.sdg.t;
         static_cast<float*>(a.dla)[o] = dl;
@@ -515,13 +514,148 @@ __global__ __launch_bounds__(256, 2) void delta_grad_f32(ChunkArgs ca) {
   else grad_block<DK, 3>(ca, lds, slot, sr, t0, hk, lane);
 }
 
+// dlog_alpha of the tokens that keep little (delta_solve.hpp), for chunks that have
+// one: the terms of the bf16 form (delta_chunk_decay) in fp32, one work-group per
+// chunk and value head, wave w with the tokens of block w.
+template <int DK>
+struct DecayLds {
+  alignas(16) char k[64 * DK * 4];
+  alignas(16) char q[64 * DK * 4];
+  float a[64], b[64], c;
+  Crossing x;
+  uint64_t found[16];
+};
+
+template <int DK>
+__global__ __launch_bounds__(256) void delta_decay_f32(ChunkArgs ca) {
+  const DeltaArgs& a = ca.a;
+  constexpr int NB = DK / 16;
+  __shared__ DecayLds<DK> lds;
+  const int lane = threadIdx.x & 63, l = lane & 15, g = lane >> 4;
+  const int w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  for_strong(ca, lds.found, w, lane, [&](int64_t rec, uint64_t strong) {
+    const int h = static_cast<int>(static_cast<uint32_t>(rec) % static_cast<uint32_t>(a.H));
+    const int64_t slot = static_cast<uint32_t>(rec) / static_cast<uint32_t>(a.H);
+    const int hk = h / (a.H / a.Hk);
+    SeqRange sr;
+    int64_t t0;
+    if (!chunk_of_slot(a, slot, sr, t0)) return;
+    __syncthreads();  // the one before is done with the tiles
+    const float* gt = ca.gates + rec * kGates;
+    const int nt = static_cast<int>(sr.len - t0 < 64 ? sr.len - t0 : 64);
+    const int n_rt = delta_row_tiles(a.dv), VP = 16 * n_rt;
+    const float sc = static_cast<float>(a.scale);
+    {
+      const float* kp = static_cast<const float*>(a.k) + sr.b * a.sk.b + hk * a.sk.h + sr.t0 * a.sk.t;
+      const float* qp = static_cast<const float*>(a.q) + sr.b * a.sq.b + hk * a.sq.h + sr.t0 * a.sq.t;
+      const __amdgpu_buffer_rsrc_t rk = rows_f32(kp, t0, sr.len, a.sk.t, a.dk);
+      const __amdgpu_buffer_rsrc_t rq = rows_f32(qp, t0, sr.len, a.sq.t, a.dk);
+#pragma unroll
+      for (int j = 0; j < DK / 16; ++j) {
+        const int i = w * (DK / 16) + j;
+        dma16(rk, tile_off_f32<DK>(i, lane, a.sk.t, a.dk), lds.k + i * 1024);
+        dma16(rq, tile_off_f32<DK>(i, lane, a.sq.t, a.dk), lds.q + i * 1024);
+      }
+    }
+    const __amdgpu_buffer_rsrc_t ro = rows_f32(
+        static_cast<const float*>(a.dy) + sr.b * a.sdy.b + h * a.sdy.h + sr.t0 * a.sdy.t, t0, sr.len, a.sdy.t, a.dv);
+    const float* ep = ca.e32 + (rec * 64 + l) * VP + 4 * g;
+    const float* gp = ca.g32 + (rec * 64 + l) * VP + 4 * g;
+    const float* sp = ca.s32 + rec * n_rt * (NB * 256) + lane * 4;
+    const float* lp = ca.l32 + rec * n_rt * (NB * 256) + lane * 4;
+    f32x4 oe[4], ge[4], os[NB], gs[NB], el[NB];
+    float c = 0.f;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) oe[j] = ge[j] = zero4();
+#pragma unroll
+    for (int b = 0; b < NB; ++b) os[b] = gs[b] = el[b] = zero4();
+#pragma unroll 1
+    for (int rt = 0; rt < n_rt; ++rt) {
+      const int r = 16 * rt + 4 * g;
+      const f32x4 d = load_f32x4(ro, r < a.dv ? static_cast<uint32_t>(((16 * w + l) * static_cast<int>(a.sdy.t) + r) * 4)
+                                              : kPastEnd);
+      const f32x4 G = *reinterpret_cast<const f32x4*>(gp + 16 * w * VP + 16 * rt);
+      const f32x4 own = *reinterpret_cast<const f32x4*>(ep + 16 * w * VP + 16 * rt);
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        if (j > w) break;
+        const f32x4 e = *reinterpret_cast<const f32x4*>(ep + 16 * j * VP + 16 * rt);
+        oe[j] = mul16(d, e, oe[j]);
+        ge[j] = mul16(G, e, ge[j]);
+      }
+#pragma unroll
+      for (int b = 0; b < NB; ++b) {
+        const f32x4 s = *reinterpret_cast<const f32x4*>(sp + (rt * NB + b) * 256);
+        const f32x4 lam = *reinterpret_cast<const f32x4*>(lp + (rt * NB + b) * 256);
+        os[b] = mul16(d, s, os[b]);
+        gs[b] = mul16(G, s, gs[b]);
+        el[b] = mul16(own, lam, el[b]);
+#pragma unroll
+        for (int q = 0; q < 4; ++q) c = fmaf(s[q], lam[q], c);
+      }
+    }
+    c = wave_sum(c);
+    if (w == 0 && lane == 0) lds.c = c;
+    wait_vm<0>();
+    __syncthreads();
+    const uint32_t ra = row_at<DK>(lane);
+    const uint32_t kc[4] = {col_at<DK>(lane, 0), col_at<DK>(lane, 1), col_at<DK>(lane, 2), col_at<DK>(lane, 3)};
+    // tokens 16 w + 4g + q, columns in lanes
+    f32x4 oq = zero4(), gk = zero4(), ek = zero4();
+#pragma unroll
+    for (int b = 0; b < NB; ++b) {
+      const f32x4 q = col_frag<DK>(lds.q, kc, w, b), k = col_frag<DK>(lds.k, kc, w, b);
+      oq += os[b] * q;
+      gk += gs[b] * k;
+      ek += el[b] * k;
+    }
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+      const int tok = 16 * w + 4 * g + q;
+      const float x = gt[tok] * (sc * row_sum(oq[q]) - gt[64 + tok] * row_sum(gk[q]));
+      const float y = gt[128 + tok] * gt[64 + tok] * row_sum(ek[q]);
+      if (l == 0) {
+        lds.a[tok] = x;
+        lds.b[tok] = y;
+      }
+    }
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      if (j > w) break;
+      f32x4 qk = zero4(), kk = zero4();
+#pragma unroll
+      for (int b = 0; b < NB; ++b) {
+        const f32x4 kj = row_frag<DK>(lds.k, ra, j, b);
+        qk = mul16(row_frag<DK>(lds.q, ra, w, b), kj, qk);
+        kk = mul16(row_frag<DK>(lds.k, ra, w, b), kj, kk);
+      }
+      const int y = 16 * j + l;
+#pragma unroll
+      for (int q = 0; q < 4; ++q) {
+        const int x = 16 * w + 4 * g + q;
+        const float f = gt[64 + y] * fexp2((gt[192 + x] - gt[192 + y]) + (gt[256 + x] - gt[256 + y]));
+        lds.x.m[x * 65 + y] = f * (sc * qk[q] * oe[j][q] - gt[64 + x] * kk[q] * ge[j][q]);
+      }
+    }
+    __syncthreads();
+    if (w == 0) lds.x.gather(lane);
+    __syncthreads();
+    if (w != 0) return;
+    const float z = lds.x.at(lds.a[lane], lds.b[lane], gt[63] * lds.c, lane);
+    if (lane < nt && ((strong >> lane) & 1))
+      static_cast<float*>(a.dla)[sr.b * a.sdg.b + h * a.sdg.h + (sr.t0 + t0 + lane) * a.sdg.t] = z;
+  });
+}
+
 template <int DK>
 hipError_t launch(const ChunkArgs& c, hipStream_t s) {
   delta_rev_f32<DK><<<dim3(static_cast<unsigned>(head_blocks(c.a.N * c.a.H, delta_row_tiles(c.a.dv)))), kRevThreads, 0,
                       s>>>(c);
-  const hipError_t e = hipGetLastError();
+  hipError_t e = hipGetLastError();
   if (e != hipSuccess || c.slots == 0) return e;
   delta_grad_f32<DK><<<dim3(static_cast<unsigned>(c.slots * c.a.Hk)), 256, 0, s>>>(c);
+  if ((e = hipGetLastError()) != hipSuccess) return e;
+  delta_decay_f32<DK><<<seek_groups(c, DK <= 64 ? 2 : 1), 256, 0, s>>>(c);
   return hipGetLastError();
 }
 
