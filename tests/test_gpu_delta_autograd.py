@@ -22,3 +22,18 @@ def leaves(seed, dtype, T=80, B=1, H=2, Hk=2, d=64):
 
 def rule(p, **kw):
     return ws.delta_rule(*[p[n] for n in NAMES[:5]], state=p["state"], **kw)
+
+
+def test_forward_mode_is_refused():
+    """There is no forward-mode derivative: a dual tensor is not taken for a constant."""
+    _, p = leaves(1, F32)
+    p = {n: t.detach() for n, t in p.items()}
+    for n in NAMES:
+        with forward_ad.dual_level():
+            duals = {**p, n: forward_ad.make_dual(p[n], torch.ones_like(p[n]))}
+            with pytest.raises(RuntimeError):
+                rule(duals)
+    with forward_ad.dual_level():
+        assert torch.equal(rule(p)[0], rule(p)[0])  # no dual among them
+        with pytest.raises(RuntimeError):
+            ws.qknorm_rope(forward_ad.make_dual(p["q"], torch.ones_like(p["q"])), p["k"])

@@ -456,10 +456,19 @@ def _functions():
     return _fns
 
 
+def _no_duals(inputs):
+    """Refuses dual tensors: they want a forward-mode derivative, which there is not."""
+    forward_ad = _torch().autograd.forward_ad
+    if forward_ad._current_level >= 0 and any(
+            t is not None and forward_ad.unpack_dual(t).tangent is not None for t in inputs):
+        raise NotImplementedError("the delta rule has no forward-mode derivative")
+
+
 def delta_rule(q, k, v, log_alpha, beta, *, scale=None, state=None, cu_seqlens=None, want_state=False):
     """Autograd-aware gl_delta_fwd: (y, final state or None).  Nothing is kept
     for a backward where no gradient is wanted."""
     inputs = (q, k, v, log_alpha, beta, state)
+    _no_duals(inputs)
     if not (_torch().is_grad_enabled() and any(t is not None and t.requires_grad for t in inputs)):
         return gl_delta_fwd(q, k, v, log_alpha, beta, scale=scale, state=state, want_state=want_state,
                             cu_seqlens=cu_seqlens)[:2]
