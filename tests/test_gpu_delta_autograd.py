@@ -37,3 +37,16 @@ def test_forward_mode_is_refused():
         assert torch.equal(rule(p)[0], rule(p)[0])  # no dual among them
         with pytest.raises(RuntimeError):
             ws.qknorm_rope(forward_ad.make_dual(p["q"], torch.ones_like(p["q"])), p["k"])
+
+
+def test_second_derivatives_are_refused():
+    """Gradients of gradients would lose what runs through the rule or the norms."""
+    _, p = leaves(2, F32)
+    y, end = rule(p, want_state=True)
+    dq, = torch.autograd.grad(y.square().sum() + end.square().sum(), p["q"], create_graph=True)
+    with pytest.raises(RuntimeError, match="once_differentiable"):
+        (dq.square().sum() + p["q"].square().sum()).backward()
+    qn, kn = ws.qknorm_rope(p["q"], p["k"])
+    dq, = torch.autograd.grad(qn.pow(3).sum() + kn.pow(3).sum(), p["q"], create_graph=True)
+    with pytest.raises(RuntimeError, match="once_differentiable"):
+        (dq.square().sum() + p["q"].square().sum()).backward()

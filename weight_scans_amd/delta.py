@@ -411,6 +411,8 @@ def _whole(t):
 
 def _make_functions():
     torch = _torch()
+    # the kernels leave no graph behind: gradients of gradients are refused, not lost
+    once = torch.autograd.function.once_differentiable
 
     class DeltaRule(torch.autograd.Function):
         @staticmethod
@@ -422,6 +424,7 @@ def _make_functions():
             return y, out
 
         @staticmethod
+        @once
         def backward(ctx, dy, dstate):
             q, k, v, log_alpha, beta, state, cu_seqlens, saved = ctx.saved_tensors
             grads = gl_delta_bwd(q, k, v, log_alpha, beta, _whole(dy), saved, scale=ctx.scale, state=state,
@@ -436,6 +439,7 @@ def _make_functions():
             return gl_qknorm_rope_fwd(q, k, wq, wk, cos, sin, pos=pos, **opts)
 
         @staticmethod
+        @once
         def backward(ctx, dqn, dkn):
             q, k, wq, wk, cos, sin, pos = ctx.saved_tensors
             dq, dk, dwq, dwk = gl_qknorm_rope_bwd(q, k, wq, wk, cos, sin, _whole(dqn), _whole(dkn), pos=pos,
