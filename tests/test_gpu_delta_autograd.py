@@ -50,3 +50,29 @@ def test_second_derivatives_are_refused():
     dq, = torch.autograd.grad(qn.pow(3).sum() + kn.pow(3).sum(), p["q"], create_graph=True)
     with pytest.raises(RuntimeError, match="once_differentiable"):
         (dq.square().sum() + p["q"].square().sum()).backward()
+
+
+@pytest.mark.parametrize("dtype", [F64, F32, BF16])
+@pytest.mark.parametrize("T", [3, 80])
+def test_gradients_that_begin_anywhere(dtype, T):
+    """Upstream gradients that are slices of a longer vector: of y, of the final state, of both norms."""
+    x, p = leaves(3, dtype, T)
+    for n in NAMES:
+        x[n].requires_grad_(True)
+    wy, wend = delta(x["q"], x["k"], x["v"], x["log_alpha"], x["beta"], 0.125, x["state"])
+    up, ups = x["dy"], x["dstate"]
+    want = torch.autograd.grad((wy * up).sum() + (wend * ups).sum(), [x[n] for n in NAMES])
+    y, end = rule(p, want_state=True)
+    side = torch.zeros(3, device="cuda")
+    a = (torch.cat([side.to(y.dtype), y.flatten()]) * torch.cat([side.to(y.dtype), up.to(y.dtype).cuda().flatten()])).sum()
+    b = (torch.cat([side.to(end.dtype), end.flatten()])
+         * torch.cat([side.to(end.dtype), ups.to(end.dtype).cuda().flatten()])).sum()
+    torch.autograd.backward([a, b])
+    for n, w in zip(NAMES, want):
+        assert rel(p[n].grad, w) <= (2 * STATE_TOL[dtype] if n == "state" else TOL[dtype]), n
+    qn, kn = ws.qknorm_rope(p["q"], p["k"])
+    ref = torch.autograd.grad(qn, p["q"], x["dy"].to(dtype).cuda())[0]
+    qn, kn = ws.qknorm_rope(p["q"], p["k"])
+    both = torch.cat([side[:1].to(dtype), qn.flatten(), kn.flatten()])
+    w = torch.cat([side[:1].to(dtype), x["dy"].to(dtype).cuda().flatten(), torch.zeros_like(kn).flatten()])
+    assert rel(torch.autograd.grad((both * w).sum(), p["q"])[0], ref.double().cpu()) <= TOL[dtype]

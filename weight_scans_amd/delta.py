@@ -404,9 +404,16 @@ def gl_qknorm_rope_bwd(q, k, wq, wk, cos, sin, dqn, dkn, *, pos=None, pos0=0, ep
 
 
 # ---------------------------------------------------------------- autograd
+def _aligned(t):
+    """t if it begins on 16 bytes, else a dense copy (contiguous() would return a
+    dense slice of a longer tensor as it is)."""
+    return t if t.data_ptr() % 16 == 0 else t.clone(memory_format=_torch().contiguous_format)
+
+
 def _whole(t):
-    """t as it is if it is dense in some order of its heads and tokens, else a copy."""
-    return t if _dense(t) and t.stride(-1) == 1 and t.data_ptr() % 16 == 0 else t.contiguous()
+    """t as it is if it is dense in some order of its heads and tokens and begins on
+    16 bytes, else a dense copy."""
+    return _aligned(t if _dense(t) and t.stride(-1) == 1 else t.contiguous())
 
 
 def _make_functions():
@@ -427,8 +434,9 @@ def _make_functions():
         @once
         def backward(ctx, dy, dstate):
             q, k, v, log_alpha, beta, state, cu_seqlens, saved = ctx.saved_tensors
+            dstate = None if dstate is None else _aligned(dstate.contiguous())
             grads = gl_delta_bwd(q, k, v, log_alpha, beta, _whole(dy), saved, scale=ctx.scale, state=state,
-                                 dstate=None if dstate is None else dstate.contiguous(), cu_seqlens=cu_seqlens)
+                                 dstate=dstate, cu_seqlens=cu_seqlens)
             return (*grads, None, None, None)
 
     class QkNormRope(torch.autograd.Function):
@@ -477,7 +485,7 @@ def delta_rule(q, k, v, log_alpha, beta, *, scale=None, state=None, cu_seqlens=N
         return gl_delta_fwd(q, k, v, log_alpha, beta, scale=scale, state=state, want_state=want_state,
                             cu_seqlens=cu_seqlens)[:2]
     # slices that begin between two 16-byte units: training wants them aligned
-    q, k, v = (t if t.data_ptr() % 16 == 0 else t.clone(memory_format=_torch().contiguous_format) for t in (q, k, v))
+    q, k, v = (_aligned(t) for t in (q, k, v))
     return _functions()[0].apply(q, k, v, log_alpha, beta, state, scale, cu_seqlens, want_state)
 
 
