@@ -76,3 +76,47 @@ def test_gradients_that_begin_anywhere(dtype, T):
     both = torch.cat([side[:1].to(dtype), qn.flatten(), kn.flatten()])
     w = torch.cat([side[:1].to(dtype), x["dy"].to(dtype).cuda().flatten(), torch.zeros_like(kn).flatten()])
     assert rel(torch.autograd.grad((both * w).sum(), p["q"])[0], ref.double().cpu()) <= TOL[dtype]
+
+
+def test_gates_of_other_strides():
+    """Strides of dimensions of one element say nothing; gates in different orders are
+    brought into one for the autograd form."""
+    x = inputs(4, 1, 4, 2, 70, 64, 64, BF16, F32)
+    g = to_gpu(x, BF16, F32)
+    both = torch.cat([g["log_alpha"], g["beta"]], 1)
+    log_alpha, beta = both[:, :4], g["beta"]
+    assert log_alpha.stride() != beta.stride()
+    q, k, v = g["q"], g["k"], g["v"]
+    y0, s0, _ = ws.gl_delta_fwd(q, k, v, g["log_alpha"], g["beta"], want_state=True)
+    y1, s1, saved = ws.gl_delta_fwd(q, k, v, log_alpha, beta, want_state=True, save=True)
+    assert rel(y1, y0.double().cpu()) <= TOL[BF16] and rel(s1, s0.double().cpu()) <= STATE_TOL[BF16]
+    one = ws.gl_delta_bwd(q, k, v, g["log_alpha"], g["beta"], g["dy"])
+    for a, b in zip(ws.gl_delta_bwd(q, k, v, log_alpha, beta, g["dy"], saved)[:5], one[:5]):
+        assert torch.equal(a, b)
+    pools = [torch.zeros((1, 4, 64, 64), device="cuda") for _ in range(2)]
+    tok = lambda *t: [z[:, :, 0] for z in t]  # noqa: E731
+    ya = ws.gl_delta_step(*tok(q, k, v, g["log_alpha"], g["beta"]), pools[0])
+    one = torch.cat([g["log_alpha"][:, :, 0], g["beta"][:, :, 0]], 1)
+    yb = ws.gl_delta_step(*tok(q, k, v), one[:, :4], one[:, 4:].contiguous(), pools[1])
+    assert torch.equal(ya, yb) and torch.equal(*pools)
+    with pytest.raises(ValueError):  # heads 70 and 1 elements apart: strides that matter
+        ws.gl_delta_step(*tok(q, k, v), both[:, :4, 0], g["beta"][:, :, 0].contiguous(), pools[1])
+
+
+@pytest.mark.parametrize("B", [1, 2])
+def test_gates_of_other_orders_in_autograd(B):
+    x = inputs(5, B, 4, 2, 70, 64, 64, BF16, F32)
+    for n in ("log_alpha", "beta"):
+        x[n].requires_grad_(True)
+    y, _ = delta(x["q"], x["k"], x["v"], x["log_alpha"], x["beta"], 0.125)
+    want = torch.autograd.grad((y * x["dy"]).sum(), [x["log_alpha"], x["beta"]])
+    g = to_gpu(x, BF16, F32)
+    la = g["log_alpha"].clone().requires_grad_(True)
+    be = g["beta"].transpose(1, 2).contiguous().requires_grad_(True)  # [B,T,H]
+    got, _ = ws.delta_rule(g["q"], g["k"], g["v"], la, be.transpose(1, 2))
+    (got.float() * g["dy"].float()).sum().backward()
+    assert rel(got, y) <= TOL[BF16]
+    assert rel(la.grad, want[0]) <= TOL[BF16] and rel(be.grad.transpose(1, 2), want[1]) <= TOL[BF16]
+    with torch.no_grad():
+        again, _ = ws.delta_rule(g["q"], g["k"], g["v"], la, be.transpose(1, 2))
+    assert rel(again, y) <= TOL[BF16]

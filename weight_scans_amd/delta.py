@@ -217,10 +217,19 @@ def _delta_desc(q, k, v, log_alpha, beta, scale, state, cu, flags, segments):
                            n_seq=0 if cu is None else n, flags=flags, segments=segments,
                            scale=dk ** -0.5 if scale is None else scale)
     desc.sq, desc.sk, desc.sv = _rows(q, "q"), _rows(k, "k"), _rows(v, "v")
-    if log_alpha.stride() != beta.stride():
-        raise ValueError("log_alpha and beta must have the same strides")
-    desc.sg = _three(beta.stride(), beta.shape, "beta")
+    desc.sg = _gate_strides(log_alpha, beta)
     return desc, n
+
+
+def _moves(t):
+    """t's strides in the dimensions that have any: those of one element say nothing."""
+    return [s for s, n in zip(t.stride(), t.shape) if n > 1]
+
+
+def _gate_strides(log_alpha, beta):
+    if _moves(log_alpha) != _moves(beta):
+        raise ValueError("log_alpha and beta must have the same strides")
+    return _three(beta.stride(), beta.shape, "beta")
 
 
 def _check_state(t, shape, io, name):
@@ -324,14 +333,12 @@ def gl_delta_step(q, k, v, log_alpha, beta, state, *, scale=None, slots=None, y=
             raise ValueError("slots must be a contiguous int32 tensor [B]")
         if y is not None and (tuple(y.shape) != (B, H, dv) or y.dtype != v.dtype):
             raise ValueError("y must be [B,H,dv] of v's dtype")
-        if log_alpha.stride() != beta.stride():
-            raise ValueError("log_alpha and beta must have the same strides")
         _on_gpu((q, k, v, log_alpha, beta, state, slots, y))
         desc = make_delta_desc(B, 1, H, Hk, dk, dv, _io_code(q.dtype), _io_code(beta.dtype),
                                scale=dk ** -0.5 if scale is None else scale)
         desc.sq, desc.sk, desc.sv = _rows(q, "q"), _rows(k, "k"), _rows(v, "v")
         desc.sy = _three((H * dv, dv), (B, H), "y") if y is None else _rows(y, "y")
-        desc.sg = _three(beta.stride(), beta.shape, "beta")
+        desc.sg = _gate_strides(log_alpha, beta)
         return desc, 0, state.shape[0], (_contiguous((B, H, dv), v.dtype) if y is None else None,)
     out = _run("gl_delta_step", scale, (q, k, v, log_alpha, beta, slots, state, y), plan)[0]
     return out if y is None else y
@@ -478,7 +485,10 @@ def _no_duals(inputs):
 
 def delta_rule(q, k, v, log_alpha, beta, *, scale=None, state=None, cu_seqlens=None, want_state=False):
     """Autograd-aware gl_delta_fwd: (y, final state or None).  Nothing is kept
-    for a backward where no gradient is wanted."""
+    for a backward where no gradient is wanted.  Gates of different strides are
+    copied into one order, q, k, v that do not begin on 16 bytes in training."""
+    if log_alpha.shape == beta.shape and _moves(log_alpha) != _moves(beta):  # one order for both
+        log_alpha, beta = log_alpha.contiguous(), beta.contiguous()
     inputs = (q, k, v, log_alpha, beta, state)
     _no_duals(inputs)
     if not (_torch().is_grad_enabled() and any(t is not None and t.requires_grad for t in inputs)):
