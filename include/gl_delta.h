@@ -23,6 +23,8 @@
  * saves nothing takes the other path by itself where they are not).
  * Value head h reads query and key head h / (H / Hk); dq and dk sum over the
  * value heads that share them.
+ * state_out may be state_in itself, and dstate_in dstate_out (every path has read
+ * what it writes over); no other output may overlap an input.
  *
  * Packed sequences: with n_seq > 0, B is 1, the T tokens hold n_seq sequences
  * one after another and cu_seqlens (device, int32, n_seq + 1 values, first 0,

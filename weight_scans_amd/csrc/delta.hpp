@@ -136,9 +136,9 @@ struct ChunkArgs {
   uint16_t* gf = nullptr;
   int64_t slots = 0;    // chunk slots of the call
   int n_seg = 1;        // segments per sequence
-  float* seg_s = nullptr;  // [head][n_seg][dv][dk] their first states (from the second on)
+  float* seg_s = nullptr;  // [head][n_seg][dv][dk] their first states (the first's: state_in, if given)
   float* seg_m = nullptr;  // [head][n_seg][dk][dk] what they do to a state
-  float* seg_l = nullptr;  // backward: [head][n_seg][dv][dk] their last adjoints (but the last's)
+  float* seg_l = nullptr;  // backward: [head][n_seg][dv][dk] their last adjoints (the last's: dstate_out, if given)
 };
 inline int delta_wide(int d) { return d <= 64 ? 64 : 128; }
 __host__ __device__ inline int delta_row_tiles(int dv) { return (dv + 31) / 32 * 2; }

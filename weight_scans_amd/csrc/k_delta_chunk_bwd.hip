@@ -79,9 +79,13 @@ __global__ __launch_bounds__(64 * (2 * NW + 2)) void delta_chunk_rev(ChunkArgs c
   const int64_t rec0 = slot0 * a.H + h;
   // the adjoint after the last chunk and the state there
   const int64_t dd = static_cast<int64_t>(a.dv) * a.dk;
-  const float* lam_end = last     ? (a.dstate_out ? static_cast<const float*>(a.dstate_out) + head * dd : nullptr)
+  // (in segments the call's last adjoint too comes from seg_l, where the STATES pass
+  // leaves it: the first segment writes dstate_in, which may be the same memory)
+  float* seg_l = ca.seg_l + (head * ca.n_seg + seg) * dd;
+  const float* given = last && a.dstate_out ? static_cast<const float*>(a.dstate_out) + head * dd : nullptr;
+  const float* lam_end = last     ? (given && !STATES && ca.n_seg > 1 ? seg_l : given)
                          : STATES ? nullptr
-                                  : ca.seg_l + (head * ca.n_seg + seg) * dd;
+                                  : seg_l;
   const float* state_end = last ? ca.st + head * dd : ca.seg_s + (head * ca.n_seg + seg + 1) * dd;
 
   // Step i: the helpers take chunk nc - 1 - i, the state waves the one before
@@ -194,6 +198,7 @@ __global__ __launch_bounds__(64 * (2 * NW + 2)) void delta_chunk_rev(ChunkArgs c
         for (int q = 0; q < 4; ++q) z = fmaf(u[b][q], s[b][q], z);
     }
     z = wave_sum(z);
+    wait_vm<0>();  // dstate_in may be dstate_out
     float lw = 0.f;
     for (int i = 0; i <= nc + 1; ++i) {
       lds_barrier();  // A
@@ -265,6 +270,12 @@ __global__ __launch_bounds__(64 * (2 * NW + 2)) void delta_chunk_rev(ChunkArgs c
   f32x4 S[NB];
 #pragma unroll
   for (int b = 0; b < NB; ++b) S[b] = load_f32x4(first, state_off(r, index4(b, g), a.dk));
+  if (STATES && given && r < a.dv) {
+#pragma unroll
+    for (int b = 0; b < NB; ++b)
+      if (index4(b, g) < a.dk)
+        *reinterpret_cast<f32x4*>(seg_l + static_cast<int64_t>(r) * a.dk + index4(b, g)) = S[b];
+  }
   bf16x8 yf[12], ef[2];
   const int rt = tile * NW + wave, n_rt = delta_row_tiles(a.dv);
   const auto fetch = [&](int c) {

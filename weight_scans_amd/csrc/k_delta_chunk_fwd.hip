@@ -280,10 +280,14 @@ __global__ __launch_bounds__((kFwdThreads<NW, MODE>)) void delta_chunk_fwd(Chunk
   const int64_t so = (head * a.dv + r) * a.dk;
   // segment states [head][n_seg][dv][dk], M [head][n_seg][dk][dk]
   const auto seg_at = [&](int s) { return (head * ca.n_seg + s) * a.dv * a.dk; };
-  const float* from = ident      ? nullptr
-                      : seg == 0 ? (a.state_in ? static_cast<const float*>(a.state_in) + head * a.dv * a.dk : nullptr)
-                      : OUT      ? ca.seg_s + seg_at(seg)
-                                 : nullptr;
+  // A pass over the tokens in segments takes the call's first state from seg_s too,
+  // where the STATES pass leaves it: its first segment would read it while the last
+  // one writes the final state, which may be the same memory
+  const float* given = a.state_in ? static_cast<const float*>(a.state_in) + head * a.dv * a.dk : nullptr;
+  const float* from = ident                                  ? nullptr
+                      : seg == 0 && (!OUT || ca.n_seg == 1)  ? given
+                      : OUT && (seg > 0 || given != nullptr) ? ca.seg_s + seg_at(seg)
+                                                             : nullptr;
   const __amdgpu_buffer_rsrc_t first = state_rsrc(from, a.dv, a.dk);
   f32x4 S[NB];
 #pragma unroll
@@ -293,6 +297,12 @@ __global__ __launch_bounds__((kFwdThreads<NW, MODE>)) void delta_chunk_fwd(Chunk
     for (int b = 0; b < NB; ++b)
 #pragma unroll
       for (int q = 0; q < 4; ++q) S[b][q] = index4(b, g) + q == r ? 1.f : 0.f;
+  }
+  if (!OUT && seg == 0 && given && r < a.dv) {
+    float* keep = ca.seg_s + seg_at(0) + static_cast<int64_t>(r) * a.dk;
+#pragma unroll
+    for (int b = 0; b < NB; ++b)
+      if (index4(b, g) < a.dk) *reinterpret_cast<f32x4*>(keep + index4(b, g)) = S[b];
   }
   bf16x8 yf[12];
   const uint16_t* yp = ca.yf + rec0 * kYf + lane * 8;
