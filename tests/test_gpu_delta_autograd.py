@@ -120,3 +120,28 @@ def test_gates_of_other_orders_in_autograd(B):
     with torch.no_grad():
         again, _ = ws.delta_rule(g["q"], g["k"], g["v"], la, be.transpose(1, 2))
     assert rel(again, y) <= TOL[BF16]
+
+
+@pytest.mark.parametrize("dtype", [F64, F32, BF16])
+def test_key_heads_without_value_heads(dtype):
+    """No value head reads the keys: their gradients are zero, not left as they were."""
+    B, Hk, T, d = 2, 3, 70, 16
+    q = torch.ones((B, Hk, T, d), dtype=dtype, device="cuda")
+    none = torch.ones((B, 0, T, d), dtype=dtype, device="cuda")
+    gates = torch.ones((B, 0, T), dtype=dtype, device="cuda")
+    code = {F64: ws.GL_DTYPE_F64, F32: ws.GL_DTYPE_F32, BF16: ws.GL_DTYPE_BF16}[dtype]
+    desc = ws.make_delta_desc(B, T, 0, Hk, d, d, code, code)
+    wide = [torch.full((B, T, Hk, d + 8), 7.0, dtype=dtype, device="cuda") for _ in range(2)]
+    for n in ("sdq", "sdk"):
+        s = wide[0].stride()
+        setattr(desc, n, ws.delta.Strides(s[0], s[2], s[1]))
+    ptr = lambda t: ctypes.c_void_p(t.data_ptr())  # noqa: E731
+    args = [ptr(q), ptr(q)] + [None] * 8 + [ptr(w) for w in wide] + [None] * 4
+    status = ws.delta_lib().gl_delta_bwd(ctypes.byref(desc), *args, None, 0,
+                                         ctypes.c_void_p(torch.cuda.current_stream().cuda_stream))
+    torch.cuda.synchronize()
+    assert status == 0
+    for w in wide:
+        assert (w[..., :d] == 0).all() and (w[..., d:] == 7).all()
+    dq, dk = ws.gl_delta_bwd(q, q, none, gates, gates, none)[:2]
+    assert (dq == 0).all() and (dk == 0).all()

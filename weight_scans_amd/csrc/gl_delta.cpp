@@ -137,7 +137,7 @@ gl_status_t make_plan(const gl_delta_desc_t* d, Plan* p) {
   p->tok = d->B * d->T;
   const double n_all = std::max(1.0, double(p->N)) * std::max(1.0, double(d->T)) * std::max(1.0, double(d->H));
   if (double(p->N) * double(d->H) * 8 > 2147483647.0 || n_all * 128 * 128 * 8 > 4e18 ||
-      double(d->H) > 1e6)
+      double(std::max(d->H, d->Hk)) > 1e6)
     return fail(GL_ERROR_NOT_SUPPORTED, "sizes above the launch limits");
   p->io = d->io_dtype;
   p->comp = p->io == GL_DTYPE_F64 ? 8 : 4;
@@ -350,6 +350,12 @@ gl_status_t gl_delta_bwd(const gl_delta_desc_t* desc, const void* q, const void*
   Plan p;
   gl_status_t st = make_plan(desc, &p);
   if (st != GL_SUCCESS) return st;
+  if (desc->H == 0 && desc->Hk > 0 && p.tok > 0) {  // keys that no value head reads
+    if ((st = check_ptrs(true, {dq, dk}, p.elem)) != GL_SUCCESS) return st;
+    gls::DeltaArgs a = base_args(desc, p);
+    a.dq = dq; a.dk_ = dk;
+    return hip_status(gls::launch_delta_serial_bwd(p.io, a, static_cast<hipStream_t>(stream)), "delta backward launch");
+  }
   if (p.N * desc->H == 0) return GL_SUCCESS;
   if ((st = check_cu(p, cu_seqlens)) != GL_SUCCESS) return st;
   if (p.tok > 0 && (st = check_ptrs(true, {q, k, v, dy, dq, dk, dv}, p.align)) != GL_SUCCESS) return st;

@@ -350,8 +350,8 @@ __global__ __launch_bounds__(kThreads) void delta_serial_bwd(DeltaArgs a) {
 }
 
 // dq, dk (sums over the tiles and the value heads of a key head) and the gate
-// gradients (sums over the tiles), in a fixed order.  One token and key head
-// per work-group row.
+// gradients (sums over the tiles), in a fixed order; zeros where no value head
+// reads the keys.
 template <typename IO, typename S>
 __global__ __launch_bounds__(kThreads) void delta_serial_sum(DeltaArgs a) {
   const int tiles = (a.dv + kRows - 1) / kRows;
@@ -530,12 +530,14 @@ hipError_t fwd_io(const DeltaArgs& a, hipStream_t s) {
 template <typename IO, typename S>
 hipError_t bwd_io(const DeltaArgs& a, hipStream_t s) {
   const int64_t g = a.N * a.H * ((a.dv + kRows - 1) / kRows);
-  if (g == 0) return hipSuccess;
-  const dim3 grid(static_cast<unsigned>(g));
-  if (a.dk <= 64) delta_serial_bwd<IO, S, 4><<<grid, kThreads, 0, s>>>(a);
-  else delta_serial_bwd<IO, S, 8><<<grid, kThreads, 0, s>>>(a);
-  hipError_t e = hipGetLastError();
-  if (e != hipSuccess || a.B * a.T == 0) return e;
+  if (g > 0) {
+    const dim3 grid(static_cast<unsigned>(g));
+    if (a.dk <= 64) delta_serial_bwd<IO, S, 4><<<grid, kThreads, 0, s>>>(a);
+    else delta_serial_bwd<IO, S, 8><<<grid, kThreads, 0, s>>>(a);
+    const hipError_t e = hipGetLastError();
+    if (e != hipSuccess) return e;
+  }
+  if (a.B * a.T * a.Hk == 0) return hipSuccess;
   const int64_t work = 2 * a.B * a.T * std::max<int64_t>(static_cast<int64_t>(a.Hk) * a.dk, a.H);
   const int64_t blocks = std::min<int64_t>((work + kThreads - 1) / kThreads, 8192);
   delta_serial_sum<IO, S><<<dim3(static_cast<unsigned>(blocks)), kThreads, 0, s>>>(a);
