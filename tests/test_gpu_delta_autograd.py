@@ -145,3 +145,19 @@ def test_key_heads_without_value_heads(dtype):
         assert (w[..., :d] == 0).all() and (w[..., d:] == 7).all()
     dq, dk = ws.gl_delta_bwd(q, q, none, gates, gates, none)[:2]
     assert (dq == 0).all() and (dk == 0).all()
+
+
+def test_numbers_held_in_tensors():
+    """A scale that is a tensor is read at each call, not remembered by which tensor it is."""
+    _, p = leaves(6, F32)
+    p = {n: t.detach() for n, t in p.items()}
+    scale = torch.tensor(0.5)
+    for s in (0.5, 0.25, 2.0):
+        scale.fill_(s)
+        assert torch.equal(rule(p, scale=scale)[0], rule(p, scale=s)[0])
+        one = [p[n][:, :, 0] for n in NAMES[:5]]
+        assert torch.equal(ws.gl_delta_step(*one, p["state"].clone(), scale=scale),
+                           ws.gl_delta_step(*one, p["state"].clone(), scale=s))
+        for a, b in zip(ws.gl_qknorm_rope_fwd(p["q"], p["k"], q_scale=scale, k_scale=scale, eps=scale),
+                        ws.gl_qknorm_rope_fwd(p["q"], p["k"], q_scale=s, k_scale=s, eps=s)):
+            assert torch.equal(a, b)

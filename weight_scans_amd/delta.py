@@ -251,10 +251,18 @@ def _contiguous(shape, dtype):
     return tuple(shape), tuple(reversed(st)), dtype
 
 
+def _num(x):
+    """A scale or eps as the number it is now.  One that is a tensor would be remembered
+    by which tensor it is (calls of one kind are found by their numbers)."""
+    return x if x is None or type(x) is float else float(x)
+
+
 def gl_delta_fwd(q, k, v, log_alpha, beta, *, scale=None, state=None, want_state=False, save=False,
                  cu_seqlens=None, flags=0, segments=0):
     """Gated delta rule over whole sequences.  Returns (y, final state or None,
     saved or None).  scale: of y, 1/sqrt(dk) by default."""
+    scale = _num(scale)
+
     def plan():
         desc, n = _delta_desc(q, k, v, log_alpha, beta, scale, state, cu_seqlens, flags, segments)
         shape, strides = tuple(v.shape), _strides_like(v, v.shape)
@@ -274,6 +282,7 @@ def gl_delta_bwd(q, k, v, log_alpha, beta, dy, saved=None, *, scale=None, state=
     the last is None unless `state` was given or want_dstate is true."""
     if want_dstate is None:
         want_dstate = state is not None
+    scale = _num(scale)
 
     def plan():
         desc, n = _delta_desc(q, k, v, log_alpha, beta, scale, state, cu_seqlens, flags, segments)
@@ -311,6 +320,8 @@ def gl_delta_step(q, k, v, log_alpha, beta, state, *, scale=None, slots=None, y=
     """One token of each row: q, k [B,Hk,dk], v [B,H,dv], gates [B,H]; `state`
     [n,H,dv,dk] is updated in place, row b's at slots[b] (int32; outside
     0..n-1: nothing to do, y = 0), or at b.  Returns y [B,H,dv]."""
+    scale = _num(scale)
+
     def plan():
         torch = _torch()
         if q.dim() != 3 or k.shape != q.shape or v.dim() != 3 or v.shape[0] != q.shape[0] or state.dim() != 4:
@@ -379,6 +390,8 @@ def gl_qknorm_rope_fwd(q, k, wq=None, wk=None, cos=None, sin=None, *, pos=None, 
     [B,Hk,T,d], weights wq, wk [d], and the rotation by the tables cos, sin
     [n_pos, rot/2] at pos [B,T] (or pos0 + t).  Returns the two results, dense
     [B,H,T,d] (what gl_delta_fwd reads row after row)."""
+    eps, q_scale, k_scale = _num(eps), _num(q_scale), _num(k_scale)
+
     def plan():
         desc = _qk_desc(q, k, wq, wk, cos, sin, pos, pos0, eps, q_scale, k_scale, interleaved)
         return desc, 0, 0, (_contiguous(q.shape, q.dtype), _contiguous(k.shape, q.dtype))
@@ -391,6 +404,8 @@ def gl_qknorm_rope_bwd(q, k, wq, wk, cos, sin, dqn, dkn, *, pos=None, pos0=0, ep
     """Gradients of gl_qknorm_rope_fwd for upstream dqn, dkn: (dq, dk, dwq,
     dwk), dq and dk in their inputs' order of dimensions, dwq and dwk [d] in
     fp32 (fp64), None where there is no weight."""
+    eps, q_scale, k_scale = _num(eps), _num(q_scale), _num(k_scale)
+
     def plan():
         desc = _qk_desc(q, k, wq, wk, cos, sin, pos, pos0, eps, q_scale, k_scale, interleaved)
         if dqn.shape != q.shape or dkn.shape != k.shape or dqn.dtype != q.dtype or dkn.dtype != k.dtype:
@@ -496,11 +511,11 @@ def delta_rule(q, k, v, log_alpha, beta, *, scale=None, state=None, cu_seqlens=N
                             cu_seqlens=cu_seqlens)[:2]
     # slices that begin between two 16-byte units: training wants them aligned
     q, k, v = (_aligned(t) for t in (q, k, v))
-    return _functions()[0].apply(q, k, v, log_alpha, beta, state, scale, cu_seqlens, want_state)
+    return _functions()[0].apply(q, k, v, log_alpha, beta, state, _num(scale), cu_seqlens, want_state)
 
 
 def qknorm_rope(q, k, wq=None, wk=None, cos=None, sin=None, *, pos=None, pos0=0, eps=1e-6, q_scale=1.0,
                 k_scale=1.0, interleaved=False):
     """Autograd-aware gl_qknorm_rope_fwd."""
-    opts = dict(pos0=pos0, eps=eps, q_scale=q_scale, k_scale=k_scale, interleaved=interleaved)
+    opts = dict(pos0=int(pos0), eps=_num(eps), q_scale=_num(q_scale), k_scale=_num(k_scale), interleaved=interleaved)
     return _functions()[1].apply(q, k, wq, wk, cos, sin, pos, opts)
