@@ -161,3 +161,19 @@ def test_numbers_held_in_tensors():
         for a, b in zip(ws.gl_qknorm_rope_fwd(p["q"], p["k"], q_scale=scale, k_scale=scale, eps=scale),
                         ws.gl_qknorm_rope_fwd(p["q"], p["k"], q_scale=s, k_scale=s, eps=s)):
             assert torch.equal(a, b)
+
+
+def test_what_takes_no_gradient_is_refused():
+    """No gradient is formed for the scales and the tables: one that wants it is not left without."""
+    _, p = leaves(7, F32)
+    scale = torch.tensor(0.5, requires_grad=True)
+    table = torch.rand(100, 8, device="cuda", requires_grad=True)
+    with pytest.raises(TypeError):
+        rule(p, scale=scale)
+    with pytest.raises(TypeError):
+        ws.qknorm_rope(p["q"], p["k"], q_scale=scale)
+    for tables in ((table, table.detach()), (table.detach(), table)):
+        with pytest.raises(ValueError):
+            ws.qknorm_rope(p["q"], p["k"], None, None, *tables)
+        with torch.no_grad():
+            ws.qknorm_rope(p["q"], p["k"], None, None, *tables)

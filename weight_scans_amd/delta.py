@@ -498,10 +498,20 @@ def _no_duals(inputs):
         raise NotImplementedError("the delta rule has no forward-mode derivative")
 
 
+def _no_gradient(error, names, *values):
+    """Refuses what wants a gradient that the functions do not form."""
+    torch = _torch()
+    if torch.is_grad_enabled():
+        for x in values:
+            if torch.is_tensor(x) and x.requires_grad:
+                raise error(f"no gradient is formed for {names}: detach it")
+
+
 def delta_rule(q, k, v, log_alpha, beta, *, scale=None, state=None, cu_seqlens=None, want_state=False):
     """Autograd-aware gl_delta_fwd: (y, final state or None).  Nothing is kept
     for a backward where no gradient is wanted.  Gates of different strides are
     copied into one order, q, k, v that do not begin on 16 bytes in training."""
+    _no_gradient(TypeError, "scale", scale)
     if log_alpha.shape == beta.shape and _moves(log_alpha) != _moves(beta):  # one order for both
         log_alpha, beta = log_alpha.contiguous(), beta.contiguous()
     inputs = (q, k, v, log_alpha, beta, state)
@@ -517,5 +527,7 @@ def delta_rule(q, k, v, log_alpha, beta, *, scale=None, state=None, cu_seqlens=N
 def qknorm_rope(q, k, wq=None, wk=None, cos=None, sin=None, *, pos=None, pos0=0, eps=1e-6, q_scale=1.0,
                 k_scale=1.0, interleaved=False):
     """Autograd-aware gl_qknorm_rope_fwd."""
+    _no_gradient(TypeError, "the scales and eps", q_scale, k_scale, eps)
+    _no_gradient(ValueError, "cos and sin", cos, sin)
     opts = dict(pos0=int(pos0), eps=_num(eps), q_scale=_num(q_scale), k_scale=_num(k_scale), interleaved=interleaved)
     return _functions()[1].apply(q, k, wq, wk, cos, sin, pos, opts)
