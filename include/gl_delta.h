@@ -49,9 +49,9 @@
  * dtype, is a running sum where tokens keep more than 0.022 of the state: 1e-5 where
  * they keep nearly all, growing as 1 / alpha (uniform log_alpha -3, 4096 tokens:
  * 2e-3); a token that keeps less has the sum of what crosses it (1e-3, up to 5e-3 for
- * single heads).  y is rounded once, at the end (1.7e-3).  dq and dk
- * come from products of two bf16 operands of which one (states, e_t, dv / beta)
- * was rounded once: 3e-3; dv and dbeta 2.5e-3.
+ * single heads).  y and dv are rounded once, at the end (1.7e-3).  dq and
+ * dk come from products of two bf16 operands of which one (states, e_t, dv / beta)
+ * was rounded once: 3e-3; dbeta takes e_t rounded once: 2.5e-3.
  *
  * Kernels: BF16 io with dk and dv multiples of 8, and F32 io with multiples of
  * 4, run in chunks of 64 tokens on the matrix cores.  Everything else goes token
