@@ -131,3 +131,16 @@ def test_value_gradients_are_rounded_once(dk, dv, T, decay):
         got = ws.gl_delta_bwd(*args, g["dy"], saved, segments=segments)[2]
         for h in range(4):
             assert rel(got[0, h], want[0, h]) <= 2e-3, (segments, h)
+
+
+# ------------------------------------------------------------ lengths
+@pytest.mark.parametrize("lens", [[700] + [1] * 30, [1] * 30 + [700], [2, 900, 0] + [1] * 230, [65] + [3] * 200])
+@pytest.mark.parametrize("dtype,d", [(BF16, 64), (BF16, 128), (F32, 64)])
+def test_packed_of_very_unequal_lengths(lens, dtype, d):
+    for saved in (True, False):
+        run_case(len(lens), 1, 2, 1, sum(lens), d, d, dtype, lens=lens, order="bthd", saved=saved)
+
+
+@pytest.mark.parametrize("dk,dv,segments", [(64, 64, 1), (128, 128, 0)])
+def test_long_sequences(dk, dv, segments):
+    run_case(dk, 1, 2, 1, 4100, dk, dv, BF16, gate=F32, decay="near1", segments=segments)
