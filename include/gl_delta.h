@@ -45,18 +45,19 @@
  * states and every accumulator in fp32.  Its matrix-core path carries the
  * recurrences (states in both directions, e_t) through operands split into two
  * bf16 terms (16 significand bits): final states and the gradient of the first
- * hold about 3e-6 (relative 2-norm).  dlog_alpha, before it is rounded to the gate
+ * hold 3.5e-6 (relative 2-norm).  dlog_alpha, before it is rounded to the gate
  * dtype, is a running sum where tokens keep more than 0.022 of the state: 1e-5 where
  * they keep nearly all, growing as 1 / alpha (uniform log_alpha -3, 4096 tokens:
- * 2e-3); a token that keeps less has the sum of what crosses it (1e-3, up to 5e-3 for
+ * 2e-3); a token that keeps less has the sum of what crosses it (1e-3, up to 6e-3 for
  * single heads).  y and dv are rounded once, at the end (1.7e-3).  dq and
  * dk come from products of two bf16 operands of which one (states, e_t, dv / beta)
- * was rounded once: 3e-3; dbeta takes e_t rounded once: 2.5e-3.
+ * was rounded once: 3.1e-3; dbeta takes e_t rounded once: 2.5e-3.
  *
  * Kernels: BF16 io with dk and dv multiples of 8, and F32 io with multiples of
  * 4, run in chunks of 64 tokens on the matrix cores.  Everything else goes token
  * by token on the vector ALU, and so do sequences of fewer than 4 tokens on
- * average (fewer than 24 in a forward that saves nothing).
+ * average (fewer than 24 in a forward that saves nothing): a long sequence packed
+ * with very many short ones is faster in a call of its own.
  */
 #ifndef GL_DELTA_H
 #define GL_DELTA_H
@@ -115,7 +116,7 @@ gl_status_t gl_delta_bwd(const gl_delta_desc_t* desc, const void* q, const void*
  * [n_slots][H][dv][dk], updated in place.  Row b uses state slots[b] (device
  * int32; NULL = b, n_slots >= B); a slot outside 0..n_slots-1 marks a row with
  * nothing to do: its y is zero and no state changes.  No two rows may name one
- * slot.  desc->T is ignored (q, k are [B][Hk][dk], v, y [B][H][dv], gates
+ * slot.  desc->T is checked and not used (q, k are [B][Hk][dk], v, y [B][H][dv], gates
  * [B][H]; the t strides are not used), n_seq must be 0. */
 gl_status_t gl_delta_step(const gl_delta_desc_t* desc, const void* q, const void* k, const void* v,
                           const void* log_alpha, const void* beta, const int32_t* slots,

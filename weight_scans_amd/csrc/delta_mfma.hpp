@@ -47,8 +47,10 @@ __device__ __forceinline__ Pair8 split8(const f32x4& x, const f32x4& y) {
 }
 
 // ---- LDS tiles [64][W] bf16, W in {32, 64, 128}: 16-byte groups XORed with
-// swz<W>(row), which makes the 16-byte operand reads conflict-free; the
-// transposing reads (four 8-byte halves of neighbouring groups) are two-way.
+// swz<W>(row), which spreads the 16-byte operand reads over the banks, and the
+// transposing reads (four 8-byte halves of neighbouring groups) less evenly: with the
+// turned blocks the recurrences lose 0.9 to 2.0 cycles to bank conflicts per cycle of
+// LDS issue, and 1 or 2 per cent of their waves' time waiting for LDS.
 typedef __attribute__((address_space(3))) s16x4 lds_s16x4_t;
 __device__ __forceinline__ s16x4 tr4(const char* p) {
   return __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4_t*)(p));

@@ -8,12 +8,13 @@
 // is again a recurrence of independent rows (delta_chunk_rev, the mirror of the
 // forward kernel: state waves with Lam^T in their accumulators; helper waves
 // form the two products with dO one chunk ahead and hand them over in fp32).  As
-// there the chain of a chunk in one wave bounds it, 3.2 us a step at 128 x 128:
-// 4 x 16 x 4096 x 128 takes 205 us (794 MB, 3.9 TB/s), 8 x 16 x 4096 x 64 175 us (829
+// there the chain of a chunk in one wave bounds it, 3.4 us a step at 128 x 128:
+// 4 x 16 x 4096 x 128 takes 222 us (860 MB, 3.9 TB/s), 8 x 16 x 4096 x 64 190 us (898
 // MB, 4.7 TB/s: near what a copy reaches).  P^T is read, not formed here: the
-// helpers would outlast the state waves (252 and 207 us).  Segments as in the
+// helpers would outlast the state waves (before dv left here too: 205 and 175 us, so
+// 252 and 207).  Segments as in the
 // forward, from the right: Lam_begin = Lam_end M^T + Z, with M the forward's (1 x 16
-// x 32768 x 128: the whole backward 942 us in four, 1588 in one).
+// x 32768 x 128: the whole backward 952 us in four, 1588 in one).
 // The rest is one work-group per chunk and key head (delta_chunk_grad):
 //
 //   dq = scale e^l dO S + dP K,              dP_ij = scale D_ij beta_j dO_i.e_j  (j <= i)
@@ -500,8 +501,8 @@ __global__ __launch_bounds__(64 * (2 * NW + 2)) void delta_chunk_rev(ChunkArgs c
 // memory.  Loading a chunk's 160 KB (128 x 128) and multiplying take about as
 // long: dO, e and G are done with before K and Q are needed, which take their
 // place, so that two work-groups fit a CU and one loads while the other
-// multiplies.  Bound by HBM: 4 x 16 x 4096 x 128 moves 833 MB in 164 us, 8 x 16 x
-// 4096 x 64 709 MB in 141 us, 5.1 TB/s both, what a large copy reaches.  S, Lam, e
+// multiplies.  Bound by HBM: 4 x 16 x 4096 x 128 moves 766 MB in 154 us, 8 x 16 x
+// 4096 x 64 642 MB in 129 us, 5.0 TB/s both, what a large copy reaches.  S, Lam, e
 // and G were rounded once to bf16 by the recurrences (dq, dk: 3e-3 against 1.7e-3 of
 // their own rounding); as two terms each they would add half to that traffic.
 template <int DK, int DV>
@@ -792,7 +793,8 @@ delta_chunk_grad(ChunkArgs ca) {
 //   b_j = e^(l_C - l_j) beta_j k_j.(e Lam)_j,  c = e^l_C <S, Lam>
 // from the same rounded S, Lam, e and G: relative errors of some 3e-3 of a gradient
 // that the running sum would lose.  Products as in delta_chunk_grad.  Where no chunk
-// has such a token a launch that reads 256 bytes a head and chunk.
+// has such a token a launch that reads 256 bytes a head and chunk, 4.5 us; where every
+// one has, 235 us at 8 x 16 x 4096 x 64 and at 4 x 16 x 4096 x 128.
 template <int DV>
 struct DecayLds {
   alignas(16) char o[64 * DV * 2];

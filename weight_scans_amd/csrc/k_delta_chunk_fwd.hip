@@ -32,7 +32,7 @@
 // segment from S = 0 and M as its end from S = I without values, delta_join
 // forms the segments' first states one after another, and the pass over the
 // tokens then starts every segment from its own.  1 x 16 x 32768 x 128, four
-// segments: 204 us + 8 us + 263 us for the passes, 940 us in one.
+// segments: 198 us + 8 us + 252 us for the passes, 940 us in one.
 #include "delta_mfma.hpp"
 #include "dev_common.hpp"
 

@@ -391,7 +391,8 @@ __global__ __launch_bounds__(kThreads) void delta_serial_sum(DeltaArgs a) {
 // ---- one token: the state read and written once.  Bound by that traffic
 // (64 KB each way per head of 128 x 128); L lanes to a row (four columns
 // each), RU row sets in flight per wave.  256 rows of 16 heads of 128 x 128: 540 MB
-// in 97 us, 5.6 TB/s (a large copy: 5.2); one row: 4.5 us, a launch.
+// in 105 us with other states at each call, 5.1 TB/s (a large copy: 5.2), 93 on the
+// same ones again; one row: 4.5 us, a launch.
 template <int L>
 __device__ __forceinline__ float sum_l(float x) {
   x = sum16(x);
@@ -501,7 +502,8 @@ __global__ __launch_bounds__(kThreads) void delta_step(DeltaArgs a) {
 
 template <typename IO, typename S, int L, bool VEC>
 hipError_t step_ru(const DeltaArgs& a, hipStream_t s) {
-  // Two / four / eight row sets a wave at 16 heads of 128 x 128: 1 row 4.3 / 4.6 /
+  // Two / four / eight row sets a wave at 16 heads of 128 x 128, the same states at
+  // each call: 1 row 4.3 / 4.6 /
   // 5.2 us, 32 rows 14.5 / 12.5 / 12.6, 256 rows 97 / 97 / 100; of 64 x 64, 256
   // rows 26 / 24 / 27
   constexpr int RU = 4, RB = 64 / L * RU * (kThreads / 64);
