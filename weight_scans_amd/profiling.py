@@ -3,6 +3,7 @@
     python -m weight_scans_amd.profiling stats  <kernel_stats.csv>
     python -m weight_scans_amd.profiling traffic <fetch_dir> <write_dir> <config>
     python -m weight_scans_amd.profiling counters <pmc_dir> [<pmc_dir> ...]
+    python -m weight_scans_amd.profiling stale
 
 `stats` prints a markdown table from a rocprofv3 `--stats` kernel summary CSV
 (or a rocpd2summary kernels CSV).  `traffic` reads the counter CSVs of two
@@ -25,6 +26,8 @@ cores, the vector ALU and the LDS were used:
               conflicts per cycle of LDS issue)
   wait LDS / wait any  SQ_WAIT_INST_LDS and SQ_WAIT_ANY over SQ_WAVE_CYCLES
               (share of the waves' lifetime spent waiting)
+`stale` lists the summaries under profiles/ that are of other kernel sources than
+those here.
 """
 from __future__ import annotations
 
@@ -41,17 +44,43 @@ ROOT = os.path.dirname(HERE)
 CALIB_BYTES = 256 << 20  # the calibration kernel in bench.py: 256 MiB read + 256 MiB written
 
 
-def kernel_source_hash() -> str:
-    """Hash of every source the scans are built from (the kernels of the gated
-    delta rule and of the norms are no part of what bench.py runs)."""
+DELTA_SOURCES = ("delta", "gl_delta", "k_delta", "k_qknorm")
+
+
+def _source_hash(take) -> str:
     h = hashlib.sha256()
     for p in sorted(glob.glob(os.path.join(HERE, "csrc", "*"))):
-        if os.path.basename(p).startswith(("delta", "gl_delta", "k_delta", "k_qknorm")):
+        if not take(os.path.basename(p)):
             continue
         with open(p, "rb") as fh:
             h.update(os.path.basename(p).encode())
             h.update(fh.read())
     return h.hexdigest()[:16]
+
+
+def kernel_source_hash() -> str:
+    """Hash of every source the scans are built from (those of the gated delta rule
+    and of the norms, which only bench.py --delta runs, have one of their own)."""
+    return _source_hash(lambda name: not name.startswith(DELTA_SOURCES))
+
+
+def delta_source_hash() -> str:
+    """Hash of the sources of the gated delta rule and of the norms, with the
+    helpers that they share with the scans."""
+    return _source_hash(lambda name: name.startswith(DELTA_SOURCES)
+                        or name in ("dev_common.hpp", "internal.hpp", "mfma.hpp"))
+
+
+def stale_profiles() -> list[str]:
+    """The summaries under profiles/ that were taken of other kernel sources than
+    these, or that do not say of which."""
+    out = []
+    for p in sorted(glob.glob(os.path.join(ROOT, "profiles", "*.md"))):
+        name = os.path.basename(p)
+        want = delta_source_hash() if name.startswith("delta_") else kernel_source_hash()
+        if f"Kernel source hash: `{want}`" not in open(p).read():
+            out.append(name)
+    return out
 
 
 def short_name(kernel: str) -> str:
@@ -175,6 +204,10 @@ def traffic(fetch_dir: str, write_dir: str):
 
 
 def main(argv):
+    if argv == ["stale"]:
+        old = stale_profiles()
+        print("\n".join(old) if old else "every summary is of these sources")
+        return 1 if old else 0
     if len(argv) >= 2 and argv[0] == "stats":
         print(stats_table(argv[1]))
         return 0
