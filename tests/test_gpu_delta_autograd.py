@@ -177,3 +177,32 @@ def test_what_takes_no_gradient_is_refused():
             ws.qknorm_rope(p["q"], p["k"], None, None, *tables)
         with torch.no_grad():
             ws.qknorm_rope(p["q"], p["k"], None, None, *tables)
+
+
+@pytest.mark.parametrize("dtype,d", [(F64, 7), (F32, 7), (BF16, 64)])
+@pytest.mark.parametrize("T", [2, 70])
+def test_states_and_gates_that_are_broadcast_or_begin_anywhere(dtype, d, T):
+    """A first state shared by the batch, one out of a pool whose entries are no 16 bytes
+    long, gates that are one number for all: as their copies, gradients included."""
+    x, p = leaves(8, dtype, T, B=2, d=d)
+    p = {n: t.detach() for n, t in p.items()}
+    st = p["state"].dtype
+    first = p["state"][:1].clone().requires_grad_(True)
+    pool = torch.cat([torch.zeros(1, 2, d, d, dtype=st, device="cuda"), p["state"]]).flatten()
+    pool = torch.cat([torch.zeros(1, dtype=st, device="cuda"), pool]).requires_grad_(True)
+    gate = torch.tensor(-0.25, dtype=p["beta"].dtype, device="cuda", requires_grad=True)
+    wide = gate.expand(2, 2, T)
+    cases = [(first, first.expand(2, -1, -1, -1), p["log_alpha"], p["beta"]),
+             (pool, pool[1:].view(3, 2, d, d)[1:], p["log_alpha"], p["beta"]),
+             (gate, p["state"], wide, -wide), (gate, p["state"], wide, p["beta"])]
+    for leaf, state, log_alpha, beta in cases:
+        copies = [t.clone(memory_format=torch.contiguous_format) for t in (state, log_alpha, beta)]
+        both = []
+        for s, a, b in ((state, log_alpha, beta), copies):
+            with torch.no_grad():
+                quiet = ws.delta_rule(p["q"], p["k"], p["v"], a, b, state=s, want_state=True)
+            y, end = ws.delta_rule(p["q"], p["k"], p["v"], a, b, state=s, want_state=True)
+            g, = torch.autograd.grad([y, end], leaf, [p["dy"], p["dstate"]], retain_graph=True)
+            both.append([*quiet, y, end, g])
+        for a, b in zip(*both):
+            assert torch.equal(a, b)

@@ -510,10 +510,15 @@ def _no_gradient(error, names, *values):
 def delta_rule(q, k, v, log_alpha, beta, *, scale=None, state=None, cu_seqlens=None, want_state=False):
     """Autograd-aware gl_delta_fwd: (y, final state or None).  Nothing is kept
     for a backward where no gradient is wanted.  Gates of different strides are
-    copied into one order, q, k, v that do not begin on 16 bytes in training."""
+    copied into one order, a state that is broadcast or does not begin on 16 bytes
+    into one that is and does, and so are q, k, v that do not in training."""
     _no_gradient(TypeError, "scale", scale)
-    if log_alpha.shape == beta.shape and _moves(log_alpha) != _moves(beta):  # one order for both
-        log_alpha, beta = log_alpha.contiguous(), beta.contiguous()
+    if log_alpha.shape == beta.shape and (log_alpha.stride() != beta.stride() or 0 in beta.stride()):
+        order = _moves(log_alpha)
+        if order != _moves(beta) or not any(order):  # one order for both; one number for all written out
+            log_alpha, beta = log_alpha.contiguous(), beta.contiguous()
+    if state is not None:
+        state = _aligned(state.contiguous())
     inputs = (q, k, v, log_alpha, beta, state)
     _no_duals(inputs)
     if not (_torch().is_grad_enabled() and any(t is not None and t.requires_grad for t in inputs)):
