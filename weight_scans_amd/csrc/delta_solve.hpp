@@ -174,7 +174,7 @@ __device__ __forceinline__ float decay_sum(float x, float z, uint64_t forget, in
 
 // Work-groups of four waves look for the heads' chunks that have such tokens, 16
 // at a time with all loads in flight (a work-group to each of 8 x 16 x 4096 / 64 took
-// 9 us where there are none, this one 3), and take those in turn: work(record, its
+// 9 us where there are none, this takes 4), and take those in turn: work(record, its
 // tokens as bits).  A slot that holds no chunk may show any bits.
 template <typename F>
 __device__ __forceinline__ void for_strong(const ChunkArgs& ca, uint64_t (&found)[16], int w, int lane, F&& work) {

@@ -12,9 +12,10 @@
 // 4 x 16 x 4096 x 128 takes 222 us (860 MB, 3.9 TB/s), 8 x 16 x 4096 x 64 190 us (898
 // MB, 4.7 TB/s: near what a copy reaches).  P^T is read, not formed here: the
 // helpers would outlast the state waves (before dv left here too: 205 and 175 us, so
-// 252 and 207).  Segments as in the
-// forward, from the right: Lam_begin = Lam_end M^T + Z, with M the forward's (1 x 16
-// x 32768 x 128: the whole backward 952 us in four, 1588 in one).
+// 252 and 207).  Segments as in the forward, from the right: Lam_begin = Lam_end M^T +
+// Z, with M the forward's (1 x 16 x 32768 x 128: the whole backward 952 us in four,
+// 1588 in one).
+//
 // The rest is one work-group per chunk and key head (delta_chunk_grad):
 //
 //   dq = scale e^l dO S + dP K,              dP_ij = scale D_ij beta_j dO_i.e_j  (j <= i)
@@ -36,8 +37,8 @@
 // rounded states and e, as the sum of the flows past token t, has no long sum,
 // but the rounding of each flow left errors of up to 7e-3.  It is what tokens that keep
 // little of the state get, where the difference of the terms is lost in their own
-// rounding: delta_chunk_decay.)  dbeta = G.e is
-// formed there too, from the fp32 G.
+// rounding: delta_chunk_decay.)  dbeta = G.e is formed there too, from the fp32 G and
+// the rounded e.
 #include "delta_solve.hpp"
 #include "dev_common.hpp"
 

@@ -11,9 +11,10 @@
 // The recurrence is bound by the matrix rate of the waves that have a row tile's
 // chain, the gradients by the matrix cores and HBM: 4 x 8 x 1024 x 64 takes 56 us
 // and 32 us, 128 x 128 heads 78 us and 73 us, and 4 us to look for tokens that keep
-// little (token by token all together: 1058 and 1728 us).  With one wave to a row tile's chain the recurrence took 106 and
-// 150 us; where heads fill the card by themselves the two are level (256 heads of
-// 64: 439 us with the gradients, before 435).
+// little (token by token all together: 1058 and 1728 us).  With one wave to a row
+// tile's chain the recurrence took 106 and 150 us; where heads fill the card by
+// themselves the two are level (256 heads of 64: 439 us with the gradients, before
+// 435).
 #include <type_traits>
 
 #include "delta_f32.hpp"
