@@ -501,3 +501,9 @@ from .delta import (DELTA_EXPORTS, GL_FLAG_INTERLEAVED, DeltaDesc, QkDesc, delta
                     delta_path_name, delta_rule, delta_saved_size, delta_workspace_size, gl_delta_bwd,
                     gl_delta_fwd, gl_delta_step, gl_qknorm_rope_bwd, gl_qknorm_rope_fwd, make_delta_desc,
                     qknorm_rope)
+# The selective scan, the short causal convolution and the norms around a block
+# (include/gl_ssm.h).
+from .ssm import (GL_FLAG_GATE_FIRST, GL_FLAG_GROUP_WEIGHTS, GL_FLAG_SILU, GL_FLAG_SOFTPLUS,  # noqa: E402,F401
+                  SSM_EXPORTS, AddNormDesc, ConvDesc, GateNormDesc, Rows, SsmDesc, add_norm, causal_conv, gated_norm,
+                  gl_addnorm_bwd, gl_addnorm_fwd, gl_conv_bwd, gl_conv_fwd, gl_conv_step, gl_gatenorm_bwd,
+                  gl_gatenorm_fwd, gl_ssm_bwd, gl_ssm_fwd, gl_ssm_step, selective_scan, ssm_lib, ssm_workspace_size)

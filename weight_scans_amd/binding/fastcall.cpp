@@ -1,10 +1,10 @@
-// fastcall.cpp -- repeated calls of include/gl_delta.h from Python.
+// fastcall.cpp -- repeated calls of include/gl_delta.h and include/gl_ssm.h from Python.
 //
 // The checks of a call's tensors, its descriptor and the sizes of what it
 // returns depend on shapes, strides, types and devices only, and a decoding loop
 // makes thousands of calls that agree in all of them: in Python, looking that
 // up took longer (8 us of a one-token step) than the launch.  A `Calls` object
-// keeps the descriptors that delta.py has checked for one kind of call and its
+// keeps the descriptors that delta.py or ssm.py has checked for one kind of call and its
 // numbers (scale, flags, ...), compares the tensors at hand with what they were
 // recorded for, allocates the outputs and calls the library: one kind of call,
 // one place, no arithmetic.  Nothing is kept of the tensors but their shapes,
@@ -25,13 +25,15 @@
 #include <vector>
 
 #include "gl_delta.h"
+#include "gl_ssm.h"
 
 namespace {
 
-enum Kind { DELTA_FWD, DELTA_BWD, DELTA_STEP, QK_FWD, QK_BWD, KINDS };
-constexpr int kInputs[KINDS] = {7, 10, 8, 7, 9};
-constexpr int kOutputs[KINDS] = {3, 6, 1, 2, 4};
-constexpr int kMostInputs = 10, kMostOutputs = 6;
+enum Kind { DELTA_FWD, DELTA_BWD, DELTA_STEP, QK_FWD, QK_BWD,
+            CONV_FWD, CONV_BWD, CONV_STEP, SSM_FWD, SSM_BWD, SSM_STEP, ADD_FWD, ADD_BWD, GATE_FWD, GATE_BWD, KINDS };
+constexpr int kInputs[KINDS] = {7, 10, 8, 7, 9, 5, 7, 5, 10, 13, 10, 5, 7, 3, 4};
+constexpr int kOutputs[KINDS] = {3, 6, 1, 2, 4, 2, 4, 1, 3, 9, 1, 2, 5, 1, 3};
+constexpr int kMostInputs = 13, kMostOutputs = 9;
 constexpr size_t kMostRecords = 32;
 
 struct Shape {  // of an input, or of an output to be made
@@ -118,6 +120,42 @@ int launch(const Calls* c, const Record& r, int64_t pos0, void* const* in, void*
     case QK_FWD:  // q k wq wk cos sin pos | q k
       return reinterpret_cast<decltype(&gl_qknorm_rope_fwd)>(c->fn)(dq, in[0], in[1], in[2], in[3], in[4], in[5], i32(6),
                                                                     out[0], out[1], stream);
+    case CONV_FWD:  // x w bias state cu | y state
+      return reinterpret_cast<decltype(&gl_conv_fwd)>(c->fn)(static_cast<const gl_conv_desc_t*>(r.d), in[0], in[1], in[2],
+                                                             in[3], i32(4), out[0], out[1], stream);
+    case CONV_BWD:  // x w bias state cu dy dstate | dx dw dbias dstate
+      return reinterpret_cast<decltype(&gl_conv_bwd)>(c->fn)(static_cast<const gl_conv_desc_t*>(r.d), in[0], in[1], in[2],
+                                                             in[3], i32(4), in[5], in[6], out[0], out[1], out[2], out[3],
+                                                             ws, nb, stream);
+    case CONV_STEP:  // x w bias slots state | y
+      return reinterpret_cast<decltype(&gl_conv_step)>(c->fn)(static_cast<const gl_conv_desc_t*>(r.d), in[0], in[1],
+                                                              in[2], i32(3), r.count, in[4], out[0], stream);
+    case SSM_FWD:  // x dt A B C skip z dt_bias state cu | y state saved
+      return reinterpret_cast<decltype(&gl_ssm_fwd)>(c->fn)(static_cast<const gl_ssm_desc_t*>(r.d), in[0], in[1], in[2],
+                                                            in[3], in[4], in[5], in[6], in[7], in[8], i32(9), out[0],
+                                                            out[1], out[2], ws, nb, stream);
+    case SSM_BWD:  // x dt A B C skip z dt_bias state cu dy dstate saved | dx ddt dA dB dC dskip dz ddt_bias dstate
+      return reinterpret_cast<decltype(&gl_ssm_bwd)>(c->fn)(
+          static_cast<const gl_ssm_desc_t*>(r.d), in[0], in[1], in[2], in[3], in[4], in[5], in[6], in[7], in[8], i32(9),
+          in[10], in[11], in[12], out[0], out[1], out[2], out[3], out[4], out[5], out[6], out[7], out[8], ws, nb, stream);
+    case SSM_STEP:  // x dt A B C skip z dt_bias slots state | y
+      return reinterpret_cast<decltype(&gl_ssm_step)>(c->fn)(static_cast<const gl_ssm_desc_t*>(r.d), in[0], in[1], in[2],
+                                                             in[3], in[4], in[5], in[6], in[7], i32(8), r.count, in[9],
+                                                             out[0], stream);
+    case ADD_FWD:  // x r w wx scale | n r
+      return reinterpret_cast<decltype(&gl_addnorm_fwd)>(c->fn)(static_cast<const gl_addnorm_desc_t*>(r.d), in[0], in[1],
+                                                                in[2], in[3], in[4], out[0], out[1], stream);
+    case ADD_BWD:  // x r w wx scale dn dr | dx dr dw dwx dscale
+      return reinterpret_cast<decltype(&gl_addnorm_bwd)>(c->fn)(
+          static_cast<const gl_addnorm_desc_t*>(r.d), in[0], in[1], in[2], in[3], in[4], in[5], in[6], out[0], out[1],
+          out[2], out[3], out[4], ws, nb, stream);
+    case GATE_FWD:  // x z w | y
+      return reinterpret_cast<decltype(&gl_gatenorm_fwd)>(c->fn)(static_cast<const gl_gatenorm_desc_t*>(r.d), in[0],
+                                                                 in[1], in[2], out[0], stream);
+    case GATE_BWD:  // x z w dy | dx dz dw
+      return reinterpret_cast<decltype(&gl_gatenorm_bwd)>(c->fn)(static_cast<const gl_gatenorm_desc_t*>(r.d), in[0],
+                                                                 in[1], in[2], in[3], out[0], out[1], out[2], ws, nb,
+                                                                 stream);
     default:  // q k wq wk cos sin pos dqn dkn | dq dk dwq dwk
       return reinterpret_cast<decltype(&gl_qknorm_rope_bwd)>(c->fn)(dq, in[0], in[1], in[2], in[3], in[4], in[5], i32(6),
                                                                     in[7], in[8], out[0], out[1], out[2], out[3], ws, nb,
@@ -275,7 +313,7 @@ PyMethodDef methods[] = {
     {nullptr, nullptr, 0, nullptr}};
 
 PyTypeObject type = {PyVarObject_HEAD_INIT(nullptr, 0)};
-PyModuleDef module = {PyModuleDef_HEAD_INIT, "_fastcall", "Repeated calls of gl_delta.h.", -1, nullptr};
+PyModuleDef module = {PyModuleDef_HEAD_INIT, "_fastcall", "Repeated calls of gl_delta.h and gl_ssm.h.", -1, nullptr};
 
 }  // namespace
 

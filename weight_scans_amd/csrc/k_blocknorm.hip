@@ -1,0 +1,514 @@
+// k_blocknorm.hip -- the norms around a block: the residual norm (norm of what the
+// block gives, scale, sum with the residual, norm for the next block) and the
+// gated norm of every head's row, with their gradients (any io dtype, d <= 16384).
+//
+//   hat(v) = v r(v),  r(v) = 1 / sqrt(mean(v^2) + eps);  for the gradient g of hat(v):
+//   dv = r (g - hat mean(g hat))
+//
+// Bound by memory: each row is read and written once.  TPR threads share a row,
+// a thread with E elements of it in registers: vectors of 16 bytes, TPR of them
+// side by side (single elements where rows do not begin on 16 bytes).  Sums over
+// a row cross lanes by shuffles and, from 128 threads on, waves through LDS.  The
+// backward's work-groups walk rows with the sums for the weights in registers and
+// leave one part each.
+#include <algorithm>
+
+#include "ssm_dev.hpp"
+
+namespace gls {
+namespace {
+
+// A thread's E elements of a row of d: vectors (VEC) or single ones at a stride.
+template <typename S, int TPR, int E, bool VEC>
+struct Slice {
+  template <typename IO>
+  __device__ static __forceinline__ int col(int j, int e) {
+    if constexpr (VEC) return (e / Vec<IO>::n * TPR + j) * Vec<IO>::n + e % Vec<IO>::n;
+    else return e * TPR + j;
+  }
+  // Elements past the row are `fill`.  Q sets the order of columns (the io dtype,
+  // also for tensors of another type, so that elements of one register belong together).
+  template <typename Q, typename IO>
+  __device__ static __forceinline__ void ld(const IO* p, int j, int d, S (&v)[E], S fill = S(0)) {
+    if constexpr (VEC) {
+      constexpr int n = Vec<Q>::n, m = Vec<IO>::n;
+#pragma unroll
+      for (int e = 0; e < E; e += n) {
+        const int c = col<Q>(j, e);
+        if (c < d) {
+#pragma unroll
+          for (int k = 0; k < n; k += m) Vec<IO>::ld(p + c + k, v + e + k);
+        } else {
+#pragma unroll
+          for (int k = 0; k < n; ++k) v[e + k] = fill;
+        }
+      }
+    } else {
+#pragma unroll
+      for (int e = 0; e < E; ++e) {
+        const int c = e * TPR + j;
+        v[e] = c < d ? load_as<S>(p, c) : fill;
+      }
+    }
+  }
+  template <typename Q, typename IO>
+  __device__ static __forceinline__ void st(IO* p, int j, int d, const S (&v)[E]) {
+    if constexpr (VEC) {
+      constexpr int n = Vec<Q>::n, m = Vec<IO>::n;
+#pragma unroll
+      for (int e = 0; e < E; e += n) {
+        const int c = col<Q>(j, e);
+        if (c < d) {
+#pragma unroll
+          for (int k = 0; k < n; k += m) Vec<IO>::st(p + c + k, v + e + k);
+        }
+      }
+    } else {
+#pragma unroll
+      for (int e = 0; e < E; ++e)
+        if (e * TPR + j < d) store_from(p, e * TPR + j, v[e]);
+    }
+  }
+};
+
+// Sum over the TPR threads of a row; every thread of the work-group calls it the
+// same number of times.  `turn` alternates between two sets of places, so that one
+// barrier a sum is enough.
+template <typename S, int TPR, int THREADS, int M>
+__device__ __forceinline__ void row_sum(S (&x)[M], int& turn) {
+#pragma unroll
+  for (int i = 0; i < M; ++i)
+#pragma unroll
+    for (int m = (TPR < 64 ? TPR : 64) / 2; m >= 1; m >>= 1) x[i] += __shfl_xor(x[i], m, 64);
+  if constexpr (TPR > 64) {
+    constexpr int WV = TPR / 64;
+    __shared__ S at[2][THREADS / 64][M];
+    const int wave = threadIdx.x / 64, first = wave / WV * WV;
+    if ((threadIdx.x & 63) == 0)
+#pragma unroll
+      for (int i = 0; i < M; ++i) at[turn][wave][i] = x[i];
+    __syncthreads();
+#pragma unroll
+    for (int i = 0; i < M; ++i) {
+      x[i] = S(0);
+#pragma unroll
+      for (int w = 0; w < WV; ++w) x[i] += at[turn][first + w][i];
+    }
+    turn ^= 1;
+  }
+}
+
+template <typename IO>
+__device__ __forceinline__ const IO* row_in(const void* p, const Rows& s, int64_t b, int64_t t, int64_t g = 0) {
+  return static_cast<const IO*>(p) + b * s.b + t * s.t + g * s.g;
+}
+template <typename IO>
+__device__ __forceinline__ IO* row_out(void* p, const Rows& s, int64_t b, int64_t t, int64_t g = 0) {
+  return static_cast<IO*>(p) + b * s.b + t * s.t + g * s.g;
+}
+
+// ---------------------------------------------------------------- residual norm
+template <typename IO, typename RES, typename S, int TPR, int E, bool VEC, int THREADS>
+__global__ __launch_bounds__(THREADS) void addnorm_fwd(AddNormArgs a) {
+  using L = Slice<S, TPR, E, VEC>;
+  constexpr int R = THREADS / TPR;
+  const int j = threadIdx.x % TPR;
+  const int64_t rows = a.B * a.T;
+  const int64_t want = blockIdx.x * static_cast<int64_t>(R) + threadIdx.x / TPR;
+  const int64_t row = want < rows ? want : rows - 1;  // spare threads sum with the others
+  const int64_t b = row / a.T, t = row % a.T;
+  int turn = 0;
+  S x[E], r[E], c[E];
+  L::template ld<IO>(row_in<IO>(a.x, a.sx, b, t), j, a.d, x);
+  L::template ld<IO>(row_in<RES>(a.r, a.sr, b, t), j, a.d, r);
+  if (a.wx) {
+    S ss[1] = {S(0)};
+#pragma unroll
+    for (int e = 0; e < E; ++e) ss[0] = fma_(x[e], x[e], ss[0]);
+    row_sum<S, TPR, THREADS, 1>(ss, turn);
+    const S rx = S(1) / sqrt_(ss[0] / a.d + static_cast<S>(a.eps));
+    L::template ld<IO>(static_cast<const IO*>(a.wx), j, a.d, c);
+#pragma unroll
+    for (int e = 0; e < E; ++e) x[e] *= rx * c[e];
+  }
+  if (a.scale) {
+    L::template ld<IO>(static_cast<const IO*>(a.scale), j, a.d, c);
+#pragma unroll
+    for (int e = 0; e < E; ++e) x[e] *= c[e];
+  }
+  S ss[1] = {S(0)};
+#pragma unroll
+  for (int e = 0; e < E; ++e) {
+    r[e] += x[e];
+    ss[0] = fma_(r[e], r[e], ss[0]);
+  }
+  row_sum<S, TPR, THREADS, 1>(ss, turn);
+  if (want >= rows) return;
+  L::template st<IO>(row_out<RES>(a.r_out, a.sro, b, t), j, a.d, r);
+  const S rr = S(1) / sqrt_(ss[0] / a.d + static_cast<S>(a.eps));
+  L::template ld<IO>(static_cast<const IO*>(a.w), j, a.d, c);
+#pragma unroll
+  for (int e = 0; e < E; ++e) r[e] *= rr * c[e];
+  L::template st<IO>(row_out<IO>(a.n, a.sn, b, t), j, a.d, r);
+}
+
+// Sums of a work-group's rows for the weights: its R rows of threads meet in LDS.
+template <typename IO, typename S, int TPR, int E, bool VEC, int R>
+__device__ __forceinline__ void leave_part(S* part, int d, const S (&v)[E]) {
+  using L = Slice<S, TPR, E, VEC>;
+  const int j = threadIdx.x % TPR, q = threadIdx.x / TPR;
+  if constexpr (R == 1) {
+#pragma unroll
+    for (int e = 0; e < E; ++e) {
+      const int c = L::template col<IO>(j, e);
+      if (c < d) part[c] = v[e];
+    }
+  } else {
+    __shared__ S red[R][TPR * E];
+    __syncthreads();
+#pragma unroll
+    for (int e = 0; e < E; ++e) red[q][L::template col<IO>(j, e)] = v[e];
+    __syncthreads();
+    for (int c = threadIdx.x; c < d; c += TPR * R) {
+      S s = S(0);
+#pragma unroll
+      for (int i = 0; i < R; ++i) s += red[i][c];
+      part[c] = s;
+    }
+  }
+}
+
+template <typename IO, typename RES, typename S, int TPR, int E, bool VEC, int THREADS>
+__global__ __launch_bounds__(THREADS) void addnorm_bwd(AddNormArgs a) {
+  using L = Slice<S, TPR, E, VEC>;
+  constexpr int R = THREADS / TPR;
+  const int j = threadIdx.x % TPR;
+  const int64_t rows = a.B * a.T;
+  int turn = 0;
+  S w[E], wx[E], sc[E], dw[E], dwx[E], ds[E];
+  L::template ld<IO>(static_cast<const IO*>(a.w), j, a.d, w);
+#pragma unroll
+  for (int e = 0; e < E; ++e) {
+    wx[e] = sc[e] = S(1);
+    dw[e] = dwx[e] = ds[e] = S(0);
+  }
+  if (a.wx) L::template ld<IO>(static_cast<const IO*>(a.wx), j, a.d, wx);
+  if (a.scale) L::template ld<IO>(static_cast<const IO*>(a.scale), j, a.d, sc);
+  const S inv = S(1) / a.d, eps = static_cast<S>(a.eps);
+  for (int64_t base = blockIdx.x * static_cast<int64_t>(R); base < rows; base += gridDim.x * static_cast<int64_t>(R)) {
+    const int64_t want = base + threadIdx.x / TPR;
+    const bool in = want < rows;
+    const int64_t row = in ? want : rows - 1;
+    const int64_t b = row / a.T, t = row % a.T;
+    S x[E], r[E], g[E], go[E];
+    L::template ld<IO>(row_in<IO>(a.x, a.sx, b, t), j, a.d, x);
+    L::template ld<IO>(row_in<RES>(a.r, a.sr, b, t), j, a.d, r);
+    L::template ld<IO>(row_in<IO>(a.dn, a.sdn, b, t), j, a.d, g);
+    if (a.dro) {
+      L::template ld<IO>(row_in<RES>(a.dro, a.sdro, b, t), j, a.d, go);
+    } else {
+#pragma unroll
+      for (int e = 0; e < E; ++e) go[e] = S(0);
+    }
+    S rx = S(1);
+    if (a.wx) {
+      S ss[1] = {S(0)};
+#pragma unroll
+      for (int e = 0; e < E; ++e) ss[0] = fma_(x[e], x[e], ss[0]);
+      row_sum<S, TPR, THREADS, 1>(ss, turn);
+      rx = S(1) / sqrt_(ss[0] * inv + eps);
+    }
+    S two[2] = {S(0), S(0)};
+#pragma unroll
+    for (int e = 0; e < E; ++e) {
+      x[e] *= rx;  // hat(x), or x
+      r[e] = fma_(sc[e], wx[e] * x[e], r[e]);
+      two[0] = fma_(r[e], r[e], two[0]);
+      two[1] = fma_(w[e] * g[e], r[e], two[1]);
+    }
+    row_sum<S, TPR, THREADS, 2>(two, turn);
+    const S rr = S(1) / sqrt_(two[0] * inv + eps);
+    const S m = two[1] * rr * rr * inv;
+    S dot[1] = {S(0)};
+#pragma unroll
+    for (int e = 0; e < E; ++e) {
+      const S dr = fma_(rr, w[e] * g[e] - r[e] * m, go[e]);
+      if (in) {
+        dw[e] = fma_(g[e], r[e] * rr, dw[e]);
+        ds[e] = fma_(dr, wx[e] * x[e], ds[e]);
+        dwx[e] = fma_(dr * sc[e], x[e], dwx[e]);
+      }
+      r[e] = dr;
+      g[e] = dr * sc[e] * wx[e];
+      dot[0] = fma_(g[e], x[e], dot[0]);
+    }
+    if (in) L::template st<IO>(row_out<RES>(a.dr, a.sdr, b, t), j, a.d, r);
+    if (a.wx) {
+      row_sum<S, TPR, THREADS, 1>(dot, turn);
+#pragma unroll
+      for (int e = 0; e < E; ++e) g[e] = rx * (g[e] - x[e] * (dot[0] * inv));
+    }
+    if (in) L::template st<IO>(row_out<IO>(a.dx, a.sdx, b, t), j, a.d, g);
+  }
+  const int64_t plane = static_cast<int64_t>(gridDim.x) * a.d;
+  S* part = static_cast<S*>(a.part) + blockIdx.x * static_cast<int64_t>(a.d);
+  if (a.dw[0]) leave_part<IO, S, TPR, E, VEC, R>(part, a.d, dw);
+  if (a.dw[1]) leave_part<IO, S, TPR, E, VEC, R>(part + plane, a.d, dwx);
+  if (a.dw[2]) leave_part<IO, S, TPR, E, VEC, R>(part + 2 * plane, a.d, ds);
+}
+
+// ---------------------------------------------------------------- gated norm
+template <typename S>
+__device__ __forceinline__ S silu_(S z) { return z * sigmoid_(z); }
+
+template <typename IO, typename S, int TPR, int E, bool VEC, int THREADS>
+__global__ __launch_bounds__(THREADS) void gatenorm_fwd(GateNormArgs a) {
+  using L = Slice<S, TPR, E, VEC>;
+  constexpr int R = THREADS / TPR;
+  const int j = threadIdx.x % TPR;
+  const int64_t rows = a.B * a.T * a.G;
+  const int64_t want = blockIdx.x * static_cast<int64_t>(R) + threadIdx.x / TPR;
+  const int64_t row = want < rows ? want : rows - 1;
+  const int64_t gr = row % a.G, bt = row / a.G, b = bt / a.T, t = bt % a.T;
+  int turn = 0;
+  S x[E], z[E], w[E];
+  L::template ld<IO>(row_in<IO>(a.x, a.sx, b, t, gr), j, a.d, x);
+  if (a.z) {
+    L::template ld<IO>(row_in<IO>(a.z, a.sz, b, t, gr), j, a.d, z);
+#pragma unroll
+    for (int e = 0; e < E; ++e) z[e] = silu_(z[e]);
+  } else {
+#pragma unroll
+    for (int e = 0; e < E; ++e) z[e] = S(1);
+  }
+  S ss[1] = {S(0)};
+#pragma unroll
+  for (int e = 0; e < E; ++e) {
+    if (a.first) {
+      x[e] *= z[e];
+      z[e] = S(1);
+    }
+    ss[0] = fma_(x[e], x[e], ss[0]);
+  }
+  row_sum<S, TPR, THREADS, 1>(ss, turn);
+  if (want >= rows) return;
+  const S rr = S(1) / sqrt_(ss[0] / a.d + static_cast<S>(a.eps));
+  if (a.w) {
+    L::template ld<IO>(static_cast<const IO*>(a.w) + (a.group_w ? gr * a.d : 0), j, a.d, w);
+  } else {
+#pragma unroll
+    for (int e = 0; e < E; ++e) w[e] = S(1);
+  }
+#pragma unroll
+  for (int e = 0; e < E; ++e) x[e] *= rr * w[e] * z[e];
+  L::template st<IO>(row_out<IO>(a.y, a.sy, b, t, gr), j, a.d, x);
+}
+
+// Rows of the work-groups blockIdx.y: all rows, or (weights of each group) the
+// rows of that group.
+template <typename IO, typename S, int TPR, int E, bool VEC, int THREADS>
+__global__ __launch_bounds__(THREADS) void gatenorm_bwd(GateNormArgs a) {
+  using L = Slice<S, TPR, E, VEC>;
+  constexpr int R = THREADS / TPR;
+  const int j = threadIdx.x % TPR;
+  const int64_t rows = a.B * a.T * (a.group_w ? 1 : a.G);
+  int turn = 0;
+  S w[E], dw[E];
+#pragma unroll
+  for (int e = 0; e < E; ++e) {
+    w[e] = S(1);
+    dw[e] = S(0);
+  }
+  if (a.w) L::template ld<IO>(static_cast<const IO*>(a.w) + (a.group_w ? blockIdx.y * static_cast<int64_t>(a.d) : 0), j, a.d, w);
+  const S inv = S(1) / a.d, eps = static_cast<S>(a.eps);
+  for (int64_t base = blockIdx.x * static_cast<int64_t>(R); base < rows; base += gridDim.x * static_cast<int64_t>(R)) {
+    const int64_t want = base + threadIdx.x / TPR;
+    const bool in = want < rows;
+    const int64_t row = in ? want : rows - 1;
+    const int64_t gr = a.group_w ? blockIdx.y : row % a.G, bt = a.group_w ? row : row / a.G;
+    const int64_t b = bt / a.T, t = bt % a.T;
+    S x[E], z[E], g[E], gate[E], slope[E];
+    L::template ld<IO>(row_in<IO>(a.x, a.sx, b, t, gr), j, a.d, x);
+    L::template ld<IO>(row_in<IO>(a.dy, a.sdy, b, t, gr), j, a.d, g);
+    if (a.z) {
+      L::template ld<IO>(row_in<IO>(a.z, a.sz, b, t, gr), j, a.d, z);
+#pragma unroll
+      for (int e = 0; e < E; ++e) {
+        const S q = sigmoid_(z[e]);
+        gate[e] = z[e] * q;
+        slope[e] = q * (S(1) + z[e] * (S(1) - q));
+      }
+    } else {
+#pragma unroll
+      for (int e = 0; e < E; ++e) {
+        gate[e] = S(1);
+        slope[e] = S(0);
+      }
+    }
+    // v = what is normed, and dy as it reaches w hat(v)
+    S two[2] = {S(0), S(0)};
+#pragma unroll
+    for (int e = 0; e < E; ++e) {
+      const S v = a.first ? x[e] * gate[e] : x[e], u = a.first ? g[e] : g[e] * gate[e];
+      two[0] = fma_(v, v, two[0]);
+      two[1] = fma_(w[e] * u, v, two[1]);
+    }
+    row_sum<S, TPR, THREADS, 2>(two, turn);
+    const S rr = S(1) / sqrt_(two[0] * inv + eps);
+    const S m = two[1] * rr * rr * inv;
+#pragma unroll
+    for (int e = 0; e < E; ++e) {
+      const S v = a.first ? x[e] * gate[e] : x[e], u = a.first ? g[e] : g[e] * gate[e];
+      const S dv = rr * (w[e] * u - v * m);
+      if (in) dw[e] = fma_(u, v * rr, dw[e]);
+      z[e] = slope[e] * (a.first ? dv * x[e] : g[e] * w[e] * (x[e] * rr));
+      x[e] = a.first ? dv * gate[e] : dv;
+    }
+    if (!in) continue;
+    L::template st<IO>(row_out<IO>(a.dx, a.sdx, b, t, gr), j, a.d, x);
+    if (a.z) L::template st<IO>(row_out<IO>(a.dz, a.sdz, b, t, gr), j, a.d, z);
+  }
+  if (a.dw)
+    leave_part<IO, S, TPR, E, VEC, R>(
+        static_cast<S*>(a.part) + (blockIdx.x * static_cast<int64_t>(gridDim.y) + blockIdx.y) * a.d, a.d, dw);
+}
+
+bool addnorm_vec(int io, const AddNormArgs& a, bool bwd) {
+  // vectors are of the io dtype; a residual of twice its size takes two each
+  const int v = vec_of(io);
+  const int res = a.res_f32 ? IO_F32 : io;
+  bool ok = a.d % v == 0 && aligned16(a.x) && aligned16(io, a.sx) && aligned16(a.r) && aligned16(res, a.sr) &&
+            aligned16(a.w) && aligned16(a.wx) && aligned16(a.scale);
+  if (!bwd) return ok && aligned16(a.n) && aligned16(io, a.sn) && aligned16(a.r_out) && aligned16(res, a.sro);
+  return ok && aligned16(a.dn) && aligned16(io, a.sdn) && aligned16(a.dro) && aligned16(res, a.sdro) && aligned16(a.dx) &&
+         aligned16(io, a.sdx) && aligned16(a.dr) && aligned16(res, a.sdr);
+}
+bool gatenorm_vec(int io, const GateNormArgs& a, bool bwd) {
+  bool ok = a.d % vec_of(io) == 0 && aligned16(a.x) && aligned16(io, a.sx) && aligned16(a.z) && aligned16(io, a.sz) &&
+            aligned16(a.w);
+  if (!bwd) return ok && aligned16(a.y) && aligned16(io, a.sy);
+  return ok && aligned16(a.dy) && aligned16(io, a.sdy) && aligned16(a.dx) && aligned16(io, a.sdx) && aligned16(a.dz) &&
+         aligned16(io, a.sdz);
+}
+
+// Threads a row, with eight elements each: 16 to d = 128, 64 to 512, 256 to 2048,
+// 1024 to 8192, and with sixteen each to 16384.
+template <template <int, int, bool, int> class Do, typename... A>
+hipError_t by_width(int d, bool vec, A... args) {
+  if (vec) {
+    if (d <= 128) return Do<16, 8, true, 256>::go(args...);
+    if (d <= 512) return Do<64, 8, true, 256>::go(args...);
+    if (d <= 2048) return Do<256, 8, true, 256>::go(args...);
+    if (d <= 8192) return Do<1024, 8, true, 1024>::go(args...);
+    return Do<1024, 16, true, 1024>::go(args...);
+  }
+  if (d <= 128) return Do<16, 8, false, 256>::go(args...);
+  if (d <= 512) return Do<64, 8, false, 256>::go(args...);
+  if (d <= 2048) return Do<256, 8, false, 256>::go(args...);
+  if (d <= 8192) return Do<1024, 8, false, 1024>::go(args...);
+  return Do<1024, 16, false, 1024>::go(args...);
+}
+int rows_at_once(int d) { return d <= 128 ? 16 : d <= 512 ? 4 : 1; }
+
+constexpr int64_t kMaxParts = 1024;
+
+template <typename IO, typename RES, typename S>
+struct Add {
+  template <int TPR, int E, bool VEC, int TH>
+  struct Fwd {
+    static hipError_t go(const AddNormArgs& a, hipStream_t s) {
+      const int64_t g = (a.B * a.T + TH / TPR - 1) / (TH / TPR);
+      addnorm_fwd<IO, RES, S, TPR, E, VEC, TH><<<static_cast<unsigned>(g), TH, 0, s>>>(a);
+      return hipGetLastError();
+    }
+  };
+  template <int TPR, int E, bool VEC, int TH>
+  struct Bwd {
+    static hipError_t go(const AddNormArgs& a, hipStream_t s) {
+      addnorm_bwd<IO, RES, S, TPR, E, VEC, TH><<<static_cast<unsigned>(addnorm_parts(a)), TH, 0, s>>>(a);
+      return hipGetLastError();
+    }
+  };
+};
+template <typename IO, typename S>
+struct Gate {
+  template <int TPR, int E, bool VEC, int TH>
+  struct Fwd {
+    static hipError_t go(const GateNormArgs& a, hipStream_t s) {
+      const int64_t g = (a.B * a.T * a.G + TH / TPR - 1) / (TH / TPR);
+      gatenorm_fwd<IO, S, TPR, E, VEC, TH><<<static_cast<unsigned>(g), TH, 0, s>>>(a);
+      return hipGetLastError();
+    }
+  };
+  template <int TPR, int E, bool VEC, int TH>
+  struct Bwd {
+    static hipError_t go(const GateNormArgs& a, hipStream_t s) {
+      const dim3 g(static_cast<unsigned>(gatenorm_parts(a)), a.group_w ? a.G : 1);
+      gatenorm_bwd<IO, S, TPR, E, VEC, TH><<<g, TH, 0, s>>>(a);
+      return hipGetLastError();
+    }
+  };
+};
+
+template <typename IO, typename RES, typename S>
+hipError_t add_fwd(int io, const AddNormArgs& a, hipStream_t s) {
+  return by_width<Add<IO, RES, S>::template Fwd>(a.d, addnorm_vec(io, a, false), a, s);
+}
+template <typename IO, typename RES, typename S>
+hipError_t add_bwd(int io, const AddNormArgs& a, hipStream_t s) {
+  return by_width<Add<IO, RES, S>::template Bwd>(a.d, addnorm_vec(io, a, true), a, s);
+}
+
+}  // namespace
+
+int64_t addnorm_parts(const AddNormArgs& a) {
+  const int q = rows_at_once(a.d);
+  return std::max<int64_t>(1, std::min<int64_t>((a.B * a.T + q - 1) / q, kMaxParts));
+}
+int64_t gatenorm_parts(const GateNormArgs& a) {
+  const int q = rows_at_once(a.d);
+  const int64_t rows = a.B * a.T * (a.group_w ? 1 : a.G);
+  const int64_t most = a.group_w ? std::max<int64_t>(1, kMaxParts / std::max(1, a.G)) : kMaxParts;
+  return std::max<int64_t>(1, std::min<int64_t>((rows + q - 1) / q, most));
+}
+
+hipError_t launch_addnorm_fwd(int io, const AddNormArgs& a, hipStream_t s) {
+  if (io == IO_F64) return add_fwd<double, double, double>(io, a, s);
+  if (io == IO_F32) return add_fwd<float, float, float>(io, a, s);
+  if (a.res_f32) return add_fwd<bf16, float, float>(io, a, s);
+  return add_fwd<bf16, bf16, float>(io, a, s);
+}
+hipError_t launch_addnorm_bwd(int io, const AddNormArgs& a, hipStream_t s) {
+  const bool any = a.B * a.T > 0;
+  hipError_t e = hipSuccess;
+  if (any) {
+    if (io == IO_F64) e = add_bwd<double, double, double>(io, a, s);
+    else if (io == IO_F32) e = add_bwd<float, float, float>(io, a, s);
+    else if (a.res_f32) e = add_bwd<bf16, float, float>(io, a, s);
+    else e = add_bwd<bf16, bf16, float>(io, a, s);
+  }
+  if (e != hipSuccess) return e;
+  const SumOut out[3] = {{a.dw[0], 1}, {a.dw[1], 1}, {a.dw[2], 1}};
+  return launch_sum_rows(io, a.part, out, 3, any ? addnorm_parts(a) : 0, a.d, s);
+}
+hipError_t launch_gatenorm_fwd(int io, const GateNormArgs& a, hipStream_t s) {
+  const bool v = gatenorm_vec(io, a, false);
+  if (io == IO_F64) return by_width<Gate<double, double>::Fwd>(a.d, v, a, s);
+  if (io == IO_F32) return by_width<Gate<float, float>::Fwd>(a.d, v, a, s);
+  return by_width<Gate<bf16, float>::Fwd>(a.d, v, a, s);
+}
+hipError_t launch_gatenorm_bwd(int io, const GateNormArgs& a, hipStream_t s) {
+  const bool v = gatenorm_vec(io, a, true), any = a.B * a.T * a.G > 0;
+  hipError_t e = hipSuccess;
+  if (any) {
+    if (io == IO_F64) e = by_width<Gate<double, double>::Bwd>(a.d, v, a, s);
+    else if (io == IO_F32) e = by_width<Gate<float, float>::Bwd>(a.d, v, a, s);
+    else e = by_width<Gate<bf16, float>::Bwd>(a.d, v, a, s);
+  }
+  if (e != hipSuccess) return e;
+  const SumOut out[1] = {{a.dw, 1}};
+  return launch_sum_rows(io, a.part, out, 1, any ? gatenorm_parts(a) : 0,
+                         static_cast<int64_t>(a.d) * (a.group_w ? a.G : 1), s);
+}
+
+}  // namespace gls

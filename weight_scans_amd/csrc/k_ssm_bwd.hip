@@ -1,0 +1,382 @@
+// k_ssm_bwd.hip -- selective scan, backward.
+//
+// With s_t the gradient that reaches h_t from later tokens, dy already through the
+// gate, and q_t = e_t h_(t-1) (what token t keeps):
+//
+//   g_t = s_t + dy_t C_t,        s_(t-1) = e_t g_t
+//   dC_t = sum_d dy_t h_t        dB_t = sum_d D_t x_t g_t
+//   du_t = sum_n B_t g_t         dx_t = D_t du_t + skip dy_t
+//   dD_t = x_t du_t + sum_n A q_t g_t,      dA = sum_t D_t q_t g_t
+//
+// Tiles run backwards, each from the state that the forward kept before it: the
+// forward's two passes over a slot's tokens again, then the same two in reverse
+// (ssm_scan.hpp).  The sums over channels are formed within a work-group, lanes
+// halving the number of values with every exchange, and leave as one part per
+// work-group and token, [block][state group][token][NS], added by a second kernel in a
+// fixed order.
+#include <algorithm>
+
+#include "ssm_scan.hpp"
+
+namespace gls {
+namespace {
+
+// Sums of V values over CH neighbouring lanes: each exchange hands half of the
+// values that are left to the other half of the lanes.  On return v[k] of lane c is
+// the sum of value c V / CH + k (V < CH: lanes c .. c + CH / V - 1 hold the same).
+template <typename S, int CH, int V>
+__device__ __forceinline__ void sum_lanes(S (&v)[V], int c) {
+  int n = V;
+#pragma unroll
+  for (int m = CH / 2; m >= 1; m >>= 1) {
+    if (n > 1) {
+      n /= 2;
+      const bool up = c & m;
+#pragma unroll
+      for (int k = 0; k < V / 2; ++k)
+        if (k < n) {
+          const S keep = up ? v[k + n] : v[k], give = up ? v[k] : v[k + n];
+          v[k] = keep + __shfl_xor(give, m, 64);
+        }
+    } else {
+      v[0] += __shfl_xor(v[0], m, 64);
+    }
+  }
+}
+
+// Leaves sums of a slot's TT x NS values over the channels at part + token NS + j.
+template <typename L>
+__device__ __forceinline__ void leave_sums(typename L::S (&v)[L::TT * L::NS], int c, typename L::S* part, int64_t t0,
+                                           int64_t len) {
+  using S = typename L::S;
+  constexpr int CH = L::CH, V = L::TT * L::NS, NS = L::NS;
+  sum_lanes<S, CH, V>(v, c);
+  if constexpr (V >= CH) {
+    constexpr int k = V / CH;
+#pragma unroll
+    for (int i = 0; i < k; ++i) {
+      const int at = c * k + i;
+      if (t0 + at / NS < len) part[t0 * NS + at] = v[i];
+    }
+  } else {
+    constexpr int k = CH / V;
+    const int at = c / k;
+    if (c % k == 0 && t0 + at / NS < len) part[t0 * NS + at] = v[0];
+  }
+}
+
+// LDS besides the forward's: what the waves pass on of dA, and its sums.
+template <typename L>
+size_t bwd_lds(int N) {
+  return sizeof(typename L::S) * (2 * L::BC + 4 * static_cast<size_t>(L::npad(N)) * L::CH + 2 * L::W * L::CH * 2 * L::NS +
+                                  2 * L::W * L::CH * L::NS);
+}
+
+template <typename IO, typename L>
+__global__ __launch_bounds__(L::THREADS) void ssm_bwd(SsmArgs a) {
+  using S = typename L::S;
+  constexpr int CH = L::CH, TT = L::TT, NS = L::NS, NB = L::NB, W = L::W;
+  extern __shared__ __align__(16) char lds[];
+  const int np = L::npad(a.Ns);
+  S* const sB = reinterpret_cast<S*>(lds);
+  S* const sC = sB + L::BC;
+  S* const agg = sC + L::BC;                      // [2][W][CH][2 NS]
+  S* const red = agg + 2 * W * CH * 2 * NS;       // [2][W][CH][NS]
+  S* const sA = red + 2 * W * CH * NS;            // [np][CH]
+  S* const sdA = sA + np * CH;                    // [np][CH]
+  S* sl = sdA + np * CH;                          // [2][np][CH]
+  S* sl1 = sl + np * CH;
+  const int64_t blocks = static_cast<int64_t>(gridDim.x) / a.N;
+  const int64_t id = xcd_order(blockIdx.x, gridDim.x);
+  const SsmPlace p = ssm_place(a, CH, id);
+  const SeqRange r = seq_range(a.cu, p.n, a.T);
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  const int c = lane % CH, ts = lane / CH, slot = wave * L::TS + ts;
+  const bool in = c < p.nch;
+  const int d = p.d0 + (in ? c : 0);
+  for (int i = threadIdx.x; i < np * CH; i += L::THREADS) {
+    const int n = i / CH, ch = i % CH;
+    const bool there = n < a.Ns && ch < p.nch;
+    const int64_t o = static_cast<int64_t>(p.d0 + (there ? ch : 0)) * a.Ns + (there ? n : 0);
+    sA[i] = there ? static_cast<const S*>(a.A)[o] * static_cast<S>(kLog2e) : S(0);
+    sl[i] = there && a.dstate_out ? static_cast<const S*>(a.dstate_out)[p.n * a.D * a.Ns + o] : S(0);
+    sdA[i] = S(0);
+  }
+  const S skip = a.skip ? static_cast<const S*>(a.skip)[d] : S(0);
+  const S bias = a.bias ? static_cast<const S*>(a.bias)[d] : S(0);
+  const IO* px = static_cast<const IO*>(a.x) + r.b * a.sx.b + r.t0 * a.sx.t + d;
+  const IO* pd = static_cast<const IO*>(a.dt) + r.b * a.sdt.b + r.t0 * a.sdt.t + d;
+  const IO* pz = static_cast<const IO*>(a.z) + r.b * a.sz.b + r.t0 * a.sz.t + d;
+  const IO* pg = static_cast<const IO*>(a.dy) + r.b * a.sdy.b + r.t0 * a.sdy.t + d;
+  const int64_t ck0 = chunk_slot0(a.packed, p.n, r.t0, a.T, L::TILE);
+  // parts of the sums over channels: [2][blocks][state groups][B T][NS]
+  const int groups = (a.Ns + NS - 1) / NS;
+  const int64_t tok = a.B * a.T, plane = tok * NS;
+  S* const partB = static_cast<S*>(a.part_bc) + (id % blocks) * groups * plane + (r.b * a.T + r.t0) * NS;
+  S* const partC = partB + blocks * groups * plane;
+  S dskip = S(0), dbias = S(0);
+  int turn = 0, rturn = 0, pending = -1;
+  // dA of the state group before: its waves' sums into sdA, by one thread each
+  const auto settle = [&] {
+    if (pending >= 0 && threadIdx.x < CH * NS) {
+      S x = S(0);
+#pragma unroll
+      for (int w = 0; w < W; ++w) x += red[(rturn ^ 1) * W * CH * NS + w * CH * NS + threadIdx.x];
+      sdA[(pending + threadIdx.x % NS) * CH + threadIdx.x / NS] += x;
+    }
+  };
+  for (int64_t tile = r.len ? (r.len - 1) / L::TILE : -1; tile >= 0; --tile) {
+    const int64_t tile0 = tile * L::TILE, t0 = tile0 + slot * TT;
+    S D[TT], u[TT], g[TT], y[TT], du[TT], dD[TT], sum = S(0);
+#pragma unroll
+    for (int i = 0; i < TT; ++i) {
+      const int64_t t = t0 + i < r.len ? t0 + i : r.len - 1;
+      u[i] = load_as<S>(px, t * a.sx.t);
+      D[i] = load_as<S>(pd, t * a.sdt.t);
+      g[i] = load_as<S>(pg, t * a.sdy.t);
+      y[i] = S(0);
+      du[i] = S(0);
+      dD[i] = S(0);
+    }
+    if (a.z) {
+#pragma unroll
+      for (int i = 0; i < TT; ++i) {
+        const int64_t t = t0 + i < r.len ? t0 + i : r.len - 1;
+        const S z = load_as<S>(pz, t * a.sz.t);
+        g[i] *= z * sigmoid_(z);
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < TT; ++i) {
+      const bool there = in && t0 + i < r.len;
+      const S v = D[i] + bias;
+      D[i] = there ? (a.softplus ? softplus_(v) : v) : S(0);
+      u[i] = there ? u[i] : S(0);
+      g[i] = there ? g[i] : S(0);
+      dskip = fma_(g[i], u[i], dskip);
+      y[i] = skip * u[i];
+      u[i] *= D[i];
+      sum += D[i];
+    }
+    for (int n0 = 0; n0 < np; n0 += NB) {
+      __syncthreads();
+      ssm_load_bc<IO, L>(a, p, r, tile0, n0, sB, sC);
+      __syncthreads();
+      for (int n1 = 0; n1 < NB; n1 += NS) {
+        const int n = n0 + n1;
+        if (n >= a.Ns) break;
+        const S* bp = sB + L::at(slot * TT, n1);
+        const S* cp = sC + L::at(slot * TT, n1);
+        S A[NS], P[NS], Pb[NS], h[NS], s[NS], enter[NS], e[TT][NS], q[TT][NS], v[TT * NS];
+        const S* kept = static_cast<const S*>(a.ckpt) + ((ck0 + tile) * a.Ns + n) * a.D + d;
+#pragma unroll
+        for (int j = 0; j < NS; ++j) {
+          A[j] = sA[(n + j) * CH + c];
+          enter[j] = n + j < a.Ns ? kept[static_cast<int64_t>(j) * a.D] : S(0);
+          P[j] = Pb[j] = exp2_(A[j] * sum);
+          h[j] = S(0);
+        }
+#pragma unroll
+        for (int i = 0; i < TT; ++i) {
+          S B[NS];
+          lds_get<S, NS>(bp + i * NB, B);
+#pragma unroll
+          for (int j = 0; j < NS; ++j) {
+            e[i][j] = exp2_(D[i] * A[j]);
+            h[j] = fma_(e[i][j], h[j], u[i] * B[j]);
+          }
+        }
+        ssm_scan<L, false>(P, h, enter, agg, turn);
+        settle();
+#pragma unroll
+        for (int i = 0; i < TT; ++i) {
+          S B[NS], C[NS];
+          lds_get<S, NS>(bp + i * NB, B);
+          lds_get<S, NS>(cp + i * NB, C);
+#pragma unroll
+          for (int j = 0; j < NS; ++j) {
+            q[i][j] = e[i][j] * h[j];
+            h[j] = fma_(u[i], B[j], q[i][j]);
+            y[i] = fma_(C[j], h[j], y[i]);
+            v[i * NS + j] = g[i] * h[j];
+          }
+        }
+        leave_sums<L>(v, c, partC + (n / NS) * plane, t0, r.len);
+#pragma unroll
+        for (int j = 0; j < NS; ++j) {
+          s[j] = S(0);
+          enter[j] = sl[(n + j) * CH + c];
+        }
+#pragma unroll
+        for (int i = TT - 1; i >= 0; --i) {
+          S C[NS];
+          lds_get<S, NS>(cp + i * NB, C);
+#pragma unroll
+          for (int j = 0; j < NS; ++j) s[j] = e[i][j] * fma_(C[j], g[i], s[j]);
+        }
+        ssm_scan<L, true>(Pb, s, enter, agg, turn);
+        S dA[NS];
+#pragma unroll
+        for (int j = 0; j < NS; ++j) dA[j] = S(0);
+#pragma unroll
+        for (int i = TT - 1; i >= 0; --i) {
+          S B[NS], C[NS];
+          lds_get<S, NS>(bp + i * NB, B);
+          lds_get<S, NS>(cp + i * NB, C);
+#pragma unroll
+          for (int j = 0; j < NS; ++j) {
+            const S gt = fma_(C[j], g[i], s[j]), gq = gt * q[i][j];
+            du[i] = fma_(gt, B[j], du[i]);
+            dD[i] = fma_(gq, A[j], dD[i]);
+            dA[j] = fma_(gq, D[i], dA[j]);
+            v[i * NS + j] = gt * u[i];
+            s[j] = e[i][j] * gt;
+          }
+        }
+        if (slot == 0) {
+#pragma unroll
+          for (int j = 0; j < NS; ++j) sl1[(n + j) * CH + c] = s[j];
+        }
+        leave_sums<L>(v, c, partB + (n / NS) * plane, t0, r.len);
+#pragma unroll
+        for (int j = 0; j < NS; ++j) {
+#pragma unroll
+          for (int m = CH; m < 64; m <<= 1) dA[j] += __shfl_xor(dA[j], m, 64);
+          if (ts == 0) red[rturn * W * CH * NS + wave * CH * NS + c * NS + j] = dA[j];
+        }
+        rturn ^= 1;
+        pending = n;
+      }
+    }
+    S* const other = sl;
+    sl = sl1;
+    sl1 = other;
+    if (in) {
+#pragma unroll
+      for (int i = 0; i < TT; ++i)
+        if (t0 + i < r.len) {
+          const int64_t t = t0 + i;
+          const S x = load_as<S>(px, t * a.sx.t);
+          S dd = fma_(dD[i], static_cast<S>(1.0 / kLog2e), x * du[i]);
+          if (a.softplus) dd *= sigmoid_(load_as<S>(pd, t * a.sdt.t) + bias);
+          dbias += dd;
+          store_from(static_cast<IO*>(a.ddt) + r.b * a.sddt.b + (r.t0 + t) * a.sddt.t, d, dd);
+          store_from(static_cast<IO*>(a.dx) + r.b * a.sdx.b + (r.t0 + t) * a.sdx.t, d, fma_(D[i], du[i], skip * g[i]));
+          if (a.z) {
+            const S z = load_as<S>(pz, t * a.sz.t), k = sigmoid_(z);
+            store_from(static_cast<IO*>(a.dz) + r.b * a.sdz.b + (r.t0 + t) * a.sdz.t, d,
+                       load_as<S>(pg, t * a.sdy.t) * y[i] * (k * (S(1) + z * (S(1) - k))));
+          }
+        }
+    }
+  }
+  __syncthreads();
+  settle();
+  // sums over the slots
+  sB[threadIdx.x] = dskip;
+  sB[L::THREADS + threadIdx.x] = dbias;
+  static_assert(L::BC >= 2 * L::THREADS, "room for the slots' sums");
+  __syncthreads();
+  S* const par = static_cast<S*>(a.part_par) + p.n * (a.Ns + 2) * a.D;
+  for (int i = threadIdx.x; i < np * CH; i += L::THREADS) {
+    const int n = i / CH, ch = i % CH;
+    if (n < a.Ns && ch < p.nch) par[static_cast<int64_t>(n) * a.D + p.d0 + ch] = sdA[i];
+  }
+  for (int i = threadIdx.x; i < 2 * CH; i += L::THREADS) {
+    const int which = i / CH, ch = i % CH;
+    S x = S(0);
+    for (int k = 0; k < L::SL; ++k) x += sB[which * L::THREADS + k * CH + ch];
+    if (ch < p.nch) par[static_cast<int64_t>(a.Ns + which) * a.D + p.d0 + ch] = x;
+  }
+  if (!a.dstate_in) return;
+  for (int i = threadIdx.x; i < np * CH; i += L::THREADS) {
+    const int n = i % np, ch = i / np;
+    if (n < a.Ns && ch < p.nch)
+      static_cast<S*>(a.dstate_in)[(p.n * a.D + p.d0 + ch) * a.Ns + n] = sl[n * CH + ch];
+  }
+}
+
+// dB and dC from the parts of the channel blocks, dA, dskip and dbias from those
+// of the sequences.
+constexpr int kSumThreads = 256;
+template <typename IO, typename S, int NS>
+__global__ __launch_bounds__(kSumThreads) void ssm_bwd_sums(SsmArgs a, int nb, int64_t bc_groups) {
+  const int groups = (a.Ns + NS - 1) / NS;
+  const int64_t tok = a.B * a.T;
+  if (blockIdx.x < bc_groups) {
+    const int64_t per = groups * tok * NS;  // of one group of channels, of B or of C
+    const int64_t i = blockIdx.x * static_cast<int64_t>(kSumThreads) + threadIdx.x;
+    if (i >= 2 * a.G * per) return;
+    const int64_t which = i / (a.G * per), g = i / per % a.G, o = i % per;
+    const int j = static_cast<int>(o % NS);
+    const int64_t t = o / NS % tok, n = o / (NS * tok) * NS + j;
+    if (n >= a.Ns) return;
+    const S* part = static_cast<const S*>(a.part_bc) + (which * a.G + g) * nb * per + o;
+    S x = S(0);
+    int k = 0;
+    for (; k + 8 <= nb; k += 8) {
+      S v[8];
+#pragma unroll
+      for (int m = 0; m < 8; ++m) v[m] = part[(k + m) * per];
+#pragma unroll
+      for (int m = 0; m < 8; ++m) x += v[m];
+    }
+    for (; k < nb; ++k) x += part[k * per];
+    const Rows& st = which ? a.sdC : a.sdB;
+    IO* out = static_cast<IO*>(which ? a.dC : a.dB) + t / a.T * st.b + t % a.T * st.t + g * st.g;
+    store_from(out, n, x);
+    return;
+  }
+  const int64_t i = (blockIdx.x - bc_groups) * kSumThreads + threadIdx.x;
+  if (i >= static_cast<int64_t>(a.Ns + 2) * a.D) return;
+  const int n = static_cast<int>(i / a.D), d = static_cast<int>(i % a.D);
+  S* out = static_cast<S*>(n < a.Ns ? a.dA : n == a.Ns ? a.dskip : a.dbias);
+  if (!out) return;
+  const S* part = static_cast<const S*>(a.part_par) + i;
+  const int64_t step = static_cast<int64_t>(a.Ns + 2) * a.D;
+  S x = S(0);
+#pragma unroll 4
+  for (int64_t k = 0; k < a.N; ++k) x += part[k * step];
+  out[n < a.Ns ? static_cast<int64_t>(d) * a.Ns + n : d] = x;
+}
+
+constexpr int kNS = 2;
+
+template <typename IO, typename L>
+hipError_t go(const SsmArgs& a, hipStream_t s) {
+  const int64_t blocks = ssm_blocks(a, L::CH);
+  if (a.N * blocks > 0) {
+    ssm_bwd<IO, L><<<static_cast<unsigned>(a.N * blocks), L::THREADS, bwd_lds<L>(a.Ns), s>>>(a);
+    const hipError_t e = hipGetLastError();
+    if (e != hipSuccess) return e;
+  }
+  const int64_t bc = 2 * a.G * ((a.Ns + kNS - 1) / kNS) * a.B * a.T * kNS, par = static_cast<int64_t>(a.Ns + 2) * a.D;
+  const int64_t g1 = (bc + kSumThreads - 1) / kSumThreads, g2 = (par + kSumThreads - 1) / kSumThreads;
+  if (g1 + g2 == 0) return hipSuccess;
+  ssm_bwd_sums<IO, typename L::S, kNS>
+      <<<static_cast<unsigned>(g1 + g2), kSumThreads, 0, s>>>(a, static_cast<int>(a.G ? blocks / a.G : 0), g1);
+  return hipGetLastError();
+}
+
+template <typename IO, typename S, int TT>
+hipError_t by_states(const SsmArgs& a, hipStream_t s) {
+  switch (ssm_bwd_channels(a.Ns)) {
+    case 32: return go<IO, SsmTile<S, 32, 8, TT, kNS, 16>>(a, s);
+    case 16: return go<IO, SsmTile<S, 16, 8, TT, kNS, 8>>(a, s);
+    default: return go<IO, SsmTile<S, 8, 8, TT, kNS, 8>>(a, s);
+  }
+}
+
+}  // namespace
+
+size_t ssm_bc_bytes(int io, const SsmArgs& a) {
+  const int64_t blocks = ssm_blocks(a, ssm_bwd_channels(a.Ns));
+  return static_cast<size_t>(2 * blocks) * ((a.Ns + kNS - 1) / kNS * kNS) * a.B * a.T * (io == IO_F64 ? 8 : 4);
+}
+hipError_t launch_ssm_bwd(int io, const SsmArgs& a, hipStream_t s) {
+  if (io == IO_F64) return by_states<double, double, 8>(a, s);
+  if (io == IO_F32) return by_states<float, float, 16>(a, s);
+  return by_states<bf16, float, 16>(a, s);
+}
+
+}  // namespace gls

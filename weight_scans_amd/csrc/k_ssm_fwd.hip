@@ -1,0 +1,169 @@
+// k_ssm_fwd.hip -- selective scan, forward (training and prefill).
+//
+//   D = softplus(dt + bias),  h = e h + (D x) B,  e = exp(D A),  y = (C h + skip x) silu(z)
+//
+// The decays differ per channel and state, so nothing of this is a matrix product:
+// per token, channel and state it is a product and an exponential (four cycles of
+// the vector ALU to a product's one) for e, and two products and two sums of products.
+// How the lanes cut the work: ssm_scan.hpp.  A slot keeps its decays in registers
+// between the two passes over its tokens: from zero, for its effect, and from what
+// enters it, for y.
+#include <algorithm>
+
+#include "ssm_scan.hpp"
+
+namespace gls {
+namespace {
+
+template <typename IO, typename L>
+__global__ __launch_bounds__(L::THREADS) void ssm_fwd(SsmArgs a, int ck) {
+  using S = typename L::S;
+  constexpr int CH = L::CH, TT = L::TT, NS = L::NS, NB = L::NB;
+  extern __shared__ __align__(16) char lds[];
+  const int np = L::npad(a.Ns);
+  S* const sB = reinterpret_cast<S*>(lds);
+  S* const sC = sB + L::BC;
+  S* const agg = sC + L::BC;                     // [2][W][CH][2 NS]
+  S* const sA = agg + 2 * L::W * CH * 2 * NS;    // [np][CH]
+  S* sh = sA + np * CH;                          // [2][np][CH]
+  const SsmPlace p = ssm_place(a, CH, xcd_order(blockIdx.x, gridDim.x));
+  const SeqRange r = seq_range(a.cu, p.n, a.T);
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  const int c = lane % CH, slot = wave * L::TS + lane / CH;
+  const bool in = c < p.nch;
+  const int d = p.d0 + (in ? c : 0);
+  for (int i = threadIdx.x; i < np * CH; i += L::THREADS) {
+    const int n = i / CH, ch = i % CH;
+    const bool there = n < a.Ns && ch < p.nch;
+    const int64_t o = static_cast<int64_t>(p.d0 + (there ? ch : 0)) * a.Ns + (there ? n : 0);
+    sA[i] = there ? static_cast<const S*>(a.A)[o] * static_cast<S>(kLog2e) : S(0);
+    sh[i] = there && a.state_in ? static_cast<const S*>(a.state_in)[p.n * a.D * a.Ns + o] : S(0);
+  }
+  const S skip = a.skip ? static_cast<const S*>(a.skip)[d] : S(0);
+  const S bias = a.bias ? static_cast<const S*>(a.bias)[d] : S(0);
+  const IO* px = static_cast<const IO*>(a.x) + r.b * a.sx.b + r.t0 * a.sx.t + d;
+  const IO* pd = static_cast<const IO*>(a.dt) + r.b * a.sdt.b + r.t0 * a.sdt.t + d;
+  const IO* pz = static_cast<const IO*>(a.z) + r.b * a.sz.b + r.t0 * a.sz.t + d;
+  IO* py = static_cast<IO*>(a.y) + r.b * a.sy.b + r.t0 * a.sy.t + d;
+  const int64_t ck0 = chunk_slot0(a.packed, p.n, r.t0, a.T, ck);
+  int turn = 0;
+  S* sh1 = sh + np * CH;
+  for (int64_t tile0 = 0; tile0 < r.len; tile0 += L::TILE) {
+    const int64_t t0 = tile0 + slot * TT;
+    S D[TT], u[TT], y[TT], sum = S(0);
+#pragma unroll
+    for (int i = 0; i < TT; ++i) {
+      const int64_t t = t0 + i < r.len ? t0 + i : r.len - 1;
+      u[i] = load_as<S>(px, t * a.sx.t);
+      D[i] = load_as<S>(pd, t * a.sdt.t);
+    }
+#pragma unroll
+    for (int i = 0; i < TT; ++i) {
+      const S v = D[i] + bias;
+      D[i] = t0 + i < r.len ? (a.softplus ? softplus_(v) : v) : S(0);
+      u[i] = t0 + i < r.len ? u[i] : S(0);
+      y[i] = skip * u[i];
+      u[i] *= D[i];
+      sum += D[i];
+    }
+    for (int n0 = 0; n0 < np; n0 += NB) {
+      __syncthreads();
+      ssm_load_bc<IO, L>(a, p, r, tile0, n0, sB, sC);
+      __syncthreads();
+      for (int n1 = 0; n1 < NB; n1 += NS) {
+        if (n0 + n1 >= a.Ns) break;
+        const S* bp = sB + L::at(slot * TT, n1);
+        const S* cp = sC + L::at(slot * TT, n1);
+        S A[NS], P[NS], h[NS], h0[NS], e[TT][NS];
+#pragma unroll
+        for (int j = 0; j < NS; ++j) {
+          A[j] = sA[(n0 + n1 + j) * CH + c];
+          P[j] = exp2_(A[j] * sum);
+          h[j] = S(0);
+          h0[j] = sh[(n0 + n1 + j) * CH + c];
+        }
+#pragma unroll
+        for (int i = 0; i < TT; ++i) {
+          S B[NS];
+          lds_get<S, NS>(bp + i * NB, B);
+#pragma unroll
+          for (int j = 0; j < NS; ++j) {
+            e[i][j] = exp2_(D[i] * A[j]);
+            h[j] = fma_(e[i][j], h[j], u[i] * B[j]);
+          }
+        }
+        ssm_scan<L, false>(P, h, h0, agg, turn);
+        if (a.ckpt && in && t0 < r.len && t0 % ck == 0) {
+          S* o = static_cast<S*>(a.ckpt) + ((ck0 + t0 / ck) * a.Ns + n0 + n1) * a.D + d;
+#pragma unroll
+          for (int j = 0; j < NS; ++j)
+            if (n0 + n1 + j < a.Ns) o[static_cast<int64_t>(j) * a.D] = h[j];
+        }
+#pragma unroll
+        for (int i = 0; i < TT; ++i) {
+          S B[NS], C[NS];
+          lds_get<S, NS>(bp + i * NB, B);
+          lds_get<S, NS>(cp + i * NB, C);
+#pragma unroll
+          for (int j = 0; j < NS; ++j) {
+            h[j] = fma_(e[i][j], h[j], u[i] * B[j]);
+            y[i] = fma_(C[j], h[j], y[i]);
+          }
+        }
+        if (slot == L::SL - 1) {
+#pragma unroll
+          for (int j = 0; j < NS; ++j) sh1[(n0 + n1 + j) * CH + c] = h[j];
+        }
+      }
+    }
+    S* const other = sh;
+    sh = sh1;
+    sh1 = other;
+    if (a.y && in) {
+#pragma unroll
+      for (int i = 0; i < TT; ++i)
+        if (t0 + i < r.len) {
+          if (a.z) {
+            const S z = load_as<S>(pz, (t0 + i) * a.sz.t);
+            y[i] *= z * sigmoid_(z);
+          }
+          store_from(py, (t0 + i) * a.sy.t, y[i]);
+        }
+    }
+  }
+  if (!a.state_out) return;
+  __syncthreads();
+  for (int i = threadIdx.x; i < np * CH; i += L::THREADS) {
+    const int n = i % np, ch = i / np;
+    if (n < a.Ns && ch < p.nch)
+      static_cast<S*>(a.state_out)[(p.n * a.D + p.d0 + ch) * a.Ns + n] = sh[n * CH + ch];
+  }
+}
+
+template <typename IO, typename L>
+hipError_t go(int io, const SsmArgs& a, hipStream_t s) {
+  const int64_t g = a.N * ssm_blocks(a, L::CH);
+  if (g == 0) return hipSuccess;
+  ssm_fwd<IO, L><<<static_cast<unsigned>(g), L::THREADS, L::lds(a.Ns), s>>>(a, ssm_ck(io, a.Ns));
+  return hipGetLastError();
+}
+
+// As many channels a work-group as leave the 256 CUs one each (and fit the LDS).
+template <typename IO, typename S, int TT, int NS>
+hipError_t by_channels(int io, const SsmArgs& a, hipStream_t s) {
+  if (a.N * ssm_blocks(a, 64) >= 256 && a.Ns <= 64) return go<IO, SsmTile<S, 64, 8, TT, NS, 16>>(io, a, s);
+  if (a.N * ssm_blocks(a, 32) >= 256 && a.Ns <= 128) return go<IO, SsmTile<S, 32, 8, TT, NS, 16>>(io, a, s);
+  return go<IO, SsmTile<S, 16, 8, TT, NS, 8>>(io, a, s);
+}
+
+}  // namespace
+
+int ssm_ck(int io, int Ns) { return (io == IO_F64 ? 8 : 16) * 8 * (64 / ssm_bwd_channels(Ns)); }
+
+hipError_t launch_ssm_fwd(int io, const SsmArgs& a, hipStream_t s) {
+  if (io == IO_F64) return by_channels<double, double, 8, 2>(io, a, s);
+  if (io == IO_F32) return by_channels<float, float, 16, 4>(io, a, s);
+  return by_channels<bf16, float, 16, 4>(io, a, s);
+}
+
+}  // namespace gls

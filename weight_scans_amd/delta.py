@@ -141,7 +141,10 @@ def _three(st, shape, name):
     return Strides(*st)
 
 
-_KINDS = {"gl_delta_fwd": 0, "gl_delta_bwd": 1, "gl_delta_step": 2, "gl_qknorm_rope_fwd": 3, "gl_qknorm_rope_bwd": 4}
+_KINDS = {n: i for i, n in enumerate((  # as in binding/fastcall.cpp
+    "gl_delta_fwd", "gl_delta_bwd", "gl_delta_step", "gl_qknorm_rope_fwd", "gl_qknorm_rope_bwd",
+    "gl_conv_fwd", "gl_conv_bwd", "gl_conv_step", "gl_ssm_fwd", "gl_ssm_bwd", "gl_ssm_step",
+    "gl_addnorm_fwd", "gl_addnorm_bwd", "gl_gatenorm_fwd", "gl_gatenorm_bwd"))}
 _calls: dict = {}
 
 

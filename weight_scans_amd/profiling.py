@@ -45,6 +45,7 @@ CALIB_BYTES = 256 << 20  # the calibration kernel in bench.py: 256 MiB read + 25
 
 
 DELTA_SOURCES = ("delta", "gl_delta", "k_delta", "k_qknorm")
+SSM_SOURCES = ("ssm", "gl_ssm", "k_ssm", "k_conv", "k_blocknorm")
 
 
 def _source_hash(take) -> str:
@@ -60,8 +61,9 @@ def _source_hash(take) -> str:
 
 def kernel_source_hash() -> str:
     """Hash of every source the scans are built from (those of the gated delta rule
-    and of the norms, which only bench.py --delta runs, have one of their own)."""
-    return _source_hash(lambda name: not name.startswith(DELTA_SOURCES))
+    and of the norms, which only bench.py --delta runs, have one of their own, and
+    so have those of the selective scan)."""
+    return _source_hash(lambda name: not name.startswith(DELTA_SOURCES + SSM_SOURCES))
 
 
 def delta_source_hash() -> str:
@@ -71,13 +73,21 @@ def delta_source_hash() -> str:
                         or name in ("dev_common.hpp", "internal.hpp", "mfma.hpp"))
 
 
+def ssm_source_hash() -> str:
+    """Hash of the sources of the selective scan, the short convolution and the norms
+    around a block, with the helpers that they share with the others."""
+    return _source_hash(lambda name: name.startswith(SSM_SOURCES)
+                        or name in ("dev_common.hpp", "internal.hpp", "delta.hpp"))
+
+
 def stale_profiles() -> list[str]:
     """The summaries under profiles/ that were taken of other kernel sources than
     these, or that do not say of which."""
     out = []
     for p in sorted(glob.glob(os.path.join(ROOT, "profiles", "*.md"))):
         name = os.path.basename(p)
-        want = delta_source_hash() if name.startswith("delta_") else kernel_source_hash()
+        want = (delta_source_hash() if name.startswith("delta_") else
+                ssm_source_hash() if name.startswith("ssm_") else kernel_source_hash())
         if f"Kernel source hash: `{want}`" not in open(p).read():
             out.append(name)
     return out
