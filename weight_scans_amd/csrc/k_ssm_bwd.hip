@@ -21,33 +21,55 @@
 namespace gls {
 namespace {
 
-// Sums of V values over CH neighbouring lanes: each exchange hands half of the
-// values that are left to the other half of the lanes.  On return v[k] of lane c is
-// the sum of value c V / CH + k (V < CH: lanes c .. c + CH / V - 1 hold the same).
-template <typename S, int CH, int V>
+// x of the lanes that a row's rotation or mirror hands it (the vector ALU's own lane
+// patterns; they cost nothing beside the sum that takes them).
+template <int PATTERN>
+__device__ __forceinline__ float from_lane(float x) {
+  return __uint_as_float(__builtin_amdgcn_update_dpp(0, __float_as_uint(x), PATTERN, 0xf, 0xf, true));
+}
+constexpr int kRowRor8 = 0x128, kHalfMirror = 0x141, kXor2 = 0x4e, kXor1 = 0xb1;
+
+// a summed over the two groups of lanes that differ in bit m, in those where it is 0; b in
+// the others.  (For m = 4 with the lanes of one group in reverse: a sum over all of
+// them is left.)
+template <int m>
+__device__ __forceinline__ float fold(float a, float b, bool up) {
+  if constexpr (m == 16) {
+    const auto r = __builtin_amdgcn_permlane16_swap(__float_as_uint(a), __float_as_uint(b), false, false);
+    return __uint_as_float(r[0]) + __uint_as_float(r[1]);
+  } else {
+    constexpr int P = m == 8 ? kRowRor8 : m == 4 ? kHalfMirror : m == 2 ? kXor2 : kXor1;
+    const float s = a + from_lane<P>(a), t = b + from_lane<P>(b);
+    return up ? t : s;
+  }
+}
+template <int m>
+__device__ __forceinline__ double fold(double a, double b, bool up) {
+  const double keep = up ? b : a, give = up ? a : b;
+  return keep + __shfl_xor(give, m, 64);
+}
+
+// Sums of V values over CH neighbouring lanes: each exchange hands half of the values
+// that are left to half of the lanes.  On return v[k] of lane c is the sum of value c V / CH
+// + k (V < CH: lanes c .. c + CH / V - 1 hold the same).
+template <typename S, int CH, int V, int n = V, int m = CH / 2>
 __device__ __forceinline__ void sum_lanes(S (&v)[V], int c) {
-  int n = V;
+  if constexpr (m >= 1) {
+    const bool up = c & m;
+    if constexpr (n > 1) {
 #pragma unroll
-  for (int m = CH / 2; m >= 1; m >>= 1) {
-    if (n > 1) {
-      n /= 2;
-      const bool up = c & m;
-#pragma unroll
-      for (int k = 0; k < V / 2; ++k)
-        if (k < n) {
-          const S keep = up ? v[k + n] : v[k], give = up ? v[k] : v[k + n];
-          v[k] = keep + __shfl_xor(give, m, 64);
-        }
+      for (int k = 0; k < n / 2; ++k) v[k] = fold<m>(v[k], v[k + n / 2], up);
     } else {
-      v[0] += __shfl_xor(v[0], m, 64);
+      v[0] = fold<m>(v[0], v[0], up);
     }
+    sum_lanes<S, CH, V, (n > 1 ? n / 2 : 1), m / 2>(v, c);
   }
 }
 
 // Leaves sums of a slot's TT x NS values over the channels at part + token NS + j.
 template <typename L>
-__device__ __forceinline__ void leave_sums(typename L::S (&v)[L::TT * L::NS], int c, typename L::S* part, int64_t t0,
-                                           int64_t len) {
+__device__ __forceinline__ void leave_sums(typename L::S (&v)[L::TT * L::NS], int c, typename L::S* part, int t0,
+                                           int len) {
   using S = typename L::S;
   constexpr int CH = L::CH, V = L::TT * L::NS, NS = L::NS;
   sum_lanes<S, CH, V>(v, c);
@@ -72,10 +94,11 @@ size_t bwd_lds(int N) {
                                   2 * L::W * L::CH * L::NS);
 }
 
-template <typename IO, typename L>
+template <typename IO, typename L, bool Z>
 __global__ __launch_bounds__(L::THREADS) void ssm_bwd(SsmArgs a) {
   using S = typename L::S;
-  constexpr int CH = L::CH, TT = L::TT, NS = L::NS, NB = L::NB, W = L::W;
+  using BC = SlotBC<L>;
+  constexpr int CH = L::CH, TT = L::TT, NS = L::NS, NB = L::NB, W = L::W, K = BC::K;
   extern __shared__ __align__(16) char lds[];
   const int np = L::npad(a.Ns);
   S* const sB = reinterpret_cast<S*>(lds);
@@ -93,7 +116,7 @@ __global__ __launch_bounds__(L::THREADS) void ssm_bwd(SsmArgs a) {
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
   const int c = lane % CH, ts = lane / CH, slot = wave * L::TS + ts;
   const bool in = c < p.nch;
-  const int d = p.d0 + (in ? c : 0);
+  const int cc = in ? c : 0, d = p.d0 + cc;
   for (int i = threadIdx.x; i < np * CH; i += L::THREADS) {
     const int n = i / CH, ch = i % CH;
     const bool there = n < a.Ns && ch < p.nch;
@@ -104,10 +127,6 @@ __global__ __launch_bounds__(L::THREADS) void ssm_bwd(SsmArgs a) {
   }
   const S skip = a.skip ? static_cast<const S*>(a.skip)[d] : S(0);
   const S bias = a.bias ? static_cast<const S*>(a.bias)[d] : S(0);
-  const IO* px = static_cast<const IO*>(a.x) + r.b * a.sx.b + r.t0 * a.sx.t + d;
-  const IO* pd = static_cast<const IO*>(a.dt) + r.b * a.sdt.b + r.t0 * a.sdt.t + d;
-  const IO* pz = static_cast<const IO*>(a.z) + r.b * a.sz.b + r.t0 * a.sz.t + d;
-  const IO* pg = static_cast<const IO*>(a.dy) + r.b * a.sdy.b + r.t0 * a.sdy.t + d;
   const int64_t ck0 = chunk_slot0(a.packed, p.n, r.t0, a.T, L::TILE);
   // parts of the sums over channels: [2][blocks][state groups][B T][NS]
   const int groups = (a.Ns + NS - 1) / NS;
@@ -126,37 +145,31 @@ __global__ __launch_bounds__(L::THREADS) void ssm_bwd(SsmArgs a) {
     }
   };
   for (int64_t tile = r.len ? (r.len - 1) / L::TILE : -1; tile >= 0; --tile) {
-    const int64_t tile0 = tile * L::TILE, t0 = tile0 + slot * TT;
-    S D[TT], u[TT], g[TT], y[TT], du[TT], dD[TT], sum = S(0);
+    const int64_t tile0 = tile * L::TILE;
+    const int left = static_cast<int>(r.len - tile0 < L::TILE ? r.len - tile0 : L::TILE);
+    const int here = left - slot * TT;
+    S D[TT], u[TT], g[TT], y[Z ? TT : 1], du[TT], dD[TT], sum = S(0);
+    SlotRows<IO, L>(a.x, a.sx, r, p.d0, cc, slot, tile0).ld(left, slot, u);
+    SlotRows<IO, L>(a.dt, a.sdt, r, p.d0, cc, slot, tile0).ld(left, slot, D);
+    SlotRows<IO, L>(a.dy, a.sdy, r, p.d0, cc, slot, tile0).ld(left, slot, g);
+    if constexpr (Z) {
+      S z[TT];
+      SlotRows<IO, L>(a.z, a.sz, r, p.d0, cc, slot, tile0).ld(left, slot, z);
+#pragma unroll
+      for (int i = 0; i < TT; ++i) g[i] *= z[i] * sigmoid_(z[i]);
+    }
+    ssm_steps<S, TT>(a.softplus, bias, in ? here : 0, D);
 #pragma unroll
     for (int i = 0; i < TT; ++i) {
-      const int64_t t = t0 + i < r.len ? t0 + i : r.len - 1;
-      u[i] = load_as<S>(px, t * a.sx.t);
-      D[i] = load_as<S>(pd, t * a.sdt.t);
-      g[i] = load_as<S>(pg, t * a.sdy.t);
-      y[i] = S(0);
-      du[i] = S(0);
-      dD[i] = S(0);
-    }
-    if (a.z) {
-#pragma unroll
-      for (int i = 0; i < TT; ++i) {
-        const int64_t t = t0 + i < r.len ? t0 + i : r.len - 1;
-        const S z = load_as<S>(pz, t * a.sz.t);
-        g[i] *= z * sigmoid_(z);
-      }
-    }
-#pragma unroll
-    for (int i = 0; i < TT; ++i) {
-      const bool there = in && t0 + i < r.len;
-      const S v = D[i] + bias;
-      D[i] = there ? (a.softplus ? softplus_(v) : v) : S(0);
+      const bool there = in && i < here;
       u[i] = there ? u[i] : S(0);
       g[i] = there ? g[i] : S(0);
       dskip = fma_(g[i], u[i], dskip);
-      y[i] = skip * u[i];
+      if constexpr (Z) y[i] = skip * u[i];
       u[i] *= D[i];
       sum += D[i];
+      du[i] = S(0);
+      dD[i] = S(0);
     }
     for (int n0 = 0; n0 < np; n0 += NB) {
       __syncthreads();
@@ -176,68 +189,80 @@ __global__ __launch_bounds__(L::THREADS) void ssm_bwd(SsmArgs a) {
           P[j] = Pb[j] = exp2_(A[j] * sum);
           h[j] = S(0);
         }
+        // the slot's effect on the state
 #pragma unroll
-        for (int i = 0; i < TT; ++i) {
-          S B[NS];
-          lds_get<S, NS>(bp + i * NB, B);
+        for (int i = 0; i < TT; i += K) {
+          const BC B(bp, i);
 #pragma unroll
-          for (int j = 0; j < NS; ++j) {
-            e[i][j] = exp2_(D[i] * A[j]);
-            h[j] = fma_(e[i][j], h[j], u[i] * B[j]);
-          }
+          for (int k = 0; k < K; ++k)
+#pragma unroll
+            for (int j = 0; j < NS; ++j) {
+              e[i + k][j] = exp2_(D[i + k] * A[j]);
+              h[j] = fma_(e[i + k][j], h[j], u[i + k] * B.v[k][j]);
+            }
+          if (i % 4 == 0) fence_order();
         }
         ssm_scan<L, false>(P, h, enter, agg, turn);
         settle();
+        fence_order();
+        // the states, and the products that dC sums
 #pragma unroll
-        for (int i = 0; i < TT; ++i) {
-          S B[NS], C[NS];
-          lds_get<S, NS>(bp + i * NB, B);
-          lds_get<S, NS>(cp + i * NB, C);
+        for (int i = 0; i < TT; i += K) {
+          const BC B(bp, i), C(cp, i);
 #pragma unroll
-          for (int j = 0; j < NS; ++j) {
-            q[i][j] = e[i][j] * h[j];
-            h[j] = fma_(u[i], B[j], q[i][j]);
-            y[i] = fma_(C[j], h[j], y[i]);
-            v[i * NS + j] = g[i] * h[j];
-          }
+          for (int k = 0; k < K; ++k)
+#pragma unroll
+            for (int j = 0; j < NS; ++j) {
+              q[i + k][j] = e[i + k][j] * h[j];
+              h[j] = fma_(u[i + k], B.v[k][j], q[i + k][j]);
+              if constexpr (Z) y[i + k] = fma_(C.v[k][j], h[j], y[i + k]);
+              v[(i + k) * NS + j] = g[i + k] * h[j];
+            }
+          if (i % 4 == 0) fence_order();
         }
-        leave_sums<L>(v, c, partC + (n / NS) * plane, t0, r.len);
+        leave_sums<L>(v, c, partC + (n / NS) * plane + tile0 * NS, slot * TT, left);
+        fence_order();
+        // the slot's effect on the gradient that comes from later tokens
 #pragma unroll
         for (int j = 0; j < NS; ++j) {
           s[j] = S(0);
           enter[j] = sl[(n + j) * CH + c];
         }
 #pragma unroll
-        for (int i = TT - 1; i >= 0; --i) {
-          S C[NS];
-          lds_get<S, NS>(cp + i * NB, C);
+        for (int i = TT - K; i >= 0; i -= K) {
+          const BC C(cp, i);
 #pragma unroll
-          for (int j = 0; j < NS; ++j) s[j] = e[i][j] * fma_(C[j], g[i], s[j]);
+          for (int k = K - 1; k >= 0; --k)
+#pragma unroll
+            for (int j = 0; j < NS; ++j) s[j] = e[i + k][j] * fma_(C.v[k][j], g[i + k], s[j]);
+          if (i % 4 == 0) fence_order();
         }
         ssm_scan<L, true>(Pb, s, enter, agg, turn);
+        fence_order();
         S dA[NS];
 #pragma unroll
         for (int j = 0; j < NS; ++j) dA[j] = S(0);
 #pragma unroll
-        for (int i = TT - 1; i >= 0; --i) {
-          S B[NS], C[NS];
-          lds_get<S, NS>(bp + i * NB, B);
-          lds_get<S, NS>(cp + i * NB, C);
+        for (int i = TT - K; i >= 0; i -= K) {
+          const BC B(bp, i), C(cp, i);
 #pragma unroll
-          for (int j = 0; j < NS; ++j) {
-            const S gt = fma_(C[j], g[i], s[j]), gq = gt * q[i][j];
-            du[i] = fma_(gt, B[j], du[i]);
-            dD[i] = fma_(gq, A[j], dD[i]);
-            dA[j] = fma_(gq, D[i], dA[j]);
-            v[i * NS + j] = gt * u[i];
-            s[j] = e[i][j] * gt;
-          }
+          for (int k = K - 1; k >= 0; --k)
+#pragma unroll
+            for (int j = 0; j < NS; ++j) {
+              const S gt = fma_(C.v[k][j], g[i + k], s[j]), gq = gt * q[i + k][j];
+              du[i + k] = fma_(gt, B.v[k][j], du[i + k]);
+              dD[i + k] = fma_(gq, A[j], dD[i + k]);
+              dA[j] = fma_(gq, D[i + k], dA[j]);
+              v[(i + k) * NS + j] = gt * u[i + k];
+              s[j] = e[i + k][j] * gt;
+            }
+          if (i % 4 == 0) fence_order();
         }
         if (slot == 0) {
 #pragma unroll
           for (int j = 0; j < NS; ++j) sl1[(n + j) * CH + c] = s[j];
         }
-        leave_sums<L>(v, c, partB + (n / NS) * plane, t0, r.len);
+        leave_sums<L>(v, c, partB + (n / NS) * plane + tile0 * NS, slot * TT, left);
 #pragma unroll
         for (int j = 0; j < NS; ++j) {
 #pragma unroll
@@ -251,23 +276,36 @@ __global__ __launch_bounds__(L::THREADS) void ssm_bwd(SsmArgs a) {
     S* const other = sl;
     sl = sl1;
     sl1 = other;
-    if (in) {
+    S x[TT], raw[TT];
+    SlotRows<IO, L>(a.x, a.sx, r, p.d0, cc, slot, tile0).ld(left, slot, x);
+    SlotRows<IO, L>(a.dt, a.sdt, r, p.d0, cc, slot, tile0).ld(left, slot, raw);
+    const SlotRows<IO, L> odx(a.dx, a.sdx, r, p.d0, cc, slot, tile0), odt(a.ddt, a.sddt, r, p.d0, cc, slot, tile0);
+    if (a.softplus) {
 #pragma unroll
-      for (int i = 0; i < TT; ++i)
-        if (t0 + i < r.len) {
-          const int64_t t = t0 + i;
-          const S x = load_as<S>(px, t * a.sx.t);
-          S dd = fma_(dD[i], static_cast<S>(1.0 / kLog2e), x * du[i]);
-          if (a.softplus) dd *= sigmoid_(load_as<S>(pd, t * a.sdt.t) + bias);
-          dbias += dd;
-          store_from(static_cast<IO*>(a.ddt) + r.b * a.sddt.b + (r.t0 + t) * a.sddt.t, d, dd);
-          store_from(static_cast<IO*>(a.dx) + r.b * a.sdx.b + (r.t0 + t) * a.sdx.t, d, fma_(D[i], du[i], skip * g[i]));
-          if (a.z) {
-            const S z = load_as<S>(pz, t * a.sz.t), k = sigmoid_(z);
-            store_from(static_cast<IO*>(a.dz) + r.b * a.sdz.b + (r.t0 + t) * a.sdz.t, d,
-                       load_as<S>(pg, t * a.sdy.t) * y[i] * (k * (S(1) + z * (S(1) - k))));
-          }
-        }
+      for (int i = 0; i < TT; ++i) raw[i] = sigmoid_(raw[i] + bias);
+    } else {
+#pragma unroll
+      for (int i = 0; i < TT; ++i) raw[i] = S(1);
+    }
+#pragma unroll
+    for (int i = 0; i < TT; ++i) {
+      if (in && i < here) {
+        const S dd = fma_(dD[i], static_cast<S>(1.0 / kLog2e), x[i] * du[i]) * raw[i];
+        dbias += dd;
+        put(odt.out(i), dd);
+        put(odx.out(i), fma_(D[i], du[i], skip * g[i]));
+      }
+    }
+    if constexpr (Z) {
+      S z[TT], dy[TT];
+      SlotRows<IO, L>(a.z, a.sz, r, p.d0, cc, slot, tile0).ld(left, slot, z);
+      SlotRows<IO, L>(a.dy, a.sdy, r, p.d0, cc, slot, tile0).ld(left, slot, dy);
+      const SlotRows<IO, L> odz(a.dz, a.sdz, r, p.d0, cc, slot, tile0);
+#pragma unroll
+      for (int i = 0; i < TT; ++i) {
+        const S k = sigmoid_(z[i]);
+        if (in && i < here) put(odz.out(i), dy[i] * y[i] * (k * (S(1) + z[i] * (S(1) - k))));
+      }
     }
   }
   __syncthreads();
@@ -343,10 +381,14 @@ __global__ __launch_bounds__(kSumThreads) void ssm_bwd_sums(SsmArgs a, int nb, i
 constexpr int kNS = 2;
 
 template <typename IO, typename L>
-hipError_t go(const SsmArgs& a, hipStream_t s) {
+hipError_t go(int io, const SsmArgs& a, hipStream_t s) {
   const int64_t blocks = ssm_blocks(a, L::CH);
   if (a.N * blocks > 0) {
-    ssm_bwd<IO, L><<<static_cast<unsigned>(a.N * blocks), L::THREADS, bwd_lds<L>(a.Ns), s>>>(a);
+    SsmArgs b = a;
+    b.vec_bc = ssm_vec_bc(io, a);
+    const unsigned g = static_cast<unsigned>(a.N * blocks);
+    if (a.z) ssm_bwd<IO, L, true><<<g, L::THREADS, bwd_lds<L>(a.Ns), s>>>(b);
+    else ssm_bwd<IO, L, false><<<g, L::THREADS, bwd_lds<L>(a.Ns), s>>>(b);
     const hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
   }
@@ -359,11 +401,11 @@ hipError_t go(const SsmArgs& a, hipStream_t s) {
 }
 
 template <typename IO, typename S, int TT>
-hipError_t by_states(const SsmArgs& a, hipStream_t s) {
+hipError_t by_states(int io, const SsmArgs& a, hipStream_t s) {
   switch (ssm_bwd_channels(a.Ns)) {
-    case 32: return go<IO, SsmTile<S, 32, 8, TT, kNS, 16>>(a, s);
-    case 16: return go<IO, SsmTile<S, 16, 8, TT, kNS, 8>>(a, s);
-    default: return go<IO, SsmTile<S, 8, 8, TT, kNS, 8>>(a, s);
+    case 32: return go<IO, SsmTile<S, 32, 8, TT, kNS, 16>>(io, a, s);
+    case 16: return go<IO, SsmTile<S, 16, 8, TT, kNS, 8>>(io, a, s);
+    default: return go<IO, SsmTile<S, 8, 8, TT, kNS, 8>>(io, a, s);
   }
 }
 
@@ -374,9 +416,9 @@ size_t ssm_bc_bytes(int io, const SsmArgs& a) {
   return static_cast<size_t>(2 * blocks) * ((a.Ns + kNS - 1) / kNS * kNS) * a.B * a.T * (io == IO_F64 ? 8 : 4);
 }
 hipError_t launch_ssm_bwd(int io, const SsmArgs& a, hipStream_t s) {
-  if (io == IO_F64) return by_states<double, double, 8>(a, s);
-  if (io == IO_F32) return by_states<float, float, 16>(a, s);
-  return by_states<bf16, float, 16>(a, s);
+  if (io == IO_F64) return by_states<double, double, 8>(io, a, s);
+  if (io == IO_F32) return by_states<float, float, 16>(io, a, s);
+  return by_states<bf16, float, 16>(io, a, s);
 }
 
 }  // namespace gls

@@ -15,10 +15,11 @@
 namespace gls {
 namespace {
 
-template <typename IO, typename L>
+template <typename IO, typename L, bool Z>
 __global__ __launch_bounds__(L::THREADS) void ssm_fwd(SsmArgs a, int ck) {
   using S = typename L::S;
-  constexpr int CH = L::CH, TT = L::TT, NS = L::NS, NB = L::NB;
+  using BC = SlotBC<L>;
+  constexpr int CH = L::CH, TT = L::TT, NS = L::NS, NB = L::NB, K = BC::K;
   extern __shared__ __align__(16) char lds[];
   const int np = L::npad(a.Ns);
   S* const sB = reinterpret_cast<S*>(lds);
@@ -29,9 +30,9 @@ __global__ __launch_bounds__(L::THREADS) void ssm_fwd(SsmArgs a, int ck) {
   const SsmPlace p = ssm_place(a, CH, xcd_order(blockIdx.x, gridDim.x));
   const SeqRange r = seq_range(a.cu, p.n, a.T);
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-  const int c = lane % CH, slot = wave * L::TS + lane / CH;
-  const bool in = c < p.nch;
-  const int d = p.d0 + (in ? c : 0);
+  const int slot = wave * L::TS + lane / CH;
+  const bool in = lane % CH < p.nch;
+  const int c = lane % CH, cc = in ? c : 0, d = p.d0 + cc;
   for (int i = threadIdx.x; i < np * CH; i += L::THREADS) {
     const int n = i / CH, ch = i % CH;
     const bool there = n < a.Ns && ch < p.nch;
@@ -41,27 +42,19 @@ __global__ __launch_bounds__(L::THREADS) void ssm_fwd(SsmArgs a, int ck) {
   }
   const S skip = a.skip ? static_cast<const S*>(a.skip)[d] : S(0);
   const S bias = a.bias ? static_cast<const S*>(a.bias)[d] : S(0);
-  const IO* px = static_cast<const IO*>(a.x) + r.b * a.sx.b + r.t0 * a.sx.t + d;
-  const IO* pd = static_cast<const IO*>(a.dt) + r.b * a.sdt.b + r.t0 * a.sdt.t + d;
-  const IO* pz = static_cast<const IO*>(a.z) + r.b * a.sz.b + r.t0 * a.sz.t + d;
-  IO* py = static_cast<IO*>(a.y) + r.b * a.sy.b + r.t0 * a.sy.t + d;
   const int64_t ck0 = chunk_slot0(a.packed, p.n, r.t0, a.T, ck);
   int turn = 0;
   S* sh1 = sh + np * CH;
   for (int64_t tile0 = 0; tile0 < r.len; tile0 += L::TILE) {
-    const int64_t t0 = tile0 + slot * TT;
+    const int left = static_cast<int>(r.len - tile0 < L::TILE ? r.len - tile0 : L::TILE);
+    const int here = left - slot * TT;  // the slot's tokens that are there, if positive
     S D[TT], u[TT], y[TT], sum = S(0);
+    SlotRows<IO, L>(a.x, a.sx, r, p.d0, cc, slot, tile0).ld(left, slot, u);
+    SlotRows<IO, L>(a.dt, a.sdt, r, p.d0, cc, slot, tile0).ld(left, slot, D);
+    ssm_steps<S, TT>(a.softplus, bias, here, D);
 #pragma unroll
     for (int i = 0; i < TT; ++i) {
-      const int64_t t = t0 + i < r.len ? t0 + i : r.len - 1;
-      u[i] = load_as<S>(px, t * a.sx.t);
-      D[i] = load_as<S>(pd, t * a.sdt.t);
-    }
-#pragma unroll
-    for (int i = 0; i < TT; ++i) {
-      const S v = D[i] + bias;
-      D[i] = t0 + i < r.len ? (a.softplus ? softplus_(v) : v) : S(0);
-      u[i] = t0 + i < r.len ? u[i] : S(0);
+      u[i] = i < here ? u[i] : S(0);
       y[i] = skip * u[i];
       u[i] *= D[i];
       sum += D[i];
@@ -83,32 +76,36 @@ __global__ __launch_bounds__(L::THREADS) void ssm_fwd(SsmArgs a, int ck) {
           h0[j] = sh[(n0 + n1 + j) * CH + c];
         }
 #pragma unroll
-        for (int i = 0; i < TT; ++i) {
-          S B[NS];
-          lds_get<S, NS>(bp + i * NB, B);
+        for (int i = 0; i < TT; i += K) {
+          const BC B(bp, i);
 #pragma unroll
-          for (int j = 0; j < NS; ++j) {
-            e[i][j] = exp2_(D[i] * A[j]);
-            h[j] = fma_(e[i][j], h[j], u[i] * B[j]);
-          }
+          for (int k = 0; k < K; ++k)
+#pragma unroll
+            for (int j = 0; j < NS; ++j) {
+              e[i + k][j] = exp2_(D[i + k] * A[j]);
+              h[j] = fma_(e[i + k][j], h[j], u[i + k] * B.v[k][j]);
+            }
+          if (i % 4 == 0) fence_order();
         }
         ssm_scan<L, false>(P, h, h0, agg, turn);
-        if (a.ckpt && in && t0 < r.len && t0 % ck == 0) {
-          S* o = static_cast<S*>(a.ckpt) + ((ck0 + t0 / ck) * a.Ns + n0 + n1) * a.D + d;
+        if (a.ckpt && in && here > 0 && (tile0 + slot * TT) % ck == 0) {
+          S* o = static_cast<S*>(a.ckpt) + ((ck0 + (tile0 + slot * TT) / ck) * a.Ns + n0 + n1) * a.D + d;
 #pragma unroll
           for (int j = 0; j < NS; ++j)
             if (n0 + n1 + j < a.Ns) o[static_cast<int64_t>(j) * a.D] = h[j];
         }
+        fence_order();
 #pragma unroll
-        for (int i = 0; i < TT; ++i) {
-          S B[NS], C[NS];
-          lds_get<S, NS>(bp + i * NB, B);
-          lds_get<S, NS>(cp + i * NB, C);
+        for (int i = 0; i < TT; i += K) {
+          const BC B(bp, i), C(cp, i);
 #pragma unroll
-          for (int j = 0; j < NS; ++j) {
-            h[j] = fma_(e[i][j], h[j], u[i] * B[j]);
-            y[i] = fma_(C[j], h[j], y[i]);
-          }
+          for (int k = 0; k < K; ++k)
+#pragma unroll
+            for (int j = 0; j < NS; ++j) {
+              h[j] = fma_(e[i + k][j], h[j], u[i + k] * B.v[k][j]);
+              y[i + k] = fma_(C.v[k][j], h[j], y[i + k]);
+            }
+          if (i % 4 == 0) fence_order();
         }
         if (slot == L::SL - 1) {
 #pragma unroll
@@ -119,16 +116,18 @@ __global__ __launch_bounds__(L::THREADS) void ssm_fwd(SsmArgs a, int ck) {
     S* const other = sh;
     sh = sh1;
     sh1 = other;
-    if (a.y && in) {
+    if (!a.y) continue;
+    if constexpr (Z) {
+      S z[TT];
+      SlotRows<IO, L>(a.z, a.sz, r, p.d0, cc, slot, tile0).ld(left, slot, z);
+#pragma unroll
+      for (int i = 0; i < TT; ++i) y[i] *= z[i] * sigmoid_(z[i]);
+    }
+    const SlotRows<IO, L> out(a.y, a.sy, r, p.d0, cc, slot, tile0);
+    if (in) {
 #pragma unroll
       for (int i = 0; i < TT; ++i)
-        if (t0 + i < r.len) {
-          if (a.z) {
-            const S z = load_as<S>(pz, (t0 + i) * a.sz.t);
-            y[i] *= z * sigmoid_(z);
-          }
-          store_from(py, (t0 + i) * a.sy.t, y[i]);
-        }
+        if (i < here) put(out.out(i), y[i]);
     }
   }
   if (!a.state_out) return;
@@ -144,7 +143,10 @@ template <typename IO, typename L>
 hipError_t go(int io, const SsmArgs& a, hipStream_t s) {
   const int64_t g = a.N * ssm_blocks(a, L::CH);
   if (g == 0) return hipSuccess;
-  ssm_fwd<IO, L><<<static_cast<unsigned>(g), L::THREADS, L::lds(a.Ns), s>>>(a, ssm_ck(io, a.Ns));
+  SsmArgs b = a;
+  b.vec_bc = ssm_vec_bc(io, a);
+  if (a.z) ssm_fwd<IO, L, true><<<static_cast<unsigned>(g), L::THREADS, L::lds(a.Ns), s>>>(b, ssm_ck(io, a.Ns));
+  else ssm_fwd<IO, L, false><<<static_cast<unsigned>(g), L::THREADS, L::lds(a.Ns), s>>>(b, ssm_ck(io, a.Ns));
   return hipGetLastError();
 }
 

@@ -78,6 +78,7 @@ struct SsmArgs {
   int64_t N = 0, B = 0, T = 0;  // sequences, batch, tokens
   int D = 0, Ns = 0, G = 0;     // channels, states, groups
   bool packed = false, softplus = false;
+  bool vec_bc = false;          // rows of B and C in vectors of 16 bytes (set by the launchers)
   Rows sx{}, sdt{}, sz{}, sB{}, sC{}, sy{};
   Rows sdy{}, sdx{}, sddt{}, sdz{}, sdB{}, sdC{};
 };

@@ -7,6 +7,18 @@
 
 namespace gls {
 
+// One rounding to bf16 (to nearest, ties to even), by the hardware.
+__device__ __forceinline__ uint32_t pack_bf16(float a, float b) {
+  typedef __bf16 two __attribute__((ext_vector_type(2)));
+  typedef float ftwo __attribute__((ext_vector_type(2)));
+  return __builtin_bit_cast(uint32_t, __builtin_convertvector((ftwo){a, b}, two));
+}
+template <typename IO, typename S>
+__device__ __forceinline__ void put(IO* p, S v) {
+  if constexpr (sizeof(IO) == 2) reinterpret_cast<uint16_t*>(p)[0] = __builtin_bit_cast(uint16_t, static_cast<__bf16>(v));
+  else p[0] = static_cast<IO>(v);
+}
+
 constexpr double kLog2e = 1.4426950408889634;
 
 __device__ __forceinline__ float exp2_(float x) { return __builtin_amdgcn_exp2f(x); }
@@ -63,8 +75,7 @@ struct Vec<bf16> {
   __device__ static __forceinline__ void st(bf16* p, const S* v) {
     uint32_t w[4];
 #pragma unroll
-    for (int i = 0; i < 4; ++i)
-      w[i] = f32_to_bf16(v[2 * i]) | (static_cast<uint32_t>(f32_to_bf16(v[2 * i + 1])) << 16);
+    for (int i = 0; i < 4; ++i) w[i] = pack_bf16(v[2 * i], v[2 * i + 1]);
     *reinterpret_cast<uint4*>(p) = make_uint4(w[0], w[1], w[2], w[3]);
   }
 };
@@ -108,7 +119,7 @@ __device__ __forceinline__ void load_w(const IO* p, S* v) {
 template <typename IO, typename S, int W>
 __device__ __forceinline__ void store_w(IO* p, const S* v) {
   if constexpr (W == 1) {
-    store_from(p, 0, v[0]);
+    put(p, v[0]);
   } else {
     static_assert(W == Vec<IO>::n, "16 bytes");
     Vec<IO>::st(p, v);
