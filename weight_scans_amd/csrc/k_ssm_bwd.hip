@@ -49,43 +49,65 @@ __device__ __forceinline__ double fold(double a, double b, bool up) {
   return keep + __shfl_xor(give, m, 64);
 }
 
-// Sums of V values over CH neighbouring lanes: each exchange hands half of the values
-// that are left to half of the lanes.  On return v[k] of lane c is the sum of value c V / CH
-// + k (V < CH: lanes c .. c + CH / V - 1 hold the same).
-template <typename S, int CH, int V, int n = V, int m = CH / 2>
-__device__ __forceinline__ void sum_lanes(S (&v)[V], int c) {
-  if constexpr (m >= 1) {
-    const bool up = c & m;
-    if constexpr (n > 1) {
-#pragma unroll
-      for (int k = 0; k < n / 2; ++k) v[k] = fold<m>(v[k], v[k + n / 2], up);
-    } else {
-      v[0] = fold<m>(v[0], v[0], up);
-    }
-    sum_lanes<S, CH, V, (n > 1 ? n / 2 : 1), m / 2>(v, c);
-  }
-}
-
-// Leaves sums of a slot's TT x NS values over the channels at part + token NS + j.
-template <typename L>
-__device__ __forceinline__ void leave_sums(typename L::S (&v)[L::TT * L::NS], int c, typename L::S* part, int t0,
-                                           int len) {
+// Sums of a slot's TT x NS values over the CH channels.  Every fold hands half of what is
+// left to half of the lanes: first over a token's states, then over pairs of tokens,
+// of pairs, ... as they come (BACK: from the last token on), so that few values wait.
+// What is left when the lanes are used up is one sum a lane, at part[token NS + state].
+template <typename L, bool BACK>
+struct Sums {
   using S = typename L::S;
-  constexpr int CH = L::CH, V = L::TT * L::NS, NS = L::NS;
-  sum_lanes<S, CH, V>(v, c);
-  if constexpr (V >= CH) {
-    constexpr int k = V / CH;
+  static constexpr int CH = L::CH, TT = L::TT, NS = L::NS;
+  static constexpr int lg(int n) { return n <= 1 ? 0 : 1 + lg(n / 2); }
+  static constexpr int STATES = lg(NS), LANES = lg(CH) - STATES;
+  static constexpr int DEPTH = LANES < lg(TT) ? LANES : lg(TT);
+  static constexpr int bit(int k) { return CH >> (1 + STATES + k); }  // lanes folded at depth k over tokens
+  S* part;         // of the slot's first token, with the lane's own token and state
+  int c, here;     // the lane's channel; tokens that are there, counted from the lane's own
+  S t[DEPTH + 1][TT];
+
+  __device__ __forceinline__ Sums(S* first, int c_, int here_) : part(first), c(c_), here(here_) {
 #pragma unroll
-    for (int i = 0; i < k; ++i) {
-      const int at = c * k + i;
-      if (t0 + at / NS < len) part[t0 * NS + at] = v[i];
+    for (int k = 0; k < STATES; ++k) part += c & (CH >> (1 + k)) ? NS >> (1 + k) : 0;
+#pragma unroll
+    for (int k = 0; k < DEPTH; ++k) {
+      const int own = c & bit(k) ? 1 << k : 0;
+      part += own * NS;
+      here -= own;
     }
-  } else {
-    constexpr int k = CH / V;
-    const int at = c / k;
-    if (c % k == 0 && t0 + at / NS < len) part[t0 * NS + at] = v[0];
+    if (DEPTH < LANES && (c & (2 * bit(DEPTH) - 1))) here = 0;  // lanes that hold what another one does
   }
-}
+  template <int k, int n>
+  __device__ __forceinline__ S states(S (&v)[NS]) {
+    if constexpr (n == 1) {
+      return v[0];
+    } else {
+#pragma unroll
+      for (int j = 0; j < n / 2; ++j) v[j] = fold<(CH >> (1 + k))>(v[j], v[j + n / 2], c & (CH >> (1 + k)));
+      return states<k + 1, n / 2>(v);
+    }
+  }
+  template <int m>
+  __device__ __forceinline__ S rest(S x) {
+    if constexpr (m < 1) return x;
+    else return rest<m / 2>(fold<m>(x, x, false));
+  }
+  template <int k>
+  __device__ __forceinline__ void tokens(int i, S x) {
+    if constexpr (k == DEPTH) {
+      const int first = i >> DEPTH << DEPTH;
+      x = rest<bit(DEPTH)>(x);
+      if (first < here) part[first * NS] = x;
+    } else {
+      t[k][i >> k] = x;
+      if (((i >> k) & 1) == (BACK ? 0 : 1)) {
+        const int q = i >> (k + 1) << 1;
+        tokens<k + 1>(i, fold<bit(k)>(t[k][q], t[k][q + 1], c & bit(k)));
+      }
+    }
+  }
+  // token i's values, in order
+  __device__ __forceinline__ void put(int i, S (&v)[NS]) { tokens<0>(i, states<0, NS>(v)); }
+};
 
 // LDS besides the forward's: what the waves pass on of dA, and its sums.
 template <typename L>
@@ -180,7 +202,7 @@ __global__ __launch_bounds__(L::THREADS) void ssm_bwd(SsmArgs a) {
         if (n >= a.Ns) break;
         const S* bp = sB + L::at(slot * TT, n1);
         const S* cp = sC + L::at(slot * TT, n1);
-        S A[NS], P[NS], Pb[NS], h[NS], s[NS], enter[NS], e[TT][NS], q[TT][NS], v[TT * NS];
+        S A[NS], P[NS], Pb[NS], h[NS], s[NS], enter[NS], e[TT][NS], q[TT][NS];
         const S* kept = static_cast<const S*>(a.ckpt) + ((ck0 + tile) * a.Ns + n) * a.D + d;
 #pragma unroll
         for (int j = 0; j < NS; ++j) {
@@ -206,21 +228,24 @@ __global__ __launch_bounds__(L::THREADS) void ssm_bwd(SsmArgs a) {
         settle();
         fence_order();
         // the states, and the products that dC sums
+        Sums<L, false> sumC(partC + (n / NS) * plane + (tile0 + slot * TT) * NS, c, here);
 #pragma unroll
         for (int i = 0; i < TT; i += K) {
           const BC B(bp, i), C(cp, i);
 #pragma unroll
-          for (int k = 0; k < K; ++k)
+          for (int k = 0; k < K; ++k) {
+            S v[NS];
 #pragma unroll
             for (int j = 0; j < NS; ++j) {
               q[i + k][j] = e[i + k][j] * h[j];
               h[j] = fma_(u[i + k], B.v[k][j], q[i + k][j]);
               if constexpr (Z) y[i + k] = fma_(C.v[k][j], h[j], y[i + k]);
-              v[(i + k) * NS + j] = g[i + k] * h[j];
+              v[j] = g[i + k] * h[j];
             }
+            sumC.put(i + k, v);
+          }
           if (i % 4 == 0) fence_order();
         }
-        leave_sums<L>(v, c, partC + (n / NS) * plane + tile0 * NS, slot * TT, left);
         fence_order();
         // the slot's effect on the gradient that comes from later tokens
 #pragma unroll
@@ -242,27 +267,30 @@ __global__ __launch_bounds__(L::THREADS) void ssm_bwd(SsmArgs a) {
         S dA[NS];
 #pragma unroll
         for (int j = 0; j < NS; ++j) dA[j] = S(0);
+        Sums<L, true> sumB(partB + (n / NS) * plane + (tile0 + slot * TT) * NS, c, here);
 #pragma unroll
         for (int i = TT - K; i >= 0; i -= K) {
           const BC B(bp, i), C(cp, i);
 #pragma unroll
-          for (int k = K - 1; k >= 0; --k)
+          for (int k = K - 1; k >= 0; --k) {
+            S v[NS];
 #pragma unroll
             for (int j = 0; j < NS; ++j) {
               const S gt = fma_(C.v[k][j], g[i + k], s[j]), gq = gt * q[i + k][j];
               du[i + k] = fma_(gt, B.v[k][j], du[i + k]);
               dD[i + k] = fma_(gq, A[j], dD[i + k]);
               dA[j] = fma_(gq, D[i + k], dA[j]);
-              v[(i + k) * NS + j] = gt * u[i + k];
+              v[j] = gt * u[i + k];
               s[j] = e[i + k][j] * gt;
             }
+            sumB.put(i + k, v);
+          }
           if (i % 4 == 0) fence_order();
         }
         if (slot == 0) {
 #pragma unroll
           for (int j = 0; j < NS; ++j) sl1[(n + j) * CH + c] = s[j];
         }
-        leave_sums<L>(v, c, partB + (n / NS) * plane + tile0 * NS, slot * TT, left);
 #pragma unroll
         for (int j = 0; j < NS; ++j) {
 #pragma unroll

@@ -89,9 +89,11 @@ struct SlotRows {
 #pragma unroll
       for (int i = 0; i < L::TT; ++i) v[i] = load_as<S>(reinterpret_cast<const IO*>(base + i * step + off), 0);
     } else {
+      int first = slot * L::TT;
+      asm volatile("" : "+v"(first));  // likewise: not kept for the next use
 #pragma unroll
       for (int i = 0; i < L::TT; ++i) {
-        const int tok = min(slot * L::TT + i, left - 1);
+        const int tok = min(first + i, left - 1);
         v[i] = load_as<S>(reinterpret_cast<const IO*>(base + static_cast<uint32_t>(tok) * step + col), 0);
       }
     }
