@@ -109,11 +109,12 @@ struct Sums {
   __device__ __forceinline__ void put(int i, S (&v)[NS]) { tokens<0>(i, states<0, NS>(v)); }
 };
 
-// LDS besides the forward's: what the waves pass on of dA, and its sums.
-template <typename L>
+// LDS: B and C of the tile, what the waves pass on of the scans and of dA; A log2 e, dA,
+// the state before the tile and two of the gradient that enters it; y of the tile's tokens.
+template <typename L, bool Z>
 size_t bwd_lds(int N) {
-  return sizeof(typename L::S) * (2 * L::BC + 4 * static_cast<size_t>(L::npad(N)) * L::CH + 2 * L::W * L::CH * 2 * L::NS +
-                                  2 * L::W * L::CH * L::NS);
+  return sizeof(typename L::S) * (2 * L::BC + 5 * static_cast<size_t>(L::npad(N)) * L::CH + 2 * L::W * L::CH * 2 * L::NS +
+                                  2 * L::W * L::CH * L::NS + (Z ? L::THREADS * L::TT : 0));
 }
 
 template <typename IO, typename L, bool Z>
@@ -129,8 +130,14 @@ __global__ __launch_bounds__(L::THREADS) void ssm_bwd(SsmArgs a) {
   S* const red = agg + 2 * W * CH * 2 * NS;       // [2][W][CH][NS]
   S* const sA = red + 2 * W * CH * NS;            // [np][CH]
   S* const sdA = sA + np * CH;                    // [np][CH]
-  S* sl = sdA + np * CH;                          // [2][np][CH]
+  S* const sS = sdA + np * CH;                    // [np][CH]
+  S* sl = sS + np * CH;                           // [2][np][CH]
   S* sl1 = sl + np * CH;
+  // y before the gate, in LDS: kept over all states, it is more than the registers hold
+  // beside what the passes need (98 registers spilled, and every wait for one of them a
+  // wait for the sums' stores: 1587 us instead of 749 at 4 x 4096 x 2048 x 16)
+  constexpr int YV = 16 / sizeof(S);
+  S* const sy = sS + 3 * np * CH + threadIdx.x * YV;  // [TT / YV][threads][YV]
   const int64_t blocks = static_cast<int64_t>(gridDim.x) / a.N;
   const int64_t id = xcd_order(blockIdx.x, gridDim.x);
   const SsmPlace p = ssm_place(a, CH, id);
@@ -170,7 +177,7 @@ __global__ __launch_bounds__(L::THREADS) void ssm_bwd(SsmArgs a) {
     const int64_t tile0 = tile * L::TILE;
     const int left = static_cast<int>(r.len - tile0 < L::TILE ? r.len - tile0 : L::TILE);
     const int here = left - slot * TT;
-    S D[TT], u[TT], g[TT], y[Z ? TT : 1], du[TT], dD[TT], sum = S(0);
+    S D[TT], u[TT], g[TT], du[TT], dD[TT], sum = S(0);
     SlotRows<IO, L>(a.x, a.sx, r, p.d0, cc, slot, tile0).ld(left, slot, u);
     SlotRows<IO, L>(a.dt, a.sdt, r, p.d0, cc, slot, tile0).ld(left, slot, D);
     SlotRows<IO, L>(a.dy, a.sdy, r, p.d0, cc, slot, tile0).ld(left, slot, g);
@@ -187,7 +194,7 @@ __global__ __launch_bounds__(L::THREADS) void ssm_bwd(SsmArgs a) {
       u[i] = there ? u[i] : S(0);
       g[i] = there ? g[i] : S(0);
       dskip = fma_(g[i], u[i], dskip);
-      if constexpr (Z) y[i] = skip * u[i];
+      if constexpr (Z) sy[i / YV * YV * L::THREADS + i % YV] = skip * u[i];
       u[i] *= D[i];
       sum += D[i];
       du[i] = S(0);
@@ -196,6 +203,11 @@ __global__ __launch_bounds__(L::THREADS) void ssm_bwd(SsmArgs a) {
     for (int n0 = 0; n0 < np; n0 += NB) {
       __syncthreads();
       ssm_load_bc<IO, L>(a, p, r, tile0, n0, sB, sC);
+      for (int i = threadIdx.x; i < NB * CH; i += L::THREADS) {
+        const int n = n0 + i / CH, ch = i % CH;
+        const bool there = n < a.Ns && ch < p.nch;
+        sS[n0 * CH + i] = there ? static_cast<const S*>(a.ckpt)[((ck0 + tile) * a.Ns + n) * a.D + p.d0 + ch] : S(0);
+      }
       __syncthreads();
       for (int n1 = 0; n1 < NB; n1 += NS) {
         const int n = n0 + n1;
@@ -203,11 +215,10 @@ __global__ __launch_bounds__(L::THREADS) void ssm_bwd(SsmArgs a) {
         const S* bp = sB + L::at(slot * TT, n1);
         const S* cp = sC + L::at(slot * TT, n1);
         S A[NS], P[NS], Pb[NS], h[NS], s[NS], enter[NS], e[TT][NS], q[TT][NS];
-        const S* kept = static_cast<const S*>(a.ckpt) + ((ck0 + tile) * a.Ns + n) * a.D + d;
 #pragma unroll
         for (int j = 0; j < NS; ++j) {
           A[j] = sA[(n + j) * CH + c];
-          enter[j] = n + j < a.Ns ? kept[static_cast<int64_t>(j) * a.D] : S(0);
+          enter[j] = sS[(n + j) * CH + c];
           P[j] = Pb[j] = exp2_(A[j] * sum);
           h[j] = S(0);
         }
@@ -229,9 +240,13 @@ __global__ __launch_bounds__(L::THREADS) void ssm_bwd(SsmArgs a) {
         fence_order();
         // the states, and the products that dC sums
         Sums<L, false> sumC(partC + (n / NS) * plane + (tile0 + slot * TT) * NS, c, here);
+        S y[YV];
 #pragma unroll
         for (int i = 0; i < TT; i += K) {
           const BC B(bp, i), C(cp, i);
+          if constexpr (Z) {
+            if (i % YV == 0) lds_get<S, YV>(sy + i * L::THREADS, y);
+          }
 #pragma unroll
           for (int k = 0; k < K; ++k) {
             S v[NS];
@@ -239,10 +254,16 @@ __global__ __launch_bounds__(L::THREADS) void ssm_bwd(SsmArgs a) {
             for (int j = 0; j < NS; ++j) {
               q[i + k][j] = e[i + k][j] * h[j];
               h[j] = fma_(u[i + k], B.v[k][j], q[i + k][j]);
-              if constexpr (Z) y[i + k] = fma_(C.v[k][j], h[j], y[i + k]);
+              if constexpr (Z) y[(i + k) % YV] = fma_(C.v[k][j], h[j], y[(i + k) % YV]);
               v[j] = g[i + k] * h[j];
             }
             sumC.put(i + k, v);
+          }
+          if constexpr (Z) {
+            if ((i + K) % YV == 0) {
+#pragma unroll
+              for (int k = 0; k < YV; ++k) sy[(i + K - YV) * L::THREADS + k] = y[k];
+            }
           }
           if (i % 4 == 0) fence_order();
         }
@@ -332,7 +353,8 @@ __global__ __launch_bounds__(L::THREADS) void ssm_bwd(SsmArgs a) {
 #pragma unroll
       for (int i = 0; i < TT; ++i) {
         const S k = sigmoid_(z[i]);
-        if (in && i < here) put(odz.out(i), dy[i] * y[i] * (k * (S(1) + z[i] * (S(1) - k))));
+        const S y = sy[i / YV * YV * L::THREADS + i % YV];
+        if (in && i < here) put(odz.out(i), dy[i] * y * (k * (S(1) + z[i] * (S(1) - k))));
       }
     }
   }
@@ -415,8 +437,8 @@ hipError_t go(int io, const SsmArgs& a, hipStream_t s) {
     SsmArgs b = a;
     b.vec_bc = ssm_vec_bc(io, a);
     const unsigned g = static_cast<unsigned>(a.N * blocks);
-    if (a.z) ssm_bwd<IO, L, true><<<g, L::THREADS, bwd_lds<L>(a.Ns), s>>>(b);
-    else ssm_bwd<IO, L, false><<<g, L::THREADS, bwd_lds<L>(a.Ns), s>>>(b);
+    if (a.z) ssm_bwd<IO, L, true><<<g, L::THREADS, bwd_lds<L, true>(a.Ns), s>>>(b);
+    else ssm_bwd<IO, L, false><<<g, L::THREADS, bwd_lds<L, false>(a.Ns), s>>>(b);
     const hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
   }
@@ -430,17 +452,17 @@ hipError_t go(int io, const SsmArgs& a, hipStream_t s) {
 
 template <typename IO, typename S, int TT>
 hipError_t by_states(int io, const SsmArgs& a, hipStream_t s) {
-  switch (ssm_bwd_channels(a.Ns)) {
+  switch (ssm_bwd_channels(io, a.Ns)) {
     case 32: return go<IO, SsmTile<S, 32, 8, TT, kNS, 16>>(io, a, s);
     case 16: return go<IO, SsmTile<S, 16, 8, TT, kNS, 8>>(io, a, s);
-    default: return go<IO, SsmTile<S, 8, 8, TT, kNS, 8>>(io, a, s);
+    default: return go<IO, SsmTile<S, 8, 8, TT, kNS, sizeof(S) == 8 ? 4 : 8>>(io, a, s);
   }
 }
 
 }  // namespace
 
 size_t ssm_bc_bytes(int io, const SsmArgs& a) {
-  const int64_t blocks = ssm_blocks(a, ssm_bwd_channels(a.Ns));
+  const int64_t blocks = ssm_blocks(a, ssm_bwd_channels(io, a.Ns));
   return static_cast<size_t>(2 * blocks) * ((a.Ns + kNS - 1) / kNS * kNS) * a.B * a.T * (io == IO_F64 ? 8 : 4);
 }
 hipError_t launch_ssm_bwd(int io, const SsmArgs& a, hipStream_t s) {

@@ -160,7 +160,7 @@ hipError_t by_channels(int io, const SsmArgs& a, hipStream_t s) {
 
 }  // namespace
 
-int ssm_ck(int io, int Ns) { return (io == IO_F64 ? 8 : 16) * 8 * (64 / ssm_bwd_channels(Ns)); }
+int ssm_ck(int io, int Ns) { return (io == IO_F64 ? 8 : 16) * 8 * (64 / ssm_bwd_channels(io, Ns)); }
 
 hipError_t launch_ssm_fwd(int io, const SsmArgs& a, hipStream_t s) {
   if (io == IO_F64) return by_channels<double, double, 8, 2>(io, a, s);

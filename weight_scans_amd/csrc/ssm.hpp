@@ -84,7 +84,11 @@ struct SsmArgs {
 };
 // Channels a work-group of the backward, and the tokens of its tiles: a forward that
 // trains keeps the state before each.
-inline int ssm_bwd_channels(int Ns) { return Ns <= 64 ? 32 : Ns <= 128 ? 16 : 8; }
+// (As many as leave the LDS room for N states of each.)
+inline int ssm_bwd_channels(int io, int Ns) {
+  const int n = io == IO_F64 ? 2 * Ns : Ns;
+  return n <= 64 ? 32 : n <= 128 ? 16 : 8;
+}
 int ssm_ck(int io, int Ns);
 size_t ssm_bc_bytes(int io, const SsmArgs& a);
 hipError_t launch_ssm_fwd(int io, const SsmArgs& a, hipStream_t s);
