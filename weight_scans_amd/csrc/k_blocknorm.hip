@@ -66,7 +66,7 @@ struct Slice {
     } else {
 #pragma unroll
       for (int e = 0; e < E; ++e)
-        if (e * TPR + j < d) store_from(p, e * TPR + j, v[e]);
+        if (e * TPR + j < d) put(p + e * TPR + j, v[e]);
     }
   }
 };
@@ -153,15 +153,15 @@ __global__ __launch_bounds__(THREADS) void addnorm_fwd(AddNormArgs a) {
 }
 
 // Sums of a work-group's rows for the weights: its R rows of threads meet in LDS.
-template <typename IO, typename S, int TPR, int E, bool VEC, int R>
-__device__ __forceinline__ void leave_part(S* part, int d, const S (&v)[E]) {
+template <typename IO, typename PAR, typename S, int TPR, int E, bool VEC, int R>
+__device__ __forceinline__ void leave_part(PAR* part, int d, const S (&v)[E]) {
   using L = Slice<S, TPR, E, VEC>;
   const int j = threadIdx.x % TPR, q = threadIdx.x / TPR;
   if constexpr (R == 1) {
 #pragma unroll
     for (int e = 0; e < E; ++e) {
       const int c = L::template col<IO>(j, e);
-      if (c < d) part[c] = v[e];
+      if (c < d) part[c] = static_cast<PAR>(v[e]);
     }
   } else {
     __shared__ S red[R][TPR * E];
@@ -173,12 +173,12 @@ __device__ __forceinline__ void leave_part(S* part, int d, const S (&v)[E]) {
       S s = S(0);
 #pragma unroll
       for (int i = 0; i < R; ++i) s += red[i][c];
-      part[c] = s;
+      part[c] = static_cast<PAR>(s);
     }
   }
 }
 
-template <typename IO, typename RES, typename S, int TPR, int E, bool VEC, int THREADS>
+template <typename IO, typename RES, typename PAR, typename S, int TPR, int E, bool VEC, int THREADS>
 __global__ __launch_bounds__(THREADS) void addnorm_bwd(AddNormArgs a) {
   using L = Slice<S, TPR, E, VEC>;
   constexpr int R = THREADS / TPR;
@@ -251,10 +251,10 @@ __global__ __launch_bounds__(THREADS) void addnorm_bwd(AddNormArgs a) {
     if (in) L::template st<IO>(row_out<IO>(a.dx, a.sdx, b, t), j, a.d, g);
   }
   const int64_t plane = static_cast<int64_t>(gridDim.x) * a.d;
-  S* part = static_cast<S*>(a.part) + blockIdx.x * static_cast<int64_t>(a.d);
-  if (a.dw[0]) leave_part<IO, S, TPR, E, VEC, R>(part, a.d, dw);
-  if (a.dw[1]) leave_part<IO, S, TPR, E, VEC, R>(part + plane, a.d, dwx);
-  if (a.dw[2]) leave_part<IO, S, TPR, E, VEC, R>(part + 2 * plane, a.d, ds);
+  PAR* part = static_cast<PAR*>(a.part) + blockIdx.x * static_cast<int64_t>(a.d);
+  if (a.dw[0]) leave_part<IO, PAR, S, TPR, E, VEC, R>(part, a.d, dw);
+  if (a.dw[1]) leave_part<IO, PAR, S, TPR, E, VEC, R>(part + plane, a.d, dwx);
+  if (a.dw[2]) leave_part<IO, PAR, S, TPR, E, VEC, R>(part + 2 * plane, a.d, ds);
 }
 
 // ---------------------------------------------------------------- gated norm
@@ -306,7 +306,7 @@ __global__ __launch_bounds__(THREADS) void gatenorm_fwd(GateNormArgs a) {
 
 // Rows of the work-groups blockIdx.y: all rows, or (weights of each group) the
 // rows of that group.
-template <typename IO, typename S, int TPR, int E, bool VEC, int THREADS>
+template <typename IO, typename PAR, typename S, int TPR, int E, bool VEC, int THREADS>
 __global__ __launch_bounds__(THREADS) void gatenorm_bwd(GateNormArgs a) {
   using L = Slice<S, TPR, E, VEC>;
   constexpr int R = THREADS / TPR;
@@ -369,8 +369,8 @@ __global__ __launch_bounds__(THREADS) void gatenorm_bwd(GateNormArgs a) {
     if (a.z) L::template st<IO>(row_out<IO>(a.dz, a.sdz, b, t, gr), j, a.d, z);
   }
   if (a.dw)
-    leave_part<IO, S, TPR, E, VEC, R>(
-        static_cast<S*>(a.part) + (blockIdx.x * static_cast<int64_t>(gridDim.y) + blockIdx.y) * a.d, a.d, dw);
+    leave_part<IO, PAR, S, TPR, E, VEC, R>(
+        static_cast<PAR*>(a.part) + (blockIdx.x * static_cast<int64_t>(gridDim.y) + blockIdx.y) * a.d, a.d, dw);
 }
 
 bool addnorm_vec(int io, const AddNormArgs& a, bool bwd) {
@@ -392,29 +392,32 @@ bool gatenorm_vec(int io, const GateNormArgs& a, bool bwd) {
 }
 
 // Threads a row, with eight elements each: 16 to d = 128, 64 to 512, 256 to 2048,
-// 1024 to 8192, and with sixteen each to 16384.
-template <template <int, int, bool, int> class Do, typename... A>
+// 1024 to 8192, and with sixteen each to 16384.  Rows of fewer than eight elements
+// are computed in fp64: w dz - hat mean(w dz hat) all but cancels in some of them (for
+// d = 1 it is eps / (x^2 + eps) of its first term).
+template <template <typename, int, int, bool, int> class Do, typename S, typename... A>
 hipError_t by_width(int d, bool vec, A... args) {
+  if (d < 8) return Do<double, 16, 1, false, 256>::go(args...);
   if (vec) {
-    if (d <= 128) return Do<16, 8, true, 256>::go(args...);
-    if (d <= 512) return Do<64, 8, true, 256>::go(args...);
-    if (d <= 2048) return Do<256, 8, true, 256>::go(args...);
-    if (d <= 8192) return Do<1024, 8, true, 1024>::go(args...);
-    return Do<1024, 16, true, 1024>::go(args...);
+    if (d <= 128) return Do<S, 16, 8, true, 256>::go(args...);
+    if (d <= 512) return Do<S, 64, 8, true, 256>::go(args...);
+    if (d <= 2048) return Do<S, 256, 8, true, 256>::go(args...);
+    if (d <= 8192) return Do<S, 1024, 8, true, 1024>::go(args...);
+    return Do<S, 1024, 16, true, 1024>::go(args...);
   }
-  if (d <= 128) return Do<16, 8, false, 256>::go(args...);
-  if (d <= 512) return Do<64, 8, false, 256>::go(args...);
-  if (d <= 2048) return Do<256, 8, false, 256>::go(args...);
-  if (d <= 8192) return Do<1024, 8, false, 1024>::go(args...);
-  return Do<1024, 16, false, 1024>::go(args...);
+  if (d <= 128) return Do<S, 16, 8, false, 256>::go(args...);
+  if (d <= 512) return Do<S, 64, 8, false, 256>::go(args...);
+  if (d <= 2048) return Do<S, 256, 8, false, 256>::go(args...);
+  if (d <= 8192) return Do<S, 1024, 8, false, 1024>::go(args...);
+  return Do<S, 1024, 16, false, 1024>::go(args...);
 }
 int rows_at_once(int d) { return d <= 128 ? 16 : d <= 512 ? 4 : 1; }
 
 constexpr int64_t kMaxParts = 1024;
 
-template <typename IO, typename RES, typename S>
+template <typename IO, typename RES, typename PAR>
 struct Add {
-  template <int TPR, int E, bool VEC, int TH>
+  template <typename S, int TPR, int E, bool VEC, int TH>
   struct Fwd {
     static hipError_t go(const AddNormArgs& a, hipStream_t s) {
       const int64_t g = (a.B * a.T + TH / TPR - 1) / (TH / TPR);
@@ -422,17 +425,17 @@ struct Add {
       return hipGetLastError();
     }
   };
-  template <int TPR, int E, bool VEC, int TH>
+  template <typename S, int TPR, int E, bool VEC, int TH>
   struct Bwd {
     static hipError_t go(const AddNormArgs& a, hipStream_t s) {
-      addnorm_bwd<IO, RES, S, TPR, E, VEC, TH><<<static_cast<unsigned>(addnorm_parts(a)), TH, 0, s>>>(a);
+      addnorm_bwd<IO, RES, PAR, S, TPR, E, VEC, TH><<<static_cast<unsigned>(addnorm_parts(a)), TH, 0, s>>>(a);
       return hipGetLastError();
     }
   };
 };
-template <typename IO, typename S>
+template <typename IO, typename PAR>
 struct Gate {
-  template <int TPR, int E, bool VEC, int TH>
+  template <typename S, int TPR, int E, bool VEC, int TH>
   struct Fwd {
     static hipError_t go(const GateNormArgs& a, hipStream_t s) {
       const int64_t g = (a.B * a.T * a.G + TH / TPR - 1) / (TH / TPR);
@@ -440,11 +443,11 @@ struct Gate {
       return hipGetLastError();
     }
   };
-  template <int TPR, int E, bool VEC, int TH>
+  template <typename S, int TPR, int E, bool VEC, int TH>
   struct Bwd {
     static hipError_t go(const GateNormArgs& a, hipStream_t s) {
       const dim3 g(static_cast<unsigned>(gatenorm_parts(a)), a.group_w ? a.G : 1);
-      gatenorm_bwd<IO, S, TPR, E, VEC, TH><<<g, TH, 0, s>>>(a);
+      gatenorm_bwd<IO, PAR, S, TPR, E, VEC, TH><<<g, TH, 0, s>>>(a);
       return hipGetLastError();
     }
   };
@@ -452,11 +455,11 @@ struct Gate {
 
 template <typename IO, typename RES, typename S>
 hipError_t add_fwd(int io, const AddNormArgs& a, hipStream_t s) {
-  return by_width<Add<IO, RES, S>::template Fwd>(a.d, addnorm_vec(io, a, false), a, s);
+  return by_width<Add<IO, RES, S>::template Fwd, S>(a.d, addnorm_vec(io, a, false), a, s);
 }
 template <typename IO, typename RES, typename S>
 hipError_t add_bwd(int io, const AddNormArgs& a, hipStream_t s) {
-  return by_width<Add<IO, RES, S>::template Bwd>(a.d, addnorm_vec(io, a, true), a, s);
+  return by_width<Add<IO, RES, S>::template Bwd, S>(a.d, addnorm_vec(io, a, true), a, s);
 }
 
 }  // namespace
@@ -493,17 +496,17 @@ hipError_t launch_addnorm_bwd(int io, const AddNormArgs& a, hipStream_t s) {
 }
 hipError_t launch_gatenorm_fwd(int io, const GateNormArgs& a, hipStream_t s) {
   const bool v = gatenorm_vec(io, a, false);
-  if (io == IO_F64) return by_width<Gate<double, double>::Fwd>(a.d, v, a, s);
-  if (io == IO_F32) return by_width<Gate<float, float>::Fwd>(a.d, v, a, s);
-  return by_width<Gate<bf16, float>::Fwd>(a.d, v, a, s);
+  if (io == IO_F64) return by_width<Gate<double, double>::Fwd, double>(a.d, v, a, s);
+  if (io == IO_F32) return by_width<Gate<float, float>::Fwd, float>(a.d, v, a, s);
+  return by_width<Gate<bf16, float>::Fwd, float>(a.d, v, a, s);
 }
 hipError_t launch_gatenorm_bwd(int io, const GateNormArgs& a, hipStream_t s) {
   const bool v = gatenorm_vec(io, a, true), any = a.B * a.T * a.G > 0;
   hipError_t e = hipSuccess;
   if (any) {
-    if (io == IO_F64) e = by_width<Gate<double, double>::Bwd>(a.d, v, a, s);
-    else if (io == IO_F32) e = by_width<Gate<float, float>::Bwd>(a.d, v, a, s);
-    else e = by_width<Gate<bf16, float>::Bwd>(a.d, v, a, s);
+    if (io == IO_F64) e = by_width<Gate<double, double>::Bwd, double>(a.d, v, a, s);
+    else if (io == IO_F32) e = by_width<Gate<float, float>::Bwd, float>(a.d, v, a, s);
+    else e = by_width<Gate<bf16, float>::Bwd, float>(a.d, v, a, s);
   }
   if (e != hipSuccess) return e;
   const SumOut out[1] = {{a.dw, 1}};
