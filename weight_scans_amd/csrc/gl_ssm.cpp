@@ -179,7 +179,7 @@ gl_status_t plan_ssm(const gl_ssm_desc_t* d, SsmPlan* p) {
   p->par = par_of(d->io_dtype);
   p->elem = elem_of(d->io_dtype);
   const gls::SsmArgs a = ssm_args(d);
-  p->saved = round_up(static_cast<size_t>(gls::chunk_slots(a.packed, a.N, a.T, gls::ssm_ck(d->io_dtype, a.Ns))) * a.D *
+  p->saved = round_up(static_cast<size_t>(gls::chunk_slots(a.packed, a.N, a.T, gls::ssm_ck(d->io_dtype, a))) * a.D *
                       a.Ns * p->par);
   p->bc = round_up(gls::ssm_bc_bytes(d->io_dtype, a));
   p->bwd_ws = p->bc + round_up(static_cast<size_t>(a.N) * (a.Ns + 2) * a.D * p->par);

@@ -113,21 +113,21 @@ struct Sums {
 // the state before the tile and two of the gradient that enters it; y of the tile's tokens.
 template <typename L, bool Z>
 size_t bwd_lds(int N) {
-  return sizeof(typename L::S) * (2 * L::BC + 5 * static_cast<size_t>(L::npad(N)) * L::CH + 2 * L::W * L::CH * 2 * L::NS +
+  return sizeof(typename L::S) * (2 * L::BC + 5 * static_cast<size_t>(L::npad(N)) * L::CH + 4 * L::AGG +
                                   2 * L::W * L::CH * L::NS + (Z ? L::THREADS * L::TT : 0));
 }
 
 template <typename IO, typename L, bool Z>
 __global__ __launch_bounds__(L::THREADS) void ssm_bwd(SsmArgs a) {
   using S = typename L::S;
-  using BC = SlotBC<L>;
-  constexpr int CH = L::CH, TT = L::TT, NS = L::NS, NB = L::NB, W = L::W, K = BC::K;
+  using BC = SlotBC<L, 2>;
+  constexpr int CH = L::CH, TT = L::TT, NS = L::NS, NB = L::NB, W = L::W, BL = BC::BLOCK;
   extern __shared__ __align__(16) char lds[];
   const int np = L::npad(a.Ns);
   S* const sB = reinterpret_cast<S*>(lds);
   S* const sC = sB + L::BC;
-  S* const agg = sC + L::BC;                      // [2][W][CH][2 NS]
-  S* const red = agg + 2 * W * CH * 2 * NS;       // [2][W][CH][NS]
+  S* const agg = sC + L::BC;                      // [2 turns][forward, back][W][CH][2 NS]
+  S* const red = agg + 4 * L::AGG;                // [2][W][CH][NS]
   S* const sA = red + 2 * W * CH * NS;            // [np][CH]
   S* const sdA = sA + np * CH;                    // [np][CH]
   S* const sS = sdA + np * CH;                    // [np][CH]
@@ -178,21 +178,37 @@ __global__ __launch_bounds__(L::THREADS) void ssm_bwd(SsmArgs a) {
     const int left = static_cast<int>(r.len - tile0 < L::TILE ? r.len - tile0 : L::TILE);
     const int here = left - slot * TT;
     S D[TT], u[TT], g[TT], du[TT], dD[TT], sum = S(0);
-    SlotRows<IO, L>(a.x, a.sx, r, p.d0, cc, slot, tile0).ld(left, slot, u);
-    SlotRows<IO, L>(a.dt, a.sdt, r, p.d0, cc, slot, tile0).ld(left, slot, D);
-    SlotRows<IO, L>(a.dy, a.sdy, r, p.d0, cc, slot, tile0).ld(left, slot, g);
-    if constexpr (Z) {
-      S z[TT];
-      SlotRows<IO, L>(a.z, a.sz, r, p.d0, cc, slot, tile0).ld(left, slot, z);
+    TileBC<IO, L> bc;
+    {
+      IO x[TT], dt[TT], dy[TT], z[Z ? TT : 1];
+      SlotRows<IO, L>(a.x, a.sx, r, p.d0, cc, slot, tile0).fetch(left, slot, x);
+      SlotRows<IO, L>(a.dt, a.sdt, r, p.d0, cc, slot, tile0).fetch(left, slot, dt);
+      SlotRows<IO, L>(a.dy, a.sdy, r, p.d0, cc, slot, tile0).fetch(left, slot, dy);
+      if constexpr (Z) SlotRows<IO, L>(a.z, a.sz, r, p.d0, cc, slot, tile0).fetch(left, slot, z);
+      bc.fetch(a, p, r, tile0, left, 0);
 #pragma unroll
-      for (int i = 0; i < TT; ++i) g[i] *= z[i] * sigmoid_(z[i]);
+      for (int i = 0; i < TT; ++i) {
+        u[i] = load_as<S>(&x[i], 0);
+        D[i] = load_as<S>(&dt[i], 0);
+        g[i] = load_as<S>(&dy[i], 0);
+        if constexpr (Z) {
+          const S v = load_as<S>(&z[i], 0);
+          g[i] *= v * sigmoid_(v);
+        }
+      }
     }
-    ssm_steps<S, TT>(a.softplus, bias, in ? here : 0, D);
+    ssm_steps<S, TT>(a.softplus, bias, D);
+    if (left < L::TILE || p.nch < CH) {  // past the end and beside the channels nothing changes
+#pragma unroll
+      for (int i = 0; i < TT; ++i) {
+        const bool there = in && i < here;
+        D[i] = there ? D[i] : S(0);
+        u[i] = there ? u[i] : S(0);
+        g[i] = there ? g[i] : S(0);
+      }
+    }
 #pragma unroll
     for (int i = 0; i < TT; ++i) {
-      const bool there = in && i < here;
-      u[i] = there ? u[i] : S(0);
-      g[i] = there ? g[i] : S(0);
       dskip = fma_(g[i], u[i], dskip);
       if constexpr (Z) sy[i / YV * YV * L::THREADS + i % YV] = skip * u[i];
       u[i] *= D[i];
@@ -201,8 +217,9 @@ __global__ __launch_bounds__(L::THREADS) void ssm_bwd(SsmArgs a) {
       dD[i] = S(0);
     }
     for (int n0 = 0; n0 < np; n0 += NB) {
+      if (n0) bc.fetch(a, p, r, tile0, left, n0);
       __syncthreads();
-      ssm_load_bc<IO, L>(a, p, r, tile0, n0, sB, sC);
+      bc.store(a, p, r, tile0, left, n0, sB, sC);
       for (int i = threadIdx.x; i < NB * CH; i += L::THREADS) {
         const int n = n0 + i / CH, ch = i % CH;
         const bool there = n < a.Ns && ch < p.nch;
@@ -212,101 +229,106 @@ __global__ __launch_bounds__(L::THREADS) void ssm_bwd(SsmArgs a) {
       for (int n1 = 0; n1 < NB; n1 += NS) {
         const int n = n0 + n1;
         if (n >= a.Ns) break;
-        const S* bp = sB + L::at(slot * TT, n1);
-        const S* cp = sC + L::at(slot * TT, n1);
+        BC B(sB + L::at(slot * TT, n1)), C(sC + L::at(slot * TT, n1));
+        B.load(0);
         S A[NS], P[NS], Pb[NS], h[NS], s[NS], enter[NS], e[TT][NS], q[TT][NS];
 #pragma unroll
         for (int j = 0; j < NS; ++j) {
           A[j] = sA[(n + j) * CH + c];
           enter[j] = sS[(n + j) * CH + c];
           P[j] = Pb[j] = exp2_(A[j] * sum);
-          h[j] = S(0);
+          h[j] = s[j] = S(0);
         }
-        // the slot's effect on the state
+        // the slot's effect on the state, and on the gradient that comes from later tokens
 #pragma unroll
-        for (int i = 0; i < TT; i += K) {
-          const BC B(bp, i);
+        for (int i = 0; i < TT; i += BL) {
+          if (i + BL < TT) B.load(i + BL);
+          else C.load(i);
 #pragma unroll
-          for (int k = 0; k < K; ++k)
+          for (int k = i; k < i + BL; ++k)
 #pragma unroll
             for (int j = 0; j < NS; ++j) {
-              e[i + k][j] = exp2_(D[i + k] * A[j]);
-              h[j] = fma_(e[i + k][j], h[j], u[i + k] * B.v[k][j]);
+              e[k][j] = exp2_(D[k] * A[j]);
+              h[j] = fma_(e[k][j], h[j], u[k] * B.at(k, j));
             }
-          if (i % 4 == 0) fence_order();
+          fence_order();
         }
-        ssm_scan<L, false>(P, h, enter, agg, turn);
+#pragma unroll
+        for (int i = TT - BL; i >= 0; i -= BL) {
+          if (i > 0) C.load(i - BL);
+          else B.load(0);
+#pragma unroll
+          for (int k = i + BL - 1; k >= i; --k)
+#pragma unroll
+            for (int j = 0; j < NS; ++j) s[j] = e[k][j] * fma_(C.at(k, j), g[k], s[j]);
+          fence_order();
+        }
+        S* const at = agg + turn * 2 * L::AGG;
+        turn ^= 1;
+        SsmScan<L, false>::leave(P, h, at);
+        SsmScan<L, true>::leave(Pb, s, at + L::AGG);
+        __syncthreads();
+        SsmScan<L, false>::take(P, h, enter, at);
         settle();
         fence_order();
         // the states, and the products that dC sums
         Sums<L, false> sumC(partC + (n / NS) * plane + (tile0 + slot * TT) * NS, c, here);
-        S y[YV];
+        static_assert(YV == BL, "y in the same blocks");
 #pragma unroll
-        for (int i = 0; i < TT; i += K) {
-          const BC B(bp, i), C(cp, i);
-          if constexpr (Z) {
-            if (i % YV == 0) lds_get<S, YV>(sy + i * L::THREADS, y);
+        for (int i = 0; i < TT; i += BL) {
+          if (i + BL < TT) {
+            B.load(i + BL);
+            C.load(i + BL);
           }
+          S y[BL];
+          if constexpr (Z) lds_get<S, BL>(sy + i * L::THREADS, y);
 #pragma unroll
-          for (int k = 0; k < K; ++k) {
+          for (int k = 0; k < BL; ++k) {
             S v[NS];
 #pragma unroll
             for (int j = 0; j < NS; ++j) {
               q[i + k][j] = e[i + k][j] * h[j];
-              h[j] = fma_(u[i + k], B.v[k][j], q[i + k][j]);
-              if constexpr (Z) y[(i + k) % YV] = fma_(C.v[k][j], h[j], y[(i + k) % YV]);
+              h[j] = fma_(u[i + k], B.at(i + k, j), q[i + k][j]);
+              if constexpr (Z) y[k] = fma_(C.at(i + k, j), h[j], y[k]);
               v[j] = g[i + k] * h[j];
             }
             sumC.put(i + k, v);
           }
           if constexpr (Z) {
-            if ((i + K) % YV == 0) {
 #pragma unroll
-              for (int k = 0; k < YV; ++k) sy[(i + K - YV) * L::THREADS + k] = y[k];
-            }
+            for (int k = 0; k < BL; ++k) sy[i * L::THREADS + k] = y[k];
           }
-          if (i % 4 == 0) fence_order();
-        }
-        fence_order();
-        // the slot's effect on the gradient that comes from later tokens
-#pragma unroll
-        for (int j = 0; j < NS; ++j) {
-          s[j] = S(0);
-          enter[j] = sl[(n + j) * CH + c];
+          fence_order();
         }
 #pragma unroll
-        for (int i = TT - K; i >= 0; i -= K) {
-          const BC C(cp, i);
-#pragma unroll
-          for (int k = K - 1; k >= 0; --k)
-#pragma unroll
-            for (int j = 0; j < NS; ++j) s[j] = e[i + k][j] * fma_(C.v[k][j], g[i + k], s[j]);
-          if (i % 4 == 0) fence_order();
-        }
-        ssm_scan<L, true>(Pb, s, enter, agg, turn);
+        for (int j = 0; j < NS; ++j) enter[j] = sl[(n + j) * CH + c];
+        SsmScan<L, true>::take(Pb, s, enter, at + L::AGG);
         fence_order();
         S dA[NS];
 #pragma unroll
         for (int j = 0; j < NS; ++j) dA[j] = S(0);
         Sums<L, true> sumB(partB + (n / NS) * plane + (tile0 + slot * TT) * NS, c, here);
 #pragma unroll
-        for (int i = TT - K; i >= 0; i -= K) {
-          const BC B(bp, i), C(cp, i);
+        for (int i = TT - BL; i >= 0; i -= BL) {
+          if (i > 0) {
+            B.load(i - BL);
+            C.load(i - BL);
+          }
 #pragma unroll
-          for (int k = K - 1; k >= 0; --k) {
+          for (int k = i + BL - 1; k >= i; --k) {
             S v[NS];
 #pragma unroll
             for (int j = 0; j < NS; ++j) {
-              const S gt = fma_(C.v[k][j], g[i + k], s[j]), gq = gt * q[i + k][j];
-              du[i + k] = fma_(gt, B.v[k][j], du[i + k]);
-              dD[i + k] = fma_(gq, A[j], dD[i + k]);
-              dA[j] = fma_(gq, D[i + k], dA[j]);
-              v[j] = gt * u[i + k];
-              s[j] = e[i + k][j] * gt;
+              const S gt = fma_(C.at(k, j), g[k], s[j]), gq = gt * q[k][j];
+              du[k] = fma_(gt, B.at(k, j), du[k]);
+              dD[k] = fma_(gq, A[j], dD[k]);
+              dA[j] = fma_(gq, D[k], dA[j]);
+              v[j] = gt * u[k];
+              s[j] = e[k][j] * gt;
             }
-            sumB.put(i + k, v);
+            sumB.put(k, v);
           }
-          if (i % 4 == 0) fence_order();
+          fence_order();
         }
         if (slot == 0) {
 #pragma unroll
@@ -325,13 +347,18 @@ __global__ __launch_bounds__(L::THREADS) void ssm_bwd(SsmArgs a) {
     S* const other = sl;
     sl = sl1;
     sl1 = other;
-    S x[TT], raw[TT];
-    SlotRows<IO, L>(a.x, a.sx, r, p.d0, cc, slot, tile0).ld(left, slot, x);
-    SlotRows<IO, L>(a.dt, a.sdt, r, p.d0, cc, slot, tile0).ld(left, slot, raw);
+    IO ex[TT], ed[TT], eg[Z ? TT : 1], ez[Z ? TT : 1];
+    SlotRows<IO, L>(a.x, a.sx, r, p.d0, cc, slot, tile0).fetch(left, slot, ex);
+    SlotRows<IO, L>(a.dt, a.sdt, r, p.d0, cc, slot, tile0).fetch(left, slot, ed);
+    if constexpr (Z) {
+      SlotRows<IO, L>(a.dy, a.sdy, r, p.d0, cc, slot, tile0).fetch(left, slot, eg);
+      SlotRows<IO, L>(a.z, a.sz, r, p.d0, cc, slot, tile0).fetch(left, slot, ez);
+    }
     const SlotRows<IO, L> odx(a.dx, a.sdx, r, p.d0, cc, slot, tile0), odt(a.ddt, a.sddt, r, p.d0, cc, slot, tile0);
+    S raw[TT];
     if (a.softplus) {
 #pragma unroll
-      for (int i = 0; i < TT; ++i) raw[i] = sigmoid_(raw[i] + bias);
+      for (int i = 0; i < TT; ++i) raw[i] = sigmoid_(load_as<S>(&ed[i], 0) + bias);
     } else {
 #pragma unroll
       for (int i = 0; i < TT; ++i) raw[i] = S(1);
@@ -339,22 +366,19 @@ __global__ __launch_bounds__(L::THREADS) void ssm_bwd(SsmArgs a) {
 #pragma unroll
     for (int i = 0; i < TT; ++i) {
       if (in && i < here) {
-        const S dd = fma_(dD[i], static_cast<S>(1.0 / kLog2e), x[i] * du[i]) * raw[i];
+        const S dd = fma_(dD[i], static_cast<S>(1.0 / kLog2e), load_as<S>(&ex[i], 0) * du[i]) * raw[i];
         dbias += dd;
         put(odt.out(i), dd);
         put(odx.out(i), fma_(D[i], du[i], skip * g[i]));
       }
     }
     if constexpr (Z) {
-      S z[TT], dy[TT];
-      SlotRows<IO, L>(a.z, a.sz, r, p.d0, cc, slot, tile0).ld(left, slot, z);
-      SlotRows<IO, L>(a.dy, a.sdy, r, p.d0, cc, slot, tile0).ld(left, slot, dy);
       const SlotRows<IO, L> odz(a.dz, a.sdz, r, p.d0, cc, slot, tile0);
 #pragma unroll
       for (int i = 0; i < TT; ++i) {
-        const S k = sigmoid_(z[i]);
+        const S z = load_as<S>(&ez[i], 0), k = sigmoid_(z);
         const S y = sy[i / YV * YV * L::THREADS + i % YV];
-        if (in && i < here) put(odz.out(i), dy[i] * y * (k * (S(1) + z[i] * (S(1) - k))));
+        if (in && i < here) put(odz.out(i), load_as<S>(&eg[i], 0) * y * (k * (S(1) + z * (S(1) - k))));
       }
     }
   }
@@ -452,7 +476,7 @@ hipError_t go(int io, const SsmArgs& a, hipStream_t s) {
 
 template <typename IO, typename S, int TT>
 hipError_t by_states(int io, const SsmArgs& a, hipStream_t s) {
-  switch (ssm_bwd_channels(io, a.Ns)) {
+  switch (ssm_bwd_channels(io, a)) {
     case 32: return go<IO, SsmTile<S, 32, 8, TT, kNS, 16>>(io, a, s);
     case 16: return go<IO, SsmTile<S, 16, 8, TT, kNS, 8>>(io, a, s);
     default: return go<IO, SsmTile<S, 8, 8, TT, kNS, sizeof(S) == 8 ? 4 : 8>>(io, a, s);
@@ -461,10 +485,16 @@ hipError_t by_states(int io, const SsmArgs& a, hipStream_t s) {
 
 }  // namespace
 
-size_t ssm_bc_bytes(int io, const SsmArgs& a) {
-  const int64_t blocks = ssm_blocks(a, ssm_bwd_channels(io, a.Ns));
-  return static_cast<size_t>(2 * blocks) * ((a.Ns + kNS - 1) / kNS * kNS) * a.B * a.T * (io == IO_F64 ? 8 : 4);
+static size_t bc_bytes(int io, const SsmArgs& a, int CH) {
+  return static_cast<size_t>(2 * ssm_blocks(a, CH)) * ((a.Ns + kNS - 1) / kNS * kNS) * a.B * a.T * (io == IO_F64 ? 8 : 4);
 }
+int ssm_bwd_channels(int io, const SsmArgs& a) {
+  const int n = io == IO_F64 ? 2 * a.Ns : a.Ns;
+  int CH = n <= 64 ? 32 : n <= 128 ? 16 : 8;
+  while (CH > 8 && a.N * ssm_blocks(a, CH) < 256 && bc_bytes(io, a, CH / 2) < (size_t(1) << 30)) CH /= 2;
+  return CH;
+}
+size_t ssm_bc_bytes(int io, const SsmArgs& a) { return bc_bytes(io, a, ssm_bwd_channels(io, a)); }
 hipError_t launch_ssm_bwd(int io, const SsmArgs& a, hipStream_t s) {
   if (io == IO_F64) return by_states<double, double, 8>(io, a, s);
   if (io == IO_F32) return by_states<float, float, 16>(io, a, s);

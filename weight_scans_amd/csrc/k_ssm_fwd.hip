@@ -18,14 +18,14 @@ namespace {
 template <typename IO, typename L, bool Z>
 __global__ __launch_bounds__(L::THREADS) void ssm_fwd(SsmArgs a, int ck) {
   using S = typename L::S;
-  using BC = SlotBC<L>;
-  constexpr int CH = L::CH, TT = L::TT, NS = L::NS, NB = L::NB, K = BC::K;
+  using BC = SlotBC<L, 1>;
+  constexpr int CH = L::CH, TT = L::TT, NS = L::NS, NB = L::NB, BL = BC::BLOCK;
   extern __shared__ __align__(16) char lds[];
   const int np = L::npad(a.Ns);
   S* const sB = reinterpret_cast<S*>(lds);
   S* const sC = sB + L::BC;
   S* const agg = sC + L::BC;                     // [2][W][CH][2 NS]
-  S* const sA = agg + 2 * L::W * CH * 2 * NS;    // [np][CH]
+  S* const sA = agg + 2 * L::AGG;                // [np][CH]
   S* sh = sA + np * CH;                          // [2][np][CH]
   const SsmPlace p = ssm_place(a, CH, xcd_order(blockIdx.x, gridDim.x));
   const SeqRange r = seq_range(a.cu, p.n, a.T);
@@ -49,24 +49,41 @@ __global__ __launch_bounds__(L::THREADS) void ssm_fwd(SsmArgs a, int ck) {
     const int left = static_cast<int>(r.len - tile0 < L::TILE ? r.len - tile0 : L::TILE);
     const int here = left - slot * TT;  // the slot's tokens that are there, if positive
     S D[TT], u[TT], y[TT], sum = S(0);
-    SlotRows<IO, L>(a.x, a.sx, r, p.d0, cc, slot, tile0).ld(left, slot, u);
-    SlotRows<IO, L>(a.dt, a.sdt, r, p.d0, cc, slot, tile0).ld(left, slot, D);
-    ssm_steps<S, TT>(a.softplus, bias, here, D);
+    TileBC<IO, L> bc;
+    {
+      IO x[TT], dt[TT];
+      SlotRows<IO, L>(a.x, a.sx, r, p.d0, cc, slot, tile0).fetch(left, slot, x);
+      SlotRows<IO, L>(a.dt, a.sdt, r, p.d0, cc, slot, tile0).fetch(left, slot, dt);
+      bc.fetch(a, p, r, tile0, left, 0);
+#pragma unroll
+      for (int i = 0; i < TT; ++i) {
+        u[i] = load_as<S>(&x[i], 0);
+        D[i] = load_as<S>(&dt[i], 0);
+      }
+    }
+    ssm_steps<S, TT>(a.softplus, bias, D);
+    if (left < L::TILE) {  // past the end nothing changes
+#pragma unroll
+      for (int i = 0; i < TT; ++i) {
+        D[i] = i < here ? D[i] : S(0);
+        u[i] = i < here ? u[i] : S(0);
+      }
+    }
 #pragma unroll
     for (int i = 0; i < TT; ++i) {
-      u[i] = i < here ? u[i] : S(0);
       y[i] = skip * u[i];
       u[i] *= D[i];
       sum += D[i];
     }
+    const bool work = left > wave * (L::TS * TT);  // a wave past the end only hands on
     for (int n0 = 0; n0 < np; n0 += NB) {
+      if (n0) bc.fetch(a, p, r, tile0, left, n0);
       __syncthreads();
-      ssm_load_bc<IO, L>(a, p, r, tile0, n0, sB, sC);
+      bc.store(a, p, r, tile0, left, n0, sB, sC);
       __syncthreads();
       for (int n1 = 0; n1 < NB; n1 += NS) {
         if (n0 + n1 >= a.Ns) break;
-        const S* bp = sB + L::at(slot * TT, n1);
-        const S* cp = sC + L::at(slot * TT, n1);
+        BC B(sB + L::at(slot * TT, n1)), C(sC + L::at(slot * TT, n1));
         S A[NS], P[NS], h[NS], h0[NS], e[TT][NS];
 #pragma unroll
         for (int j = 0; j < NS; ++j) {
@@ -75,19 +92,25 @@ __global__ __launch_bounds__(L::THREADS) void ssm_fwd(SsmArgs a, int ck) {
           h[j] = S(0);
           h0[j] = sh[(n0 + n1 + j) * CH + c];
         }
+        if (work) {
 #pragma unroll
-        for (int i = 0; i < TT; i += K) {
-          const BC B(bp, i);
+          for (int i = 0; i < TT; i += BL) {
+            B.load(i);
 #pragma unroll
-          for (int k = 0; k < K; ++k)
+            for (int k = i; k < i + BL; ++k)
 #pragma unroll
-            for (int j = 0; j < NS; ++j) {
-              e[i + k][j] = exp2_(D[i + k] * A[j]);
-              h[j] = fma_(e[i + k][j], h[j], u[i + k] * B.v[k][j]);
-            }
-          if (i % 4 == 0) fence_order();
+              for (int j = 0; j < NS; ++j) {
+                e[k][j] = exp2_(D[k] * A[j]);
+                h[j] = fma_(e[k][j], h[j], u[k] * B.at(k, j));
+              }
+            fence_order();
+          }
         }
-        ssm_scan<L, false>(P, h, h0, agg, turn);
+        S* const at = agg + turn * L::AGG;
+        turn ^= 1;
+        SsmScan<L, false>::leave(P, h, at);
+        __syncthreads();
+        SsmScan<L, false>::take(P, h, h0, at);
         if (a.ckpt && in && here > 0 && (tile0 + slot * TT) % ck == 0) {
           S* o = static_cast<S*>(a.ckpt) + ((ck0 + (tile0 + slot * TT) / ck) * a.Ns + n0 + n1) * a.D + d;
 #pragma unroll
@@ -95,17 +118,20 @@ __global__ __launch_bounds__(L::THREADS) void ssm_fwd(SsmArgs a, int ck) {
             if (n0 + n1 + j < a.Ns) o[static_cast<int64_t>(j) * a.D] = h[j];
         }
         fence_order();
+        if (work) {
 #pragma unroll
-        for (int i = 0; i < TT; i += K) {
-          const BC B(bp, i), C(cp, i);
+          for (int i = 0; i < TT; i += BL) {
+            B.load(i);
+            C.load(i);
 #pragma unroll
-          for (int k = 0; k < K; ++k)
+            for (int k = i; k < i + BL; ++k)
 #pragma unroll
-            for (int j = 0; j < NS; ++j) {
-              h[j] = fma_(e[i + k][j], h[j], u[i + k] * B.v[k][j]);
-              y[i + k] = fma_(C.v[k][j], h[j], y[i + k]);
-            }
-          if (i % 4 == 0) fence_order();
+              for (int j = 0; j < NS; ++j) {
+                h[j] = fma_(e[k][j], h[j], u[k] * B.at(k, j));
+                y[k] = fma_(C.at(k, j), h[j], y[k]);
+              }
+            fence_order();
+          }
         }
         if (slot == L::SL - 1) {
 #pragma unroll
@@ -116,15 +142,23 @@ __global__ __launch_bounds__(L::THREADS) void ssm_fwd(SsmArgs a, int ck) {
     S* const other = sh;
     sh = sh1;
     sh1 = other;
+    IO raw[Z ? TT : 1];
+    if constexpr (Z) SlotRows<IO, L>(a.z, a.sz, r, p.d0, cc, slot, tile0).fetch(left, slot, raw);
     if (!a.y) continue;
     if constexpr (Z) {
-      S z[TT];
-      SlotRows<IO, L>(a.z, a.sz, r, p.d0, cc, slot, tile0).ld(left, slot, z);
 #pragma unroll
-      for (int i = 0; i < TT; ++i) y[i] *= z[i] * sigmoid_(z[i]);
+      for (int i = 0; i < TT; ++i) {
+        const S z = load_as<S>(&raw[i], 0);
+        y[i] *= z * sigmoid_(z);
+      }
     }
     const SlotRows<IO, L> out(a.y, a.sy, r, p.d0, cc, slot, tile0);
-    if (in) {
+    if (left >= L::TILE) {
+      if (in) {
+#pragma unroll
+        for (int i = 0; i < TT; ++i) put(out.out(i), y[i]);
+      }
+    } else if (in) {
 #pragma unroll
       for (int i = 0; i < TT; ++i)
         if (i < here) put(out.out(i), y[i]);
@@ -145,8 +179,8 @@ hipError_t go(int io, const SsmArgs& a, hipStream_t s) {
   if (g == 0) return hipSuccess;
   SsmArgs b = a;
   b.vec_bc = ssm_vec_bc(io, a);
-  if (a.z) ssm_fwd<IO, L, true><<<static_cast<unsigned>(g), L::THREADS, L::lds(a.Ns), s>>>(b, ssm_ck(io, a.Ns));
-  else ssm_fwd<IO, L, false><<<static_cast<unsigned>(g), L::THREADS, L::lds(a.Ns), s>>>(b, ssm_ck(io, a.Ns));
+  if (a.z) ssm_fwd<IO, L, true><<<static_cast<unsigned>(g), L::THREADS, L::lds(a.Ns), s>>>(b, ssm_ck(io, a));
+  else ssm_fwd<IO, L, false><<<static_cast<unsigned>(g), L::THREADS, L::lds(a.Ns), s>>>(b, ssm_ck(io, a));
   return hipGetLastError();
 }
 
@@ -155,12 +189,13 @@ template <typename IO, typename S, int TT, int NS>
 hipError_t by_channels(int io, const SsmArgs& a, hipStream_t s) {
   if (a.N * ssm_blocks(a, 64) >= 256 && a.Ns <= 64) return go<IO, SsmTile<S, 64, 8, TT, NS, 16>>(io, a, s);
   if (a.N * ssm_blocks(a, 32) >= 256 && a.Ns <= 128) return go<IO, SsmTile<S, 32, 8, TT, NS, 16>>(io, a, s);
-  return go<IO, SsmTile<S, 16, 8, TT, NS, 8>>(io, a, s);
+  if (a.N * ssm_blocks(a, 16) >= 256) return go<IO, SsmTile<S, 16, 8, TT, NS, 8>>(io, a, s);
+  return go<IO, SsmTile<S, 8, 8, TT, NS, 8>>(io, a, s);
 }
 
 }  // namespace
 
-int ssm_ck(int io, int Ns) { return (io == IO_F64 ? 8 : 16) * 8 * (64 / ssm_bwd_channels(io, Ns)); }
+int ssm_ck(int io, const SsmArgs& a) { return (io == IO_F64 ? 8 : 16) * 8 * (64 / ssm_bwd_channels(io, a)); }
 
 hipError_t launch_ssm_fwd(int io, const SsmArgs& a, hipStream_t s) {
   if (io == IO_F64) return by_channels<double, double, 8, 2>(io, a, s);

@@ -82,14 +82,16 @@ struct SsmArgs {
   Rows sx{}, sdt{}, sz{}, sB{}, sC{}, sy{};
   Rows sdy{}, sdx{}, sddt{}, sdz{}, sdB{}, sdC{};
 };
-// Channels a work-group of the backward, and the tokens of its tiles: a forward that
-// trains keeps the state before each.
-// (As many as leave the LDS room for N states of each.)
-inline int ssm_bwd_channels(int io, int Ns) {
-  const int n = io == IO_F64 ? 2 * Ns : Ns;
-  return n <= 64 ? 32 : n <= 128 ? 16 : 8;
+inline int64_t ssm_blocks(const SsmArgs& a, int CH) {
+  const int dg = a.D / a.G;
+  return static_cast<int64_t>((dg + CH - 1) / CH) * a.G;
 }
-int ssm_ck(int io, int Ns);
+// Channels a work-group of the backward: as many as leave the LDS room for N states of
+// each, fewer (not under 8) where that gives work to more of the 256 CUs and the parts of
+// the sums over channels, which grow, stay under a gigabyte.  A forward that trains
+// keeps the states before its tiles, of ssm_ck tokens.
+int ssm_bwd_channels(int io, const SsmArgs& a);
+int ssm_ck(int io, const SsmArgs& a);
 size_t ssm_bc_bytes(int io, const SsmArgs& a);
 hipError_t launch_ssm_fwd(int io, const SsmArgs& a, hipStream_t s);
 hipError_t launch_ssm_bwd(int io, const SsmArgs& a, hipStream_t s);

@@ -36,10 +36,11 @@ struct SsmTile {
     return n / NS * GROUP + token * NS + token / TT * PAD + n % NS;
   }
   __host__ __device__ static constexpr int npad(int N) { return (N + NB - 1) / NB * NB; }
+  static constexpr int AGG = W * CH * 2 * NS;
   // LDS: B, C of the tile; A log2 e and the state that enters it (two: this tile's and the
   // next one's) per channel; what the waves pass on (two turns of (P, H))
   static size_t lds(int N) {
-    return sizeof(S) * (2 * BC + 3 * static_cast<size_t>(npad(N)) * CH + 2 * W * CH * 2 * NS);
+    return sizeof(S) * (2 * BC + 3 * static_cast<size_t>(npad(N)) * CH + 2 * AGG);
   }
 };
 
@@ -60,11 +61,6 @@ __device__ __forceinline__ SsmPlace ssm_place(const SsmArgs& a, int CH, int64_t 
   p.n = i / blocks;
   return p;
 }
-inline int64_t ssm_blocks(const SsmArgs& a, int CH) {
-  const int dg = a.D / a.G;
-  return static_cast<int64_t>((dg + CH - 1) / CH) * a.G;
-}
-
 // A tensor of rows as a work-group reads it: one base for the tile (the same in all
 // lanes, so that it is kept and moved on by the scalar unit), and the lane's offset
 // in bytes, which stays (below 2^32: the host bounds the strides).
@@ -82,19 +78,21 @@ struct SlotRows {
     // loop over the tiles, are more than the scalar registers
     asm volatile("" : "+s"(step));
   }
-  // The lane's TT tokens of a tile that has `left` (past its end: the last one again).
-  template <typename S>
-  __device__ __forceinline__ void ld(int left, int slot, S (&v)[L::TT]) const {
+  // The lane's TT tokens of a tile that has `left` (past its end: the last one again), as
+  // they lie in memory: what is not yet converted is not yet waited for.
+  template <int n>
+  __device__ __forceinline__ void fetch(int left, int slot, IO (&v)[n]) const {
+    static_assert(n == L::TT, "a slot's tokens");
     if (left >= L::TILE) {
 #pragma unroll
-      for (int i = 0; i < L::TT; ++i) v[i] = load_as<S>(reinterpret_cast<const IO*>(base + i * step + off), 0);
+      for (int i = 0; i < L::TT; ++i) v[i] = *reinterpret_cast<const IO*>(base + i * step + off);
     } else {
       int first = slot * L::TT;
       asm volatile("" : "+v"(first));  // likewise: not kept for the next use
 #pragma unroll
       for (int i = 0; i < L::TT; ++i) {
         const int tok = min(first + i, left - 1);
-        v[i] = load_as<S>(reinterpret_cast<const IO*>(base + static_cast<uint32_t>(tok) * step + col), 0);
+        v[i] = *reinterpret_cast<const IO*>(base + static_cast<uint32_t>(tok) * step + col);
       }
     }
   }
@@ -103,9 +101,9 @@ struct SlotRows {
   }
 };
 
-// D of the slot's tokens from dt and its bias; zero, as nothing then changes, past its end.
+// D of the slot's tokens from dt and its bias.
 template <typename S, int TT>
-__device__ __forceinline__ void ssm_steps(bool softplus, S bias, int here, S (&D)[TT]) {
+__device__ __forceinline__ void ssm_steps(bool softplus, S bias, S (&D)[TT]) {
   if (softplus) {
 #pragma unroll
     for (int i = 0; i < TT; ++i) D[i] = softplus_(D[i] + bias);
@@ -113,8 +111,6 @@ __device__ __forceinline__ void ssm_steps(bool softplus, S bias, int here, S (&D
 #pragma unroll
     for (int i = 0; i < TT; ++i) D[i] += bias;
   }
-#pragma unroll
-  for (int i = 0; i < TT; ++i) D[i] = i < here ? D[i] : S(0);
 }
 
 inline bool ssm_vec_bc(int io, const SsmArgs& a) {
@@ -122,55 +118,65 @@ inline bool ssm_vec_bc(int io, const SsmArgs& a) {
 }
 
 // B and C of states n0 .. n0 + NB - 1 for the tile's tokens into LDS, zero past N and
-// past the sequence; in vectors where rows begin on 16 bytes and N is whole vectors.
+// past the sequence: `fetch` asks for them (in vectors, where rows begin on 16 bytes
+// and N is whole vectors), `store` puts them there.
 template <typename IO, typename L>
-__device__ __forceinline__ void ssm_load_bc(const SsmArgs& a, const SsmPlace& p, const SeqRange& r, int64_t tile0, int n0,
-                                            typename L::S* sB, typename L::S* sC) {
+struct TileBC {
   using S = typename L::S;
-  const IO* B = static_cast<const IO*>(a.Bm) + r.b * a.sB.b + (r.t0 + tile0) * a.sB.t + p.g * a.sB.g + n0;
-  const IO* C = static_cast<const IO*>(a.Cm) + r.b * a.sC.b + (r.t0 + tile0) * a.sC.t + p.g * a.sC.g + n0;
-  const int left = static_cast<int>(r.len - tile0 < L::TILE ? r.len - tile0 : L::TILE), states = a.Ns - n0;
-  constexpr int V = Vec<IO>::n < L::NB ? Vec<IO>::n : L::NB;
-  if (a.vec_bc) {
-    constexpr int per = L::TILE * L::NB / V;
-    constexpr int rounds = (per + L::THREADS - 1) / L::THREADS;
-    S b[rounds][V], c[rounds][V];
+  static constexpr int V = Vec<IO>::n < L::NB ? Vec<IO>::n : L::NB;
+  static constexpr int PER = L::TILE * L::NB / V, ROUNDS = (PER + L::THREADS - 1) / L::THREADS;
+  uint4 b[ROUNDS], c[ROUNDS];
+
+  __device__ static __forceinline__ const IO* first(const void* p, const Rows& s, const SsmPlace& w, const SeqRange& r,
+                                                    int64_t tile0, int n0) {
+    return static_cast<const IO*>(p) + r.b * s.b + (r.t0 + tile0) * s.t + w.g * s.g + n0;
+  }
+  __device__ __forceinline__ void fetch(const SsmArgs& a, const SsmPlace& w, const SeqRange& r, int64_t tile0, int left, int n0) {
+    if (!a.vec_bc) return;
+    const IO *B = first(a.Bm, a.sB, w, r, tile0, n0), *C = first(a.Cm, a.sC, w, r, tile0, n0);
+    const int states = a.Ns - n0;
 #pragma unroll
-    for (int k = 0; k < rounds; ++k) {
-      const int i = k * L::THREADS + threadIdx.x, tok = i * V / L::NB, nn = i * V % L::NB;
+    for (int k = 0; k < ROUNDS; ++k) {
+      const int i = (k * L::THREADS + threadIdx.x) * V, tok = i / L::NB, nn = i % L::NB;
       const bool in = tok < left && nn < states;
       const int64_t tc = in ? tok : 0, nc = in ? nn : 0;
-      load_w<IO, S, V>(B + tc * a.sB.t + nc, b[k]);
-      load_w<IO, S, V>(C + tc * a.sC.t + nc, c[k]);
-#pragma unroll
-      for (int e = 0; e < V; ++e) {
-        b[k][e] = in ? b[k][e] : S(0);
-        c[k][e] = in ? c[k][e] : S(0);
-      }
+      b[k] = *reinterpret_cast<const uint4*>(B + tc * a.sB.t + nc);
+      c[k] = *reinterpret_cast<const uint4*>(C + tc * a.sC.t + nc);
     }
+  }
+  __device__ __forceinline__ void store(const SsmArgs& a, const SsmPlace& w, const SeqRange& r, int64_t tile0, int left, int n0,
+                                        S* sB, S* sC) const {
+    const int states = a.Ns - n0;
+    if (a.vec_bc) {
 #pragma unroll
-    for (int k = 0; k < rounds; ++k) {
-      const int i = k * L::THREADS + threadIdx.x, tok = i * V / L::NB, nn = i * V % L::NB;
-      if (per % L::THREADS == 0 || i < per) {
+      for (int k = 0; k < ROUNDS; ++k) {
+        const int i = (k * L::THREADS + threadIdx.x) * V, tok = i / L::NB, nn = i % L::NB;
+        const bool in = tok < left && nn < states;
+        S vb[Vec<IO>::n], vc[Vec<IO>::n];
+        Vec<IO>::ld(reinterpret_cast<const IO*>(&b[k]), vb);
+        Vec<IO>::ld(reinterpret_cast<const IO*>(&c[k]), vc);
+        if (PER % L::THREADS == 0 || k * L::THREADS + static_cast<int>(threadIdx.x) < PER) {
 #pragma unroll
-        for (int e = 0; e < V; ++e) {
-          sB[L::at(tok, nn + e)] = b[k][e];
-          sC[L::at(tok, nn + e)] = c[k][e];
+          for (int e = 0; e < V; ++e) {
+            sB[L::at(tok, nn + e)] = in ? vb[e] : S(0);
+            sC[L::at(tok, nn + e)] = in ? vc[e] : S(0);
+          }
         }
       }
+      return;
     }
-    return;
-  }
+    const IO *B = first(a.Bm, a.sB, w, r, tile0, n0), *C = first(a.Cm, a.sC, w, r, tile0, n0);
 #pragma unroll 4
-  for (int k = 0; k < L::TILE * L::NB / L::THREADS; ++k) {
-    const int i = k * L::THREADS + threadIdx.x, tok = i / L::NB, nn = i % L::NB;
-    const bool in = tok < left && nn < states;
-    const int64_t tc = in ? tok : 0, nc = in ? nn : 0;
-    const S b = load_as<S>(B, tc * a.sB.t + nc), c = load_as<S>(C, tc * a.sC.t + nc);
-    sB[L::at(tok, nn)] = in ? b : S(0);
-    sC[L::at(tok, nn)] = in ? c : S(0);
+    for (int k = 0; k < L::TILE * L::NB / L::THREADS; ++k) {
+      const int i = k * L::THREADS + threadIdx.x, tok = i / L::NB, nn = i % L::NB;
+      const bool in = tok < left && nn < states;
+      const int64_t tc = in ? tok : 0, nc = in ? nn : 0;
+      const S vb = load_as<S>(B, tc * a.sB.t + nc), vc = load_as<S>(C, tc * a.sC.t + nc);
+      sB[L::at(tok, nn)] = in ? vb : S(0);
+      sC[L::at(tok, nn)] = in ? vc : S(0);
+    }
   }
-}
+};
 
 template <typename S, int NS>
 __device__ __forceinline__ void lds_get(const S* p, S (&v)[NS]) {
@@ -186,118 +192,133 @@ __device__ __forceinline__ void lds_get(const S* p, S (&v)[NS]) {
   }
 }
 
-// NS values of each of K = 16 bytes / NS tokens from token i on.
-template <typename L>
+// A slot's B or C of one state group, four tokens at a time (two in fp64).  BUFS = 2:
+// the next block is on its way while one is used.
+template <typename L, int BUFS>
 struct SlotBC {
   using S = typename L::S;
-  static constexpr int K = 16 / (sizeof(S) * L::NS);
-  S v[K][L::NS];
-  __device__ __forceinline__ SlotBC(const S* p, int i) {
-    const uint4 t = *reinterpret_cast<const uint4*>(p + i * L::NS);
-    __builtin_memcpy(v, &t, 16);
+  static constexpr int BLOCK = 16 / sizeof(S);
+  static_assert(L::TT % BLOCK == 0, "whole blocks");
+  const S* p;
+  S v[BUFS][BLOCK][L::NS];
+  __device__ __forceinline__ explicit SlotBC(const S* first) : p(first) {}
+  __device__ __forceinline__ void load(int i) {  // tokens i .. i + BLOCK - 1
+    const uint4* s = reinterpret_cast<const uint4*>(p + i * L::NS);
+    uint4 t[L::NS];
+#pragma unroll
+    for (int k = 0; k < L::NS; ++k) t[k] = s[k];
+    __builtin_memcpy(v[i / BLOCK % BUFS], t, sizeof(t));
   }
+  __device__ __forceinline__ S at(int i, int j) const { return v[i / BLOCK % BUFS][i % BLOCK][j]; }
 };
 
-// The lanes' values of the other half of the wave: a from lanes 0..31, b from 32..63.
-template <typename S>
-__device__ __forceinline__ void halves(S x, S& lo, S& hi) {
-  if constexpr (sizeof(S) == 4) {
+// x of the lower and of the upper of the two groups of m lanes that a lane's pair of groups
+// is (m = 8, 16 or 32), lane by lane.
+template <int m, typename S>
+__device__ __forceinline__ void pair_of(S x, S& lo, S& hi) {
+  if constexpr (sizeof(S) == 4 && m == 32) {
     const auto r = __builtin_amdgcn_permlane32_swap(__float_as_uint(x), __float_as_uint(x), false, false);
     lo = __uint_as_float(r[0]);
     hi = __uint_as_float(r[1]);
+  } else if constexpr (sizeof(S) == 4 && m == 16) {
+    const auto r = __builtin_amdgcn_permlane16_swap(__float_as_uint(x), __float_as_uint(x), false, false);
+    lo = __uint_as_float(r[0]);
+    hi = __uint_as_float(r[1]);
+  } else if constexpr (sizeof(S) == 4 && m == 8) {
+    const float o = __uint_as_float(__builtin_amdgcn_update_dpp(0, __float_as_uint(x), 0x128, 0xf, 0xf, true));  // row_ror:8
+    const bool up = threadIdx.x & 8;
+    lo = up ? o : x;
+    hi = up ? x : o;
   } else {
-    const int l = threadIdx.x & 31;
-    lo = __shfl(x, l, 64);
-    hi = __shfl(x, l + 32, 64);
+    const S o = __shfl_xor(x, m, 64);
+    const bool up = threadIdx.x & m;
+    lo = up ? o : x;
+    hi = up ? x : o;
   }
 }
 
-// Scan over the slots of (P, H), forward or (BACK) from the last slot: on return
-// H is what enters the lane's slot, given that h enters the tile's first (last).
-// One barrier; agg is [2][W][CH][2 NS], `turn` changes with every call.
+// Scan over the slots of (P, H), forward or (BACK) from the last slot, in two halves with
+// a barrier of the caller between them: `leave` composes a wave's slots and leaves the
+// whole in LDS; `take` returns in H what enters the lane's slot, given that h enters
+// the tile's first (last).  agg: [W][CH][2 NS].
 template <typename L, bool BACK>
-__device__ __forceinline__ void ssm_scan(typename L::S (&P)[L::NS], typename L::S (&H)[L::NS], typename L::S (&h)[L::NS],
-                                         typename L::S* agg, int& turn) {
+struct SsmScan {
   using S = typename L::S;
-  constexpr int CH = L::CH, TS = L::TS, W = L::W, NS = L::NS;
-  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), c = lane % CH;
-  const int ts = BACK ? TS - 1 - lane / CH : lane / CH;  // order of the scan
-  S* const mine = agg + ((turn * W + wave) * CH + c) * 2 * NS;
-  S wp[NS], wh[NS];  // of the whole wave, in the lanes that hold it
-  if constexpr (TS == 2) {
+  static constexpr int CH = L::CH, TS = L::TS, W = L::W, NS = L::NS;
+
+  __device__ static __forceinline__ int order(int lane) { return BACK ? TS - 1 - lane / CH : lane / CH; }
+
+  __device__ static __forceinline__ void leave(S (&P)[NS], S (&H)[NS], S* agg) {
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+    S pe[NS], he[NS];  // of the slots before the lane's
 #pragma unroll
     for (int j = 0; j < NS; ++j) {
-      S p0, p1, h0, h1;
-      if constexpr (BACK) {
-        halves(P[j], p1, p0);
-        halves(H[j], h1, h0);
-      } else {
-        halves(P[j], p0, p1);
-        halves(H[j], h0, h1);
-      }
-      wp[j] = p0 * p1;
-      wh[j] = fma_(p1, h0, h1);
-      P[j] = ts ? p0 : S(1);
-      H[j] = ts ? h0 : S(0);
+      pe[j] = S(1);
+      he[j] = S(0);
     }
-  } else {
-#pragma unroll
-    for (int m = 1; m < TS; m <<= 1) {
+    level<CH>(P, H, pe, he);  // P, H: now of the whole wave
+    if (order(lane) == TS - 1) {
+      S* const mine = agg + (wave * CH + lane % CH) * 2 * NS;
 #pragma unroll
       for (int j = 0; j < NS; ++j) {
-        const S p = BACK ? __shfl_down(P[j], m * CH, 64) : __shfl_up(P[j], m * CH, 64);
-        const S q = BACK ? __shfl_down(H[j], m * CH, 64) : __shfl_up(H[j], m * CH, 64);
-        if (ts >= m) {
-          H[j] = fma_(P[j], q, H[j]);
-          P[j] *= p;
+        mine[j] = P[j];
+        mine[NS + j] = H[j];
+      }
+    }
+#pragma unroll
+    for (int j = 0; j < NS; ++j) {
+      P[j] = pe[j];
+      H[j] = he[j];
+    }
+  }
+
+  // Groups of m lanes into groups of 2 m.
+  template <int m>
+  __device__ static __forceinline__ void level(S (&P)[NS], S (&H)[NS], S (&pe)[NS], S (&he)[NS]) {
+    if constexpr (m < 64) {
+      const bool second = ((threadIdx.x & m) != 0) != BACK;
+#pragma unroll
+      for (int j = 0; j < NS; ++j) {
+        S p0, p1, h0, h1;
+        if constexpr (BACK) {
+          pair_of<m>(P[j], p1, p0);
+          pair_of<m>(H[j], h1, h0);
+        } else {
+          pair_of<m>(P[j], p0, p1);
+          pair_of<m>(H[j], h0, h1);
         }
+        he[j] = second ? fma_(pe[j], h0, he[j]) : he[j];
+        pe[j] = second ? pe[j] * p0 : pe[j];
+        P[j] = p0 * p1;
+        H[j] = fma_(p1, h0, h1);
+      }
+      level<2 * m>(P, H, pe, he);
+    }
+  }
+
+  __device__ static __forceinline__ void take(const S (&P)[NS], S (&H)[NS], S (&h)[NS], const S* agg) {
+    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int before = BACK ? W - 1 - wave : wave;  // waves, in order
+    S p[W - 1][NS], q[W - 1][NS];
+#pragma unroll
+    for (int k = 0; k < W - 1; ++k) {
+      const int w = BACK ? W - 1 - k : k;
+      const S* o = agg + (w * CH + lane % CH) * 2 * NS;
+      if (k < before) {
+        lds_get<S, NS>(o, p[k]);
+        lds_get<S, NS>(o + NS, q[k]);
       }
     }
 #pragma unroll
-    for (int j = 0; j < NS; ++j) {
-      wp[j] = P[j];
-      wh[j] = H[j];
-      if constexpr (TS > 1) {
-        const S p = BACK ? __shfl_down(P[j], CH, 64) : __shfl_up(P[j], CH, 64);
-        const S q = BACK ? __shfl_down(H[j], CH, 64) : __shfl_up(H[j], CH, 64);
-        P[j] = ts ? p : S(1);
-        H[j] = ts ? q : S(0);
-      } else {
-        P[j] = S(1);
-        H[j] = S(0);
+    for (int k = 0; k < W - 1; ++k)
+      if (k < before) {
+#pragma unroll
+        for (int j = 0; j < NS; ++j) h[j] = fma_(p[k][j], h[j], q[k][j]);
       }
-    }
+#pragma unroll
+    for (int j = 0; j < NS; ++j) H[j] = fma_(P[j], h[j], H[j]);
   }
-  if (ts == TS - 1) {
-#pragma unroll
-    for (int j = 0; j < NS; ++j) {
-      mine[j] = wp[j];
-      mine[NS + j] = wh[j];
-    }
-  }
-  __syncthreads();
-  // the waves before, in order
-  const int before = BACK ? W - 1 - wave : wave;
-  S p[W - 1][NS], q[W - 1][NS];
-#pragma unroll
-  for (int k = 0; k < W - 1; ++k) {
-    const int w = BACK ? W - 1 - k : k;
-    const S* o = agg + ((turn * W + w) * CH + c) * 2 * NS;
-    if (k < before) {
-      lds_get<S, NS>(o, p[k]);
-      lds_get<S, NS>(o + NS, q[k]);
-    }
-  }
-#pragma unroll
-  for (int k = 0; k < W - 1; ++k)
-    if (k < before) {
-#pragma unroll
-      for (int j = 0; j < NS; ++j) h[j] = fma_(p[k][j], h[j], q[k][j]);
-    }
-#pragma unroll
-  for (int j = 0; j < NS; ++j) H[j] = fma_(P[j], h[j], H[j]);
-  turn ^= 1;
-}
+};
 
 // Keeps the compiler from moving instructions across: loads of later tokens that are
 // issued all at once take more registers than there are.
