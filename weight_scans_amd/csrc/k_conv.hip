@@ -15,6 +15,7 @@ namespace {
 
 constexpr int kThreads = 256;
 constexpr int kAhead = 8;   // tokens whose loads are in flight together
+constexpr int kBack = 4;    // the same in the backward, which holds more
 constexpr int kAnyK = 8;    // taps of the kernels for any K: the first 8 - K are not there
 
 // W elements as they lie in memory.
@@ -215,16 +216,16 @@ __global__ __launch_bounds__(kThreads) void conv_bwd(ConvArgs a, int L, int64_t 
     const IO* px = static_cast<const IO*>(a.x) + b * a.sx.b + d;
     const IO* pg = static_cast<const IO*>(a.dy) + b * a.sdy.b + d;
     IO* po = static_cast<IO*>(a.dx) + b * a.sdx.b + d;
-    for (int64_t t0 = lo; t0 < hi + KT - 1; t0 += kAhead) {
-      Raw<IO, W> rx[kAhead], rg[kAhead];
+    for (int64_t t0 = lo; t0 < hi + KT - 1; t0 += kBack) {
+      Raw<IO, W> rx[kBack], rg[kBack];
 #pragma unroll
-      for (int k = 0; k < kAhead; ++k) {
+      for (int k = 0; k < kBack; ++k) {
         const int64_t t = t0 + k < end ? t0 + k : end - 1;
         rx[k].get(px + t * a.sx.t);
         rg[k].get(pg + t * a.sdy.t);
       }
 #pragma unroll
-      for (int k = 0; k < kAhead; ++k) {
+      for (int k = 0; k < kBack; ++k) {
         const int64_t t = t0 + k;
         if (t >= hi + KT - 1) continue;
         if (t < end) {
