@@ -12,6 +12,7 @@
 // backward's work-groups walk rows with the sums for the weights in registers and
 // leave one part each.
 #include <algorithm>
+#include <type_traits>
 
 #include "ssm_dev.hpp"
 
@@ -67,6 +68,40 @@ struct Slice {
 #pragma unroll
       for (int e = 0; e < E; ++e)
         if (e * TPR + j < d) put(p + e * TPR + j, v[e]);
+    }
+  }
+};
+
+// A thread's elements of a row as they lie in memory: asked for while another row is
+// computed (Q: as above).
+template <typename S, int TPR, int E, bool VEC, typename Q, typename IO>
+struct RawSlice {
+  static constexpr int m = Vec<IO>::n;
+  typename std::conditional<VEC, u32x4, IO>::type v[VEC ? E / m : E];
+  __device__ __forceinline__ void ask(const IO* p, int j, int d) {
+    if constexpr (VEC) {
+#pragma unroll
+      for (int e = 0; e < E; e += m) {
+        const int c = Slice<S, TPR, E, VEC>::template col<Q>(j, e / Vec<Q>::n * Vec<Q>::n) + e % Vec<Q>::n;
+        v[e / m] = *reinterpret_cast<const u32x4*>(p + (c < d ? c : 0));
+      }
+    } else {
+#pragma unroll
+      for (int e = 0; e < E; ++e) v[e] = p[e * TPR + j < d ? e * TPR + j : 0];
+    }
+  }
+  __device__ __forceinline__ void get(int j, int d, S (&x)[E]) const {
+    if constexpr (VEC) {
+#pragma unroll
+      for (int e = 0; e < E; e += m) {
+        Vec<IO>::ld(reinterpret_cast<const IO*>(&v[e / m]), x + e);
+        const bool in = Slice<S, TPR, E, VEC>::template col<Q>(j, e / Vec<Q>::n * Vec<Q>::n) < d;
+#pragma unroll
+        for (int k = 0; k < m; ++k) x[e + k] = in ? x[e + k] : S(0);
+      }
+    } else {
+#pragma unroll
+      for (int e = 0; e < E; ++e) x[e] = e * TPR + j < d ? load_as<S>(&v[e], 0) : S(0);
     }
   }
 };
@@ -195,21 +230,33 @@ __global__ __launch_bounds__(THREADS) void addnorm_bwd(AddNormArgs a) {
   if (a.wx) L::template ld<IO>(static_cast<const IO*>(a.wx), j, a.d, wx);
   if (a.scale) L::template ld<IO>(static_cast<const IO*>(a.scale), j, a.d, sc);
   const S inv = S(1) / a.d, eps = static_cast<S>(a.eps);
-  for (int64_t base = blockIdx.x * static_cast<int64_t>(R); base < rows; base += gridDim.x * static_cast<int64_t>(R)) {
+  const int64_t step = gridDim.x * static_cast<int64_t>(R);
+  RawSlice<S, TPR, E, VEC, IO, IO> nx, ng;
+  RawSlice<S, TPR, E, VEC, IO, RES> nr, no;
+  const auto ask = [&](int64_t base) {
+    const int64_t want = base + threadIdx.x / TPR, row = want < rows ? want : rows - 1, b = row / a.T, t = row % a.T;
+    nx.ask(row_in<IO>(a.x, a.sx, b, t), j, a.d);
+    nr.ask(row_in<RES>(a.r, a.sr, b, t), j, a.d);
+    ng.ask(row_in<IO>(a.dn, a.sdn, b, t), j, a.d);
+    if (a.dro) no.ask(row_in<RES>(a.dro, a.sdro, b, t), j, a.d);
+  };
+  if (blockIdx.x * static_cast<int64_t>(R) < rows) ask(blockIdx.x * static_cast<int64_t>(R));
+  for (int64_t base = blockIdx.x * static_cast<int64_t>(R); base < rows; base += step) {
     const int64_t want = base + threadIdx.x / TPR;
     const bool in = want < rows;
     const int64_t row = in ? want : rows - 1;
     const int64_t b = row / a.T, t = row % a.T;
     S x[E], r[E], g[E], go[E];
-    L::template ld<IO>(row_in<IO>(a.x, a.sx, b, t), j, a.d, x);
-    L::template ld<IO>(row_in<RES>(a.r, a.sr, b, t), j, a.d, r);
-    L::template ld<IO>(row_in<IO>(a.dn, a.sdn, b, t), j, a.d, g);
+    nx.get(j, a.d, x);
+    nr.get(j, a.d, r);
+    ng.get(j, a.d, g);
     if (a.dro) {
-      L::template ld<IO>(row_in<RES>(a.dro, a.sdro, b, t), j, a.d, go);
+      no.get(j, a.d, go);
     } else {
 #pragma unroll
       for (int e = 0; e < E; ++e) go[e] = S(0);
     }
+    if (base + step < rows) ask(base + step);
     S rx = S(1);
     if (a.wx) {
       S ss[1] = {S(0)};
@@ -321,17 +368,28 @@ __global__ __launch_bounds__(THREADS) void gatenorm_bwd(GateNormArgs a) {
   }
   if (a.w) L::template ld<IO>(static_cast<const IO*>(a.w) + (a.group_w ? blockIdx.y * static_cast<int64_t>(a.d) : 0), j, a.d, w);
   const S inv = S(1) / a.d, eps = static_cast<S>(a.eps);
-  for (int64_t base = blockIdx.x * static_cast<int64_t>(R); base < rows; base += gridDim.x * static_cast<int64_t>(R)) {
+  const int64_t step = gridDim.x * static_cast<int64_t>(R);
+  RawSlice<S, TPR, E, VEC, IO, IO> nx, nz, ng;
+  const auto ask = [&](int64_t base) {
+    const int64_t want = base + threadIdx.x / TPR, row = want < rows ? want : rows - 1;
+    const int64_t gr = a.group_w ? blockIdx.y : row % a.G, bt = a.group_w ? row : row / a.G, b = bt / a.T, t = bt % a.T;
+    nx.ask(row_in<IO>(a.x, a.sx, b, t, gr), j, a.d);
+    ng.ask(row_in<IO>(a.dy, a.sdy, b, t, gr), j, a.d);
+    if (a.z) nz.ask(row_in<IO>(a.z, a.sz, b, t, gr), j, a.d);
+  };
+  if (blockIdx.x * static_cast<int64_t>(R) < rows) ask(blockIdx.x * static_cast<int64_t>(R));
+  for (int64_t base = blockIdx.x * static_cast<int64_t>(R); base < rows; base += step) {
     const int64_t want = base + threadIdx.x / TPR;
     const bool in = want < rows;
     const int64_t row = in ? want : rows - 1;
     const int64_t gr = a.group_w ? blockIdx.y : row % a.G, bt = a.group_w ? row : row / a.G;
     const int64_t b = bt / a.T, t = bt % a.T;
     S x[E], z[E], g[E], gate[E], slope[E];
-    L::template ld<IO>(row_in<IO>(a.x, a.sx, b, t, gr), j, a.d, x);
-    L::template ld<IO>(row_in<IO>(a.dy, a.sdy, b, t, gr), j, a.d, g);
+    nx.get(j, a.d, x);
+    ng.get(j, a.d, g);
+    if (a.z) nz.get(j, a.d, z);
+    if (base + step < rows) ask(base + step);
     if (a.z) {
-      L::template ld<IO>(row_in<IO>(a.z, a.sz, b, t, gr), j, a.d, z);
 #pragma unroll
       for (int e = 0; e < E; ++e) {
         const S q = sigmoid_(z[e]);
@@ -391,17 +449,21 @@ bool gatenorm_vec(int io, const GateNormArgs& a, bool bwd) {
          aligned16(io, a.sdz);
 }
 
-// Threads a row, with eight elements each: 16 to d = 128, 64 to 512, 256 to 2048,
-// 1024 to 8192, and with sixteen each to 16384.  Rows of fewer than eight elements
+// Threads a row: the fewest that hold it with eight elements each (from 8192 on with
+// sixteen); of the kernels for single elements only every other size.  Rows of fewer than eight elements
 // are computed in fp64: w dz - hat mean(w dz hat) all but cancels in some of them (for
 // d = 1 it is eps / (x^2 + eps) of its first term).
 template <template <typename, int, int, bool, int> class Do, typename S, typename... A>
 hipError_t by_width(int d, bool vec, A... args) {
   if (d < 8) return Do<double, 16, 1, false, 256>::go(args...);
   if (vec) {
+    if (d <= 64) return Do<S, 8, 8, true, 256>::go(args...);
     if (d <= 128) return Do<S, 16, 8, true, 256>::go(args...);
+    if (d <= 256) return Do<S, 32, 8, true, 256>::go(args...);
     if (d <= 512) return Do<S, 64, 8, true, 256>::go(args...);
+    if (d <= 1024) return Do<S, 128, 8, true, 256>::go(args...);
     if (d <= 2048) return Do<S, 256, 8, true, 256>::go(args...);
+    if (d <= 4096) return Do<S, 512, 8, true, 512>::go(args...);
     if (d <= 8192) return Do<S, 1024, 8, true, 1024>::go(args...);
     return Do<S, 1024, 16, true, 1024>::go(args...);
   }
@@ -411,7 +473,12 @@ hipError_t by_width(int d, bool vec, A... args) {
   if (d <= 8192) return Do<S, 1024, 8, false, 1024>::go(args...);
   return Do<S, 1024, 16, false, 1024>::go(args...);
 }
-int rows_at_once(int d) { return d <= 128 ? 16 : d <= 512 ? 4 : 1; }
+// (of the vector kernels; the others may take fewer, and leave some parts at zero)
+int rows_at_once(int d) {
+  int q = 32;
+  while (q > 1 && d * q > 2048) q /= 2;
+  return q;
+}
 
 constexpr int64_t kMaxParts = 1024;
 

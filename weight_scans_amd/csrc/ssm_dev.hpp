@@ -19,6 +19,9 @@ __device__ __forceinline__ void put(IO* p, S v) {
   else p[0] = static_cast<IO>(v);
 }
 
+// Sixteen bytes as the registers hold them.
+typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
+
 constexpr double kLog2e = 1.4426950408889634;
 
 __device__ __forceinline__ float exp2_(float x) { return __builtin_amdgcn_exp2f(x); }
