@@ -240,13 +240,15 @@ __global__ __launch_bounds__(THREADS) void addnorm_bwd(AddNormArgs a) {
     ng.ask(row_in<IO>(a.dn, a.sdn, b, t), j, a.d);
     if (a.dro) no.ask(row_in<RES>(a.dro, a.sdro, b, t), j, a.d);
   };
-  if (blockIdx.x * static_cast<int64_t>(R) < rows) ask(blockIdx.x * static_cast<int64_t>(R));
+  // (only of vectors: single elements take too many registers to wait in)
+  if (VEC && blockIdx.x * static_cast<int64_t>(R) < rows) ask(blockIdx.x * static_cast<int64_t>(R));
   for (int64_t base = blockIdx.x * static_cast<int64_t>(R); base < rows; base += step) {
     const int64_t want = base + threadIdx.x / TPR;
     const bool in = want < rows;
     const int64_t row = in ? want : rows - 1;
     const int64_t b = row / a.T, t = row % a.T;
     S x[E], r[E], g[E], go[E];
+    if (!VEC) ask(base);
     nx.get(j, a.d, x);
     nr.get(j, a.d, r);
     ng.get(j, a.d, g);
@@ -256,7 +258,7 @@ __global__ __launch_bounds__(THREADS) void addnorm_bwd(AddNormArgs a) {
 #pragma unroll
       for (int e = 0; e < E; ++e) go[e] = S(0);
     }
-    if (base + step < rows) ask(base + step);
+    if (VEC && base + step < rows) ask(base + step);
     S rx = S(1);
     if (a.wx) {
       S ss[1] = {S(0)};
@@ -377,7 +379,8 @@ __global__ __launch_bounds__(THREADS) void gatenorm_bwd(GateNormArgs a) {
     ng.ask(row_in<IO>(a.dy, a.sdy, b, t, gr), j, a.d);
     if (a.z) nz.ask(row_in<IO>(a.z, a.sz, b, t, gr), j, a.d);
   };
-  if (blockIdx.x * static_cast<int64_t>(R) < rows) ask(blockIdx.x * static_cast<int64_t>(R));
+  // (only of vectors: single elements take too many registers to wait in)
+  if (VEC && blockIdx.x * static_cast<int64_t>(R) < rows) ask(blockIdx.x * static_cast<int64_t>(R));
   for (int64_t base = blockIdx.x * static_cast<int64_t>(R); base < rows; base += step) {
     const int64_t want = base + threadIdx.x / TPR;
     const bool in = want < rows;
@@ -385,10 +388,11 @@ __global__ __launch_bounds__(THREADS) void gatenorm_bwd(GateNormArgs a) {
     const int64_t gr = a.group_w ? blockIdx.y : row % a.G, bt = a.group_w ? row : row / a.G;
     const int64_t b = bt / a.T, t = bt % a.T;
     S x[E], z[E], g[E], gate[E], slope[E];
+    if (!VEC) ask(base);
     nx.get(j, a.d, x);
     ng.get(j, a.d, g);
     if (a.z) nz.get(j, a.d, z);
-    if (base + step < rows) ask(base + step);
+    if (VEC && base + step < rows) ask(base + step);
     if (a.z) {
 #pragma unroll
       for (int e = 0; e < E; ++e) {

@@ -490,8 +490,9 @@ static size_t bc_bytes(int io, const SsmArgs& a, int CH) {
 }
 int ssm_bwd_channels(int io, const SsmArgs& a) {
   const int n = io == IO_F64 ? 2 * a.Ns : a.Ns;
-  int CH = n <= 64 ? 32 : n <= 128 ? 16 : 8;
-  while (CH > 8 && a.N * ssm_blocks(a, CH) < 256 && bc_bytes(io, a, CH / 2) < (size_t(1) << 30)) CH /= 2;
+  const int most = n <= 64 ? 32 : n <= 128 ? 16 : 8;
+  int CH = ssm_channels(a, most, 8 * (io == IO_F64 ? 8 : 16));
+  while (CH < most && bc_bytes(io, a, CH) > (size_t(1) << 30)) CH *= 2;
   return CH;
 }
 size_t ssm_bc_bytes(int io, const SsmArgs& a) { return bc_bytes(io, a, ssm_bwd_channels(io, a)); }

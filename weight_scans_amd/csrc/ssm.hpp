@@ -86,10 +86,11 @@ inline int64_t ssm_blocks(const SsmArgs& a, int CH) {
   const int dg = a.D / a.G;
   return static_cast<int64_t>((dg + CH - 1) / CH) * a.G;
 }
-// Channels a work-group of the backward: as many as leave the LDS room for N states of
-// each, fewer (not under 8) where that gives work to more of the 256 CUs and the parts of
-// the sums over channels, which grow, stay under a gigabyte.  A forward that trains
-// keeps the states before its tiles, of ssm_ck tokens.
+// Channels a work-group, at most `most`, in tiles of tokens * 64 / channels.
+int ssm_channels(const SsmArgs& a, int most, int tokens);
+// Those of the backward: as many as leave the LDS room for N states of each at most, and no
+// fewer than keep the parts of the sums over channels, which grow, under a gigabyte.
+// A forward that trains keeps the states before its tiles, of ssm_ck tokens.
 int ssm_bwd_channels(int io, const SsmArgs& a);
 int ssm_ck(int io, const SsmArgs& a);
 size_t ssm_bc_bytes(int io, const SsmArgs& a);
