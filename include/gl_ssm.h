@@ -80,7 +80,7 @@ gl_status_t gl_conv_step(const gl_conv_desc_t* desc, const void* x, const void* 
  *   h_t = exp(D_t A[d][n]) h_(t-1) + D_t x_t B_t[n],   h_0 given or zero
  *   y_t = (sum_n C_t[n] h_t + skip[d] x_t) (z_t / (1 + e^-z_t), if z is given)
  *
- *   x, dt, z, y and gradients    [B][T][D]      io
+ *   x, dt, z, y and gradients    [B][T][D]      io (tokens less than 2^19 elements apart)
  *   B, C and gradients           [B][T][G][N]   io
  *   A, dA                        [D][N]         par, dense
  *   skip, dt_bias and gradients  [D]            par (NULL = zero)

@@ -91,6 +91,8 @@ gls::Rows rows(const gl_rows_t& s, int64_t T, int64_t G, int64_t d) {
   return {s.b, s.t, s.g};
 }
 
+constexpr int64_t kMaxTokenStride = int64_t(1) << 19;
+
 struct Cut {  // runs of a workspace
   char* at;
   void* take(size_t bytes) {
@@ -153,6 +155,10 @@ gl_status_t check_ssm(const gl_ssm_desc_t* d) {
   TRY(check_strides({d->sx, d->sdt, d->sz, d->sB, d->sC, d->sy, d->sdy, d->sdx, d->sddt, d->sdz, d->sdB, d->sdC}));
   if (d->N > 256) return fail(GL_ERROR_NOT_SUPPORTED, "N above 256");
   if (d->D > (1 << 24)) return fail(GL_ERROR_NOT_SUPPORTED, "D above 2^24");
+  // the kernels keep a lane's place in a tile of 1024 tokens as 32 bits
+  for (const gl_rows_t& s : {d->sx, d->sdt, d->sz, d->sy, d->sdy, d->sdx, d->sddt, d->sdz})
+    if (rows(s, d->T, 1, d->D).t >= kMaxTokenStride)
+      return fail(GL_ERROR_NOT_SUPPORTED, "a token stride above %lld elements", (long long)kMaxTokenStride - 1);
   const int64_t n = d->n_seq ? d->n_seq : d->B;
   TRY(check_sizes({n, d->D, 16}, 2e9));  // work-groups, lanes of a step / 256
   TRY(check_sizes({d->B, d->T, d->G, d->N}, 2e11));

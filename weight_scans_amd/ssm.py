@@ -450,10 +450,12 @@ def gl_gatenorm_bwd(x, z, w, dy, *, eps=1e-6, gate_first=False):
 
 # ---------------------------------------------------------------- autograd
 def _row_tensor(t):
-    """t, or a dense copy where its last dimension is not contiguous or it is
-    broadcast."""
-    if t is None or (t.stride(-1) == 1 or t.shape[-1] <= 1) and not any(
-            s == 0 and n > 1 for s, n in zip(t.stride(), t.shape)):
+    """t, or a dense copy where its last dimension is not contiguous, it is broadcast or
+    its tokens lie too far apart for the scan."""
+    if t is None:
+        return t
+    moves = [s for s, n in zip(t.stride()[:-1], t.shape) if n > 1]
+    if (t.stride(-1) == 1 or t.shape[-1] <= 1) and 0 not in moves and (t.dim() < 3 or t.stride(1) < 1 << 19):
         return t
     return t.contiguous()
 
