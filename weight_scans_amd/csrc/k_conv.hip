@@ -247,11 +247,18 @@ __global__ __launch_bounds__(kThreads) void conv_bwd(ConvArgs a, int L, int64_t 
 #pragma unroll
             for (int e = 0; e < W; ++e) acc[KT - 1][e] = S(0);
           }
+          if (KT < kAnyK && t - (KT - 1) >= r.t0) {  // all taps read inputs of this sequence
 #pragma unroll
-          for (int j = 0; j < KT; ++j) {
-            const bool own = tap<KT>(a, j) && t - (KT - 1 - j) >= r.t0;
+            for (int j = 0; j < KT; ++j)
 #pragma unroll
-            for (int e = 0; e < W; ++e) acc[j][e] = own ? fma_(w[j][e], g[e], acc[j][e]) : acc[j][e];
+              for (int e = 0; e < W; ++e) acc[j][e] = fma_(w[j][e], g[e], acc[j][e]);
+          } else {
+#pragma unroll
+            for (int j = 0; j < KT; ++j) {
+              const bool own = tap<KT>(a, j) && t - (KT - 1 - j) >= r.t0;
+#pragma unroll
+              for (int e = 0; e < W; ++e) acc[j][e] = own ? fma_(w[j][e], g[e], acc[j][e]) : acc[j][e];
+            }
           }
           if (t < hi) {
 #pragma unroll
