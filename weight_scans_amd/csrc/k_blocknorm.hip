@@ -468,7 +468,7 @@ hipError_t by_width(int d, bool vec, A... args) {
     if (d <= 1024) return Do<S, 128, 8, true, 256>::go(args...);
     if (d <= 2048) return Do<S, 256, 8, true, 256>::go(args...);
     if (d <= 4096) return Do<S, 512, 8, true, 512>::go(args...);
-    if (d <= 8192) return Do<S, 1024, 8, true, 1024>::go(args...);
+    if (d <= 8192) return Do<S, 512, 16, true, 512>::go(args...);
     return Do<S, 1024, 16, true, 1024>::go(args...);
   }
   if (d <= 128) return Do<S, 16, 8, false, 256>::go(args...);
