@@ -394,17 +394,20 @@ hipError_t step_k(const ConvArgs& a, hipStream_t s) {
   return hipGetLastError();
 }
 
-constexpr int kBwdRun = 32;
+// Tokens a run of the backward: four are read again behind it.
+int bwd_run(int64_t items) { return std::max(8, run_tokens(2 * items, 32)); }
 constexpr int64_t kBwdParts = 128;
 template <typename IO, typename S, int KT, int W>
 hipError_t bwd_k(const ConvArgs& a, int64_t parts, hipStream_t s) {
-  const int64_t runs_b = (a.T + kBwdRun - 1) / kBwdRun;
+  const int L = bwd_run(a.B * a.T * (a.D / 8 + 1));
+  const int64_t runs_b = (a.T + L - 1) / L;
   const dim3 grid(static_cast<unsigned>((a.D / W + kChLanes - 1) / kChLanes), static_cast<unsigned>(parts));
-  conv_bwd<IO, S, KT, W><<<grid, kThreads, 0, s>>>(a, kBwdRun, runs_b, a.B * runs_b);
+  conv_bwd<IO, S, KT, W><<<grid, kThreads, 0, s>>>(a, L, runs_b, a.B * runs_b);
   return hipGetLastError();
 }
 int64_t bwd_parts(const ConvArgs& a) {
-  const int64_t runs = a.B * ((a.T + kBwdRun - 1) / kBwdRun);
+  const int L = bwd_run(a.B * a.T * (a.D / 8 + 1));
+  const int64_t runs = a.B * ((a.T + L - 1) / L);
   return std::max<int64_t>(1, std::min((runs + kRunLanes - 1) / kRunLanes, kBwdParts));
 }
 
