@@ -111,6 +111,14 @@ def test_packed(lens, dtype):
     case(len(lens), 1, sum(lens), 40, 16, 1, dtype, lens=lens)
 
 
+@pytest.mark.parametrize("dtype", [F64, F32, BF16])
+@pytest.mark.parametrize("N", [16, 100, 200])
+@pytest.mark.parametrize("lens", [[200], [1100], [700, 0, 401], [1030, 3]])
+def test_few_channels(lens, N, dtype):
+    """Eight channels a work-group, slots of few and of many tokens, several tiles a sequence."""
+    case(len(lens) + N, 1, sum(lens), 12, N, 1, dtype, lens=lens)
+
+
 @pytest.mark.parametrize("dtype", [F32, BF16])
 @pytest.mark.parametrize("B,D", [(4, 2048), (8, 4096), (1, 64)])
 def test_channels_a_work_group(B, D, dtype):
@@ -223,7 +231,7 @@ def test_extreme_steps():
 def test_not_finite_stays_in_its_channel_and_later():
     g = to_gpu(inputs(7, 1, 600, 40, 16, 1, F32), F32)
     args = {n: g[n] for n in NAMES[:8]}
-    clean = ws.gl_ssm_fwd(**args)[0] if False else ws.gl_ssm_fwd(*args.values())[0]
+    clean = ws.gl_ssm_fwd(*args.values())[0]
     g["x"][0, 300, 5] = torch.nan
     y = ws.gl_ssm_fwd(*args.values())[0]
     hit = torch.zeros_like(y, dtype=torch.bool)

@@ -475,12 +475,17 @@ hipError_t go(int io, const SsmArgs& a, hipStream_t s) {
 }
 
 template <typename IO, typename S, int TT>
-hipError_t by_states(int io, const SsmArgs& a, hipStream_t s) {
-  switch (ssm_bwd_channels(io, a)) {
+hipError_t by_channels(int io, int channels, const SsmArgs& a, hipStream_t s) {
+  switch (channels) {
     case 32: return go<IO, SsmTile<S, 32, 8, TT, kNS, 16>>(io, a, s);
     case 16: return go<IO, SsmTile<S, 16, 8, TT, kNS, 8>>(io, a, s);
     default: return go<IO, SsmTile<S, 8, 8, TT, kNS, sizeof(S) == 8 ? 4 : 8>>(io, a, s);
   }
+}
+template <typename IO>
+hipError_t by_shape(int io, const SsmShape& p, const SsmArgs& a, hipStream_t s) {
+  if (p.tokens == kSsmShort) return by_channels<IO, float, kSsmShort>(io, p.channels, a, s);
+  return by_channels<IO, float, 16>(io, p.channels, a, s);
 }
 
 }  // namespace
@@ -488,18 +493,20 @@ hipError_t by_states(int io, const SsmArgs& a, hipStream_t s) {
 static size_t bc_bytes(int io, const SsmArgs& a, int CH) {
   return static_cast<size_t>(2 * ssm_blocks(a, CH)) * ((a.Ns + kNS - 1) / kNS * kNS) * a.B * a.T * (io == IO_F64 ? 8 : 4);
 }
-int ssm_bwd_channels(int io, const SsmArgs& a) {
+SsmShape ssm_bwd_shape(int io, const SsmArgs& a) {
   const int n = io == IO_F64 ? 2 * a.Ns : a.Ns;
   const int most = n <= 64 ? 32 : n <= 128 ? 16 : 8;
-  int CH = ssm_channels(a, most, 8 * (io == IO_F64 ? 8 : 16));
-  while (CH < most && bc_bytes(io, a, CH) > (size_t(1) << 30)) CH *= 2;
-  return CH;
+  SsmShape p = ssm_shape(a, io, most);
+  while (p.channels < most && bc_bytes(io, a, p.channels) > (size_t(1) << 30)) p.channels *= 2;
+  return p;
 }
-size_t ssm_bc_bytes(int io, const SsmArgs& a) { return bc_bytes(io, a, ssm_bwd_channels(io, a)); }
+size_t ssm_bc_bytes(int io, const SsmArgs& a) { return bc_bytes(io, a, ssm_bwd_shape(io, a).channels); }
+
 hipError_t launch_ssm_bwd(int io, const SsmArgs& a, hipStream_t s) {
-  if (io == IO_F64) return by_states<double, double, 8>(io, a, s);
-  if (io == IO_F32) return by_states<float, float, 16>(io, a, s);
-  return by_states<bf16, float, 16>(io, a, s);
+  const SsmShape p = ssm_bwd_shape(io, a);
+  if (io == IO_F64) return by_channels<double, double, 8>(io, p.channels, a, s);
+  if (io == IO_F32) return by_shape<float>(io, p, a, s);
+  return by_shape<bf16>(io, p, a, s);
 }
 
 }  // namespace gls

@@ -184,43 +184,51 @@ hipError_t go(int io, const SsmArgs& a, hipStream_t s) {
   return hipGetLastError();
 }
 
-// Channels a work-group: those with the least rounds of tiles for the 256 CUs, the most
-// where two have the same (and no more than fit the LDS).  One sequence of 32768 tokens of
-// 2048 channels: 16 channels 1134 us, 8 685 us; 5 sequences of 777 tokens in all: 64
-// channels 53 us, 32 75 us, 8 86 us.
 template <typename IO, typename S, int TT, int NS>
-hipError_t by_channels(int io, const SsmArgs& a, hipStream_t s) {
-  const int most = a.Ns <= 64 ? 64 : a.Ns <= 128 ? 32 : 16;
-  switch (ssm_channels(a, most, 8 * TT)) {
+hipError_t by_channels(int io, int channels, const SsmArgs& a, hipStream_t s) {
+  switch (channels) {
     case 64: return go<IO, SsmTile<S, 64, 8, TT, NS, 16>>(io, a, s);
     case 32: return go<IO, SsmTile<S, 32, 8, TT, NS, 16>>(io, a, s);
     case 16: return go<IO, SsmTile<S, 16, 8, TT, NS, 8>>(io, a, s);
     default: return go<IO, SsmTile<S, 8, 8, TT, NS, 8>>(io, a, s);
   }
 }
+template <typename IO>
+hipError_t by_shape(int io, const SsmShape& p, const SsmArgs& a, hipStream_t s) {
+  if (p.tokens == kSsmShort) return by_channels<IO, float, kSsmShort, 4>(io, p.channels, a, s);
+  return by_channels<IO, float, 16, 4>(io, p.channels, a, s);
+}
 
 }  // namespace
 
-int ssm_channels(const SsmArgs& a, int most, int tokens) {
-  const int64_t len = a.packed ? (a.T + std::max<int64_t>(a.N, 1) - 1) / std::max<int64_t>(a.N, 1) : a.T;
-  int best = most;
+// Channels and tokens with the least rounds of tiles for the 256 CUs (a tile costs its
+// slots' tokens and about eight more for the exchanges), the most channels where two
+// have the same.  One sequence of 32768 tokens of 2048 channels: 16 channels 1134 us, 8
+// 685 us; 5 sequences of 777 tokens in all: 64 channels 53 us, 32 75 us, 8 86 us (all of 16
+// tokens a slot).  Forward and backward of 4 x 24 tokens of 1280 channels, 64 states: 16
+// tokens a slot 183 us, 4 100 us; of 2 x 90 of 192 channels, 16 states: 58 us and 41 us.
+SsmShape ssm_shape(const SsmArgs& a, int io, int most) {
+  const int64_t n = std::max<int64_t>(a.N, 1), len = a.packed ? (a.T + n - 1) / n : a.T;
+  SsmShape best{most, io == IO_F64 ? 8 : 16};
   int64_t least = INT64_MAX;
-  for (int CH = most; CH >= 8; CH /= 2) {
-    const int64_t tile = static_cast<int64_t>(tokens) * (64 / CH);
-    const int64_t cost = ((a.N * ssm_blocks(a, CH) + 255) / 256) * std::max<int64_t>(1, (len + tile - 1) / tile);
-    if (cost < least) {
-      least = cost;
-      best = CH;
+  for (int CH = most; CH >= 8; CH /= 2)
+    for (const int TT : {16, kSsmShort}) {
+      const SsmShape p{CH, io == IO_F64 ? 8 : TT};
+      const int64_t tiles = std::max<int64_t>(1, (len + p.tile() - 1) / p.tile());
+      const int64_t cost = (n * ssm_blocks(a, CH) + 255) / 256 * tiles * (p.tokens + 8);
+      if (cost < least) {
+        least = cost;
+        best = p;
+      }
     }
-  }
   return best;
 }
-int ssm_ck(int io, const SsmArgs& a) { return (io == IO_F64 ? 8 : 16) * 8 * (64 / ssm_bwd_channels(io, a)); }
 
 hipError_t launch_ssm_fwd(int io, const SsmArgs& a, hipStream_t s) {
-  if (io == IO_F64) return by_channels<double, double, 8, 2>(io, a, s);
-  if (io == IO_F32) return by_channels<float, float, 16, 4>(io, a, s);
-  return by_channels<bf16, float, 16, 4>(io, a, s);
+  const SsmShape p = ssm_shape(a, io, a.Ns <= 64 ? 64 : a.Ns <= 128 ? 32 : 16);  // (by the LDS)
+  if (io == IO_F64) return by_channels<double, double, 8, 2>(io, p.channels, a, s);
+  if (io == IO_F32) return by_shape<float>(io, p, a, s);
+  return by_shape<bf16>(io, p, a, s);
 }
 
 }  // namespace gls

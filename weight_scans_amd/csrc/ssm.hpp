@@ -86,13 +86,17 @@ inline int64_t ssm_blocks(const SsmArgs& a, int CH) {
   const int dg = a.D / a.G;
   return static_cast<int64_t>((dg + CH - 1) / CH) * a.G;
 }
-// Channels a work-group, at most `most`, in tiles of tokens * 64 / channels.
-int ssm_channels(const SsmArgs& a, int most, int tokens);
-// Those of the backward: as many as leave the LDS room for N states of each at most, and no
-// fewer than keep the parts of the sums over channels, which grow, under a gigabyte.
-// A forward that trains keeps the states before its tiles, of ssm_ck tokens.
-int ssm_bwd_channels(int io, const SsmArgs& a);
-int ssm_ck(int io, const SsmArgs& a);
+// Channels a work-group and tokens a slot; tiles are of 8 * 64 / channels slots.
+struct SsmShape {
+  int channels, tokens;
+  int tile() const { return tokens * 8 * (64 / channels); }
+};
+SsmShape ssm_shape(const SsmArgs& a, int io, int most);
+// Those of the backward: as many channels as leave the LDS room for N states of each at most,
+// and no fewer than keep the parts of the sums over channels, which grow, under a
+// gigabyte.  A forward that trains keeps the states before its tiles.
+SsmShape ssm_bwd_shape(int io, const SsmArgs& a);
+inline int ssm_ck(int io, const SsmArgs& a) { return ssm_bwd_shape(io, a).tile(); }
 size_t ssm_bc_bytes(int io, const SsmArgs& a);
 hipError_t launch_ssm_fwd(int io, const SsmArgs& a, hipStream_t s);
 hipError_t launch_ssm_bwd(int io, const SsmArgs& a, hipStream_t s);

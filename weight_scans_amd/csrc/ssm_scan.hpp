@@ -15,6 +15,8 @@
 
 namespace gls {
 
+constexpr int kSsmShort = 4;  // tokens a slot where sequences are short (16 else, 8 in fp64)
+
 template <typename S_, int CH_, int W_, int TT_, int NS_, int NB_>
 struct SsmTile {
   using S = S_;
