@@ -14,11 +14,12 @@
  *
  * Packed sequences: with n_seq > 0, B is 1, the T tokens hold n_seq sequences
  * one after another and cu_seqlens (device, int32, n_seq + 1 values, first 0,
- * last T, not decreasing) says where each begins.  States then number n_seq;
- * otherwise B.  A sequence may be empty: its state passes through.  Values out
- * of range are clamped to it, so that no call reads or writes outside its
- * tensors; where the sequences do not cover 0..T-1 once, what the outputs hold
- * at the other tokens is undefined.
+ * last T or less, not decreasing) says where each begins.  States then number
+ * n_seq; otherwise B.  A sequence may be empty: its state passes through.  Tokens
+ * behind the last sequence belong to none: whatever they hold adds nothing to any
+ * sum, and all outputs and gradients are zero there.  Values out of range are
+ * clamped to it, so that no call reads or writes outside its tensors; where a
+ * table is not as said, what the outputs hold is undefined.
  */
 #ifndef GL_SSM_H
 #define GL_SSM_H

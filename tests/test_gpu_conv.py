@@ -152,3 +152,24 @@ def test_not_finite_stays_in_its_channel_and_window():
     hit = torch.zeros(1, 40, 16, dtype=torch.bool, device="cuda")
     hit[0, 20:25, 3] = True
     assert torch.equal(y[~hit], clean[~hit])
+
+
+@pytest.mark.parametrize("dtype", [F64, F32, BF16])
+@pytest.mark.parametrize("lens", [[70, 0, 20], [90, 0], [0, 0], [2, 1]])
+@pytest.mark.parametrize("D,K,behind", [(40, 4, 1), (7, 3, 300), (64, 8, 40), (16, 1, 5)])
+def test_tokens_behind_the_last_sequence(D, K, behind, lens, dtype):
+    """They hold NaN: their outputs and gradients are zero, the others as without them."""
+    T = sum(lens)
+    g = {n: dev(t, dtype) for n, t in inputs(D + T, 1, T, D, K, dtype, lens).items()}
+    p = {n: torch.cat([t, torch.full((1, behind, D), torch.nan, dtype=dtype, device="cuda")], 1) if n in ("x", "dy") else t
+         for n, t in g.items()}
+    run = lambda a: (*ws.gl_conv_fwd(a["x"], a["w"], a["bias"], state=a["state"], want_state=True,  # noqa: E731
+                                     cu_seqlens=cu(lens)),
+                     *ws.gl_conv_bwd(a["x"], a["w"], a["bias"], a["dy"], state=a["state"], dstate=a["dstate"],
+                                     cu_seqlens=cu(lens)))
+    # both are within the tolerance of the definition
+    for n, want, got in zip(("y", "end", "x", "w", "bias", "state"), run(g), run(p)):
+        if n in ("y", "x"):
+            assert not got[:, T:].any(), n
+            got = got[:, :T]
+        assert rel(got, want) <= 2 * (SUM_TOL if n in ("w", "bias") else TOL)[dtype], n

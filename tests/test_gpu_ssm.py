@@ -6,9 +6,10 @@ step, 2^-8 = 3.91e-3 of it, and so the norm of all).  fp32: a decay e^(D A) is o
 its argument's rounding and its own, (|D A| + 2) 6e-8, and a state carries what
 came in k tokens ago through k of them: with a memory of L = 1 / |D A| tokens the
 errors of L decays of about 1.3e-7 add up, by their squares, to 1.3e-7 sqrt(L),
-2.3e-6 for L = 300 (the inputs' is at most that, as no sequence is longer); with
-the sums' own roundings 4e-6, and twice that for gradients, which carry a state and
-an adjoint.  fp64 1e-12.  The inputs are values of their type."""
+2.3e-6 for L = 300 (the inputs' is at most that, as no sequence is longer but
+test_few_channels', whose memory is as long in the first of their 16 states or more at
+most); with the sums' own roundings 4e-6, and twice that for gradients, which
+carry a state and an adjoint.  fp64 1e-12.  The inputs are values of their type."""
 import pytest
 import torch
 
@@ -109,6 +110,29 @@ def test_groups_and_without(G, kw, dtype):
 @pytest.mark.parametrize("lens", [[5, 0, 1, 40, 2, 16, 0], [0, 0, 3], [1] * 7, [300], [0, 256, 17, 0], [128, 128, 1]])
 def test_packed(lens, dtype):
     case(len(lens), 1, sum(lens), 40, 16, 1, dtype, lens=lens)
+
+
+@pytest.mark.parametrize("dtype", [F64, F32, BF16])
+@pytest.mark.parametrize("lens", [[70, 0, 20], [90, 0], [0, 0]])
+@pytest.mark.parametrize("D,G,behind", [(40, 2, 1), (12, 1, 300), (130, 1, 40)])
+def test_tokens_behind_the_last_sequence(D, G, behind, lens, dtype):
+    """They hold NaN: their outputs and gradients are zero, the others as without them."""
+    T, N = sum(lens), 5
+    g = to_gpu(inputs(D + T, 1, T, D, N, G, dtype, lens), dtype)
+    pad = lambda n, t: t if n not in ("x", "dt", "B", "C", "z", "dy") else torch.cat(  # noqa: E731
+        [t, torch.full((1, behind, *t.shape[2:]), torch.nan, dtype=dtype, device="cuda")], 1)
+    p = {n: pad(n, t) for n, t in g.items()}
+    kw = dict(cu_seqlens=cu(lens), state=g["state"])
+    run = lambda a, save: (lambda f: (*f[:2], *ws.gl_ssm_bwd(  # noqa: E731
+        *(a[n] for n in NAMES[:8]), a["dy"], f[2], dstate=a["dstate"], **kw)))(
+            ws.gl_ssm_fwd(*(a[n] for n in NAMES[:8]), want_state=True, save=save, **kw))
+    for save in (True, False):
+        # both are within the tolerance of the definition
+        for n, want, got in zip(("y", "end", *(NAMES)), run(g, save), run(p, save)):
+            if n in ("x", "dt", "B", "C", "z", "y"):
+                assert not got[:, T:].any(), n
+                got = got[:, :T]
+            assert rel(got, want) <= 2 * tol(n, dtype, True), n
 
 
 @pytest.mark.parametrize("dtype", [F64, F32, BF16])

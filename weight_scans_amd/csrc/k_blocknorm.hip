@@ -497,6 +497,7 @@ struct Add {
   struct Fwd {
     static hipError_t go(const AddNormArgs& a, hipStream_t s) {
       const int64_t g = (a.B * a.T + TH / TPR - 1) / (TH / TPR);
+      if (!launch_fits(g * TH)) return hipErrorInvalidConfiguration;
       addnorm_fwd<IO, RES, S, TPR, E, VEC, TH><<<static_cast<unsigned>(g), TH, 0, s>>>(a);
       return hipGetLastError();
     }
@@ -515,6 +516,7 @@ struct Gate {
   struct Fwd {
     static hipError_t go(const GateNormArgs& a, hipStream_t s) {
       const int64_t g = (a.B * a.T * a.G + TH / TPR - 1) / (TH / TPR);
+      if (!launch_fits(g * TH)) return hipErrorInvalidConfiguration;
       gatenorm_fwd<IO, S, TPR, E, VEC, TH><<<static_cast<unsigned>(g), TH, 0, s>>>(a);
       return hipGetLastError();
     }

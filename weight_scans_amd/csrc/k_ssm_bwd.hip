@@ -142,6 +142,9 @@ __global__ __launch_bounds__(L::THREADS) void ssm_bwd(SsmArgs a) {
   const int64_t id = xcd_order(blockIdx.x, gridDim.x);
   const SsmPlace p = ssm_place(a, CH, id);
   const SeqRange r = seq_range(a.cu, p.n, a.T);
+  clear_behind<IO, L>(a, p, r, a.dx, a.sdx);
+  clear_behind<IO, L>(a, p, r, a.ddt, a.sddt);
+  if constexpr (Z) clear_behind<IO, L>(a, p, r, a.dz, a.sdz);
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
   const int c = lane % CH, ts = lane / CH, slot = wave * L::TS + ts;
   const bool in = c < p.nch;
@@ -417,26 +420,33 @@ __global__ __launch_bounds__(kSumThreads) void ssm_bwd_sums(SsmArgs a, int nb, i
   const int64_t tok = a.B * a.T;
   if (blockIdx.x < bc_groups) {
     const int64_t per = groups * tok * NS;  // of one group of channels, of B or of C
-    const int64_t i = blockIdx.x * static_cast<int64_t>(kSumThreads) + threadIdx.x;
-    if (i >= 2 * a.G * per) return;
-    const int64_t which = i / (a.G * per), g = i / per % a.G, o = i % per;
-    const int j = static_cast<int>(o % NS);
-    const int64_t t = o / NS % tok, n = o / (NS * tok) * NS + j;
-    if (n >= a.Ns) return;
-    const S* part = static_cast<const S*>(a.part_bc) + (which * a.G + g) * nb * per + o;
-    S x = S(0);
-    int k = 0;
-    for (; k + 8 <= nb; k += 8) {
-      S v[8];
-#pragma unroll
-      for (int m = 0; m < 8; ++m) v[m] = part[(k + m) * per];
-#pragma unroll
-      for (int m = 0; m < 8; ++m) x += v[m];
+    int64_t behind = tok;  // no parts are there for the tokens behind the last packed sequence
+    if (a.packed) {
+      const SeqRange r = seq_range(a.cu, a.N - 1, a.T);
+      behind = r.t0 + r.len;
     }
-    for (; k < nb; ++k) x += part[k * per];
-    const Rows& st = which ? a.sdC : a.sdB;
-    IO* out = static_cast<IO*>(which ? a.dC : a.dB) + t / a.T * st.b + t % a.T * st.t + g * st.g;
-    store_from(out, n, x);
+    for (int64_t i = blockIdx.x * static_cast<int64_t>(kSumThreads) + threadIdx.x; i < 2 * a.G * per;
+         i += bc_groups * kSumThreads) {
+      const int64_t which = i / (a.G * per), g = i / per % a.G, o = i % per;
+      const int j = static_cast<int>(o % NS);
+      const int64_t t = o / NS % tok, n = o / (NS * tok) * NS + j;
+      if (n >= a.Ns) continue;
+      const S* part = static_cast<const S*>(a.part_bc) + (which * a.G + g) * nb * per + o;
+      const int there = t < behind ? nb : 0;
+      S x = S(0);
+      int k = 0;
+      for (; k + 8 <= there; k += 8) {
+        S v[8];
+#pragma unroll
+        for (int m = 0; m < 8; ++m) v[m] = part[(k + m) * per];
+#pragma unroll
+        for (int m = 0; m < 8; ++m) x += v[m];
+      }
+      for (; k < there; ++k) x += part[k * per];
+      const Rows& st = which ? a.sdC : a.sdB;
+      IO* out = static_cast<IO*>(which ? a.dC : a.dB) + t / a.T * st.b + t % a.T * st.t + g * st.g;
+      store_from(out, n, x);
+    }
     return;
   }
   const int64_t i = (blockIdx.x - bc_groups) * kSumThreads + threadIdx.x;
@@ -460,6 +470,7 @@ hipError_t go(int io, const SsmArgs& a, hipStream_t s) {
   if (a.N * blocks > 0) {
     SsmArgs b = a;
     b.vec_bc = ssm_vec_bc(io, a);
+    if (!launch_fits(a.N * blocks * L::THREADS)) return hipErrorInvalidConfiguration;
     const unsigned g = static_cast<unsigned>(a.N * blocks);
     if (a.z) ssm_bwd<IO, L, true><<<g, L::THREADS, bwd_lds<L, true>(a.Ns), s>>>(b);
     else ssm_bwd<IO, L, false><<<g, L::THREADS, bwd_lds<L, false>(a.Ns), s>>>(b);
@@ -467,7 +478,7 @@ hipError_t go(int io, const SsmArgs& a, hipStream_t s) {
     if (e != hipSuccess) return e;
   }
   const int64_t bc = 2 * a.G * ((a.Ns + kNS - 1) / kNS) * a.B * a.T * kNS, par = static_cast<int64_t>(a.Ns + 2) * a.D;
-  const int64_t g1 = (bc + kSumThreads - 1) / kSumThreads, g2 = (par + kSumThreads - 1) / kSumThreads;
+  const int64_t g1 = std::min<int64_t>((bc + kSumThreads - 1) / kSumThreads, 1 << 23), g2 = (par + kSumThreads - 1) / kSumThreads;
   if (g1 + g2 == 0) return hipSuccess;
   ssm_bwd_sums<IO, typename L::S, kNS>
       <<<static_cast<unsigned>(g1 + g2), kSumThreads, 0, s>>>(a, static_cast<int>(a.G ? blocks / a.G : 0), g1);

@@ -29,6 +29,7 @@ __global__ __launch_bounds__(L::THREADS) void ssm_fwd(SsmArgs a, int ck) {
   S* sh = sA + np * CH;                          // [2][np][CH]
   const SsmPlace p = ssm_place(a, CH, xcd_order(blockIdx.x, gridDim.x));
   const SeqRange r = seq_range(a.cu, p.n, a.T);
+  clear_behind<IO, L>(a, p, r, a.y, a.sy);
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
   const int slot = wave * L::TS + lane / CH;
   const bool in = lane % CH < p.nch;
@@ -177,6 +178,7 @@ template <typename IO, typename L>
 hipError_t go(int io, const SsmArgs& a, hipStream_t s) {
   const int64_t g = a.N * ssm_blocks(a, L::CH);
   if (g == 0) return hipSuccess;
+  if (!launch_fits(g * L::THREADS)) return hipErrorInvalidConfiguration;
   SsmArgs b = a;
   b.vec_bc = ssm_vec_bc(io, a);
   if (a.z) ssm_fwd<IO, L, true><<<static_cast<unsigned>(g), L::THREADS, L::lds(a.Ns), s>>>(b, ssm_ck(io, a));

@@ -65,6 +65,7 @@ __global__ __launch_bounds__(kThreads) void ssm_step(SsmArgs a) {
 template <typename IO, typename S, int L, int W>
 hipError_t go(const SsmArgs& a, hipStream_t s) {
   const int64_t n = a.B * a.D * L;
+  if (!launch_fits(n)) return hipErrorInvalidConfiguration;
   ssm_step<IO, S, L, W><<<static_cast<unsigned>((n + kThreads - 1) / kThreads), kThreads, 0, s>>>(a);
   return hipGetLastError();
 }

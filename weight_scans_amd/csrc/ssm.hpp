@@ -15,6 +15,8 @@ namespace gls {
 struct Rows {
   int64_t b, t, g;
 };
+// A launch counts its threads in 32 bits.
+inline bool launch_fits(int64_t threads) { return threads <= 0xffffffffLL - 1024; }
 
 // ---- convolution
 struct ConvArgs {

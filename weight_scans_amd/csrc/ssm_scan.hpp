@@ -63,6 +63,16 @@ __device__ __forceinline__ SsmPlace ssm_place(const SsmArgs& a, int CH, int64_t 
   p.n = i / blocks;
   return p;
 }
+// The rows behind the last packed sequence belong to none: the last sequence's work-groups
+// make them zeros.
+template <typename IO, typename L>
+__device__ __forceinline__ void clear_behind(const SsmArgs& a, const SsmPlace& p, const SeqRange& r, void* out, const Rows& s) {
+  if (!a.packed || p.n + 1 < a.N || !out) return;
+  const int c = threadIdx.x % L::CH;
+  if (c >= p.nch) return;
+  for (int64_t t = r.t0 + r.len + threadIdx.x / L::CH; t < a.T; t += L::THREADS / L::CH)
+    store_from(static_cast<IO*>(out) + t * s.t, p.d0 + c, typename L::S(0));
+}
 // A tensor of rows as a work-group reads it: one base for the tile (the same in all
 // lanes, so that it is kept and moved on by the scalar unit), and the lane's offset
 // in bytes, which stays (below 2^32: the host bounds the strides).
