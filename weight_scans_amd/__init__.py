@@ -26,6 +26,18 @@ and a command that run them together: ``gated_delta.py``):
     y1 = gl_delta_step(q1, k1, v1, log_alpha1, beta1, state)           # one token
     qn, kn = qknorm_rope(q, k, wq, wk, cos, sin)                       # autograd-aware
 
+The selective state space scan (a state per channel that decays by what the token
+says), the short causal convolution before it and the norms after a block's heads and
+between blocks, behind ``include/gl_ssm.h`` (see ``ssm.py``; a layer and a command that
+run them together: ``selective.py``):
+
+    x, last = causal_conv(x, taps, bias, want_state=True)              # autograd-aware
+    y, state = selective_scan(x, dt, A, B, C, skip, z, dt_bias, want_state=True)
+    x1 = gl_conv_step(x1, taps, bias, last)                            # one token
+    y1 = gl_ssm_step(x1, dt1, A, B1, C1, skip, z1, dt_bias, state)
+    y = gated_norm(y, z, w)                                            # autograd-aware
+    n, r = add_norm(x, r, w, wx, scale)                                # autograd-aware
+
 Shapes: x [B,H,T,d_in], g [B,H,T,d_out], eta/alpha [B,H,T], W0 [H,d_out,d_in];
 one decode token: x1 [B,H,d_in], g1 [B,H,d_out], eta1/alpha1 [B,H];
 state [B,H,d_out,d_in] in the gate dtype.

@@ -5,7 +5,9 @@
 // neighbouring channels (one element where rows do not begin on 16 bytes) and a
 // run of tokens, with the last K - 1 inputs in registers; neighbouring threads
 // own neighbouring channels.  The inputs before a run are read again by it, in
-// the backward also what its last inputs reach behind it.
+// the backward also what its last inputs reach behind it.  4 x 4096
+// tokens of 2048 channels in bf16, K = 4: forward 30 us, 4.5 TB/s, backward 56 us, 3.6 TB/s
+// (a thread's forty sums for the weights' gradients leave it fewer loads in flight).
 #include <algorithm>
 
 #include "ssm_dev.hpp"
@@ -408,9 +410,9 @@ hipError_t step_k(const ConvArgs& a, hipStream_t s) {
   return hipGetLastError();
 }
 
-// Tokens a run of the backward, which reads the K - 1 tokens behind it once more: 4 x 4096
-// of 4096 channels 90.6 us with 32, ... where there are few, shorter ones, for
-// more threads: 3 x 88 tokens of 512 channels 43 us with 32 (forward and backward), 29 with 8.
+// Tokens a run of the backward, which reads the K - 1 tokens behind it once more: 32, and
+// where there are few tokens less, for more threads: 3 x 88 tokens of 512 channels take 43 us
+// with 32 (forward and backward), 29 with 8.
 int bwd_run(int64_t items) { return std::max(8, run_tokens(2 * items, 32)); }
 constexpr int64_t kBwdParts = 128;
 template <typename IO, typename S, int KT, int W>

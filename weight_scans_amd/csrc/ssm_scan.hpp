@@ -9,6 +9,13 @@
 // it makes of zero and P = exp(A sum D); effects compose along the slots by
 //   (P2, H2) o (P1, H1) = (P2 P1, P2 H1 + H2),
 // first across a wave's slots by shuffles, then across the waves in LDS.
+//
+// Tokens in a lane, not in a matrix product: decays differ per channel and state, so
+// that a product over tokens would need one matrix of them each.  States one after
+// another in groups of NS, not side by side in lanes: a lane's x, D and y then serve all
+// states, and only B and C are read per state, from LDS.  Longer slots cost less in
+// exchanges (16 tokens: 690 us the backward at 4 x 4096 x 2048 x 16; 8 with twice the states
+// at once: 890), shorter ones leave less of a short sequence's tile empty.
 #pragma once
 
 #include "ssm_dev.hpp"

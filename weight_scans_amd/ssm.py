@@ -21,7 +21,8 @@ Shapes: rows x, dt, z, y [B,T,D]; B, C [B,T,G,N] (channel d reads group
 d / (D / G)) or [B,T,N]; A [D,N], skip, dt_bias [D]; convolution weights [D,K];
 states [B,D,N] of the scan and [B,K-1,D] (the last inputs, oldest first) of the
 convolution; with cu_seqlens [n + 1] (int32, on the device) B is 1 and there are
-n states.  A, skip, dt_bias and the scan's states are fp32 (fp64 for fp64 io),
+n states, and tokens behind the last sequence add nothing: outputs and gradients
+are zero there.  A, skip, dt_bias and the scan's states are fp32 (fp64 for fp64 io),
 all others of the io dtype; the residual of add_norm is either.  Tensors of rows
 may be views with any strides whose last dimension is contiguous (slices of a
 fused projection); outputs are dense.
