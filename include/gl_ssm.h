@@ -89,7 +89,8 @@ gl_status_t gl_conv_step(const gl_conv_desc_t* desc, const void* x, const void* 
  *
  * Numerical preconditions (not checked on the device): finite inputs, D_t >= 0
  * and A <= 0 (every factor is then a contraction; a state that grows is computed
- * as long as its growth over 1024 tokens stays within the type).  A value that is
+ * as long as its growth over 1024 tokens stays within the type); with
+ * GL_FLAG_SOFTPLUS dt_t may be -infinity: the token then passes by.  A value that is
  * not finite reaches its own channel's later tokens only, in a backward also the
  * earlier ones and the sums over channels and tokens that it is part of.
  *

@@ -113,6 +113,28 @@ def test_packed(lens, dtype):
 
 
 @pytest.mark.parametrize("dtype", [F64, F32, BF16])
+@pytest.mark.parametrize("D,T", [(40, 90), (12, 300), (64, 17)])
+def test_tokens_that_pass_by(D, T, dtype):
+    """Steps of softplus(-inf) or of the type's lowest value are 0: the state stays, dt's gradient is 0; also for
+    all tokens of a row."""
+    x = inputs(D, 3, T, D, 8, 1, dtype)
+    low = torch.finfo(dtype).min
+    x["dt"][0, : T // 2], x["dt"][1] = -torch.inf, low
+    x["dt"][2, 1::2] = low
+    leaves = {n: x[n].requires_grad_(True) for n in NAMES}
+    y, end = ref.scan(*(x[n] for n in NAMES), None, True)
+    want = torch.autograd.grad((y * x["dy"]).sum() + (end * x["dstate"]).sum(), list(leaves.values()))
+    g = to_gpu(x, dtype)
+    args = [g[n] for n in NAMES[:8]]
+    yg, eg, saved = ws.gl_ssm_fwd(*args, state=g["state"], want_state=True, save=True)
+    got = ws.gl_ssm_bwd(*args, g["dy"], saved, state=g["state"], dstate=g["dstate"])
+    assert torch.equal(eg[1], g["state"][1])
+    assert not got[1][0, : T // 2].any() and not got[1][1].any() and not got[1][2, 1::2].any()
+    errs = {"y": (rel(yg, y), tol("y", dtype, False)), "end": (rel(eg, end), tol("end", dtype, False))}
+    check(errs | {"d" + n: (rel(t, w), tol(n, dtype, True)) for n, t, w in zip(NAMES, got, want)})
+
+
+@pytest.mark.parametrize("dtype", [F64, F32, BF16])
 @pytest.mark.parametrize("lens", [[70, 0, 20], [90, 0], [0, 0]])
 @pytest.mark.parametrize("D,G,behind", [(40, 2, 1), (12, 1, 300), (130, 1, 40)])
 def test_tokens_behind_the_last_sequence(D, G, behind, lens, dtype):
