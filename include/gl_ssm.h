@@ -70,7 +70,7 @@ gl_status_t gl_conv_bwd(const gl_conv_desc_t* desc, const void* x, const void* w
  * of n_slots states, moved on by one input in place.  Row b uses state slots[b]
  * (device int32; NULL = b, n_slots >= B); a slot outside 0..n_slots-1 marks a
  * row with nothing to do: its y is zero and no state changes.  No two rows may
- * name one slot.  desc->T is not used, n_seq must be 0. */
+ * name one slot.  desc->T is not used (any T >= 0), n_seq must be 0. */
 gl_status_t gl_conv_step(const gl_conv_desc_t* desc, const void* x, const void* w, const void* bias,
                          const int32_t* slots, int64_t n_slots, void* state, void* y, void* stream);
 

@@ -289,3 +289,23 @@ def test_offsets_past_32_bits():
     assert torch.equal(c[1:], ws.gl_conv_fwd(one, w)[0])
     assert torch.equal(n[1:], ws.gl_gatenorm_fwd(one, one))
     assert torch.equal(r[1:], ws.gl_addnorm_fwd(one, one, w[:, 0].contiguous())[0])
+
+
+@pytest.mark.parametrize("T", [0, 7, 4096])
+@pytest.mark.parametrize("dtype,D,K", [(BF16, 64, 4), (F32, 13, 2), (F64, 6, 6)])
+def test_convolution_step_with_the_descriptor_of_a_prompt(T, dtype, D, K):
+    """Dense rows of a step are D apart whatever T the descriptor holds: the bits of T = 1, the rest untouched."""
+    B = 5
+    x, w, bias, state = (torch.randn(s, device="cuda").to(dtype) for s in ((B, D), (D, K), (D,), (B, K - 1, D)))
+    want, ends = torch.empty_like(x), state.clone()
+
+    def step(T, st, y):
+        desc = ws.ConvDesc(B, T, D, K, 0, CODE[dtype], ws.GL_FLAG_SILU)
+        status = ws.ssm_lib().gl_conv_step(ctypes.byref(desc), ptr(x), ptr(w), ptr(bias), None, B, ptr(st), ptr(y),
+                                           ctypes.c_void_p(torch.cuda.current_stream().cuda_stream))
+        assert status == 0, ws.lib().gl_last_error()
+    step(1, ends, want)
+    out = Outputs([x, state])
+    out.t[1].copy_(state)
+    step(T, out.t[1], out.t[0])
+    assert out.whole() and torch.equal(out.t[0], want) and torch.equal(out.t[1], ends)

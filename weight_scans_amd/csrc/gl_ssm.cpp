@@ -109,7 +109,8 @@ struct Cut {  // runs of a workspace
   } while (0)
 
 // ------------------------------------------------------------ convolution
-gl_status_t check_conv(const gl_conv_desc_t* d) {
+// (A step is one token of each row, whatever T its descriptor holds.)
+gl_status_t check_conv(const gl_conv_desc_t* d, bool step = false) {
   if (!d) return fail(GL_ERROR_INVALID_VALUE, "desc is NULL");
   if (d->B < 0 || d->T < 0 || d->D < 0) return fail(GL_ERROR_INVALID_VALUE, "negative B, T or D");
   if (d->K < 1) return fail(GL_ERROR_INVALID_VALUE, "K must be >= 1");
@@ -120,7 +121,7 @@ gl_status_t check_conv(const gl_conv_desc_t* d) {
   if (d->K > 8) return fail(GL_ERROR_NOT_SUPPORTED, "K above 8");
   if (d->D > (1 << 24)) return fail(GL_ERROR_NOT_SUPPORTED, "D above 2^24");
   const int64_t n = d->n_seq ? d->n_seq : d->B;
-  TRY(check_sizes({d->B, d->T, d->D}, 5e11));
+  TRY(check_sizes({d->B, step ? 1 : d->T, d->D}, 5e11));
   return check_sizes({n, d->D, 8}, 2e11);
 }
 
@@ -294,9 +295,11 @@ gl_status_t gl_conv_bwd(const gl_conv_desc_t* desc, const void* x, const void* w
 
 gl_status_t gl_conv_step(const gl_conv_desc_t* desc, const void* x, const void* w, const void* bias,
                          const int32_t* slots, int64_t n_slots, void* state, void* y, void* stream) {
-  TRY(check_conv(desc));
+  TRY(check_conv(desc, true));
   if (desc->n_seq) return fail(GL_ERROR_INVALID_VALUE, "a step takes no packed sequences");
-  gls::ConvArgs a = conv_args(desc);
+  gl_conv_desc_t one = *desc;
+  one.T = 1;
+  gls::ConvArgs a = conv_args(&one);
   if (a.B * a.D == 0) {
     return n_slots < 0 ? fail(GL_ERROR_INVALID_VALUE, "n_slots is negative") : GL_SUCCESS;
   }
