@@ -127,7 +127,8 @@ gl_status_t gl_ssm_bwd(const gl_ssm_desc_t* desc, const void* x, const void* dt,
                        void* dstate_in, void* ws, size_t ws_bytes, void* stream);
 
 /* One token of B sequences, x, dt, z, y [B][D], B, C [B][G][N] (strides b and g),
- * against a pool of n_slots states updated in place; slots as in gl_conv_step. */
+ * against a pool of n_slots states updated in place; slots, T and n_seq as in
+ * gl_conv_step. */
 gl_status_t gl_ssm_step(const gl_ssm_desc_t* desc, const void* x, const void* dt, const void* A, const void* B,
                         const void* C, const void* skip, const void* z, const void* dt_bias, const int32_t* slots,
                         int64_t n_slots, void* state, void* y, void* stream);

@@ -309,3 +309,24 @@ def test_convolution_step_with_the_descriptor_of_a_prompt(T, dtype, D, K):
     out.t[1].copy_(state)
     step(T, out.t[1], out.t[0])
     assert out.whole() and torch.equal(out.t[0], want) and torch.equal(out.t[1], ends)
+
+
+@pytest.mark.parametrize("T", [0, 7, 4096, 1 << 40])
+@pytest.mark.parametrize("dtype,D,N", [(BF16, 64, 16), (F32, 14, 5)])
+def test_scan_step_with_the_descriptor_of_a_prompt(T, dtype, D, N):
+    """Likewise the scan's step, with dense B and C of two groups."""
+    B = 5
+    g = to_gpu(inputs(D, B, 1, D, N, 2, dtype), dtype)
+    args = [t[:, 0].contiguous() if n in ("x", "dt", "B", "C", "z") else t for n, t in g.items() if n in NAMES[:8]]
+    want, ends = torch.empty_like(args[0]), g["state"].clone()
+
+    def step(T, st, y):
+        desc = ws.SsmDesc(B, T, D, N, 2, 0, CODE[dtype], ws.GL_FLAG_SOFTPLUS)
+        status = ws.ssm_lib().gl_ssm_step(ctypes.byref(desc), *(ptr(t) for t in args), None, B, ptr(st), ptr(y),
+                                          ctypes.c_void_p(torch.cuda.current_stream().cuda_stream))
+        assert status == 0, ws.lib().gl_last_error()
+    step(1, ends, want)
+    out = Outputs([want, ends])
+    out.t[1].copy_(g["state"])
+    step(T, out.t[1], out.t[0])
+    assert out.whole() and torch.equal(out.t[0], want) and torch.equal(out.t[1], ends)

@@ -275,3 +275,10 @@ def test_convolution_step_does_not_use_the_tokens_of_its_descriptor(T):
     """A step takes the descriptor of any number of tokens: sizes are checked as for one."""
     none = [0 if n == "n_slots" else None for n, *_ in CALLS["gl_conv_step"]]
     assert call("gl_conv_step", desc("conv", B=0, T=T), none) == 0
+
+
+@pytest.mark.parametrize("T", [0, 7, 1 << 40])
+def test_scan_step_does_not_use_the_tokens_of_its_descriptor(T):
+    """Likewise of the scan's step, whose sizes were checked as those of T tokens."""
+    none = [0 if n == "n_slots" else None for n, *_ in CALLS["gl_ssm_step"]]
+    assert call("gl_ssm_step", desc("ssm", B=0, T=T), none) == 0

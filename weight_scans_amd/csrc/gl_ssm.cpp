@@ -144,7 +144,7 @@ struct SsmPlan {
   size_t par = 4, elem = 2, saved = 0, bc = 0, bwd_ws = 0;  // bwd_ws: with `saved` given
 };
 
-gl_status_t check_ssm(const gl_ssm_desc_t* d) {
+gl_status_t check_ssm(const gl_ssm_desc_t* d, bool step = false) {
   if (!d) return fail(GL_ERROR_INVALID_VALUE, "desc is NULL");
   if (d->B < 0 || d->T < 0 || d->D < 0) return fail(GL_ERROR_INVALID_VALUE, "negative B, T or D");
   if (d->N < 1) return fail(GL_ERROR_INVALID_VALUE, "N must be >= 1");
@@ -158,12 +158,12 @@ gl_status_t check_ssm(const gl_ssm_desc_t* d) {
   if (d->D > (1 << 24)) return fail(GL_ERROR_NOT_SUPPORTED, "D above 2^24");
   // the kernels keep a lane's place in a tile of 1024 tokens as 32 bits
   for (const gl_rows_t& s : {d->sx, d->sdt, d->sz, d->sy, d->sdy, d->sdx, d->sddt, d->sdz})
-    if (rows(s, d->T, 1, d->D).t >= kMaxTokenStride)
+    if (rows(s, 1, 1, d->D).t >= kMaxTokenStride)
       return fail(GL_ERROR_NOT_SUPPORTED, "a token stride above %lld elements", (long long)kMaxTokenStride - 1);
-  const int64_t n = d->n_seq ? d->n_seq : d->B;
+  const int64_t n = d->n_seq ? d->n_seq : d->B, T = step ? 1 : d->T;
   TRY(check_sizes({n, d->D, 16}, 2e9));  // work-groups, lanes of a step / 256
-  TRY(check_sizes({d->B, d->T, d->G, d->N}, 2e11));
-  return check_sizes({d->B, d->T, d->D, d->N}, 1e15);
+  TRY(check_sizes({d->B, T, d->G, d->N}, 2e11));
+  return check_sizes({d->B, T, d->D, d->N}, 1e15);
 }
 
 gls::SsmArgs ssm_args(const gl_ssm_desc_t* d) {
@@ -389,9 +389,9 @@ gl_status_t gl_ssm_bwd(const gl_ssm_desc_t* desc, const void* x, const void* dt,
 gl_status_t gl_ssm_step(const gl_ssm_desc_t* desc, const void* x, const void* dt, const void* A, const void* B,
                         const void* C, const void* skip, const void* z, const void* dt_bias, const int32_t* slots,
                         int64_t n_slots, void* state, void* y, void* stream) {
-  SsmPlan p;
-  TRY(plan_ssm(desc, &p));
+  TRY(check_ssm(desc, true));
   if (desc->n_seq) return fail(GL_ERROR_INVALID_VALUE, "a step takes no packed sequences");
+  const SsmPlan p{par_of(desc->io_dtype), elem_of(desc->io_dtype)};
   gl_ssm_desc_t one = *desc;
   one.T = 1;
   gls::SsmArgs a = ssm_args(&one);
