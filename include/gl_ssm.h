@@ -10,7 +10,8 @@
  * is F64, else fp32.  Pointers are aligned to their elements, workspaces and
  * saved states to 16 bytes; tensors whose rows begin on 16 bytes take the
  * faster kernels where there are two.  Unless said otherwise no output may
- * overlap an input or another output.
+ * overlap an input or another output.  Sizes of which a launch would have 2^32
+ * threads or more are not supported; a call says so before it writes anything.
  *
  * Packed sequences: with n_seq > 0, B is 1, the T tokens hold n_seq sequences
  * one after another and cu_seqlens (device, int32, n_seq + 1 values, first 0,

@@ -282,3 +282,31 @@ def test_scan_step_does_not_use_the_tokens_of_its_descriptor(T):
     """Likewise of the scan's step, whose sizes were checked as those of T tokens."""
     none = [0 if n == "n_slots" else None for n, *_ in CALLS["gl_ssm_step"]]
     assert call("gl_ssm_step", desc("ssm", B=0, T=T), none) == 0
+
+
+ROWS_64 = {s: (64, 64, 64) for s in ("sx", "sdt", "sz", "sB", "sC", "sy", "sdy", "sdx", "sddt", "sdz", "sdB", "sdC")}
+
+
+@pytest.mark.parametrize("name,kw,edit", [
+    ("gl_conv_fwd", dict(B=1 << 14, T=1, D=65537, K=8), {}),
+    ("gl_conv_step", dict(B=1 << 17, T=1, D=65537), dict(slots=FAKE)),
+    # a later launch of the call: gradients of the first states
+    ("gl_conv_bwd", dict(B=1 << 14, T=1, D=1 << 16, K=8), {}),
+    # work-groups of one channel each, in the forward and in the backward with and without saved states
+    ("gl_ssm_fwd", dict(B=512, T=1, D=1 << 15, G=1 << 15, N=1), {}),
+    ("gl_ssm_bwd", dict(B=512, T=1, D=1 << 15, G=1 << 15, N=1), {}),
+    ("gl_ssm_bwd", dict(B=512, T=1, D=1 << 15, G=1 << 15, N=1), dict(saved=None)),
+    # its sums over sequences
+    ("gl_ssm_bwd", dict(B=1, T=1, D=1 << 24, G=1, N=256, **ROWS_64), {}),
+    ("gl_ssm_bwd", dict(B=1, T=1, D=1 << 24, G=1, N=256, **ROWS_64), dict(saved=None)),
+    ("gl_addnorm_fwd", dict(B=1 << 14, T=1 << 15, d=64), {}),
+    ("gl_gatenorm_fwd", dict(B=1 << 14, T=1 << 15, G=1, d=64), {}),
+    # sums for the weights of very many groups
+    ("gl_gatenorm_bwd", dict(B=1, T=1, G=65535, d=16384, flags=ws.GL_FLAG_GROUP_WEIGHTS), {}),
+    ("gl_gatenorm_bwd", dict(B=0, T=1, G=65535, d=16384, flags=ws.GL_FLAG_GROUP_WEIGHTS), {}),
+])
+def test_sizes_above_a_launch_are_refused_before_the_first(name, kw, edit):
+    """Not supported, where a launch would have failed behind others that had written."""
+    usual = dict(n_slots=1 << 20)
+    assert call(name, desc(kind_of(name), **kw), pointers(name, **(usual | edit)), nb=1 << 62) == UNSUPPORTED
+    assert b"limits" in ws.lib().gl_last_error()

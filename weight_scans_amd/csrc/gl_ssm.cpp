@@ -26,6 +26,7 @@ gl_status_t fail(gl_status_t st, const char* fmt, ...) {
 }
 
 gl_status_t hip_status(hipError_t e, const char* where) {
+  if (e == hipErrorInvalidConfiguration) return fail(GL_ERROR_NOT_SUPPORTED, "%s: sizes above the launch limits", where);
   return e == hipSuccess ? GL_SUCCESS : fail(GL_ERROR_HIP, "%s: %s", where, hipGetErrorString(e));
 }
 
@@ -378,6 +379,8 @@ gl_status_t gl_ssm_bwd(const gl_ssm_desc_t* desc, const void* x, const void* dt,
   a.part_par = w.take(static_cast<size_t>(a.N) * (a.Ns + 2) * a.D * p.par);
   a.ckpt = const_cast<void*>(saved);
   const hipStream_t s = static_cast<hipStream_t>(stream);
+  if (!gls::ssm_bwd_fits(desc->io_dtype, a))  // before the forward below is launched
+    return hip_status(hipErrorInvalidConfiguration, "selective scan backward launch");
   if (!saved && p.saved) {
     a.ckpt = w.take(p.saved);
     // a.y and a.state_out NULL: the states before the tiles only

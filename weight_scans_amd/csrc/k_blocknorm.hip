@@ -582,6 +582,8 @@ hipError_t launch_gatenorm_fwd(int io, const GateNormArgs& a, hipStream_t s) {
 }
 hipError_t launch_gatenorm_bwd(int io, const GateNormArgs& a, hipStream_t s) {
   const bool v = gatenorm_vec(io, a, true), any = a.B * a.T * a.G > 0;
+  const int64_t cols = static_cast<int64_t>(a.d) * (a.group_w ? a.G : 1);
+  if (a.dw && !sums_fit(cols)) return hipErrorInvalidConfiguration;
   hipError_t e = hipSuccess;
   if (any) {
     if (io == IO_F64) e = by_width<Gate<double, double>::Bwd, double>(a.d, v, a, s);
@@ -590,8 +592,7 @@ hipError_t launch_gatenorm_bwd(int io, const GateNormArgs& a, hipStream_t s) {
   }
   if (e != hipSuccess) return e;
   const SumOut out[1] = {{a.dw, 1}};
-  return launch_sum_rows(io, a.part, out, 1, any ? gatenorm_parts(a) : 0,
-                         static_cast<int64_t>(a.d) * (a.group_w ? a.G : 1), s);
+  return launch_sum_rows(io, a.part, out, 1, any ? gatenorm_parts(a) : 0, cols, s);
 }
 
 }  // namespace gls

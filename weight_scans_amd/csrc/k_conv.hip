@@ -467,6 +467,8 @@ hipError_t launch_conv_step(int io, const ConvArgs& a, hipStream_t s) { return r
 hipError_t launch_conv_bwd(int io, const ConvArgs& a, hipStream_t s) {
   hipError_t e = hipSuccess;
   const size_t par = io == IO_F64 ? 8 : 4;
+  const int64_t items = a.dstate_in ? a.N * (a.K - 1) * a.D : 0;
+  if (!launch_fits(items)) return hipErrorInvalidConfiguration;
   if (a.B * a.T > 0) {
     if ((e = run<BWD>(io, a, s)) != hipSuccess) return e;
   }
@@ -478,9 +480,7 @@ hipError_t launch_conv_bwd(int io, const ConvArgs& a, hipStream_t s) {
     out[a.K] = {a.dbias, 1};
     if ((e = launch_sum_rows(io, a.part, out, a.K + 1, rows, a.D, s)) != hipSuccess) return e;
   }
-  const int64_t items = a.N * (a.K - 1) * a.D;
-  if (!a.dstate_in || items == 0) return e;
-  if (!launch_fits(items)) return hipErrorInvalidConfiguration;
+  if (items == 0) return e;
   const unsigned g = static_cast<unsigned>((items + kThreads - 1) / kThreads);
   if (io == IO_F64) conv_bwd_state<double, double><<<g, kThreads, 0, s>>>(a);
   else if (io == IO_F32) conv_bwd_state<float, float><<<g, kThreads, 0, s>>>(a);

@@ -470,33 +470,41 @@ __global__ __launch_bounds__(kSumThreads) void ssm_bwd_sums(SsmArgs a, int nb, i
 
 constexpr int kNS = 2;
 
+// Work-groups of the sums: for dB and dC, for the parameters.
+struct SumGroups {
+  int64_t bc, par;
+  explicit SumGroups(const SsmArgs& a) {
+    const int64_t sums = 2 * a.G * ((a.Ns + kNS - 1) / kNS) * a.B * a.T * kNS;
+    bc = std::min<int64_t>((sums + kSumThreads - 1) / kSumThreads, 1 << 23);
+    par = (static_cast<int64_t>(a.Ns + 2) * a.D + kSumThreads - 1) / kSumThreads;
+  }
+};
+
 template <typename IO, typename L>
 hipError_t go(int io, const SsmArgs& a, hipStream_t s) {
   const int64_t blocks = ssm_blocks(a, L::CH);
   if (a.N * blocks > 0) {
     SsmArgs b = a;
     b.vec_bc = ssm_vec_bc(io, a);
-    if (!launch_fits(a.N * blocks * L::THREADS)) return hipErrorInvalidConfiguration;
     const unsigned g = static_cast<unsigned>(a.N * blocks);
     if (a.z) ssm_bwd<IO, L, true><<<g, L::THREADS, bwd_lds<L, true>(a.Ns), s>>>(b);
     else ssm_bwd<IO, L, false><<<g, L::THREADS, bwd_lds<L, false>(a.Ns), s>>>(b);
     const hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
   }
-  const int64_t bc = 2 * a.G * ((a.Ns + kNS - 1) / kNS) * a.B * a.T * kNS, par = static_cast<int64_t>(a.Ns + 2) * a.D;
-  const int64_t g1 = std::min<int64_t>((bc + kSumThreads - 1) / kSumThreads, 1 << 23), g2 = (par + kSumThreads - 1) / kSumThreads;
-  if (g1 + g2 == 0) return hipSuccess;
+  const SumGroups g(a);
+  if (g.bc + g.par == 0) return hipSuccess;
   ssm_bwd_sums<IO, typename L::S, kNS>
-      <<<static_cast<unsigned>(g1 + g2), kSumThreads, 0, s>>>(a, static_cast<int>(a.G ? blocks / a.G : 0), g1);
+      <<<static_cast<unsigned>(g.bc + g.par), kSumThreads, 0, s>>>(a, static_cast<int>(a.G ? blocks / a.G : 0), g.bc);
   return hipGetLastError();
 }
 
 template <typename IO, typename S, int TT>
 hipError_t by_channels(int io, int channels, const SsmArgs& a, hipStream_t s) {
   switch (channels) {
-    case 32: return go<IO, SsmTile<S, 32, 8, TT, kNS, 16>>(io, a, s);
-    case 16: return go<IO, SsmTile<S, 16, 8, TT, kNS, 8>>(io, a, s);
-    default: return go<IO, SsmTile<S, 8, 8, TT, kNS, sizeof(S) == 8 ? 4 : 8>>(io, a, s);
+    case 32: return go<IO, SsmTile<S, 32, kSsmWaves, TT, kNS, 16>>(io, a, s);
+    case 16: return go<IO, SsmTile<S, 16, kSsmWaves, TT, kNS, 8>>(io, a, s);
+    default: return go<IO, SsmTile<S, 8, kSsmWaves, TT, kNS, sizeof(S) == 8 ? 4 : 8>>(io, a, s);
   }
 }
 template <typename IO>
@@ -519,7 +527,13 @@ SsmShape ssm_bwd_shape(int io, const SsmArgs& a) {
 }
 size_t ssm_bc_bytes(int io, const SsmArgs& a) { return bc_bytes(io, a, ssm_bwd_shape(io, a).channels); }
 
+bool ssm_bwd_fits(int io, const SsmArgs& a) {
+  const SumGroups g(a);
+  return ssm_bwd_shape(io, a).fits(a) && launch_fits((g.bc + g.par) * kSumThreads);
+}
+
 hipError_t launch_ssm_bwd(int io, const SsmArgs& a, hipStream_t s) {
+  if (!ssm_bwd_fits(io, a)) return hipErrorInvalidConfiguration;
   const SsmShape p = ssm_bwd_shape(io, a);
   if (io == IO_F64) return by_channels<double, double, 8>(io, p.channels, a, s);
   if (io == IO_F32) return by_shape<float>(io, p, a, s);

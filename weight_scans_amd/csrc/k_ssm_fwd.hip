@@ -183,7 +183,6 @@ template <typename IO, typename L>
 hipError_t go(int io, const SsmArgs& a, hipStream_t s) {
   const int64_t g = a.N * ssm_blocks(a, L::CH);
   if (g == 0) return hipSuccess;
-  if (!launch_fits(g * L::THREADS)) return hipErrorInvalidConfiguration;
   SsmArgs b = a;
   b.vec_bc = ssm_vec_bc(io, a);
   if (a.z) ssm_fwd<IO, L, true><<<static_cast<unsigned>(g), L::THREADS, L::lds(a.Ns), s>>>(b, ssm_ck(io, a));
@@ -194,10 +193,10 @@ hipError_t go(int io, const SsmArgs& a, hipStream_t s) {
 template <typename IO, typename S, int TT, int NS>
 hipError_t by_channels(int io, int channels, const SsmArgs& a, hipStream_t s) {
   switch (channels) {
-    case 64: return go<IO, SsmTile<S, 64, 8, TT, NS, 16>>(io, a, s);
-    case 32: return go<IO, SsmTile<S, 32, 8, TT, NS, 16>>(io, a, s);
-    case 16: return go<IO, SsmTile<S, 16, 8, TT, NS, 8>>(io, a, s);
-    default: return go<IO, SsmTile<S, 8, 8, TT, NS, 8>>(io, a, s);
+    case 64: return go<IO, SsmTile<S, 64, kSsmWaves, TT, NS, 16>>(io, a, s);
+    case 32: return go<IO, SsmTile<S, 32, kSsmWaves, TT, NS, 16>>(io, a, s);
+    case 16: return go<IO, SsmTile<S, 16, kSsmWaves, TT, NS, 8>>(io, a, s);
+    default: return go<IO, SsmTile<S, 8, kSsmWaves, TT, NS, 8>>(io, a, s);
   }
 }
 template <typename IO>
@@ -233,6 +232,7 @@ SsmShape ssm_shape(const SsmArgs& a, int io, int most) {
 
 hipError_t launch_ssm_fwd(int io, const SsmArgs& a, hipStream_t s) {
   const SsmShape p = ssm_shape(a, io, a.Ns <= 64 ? 64 : a.Ns <= 128 ? 32 : 16);  // (by the LDS)
+  if (!p.fits(a)) return hipErrorInvalidConfiguration;
   if (io == IO_F64) return by_channels<double, double, 8, 2>(io, p.channels, a, s);
   if (io == IO_F32) return by_shape<float>(io, p, a, s);
   return by_shape<bf16>(io, p, a, s);

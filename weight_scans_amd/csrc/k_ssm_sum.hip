@@ -6,7 +6,7 @@
 namespace gls {
 namespace {
 
-constexpr int kCols = 64, kRows = 16;
+constexpr int kCols = kSumCols, kRows = kSumRows;
 
 struct Outs {
   SumOut o[kMaxSums];
@@ -51,6 +51,7 @@ hipError_t launch_sum_rows(int io, const void* part, const SumOut* out, int nz, 
     any = any || out[i].p;
   }
   if (!any || cols == 0) return hipSuccess;
+  if (!sums_fit(cols)) return hipErrorInvalidConfiguration;
   const dim3 grid(static_cast<unsigned>((cols + kCols - 1) / kCols), static_cast<unsigned>(nz));
   if (io == IO_F64) sum_rows<<<grid, kCols * kRows, 0, s>>>(static_cast<const double*>(part), o, rows, cols);
   else sum_rows<<<grid, kCols * kRows, 0, s>>>(static_cast<const float*>(part), o, rows, cols);

@@ -15,7 +15,8 @@ namespace gls {
 struct Rows {
   int64_t b, t, g;
 };
-// A launch counts its threads in 32 bits.
+// A launch counts its threads in 32 bits.  A call's launchers return
+// hipErrorInvalidConfiguration for one that would not fit before they launch any.
 inline bool launch_fits(int64_t threads) { return threads <= 0xffffffffLL - 1024; }
 
 // ---- convolution
@@ -89,9 +90,11 @@ inline int64_t ssm_blocks(const SsmArgs& a, int CH) {
   return static_cast<int64_t>((dg + CH - 1) / CH) * a.G;
 }
 // Channels a work-group and tokens a slot; tiles are of 8 * 64 / channels slots.
+constexpr int kSsmWaves = 8;  // of a work-group
 struct SsmShape {
   int channels, tokens;
-  int tile() const { return tokens * 8 * (64 / channels); }
+  int tile() const { return tokens * kSsmWaves * (64 / channels); }
+  bool fits(const SsmArgs& a) const { return launch_fits(a.N * ssm_blocks(a, channels) * 64 * kSsmWaves); }
 };
 SsmShape ssm_shape(const SsmArgs& a, int io, int most);
 // Those of the backward: as many channels as leave the LDS room for N states of each at most,
@@ -100,6 +103,7 @@ SsmShape ssm_shape(const SsmArgs& a, int io, int most);
 SsmShape ssm_bwd_shape(int io, const SsmArgs& a);
 inline int ssm_ck(int io, const SsmArgs& a) { return ssm_bwd_shape(io, a).tile(); }
 size_t ssm_bc_bytes(int io, const SsmArgs& a);
+bool ssm_bwd_fits(int io, const SsmArgs& a);
 hipError_t launch_ssm_fwd(int io, const SsmArgs& a, hipStream_t s);
 hipError_t launch_ssm_bwd(int io, const SsmArgs& a, hipStream_t s);
 hipError_t launch_ssm_step(int io, const SsmArgs& a, hipStream_t s);
@@ -156,6 +160,8 @@ struct SumOut {
   int64_t stride;
 };
 constexpr int kMaxSums = 9;
+constexpr int kSumCols = 64, kSumRows = 16;  // threads of a work-group
+inline bool sums_fit(int64_t cols) { return launch_fits((cols + kSumCols - 1) / kSumCols * (kSumCols * kSumRows)); }
 hipError_t launch_sum_rows(int io, const void* part, const SumOut* out, int nz, int64_t rows, int64_t cols,
                            hipStream_t s);
 
