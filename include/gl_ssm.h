@@ -109,8 +109,15 @@ typedef struct {
 } gl_ssm_desc_t;
 
 /* Bytes of `saved` (what gl_ssm_fwd leaves for gl_ssm_bwd; opaque) and of the
- * workspaces.  Without `saved` the backward runs the forward again inside its own,
- * larger workspace. */
+ * workspaces (the forward's is empty).  Without `saved` the backward runs the forward
+ * again inside its own workspace, larger by what `saved` takes.  With it the backward's
+ * holds the parts of dB and dC, 2 N par values for every token and block of c channels of
+ * a group (B T G ceil(D / G / c) of them, an odd N counted as N + 1), and N + 2 for every
+ * sequence and channel.  c is 8, 16 or 32, by the work-groups that there are; while the parts
+ * are more than 2^30 bytes it is doubled, but to no more than 32 where N <= 64, 16 where
+ * N <= 128, else 8 (half these N in fp64).  So the workspace can be many times the tensors
+ * (N = 256: 128 times a bf16 x); a batch may be given in pieces, and a sequence in pieces
+ * that hand their states on. */
 gl_status_t gl_ssm_saved_size(const gl_ssm_desc_t* desc, size_t* saved_bytes);
 gl_status_t gl_ssm_workspace_size(const gl_ssm_desc_t* desc, int have_saved, size_t* fwd_ws_bytes,
                                   size_t* bwd_ws_bytes);

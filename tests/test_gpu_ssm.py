@@ -300,3 +300,39 @@ def test_results_do_not_depend_on_the_run():
     _, _, saved = ws.gl_ssm_fwd(*args, save=True)
     a, b = (ws.gl_ssm_bwd(*args, g["dy"], saved) for _ in range(2))
     assert all(torch.equal(s, t) for s, t in zip(a, b) if s is not None)
+
+
+@pytest.mark.parametrize("T,channels", [(32896, 16), (65600, 32)])
+def test_more_channels_where_the_parts_are_large(T, channels):
+    """Sequences whose parts of dB and dC would take more than 2^30 bytes at eight channels a work-group: 16 and 32
+    instead, with what the same tokens give in pieces of eight channels each (fp32; bounds as above)."""
+    D, N, piece = 512, 64, 16448
+    size = lambda t: ws.ssm_workspace_size(ws.SsmDesc(1, t, D, N, 1, 0, 1, ws.GL_FLAG_SOFTPLUS), True)[1]  # noqa: E731
+    par = 4 * (N + 2) * D
+    assert size(piece) == 2 * N * (D // 8) * piece * 4 + par
+    assert size(T) == 2 * N * (D // channels) * T * 4 + par
+    g = torch.Generator(device="cuda").manual_seed(T)
+    rnd = lambda *s: torch.randn(s, generator=g, device="cuda")  # noqa: E731
+    A = -torch.arange(1, N + 1, device="cuda") * torch.exp(0.1 * rnd(D, N))
+    bias = torch.rand(D, generator=g, device="cuda") * 3 - 4  # steps of some 0.02 .. 0.3
+    args = [rnd(1, T, D), 0.5 * rnd(1, T, D), A, rnd(1, T, 1, N), rnd(1, T, 1, N), 1 + 0.1 * rnd(D), rnd(1, T, D), bias]
+    dy, state, dstate = rnd(1, T, D), 0.3 * rnd(1, D, N), 0.3 * rnd(1, D, N)
+    y, end, saved = ws.gl_ssm_fwd(*args, state=state, want_state=True, save=True)
+    whole = ws.gl_ssm_bwd(*args, dy, saved, state=state, dstate=dstate)
+    cuts = [*range(0, T, piece), T]
+    part = lambda lo, hi: [t if t.dim() < 3 else t[:, lo:hi] for t in args]  # noqa: E731
+    st, ys, keep = state, [], []
+    for lo, hi in zip(cuts, cuts[1:]):
+        yp, nxt, s = ws.gl_ssm_fwd(*part(lo, hi), state=st, want_state=True, save=True)
+        ys.append(yp)
+        keep.append((lo, hi, st, s))
+        st = nxt
+    adj, parts = dstate, []
+    for lo, hi, first, s in reversed(keep):
+        parts.insert(0, ws.gl_ssm_bwd(*part(lo, hi), dy[:, lo:hi], s, state=first, dstate=adj))
+        adj = parts[0][8]
+    errs = {"y": (rel(torch.cat(ys, 1), y), 8e-6), "end": (rel(st, end), 8e-6), "dstate": (rel(adj, whole[8]), 1.6e-5)}
+    for i, n in enumerate(NAMES[:8]):
+        both = sum(p[i].double() for p in parts) if n in ("A", "skip", "dt_bias") else torch.cat([p[i] for p in parts], 1)
+        errs["d" + n] = (rel(both, whole[i]), 1.6e-5)
+    check(errs)

@@ -310,3 +310,20 @@ def test_sizes_above_a_launch_are_refused_before_the_first(name, kw, edit):
     usual = dict(n_slots=1 << 20)
     assert call(name, desc(kind_of(name), **kw), pointers(name, **(usual | edit)), nb=1 << 62) == UNSUPPORTED
     assert b"limits" in ws.lib().gl_last_error()
+
+
+@pytest.mark.parametrize("io,B,T,D,N,G,channels", [
+    (BF16, 4, 4096, 2048, 16, 1, 32), (BF16, 1, 32768, 2048, 16, 1, 8),
+    # above 2^30 bytes of parts more channels, as far as there are: 32 to 64 states, 16 to 128, 8 to 256 (fp64: half)
+    (BF16, 1, 32769, 2048, 16, 1, 16), (F32, 1, 65537, 2048, 16, 1, 32), (BF16, 1, 131072, 2048, 16, 1, 32),
+    (BF16, 8, 8192, 4096, 64, 1, 32), (F32, 2, 16384, 4096, 128, 2, 16), (BF16, 4, 4096, 2048, 256, 1, 8),
+    (F64, 2, 16384, 4096, 64, 1, 16), (F32, 1, 40000, 520, 64, 2, 16)])
+def test_workspace_of_the_scan_backward(io, B, T, D, N, G, channels):
+    """What the header says: the parts of dB and dC, 2 N values a token and block of channels, and those of the
+    parameters, N + 2 a channel and sequence, to 256 bytes each."""
+    n, m = ctypes.c_size_t(), ctypes.c_size_t()
+    d = desc("ssm", B=B, T=T, D=D, N=N, G=G, io_dtype=io)
+    assert ws.ssm_lib().gl_ssm_workspace_size(ctypes.byref(d), 1, ctypes.byref(n), ctypes.byref(m)) == 0
+    par, up = 8 if io == F64 else 4, lambda x: -(-x // 256) * 256
+    blocks = G * -(-(D // G) // channels)
+    assert n.value == 0 and m.value == up(2 * N * blocks * B * T * par) + up(B * (N + 2) * D * par)

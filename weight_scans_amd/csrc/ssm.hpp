@@ -97,9 +97,14 @@ struct SsmShape {
   bool fits(const SsmArgs& a) const { return launch_fits(a.N * ssm_blocks(a, channels) * 64 * kSsmWaves); }
 };
 SsmShape ssm_shape(const SsmArgs& a, int io, int most);
-// Those of the backward: as many channels as leave the LDS room for N states of each at most,
-// and no fewer than keep the parts of the sums over channels, which grow, under a
-// gigabyte.  A forward that trains keeps the states before its tiles.
+// Those of the backward: at most as many channels as leave the LDS room for N states of
+// each (32 to 64 states, 16 to 128, 8 to 256; half these states in fp64), and more than the
+// rounds of tiles ask for where the parts of the sums over channels, which are fewer then,
+// would take more than 2^30 bytes.  That bounds them only as far as those most channels
+// do: 8 * 8192 tokens of 4096 channels and 64 states leave 4 GiB, 4 * 4096 of 2048 and 256
+// 8 GiB.  It costs time: one sequence of 2048 channels and 16 states in bf16, 32896 tokens:
+// 16 channels 3.25 ms (0.5 GiB), 8 channels 2.10 ms (1.0 GiB); 131072 tokens: 32 channels 20.5 ms
+// (1 GiB), 8 channels 8.1 ms (4 GiB).  A forward that trains keeps the states before its tiles.
 SsmShape ssm_bwd_shape(int io, const SsmArgs& a);
 inline int ssm_ck(int io, const SsmArgs& a) { return ssm_bwd_shape(io, a).tile(); }
 size_t ssm_bc_bytes(int io, const SsmArgs& a);
