@@ -59,3 +59,35 @@ def test_command_runs():
     first, last, diff = selective.main(["--steps", "12", "--tokens", "4"])
     assert first == first and last == last  # numbers
     assert diff <= 3e-2  # two layers in bf16, some four roundings of 2e-3 each and the logits'
+
+
+@pytest.mark.parametrize("dtype,tol", [
+    (torch.float64, 1e-9),   # as the layer's
+    (torch.float32, 1e-4)])  # two layers of 5e-5
+@pytest.mark.parametrize("gate", ["norm", "scan"])
+def test_gradients_of_the_model(gate, dtype, tol):
+    """What training steps on: the loss of the answers and its gradient of every parameter, against the model
+    written out in 64 bits."""
+    torch.manual_seed(3)
+    back, vocab = 4, 11
+    model = selective.SelectiveModel(vocab, 24, layers=2, inner=40, states=6, rank=3, gate=gate, dtype=dtype)
+    with torch.no_grad():  # weights of ones hide what multiplies them
+        for t in (*model.norms, *model.scales):
+            t.add_(0.3 * torch.randn_like(t))
+    ids = torch.randint(0, vocab, (3, 30)).cuda()
+    names, leaves = zip(*((n, t) for n, t in model.named_parameters() if gate == "norm" or not n.endswith(".norm")))
+    entropy = lambda x, i: torch.nn.functional.cross_entropy(x[:, back:].flatten(0, 1), i[:, :-back].flatten())  # noqa: E731
+    loss = entropy(model(ids)[0], ids)
+    got = torch.autograd.grad(loss, leaves)
+
+    c = [t.detach().double().cpu().requires_grad_(True) for t in leaves]
+    p = dict(zip(names, c))
+    x = p["embed.weight"][ids.cpu()]
+    n, r = ref.add_norm(x, torch.zeros_like(x), p["norms.0"], None, None, 1e-6)
+    for i, layer in enumerate(model.layers):
+        own = {k.removeprefix(f"layers.{i}."): t for k, t in p.items() if k.startswith(f"layers.{i}.")}
+        n, r = ref.add_norm(plain(layer, own, n, None, None)[0], r, p[f"norms.{i + 1}"], None, p[f"scales.{i}"], 1e-6)
+    wanted = entropy(n @ p["head.weight"].T, ids.cpu())
+    assert abs(float(loss.detach()) - float(wanted.detach())) <= tol * float(wanted.detach())
+    for k, a, b in zip(names, got, torch.autograd.grad(wanted, c)):
+        assert float(b.norm()) > 0 and rel(a, b) <= tol, k
