@@ -136,7 +136,7 @@ gl_status_t gl_ssm_bwd(const gl_ssm_desc_t* desc, const void* x, const void* dt,
 
 /* One token of B sequences, x, dt, z, y [B][D], B, C [B][G][N] (strides b and g),
  * against a pool of n_slots states updated in place; slots, T and n_seq as in
- * gl_conv_step. */
+ * gl_conv_step.  Dense rows (all-zero strides) are of less than 2^19 channels. */
 gl_status_t gl_ssm_step(const gl_ssm_desc_t* desc, const void* x, const void* dt, const void* A, const void* B,
                         const void* C, const void* skip, const void* z, const void* dt_bias, const int32_t* slots,
                         int64_t n_slots, void* state, void* y, void* stream);
@@ -146,6 +146,9 @@ gl_status_t gl_ssm_step(const gl_ssm_desc_t* desc, const void* x, const void* dt
  *
  *   u = wx * x / rms(x)  (wx NULL: u = x),   r_out = r + scale * u,
  *   n = w * r_out / rms(r_out),              rms(v) = sqrt(mean(v^2) + eps)
+ *
+ * (in both norms; the squares are summed in fp32, fp64 if io is F64 or rows are of fewer
+ * than 8, and have to stay within it: elements up to 1e18 or so in fp32).
  *
  *   x, n, dn, dx            [B][T][d]  io
  *   r, r_out, dr_out, dr    [B][T][d]  res: the io dtype, or F32 with BF16 io

@@ -11,8 +11,20 @@
 // a row cross lanes by shuffles and, from 128 threads on, waves through LDS.  The
 // backward's work-groups walk rows with the sums for the weights in registers and
 // leave one part each, the next row's loads in flight.  4 x 4096 rows of
-// 2048 in bf16 on an fp32 residual: forward 74 us, 5.4 TB/s, backward 131 us, 4.6 TB/s; gated, 16
-// heads of 128: forward 50 us, backward 83 us, 4.0 TB/s each.
+// 2048 in bf16 on an fp32 residual: forward 73 us, 5.5 TB/s, backward 131 us, 4.6 TB/s; gated, 16
+// heads of 128: forward 50 us, 4.0 TB/s, backward 85 us, 3.9 TB/s.
+//
+// The backwards of long rows spill and are slower for it.  1024 threads a row leave a
+// thread 128 registers for the residual norm's ten arrays of elements: from 8193 columns
+// on (vectors) it spills 254 to 308, the gated norm 148 (bf16) and 226 (fp32); single
+// elements from 2049 on 71 and 21, from 8193 on 241 to 259 and 138.  512 threads
+// with 16 elements each (vectors of 4097 to 8192) spill 16 to 76 in the residual norm; fp64
+// spills from 2049 columns on.  In fp32, residual / gated norm, backward:
+//   8192 rows of 2047:   83 us, 4.8 TB/s /  74 us, 4.5 TB/s
+//   4096 rows of 4095:  325 us, 1.2      / 146 us, 2.3
+//   4096 rows of 4096:   83 us, 4.9      /  72 us, 4.7
+//   2048 rows of 8192:  191 us, 2.1      /  77 us, 4.4
+//   1024 rows of 16384: 372 us, 1.1      / 269 us, 1.2     (bf16: 278 / 175 us)
 #include <algorithm>
 #include <type_traits>
 

@@ -1,13 +1,21 @@
 // k_conv.hip -- short causal convolution per channel with its bias and SiLU, its
 // backward and its form for single tokens (any io dtype, 1 <= K <= 8).
 //
-// Bound by memory: a token is read and written once.  A thread owns 16 bytes of
+// A token is read and written once.  A thread owns 16 bytes of
 // neighbouring channels (one element where rows do not begin on 16 bytes) and a
 // run of tokens, with the last K - 1 inputs in registers; neighbouring threads
 // own neighbouring channels.  The inputs before a run are read again by it, in
-// the backward also what its last inputs reach behind it.  4 x 4096
-// tokens of 2048 channels in bf16, K = 4: forward 30 us, 4.5 TB/s, backward 56 us, 3.6 TB/s
-// (a thread's forty sums for the weights' gradients leave it fewer loads in flight).
+// the backward also what its last inputs reach behind it.
+//
+// The forward is bound by memory: 4 x 4096 tokens of 2048 channels in bf16, K = 4: 30 us,
+// 4.5 TB/s.  A small one is bound by what a thread does in series before its first tokens
+// arrive (taps, the table's search, the inputs before its run): packed 3001 tokens of 1001
+// channels in fp32, K = 3, 10.1 us; without a table 9.2, rows of 1000 in vectors 9.8, eight
+// times the tokens 43 us, 4.5 TB/s.
+// The backward is bound by the vector ALU: 56 us at the first of these sizes, 3.6 TB/s.
+// Two waves a SIMD (forty sums for the weights' gradients a thread) keep it busy 82 % of the
+// time, with 39 instructions an element, some 25 of them arithmetic: two runs share a wave,
+// so that tokens, bounds and addresses are computed lane by lane.
 #include <algorithm>
 
 #include "ssm_dev.hpp"

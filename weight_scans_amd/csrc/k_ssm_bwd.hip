@@ -16,10 +16,15 @@
 // fixed order.
 //
 // Bound by the vector ALU: 4 x 4096 tokens of 2048 channels and 16 states in bf16, gated:
-// 690 us, 32 instructions per token, channel and state, the ALU busy 73 % of the time
+// 690 us, 32 instructions per token, channel and state, the ALU busy 72 % of the time
 // (29 us more for the parts); its bytes alone would take 112 us, a fifth of
 // them the parts.  Some 70 % of the time is the loop over the states, the rest before and
 // behind it loads and stores that no other wave covers (the registers hold two waves a SIMD).
+// One sequence of 32768 tokens (8 channels a work-group): 2.04 ms, and 1 GiB of parts.
+//
+// At 16 tokens a slot all 256 registers are taken and some spill: with the gate 47, 38 and
+// 50 in bf16 (32, 16 and 8 channels), 79, 58 and 118 in fp32, and 151 to 177 in fp64 (8
+// tokens); 2 to 26 fewer without it.  At 4 tokens none do.
 #include <algorithm>
 
 #include "ssm_scan.hpp"

@@ -15,7 +15,7 @@
 // another in groups of NS, not side by side in lanes: a lane's x, D and y then serve all
 // states, and only B and C are read per state, from LDS.  Longer slots cost less in
 // exchanges (16 tokens: 690 us the backward at 4 x 4096 x 2048 x 16; 8 with twice the states
-// at once: 890), shorter ones leave less of a short sequence's tile empty.
+// at once: 903), shorter ones leave less of a short sequence's tile empty.
 #pragma once
 
 #include "ssm_dev.hpp"
