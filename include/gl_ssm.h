@@ -148,7 +148,7 @@ gl_status_t gl_ssm_step(const gl_ssm_desc_t* desc, const void* x, const void* dt
  *   n = w * r_out / rms(r_out),              rms(v) = sqrt(mean(v^2) + eps)
  *
  * (in both norms; the squares are summed in fp32, fp64 if io is F64 or rows are of fewer
- * than 8, and have to stay within it: elements up to 1e18 or so in fp32).
+ * than 8, and have to stay within it: elements up to 1e17 in fp32).
  *
  *   x, n, dn, dx            [B][T][d]  io
  *   r, r_out, dr_out, dr    [B][T][d]  res: the io dtype, or F32 with BF16 io

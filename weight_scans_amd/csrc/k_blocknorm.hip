@@ -19,7 +19,7 @@
 // on (vectors) it spills 254 to 308, the gated norm 148 (bf16) and 226 (fp32); single
 // elements from 2049 on 71 and 21, from 8193 on 241 to 259 and 138.  512 threads
 // with 16 elements each (vectors of 4097 to 8192) spill 16 to 76 in the residual norm; fp64
-// spills from 2049 columns on.  In fp32, residual / gated norm, backward:
+// spills from 2049 columns on, its forwards 8 to 23 from 8193 on.  In fp32, residual / gated norm, backward:
 //   8192 rows of 2047:   83 us, 4.8 TB/s /  74 us, 4.5 TB/s
 //   4096 rows of 4095:  325 us, 1.2      / 146 us, 2.3
 //   4096 rows of 4096:   83 us, 4.9      /  72 us, 4.7

@@ -1,10 +1,10 @@
 // k_ssm_step.hip -- selective scan, one token of each row against a pool of states.
 //
 // Bound by reading and writing the states: 256 rows of 2048 channels and 16 states in
-// 18 us, 71 MB at 3.9 TB/s; 19 us, 3.7 TB/s, under the profiler (one wave of loads and stores a lane; two or four rows a lane, rows in
-// turn with the next one's loads ahead, or other numbers of lanes came to the same or
-// more).  L lanes share a channel's N states (in vectors of 16 bytes where N allows it) and
-// meet in y's sum.
+// 18 us, 71 MB at 3.9 TB/s; 19 us, 3.7 TB/s, under the profiler (one wave of loads and stores a
+// lane; two or four rows a lane, rows in turn with the next one's loads ahead, or other
+// numbers of lanes came to the same or more).  L lanes share a channel's N states (in vectors
+// of 16 bytes where N allows it) and meet in y's sum.
 #include <algorithm>
 
 #include "ssm_dev.hpp"
